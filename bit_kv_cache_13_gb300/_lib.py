@@ -37,6 +37,14 @@ _SIGS = {
     "kvq_decode_attn_int2_noalloc": ([P, I, I, I, I, P, I64, P, I, P, P, P, F, P, I, P], I),
     "kvq_debug_drop_next_copy": ([], None),
     "kvq_decode_step_int2": ([P, P, P, I, I, I, I, P, I64, P, I, P, P, P, P, F, P, P, SZ, I, I, P], I),
+    "kvq_int4_tile_bytes": ([I], SZ),
+    "kvq_append_int4": ([P, P, I, I, I, P, P, P, P, F, P, I64, P, P], I),
+    "kvq_dequant_int4": ([P, I64, I, I, P, I, P, P, P], I),
+    "kvq_int4_workspace_bytes": ([I, I, I, I, I, I], SZ),
+    "kvq_decode_attn_int4": ([P, I, I, I, I, P, I64, P, I, P, P, P, F, P, P, SZ, I, P], I),
+    "kvq_decode_attn_int4_weights": ([P, I, I, I, I, P, I64, P, I, P, P, P, F, P, P, I64, F, P, SZ, I, P], I),
+    "kvq_evict_select": ([P, I64, I, I, I, P, I, I, I, P, P, P], I),
+    "kvq_evict_gather_int4": ([P, I64, P, I, P, I, P, I, I, I, P, I64, P, I, P, I64, P, I64, P, P], I),
     "bgtq_lloyd_max_codebook": ([I, P], I),
     "bgtq_allocate": ([P, I, I, I, I64, P], I),
     "bgtq_tile_bytes": ([I, I], SZ),
@@ -222,6 +230,147 @@ def kvq_workspace_status(workspace, stream=None) -> int:
     """Returns the status code recorded in a decode workspace (0 = OK) and
     clears it."""
     return load().kvq_workspace_status(_dev(workspace, torch.uint8, "workspace"), _stream(stream))
+
+
+# ------------------------------------------------------------------- INT4
+
+def _shape(x, shape, name: str):
+    if x is not None and tuple(x.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(x.shape)}")
+
+
+def _pool(cache, num_pages: int, h_kv: int, name: str):
+    """A cache pool of at least num_pages pages of h_kv INT4 tiles."""
+    if cache.numel() < num_pages * h_kv * 2560:
+        raise ValueError(f"{name} holds {cache.numel()} bytes, below {num_pages} pages x {h_kv} heads x 2560")
+
+
+def _one_device(*tensors):
+    """The call's tensors live on the current device, whose stream it is enqueued on."""
+    dev = torch.cuda.current_device()
+    for x in tensors:
+        if x is not None and x.is_cuda and x.get_device() != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {x.device}")
+
+
+def kvq_int4_tile_bytes(d: int = 128) -> int:
+    return load().kvq_int4_tile_bytes(d)
+
+
+def kvq_append_int4(k, v, slot_mapping, mu_k, R_k, R_v, cache, num_pages: int, clip: float = 1.0, err_count=None,
+                    stream=None):
+    """Quantise-on-append of k, v [n, H_kv, d] bf16 into the INT4 cache."""
+    n_tok, h_kv, d = k.shape
+    _shape(v, (n_tok, h_kv, d), "v")
+    _shape(slot_mapping, (n_tok,), "slot_mapping")
+    _shape(mu_k, (h_kv, d), "mu_k")
+    _shape(R_k, (h_kv, d, d), "R_k")
+    _shape(R_v, (h_kv, d, d), "R_v")
+    _pool(cache, num_pages, h_kv, "cache")
+    args = (_dev(k, torch.bfloat16, "k"), _dev(v, torch.bfloat16, "v"), n_tok, h_kv, d,
+            _dev(slot_mapping, torch.int32, "slot_mapping"), _dev(mu_k, torch.float32, "mu_k"),
+            _dev(R_k, torch.float32, "R_k"), _dev(R_v, torch.float32, "R_v"), float(clip),
+            _dev(cache, torch.uint8, "cache"), int(num_pages), _dev(err_count, torch.int32, "err_count"))
+    _one_device(k, v, slot_mapping, mu_k, R_k, R_v, cache, err_count)
+    _check(load().kvq_append_int4(*args, _stream(stream)))
+
+
+def kvq_dequant_int4(cache, num_pages: int, H_kv: int, slot_mapping, k_rot=None, v_rot=None, stream=None):
+    """Dequantised rotated vectors [n, H_kv, d] bf16 of the cached tokens at slot_mapping [n]."""
+    n = slot_mapping.shape[0]
+    _shape(slot_mapping, (n,), "slot_mapping")
+    _shape(k_rot, (n, H_kv, 128), "k_rot")
+    _shape(v_rot, (n, H_kv, 128), "v_rot")
+    _pool(cache, num_pages, H_kv, "cache")
+    args = (_dev(cache, torch.uint8, "cache"), int(num_pages), H_kv, 128,
+            _dev(slot_mapping, torch.int32, "slot_mapping"), n, _dev(k_rot, torch.bfloat16, "k_rot"),
+            _dev(v_rot, torch.bfloat16, "v_rot"))
+    _one_device(cache, slot_mapping, k_rot, v_rot)
+    _check(load().kvq_dequant_int4(*args, _stream(stream)))
+
+
+def kvq_int4_workspace_bytes(B: int, H_q: int, H_kv: int, max_pages_per_seq: int, num_splits: int = 0,
+                             weights: bool = False) -> int:
+    return load().kvq_int4_workspace_bytes(B, H_q, H_kv, max_pages_per_seq, num_splits, int(weights))
+
+
+def _decode_int4_args(q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out):
+    B, H_q, d = q.shape
+    h_kv = R_k.shape[0]
+    _shape(R_k, (h_kv, d, d), "R_k")
+    _shape(R_v, (h_kv, d, d), "R_v")
+    _shape(context_lens, (B,), "context_lens")
+    _shape(out, (B, H_q, d), "out")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, max_pages), got {tuple(block_table.shape)}")
+    _pool(cache, num_pages, h_kv, "cache")
+    return (_dev(q, torch.bfloat16, "q"), B, H_q, h_kv, d, _dev(cache, torch.uint8, "cache"), int(num_pages),
+            _dev(block_table, torch.int32, "block_table"), block_table.shape[1],
+            _dev(context_lens, torch.int32, "context_lens"), _dev(R_k, torch.float32, "R_k"),
+            _dev(R_v, torch.float32, "R_v"), float(scale), _dev(out, torch.bfloat16, "out"))
+
+
+def kvq_decode_attn_int4(q, cache, num_pages: int, block_table, context_lens, R_k, R_v, scale: float, out, workspace,
+                         num_splits: int = 0, stream=None):
+    """Decode attention of q [B, H_q, d] bf16 over the INT4 cache into out [B, H_q, d] bf16."""
+    args = _decode_int4_args(q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out)
+    ws = _dev(workspace, torch.uint8, "workspace")
+    _one_device(q, cache, block_table, context_lens, R_k, R_v, out, workspace)
+    _check(load().kvq_decode_attn_int4(*args, ws, workspace.numel(), int(num_splits), _stream(stream)))
+
+
+def kvq_decode_attn_int4_weights(q, cache, num_pages: int, block_table, context_lens, R_k, R_v, scale: float, out,
+                                 weights, decay: float, workspace, num_splits: int = 0, stream=None):
+    """kvq_decode_attn_int4 that also adds each token's attention weight, summed over the query heads of its KV head,
+    to weights [B, H_kv, >= 16 max_pages] fp32 (scaled by decay first)."""
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (q.shape[0], R_k.shape[0]):
+        raise ValueError(f"weights must have shape ({q.shape[0]}, {R_k.shape[0]}, tokens), got {tuple(weights.shape)}")
+    args = _decode_int4_args(q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out)
+    w, ws = _dev(weights, torch.float32, "weights"), _dev(workspace, torch.uint8, "workspace")
+    _one_device(q, cache, block_table, context_lens, R_k, R_v, out, weights, workspace)
+    _check(load().kvq_decode_attn_int4_weights(*args, w, weights.shape[2], float(decay), ws, workspace.numel(),
+                                               int(num_splits), _stream(stream)))
+
+
+def kvq_evict_select(weights, context_lens, budget: int, sinks: int, recent: int, keep, new_lens, stream=None):
+    """Chooses the tokens each (sequence, KV head) keeps by weights [B, H_kv, max_tokens] fp32: their indices, ascending,
+    into keep [B, H_kv, budget] int32 (-1 past them) and min(length, budget) into new_lens [B] int32."""
+    B, h_kv, max_tokens = weights.shape
+    _shape(context_lens, (B,), "context_lens")
+    _shape(new_lens, (B,), "new_lens")
+    _shape(keep, (B, h_kv, budget), "keep")
+    args = (_dev(weights, torch.float32, "weights"), max_tokens, B, h_kv, max_tokens,
+            _dev(context_lens, torch.int32, "context_lens"), int(budget), int(sinks), int(recent),
+            _dev(keep, torch.int32, "keep"), _dev(new_lens, torch.int32, "new_lens"))
+    _one_device(weights, context_lens, keep, new_lens)
+    _check(load().kvq_evict_select(*args, _stream(stream)))
+
+
+def kvq_evict_gather_int4(cache, num_pages: int, block_table, keep, new_lens, dst_cache, dst_num_pages: int,
+                          dst_block_table, weights=None, weights_out=None, err_count=None, stream=None):
+    """Moves the tokens of keep [B, H_kv, budget] from the pages of block_table into those of dst_block_table (and their
+    weights [B, H_kv, tokens] into weights_out, whose rows are zero past them)."""
+    B, h_kv, budget = keep.shape
+    _shape(new_lens, (B,), "new_lens")
+    for x, name in ((block_table, "block_table"), (dst_block_table, "dst_block_table")):
+        if x.dim() != 2 or x.shape[0] != B:
+            raise ValueError(f"{name} must have shape ({B}, pages), got {tuple(x.shape)}")
+    if (weights is None) != (weights_out is None):
+        raise ValueError("weights and weights_out go together")
+    for x, name in ((weights, "weights"), (weights_out, "weights_out")):
+        if x is not None and (x.dim() != 3 or tuple(x.shape[:2]) != (B, h_kv)):
+            raise ValueError(f"{name} must have shape ({B}, {h_kv}, tokens), got {tuple(x.shape)}")
+    _pool(cache, num_pages, h_kv, "cache")
+    _pool(dst_cache, dst_num_pages, h_kv, "dst_cache")
+    args = (_dev(cache, torch.uint8, "cache"), int(num_pages), _dev(block_table, torch.int32, "block_table"),
+            block_table.shape[1], _dev(keep, torch.int32, "keep"), budget, _dev(new_lens, torch.int32, "new_lens"),
+            B, h_kv, 128, _dev(dst_cache, torch.uint8, "dst_cache"), int(dst_num_pages),
+            _dev(dst_block_table, torch.int32, "dst_block_table"), dst_block_table.shape[1],
+            _dev(weights, torch.float32, "weights"), 0 if weights is None else weights.shape[2],
+            _dev(weights_out, torch.float32, "weights_out"), 0 if weights_out is None else weights_out.shape[2],
+            _dev(err_count, torch.int32, "err_count"))
+    _one_device(cache, block_table, keep, new_lens, dst_cache, dst_block_table, weights, weights_out, err_count)
+    _check(load().kvq_evict_gather_int4(*args, _stream(stream)))
 
 
 # -------------------------------------------------------------- Block-GTQ

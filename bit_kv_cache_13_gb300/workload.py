@@ -96,6 +96,67 @@ class Int2Layer:
         return int(self.context_lens.sum().item()) * self.spec.h_kv * 96
 
 
+class Int4Layer(Int2Layer):
+    """One attention layer's INT4 cache on `device`: the same parameters as
+    the INT2 layer, per-token attention weights [B, H_kv, tokens], and
+    eviction down to a budget by those weights."""
+
+    def __init__(self, spec: Spec, layer: int, device="cuda", block_table=None, extra_pages: int = 0):
+        super().__init__(spec, layer, device, block_table, extra_pages)
+        self.tile = _lib.kvq_int4_tile_bytes(spec.d)
+        self.cache = torch.zeros((self.num_pages, spec.h_kv, self.tile), dtype=torch.uint8, device=device)
+        self.weights = torch.zeros((spec.batch, spec.h_kv, self.block_table.shape[1] * PAGE_SIZE), device=device)
+
+    def append(self, k, v, slots, err_count=None):
+        _lib.kvq_append_int4(k, v, slots, self.mu, self.R_k, self.R_v, self.cache, self.num_pages,
+                             err_count=err_count)
+
+    def prefill(self, chunk: int = 1 << 16):
+        pos = history_positions(self.spec)
+        for b in range(self.spec.batch):
+            k, v = self.history_kv(b)
+            if self.mu is None:
+                self.mu = inputs.key_centre(k).to(self.device).contiguous()
+            sl = self.slots(b, pos)
+            for s in range(0, k.shape[0], chunk):
+                e = min(k.shape[0], s + chunk)
+                self.append(k[s:e].contiguous(), v[s:e].contiguous(), sl[s:e].contiguous())
+            del k, v
+
+    def workspace(self, num_splits: int = 0, weights: bool = True) -> torch.Tensor:
+        n = _lib.kvq_int4_workspace_bytes(self.spec.batch, self.spec.h_q, self.spec.h_kv, self.block_table.shape[1],
+                                          num_splits, weights)
+        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    def decode(self, q, out, ws, num_splits: int = 0, decay: float | None = None):
+        """Attends over context_lens tokens; with decay given, accumulates
+        the tokens' attention weights too."""
+        args = (q, self.cache, self.num_pages, self.block_table, self.context_lens, self.R_k, self.R_v, self.scale, out)
+        if decay is None:
+            _lib.kvq_decode_attn_int4(*args, ws, num_splits)
+        else:
+            _lib.kvq_decode_attn_int4_weights(*args, self.weights, decay, ws, num_splits)
+
+    def evict(self, budget: int, sinks: int, recent: int, dst_block_table) -> torch.Tensor:
+        """Shrinks every sequence to at most `budget` tokens, moved into the
+        pages of dst_block_table [B, pages] (of this layer's pool, none of
+        them in use), which becomes the block table.  Returns keep
+        [B, H_kv, budget], the kept tokens' earlier indices."""
+        B, h_kv = self.spec.batch, self.spec.h_kv
+        keep = torch.empty((B, h_kv, budget), dtype=torch.int32, device=self.device)
+        new_lens = torch.empty(B, dtype=torch.int32, device=self.device)
+        _lib.kvq_evict_select(self.weights, self.context_lens, budget, sinks, recent, keep, new_lens)
+        weights = torch.empty((B, h_kv, dst_block_table.shape[1] * PAGE_SIZE), device=self.device)
+        _lib.kvq_evict_gather_int4(self.cache, self.num_pages, self.block_table, keep, new_lens, self.cache,
+                                   self.num_pages, dst_block_table, self.weights, weights)
+        self.block_table, self.context_lens, self.weights = dst_block_table, new_lens, weights
+        return keep
+
+    def packed_bytes_per_decode(self) -> int:
+        """160 B per attended token-head."""
+        return int(self.context_lens.sum().item()) * self.spec.h_kv * (self.tile // PAGE_SIZE)
+
+
 class BgtqLayer:
     """One attention layer's Block-GTQ cache and parameters on `device`:
     per-head widths from the greedy allocator (library, host) over the

@@ -1,8 +1,9 @@
 /*
  * kvq.h - C ABI of the rotated low-bit KV-cache library (libkvq.so).
  *
- * Two cache formats, each with a quantise-on-append call and a fused
- * packed-cache decode-attention call, plus two host-only helpers:
+ * Three cache formats, each with a quantise-on-append call and a fused
+ * packed-cache decode-attention call, eviction for the INT4 one, and two
+ * host-only helpers:
  *
  *   INT2     "Output-Aware Rotation for INT2 KV-Cache Quantization":
  *            keys centred per head (§1, attention-equivalent
@@ -290,6 +291,138 @@ kvq_status kvq_decode_attn_int2_noalloc(const void* q, int B, int H_q, int H_kv,
  * kvq_workspace_status then reports KVQ_ERR_CUDA.  Nothing faults or hangs;
  * the output of that call is incomplete. */
 void kvq_debug_drop_next_copy(void);
+
+/* ------------------------------------------------------------------ INT4 */
+
+/* The INT4 cache: the INT2 cache's paging, centring and rotations with 4-bit
+ * codes (16 levels per group of 32 rotated channels, fp16 scale and min), its
+ * single-token decode attention, the same with accumulated token weights, and
+ * the eviction that goes by them.
+ *
+ * Bytes of one (page, KV head) tile (2560 at d = 128; 160 per token-head):
+ *   [   0, 1024) K codes, 16 slots x 64 B: channel 32*g + 8*t + i (g, t = 0..3,
+ *                i = 0..7) of slot s is nibble i (bits 4i..4i+3) of the 32-bit
+ *                word at 64*s + 16*t + 4*g
+ *   [1024, 1280) K meta, 16 slots x (4 fp16 scales, 4 fp16 mins)
+ *   [1280, 2304) V codes, 8 slot pairs x 128 B: channel 32*g + 4*r + i (r = 0..7,
+ *                i = 0..3) of slot s is nibble i of the 16-bit half s%2 of the
+ *                word at 1280 + 128*(s/2) + 16*r + 4*g
+ *   [2304, 2432) V scales, 8 slot pairs x 4 groups x (fp16 of slot 2j, of slot 2j+1)
+ *   [2432, 2560) V mins, the same layout
+ * The cache is tiles[num_pages][H_kv].  Returns 0 for unsupported d. */
+size_t kvq_int4_tile_bytes(int d);
+
+/* Quantise-on-append of n_tok tokens into the INT4 cache; k, v, slot_mapping,
+ * mu_k, R_k, R_v and err_count as kvq_append_int2, clip as
+ * kvq_append_int2_clip.  z = (k - mu_k) R_k and w = v R_v are taken as real
+ * numbers (the kernels evaluate them far enough to decide as the exact values
+ * would, up to about 1e-13 relative); per group of 32
+ *   scale = fp16(fp32((clip*max - clip*min) / 15)),  min = fp16(fp32(clip*min)),
+ * both saturating at +-65504, and the code counts the thresholds
+ * min + (c + 1/2)*scale, c = 0..14, strictly below the value (ties to the
+ * lower level); 0 when scale == 0.  A group holding a value that is not finite
+ * is stored with NaN scale and min (it reads back as NaN).  Tokens with equal
+ * slots race (last writer unspecified); what a token's bytes are does not
+ * depend on the tokens appended with it. */
+kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, int H_kv, int d,
+                           const int32_t* slot_mapping, const float* mu_k,
+                           const float* R_k, const float* R_v, float clip,
+                           void* cache, int64_t num_pages, int32_t* err_count, void* stream);
+
+/* Reads cached tokens back: min + code*scale of the tokens at
+ * slot_mapping[0..n), still centred and rotated, rounded once to bf16.
+ *   k_rot, v_rot  device bf16 [n][H_kv][d], either may be null; a slot outside
+ *                 the cache gives zeros */
+kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int H_kv, int d,
+                            const int32_t* slot_mapping, int n, void* k_rot, void* v_rot,
+                            void* stream);
+
+/* Bytes of workspace for the INT4 decode calls (weights = 0:
+ * kvq_decode_attn_int4; 1: kvq_decode_attn_int4_weights, which also holds the
+ * logits of every query head, 64 * H_q * B * max_pages_per_seq bytes).
+ * num_splits as passed to the call (0 = automatic on the current device).  The
+ * workspace must be zero-filled once before its first use; every call leaves
+ * its tickets at zero.  Calls (and captured graphs) that may overlap on the GPU
+ * need a workspace each.  Its error word is read by kvq_workspace_status.
+ * Returns 0 for invalid sizes. */
+size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq, int num_splits,
+                                int weights);
+
+/* Fused packed-cache decode attention over the INT4 cache:
+ *   o = softmax(<q R_k, K^> * scale) V^ R_v^T,  K^, V^ the cached values.
+ *   q    device bf16 [B][H_q][d]
+ *   out  device bf16 [B][H_q][d], rounded once (zeros for an empty context)
+ * Other arguments, the split of the work, and the treatment of block-table
+ * entries outside [0, num_pages) as kvq_decode_attn_int2.  q and out need
+ * 16-byte alignment. */
+kvq_status kvq_decode_attn_int4(const void* q, int B, int H_q, int H_kv, int d,
+                                const void* cache, int64_t num_pages,
+                                const int32_t* block_table, int max_pages_per_seq,
+                                const int32_t* context_lens,
+                                const float* R_k, const float* R_v, float scale,
+                                void* out, void* workspace, size_t workspace_bytes,
+                                int num_splits, void* stream);
+
+/* kvq_decode_attn_int4 that also accumulates the attention weight each token
+ * drew from the H_q/H_kv query heads of its KV head: for s < context_lens[b]
+ *   weights[b][h][s] = decay * weights[b][h][s] + sum_{j in G(h)} p_{j,s}.
+ *   weights  device fp32, row (b, h) at weights + (b*H_kv + h)*weights_stride;
+ *            weights_stride >= 16 * max_pages_per_seq.  Entries at and past the
+ *            context are not touched; a token starts from what the caller left
+ *            in its entry (0 for a new token).  A token dropped for its block
+ *            table entry draws no weight.
+ *   decay    finite, >= 0 (1: the plain sum over the steps) */
+kvq_status kvq_decode_attn_int4_weights(const void* q, int B, int H_q, int H_kv, int d,
+                                        const void* cache, int64_t num_pages,
+                                        const int32_t* block_table, int max_pages_per_seq,
+                                        const int32_t* context_lens,
+                                        const float* R_k, const float* R_v, float scale,
+                                        void* out, float* weights, int64_t weights_stride, float decay,
+                                        void* workspace, size_t workspace_bytes,
+                                        int num_splits, void* stream);
+
+/* Chooses the tokens each (sequence, KV head) keeps.  With n = context_lens[b]
+ * (clamped to [0, max_tokens]): all of them when n <= budget; else tokens
+ * [0, sinks), tokens [n - recent, n), and of the others the budget - sinks -
+ * recent with the largest weights (equal weights: the lower index; NaN counts
+ * as -inf, -0 as 0).
+ *   weights   device fp32, row (b, h) at weights + (b*H_kv + h)*weights_stride,
+ *             weights_stride >= max_tokens
+ *   keep      device int32 [B][H_kv][budget], written: the kept indices in
+ *             ascending order, then -1
+ *   new_lens  device int32 [B], written: min(n, budget)
+ * 1 <= budget, 0 <= sinks, 0 <= recent, sinks + recent <= budget. */
+kvq_status kvq_evict_select(const float* weights, int64_t weights_stride, int B, int H_kv, int max_tokens,
+                            const int32_t* context_lens, int budget, int sinks, int recent,
+                            int32_t* keep, int32_t* new_lens, void* stream);
+
+/* Moves the kept tokens of the INT4 cache into other pages: token i < new_lens[b]
+ * of KV head h of destination sequence b (slot i % 16 of page
+ * dst_block_table[b][i/16]) becomes source token keep[b][h][i] (page
+ * block_table[b][./16]).  Keys carry their position (they are stored after
+ * RoPE), so the moved tokens attend as before; the heads of a sequence may
+ * keep different tokens.
+ *   keep, new_lens, budget  as kvq_evict_select writes them
+ *   dst_cache        may be the same pool as cache; a destination page must not
+ *                    be a source page of the same call, nor appear twice
+ *   dst_block_table  device int32 [B][dst_max_pages], 16*dst_max_pages >= budget
+ *   weights          nullable; else row (b, h) of the accumulated weights as
+ *                    above: weights_out[b][h][i] = weights[b][h][keep[b][h][i]]
+ *                    for i < new_lens[b], and 0 for the rest of the row's
+ *                    16*dst_max_pages entries (so tokens appended later start
+ *                    from 0).  weights_out must not overlap weights.
+ *   err_count        nullable device int32, incremented once per kept
+ *                    token-head whose index or source or destination page is out
+ *                    of range; the destination slot is then left as it was (a
+ *                    bad index or source page moves weight 0)
+ * Bytes of destination slots at and past new_lens[b] are not touched. */
+kvq_status kvq_evict_gather_int4(const void* cache, int64_t num_pages, const int32_t* block_table,
+                                 int max_pages_per_seq, const int32_t* keep, int budget,
+                                 const int32_t* new_lens, int B, int H_kv, int d,
+                                 void* dst_cache, int64_t dst_num_pages, const int32_t* dst_block_table,
+                                 int dst_max_pages, const float* weights, int64_t weights_stride,
+                                 float* weights_out, int64_t weights_out_stride, int32_t* err_count,
+                                 void* stream);
 
 /* ------------------------------------------------------------- Block-GTQ */
 

@@ -16,6 +16,8 @@ Modules
   int2       rotated INT2 group quantisation D_R(z) = Q2(zR) R^T (§3.1 Eq. 4),
              attention-equivalent key centring (§1), paged cache format,
              packed-cache decode attention.
+  int4       the INT2 cache's form with 16 levels per group: append, decode
+             with accumulated token weights, eviction by those weights.
   bgtq       Gaussian Lloyd-Max codebooks, TQ-MSE encode/decode, greedy
              RoPE-block bit allocation (Theorem 1), grouped encoding and the
              packed Block-GTQ cache (RoPE-Aware Bit Allocation for KV-Cache
