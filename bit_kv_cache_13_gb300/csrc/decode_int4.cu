@@ -26,13 +26,24 @@
 //           Up to four heads fill the eight columns as (tokens 0..7, tokens 8..15) of
 //           each head, which the end adds.  The mins are one more MMA.
 //
+// Three kernels, chained by programmatic dependent launch so that each one's
+// start overlaps the end of the one before:
+//   1 rotate   q' of every (sequence, KV head), laid out as the MMA operand
+//   2 stream   the cached pages; one partial (m, l, o') per CTA and unit
+//   3 finish   merges a unit's partials by the log-sum-exp rule, rotates once by
+//              R_v^T and writes the output; in the weights form more CTAs of the same
+//              launch turn the logits that the stream left into token weights
+// Rotating inside the streaming CTAs cost each (sequence, KV head) that a CTA
+// touches about 7 us during which it streamed nothing (32 ragged sequences up to
+// 4K, 8 KV heads: 166 us).  The stream kernel's warps never wait for one another:
+// each walks the CTA's units by itself, its ring running ahead into the next
+// unit's pages; the last warp to leave a unit merges the twelve partials, which
+// stand in ring slots of their own until then.
+//
 // The work is split over the CTAs on the device, by the real page counts: the
 // pages of all (sequence, KV head) units are laid end to end and every CTA takes
 // an equal share, so a ragged batch or a short context in a long table stays
-// balanced.  A CTA publishes one partial (m, l, o') per unit its share touches;
-// the last to finish a unit (atomic ticket, no waiting) merges them by the
-// log-sum-exp rule, rotates once by R_v^T and writes the output.  A unit with one
-// partial is finished from shared memory.
+// balanced.
 #include <mutex>
 
 #include "int4_common.cuh"
@@ -68,6 +79,18 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     return y;
 }
 
+// The rotated queries of a unit as the stream kernel takes them: QK operands of
+// the 8 k steps and 32 lanes (b0, b1 of the column's part; for NT == 2 the high
+// part's, then the low part's), the min term's operand, and 2^24 / sigma and
+// 1 / sigma_s of each head.
+template <int NT>
+struct __align__(16) D4Query {
+    uint32_t bq[8][32][2 * NT];
+    uint32_t bs[32][NT];
+    float inv_q[4 * NT], inv_s[4 * NT];
+};
+static_assert(sizeof(D4Query<1>) % 16 == 0 && sizeof(D4Query<2>) % 16 == 0, "bulk copies take multiples of 16 bytes");
+
 struct D4Args {
     const __nv_bfloat16* q;
     int B, H_q, H_kv, G;
@@ -80,65 +103,192 @@ struct D4Args {
     float scale_log2;
     __nv_bfloat16* out;
     uint8_t* ws;
+    void* query;       // D4Query [unit]
+    int2* info;        // [unit] first CTA, partials
     float* partials;   // [unit + CTA][G][PART_STRIDE]
     float* logits;     // [unit][16 max_pages][G], base 2 (weights form)
-    float2* stats;     // [unit][G] (maximum, 1 / sum) (weights form)
     int automatic;     // the split is the kernel's choice (else the grid's)
+    // weights form
+    float* weights;
+    int64_t wstride;
+    float decay;
+    int n_finish, chunks;
 };
 
-template <int MAXG>
+// ------------------------------------------------------------------ 1: rotate
+
+// One CTA of 256 threads per KV head and run of `per` sequences; a thread
+// holds half a column of R_k in registers.
+template <int NT>
+__global__ void __launch_bounds__(256) rotate_int4_kernel(const __grid_constant__ D4Args a, int per) {
+    constexpr int MAXG = 4 * NT;
+    __shared__ __align__(16) float qin[MAXG][D], red[2][MAXG][D], qs[MAXG][D];
+    __shared__ float gsum[MAXG][NGROUP], sigma[MAXG], sigma_s[MAXG];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
+    const int h = blockIdx.x, G = a.G, c = tid & (D - 1), half = tid >> 7;
+    const float* R = a.Rk + (size_t)h * D * D;
+    for (int i = tid; i < D * D / 32; i += 256) prefetch_l2(R + 32 * i);
+    griddep_wait();
+    griddep_launch_dependents();  // (after the wait: what the next kernel reads early is complete)
+    float rr[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) rr[i] = __ldg(R + (size_t)(64 * half + i) * D + c);
+    for (int b = blockIdx.y * per; b < min(a.B, (int)(blockIdx.y + 1) * per); ++b) {
+        const __nv_bfloat16* qb = a.q + ((size_t)b * a.H_q + (size_t)h * G) * D;
+        for (int i = tid; i < MAXG * D; i += 256) qin[i / D][i % D] = i < G * D ? __bfloat162float(qb[i]) : 0.f;
+        __syncthreads();
+        float acc[MAXG];
+#pragma unroll
+        for (int j = 0; j < MAXG; ++j) acc[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4)
+#pragma unroll
+            for (int j = 0; j < MAXG; ++j) {
+                const float4 x = *reinterpret_cast<const float4*>(&qin[j][64 * half + i]);
+                acc[j] = fmaf(x.x, rr[i], fmaf(x.y, rr[i + 1], fmaf(x.z, rr[i + 2], fmaf(x.w, rr[i + 3], acc[j]))));
+            }
+#pragma unroll
+        for (int j = 0; j < MAXG; ++j) red[half][j][c] = acc[j];
+        __syncthreads();
+        // per head: the pre-scales (largest |q'| and |S| into [2^14, 2^15)) and the group sums
+        if (warp < MAXG) {
+            const int j = warp;
+            float mx = 0.f, ms = 0.f, gs[NGROUP];
+#pragma unroll
+            for (int g = 0; g < NGROUP; ++g) {
+                const int ch = 32 * g + lane;
+                const float x = (red[0][j][ch] + red[1][j][ch]) * a.scale_log2;
+                qs[j][ch] = x;
+                mx = fmaxf(mx, fabsf(x));
+                gs[g] = x;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll
+                for (int g = 0; g < NGROUP; ++g) gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], o);
+            }
+#pragma unroll
+            for (int g = 0; g < NGROUP; ++g) ms = fmaxf(ms, fabsf(gs[g]));
+            if (lane == 0) {
+                sigma[j] = d4_prescale(mx);
+                sigma_s[j] = d4_prescale(ms);
+#pragma unroll
+                for (int g = 0; g < NGROUP; ++g) gsum[j][g] = gs[g];
+            }
+        }
+        __syncthreads();
+        // K step s = 2 g + hs: b0 = channels 32 g + 8 t + 2 hs and + 4 (codes in the low
+        // nibble), b1 = the channels after those (the next nibble: 16 times the code)
+        auto parts = [](float v0, float v1, bool low) {
+            const float h0 = __half2float(__float2half_rn(v0)), h1 = __half2float(__float2half_rn(v1));
+            return low ? pack_half2(v0 - h0, v1 - h1) : pack_half2(h0, h1);
+        };
+        auto q_frag = [&](int j, int e, bool low) {
+            const int c0 = 32 * (warp >> 1) + 8 * t + 2 * (warp & 1) + e;
+            const float f = sigma[j] * (e ? 0.0625f : 1.f);
+            return parts(qs[j][c0] * f, qs[j][c0 + 4] * f, low);
+        };
+        auto s_frag = [&](int j, bool low) {  // group sums 2 t, 2 t + 1 (t < 2)
+            return t >= 2 ? 0u : parts(gsum[j][2 * t] * sigma_s[j], gsum[j][2 * t + 1] * sigma_s[j], low);
+        };
+        D4Query<NT>& out = static_cast<D4Query<NT>*>(a.query)[(size_t)b * a.H_kv + h];
+        if constexpr (NT == 1) {  // column r: head r / 2, high (r even) or low part
+            *reinterpret_cast<uint2*>(out.bq[warp][lane]) = make_uint2(q_frag(r >> 1, 0, r & 1), q_frag(r >> 1, 1, r & 1));
+            if (warp == 0) out.bs[lane][0] = s_frag(r >> 1, r & 1);
+        } else {                  // column r: head r
+            *reinterpret_cast<uint4*>(out.bq[warp][lane]) =
+                make_uint4(q_frag(r, 0, false), q_frag(r, 1, false), q_frag(r, 0, true), q_frag(r, 1, true));
+            if (warp == 0) *reinterpret_cast<uint2*>(out.bs[lane]) = make_uint2(s_frag(r, false), s_frag(r, true));
+        }
+        if (tid < MAXG) {
+            out.inv_q[tid] = 16777216.f / sigma[tid];
+            out.inv_s[tid] = 1.f / sigma_s[tid];
+        }
+        // (the next round's first barrier comes before anything read here is overwritten,
+        // but for qin, last read before the second barrier above)
+    }
+}
+
+// ------------------------------------------------------------------ 2: stream
+
+__device__ __forceinline__ int d4_pages(const D4Args& a, int b) {
+    const int c = __ldg(a.context_lens + b);
+    return c <= 0 ? 0 : min((int)(((int64_t)c + PAGE - 1) / PAGE), a.max_pages);
+}
+
+// A CTA's walk over its share: pages [pa, pb) of unit (b, h), which has np, and
+// `left` pages of the share after them.
+struct D4Walk {
+    int b, h, np, pa, pb, left;
+    __device__ __forceinline__ void clip(int share) {
+        pb = min((int64_t)np, (int64_t)pa + share);
+        left = share - (pb - pa);
+    }
+    __device__ __forceinline__ void next(const D4Args& a) {  // needs left > 0
+        if (++h == a.H_kv) {
+            h = 0;
+            do np = d4_pages(a, ++b);
+            while (np == 0);
+        }
+        pa = 0;
+        clip(left);
+    }
+    // units of D4_U pages that warp w takes of the segment (its pages are dealt round-robin)
+    __device__ __forceinline__ int units(int w) const {
+        const int n = pb - pa;
+        const int mine = n > w ? (n - w + D4_NW - 1) / D4_NW : 0;
+        return (mine + D4_U - 1) / D4_U;
+    }
+};
+
+template <int NT>
 struct __align__(128) D4Smem {
-    uint8_t ring[D4_NW][D4_STAGES][INT4_TILE];  // pages in flight; after a unit's last page, the warp's o' [G][D]
-    uint64_t bar[D4_NW][D4_UNITS];
+    uint8_t ring[D4_NW][D4_STAGES][INT4_TILE];  // pages in flight; a unit's last slots keep the warp's o' [4 NT][D]
+    D4Query<NT> query[2];                       // of segments s, s + 1
+    uint64_t bar[D4_NW][D4_UNITS], qbar[2], free_bar[2];
     int ntok[D4_NW][D4_STAGES];                 // valid tokens of the page in each slot
-    float qin[MAXG][D];
-    float q[MAXG][D];                           // q' * scale * log2(e); at the end the merged output
-    float red[D4_NW][D];                        // partial sums of the rotation (3 parts a head) and of the merge
-    float red2[MAXG == 8 ? 3 * MAXG - D4_NW : 1][D];
-    uint4 bq[MAXG == 8 ? 8 : 1][32];            // eight heads: QK operands (high b0, b1, low b0, b1) per k step
-    float gsum[MAXG][NGROUP];
-    float sigma[MAXG], sigma_s[MAXG];           // power-of-two pre-scales of q' and S
-    float m_part[D4_NW][MAXG], l_part[D4_NW][MAXG];
-    float Mh[MAXG], Lh[MAXG];
+    float m_part[2][D4_NW][4 * NT], l_part[2][D4_NW][4 * NT];
+    int part_at[2][D4_NW];                      // ring group that holds the warp's o', -1: no pages
+    int arrived[2];
     int64_t scan[D4_NW];
     int scan_max[D4_NW], scan_n[D4_NW];
     int64_t base0;
-    int b0, is_last, dead;
+    int b0;
 };
-static_assert(sizeof(D4Smem<4>) <= 227 * 1024 && sizeof(D4Smem<8>) <= 227 * 1024, "decode shared memory above 227 KB");
-static_assert(8 * D * 4 <= D4_STAGES * INT4_TILE, "a warp's partial fits its ring");
+static_assert(sizeof(D4Smem<1>) <= 227 * 1024 && sizeof(D4Smem<2>) <= 227 * 1024, "decode shared memory above 227 KB");
+static_assert(8 * D * 4 <= D4_U * INT4_TILE, "a warp's partial fits one ring group");
 
 // NT = 1: up to four query heads per KV head, NT = 2: up to eight.
 template <int NT, bool WTS>
 __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid_constant__ D4Args a) {
-    constexpr int MAXG = 4 * NT;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    D4Smem<MAXG>& sm = *reinterpret_cast<D4Smem<MAXG>*>(smem_raw);
+    D4Smem<NT>& sm = *reinterpret_cast<D4Smem<NT>*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, t = lane & 3;
     const int G = a.G, cta = blockIdx.x;
-    auto pages_of = [&](int b) {
-        const int c = __ldg(a.context_lens + b);
-        return c <= 0 ? 0 : min((int)(((int64_t)c + PAGE - 1) / PAGE), a.max_pages);
-    };
     if (lane == 0) {
         for (int k = 0; k < D4_UNITS; ++k) mbar_init(&sm.bar[warp][k], 1);
+        if (warp < 2) {
+            mbar_init(&sm.qbar[warp], 1);
+            mbar_init(&sm.free_bar[warp], 1);
+            sm.arrived[warp] = 0;
+        }
         fence_mbar_init();
     }
-    if (tid == 0) sm.dead = 0;
-    griddep_wait();
 
     // ---- the split: pages of all sequences (a thread sums a run of them), the
-    // CTAs that take part, and where this one's share begins
-    int64_t V, g, g1;
-    int Ceff;
-    bool empties;
+    // CTAs that take part, and where this one's share begins.  Context lengths,
+    // block table and cache are read before the dependency wait: the rotate kernel
+    // let this one start only after its own wait, when everything before it was done.
+    int64_t V, g0;
+    int Ceff, share;
     {
         const int per = (a.B + D4_THREADS - 1) / D4_THREADS, s0 = min(a.B, tid * per), s1 = min(a.B, s0 + per);
         int64_t own = 0;
         int mx = 0, ne = 0;
         for (int b = s0; b < s1; ++b) {
-            const int p = pages_of(b);
+            const int p = d4_pages(a, b);
             own += p;
             mx = max(mx, p);
             ne += p > 0;
@@ -169,7 +319,6 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
             mx = max(mx, sm.scan_max[w]);
             ne += sm.scan_n[w];
         }
-        empties = ne < a.B;
         V = P * a.H_kv;
         int64_t C = gridDim.x;
         if (a.automatic) {
@@ -184,198 +333,144 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         }
         if (C > V) C = V;
         Ceff = (int)C;
-        g = g1 = 0;
-        if (cta < Ceff) {
-            g = (int64_t)cta * V / C;
-            g1 = (int64_t)(cta + 1) * V / C;
-            int64_t first = (before + inc - own) * a.H_kv;
-            if (g >= first && g < first + own * a.H_kv) {
-                int b = s0;
-                for (; b < s1; ++b) {
-                    const int64_t n = (int64_t)pages_of(b) * a.H_kv;
-                    if (g < first + n) break;
-                    first += n;
-                }
-                sm.b0 = b;
-                sm.base0 = first;
+        if (cta >= Ceff) {
+            griddep_wait();  // (a grid is complete only after the one before it)
+            return;
+        }
+        g0 = (int64_t)cta * V / C;
+        share = (int)((int64_t)(cta + 1) * V / C - g0);
+        int64_t first = (before + inc - own) * a.H_kv;
+        if (g0 >= first && g0 < first + own * a.H_kv) {
+            int b = s0;
+            for (; b < s1; ++b) {
+                const int64_t n = (int64_t)d4_pages(a, b) * a.H_kv;
+                if (g0 < first + n) break;
+                first += n;
             }
+            sm.b0 = b;
+            sm.base0 = first;
+        }
+        __syncthreads();
+    }
+    D4Walk cs;  // what this warp consumes
+    {
+        cs.b = sm.b0;
+        cs.np = d4_pages(a, cs.b);
+        const int64_t in = g0 - sm.base0;
+        cs.h = (int)(in / cs.np);
+        cs.pa = (int)(in - (int64_t)cs.h * cs.np);
+        cs.clip(share);
+    }
+
+    // ---- what it issues, up to D4_UNITS units ahead, across segments.  Lane 2 x + e
+    // of a batch holds page e of the batch's unit x: its id, KV head and valid tokens
+    // (0: past the warp's pages).  The next batch's ids load while this one is issued.
+    D4Walk is = cs;
+    int ik = 0, in = is.units(warp), issued = 0, built = 0;
+    auto build = [&](int& pid, int& hn) {  // the 16 units after the first `built`
+        pid = hn = 0;
+        int x = 0;
+        while (x < 16) {
+            if (ik >= in) {
+                if (is.left == 0) break;
+                is.next(a);
+                ik = 0;
+                in = is.units(warp);
+                continue;
+            }
+            const int take = min(16 - x, in - ik), y = (lane >> 1) - x;
+            const int page = is.pa + warp + D4_NW * (D4_U * (ik + y) + (lane & 1));
+            if (y >= 0 && y < take && page < is.pb) {
+                pid = __ldg(a.block_table + (size_t)is.b * a.max_pages + page);
+                hn = is.h << 8 | (page + 1 < is.np ? PAGE : min(PAGE, __ldg(a.context_lens + is.b) - page * PAGE));
+            }
+            ik += take;
+            x += take;
+        }
+        built += x;
+    };
+    int pid_c, hn_c, pid_n, hn_n;
+    build(pid_c, hn_c);
+    build(pid_n, hn_n);
+    const uint64_t policy = l2_policy_evict_first();
+    // Lanes e < D4_U issue page e of the next unit (a page with a bad id counts no tokens).
+    auto issue_next = [&]() {
+        if (issued > 0 && issued % 16 == 0) {
+            pid_c = pid_n;
+            hn_c = hn_n;
+            build(pid_n, hn_n);
+        }
+        const int st = issued % D4_UNITS, from = D4_U * (issued % 16) + (lane & 1);
+        const int pid = __shfl_sync(0xffffffffu, pid_c, from), hn = __shfl_sync(0xffffffffu, hn_c, from);
+        uint64_t* bar = &sm.bar[warp][st];
+        const bool page = lane < D4_U && hn & 255, ok = page && pid >= 0 && (int64_t)pid < a.num_pages;
+        if (page && !ok) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_BAD_PAGE);
+        if (lane < D4_U) sm.ntok[warp][D4_U * st + lane] = ok ? hn & 255 : 0;
+        const uint32_t n_ok = __popc(__ballot_sync(0xffffffffu, ok));
+        __syncwarp();  // the counts are ordered before lane 0's arrive
+        if (lane == 0) {
+            if (n_ok == 0)
+                mbar_arrive(bar);
+            else
+                mbar_arrive_expect_tx(bar, n_ok * INT4_TILE);
+        }
+        __syncwarp();  // the expected bytes are set before any copy is issued
+        if (ok)
+            bulk_g2s_hint(sm.ring[warp][D4_U * st + lane], a.cache + ((size_t)pid * a.H_kv + (hn >> 8)) * INT4_TILE,
+                          INT4_TILE, bar, policy);
+        ++issued;
+    };
+#pragma unroll 1
+    for (int k = 0; k < D4_UNITS && issued < built; ++k) issue_next();
+
+    griddep_wait();  // the rotated queries are there
+    griddep_launch_dependents();
+    auto fetch_query = [&](const D4Walk& w, int buf) {  // one thread
+        mbar_arrive_expect_tx(&sm.qbar[buf], sizeof(D4Query<NT>));
+        bulk_g2s(&sm.query[buf], static_cast<const D4Query<NT>*>(a.query) + ((size_t)w.b * a.H_kv + w.h), sizeof(D4Query<NT>),
+                 &sm.qbar[buf]);
+    };
+    if (tid == 0) {
+        fetch_query(cs, 0);
+        if (cs.left > 0) {
+            D4Walk w = cs;
+            w.next(a);
+            fetch_query(w, 1);
         }
     }
-    if (empties)  // sequences without tokens: zeros
-        for (int b = cta; b < a.B; b += gridDim.x)
-            if (pages_of(b) == 0)
-                for (int i = tid; i < a.H_q * D; i += D4_THREADS)
-                    a.out[(size_t)b * a.H_q * D + i] = __float2bfloat16_rn(0.f);
-    if (g >= g1) return;
-    __syncthreads();
 
-    auto cta_of = [&](int64_t x) { return (int)(((x + 1) * Ceff - 1) / V); };
-    int b = sm.b0;
-    int64_t base = sm.base0;  // first page of unit (b, 0)
-    int np = pages_of(b);
-    int h = (int)((g - base) / np);
-    int kbase = 0;            // units this warp consumed in earlier segments
-    while (true) {
-        // ================ segment: pages [pa, pb) of unit (b, h)
-        const int64_t ub = base + (int64_t)h * np;
-        const int pa = (int)(g - ub), pb = (int)min((int64_t)np, g1 - ub);
-        const size_t u = (size_t)b * a.H_kv + h;
-        const int ctx = min(__ldg(a.context_lens + b), a.max_pages * PAGE);
-        const int32_t* bt = a.block_table + (size_t)b * a.max_pages;
-        const int count = sm.dead ? 0 : pb - pa;
-        const int my_count = count > warp ? (count - warp + D4_NW - 1) / D4_NW : 0;
-        const int n_units = (my_count + D4_U - 1) / D4_U;
-        auto page_of = [&](int j) { return pa + warp + D4_NW * j; };
-        int pid_first[D4_UNITS], pid_next = 0;
-#pragma unroll
-        for (int k = 0; k <= D4_UNITS; ++k) {
-            const int j = D4_U * k + lane;
-            const int pid = lane < D4_U && j < my_count ? __ldg(bt + page_of(j)) : 0;
-            if (k < D4_UNITS)
-                pid_first[k] = pid;
-            else
-                pid_next = pid;
+    bool dead = false;  // a wait of this warp ran out: it takes part without data
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = mbar_wait_bounded(bar, parity, WAIT_LIMIT_CYCLES);
+        if (__any_sync(0xffffffffu, !ok)) {
+            if (lane == 0) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_TIMEOUT);
+            dead = true;
         }
-        // Lanes e < D4_U issue page e of unit k into ring group st and record its valid
-        // tokens (0 for a page past the warp's or a bad id).
-        auto issue_unit = [&](int k, int st, int pid) {
-            uint64_t* bar = &sm.bar[warp][st];
-            const int j = D4_U * k + lane;
-            bool ok = false;
-            if (lane < D4_U) {
-                int n = 0;
-                if (j < my_count) {
-                    if (pid < 0 || (int64_t)pid >= a.num_pages) {
-                        atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_BAD_PAGE);
-                    } else {
-                        ok = true;
-                        n = min(PAGE, ctx - page_of(j) * PAGE);
-                    }
-                }
-                sm.ntok[warp][D4_U * st + lane] = n;
-            }
-            const uint32_t n_ok = __popc(__ballot_sync(0xffffffffu, ok));
-            __syncwarp();  // the counts are ordered before lane 0's arrive
-            if (lane == 0) {
-                if (n_ok == 0)
-                    mbar_arrive(bar);
-                else
-                    mbar_arrive_expect_tx(bar, n_ok * INT4_TILE);
-            }
-            __syncwarp();  // the expected bytes are set before any copy is issued
-            if (ok)
-                bulk_g2s_hint(sm.ring[warp][D4_U * st + lane], a.cache + ((size_t)pid * a.H_kv + h) * INT4_TILE, INT4_TILE,
-                              bar, l2_policy_evict_first());
-        };
-        const int st0 = kbase % D4_UNITS;
-        const uint32_t par0 = (kbase / D4_UNITS) & 1;
-        int n_issued = 0;
-#pragma unroll
-        for (int k = 0; k < D4_UNITS; ++k)
-            if (k < n_units) {
-                issue_unit(k, st0 + k < D4_UNITS ? st0 + k : st0 + k - D4_UNITS, pid_first[k]);
-                n_issued = k + 1;
-            }
-
-        // ---- q' = q R_k * scale * log2(e): thread (channel, third of the inputs)
-        const __nv_bfloat16* qb = a.q + ((size_t)b * a.H_q + (size_t)h * G) * D;
-        for (int i = tid; i < MAXG * D; i += D4_THREADS) sm.qin[i / D][i % D] = i < G * D ? __bfloat162float(qb[i]) : 0.f;
-        auto red_row = [&](int part, int j) -> float* {
-            const int x = part * MAXG + j;
-            return x < D4_NW ? sm.red[x] : sm.red2[x - D4_NW];
-        };
-        {
-            constexpr int PER = 44;  // 44 + 44 + 40 inputs, four at a time
-            const int c = tid & (D - 1), part = tid >> 7, i0 = part * PER, i1 = min(D, i0 + PER);
-            const float* R = a.Rk + (size_t)h * D * D + c;
-            float rr[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) rr[i] = i0 + i < i1 ? __ldg(R + (size_t)(i0 + i) * D) : 0.f;
-            __syncthreads();
-            float acc[MAXG];
-#pragma unroll
-            for (int j = 0; j < MAXG; ++j) acc[j] = 0.f;
-#pragma unroll
-            for (int i = 0; i < PER; i += 4)
-                if (i0 + i < i1) {
-#pragma unroll
-                    for (int j = 0; j < MAXG; ++j) {
-                        const float4 x = *reinterpret_cast<const float4*>(&sm.qin[j][i0 + i]);
-                        acc[j] = fmaf(x.x, rr[i], fmaf(x.y, rr[i + 1], fmaf(x.z, rr[i + 2], fmaf(x.w, rr[i + 3], acc[j]))));
-                    }
-                }
-#pragma unroll
-            for (int j = 0; j < MAXG; ++j) red_row(part, j)[c] = acc[j];
-        }
-        __syncthreads();
-        // per head: sum the parts, the pre-scales (largest |q'| and |S| into [2^14, 2^15)) and the group sums
-        if (warp < MAXG) {
-            const int j = warp;
-            float mx = 0.f, ms = 0.f, gs[NGROUP];
-#pragma unroll
-            for (int gg = 0; gg < NGROUP; ++gg) {
-                const int c = 32 * gg + lane;
-                const float x = (red_row(0, j)[c] + red_row(1, j)[c] + red_row(2, j)[c]) * a.scale_log2;
-                sm.q[j][c] = x;
-                mx = fmaxf(mx, fabsf(x));
-                gs[gg] = x;
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-#pragma unroll
-                for (int gg = 0; gg < NGROUP; ++gg) gs[gg] += __shfl_xor_sync(0xffffffffu, gs[gg], o);
-            }
-#pragma unroll
-            for (int gg = 0; gg < NGROUP; ++gg) ms = fmaxf(ms, fabsf(gs[gg]));
-            if (lane == 0) {
-                sm.sigma[j] = d4_prescale(mx);
-                sm.sigma_s[j] = d4_prescale(ms);
-#pragma unroll
-                for (int gg = 0; gg < NGROUP; ++gg) sm.gsum[j][gg] = gs[gg];
+    };
+    int done = 0;               // units consumed
+    int end1 = 0, end2 = 0;     // `done` at the end of the last segment, of the one before
+    int freed = 0;              // units whose ring groups may be issued into again
+    auto refill = [&]() {
+        if (issued >= min(built, freed + D4_UNITS) || dead) return;
+        fence_proxy_async_smem();  // the groups were read (and written) as ordinary memory
+#pragma unroll 1
+        do issue_next();
+        while (issued < min(built, freed + D4_UNITS));
+    };
+    for (int s = 0;; ++s) {
+        // ================ segment s: pages [pa, pb) of unit (b, h)
+        const size_t u = (size_t)cs.b * a.H_kv + cs.h;
+        const int buf = s & 1;
+        if (s >= 2) {
+            // segment s - 2 is merged: its buffers, this one's queries (fetched by its last
+            // warp) and the ring groups that held its partials
+            wait(&sm.free_bar[buf], ((s - 2) >> 1) & 1);
+            if (freed < end2) {
+                freed = end2;
+                refill();
             }
         }
-        __syncthreads();
-        // ---- QK operands.  K step 2 g + hs: b0 = channels 32 g + 8 t + 2 hs, + 4 (codes in
-        // the low nibble), b1 = the channels after those (the next nibble, code * 16).
-        auto q_frag = [&](int j, int s, int e, bool low) -> uint32_t {  // head j, k step s, register e
-            const int c0 = 32 * (s >> 1) + 8 * t + 2 * (s & 1) + e;
-            const float f = sm.sigma[j] * (e ? 0.0625f : 1.f);
-            const float v0 = sm.q[j][c0] * f, v1 = sm.q[j][c0 + 4] * f;
-            const float h0 = __half2float(__float2half_rn(v0)), h1 = __half2float(__float2half_rn(v1));
-            return low ? pack_half2(v0 - h0, v1 - h1) : pack_half2(h0, h1);
-        };
-        auto s_frag = [&](int j, bool low) -> uint32_t {  // group sums 2 t, 2 t + 1 (t < 2)
-            if (t >= 2) return 0u;
-            const float v0 = sm.gsum[j][2 * t] * sm.sigma_s[j], v1 = sm.gsum[j][2 * t + 1] * sm.sigma_s[j];
-            const float h0 = __half2float(__float2half_rn(v0)), h1 = __half2float(__float2half_rn(v1));
-            return low ? pack_half2(v0 - h0, v1 - h1) : pack_half2(h0, h1);
-        };
-        uint32_t bq[NT == 1 ? 8 : 1][2], bs[2];
-        float inv_q[NT], inv_s[NT];  // NT == 1: head t; NT == 2: heads 2 t, 2 t + 1
-        if constexpr (NT == 1) {     // column r: head r / 2, high (r even) or low part
-            const int j = r >> 1;
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                bq[s][0] = q_frag(j, s, 0, r & 1);
-                bq[s][1] = q_frag(j, s, 1, r & 1);
-            }
-            bs[0] = s_frag(j, r & 1);
-            inv_q[0] = 16777216.f / sm.sigma[t];
-            inv_s[0] = 1.f / sm.sigma_s[t];
-        } else {                     // column r: head r
-            if (warp < 8) sm.bq[warp][lane] = make_uint4(q_frag(r, warp, 0, false), q_frag(r, warp, 1, false),
-                                                         q_frag(r, warp, 0, true), q_frag(r, warp, 1, true));
-            bs[0] = s_frag(r, false);
-            bs[1] = s_frag(r, true);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                inv_q[e] = 16777216.f / sm.sigma[2 * t + e];
-                inv_s[e] = 1.f / sm.sigma_s[2 * t + e];
-            }
-            __syncthreads();
-        }
-
+        const int n_units = dead ? 0 : cs.units(warp);
         float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
@@ -386,232 +481,257 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
             mrun[e] = D4_NEG;
             lsum[e] = 0.f;
         }
-
-        // base-2 logits of the page in ring slot: tokens r, r + 8 of head t (NT == 1), of heads 2 t, 2 t + 1 (NT == 2)
-        auto qk_page = [&](int slot, float (&lg)[2][NT]) {
-            const uint8_t* tile = sm.ring[warp][slot];
-            const int n = sm.ntok[warp][slot];
-            const uint4 ka = lds128(tile + O4_KC + 64 * r + 16 * t), kb = lds128(tile + O4_KC + 64 * (r + 8) + 16 * t);
-            const uint2 sa = lds64(tile + O4_KM + 16 * r), sb = lds64(tile + O4_KM + 16 * (r + 8));
-            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-            const float2 fa0 = __half22float2(u32_as_h2(sa.x)), fa1 = __half22float2(u32_as_h2(sa.y));
-            const float2 fb0 = __half22float2(u32_as_h2(sb.x)), fb1 = __half22float2(u32_as_h2(sb.y));
-            const float fa[4] = {fa0.x, fa0.y, fa1.x, fa1.y}, fb[4] = {fb0.x, fb0.y, fb1.x, fb1.y};
-            // min term: A column k = group k (the columns past 3 meet zeros)
-            float cm[4] = {0.f, 0.f, 0.f, 0.f};
-            {
-                const uint32_t am[4] = {lds32(tile + O4_KM + 16 * r + 8 + 4 * (t & 1)),
-                                        lds32(tile + O4_KM + 16 * (r + 8) + 8 + 4 * (t & 1)), 0u, 0u};
-                mma_f16_16816(cm, am, bs[0], 0u);
-                if constexpr (NT == 2) mma_f16_16816(cm, am, bs[1], 0u);
+        if (n_units > 0) {
+            wait(&sm.qbar[buf], (s >> 1) & 1);
+            const D4Query<NT>& qf = sm.query[buf];
+            uint32_t bq[NT == 1 ? 8 : 1][2], bs[2];
+            float inv_q[NT], inv_s[NT];  // NT == 1: head t; NT == 2: heads 2 t, 2 t + 1
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const uint2 f = lds64(qf.bq[x][lane]);
+                    bq[x][0] = f.x;
+                    bq[x][1] = f.y;
+                }
+                bs[0] = bs[1] = qf.bs[lane][0];
+                inv_q[0] = qf.inv_q[t];
+                inv_s[0] = qf.inv_s[t];
+            } else {
+                const uint2 f = lds64(qf.bs[lane]);
+                bs[0] = f.x;
+                bs[1] = f.y;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    inv_q[e] = qf.inv_q[2 * t + e];
+                    inv_s[e] = qf.inv_s[2 * t + e];
+                }
             }
-            float xa[NT], xb[NT];
+
+            // base-2 logits of the page in ring slot: tokens r, r + 8 of head t (NT == 1), of heads 2 t, 2 t + 1 (NT == 2)
+            auto qk_page = [&](int slot, float (&lg)[2][NT]) {
+                const uint8_t* tile = sm.ring[warp][slot];
+                const uint4 ka = lds128(tile + O4_KC + 64 * r + 16 * t), kb = lds128(tile + O4_KC + 64 * (r + 8) + 16 * t);
+                const uint2 sa = lds64(tile + O4_KM + 16 * r), sb = lds64(tile + O4_KM + 16 * (r + 8));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                const float2 fa0 = __half22float2(u32_as_h2(sa.x)), fa1 = __half22float2(u32_as_h2(sa.y));
+                const float2 fb0 = __half22float2(u32_as_h2(sb.x)), fb1 = __half22float2(u32_as_h2(sb.y));
+                const float fa[4] = {fa0.x, fa0.y, fa1.x, fa1.y}, fb[4] = {fb0.x, fb0.y, fb1.x, fb1.y};
+                // min term: A column k = group k (the columns past 3 meet zeros)
+                float cm[4] = {0.f, 0.f, 0.f, 0.f};
+                {
+                    const uint32_t am[4] = {lds32(tile + O4_KM + 16 * r + 8 + 4 * (t & 1)),
+                                            lds32(tile + O4_KM + 16 * (r + 8) + 8 + 4 * (t & 1)), 0u, 0u};
+                    mma_f16_16816(cm, am, bs[0], 0u);
+                    if constexpr (NT == 2) mma_f16_16816(cm, am, bs[1], 0u);
+                }
+                float xa[NT], xb[NT];
 #pragma unroll
-            for (int e = 0; e < NT; ++e) xa[e] = xb[e] = 0.f;
+                for (int e = 0; e < NT; ++e) xa[e] = xb[e] = 0.f;
 #pragma unroll
-            for (int gg = 0; gg < NGROUP; ++gg) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int gg = 0; gg < NGROUP; ++gg) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int hs = 0; hs < 2; ++hs) {
-                    const uint32_t A = hs ? wa[gg] >> 8 : wa[gg], Bw = hs ? wb[gg] >> 8 : wb[gg];
-                    const uint32_t af[4] = {A & 0x000f000fu, Bw & 0x000f000fu, A & 0x00f000f0u, Bw & 0x00f000f0u};
-                    if constexpr (NT == 1) {
-                        mma_f16_16816(c, af, bq[2 * gg + hs][0], bq[2 * gg + hs][1]);
+                    for (int hs = 0; hs < 2; ++hs) {
+                        const uint32_t A = hs ? wa[gg] >> 8 : wa[gg], Bw = hs ? wb[gg] >> 8 : wb[gg];
+                        const uint32_t af[4] = {A & 0x000f000fu, Bw & 0x000f000fu, A & 0x00f000f0u, Bw & 0x00f000f0u};
+                        if constexpr (NT == 1) {
+                            mma_f16_16816(c, af, bq[2 * gg + hs][0], bq[2 * gg + hs][1]);
+                        } else {
+                            const uint4 f = lds128(qf.bq[2 * gg + hs][lane]);
+                            mma_f16_16816(c, af, f.x, f.y);
+                            mma_f16_16816(c, af, f.z, f.w);
+                        }
+                    }
+                    if constexpr (NT == 1) {  // high + low part
+                        xa[0] = fmaf(fa[gg], c[0] + c[1], xa[0]);
+                        xb[0] = fmaf(fb[gg], c[2] + c[3], xb[0]);
                     } else {
-                        const uint4 f = sm.bq[2 * gg + hs][lane];
-                        mma_f16_16816(c, af, f.x, f.y);
-                        mma_f16_16816(c, af, f.z, f.w);
+                        xa[0] = fmaf(fa[gg], c[0], xa[0]);
+                        xa[1] = fmaf(fa[gg], c[1], xa[1]);
+                        xb[0] = fmaf(fb[gg], c[2], xb[0]);
+                        xb[1] = fmaf(fb[gg], c[3], xb[1]);
                     }
                 }
-                if constexpr (NT == 1) {  // high + low part
-                    xa[0] = fmaf(fa[gg], c[0] + c[1], xa[0]);
-                    xb[0] = fmaf(fb[gg], c[2] + c[3], xb[0]);
+#pragma unroll
+                for (int e = 0; e < NT; ++e) {
+                    const float ma = NT == 1 ? cm[0] + cm[1] : cm[e], mb = NT == 1 ? cm[2] + cm[3] : cm[2 + e];
+                    lg[0][e] = fmaf(xa[e], inv_q[e], ma * inv_s[e]);
+                    lg[1][e] = fmaf(xb[e], inv_q[e], mb * inv_s[e]);
+                }
+            };
+
+            auto pv_page = [&](int slot, const float (&p)[2][NT]) {
+                const uint8_t* tile = sm.ring[warp][slot];
+                uint32_t pb0, pb1;  // p in the operand's layout: tokens 2 t, 2 t + 1 and 2 t + 8, 2 t + 9
+                uint32_t s0[4], s1[4];
+                if constexpr (NT == 1) {
+                    // column r: head r / 2, tokens 0..7 (r even) or 8..15 (r odd); the other half is zero
+                    const uint32_t y = movmatrix(pack_half2(p[0][0], p[1][0]));
+                    pb0 = r & 1 ? 0u : y;
+                    pb1 = r & 1 ? y : 0u;
+                    const uint4 sc = lds128(tile + O4_VS + 16 * (t + 4 * (r & 1)));
+                    s0[0] = s1[0] = sc.x;
+                    s0[1] = s1[1] = sc.y;
+                    s0[2] = s1[2] = sc.z;
+                    s0[3] = s1[3] = sc.w;
                 } else {
-                    xa[0] = fmaf(fa[gg], c[0], xa[0]);
-                    xa[1] = fmaf(fa[gg], c[1], xa[1]);
-                    xb[0] = fmaf(fb[gg], c[2], xb[0]);
-                    xb[1] = fmaf(fb[gg], c[3], xb[1]);
+                    pb0 = movmatrix(pack_half2(p[0][0], p[0][1]));
+                    pb1 = movmatrix(pack_half2(p[1][0], p[1][1]));
+                    const uint4 sA = lds128(tile + O4_VS + 16 * t), sB = lds128(tile + O4_VS + 16 * (t + 4));
+                    s0[0] = sA.x;
+                    s0[1] = sA.y;
+                    s0[2] = sA.z;
+                    s0[3] = sA.w;
+                    s1[0] = sB.x;
+                    s1[1] = sB.y;
+                    s1[2] = sB.z;
+                    s1[3] = sB.w;
                 }
-            }
+                {   // min term: row r holds group r & 3
+                    const uint32_t am[4] = {lds32(tile + O4_VM + 16 * t + 4 * (r & 3)), 0u,
+                                            lds32(tile + O4_VM + 16 * (t + 4) + 4 * (r & 3)), 0u};
+                    mma_f16_16816(cmin, am, pb0, pb1);
+                }
+                const uint4 va = lds128(tile + O4_VC + 128 * t + 16 * r), vb = lds128(tile + O4_VC + 128 * (t + 4) + 16 * r);
+                const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
-            for (int e = 0; e < NT; ++e) {
-                const float ma = NT == 1 ? cm[0] + cm[1] : cm[e], mb = NT == 1 ? cm[2] + cm[3] : cm[2 + e];
-                lg[0][e] = r < n ? fmaf(xa[e], inv_q[e], ma * inv_s[e]) : -CUDART_INF_F;
-                lg[1][e] = r + 8 < n ? fmaf(xb[e], inv_q[e], mb * inv_s[e]) : -CUDART_INF_F;
-            }
-        };
+                for (int gg = 0; gg < NGROUP; ++gg) {
+                    const uint32_t h0 = h2_as_u32(__hmul2(u32_as_h2(pb0), u32_as_h2(s0[gg])));
+                    const uint32_t h1 = h2_as_u32(__hmul2(u32_as_h2(pb1), u32_as_h2(s1[gg])));
+#pragma unroll
+                    for (int hs = 0; hs < 2; ++hs) {
+                        const uint32_t A = hs ? wa[gg] >> 8 : wa[gg], Bw = hs ? wb[gg] >> 8 : wb[gg];
+                        const uint32_t af[4] = {A & 0x000f000fu, A & 0x00f000f0u, Bw & 0x000f000fu, Bw & 0x00f000f0u};
+                        mma_f16_16816(oacc[2 * gg + hs], af, h0, h1);
+                    }
+                }
+            };
 
-        auto pv_page = [&](int slot, const float (&p)[2][NT]) {
-            const uint8_t* tile = sm.ring[warp][slot];
-            uint32_t pb0, pb1;  // p in the operand's layout: tokens 2 t, 2 t + 1 and 2 t + 8, 2 t + 9
-            uint32_t s0[4], s1[4];
-            if constexpr (NT == 1) {
-                // column r: head r / 2, tokens 0..7 (r even) or 8..15 (r odd); the other half is zero
-                const uint32_t y = movmatrix(pack_half2(p[0][0], p[1][0]));
-                pb0 = r & 1 ? 0u : y;
-                pb1 = r & 1 ? y : 0u;
-                const uint4 s = lds128(tile + O4_VS + 16 * (t + 4 * (r & 1)));
-                s0[0] = s1[0] = s.x;
-                s0[1] = s1[1] = s.y;
-                s0[2] = s1[2] = s.z;
-                s0[3] = s1[3] = s.w;
-            } else {
-                pb0 = movmatrix(pack_half2(p[0][0], p[0][1]));
-                pb1 = movmatrix(pack_half2(p[1][0], p[1][1]));
-                const uint4 sA = lds128(tile + O4_VS + 16 * t), sB = lds128(tile + O4_VS + 16 * (t + 4));
-                s0[0] = sA.x;
-                s0[1] = sA.y;
-                s0[2] = sA.z;
-                s0[3] = sA.w;
-                s1[0] = sB.x;
-                s1[1] = sB.y;
-                s1[2] = sB.z;
-                s1[3] = sB.w;
-            }
-            {   // min term: row r holds group r & 3
-                const uint32_t am[4] = {lds32(tile + O4_VM + 16 * t + 4 * (r & 3)), 0u,
-                                        lds32(tile + O4_VM + 16 * (t + 4) + 4 * (r & 3)), 0u};
-                mma_f16_16816(cmin, am, pb0, pb1);
-            }
-            const uint4 va = lds128(tile + O4_VC + 128 * t + 16 * r), vb = lds128(tile + O4_VC + 128 * (t + 4) + 16 * r);
-            const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-            for (int gg = 0; gg < NGROUP; ++gg) {
-                const uint32_t h0 = h2_as_u32(__hmul2(u32_as_h2(pb0), u32_as_h2(s0[gg])));
-                const uint32_t h1 = h2_as_u32(__hmul2(u32_as_h2(pb1), u32_as_h2(s1[gg])));
-#pragma unroll
-                for (int hs = 0; hs < 2; ++hs) {
-                    const uint32_t A = hs ? wa[gg] >> 8 : wa[gg], Bw = hs ? wb[gg] >> 8 : wb[gg];
-                    const uint32_t af[4] = {A & 0x000f000fu, A & 0x00f000f0u, Bw & 0x000f000fu, Bw & 0x00f000f0u};
-                    mma_f16_16816(oacc[2 * gg + hs], af, h0, h1);
+#pragma unroll 1
+            for (int k = 0; k < n_units; ++k) {
+                const int st = done % D4_UNITS;
+                wait(&sm.bar[warp][st], (done / D4_UNITS) & 1);
+                if (dead) break;
+                const int2 nt = *reinterpret_cast<const int2*>(&sm.ntok[warp][D4_U * st]);
+                static_assert(D4_U == 2, "a unit's token counts are read as a pair");
+                const bool short_page = min(nt.x, nt.y) < PAGE;  // warp-uniform
+                if (short_page) {
+                    // slots past the context (or of no page) may hold any bytes, NaN too: their
+                    // value scales and mins are cleared, so p = 0 meets finite factors
+                    for (int x = lane; x < D4_U * 64; x += 32) {
+                        const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = e ? nt.y : nt.x;
+                        const uint32_t keep = (2 * pair < n ? 0x0000ffffu : 0u) | (2 * pair + 1 < n ? 0xffff0000u : 0u);
+                        uint32_t* word = reinterpret_cast<uint32_t*>(sm.ring[warp][D4_U * st + e] + O4_VS) + w;
+                        if (keep != 0xffffffffu) *word &= keep;
+                    }
+                    __syncwarp();
                 }
-            }
-        };
-
-        // ---- the warp's pages
-        int k_fail = -1, st = st0;
-        uint32_t parity = par0;
-        for (int k = 0; k < n_units; ++k) {
-            const bool landed = mbar_wait_bounded(&sm.bar[warp][st], parity, WAIT_LIMIT_CYCLES);
-            if (__any_sync(0xffffffffu, !landed)) {
-                if (lane == 0) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_TIMEOUT);
-                k_fail = k;
-                break;
-            }
-            bool short_page = false;
+                float lg[D4_U][2][NT];
 #pragma unroll
-            for (int e = 0; e < D4_U; ++e) short_page |= sm.ntok[warp][D4_U * st + e] < PAGE;
-            if (short_page) {
-                // slots past the context (or of no page) may hold any bytes, NaN too: their
-                // value scales and mins are cleared, so p = 0 meets finite factors
-                for (int x = lane; x < D4_U * 64; x += 32) {
-                    const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = sm.ntok[warp][D4_U * st + e];
-                    const uint32_t keep = (2 * pair < n ? 0x0000ffffu : 0u) | (2 * pair + 1 < n ? 0xffff0000u : 0u);
-                    uint32_t* word = reinterpret_cast<uint32_t*>(sm.ring[warp][D4_U * st + e] + O4_VS) + w;
-                    if (keep != 0xffffffffu) *word &= keep;
-                }
-                __syncwarp();
-            }
-            float lg[D4_U][2][NT];
+                for (int e = 0; e < D4_U; ++e) qk_page(D4_U * st + e, lg[e]);
+                if (short_page) {
 #pragma unroll
-            for (int e = 0; e < D4_U; ++e) qk_page(D4_U * st + e, lg[e]);
-            if constexpr (WTS) {
-#pragma unroll
-                for (int e = 0; e < D4_U; ++e) {
-                    const int j = D4_U * k + e;
-                    if (j < my_count) {
-                        float* row = a.logits + ((u * a.max_pages + page_of(j)) * PAGE + r) * G;
+                    for (int e = 0; e < D4_U; ++e) {
+                        const int n = e ? nt.y : nt.x;
 #pragma unroll
                         for (int x = 0; x < NT; ++x) {
-                            const int hd = NT == 1 ? t : 2 * t + x;
-                            if (hd < G) {
-                                row[hd] = lg[e][0][x];
-                                row[(size_t)8 * G + hd] = lg[e][1][x];
+                            if (r >= n) lg[e][0][x] = -CUDART_INF_F;
+                            if (r + 8 >= n) lg[e][1][x] = -CUDART_INF_F;
+                        }
+                    }
+                }
+                if constexpr (WTS) {
+#pragma unroll
+                    for (int e = 0; e < D4_U; ++e) {
+                        const int page = cs.pa + warp + D4_NW * (D4_U * k + e);
+                        if (page < cs.pb) {
+                            float* row = a.logits + ((u * a.max_pages + page) * PAGE + r) * G;
+#pragma unroll
+                            for (int x = 0; x < NT; ++x) {
+                                const int hd = NT == 1 ? t : 2 * t + x;
+                                if (hd < G) {
+                                    row[hd] = lg[e][0][x];
+                                    row[(size_t)8 * G + hd] = lg[e][1][x];
+                                }
                             }
                         }
                     }
                 }
-            }
-            float top[NT];
-            bool grow = false;
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                top[x] = fmaxf(lg[0][0][x], lg[0][1][x]);
-#pragma unroll
-                for (int e = 1; e < D4_U; ++e) top[x] = fmaxf(top[x], fmaxf(lg[e][0][x], lg[e][1][x]));
-                grow |= top[x] > mrun[x];
-            }
-            if (__any_sync(0xffffffffu, grow)) {
+                float top[NT];
+                bool grow = false;
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 4));
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 8));
-                    top[x] = fmaxf(fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 16)), mrun[x]);
-                    const float c = d4_ex2(mrun[x] - top[x]);
-                    mrun[x] = top[x];
-                    lsum[x] *= c;
+                    top[x] = fmaxf(lg[0][0][x], lg[0][1][x]);
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        oacc[m][x] *= c;
-                        oacc[m][x + 2] *= c;
-                        if (NT == 1) {
-                            oacc[m][1] *= c;
-                            oacc[m][3] *= c;
+                    for (int e = 1; e < D4_U; ++e) top[x] = fmaxf(top[x], fmaxf(lg[e][0][x], lg[e][1][x]));
+                    grow |= top[x] > mrun[x];
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 4));
+                        top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 8));
+                        top[x] = fmaxf(fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 16)), mrun[x]);
+                        const float c = d4_ex2(mrun[x] - top[x]);
+                        mrun[x] = top[x];
+                        lsum[x] *= c;
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) {
+                            oacc[m][x] *= c;
+                            oacc[m][x + 2] *= c;
+                            if (NT == 1) {
+                                oacc[m][1] *= c;
+                                oacc[m][3] *= c;
+                            }
                         }
+                        cmin[x] *= c;
+                        if (NT == 1) cmin[1] *= c;
                     }
-                    cmin[x] *= c;
-                    if (NT == 1) cmin[1] *= c;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < D4_U; ++e)
-#pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    lg[e][0][x] = d4_ex2(lg[e][0][x] - mrun[x]);
-                    lg[e][1][x] = d4_ex2(lg[e][1][x] - mrun[x]);
-                    lsum[x] += lg[e][0][x] + lg[e][1][x];
                 }
 #pragma unroll
-            for (int e = 0; e < D4_U; ++e) pv_page(D4_U * st + e, lg[e]);
-            // hand the unit's slots back
-            __syncwarp();
-            if (k + D4_UNITS < n_units) {
-                fence_proxy_async_smem();
-                issue_unit(k + D4_UNITS, st, pid_next);
-                n_issued = k + D4_UNITS + 1;
-                const int j = D4_U * (k + D4_UNITS + 1) + lane;
-                if (lane < D4_U && j < my_count) pid_next = __ldg(bt + page_of(j));
+                for (int e = 0; e < D4_U; ++e)
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        lg[e][0][x] = d4_ex2(lg[e][0][x] - mrun[x]);
+                        lg[e][1][x] = d4_ex2(lg[e][1][x] - mrun[x]);
+                        lsum[x] += lg[e][0][x] + lg[e][1][x];
+                    }
+#pragma unroll
+                for (int e = 0; e < D4_U; ++e) pv_page(D4_U * st + e, lg[e]);
+                ++done;
+                __syncwarp();
+                if (k + 1 < n_units) {
+                    // hand the group back, and the ones that the last segment's partial held
+                    if (s > 0 && freed < end1) wait(&sm.free_bar[buf ^ 1], ((s - 1) >> 1) & 1);
+                    freed = done;
+                    refill();
+                }
             }
-            st = st + 1 == D4_UNITS ? 0 : st + 1;
-            if (st == 0) parity ^= 1u;
         }
-        if (k_fail >= 0 && lane == 0) {
-            sm.dead = 1;
-            // copies in flight land before the shared memory is reused
-            for (int v = k_fail; v < n_issued; ++v)
-                (void)mbar_wait_bounded(&sm.bar[warp][(kbase + v) % D4_UNITS], ((kbase + v) / D4_UNITS) & 1, 1000000LL);
-        }
-        __syncwarp();
-        kbase += k_fail >= 0 ? n_issued : n_units;
 
-        // ---- this warp's partial, in its own ring: channels 32 g + 4 r .. + 3 of its head(s)
-        float* op = reinterpret_cast<float*>(sm.ring[warp][0]);
+        // ---- this warp's partial, in its last ring group: channels 32 g + 4 r .. + 3 of
+        // its head(s)
+        const bool has = n_units > 0 && !dead;
+        const int at = (done - 1) % D4_UNITS;
+        if (has) {
+            float* op = reinterpret_cast<float*>(sm.ring[warp][D4_U * at]);
 #pragma unroll
-        for (int gg = 0; gg < NGROUP; ++gg) {
-            if constexpr (NT == 1) {
-                const float mt = __shfl_sync(0xffffffffu, cmin[0] + cmin[1], 4 * gg + t);
-                *reinterpret_cast<float4*>(op + t * D + 32 * gg + 4 * r) =
-                    make_float4(fmaf(oacc[2 * gg][0] + oacc[2 * gg][1], 16777216.f, mt),
-                                fmaf(oacc[2 * gg][2] + oacc[2 * gg][3], 1048576.f, mt),
-                                fmaf(oacc[2 * gg + 1][0] + oacc[2 * gg + 1][1], 16777216.f, mt),
-                                fmaf(oacc[2 * gg + 1][2] + oacc[2 * gg + 1][3], 1048576.f, mt));
-            } else {
+            for (int gg = 0; gg < NGROUP; ++gg) {
+                if constexpr (NT == 1) {
+                    const float mt = __shfl_sync(0xffffffffu, cmin[0] + cmin[1], 4 * gg + t);
+                    *reinterpret_cast<float4*>(op + t * D + 32 * gg + 4 * r) =
+                        make_float4(fmaf(oacc[2 * gg][0] + oacc[2 * gg][1], 16777216.f, mt),
+                                    fmaf(oacc[2 * gg][2] + oacc[2 * gg][3], 1048576.f, mt),
+                                    fmaf(oacc[2 * gg + 1][0] + oacc[2 * gg + 1][1], 16777216.f, mt),
+                                    fmaf(oacc[2 * gg + 1][2] + oacc[2 * gg + 1][3], 1048576.f, mt));
+                } else {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float mt = __shfl_sync(0xffffffffu, cmin[x], 4 * gg + t);
-                    *reinterpret_cast<float4*>(op + (2 * t + x) * D + 32 * gg + 4 * r) =
-                        make_float4(fmaf(oacc[2 * gg][x], 16777216.f, mt), fmaf(oacc[2 * gg][2 + x], 1048576.f, mt),
-                                    fmaf(oacc[2 * gg + 1][x], 16777216.f, mt), fmaf(oacc[2 * gg + 1][2 + x], 1048576.f, mt));
+                    for (int x = 0; x < 2; ++x) {
+                        const float mt = __shfl_sync(0xffffffffu, cmin[x], 4 * gg + t);
+                        *reinterpret_cast<float4*>(op + (2 * t + x) * D + 32 * gg + 4 * r) =
+                            make_float4(fmaf(oacc[2 * gg][x], 16777216.f, mt), fmaf(oacc[2 * gg][2 + x], 1048576.f, mt),
+                                        fmaf(oacc[2 * gg + 1][x], 16777216.f, mt), fmaf(oacc[2 * gg + 1][2 + x], 1048576.f, mt));
+                    }
                 }
             }
         }
@@ -623,164 +743,250 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (r == 0) {
                 const int hd = NT == 1 ? t : 2 * t + x;
-                sm.m_part[warp][hd] = mrun[x];
-                sm.l_part[warp][hd] = l;
+                sm.m_part[buf][warp][hd] = has ? mrun[x] : D4_NEG;
+                sm.l_part[buf][warp][hd] = has ? l : 0.f;
             }
         }
-        __syncthreads();
-        g = ub + pb;
-        if (g >= g1) griddep_launch_dependents();
-
-        // ---- merge the warps; publish, and finish the unit if this CTA is its last (or only) one
-        const int c0 = cta_of(ub), n_part = cta_of(ub + np - 1) - c0 + 1;
-        float* slot = a.partials + (u + cta) * (size_t)(G * PART_STRIDE);
-        for (int i = tid; i < G * (D / 4); i += D4_THREADS) {
-            const int j = i / (D / 4), c4 = 4 * (i % (D / 4));
-            float M = D4_NEG, L = 0.f;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < D4_NW; ++w) M = fmaxf(M, sm.m_part[w][j]);
-#pragma unroll
-            for (int w = 0; w < D4_NW; ++w) {
-                const float f = d4_ex2(sm.m_part[w][j] - M);
-                const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w][0]) + j * D + c4);
-                L = fmaf(sm.l_part[w][j], f, L);
-                O.x = fmaf(x.x, f, O.x);
-                O.y = fmaf(x.y, f, O.y);
-                O.z = fmaf(x.z, f, O.z);
-                O.w = fmaf(x.w, f, O.w);
-            }
-            if (n_part == 1) {
-                const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
-                *reinterpret_cast<float4*>(&sm.q[j][c4]) = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-                if (WTS && c4 == 0) a.stats[u * G + j] = make_float2(M, inv);
-            } else {
-                *reinterpret_cast<float4*>(slot + (size_t)j * PART_STRIDE + 4 + c4) = O;
-                if (c4 == 0) *reinterpret_cast<float2*>(slot + (size_t)j * PART_STRIDE) = make_float2(M, L);
-            }
+        if (lane == 0) sm.part_at[buf][warp] = has ? at : -1;
+        end2 = end1;
+        end1 = done;
+        __syncwarp();
+        int order = 0;
+        if (lane == 0) {
+            __threadfence_block();
+            order = atomicAdd(&sm.arrived[buf], 1);
+            __threadfence_block();
         }
-        fence_proxy_async_smem();  // the rings were written and read here: ordered before the next segment's copies
-        __syncthreads();
-        bool finish = true;
-        if (n_part > 1) {
-            int32_t* ticket = reinterpret_cast<int32_t*>(a.ws + WS_HEADER) + u;
-            if (tid == 0) sm.is_last = atomic_add_acq_rel_gpu(ticket, 1) == n_part - 1;
-            __syncthreads();
-            finish = sm.is_last;
-            if (finish) {
-                if (tid == 0) *ticket = 0;
-                // warp (part, head): partials part, part + P, ... with four channels a lane
-                const int P = D4_NW / G, j = warp % G, part = warp / G;
-                const float* ps = a.partials + (u + c0) * (size_t)(G * PART_STRIDE) + (size_t)j * PART_STRIDE;
-                if (part < P) {
-                    constexpr int CH = 8;
-                    float M = D4_NEG, L = 0.f;
-                    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int s0 = part; s0 < n_part; s0 += P * CH) {
-                        float2 ml[CH];
-                        float4 ov[CH];
+        order = __shfl_sync(0xffffffffu, order, 0);
+        if (order == D4_NW - 1) {
+            // ---- the last warp here merges the twelve partials in warp order and publishes
+            __syncwarp();
+            const int64_t ub = g0 + (share - cs.left - (cs.pb - cs.pa)) - cs.pa;  // the unit's first page
+            float* slot = a.partials + (u + cta) * (size_t)(G * PART_STRIDE);
+            {
+                // lane (row x0, head): the weights 2^(m_w - M) of warps x0, x0 + ROWS, ... in place
+                // of m_w (0 without pages), and each head's M and L
+                constexpr int MAXG = 4 * NT, ROWS = 32 / MAXG;
+                const int j = lane % MAXG, x0 = lane / MAXG;
+                float M = D4_NEG, L = 0.f;
 #pragma unroll
-                        for (int x = 0; x < CH; ++x) {
-                            const int s = s0 + P * x;
-                            const float* q = ps + (size_t)s * G * PART_STRIDE;
-                            ml[x] = s < n_part ? __ldcg(reinterpret_cast<const float2*>(q)) : make_float2(D4_NEG, 0.f);
-                            ov[x] = s < n_part ? __ldcg(reinterpret_cast<const float4*>(q + 4 + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
+                for (int w = x0; w < D4_NW; w += ROWS) M = fmaxf(M, sm.m_part[buf][w][j]);
 #pragma unroll
-                        for (int x = 0; x < CH; ++x) {
-                            const float Mn = fmaxf(M, ml[x].x), fo = d4_ex2(M - Mn), fn = d4_ex2(ml[x].x - Mn);
-                            L = fmaf(L, fo, ml[x].y * fn);
-                            O.x = fmaf(O.x, fo, ov[x].x * fn);
-                            O.y = fmaf(O.y, fo, ov[x].y * fn);
-                            O.z = fmaf(O.z, fo, ov[x].z * fn);
-                            O.w = fmaf(O.w, fo, ov[x].w * fn);
-                            M = Mn;
-                        }
-                    }
-                    *reinterpret_cast<float4*>(&sm.red[warp][4 * lane]) = O;
-                    if (lane == 0) {
-                        sm.m_part[part][j] = M;
-                        sm.l_part[part][j] = L;
-                    }
+                for (int o = 16; o >= MAXG; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+                for (int w = x0; w < D4_NW; w += ROWS) {
+                    const float f = sm.part_at[buf][w] >= 0 ? d4_ex2(sm.m_part[buf][w][j] - M) : 0.f;
+                    sm.m_part[buf][w][j] = f;
+                    L = fmaf(sm.l_part[buf][w][j], f, L);
                 }
-                __syncthreads();
-                for (int i = tid; i < G * D; i += D4_THREADS) {
-                    const int jj = i / D, c = i % D;
-                    float M = D4_NEG, L = 0.f, O = 0.f;
-                    for (int x = 0; x < P; ++x) M = fmaxf(M, sm.m_part[x][jj]);
-                    for (int x = 0; x < P; ++x) {
-                        const float f = d4_ex2(sm.m_part[x][jj] - M);
-                        L = fmaf(sm.l_part[x][jj], f, L);
-                        O = fmaf(sm.red[x * G + jj][c], f, O);
-                    }
-                    const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
-                    sm.q[jj][c] = O * inv;
-                    if (WTS && c == 0) a.stats[u * G + jj] = make_float2(M, inv);
-                }
-                __syncthreads();
-            }
-        }
-        if (finish && warp < 8) {
-            // out_i = sum_c o'_c R_v[i][c]: warp w takes rows 16 w .. + 15, a lane four
-            // columns of each; a reduce-scatter leaves row lane % 16 in each lane
-            const float* R = a.Rv + ((size_t)h * D + 16 * warp) * D + 4 * lane;
-            float4 rr[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) rr[i] = __ldg(reinterpret_cast<const float4*>(R + (size_t)i * D));
-            __nv_bfloat16* o = a.out + ((size_t)b * a.H_q + (size_t)h * G) * D + 16 * warp + lane;
+                for (int o = 16; o >= MAXG; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                if (lane < G) *reinterpret_cast<float2*>(slot + (size_t)lane * PART_STRIDE) = make_float2(M, L);
+                __syncwarp();
+            }
+            int at_w[D4_NW];
+#pragma unroll
+            for (int w = 0; w < D4_NW; ++w) at_w[w] = sm.part_at[buf][w];
+#pragma unroll 1
             for (int j = 0; j < G; ++j) {
-                const float4 x = *reinterpret_cast<const float4*>(&sm.q[j][4 * lane]);
-                float v[16];
+                float4 x[D4_NW];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = fmaf(x.x, rr[i].x, fmaf(x.y, rr[i].y, fmaf(x.z, rr[i].z, x.w * rr[i].w)));
-                    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+                for (int w = 0; w < D4_NW; ++w)
+                    x[w] = at_w[w] >= 0 ? *reinterpret_cast<const float4*>(
+                                              reinterpret_cast<const float*>(sm.ring[w][D4_U * at_w[w]]) + j * D + 4 * lane)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < D4_NW; ++w) {
+                    const float f = sm.m_part[buf][w][j];
+                    O.x = fmaf(x[w].x, f, O.x);
+                    O.y = fmaf(x[w].y, f, O.y);
+                    O.z = fmaf(x[w].z, f, O.z);
+                    O.w = fmaf(x[w].w, f, O.w);
                 }
-#pragma unroll
-                for (int off = 8; off >= 1; off >>= 1) {
-                    const bool upper = lane & off;
-#pragma unroll
-                    for (int i = 0; i < off; ++i) {
-                        const float send = upper ? v[i] : v[i + off], hold = upper ? v[i + off] : v[i];
-                        v[i] = hold + __shfl_xor_sync(0xffffffffu, send, off);
+                *reinterpret_cast<float4*>(slot + (size_t)j * PART_STRIDE + 4 + 4 * lane) = O;
+            }
+            if (lane == 0) {
+                auto cta_of = [&](int64_t x) { return (int)(((x + 1) * Ceff - 1) / V); };
+                const int c0 = cta_of(ub);
+                if (c0 == cta) a.info[u] = make_int2(c0, cta_of(ub + cs.np - 1) - c0 + 1);
+                sm.arrived[buf] = 0;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                // everyone is done with this segment's queries: fetch those of segment s + 2
+                if (cs.left > 0) {
+                    D4Walk w = cs;
+                    w.next(a);
+                    if (w.left > 0) {
+                        w.next(a);
+                        fence_proxy_async_smem();
+                        fetch_query(w, buf);
                     }
                 }
-                if (lane < 16) o[(size_t)j * D] = __float2bfloat16_rn(v[0]);
+                mbar_arrive(&sm.free_bar[buf]);
             }
         }
-        if (g >= g1) break;
-        if (pb == np && ++h == a.H_kv) {
-            h = 0;
-            base += (int64_t)np * a.H_kv;
-            do np = pages_of(++b);
-            while (np == 0);
-        }
-        __syncthreads();  // the next segment reuses the scratch
+        __syncwarp();
+        if (cs.left == 0) break;
+        cs.next(a);
     }
+    if (dead)  // copies in flight land before the block ends
+        for (int v = done; v < issued; ++v)
+            (void)mbar_wait_bounded(&sm.bar[warp][v % D4_UNITS], (v / D4_UNITS) & 1, 1000000LL);
 }
 
-// weights[s] = decay weights[s] + sum_j 2^(a_{j,s} - M_j) / L_j: reads the
-// logits that the attention kernel stored.
-__global__ void __launch_bounds__(256)
-weights_int4_kernel(const float* __restrict__ logits, const float2* __restrict__ stats, int H_kv, int G, int max_pages,
-                    const int32_t* __restrict__ context_lens, float* __restrict__ weights, int64_t stride, float decay) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int64_t unit = (int64_t)b * H_kv + h;
-    const int ctx = max(0, min(__ldg(context_lens + b), max_pages * PAGE));
-    const float2* st = stats + unit * G;
-    for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s < ctx; s += (int64_t)gridDim.x * 256) {
-        const float* lg = logits + ((size_t)unit * max_pages * PAGE + s) * G;
-        float p = 0.f;
-        for (int j = 0; j < G; ++j) {
-            const float2 ml = __ldcg(st + j);
-            const float x = __ldcg(lg + j);
-            // (a dropped token's logit is -inf: no weight, whatever the maximum)
-            p += x == -CUDART_INF_F ? 0.f : d4_ex2(x - ml.x) * ml.y;
+// ------------------------------------------------------------------ 3: finish
+
+// n_finish CTAs of 256 threads: RS of them per unit, D / RS rows of R_v each.
+// They merge the unit's partials (warp = head and every P-th partial), normalise
+// and rotate.  The others add weights: chunk x of a unit takes its tokens
+// 256 x .. + 255 and every chunks * 256 on.
+template <int RS, bool WTS>
+__global__ void __launch_bounds__(256) finish_int4_kernel(const __grid_constant__ D4Args a) {
+    constexpr int RW = D / RS / 8;  // rows of R_v a warp rotates
+    __shared__ __align__(16) float o[8][D], part[8][D];
+    __shared__ float pm[8][8], pl[8][8], Mh[8], inv[8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
+    if (!WTS || (int)blockIdx.x < a.n_finish) {
+        const size_t u = blockIdx.x / RS;
+        const int b = (int)(u / a.H_kv), h = (int)(u % a.H_kv), row0 = (blockIdx.x % RS) * (D / RS) + RW * warp;
+        // (R_v is read before the wait: the stream kernel started this one after its own wait)
+        float4 rr[RW];
+        const float* R = a.Rv + ((size_t)h * D + row0) * D + 4 * lane;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) rr[i] = __ldg(reinterpret_cast<const float4*>(R + (size_t)i * D));
+        const int pages = d4_pages(a, b);
+        griddep_wait();
+        griddep_launch_dependents();
+        __nv_bfloat16* out = a.out + ((size_t)b * a.H_q + (size_t)h * G) * D + row0;
+        if (pages == 0) {
+            for (int i = lane; i < G * RW; i += 32) out[(size_t)(i / RW) * D + i % RW] = __float2bfloat16_rn(0.f);
+            return;
         }
-        float* w = weights + unit * stride + s;
-        *w = fmaf(decay, *w, p);
+        const int2 info = __ldcg(a.info + u);
+        const int P = 8 / G, j = warp % G, p = warp / G;
+        if (p < P) {
+            constexpr int CH = 8;
+            const float* ps = a.partials + (u + info.x) * (size_t)(G * PART_STRIDE) + (size_t)j * PART_STRIDE;
+            float M = D4_NEG, L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s0 = p; s0 < info.y; s0 += P * CH) {
+                float2 ml[CH];
+                float4 ov[CH];
+#pragma unroll
+                for (int x = 0; x < CH; ++x) {
+                    const int s = s0 + P * x;
+                    const float* q = ps + (size_t)s * G * PART_STRIDE;
+                    ml[x] = s < info.y ? __ldcg(reinterpret_cast<const float2*>(q)) : make_float2(D4_NEG, 0.f);
+                    ov[x] = s < info.y ? __ldcg(reinterpret_cast<const float4*>(q + 4 + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int x = 0; x < CH; ++x) {
+                    const float Mn = fmaxf(M, ml[x].x), fo = d4_ex2(M - Mn), fn = d4_ex2(ml[x].x - Mn);
+                    L = fmaf(L, fo, ml[x].y * fn);
+                    O.x = fmaf(O.x, fo, ov[x].x * fn);
+                    O.y = fmaf(O.y, fo, ov[x].y * fn);
+                    O.z = fmaf(O.z, fo, ov[x].z * fn);
+                    O.w = fmaf(O.w, fo, ov[x].w * fn);
+                    M = Mn;
+                }
+            }
+            *reinterpret_cast<float4*>(&part[warp][4 * lane]) = O;
+            if (lane == 0) {
+                pm[p][j] = M;
+                pl[p][j] = L;
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < G * D; i += 256) {
+            const int jj = i / D, c = i % D;
+            float M = D4_NEG, L = 0.f, O = 0.f;
+            for (int x = 0; x < P; ++x) M = fmaxf(M, pm[x][jj]);
+            for (int x = 0; x < P; ++x) {
+                const float f = d4_ex2(pm[x][jj] - M);
+                L = fmaf(pl[x][jj], f, L);
+                O = fmaf(part[x * G + jj][c], f, O);
+            }
+            o[jj][c] = O * (L > 0.f ? 1.f / L : (L == L ? 0.f : L));  // no token: 0; NaN stays NaN
+        }
+        __syncthreads();
+        // out_i = sum_c o_c R_v[i][c]: a lane forms four columns of each of its warp's rows,
+        // a reduce-scatter leaves row lane % RW in each lane
+#pragma unroll 2
+        for (int jj = 0; jj < G; ++jj) {
+            const float4 x = *reinterpret_cast<const float4*>(&o[jj][4 * lane]);
+            float v[RW];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                v[i] = fmaf(x.x, rr[i].x, fmaf(x.y, rr[i].y, fmaf(x.z, rr[i].z, x.w * rr[i].w)));
+#pragma unroll
+                for (int off = 16; off >= RW; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+            }
+#pragma unroll
+            for (int off = RW / 2; off >= 1; off >>= 1) {
+                const bool upper = lane & off;
+#pragma unroll
+                for (int i = 0; i < off; ++i) {
+                    const float send = upper ? v[i] : v[i + off], hold = upper ? v[i + off] : v[i];
+                    v[i] = hold + __shfl_xor_sync(0xffffffffu, send, off);
+                }
+            }
+            if (lane < RW) out[(size_t)jj * D + lane] = __float2bfloat16_rn(v[0]);
+        }
+    } else {
+        const int x = blockIdx.x - a.n_finish;
+        const size_t u = x / a.chunks;
+        const int chunk = x % a.chunks, b = (int)(u / a.H_kv);
+        const int ctx = max(0, min(__ldg(a.context_lens + b), a.max_pages * PAGE));
+        griddep_wait();
+        griddep_launch_dependents();
+        if (chunk * 256 >= ctx) return;
+        // the unit's maximum and 1 / sum of each head
+        const int2 info = __ldcg(a.info + u);
+        if (warp < G) {
+            const float* ps = a.partials + (u + info.x) * (size_t)(G * PART_STRIDE) + (size_t)warp * PART_STRIDE;
+            float M = D4_NEG, L = 0.f;
+            for (int s = lane; s < info.y; s += 32) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(ps + (size_t)s * G * PART_STRIDE));
+                const float Mn = fmaxf(M, ml.x);
+                L = fmaf(L, d4_ex2(M - Mn), ml.y * d4_ex2(ml.x - Mn));
+                M = Mn;
+            }
+#pragma unroll
+            for (int off = 16; off; off >>= 1) {
+                const float Mo = __shfl_xor_sync(0xffffffffu, M, off), Lo = __shfl_xor_sync(0xffffffffu, L, off);
+                const float Mn = fmaxf(M, Mo);
+                L = L * d4_ex2(M - Mn) + Lo * d4_ex2(Mo - Mn);
+                M = Mn;
+            }
+            if (lane == 0) {
+                Mh[warp] = M;
+                inv[warp] = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+            }
+        }
+        __syncthreads();
+        float* w = a.weights + (int64_t)u * a.wstride;
+        const float* lg = a.logits + u * a.max_pages * PAGE * G;
+        for (int64_t s = (int64_t)chunk * 256 + tid; s < ctx; s += (int64_t)a.chunks * 256) {
+            float p = 0.f;
+            auto add = [&](float z, int j) {
+                // (a dropped token's logit is -inf: no weight, whatever the maximum)
+                p += z == -CUDART_INF_F ? 0.f : d4_ex2(z - Mh[j]) * inv[j];
+            };
+            if (G % 4 == 0) {
+                for (int j = 0; j < G; j += 4) {
+                    const float4 z = __ldcg(reinterpret_cast<const float4*>(lg + (size_t)s * G + j));
+                    add(z.x, j);
+                    add(z.y, j + 1);
+                    add(z.z, j + 2);
+                    add(z.w, j + 3);
+                }
+            } else {
+                for (int j = 0; j < G; ++j) add(__ldcg(lg + (size_t)s * G + j), j);
+            }
+            w[s] = fmaf(a.decay, w[s], p);
+        }
     }
 }
 
@@ -795,14 +1001,15 @@ static int64_t d4_ctas(int B, int H_kv, int num_splits) {
 }
 
 struct D4Layout {
-    size_t partials, stats, logits, total;
+    size_t query, info, partials, logits, total;
 };
 static D4Layout d4_layout(int B, int H_q, int H_kv, int max_pages, int64_t C, bool weights) {
     const size_t units = (size_t)B * H_kv, G = (size_t)(H_q / H_kv);
     D4Layout l;
-    l.partials = WS_HEADER + tickets_bytes(B, H_kv);
-    l.stats = align_up(l.partials + (units + (size_t)C) * G * PART_STRIDE * 4, 256);  // a slot per (unit + CTA)
-    l.logits = align_up(l.stats + (weights ? units * G * 8 : 0), 256);
+    l.query = WS_HEADER;
+    l.info = align_up(l.query + units * (G <= 4 ? sizeof(D4Query<1>) : sizeof(D4Query<2>)), 256);
+    l.partials = align_up(l.info + units * sizeof(int2), 256);
+    l.logits = align_up(l.partials + (units + (size_t)C) * G * PART_STRIDE * 4, 256);  // a slot per (unit + CTA)
     l.total = l.logits + (weights ? units * (size_t)max_pages * PAGE * G * 4 : 0);
     return l;
 }
@@ -860,9 +1067,9 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
             return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: decay %g is not finite and >= 0", fn, (double)decay);
     }
     const int64_t C = d4_ctas(B, H_kv, num_splits);
-    // (the kernel multiplies a CTA's index by the batch's pages in 64 bits)
-    if (C > (1 << 22) || (int64_t)B * H_kv * max_pages > (int64_t(1) << 40))
-        return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: %lld CTAs above 2^22, or B * H_kv * max_pages above 2^40", fn, (long long)C);
+    // (a CTA's index times the batch's pages stays within 64 bits, a CTA's share within 32)
+    if (C > (1 << 22) || (int64_t)B * H_kv * max_pages > (int64_t(1) << 36))
+        return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: %lld CTAs above 2^22, or B * H_kv * max_pages above 2^36", fn, (long long)C);
     const D4Layout lay = d4_layout(B, H_q, H_kv, max_pages, C, with_weights);
     if (workspace_bytes < lay.total)
         return kvq_set_error(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, lay.total);
@@ -883,25 +1090,50 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.ws = ws;
+    a.query = ws + lay.query;
+    a.info = reinterpret_cast<int2*>(ws + lay.info);
     a.partials = reinterpret_cast<float*>(ws + lay.partials);
-    a.stats = with_weights ? reinterpret_cast<float2*>(ws + lay.stats) : nullptr;
     a.logits = with_weights ? reinterpret_cast<float*>(ws + lay.logits) : nullptr;
     a.automatic = num_splits == 0;
+    a.weights = weights;
+    a.wstride = weights_stride;
+    a.decay = decay;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int nsm = kvq_device_sm_count();
+    const int64_t units = (int64_t)B * H_kv;
+    if (units > (1 << 24)) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: B * H_kv above 2^24", fn);
+    // 1: runs of sequences that give about one CTA per SM
+    const int per = (int)((units + nsm - 1) / nsm);
+    kvq_status st = kvq_check_cuda(launch_pdl(G <= 4 ? rotate_int4_kernel<1> : rotate_int4_kernel<2>,
+                                              dim3(H_kv, (B + per - 1) / per), dim3(256), 0, cs, a, per),
+                                   "kvq_decode_attn_int4 rotate launch");
+    if (st != KVQ_OK) return st;
+    // 2
     using Kern = decltype(&decode_int4_kernel<1, false>);
     static const Kern kerns[4] = {decode_int4_kernel<1, false>, decode_int4_kernel<1, true>, decode_int4_kernel<2, false>,
                                   decode_int4_kernel<2, true>};
     const int which = (G <= 4 ? 0 : 2) + (with_weights ? 1 : 0);
-    const size_t smem = G <= 4 ? sizeof(D4Smem<4>) : sizeof(D4Smem<8>);
-    kvq_status st = d4_smem_once((const void*)kerns[which], (int)smem, which);
+    const size_t smem = G <= 4 ? sizeof(D4Smem<1>) : sizeof(D4Smem<2>);
+    st = d4_smem_once((const void*)kerns[which], (int)smem, which);
     if (st != KVQ_OK) return st;
-    st = kvq_check_cuda(launch_pdl(kerns[which], dim3((unsigned)C), dim3(D4_THREADS), smem, static_cast<cudaStream_t>(stream), a),
+    st = kvq_check_cuda(launch_pdl(kerns[which], dim3((unsigned)C), dim3(D4_THREADS), smem, cs, a),
                         "kvq_decode_attn_int4 launch");
-    if (st != KVQ_OK || !with_weights) return st;
-    const int gx = (max_pages * PAGE + 255) / 256;
-    return kvq_check_cuda(launch_pdl(weights_int4_kernel, dim3(gx < 64 ? gx : 64, H_kv, B), dim3(256), 0,
-                                     static_cast<cudaStream_t>(stream), (const float*)a.logits, (const float2*)a.stats,
-                                     H_kv, G, max_pages, context_lens, weights, weights_stride, decay),
-                          "kvq_decode_attn_int4_weights launch");
+    if (st != KVQ_OK) return st;
+    // 3: few units are finished by four CTAs each (a quarter of R_v each), and
+    // about four CTAs per SM share the weights
+    const bool few = units * 4 <= nsm;
+    a.n_finish = (int)(units * (few ? 4 : 1));
+    a.chunks = 0;
+    if (with_weights) {
+        const int64_t blocks = ((int64_t)max_pages * PAGE + 255) / 256, most = (4 * nsm + units - 1) / units;
+        a.chunks = (int)(blocks < most ? blocks : most);
+    }
+    const dim3 grid((unsigned)(a.n_finish + units * a.chunks));
+    st = kvq_check_cuda(launch_pdl(with_weights ? (few ? finish_int4_kernel<4, true> : finish_int4_kernel<1, true>)
+                                                : (few ? finish_int4_kernel<4, false> : finish_int4_kernel<1, false>),
+                                   grid, dim3(256), 0, cs, a),
+                        "kvq_decode_attn_int4 finish launch");
+    return st;
 }
 
 extern "C" kvq_status kvq_decode_attn_int4(const void* q, int B, int H_q, int H_kv, int d, const void* cache,

@@ -341,9 +341,8 @@ kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int H_kv, int 
  * kvq_decode_attn_int4; 1: kvq_decode_attn_int4_weights, which also holds the
  * logits of every query head, 64 * H_q * B * max_pages_per_seq bytes).
  * num_splits as passed to the call (0 = automatic on the current device).  The
- * workspace must be zero-filled once before its first use; every call leaves
- * its tickets at zero.  Calls (and captured graphs) that may overlap on the GPU
- * need a workspace each.  Its error word is read by kvq_workspace_status.
+ * workspace must be zero-filled once before its first use.  Calls (and captured
+ * graphs) that may overlap on the GPU need a workspace each.  Its error word is read by kvq_workspace_status.
  * Returns 0 for invalid sizes. */
 size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq, int num_splits,
                                 int weights);

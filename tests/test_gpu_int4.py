@@ -178,7 +178,6 @@ class _Case:
             _lib.kvq_decode_attn_int4_weights(*args, w, decay, ws, splits)
         torch.cuda.synchronize()
         self.status = _lib.kvq_workspace_status(ws)
-        assert int(ws[256:256 + 4 * self.B * self.h_kv].view(torch.int32).abs().sum()) == 0   # tickets back at zero
         return out.double().cpu().numpy(), None if w is None else w.double().cpu().numpy()
 
     def check(self, got, w=None, decay=1.0, ctx=None, bt=None):
