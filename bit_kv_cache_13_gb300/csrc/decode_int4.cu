@@ -57,7 +57,7 @@ constexpr int D4_UNITS = 3;        // units in a ring
 constexpr int D4_STAGES = D4_U * D4_UNITS;
 constexpr int D4_MAX_SPLITS = 254;
 constexpr int D4_MIN_PAGES = 16;   // pages a CTA takes at least when the split is automatic
-constexpr int D4_SEG_PAGES = 50;   // what starting another unit costs a CTA, in pages streamed
+constexpr int D4_SEG_PAGES = 40;   // what starting another unit costs a CTA, in pages streamed
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
 
 __device__ __forceinline__ float d4_ex2(float x) {
@@ -75,8 +75,15 @@ __device__ __forceinline__ float d4_prescale(float x) {
 // Transpose of an 8x8 matrix of 16-bit values spread over the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+// D = A(16x16 f16, row) * B(16x8 f16, col), fp32.
+__device__ __forceinline__ void d4_mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // The rotated queries of a unit as the stream kernel takes them: QK operands of
@@ -217,22 +224,25 @@ __device__ __forceinline__ int d4_pages(const D4Args& a, int b) {
     return c <= 0 ? 0 : min((int)(((int64_t)c + PAGE - 1) / PAGE), a.max_pages);
 }
 
-// A CTA's walk over its share: pages [pa, pb) of unit (b, h), which has np, and
-// `left` pages of the share after them.
+// A CTA's walk over its share: pages [pa, pb) of unit (b, h), which has np (and
+// `extra` without work after them), and `left` pages of the share after them.
 struct D4Walk {
-    int b, h, np, pa, pb, left;
-    __device__ __forceinline__ void clip(int share) {
-        pb = min((int64_t)np, (int64_t)pa + share);
-        left = share - (pb - pa);
+    int b, h, np, pa, pb, end, left;  // end: where the share leaves the unit, work-free pages counted
+    // Takes [pa, ..) of the unit out of `share` pages; false if only work-free ones are left of it.
+    __device__ __forceinline__ bool clip(int share, int extra) {
+        end = (int)min((int64_t)np + extra, (int64_t)pa + share);
+        left = share - (end - pa);
+        pb = min(np, end);
+        return pb > pa;
     }
-    __device__ __forceinline__ void next(const D4Args& a) {  // needs left > 0
+    __device__ __forceinline__ void next(const D4Args& a, int extra) {  // needs left > 0
         if (++h == a.H_kv) {
             h = 0;
             do np = d4_pages(a, ++b);
             while (np == 0);
         }
         pa = 0;
-        clip(left);
+        clip(left, extra);  // (a unit's first page is a real one)
     }
     // units of D4_U pages that warp w takes of the segment (its pages are dealt round-robin)
     __device__ __forceinline__ int units(int w) const {
@@ -282,39 +292,45 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
     // block table and cache are read before the dependency wait: the rotate kernel
     // let this one start only after its own wait, when everything before it was done.
     int64_t V, g0;
-    int Ceff, share;
+    int Ceff, share, extra = 0;  // extra: pages without work after each unit's, for the cost of starting it
     {
         const int per = (a.B + D4_THREADS - 1) / D4_THREADS, s0 = min(a.B, tid * per), s1 = min(a.B, s0 + per);
         int64_t own = 0;
-        int mx = 0, ne = 0;
+        int mx = 0, own_ne = 0;
         for (int b = s0; b < s1; ++b) {
             const int p = d4_pages(a, b);
             own += p;
             mx = max(mx, p);
-            ne += p > 0;
+            own_ne += p > 0;
         }
         int64_t inc = own;
+        int inc_ne = own_ne;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
+            const int y = __shfl_up_sync(0xffffffffu, inc_ne, o);
+            if (lane >= o) {
+                inc += x;
+                inc_ne += y;
+            }
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            ne += __shfl_xor_sync(0xffffffffu, ne, o);
-        }
+        for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (lane == 31) {
             sm.scan[warp] = inc;
             sm.scan_max[warp] = mx;
-            sm.scan_n[warp] = ne;
+            sm.scan_n[warp] = inc_ne;
         }
         __syncthreads();
         int64_t P = 0, before = 0;
-        mx = ne = 0;
+        int ne = 0, before_ne = 0;
+        mx = 0;
 #pragma unroll
         for (int w = 0; w < D4_NW; ++w) {
-            if (w < warp) before += sm.scan[w];
+            if (w < warp) {
+                before += sm.scan[w];
+                before_ne += sm.scan_n[w];
+            }
             P += sm.scan[w];
             mx = max(mx, sm.scan_max[w]);
             ne += sm.scan_n[w];
@@ -323,13 +339,21 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         int64_t C = gridDim.x;
         if (a.automatic) {
             C = min(C, (V + D4_MIN_PAGES - 1) / D4_MIN_PAGES);
+            extra = D4_SEG_PAGES;
             // sequences of one length: a whole number of CTAs per unit, each in one
             // unit only, where that streams little more than equal shares would
             const int64_t units = (int64_t)ne * a.H_kv;
             if (units > 0 && units <= C && (int64_t)ne * mx == P) {
                 const int64_t k = C / units;
-                if ((mx + k - 1) / k <= V / C + D4_SEG_PAGES) C = units * k;
+                if ((mx + k - 1) / k <= V / C + D4_SEG_PAGES) {
+                    C = units * k;
+                    extra = 0;
+                }
             }
+            own += (int64_t)own_ne * extra;
+            before += (int64_t)before_ne * extra;
+            inc += (int64_t)inc_ne * extra;
+            V += units * extra;
         }
         if (C > V) C = V;
         Ceff = (int)C;
@@ -343,7 +367,8 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         if (g0 >= first && g0 < first + own * a.H_kv) {
             int b = s0;
             for (; b < s1; ++b) {
-                const int64_t n = (int64_t)d4_pages(a, b) * a.H_kv;
+                const int np = d4_pages(a, b);
+                const int64_t n = (int64_t)(np ? np + extra : 0) * a.H_kv;
                 if (g0 < first + n) break;
                 first += n;
             }
@@ -357,9 +382,15 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         cs.b = sm.b0;
         cs.np = d4_pages(a, cs.b);
         const int64_t in = g0 - sm.base0;
-        cs.h = (int)(in / cs.np);
-        cs.pa = (int)(in - (int64_t)cs.h * cs.np);
-        cs.clip(share);
+        cs.h = (int)(in / (cs.np + extra));
+        cs.pa = (int)(in - (int64_t)cs.h * (cs.np + extra));
+        if (!cs.clip(share, extra)) {
+            if (cs.left == 0) {  // a share of work-free pages only
+                griddep_wait();
+                return;
+            }
+            cs.next(a, extra);
+        }
     }
 
     // ---- what it issues, up to D4_UNITS units ahead, across segments.  Lane 2 x + e
@@ -373,7 +404,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         while (x < 16) {
             if (ik >= in) {
                 if (is.left == 0) break;
-                is.next(a);
+                is.next(a, extra);
                 ik = 0;
                 in = is.units(warp);
                 continue;
@@ -434,7 +465,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         fetch_query(cs, 0);
         if (cs.left > 0) {
             D4Walk w = cs;
-            w.next(a);
+            w.next(a, extra);
             fetch_query(w, 1);
         }
     }
@@ -517,11 +548,11 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                 const float2 fb0 = __half22float2(u32_as_h2(sb.x)), fb1 = __half22float2(u32_as_h2(sb.y));
                 const float fa[4] = {fa0.x, fa0.y, fa1.x, fa1.y}, fb[4] = {fb0.x, fb0.y, fb1.x, fb1.y};
                 // min term: A column k = group k (the columns past 3 meet zeros)
-                float cm[4] = {0.f, 0.f, 0.f, 0.f};
+                float cm[4];
                 {
                     const uint32_t am[4] = {lds32(tile + O4_KM + 16 * r + 8 + 4 * (t & 1)),
                                             lds32(tile + O4_KM + 16 * (r + 8) + 8 + 4 * (t & 1)), 0u, 0u};
-                    mma_f16_16816(cm, am, bs[0], 0u);
+                    d4_mma0(cm, am, bs[0], 0u);
                     if constexpr (NT == 2) mma_f16_16816(cm, am, bs[1], 0u);
                 }
                 float xa[NT], xb[NT];
@@ -529,16 +560,22 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                 for (int e = 0; e < NT; ++e) xa[e] = xb[e] = 0.f;
 #pragma unroll
                 for (int gg = 0; gg < NGROUP; ++gg) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    float c[4];
 #pragma unroll
                     for (int hs = 0; hs < 2; ++hs) {
                         const uint32_t A = hs ? wa[gg] >> 8 : wa[gg], Bw = hs ? wb[gg] >> 8 : wb[gg];
                         const uint32_t af[4] = {A & 0x000f000fu, Bw & 0x000f000fu, A & 0x00f000f0u, Bw & 0x00f000f0u};
                         if constexpr (NT == 1) {
-                            mma_f16_16816(c, af, bq[2 * gg + hs][0], bq[2 * gg + hs][1]);
+                            if (hs == 0)
+                                d4_mma0(c, af, bq[2 * gg][0], bq[2 * gg][1]);
+                            else
+                                mma_f16_16816(c, af, bq[2 * gg + 1][0], bq[2 * gg + 1][1]);
                         } else {
                             const uint4 f = lds128(qf.bq[2 * gg + hs][lane]);
-                            mma_f16_16816(c, af, f.x, f.y);
+                            if (hs == 0)
+                                d4_mma0(c, af, f.x, f.y);
+                            else
+                                mma_f16_16816(c, af, f.x, f.y);
                             mma_f16_16816(c, af, f.z, f.w);
                         }
                     }
@@ -607,17 +644,14 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                 }
             };
 
-#pragma unroll 1
-            for (int k = 0; k < n_units; ++k) {
-                const int st = done % D4_UNITS;
+            // Waits for the unit in ring group st and clears, where a page is short, what the
+            // slots past the context (or of no page) hold: any bytes, NaN too; with zero value
+            // scales and mins, p = 0 meets finite factors.  Returns the pages' token counts.
+            auto wait_unit = [&](int st) {
                 wait(&sm.bar[warp][st], (done / D4_UNITS) & 1);
-                if (dead) break;
-                const int2 nt = *reinterpret_cast<const int2*>(&sm.ntok[warp][D4_U * st]);
                 static_assert(D4_U == 2, "a unit's token counts are read as a pair");
-                const bool short_page = min(nt.x, nt.y) < PAGE;  // warp-uniform
-                if (short_page) {
-                    // slots past the context (or of no page) may hold any bytes, NaN too: their
-                    // value scales and mins are cleared, so p = 0 meets finite factors
+                const int2 nt = *reinterpret_cast<const int2*>(&sm.ntok[warp][D4_U * st]);
+                if (min(nt.x, nt.y) < PAGE && !dead) {  // warp-uniform
                     for (int x = lane; x < D4_U * 64; x += 32) {
                         const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = e ? nt.y : nt.x;
                         const uint32_t keep = (2 * pair < n ? 0x0000ffffu : 0u) | (2 * pair + 1 < n ? 0xffff0000u : 0u);
@@ -626,44 +660,40 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                     }
                     __syncwarp();
                 }
-                float lg[D4_U][2][NT];
+                return nt;
+            };
+            // Logits of page e of unit k (n valid tokens); the weights form stores them.
+            auto logits = [&](int k, int slot, int e, int n, float (&lg)[2][NT]) {
+                qk_page(slot, lg);
+                if (n < PAGE) {  // warp-uniform
 #pragma unroll
-                for (int e = 0; e < D4_U; ++e) qk_page(D4_U * st + e, lg[e]);
-                if (short_page) {
-#pragma unroll
-                    for (int e = 0; e < D4_U; ++e) {
-                        const int n = e ? nt.y : nt.x;
-#pragma unroll
-                        for (int x = 0; x < NT; ++x) {
-                            if (r >= n) lg[e][0][x] = -CUDART_INF_F;
-                            if (r + 8 >= n) lg[e][1][x] = -CUDART_INF_F;
-                        }
+                    for (int x = 0; x < NT; ++x) {
+                        if (r >= n) lg[0][x] = -CUDART_INF_F;
+                        if (r + 8 >= n) lg[1][x] = -CUDART_INF_F;
                     }
                 }
                 if constexpr (WTS) {
+                    const int page = cs.pa + warp + D4_NW * (D4_U * k + e);
+                    if (page < cs.pb) {
+                        float* row = a.logits + ((u * a.max_pages + page) * PAGE + r) * G;
 #pragma unroll
-                    for (int e = 0; e < D4_U; ++e) {
-                        const int page = cs.pa + warp + D4_NW * (D4_U * k + e);
-                        if (page < cs.pb) {
-                            float* row = a.logits + ((u * a.max_pages + page) * PAGE + r) * G;
-#pragma unroll
-                            for (int x = 0; x < NT; ++x) {
-                                const int hd = NT == 1 ? t : 2 * t + x;
-                                if (hd < G) {
-                                    row[hd] = lg[e][0][x];
-                                    row[(size_t)8 * G + hd] = lg[e][1][x];
-                                }
+                        for (int x = 0; x < NT; ++x) {
+                            const int hd = NT == 1 ? t : 2 * t + x;
+                            if (hd < G) {
+                                row[hd] = lg[0][x];
+                                row[(size_t)8 * G + hd] = lg[1][x];
                             }
                         }
                     }
                 }
+            };
+            // Raises the running maxima to the page's logits where one is larger.
+            auto raise = [&](const float (&lg)[2][NT]) {
                 float top[NT];
                 bool grow = false;
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    top[x] = fmaxf(lg[0][0][x], lg[0][1][x]);
-#pragma unroll
-                    for (int e = 1; e < D4_U; ++e) top[x] = fmaxf(top[x], fmaxf(lg[e][0][x], lg[e][1][x]));
+                    top[x] = fmaxf(lg[0][x], lg[1][x]);
                     grow |= top[x] > mrun[x];
                 }
                 if (__any_sync(0xffffffffu, grow)) {
@@ -688,25 +718,48 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                         if (NT == 1) cmin[1] *= c;
                     }
                 }
+            };
+            auto softmax = [&](const float (&lg)[2][NT], float (&p)[2][NT]) {
 #pragma unroll
-                for (int e = 0; e < D4_U; ++e)
-#pragma unroll
-                    for (int x = 0; x < NT; ++x) {
-                        lg[e][0][x] = d4_ex2(lg[e][0][x] - mrun[x]);
-                        lg[e][1][x] = d4_ex2(lg[e][1][x] - mrun[x]);
-                        lsum[x] += lg[e][0][x] + lg[e][1][x];
-                    }
-#pragma unroll
-                for (int e = 0; e < D4_U; ++e) pv_page(D4_U * st + e, lg[e]);
-                ++done;
-                __syncwarp();
-                if (k + 1 < n_units) {
-                    // hand the group back, and the ones that the last segment's partial held
-                    if (s > 0 && freed < end1) wait(&sm.free_bar[buf ^ 1], ((s - 1) >> 1) & 1);
-                    freed = done;
-                    refill();
+                for (int x = 0; x < NT; ++x) {
+                    p[0][x] = d4_ex2(lg[0][x] - mrun[x]);
+                    p[1][x] = d4_ex2(lg[1][x] - mrun[x]);
+                    lsum[x] += p[0][x] + p[1][x];
                 }
+            };
+
+            // Pipelined by pages: the logits of the next page and the weighted sum of this
+            // one share a block of code, so their latencies overlap.
+            float lg[2][NT], p[2][NT];
+            int st = done % D4_UNITS;
+            int2 nt = wait_unit(st);
+            if (!dead) logits(0, D4_U * st, 0, nt.x, lg);
+#pragma unroll 1
+            for (int k = 0; k < n_units && !dead; ++k) {
+                raise(lg);
+                softmax(lg, p);
+                logits(k, D4_U * st + 1, 1, nt.y, lg);
+                pv_page(D4_U * st, p);
+                raise(lg);
+                softmax(lg, p);
+                ++done;
+                if (k + 1 == n_units) {
+                    pv_page(D4_U * st + 1, p);
+                    break;
+                }
+                const int st1 = st + 1 == D4_UNITS ? 0 : st + 1;
+                nt = wait_unit(st1);
+                if (dead) break;
+                logits(k + 1, D4_U * st1, 0, nt.x, lg);
+                pv_page(D4_U * st + 1, p);
+                st = st1;
+                __syncwarp();
+                // hand the group back, and the ones that the last segment's partial held
+                if (s > 0 && freed < end1) wait(&sm.free_bar[buf ^ 1], ((s - 1) >> 1) & 1);
+                freed = done;
+                refill();
             }
+            __syncwarp();
         }
 
         // ---- this warp's partial, in its last ring group: channels 32 g + 4 r .. + 3 of
@@ -761,7 +814,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         if (order == D4_NW - 1) {
             // ---- the last warp here merges the twelve partials in warp order and publishes
             __syncwarp();
-            const int64_t ub = g0 + (share - cs.left - (cs.pb - cs.pa)) - cs.pa;  // the unit's first page
+            const int64_t ub = g0 + share - cs.left - cs.end;  // the unit's first page
             float* slot = a.partials + (u + cta) * (size_t)(G * PART_STRIDE);
             {
                 // lane (row x0, head): the weights 2^(m_w - M) of warps x0, x0 + ROWS, ... in place
@@ -817,9 +870,9 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                 // everyone is done with this segment's queries: fetch those of segment s + 2
                 if (cs.left > 0) {
                     D4Walk w = cs;
-                    w.next(a);
+                    w.next(a, extra);
                     if (w.left > 0) {
-                        w.next(a);
+                        w.next(a, extra);
                         fence_proxy_async_smem();
                         fetch_query(w, buf);
                     }
@@ -829,7 +882,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         }
         __syncwarp();
         if (cs.left == 0) break;
-        cs.next(a);
+        cs.next(a, extra);
     }
     if (dead)  // copies in flight land before the block ends
         for (int v = done; v < issued; ++v)
