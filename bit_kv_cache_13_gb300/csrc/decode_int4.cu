@@ -4,9 +4,9 @@
 //   q' = q R_k;  a_s = <q', K^_s> scale;  p = softmax(a);  o = (sum_s p_s V^_s) R_v^T
 //
 // Bound by the 160 bytes of packed cache per token-head, if the instructions
-// that unpack them fit under the stream: one 12-warp CTA per SM, every warp
+// that unpack them fit under the stream: one CTA of 12 or 16 warps per SM, every warp
 // streaming pages through a ring of its own (bulk copies, one mbarrier per unit
-// of D4_U pages), all products on mma.sync m16n8k16 with the codes as operands.
+// of one or two pages), all products on mma.sync m16n8k16 with the codes as operands.
 //
 //   codes   a 4-bit code masked out of its 16-bit half is an fp16 subnormal,
 //           code * 2^-24 (low nibble) or 16 code * 2^-24 (next nibble): exact, one
@@ -37,7 +37,7 @@
 // touches about 7 us during which it streamed nothing (32 ragged sequences up to
 // 4K, 8 KV heads: 166 us).  The stream kernel's warps never wait for one another:
 // each walks the CTA's units by itself, its ring running ahead into the next
-// unit's pages; the last warp to leave a unit merges the twelve partials, which
+// unit's pages; the last warp to leave a unit merges its warps' partials, which
 // stand in ring slots of their own until then.
 //
 // The work is split over the CTAs on the device, by the real page counts: the
@@ -50,11 +50,13 @@
 
 namespace kvq {
 
-constexpr int D4_NW = 12;          // warps of a CTA, three per scheduler at 168 registers
-constexpr int D4_THREADS = D4_NW * 32;
-constexpr int D4_U = 2;            // pages per unit of a warp's ring
-constexpr int D4_UNITS = 3;        // units in a ring
-constexpr int D4_STAGES = D4_U * D4_UNITS;
+// NW warps of a CTA, U pages per unit of a warp's ring (one mbarrier phase, one
+// refill), UNITS units in the ring.  Up to four heads fit 128 registers, four warps
+// per scheduler; eight take 168 and three.
+template <int NT>
+struct D4Cfg {
+    static constexpr int NW = NT == 1 ? 12 : 12, U = NT == 1 ? 2 : 2, UNITS = NT == 1 ? 3 : 3;
+};
 constexpr int D4_MAX_SPLITS = 254;
 constexpr int D4_MIN_PAGES = 16;   // pages a CTA takes at least when the split is automatic
 constexpr int D4_SEG_PAGES = 40;   // what starting another unit costs a CTA, in pages streamed
@@ -244,41 +246,44 @@ struct D4Walk {
         pa = 0;
         clip(left, extra);  // (a unit's first page is a real one)
     }
-    // units of D4_U pages that warp w takes of the segment (its pages are dealt round-robin)
+    // units of U pages that warp w of NW takes of the segment (its pages are dealt round-robin)
+    template <int NW, int U>
     __device__ __forceinline__ int units(int w) const {
         const int n = pb - pa;
-        const int mine = n > w ? (n - w + D4_NW - 1) / D4_NW : 0;
-        return (mine + D4_U - 1) / D4_U;
+        const int mine = n > w ? (n - w + NW - 1) / NW : 0;
+        return (mine + U - 1) / U;
     }
 };
 
 template <int NT>
 struct __align__(128) D4Smem {
-    uint8_t ring[D4_NW][D4_STAGES][INT4_TILE];  // pages in flight; a unit's last slots keep the warp's o' [4 NT][D]
+    static constexpr int NW = D4Cfg<NT>::NW, U = D4Cfg<NT>::U, UNITS = D4Cfg<NT>::UNITS;
+    uint8_t ring[NW][U * UNITS][INT4_TILE];  // pages in flight; a unit's last slots keep the warp's o' [4 NT][D]
     D4Query<NT> query[2];                       // of segments s, s + 1
-    uint64_t bar[D4_NW][D4_UNITS], qbar[2], free_bar[2];
-    int ntok[D4_NW][D4_STAGES];                 // valid tokens of the page in each slot
-    float m_part[2][D4_NW][4 * NT], l_part[2][D4_NW][4 * NT];
-    int part_at[2][D4_NW];                      // ring group that holds the warp's o', -1: no pages
+    uint64_t bar[NW][UNITS], qbar[2], free_bar[2];
+    int ntok[NW][U * UNITS];                 // valid tokens of the page in each slot
+    float m_part[2][NW][4 * NT], l_part[2][NW][4 * NT];
+    int part_at[2][NW];                      // ring group that holds the warp's o', -1: no pages
     int arrived[2];
-    int64_t scan[D4_NW];
-    int scan_max[D4_NW], scan_n[D4_NW];
+    int64_t scan[NW];
+    int scan_max[NW], scan_n[NW];
     int64_t base0;
     int b0;
 };
 static_assert(sizeof(D4Smem<1>) <= 227 * 1024 && sizeof(D4Smem<2>) <= 227 * 1024, "decode shared memory above 227 KB");
-static_assert(8 * D * 4 <= D4_U * INT4_TILE, "a warp's partial fits one ring group");
+static_assert(4 * D * 4 <= D4Cfg<1>::U * INT4_TILE && 8 * D * 4 <= D4Cfg<2>::U * INT4_TILE, "a warp's partial fits one ring group");
 
 // NT = 1: up to four query heads per KV head, NT = 2: up to eight.
 template <int NT, bool WTS>
-__global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid_constant__ D4Args a) {
+__global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(const __grid_constant__ D4Args a) {
+    constexpr int NW = D4Cfg<NT>::NW, U = D4Cfg<NT>::U, UNITS = D4Cfg<NT>::UNITS;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     D4Smem<NT>& sm = *reinterpret_cast<D4Smem<NT>*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, t = lane & 3;
     const int G = a.G, cta = blockIdx.x;
     if (lane == 0) {
-        for (int k = 0; k < D4_UNITS; ++k) mbar_init(&sm.bar[warp][k], 1);
+        for (int k = 0; k < UNITS; ++k) mbar_init(&sm.bar[warp][k], 1);
         if (warp < 2) {
             mbar_init(&sm.qbar[warp], 1);
             mbar_init(&sm.free_bar[warp], 1);
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
     int64_t V, g0;
     int Ceff, share, extra = 0;  // extra: pages without work after each unit's, for the cost of starting it
     {
-        const int per = (a.B + D4_THREADS - 1) / D4_THREADS, s0 = min(a.B, tid * per), s1 = min(a.B, s0 + per);
+        const int per = (a.B + (NW * 32) - 1) / (NW * 32), s0 = min(a.B, tid * per), s1 = min(a.B, s0 + per);
         int64_t own = 0;
         int mx = 0, own_ne = 0;
         for (int b = s0; b < s1; ++b) {
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         int ne = 0, before_ne = 0;
         mx = 0;
 #pragma unroll
-        for (int w = 0; w < D4_NW; ++w) {
+        for (int w = 0; w < NW; ++w) {
             if (w < warp) {
                 before += sm.scan[w];
                 before_ne += sm.scan_n[w];
@@ -393,25 +398,26 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         }
     }
 
-    // ---- what it issues, up to D4_UNITS units ahead, across segments.  Lane 2 x + e
+    // ---- what it issues, up to UNITS units ahead, across segments.  Lane U x + e
     // of a batch holds page e of the batch's unit x: its id, KV head and valid tokens
     // (0: past the warp's pages).  The next batch's ids load while this one is issued.
     D4Walk is = cs;
-    int ik = 0, in = is.units(warp), issued = 0, built = 0;
-    auto build = [&](int& pid, int& hn) {  // the 16 units after the first `built`
+    int ik = 0, in = is.units<NW, U>(warp), issued = 0, built = 0;
+    constexpr int BATCH = 32 / U;  // (for U = 3, lanes 30 and 31 hold nothing)
+    auto build = [&](int& pid, int& hn) {  // the units after the first `built`
         pid = hn = 0;
         int x = 0;
-        while (x < 16) {
+        while (x < BATCH) {
             if (ik >= in) {
                 if (is.left == 0) break;
                 is.next(a, extra);
                 ik = 0;
-                in = is.units(warp);
+                in = is.units<NW, U>(warp);
                 continue;
             }
-            const int take = min(16 - x, in - ik), y = (lane >> 1) - x;
-            const int page = is.pa + warp + D4_NW * (D4_U * (ik + y) + (lane & 1));
-            if (y >= 0 && y < take && page < is.pb) {
+            const int take = min(BATCH - x, in - ik), y = lane / U - x;
+            const int page = is.pa + warp + NW * (U * (ik + y) + lane % U);
+            if (y >= 0 && y < take && lane < U * BATCH && page < is.pb) {
                 pid = __ldg(a.block_table + (size_t)is.b * a.max_pages + page);
                 hn = is.h << 8 | (page + 1 < is.np ? PAGE : min(PAGE, __ldg(a.context_lens + is.b) - page * PAGE));
             }
@@ -424,35 +430,38 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
     build(pid_c, hn_c);
     build(pid_n, hn_n);
     const uint64_t policy = l2_policy_evict_first();
-    // Lanes e < D4_U issue page e of the next unit (a page with a bad id counts no tokens).
+    // Lanes e < U issue page e of the next unit (a page with a bad id counts no tokens).
     auto issue_next = [&]() {
-        if (issued > 0 && issued % 16 == 0) {
+        if (issued > 0 && issued % BATCH == 0) {
             pid_c = pid_n;
             hn_c = hn_n;
             build(pid_n, hn_n);
         }
-        const int st = issued % D4_UNITS, from = D4_U * (issued % 16) + (lane & 1);
+        const int st = issued % UNITS, from = U * (issued % BATCH) + lane % U;
         const int pid = __shfl_sync(0xffffffffu, pid_c, from), hn = __shfl_sync(0xffffffffu, hn_c, from);
         uint64_t* bar = &sm.bar[warp][st];
-        const bool page = lane < D4_U && hn & 255, ok = page && pid >= 0 && (int64_t)pid < a.num_pages;
+        const bool page = lane < U && hn & 255, ok = page && pid >= 0 && (int64_t)pid < a.num_pages;
         if (page && !ok) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_BAD_PAGE);
-        if (lane < D4_U) sm.ntok[warp][D4_U * st + lane] = ok ? hn & 255 : 0;
-        const uint32_t n_ok = __popc(__ballot_sync(0xffffffffu, ok));
-        __syncwarp();  // the counts are ordered before lane 0's arrive
+        if (lane < U) sm.ntok[warp][U * st + lane] = ok ? hn & 255 : 0;
+        int n_ok = ok;
+        if constexpr (U > 1) {
+            n_ok = __popc(__ballot_sync(0xffffffffu, ok));
+            __syncwarp();  // the counts are ordered before lane 0's arrive
+        }
         if (lane == 0) {
             if (n_ok == 0)
                 mbar_arrive(bar);
             else
                 mbar_arrive_expect_tx(bar, n_ok * INT4_TILE);
         }
-        __syncwarp();  // the expected bytes are set before any copy is issued
+        if constexpr (U > 1) __syncwarp();  // the expected bytes are set before any copy is issued
         if (ok)
-            bulk_g2s_hint(sm.ring[warp][D4_U * st + lane], a.cache + ((size_t)pid * a.H_kv + (hn >> 8)) * INT4_TILE,
-                          INT4_TILE, bar, policy);
+            bulk_g2s_hint(sm.ring[warp][U * st + lane], a.cache + ((size_t)pid * a.H_kv + (hn >> 8)) * INT4_TILE, INT4_TILE,
+                          bar, policy);
         ++issued;
     };
 #pragma unroll 1
-    for (int k = 0; k < D4_UNITS && issued < built; ++k) issue_next();
+    for (int k = 0; k < UNITS && issued < built; ++k) issue_next();
 
     griddep_wait();  // the rotated queries are there
     griddep_launch_dependents();
@@ -482,11 +491,8 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
     int end1 = 0, end2 = 0;     // `done` at the end of the last segment, of the one before
     int freed = 0;              // units whose ring groups may be issued into again
     auto refill = [&]() {
-        if (issued >= min(built, freed + D4_UNITS) || dead) return;
-        fence_proxy_async_smem();  // the groups were read (and written) as ordinary memory
 #pragma unroll 1
-        do issue_next();
-        while (issued < min(built, freed + D4_UNITS));
+        while (issued < min(built, freed + UNITS) && !dead) issue_next();
     };
     for (int s = 0;; ++s) {
         // ================ segment s: pages [pa, pb) of unit (b, h)
@@ -498,10 +504,11 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
             wait(&sm.free_bar[buf], ((s - 2) >> 1) & 1);
             if (freed < end2) {
                 freed = end2;
+                fence_proxy_async_smem();  // (the partials were ordinary memory)
                 refill();
             }
         }
-        const int n_units = dead ? 0 : cs.units(warp);
+        const int n_units = dead ? 0 : cs.units<NW, U>(warp);
         float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
@@ -647,20 +654,29 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
             // Waits for the unit in ring group st and clears, where a page is short, what the
             // slots past the context (or of no page) hold: any bytes, NaN too; with zero value
             // scales and mins, p = 0 meets finite factors.  Returns the pages' token counts.
+            struct Counts {
+                int n[U];
+            };
             auto wait_unit = [&](int st) {
-                wait(&sm.bar[warp][st], (done / D4_UNITS) & 1);
-                static_assert(D4_U == 2, "a unit's token counts are read as a pair");
-                const int2 nt = *reinterpret_cast<const int2*>(&sm.ntok[warp][D4_U * st]);
-                if (min(nt.x, nt.y) < PAGE && !dead) {  // warp-uniform
-                    for (int x = lane; x < D4_U * 64; x += 32) {
-                        const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = e ? nt.y : nt.x;
+                wait(&sm.bar[warp][st], (done / UNITS) & 1);
+                Counts c;
+                int least = PAGE;
+#pragma unroll
+                for (int e = 0; e < U; ++e) {
+                    c.n[e] = sm.ntok[warp][U * st + e];
+                    least = min(least, c.n[e]);
+                }
+                if (least < PAGE && !dead) {  // warp-uniform
+                    for (int x = lane; x < U * 64; x += 32) {
+                        const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = sm.ntok[warp][U * st + e];
                         const uint32_t keep = (2 * pair < n ? 0x0000ffffu : 0u) | (2 * pair + 1 < n ? 0xffff0000u : 0u);
-                        uint32_t* word = reinterpret_cast<uint32_t*>(sm.ring[warp][D4_U * st + e] + O4_VS) + w;
+                        uint32_t* word = reinterpret_cast<uint32_t*>(sm.ring[warp][U * st + e] + O4_VS) + w;
                         if (keep != 0xffffffffu) *word &= keep;
                     }
+                    fence_proxy_async_smem();  // (written as ordinary memory: before the slots' next copies)
                     __syncwarp();
                 }
-                return nt;
+                return c;
             };
             // Logits of page e of unit k (n valid tokens); the weights form stores them.
             auto logits = [&](int k, int slot, int e, int n, float (&lg)[2][NT]) {
@@ -673,7 +689,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                     }
                 }
                 if constexpr (WTS) {
-                    const int page = cs.pa + warp + D4_NW * (D4_U * k + e);
+                    const int page = cs.pa + warp + NW * (U * k + e);
                     if (page < cs.pb) {
                         float* row = a.logits + ((u * a.max_pages + page) * PAGE + r) * G;
 #pragma unroll
@@ -731,31 +747,37 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
             // Pipelined by pages: the logits of the next page and the weighted sum of this
             // one share a block of code, so their latencies overlap.
             float lg[2][NT], p[2][NT];
-            int st = done % D4_UNITS;
-            int2 nt = wait_unit(st);
-            if (!dead) logits(0, D4_U * st, 0, nt.x, lg);
+            int st = done % UNITS;
+            Counts nt = wait_unit(st);
+            if (!dead) logits(0, U * st, 0, nt.n[0], lg);
 #pragma unroll 1
             for (int k = 0; k < n_units && !dead; ++k) {
                 raise(lg);
                 softmax(lg, p);
-                logits(k, D4_U * st + 1, 1, nt.y, lg);
-                pv_page(D4_U * st, p);
-                raise(lg);
-                softmax(lg, p);
+#pragma unroll
+                for (int e = 1; e < U; ++e) {
+                    logits(k, U * st + e, e, nt.n[e], lg);
+                    pv_page(U * st + e - 1, p);
+                    raise(lg);
+                    softmax(lg, p);
+                }
                 ++done;
                 if (k + 1 == n_units) {
-                    pv_page(D4_U * st + 1, p);
+                    pv_page(U * st + U - 1, p);
                     break;
                 }
-                const int st1 = st + 1 == D4_UNITS ? 0 : st + 1;
+                const int st1 = st + 1 == UNITS ? 0 : st + 1;
                 nt = wait_unit(st1);
                 if (dead) break;
-                logits(k + 1, D4_U * st1, 0, nt.x, lg);
-                pv_page(D4_U * st + 1, p);
+                logits(k + 1, U * st1, 0, nt.n[0], lg);
+                pv_page(U * st + U - 1, p);
                 st = st1;
                 __syncwarp();
                 // hand the group back, and the ones that the last segment's partial held
-                if (s > 0 && freed < end1) wait(&sm.free_bar[buf ^ 1], ((s - 1) >> 1) & 1);
+                if (s > 0 && freed < end1) {
+                    wait(&sm.free_bar[buf ^ 1], ((s - 1) >> 1) & 1);
+                    fence_proxy_async_smem();  // (the partials were ordinary memory)
+                }
                 freed = done;
                 refill();
             }
@@ -765,9 +787,9 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         // ---- this warp's partial, in its last ring group: channels 32 g + 4 r .. + 3 of
         // its head(s)
         const bool has = n_units > 0 && !dead;
-        const int at = (done - 1) % D4_UNITS;
+        const int at = (done - 1) % UNITS;
         if (has) {
-            float* op = reinterpret_cast<float*>(sm.ring[warp][D4_U * at]);
+            float* op = reinterpret_cast<float*>(sm.ring[warp][U * at]);
 #pragma unroll
             for (int gg = 0; gg < NGROUP; ++gg) {
                 if constexpr (NT == 1) {
@@ -805,14 +827,15 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
         end1 = done;
         __syncwarp();
         int order = 0;
+        fence_proxy_async_smem();
         if (lane == 0) {
             __threadfence_block();
             order = atomicAdd(&sm.arrived[buf], 1);
             __threadfence_block();
         }
         order = __shfl_sync(0xffffffffu, order, 0);
-        if (order == D4_NW - 1) {
-            // ---- the last warp here merges the twelve partials in warp order and publishes
+        if (order == NW - 1) {
+            // ---- the last warp here merges its warps' partials in warp order and publishes
             __syncwarp();
             const int64_t ub = g0 + share - cs.left - cs.end;  // the unit's first page
             float* slot = a.partials + (u + cta) * (size_t)(G * PART_STRIDE);
@@ -823,11 +846,11 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                 const int j = lane % MAXG, x0 = lane / MAXG;
                 float M = D4_NEG, L = 0.f;
 #pragma unroll
-                for (int w = x0; w < D4_NW; w += ROWS) M = fmaxf(M, sm.m_part[buf][w][j]);
+                for (int w = x0; w < NW; w += ROWS) M = fmaxf(M, sm.m_part[buf][w][j]);
 #pragma unroll
                 for (int o = 16; o >= MAXG; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
-                for (int w = x0; w < D4_NW; w += ROWS) {
+                for (int w = x0; w < NW; w += ROWS) {
                     const float f = sm.part_at[buf][w] >= 0 ? d4_ex2(sm.m_part[buf][w][j] - M) : 0.f;
                     sm.m_part[buf][w][j] = f;
                     L = fmaf(sm.l_part[buf][w][j], f, L);
@@ -837,25 +860,28 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
                 if (lane < G) *reinterpret_cast<float2*>(slot + (size_t)lane * PART_STRIDE) = make_float2(M, L);
                 __syncwarp();
             }
-            int at_w[D4_NW];
-#pragma unroll
-            for (int w = 0; w < D4_NW; ++w) at_w[w] = sm.part_at[buf][w];
 #pragma unroll 1
             for (int j = 0; j < G; ++j) {
-                float4 x[D4_NW];
-#pragma unroll
-                for (int w = 0; w < D4_NW; ++w)
-                    x[w] = at_w[w] >= 0 ? *reinterpret_cast<const float4*>(
-                                              reinterpret_cast<const float*>(sm.ring[w][D4_U * at_w[w]]) + j * D + 4 * lane)
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
                 float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                constexpr int HALF = NW / 2;  // partials in flight
 #pragma unroll
-                for (int w = 0; w < D4_NW; ++w) {
-                    const float f = sm.m_part[buf][w][j];
-                    O.x = fmaf(x[w].x, f, O.x);
-                    O.y = fmaf(x[w].y, f, O.y);
-                    O.z = fmaf(x[w].z, f, O.z);
-                    O.w = fmaf(x[w].w, f, O.w);
+                for (int w0 = 0; w0 < NW; w0 += HALF) {
+                    float4 x[HALF];
+#pragma unroll
+                    for (int w = 0; w < HALF; ++w) {
+                        const int at_w = sm.part_at[buf][w0 + w];
+                        x[w] = at_w >= 0 ? *reinterpret_cast<const float4*>(
+                                               reinterpret_cast<const float*>(sm.ring[w0 + w][U * at_w]) + j * D + 4 * lane)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int w = 0; w < HALF; ++w) {
+                        const float f = sm.m_part[buf][w0 + w][j];
+                        O.x = fmaf(x[w].x, f, O.x);
+                        O.y = fmaf(x[w].y, f, O.y);
+                        O.z = fmaf(x[w].z, f, O.z);
+                        O.w = fmaf(x[w].w, f, O.w);
+                    }
                 }
                 *reinterpret_cast<float4*>(slot + (size_t)j * PART_STRIDE + 4 + 4 * lane) = O;
             }
@@ -886,7 +912,7 @@ __global__ void __launch_bounds__(D4_THREADS, 1) decode_int4_kernel(const __grid
     }
     if (dead)  // copies in flight land before the block ends
         for (int v = done; v < issued; ++v)
-            (void)mbar_wait_bounded(&sm.bar[warp][v % D4_UNITS], (v / D4_UNITS) & 1, 1000000LL);
+            (void)mbar_wait_bounded(&sm.bar[warp][v % UNITS], (v / UNITS) & 1, 1000000LL);
 }
 
 // ------------------------------------------------------------------ 3: finish
@@ -1169,7 +1195,7 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const size_t smem = G <= 4 ? sizeof(D4Smem<1>) : sizeof(D4Smem<2>);
     st = d4_smem_once((const void*)kerns[which], (int)smem, which);
     if (st != KVQ_OK) return st;
-    st = kvq_check_cuda(launch_pdl(kerns[which], dim3((unsigned)C), dim3(D4_THREADS), smem, cs, a),
+    st = kvq_check_cuda(launch_pdl(kerns[which], dim3((unsigned)C), dim3(32 * (G <= 4 ? D4Cfg<1>::NW : D4Cfg<2>::NW)), smem, cs, a),
                         "kvq_decode_attn_int4 launch");
     if (st != KVQ_OK) return st;
     // 3: few units are finished by four CTAs each (a quarter of R_v each), and
