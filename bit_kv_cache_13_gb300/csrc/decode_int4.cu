@@ -426,39 +426,42 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         }
         built += x;
     };
-    int pid_c, hn_c, pid_n, hn_n;
-    build(pid_c, hn_c);
-    build(pid_n, hn_n);
-    const uint64_t policy = l2_policy_evict_first();
-    // Lanes e < U issue page e of the next unit (a page with a bad id counts no tokens).
-    auto issue_next = [&]() {
-        if (issued > 0 && issued % BATCH == 0) {
-            pid_c = pid_n;
-            hn_c = hn_n;
-            build(pid_n, hn_n);
-        }
-        const int st = issued % UNITS, from = U * (issued % BATCH) + lane % U;
-        const int pid = __shfl_sync(0xffffffffu, pid_c, from), hn = __shfl_sync(0xffffffffu, hn_c, from);
-        uint64_t* bar = &sm.bar[warp][st];
-        const bool page = lane < U && hn & 255, ok = page && pid >= 0 && (int64_t)pid < a.num_pages;
+    int pid_n, hn_n;          // of the next batch: as loaded
+    uint32_t tile_c, n_c;     // of this one: (page, KV head) tile, valid tokens (0: no page, or a bad id)
+    uint32_t ok_mask = 0;     // lanes of this batch that hold a page
+    bool any_bad = false;     // a bad id was seen: token counts are read back for every unit from then on
+    auto turn = [&]() {       // the next batch becomes this one
+        const bool page = hn_n & 255, ok = page && pid_n >= 0 && (int64_t)pid_n < a.num_pages;
         if (page && !ok) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_BAD_PAGE);
-        if (lane < U) sm.ntok[warp][U * st + lane] = ok ? hn & 255 : 0;
-        int n_ok = ok;
-        if constexpr (U > 1) {
-            n_ok = __popc(__ballot_sync(0xffffffffu, ok));
-            __syncwarp();  // the counts are ordered before lane 0's arrive
+        any_bad |= __any_sync(0xffffffffu, page && !ok);
+        tile_c = ok ? (uint32_t)pid_n * (uint32_t)a.H_kv + (uint32_t)(hn_n >> 8) : 0u;
+        n_c = ok ? hn_n & 255 : 0;
+        ok_mask = __ballot_sync(0xffffffffu, ok);
+        build(pid_n, hn_n);
+    };
+    build(pid_n, hn_n);
+    turn();
+    const uint64_t policy = l2_policy_evict_first();
+    int ist = 0, ix = 0;      // ring group and batch place of the next unit
+    // Lanes e < U issue page e of the next unit.  (The copies may land before their
+    // bytes are announced: the phase is open until lane 0 arrives.)
+    auto issue_next = [&]() {
+        if (ix == BATCH) {
+            turn();
+            ix = 0;
         }
-        if (lane == 0) {
-            if (n_ok == 0)
-                mbar_arrive(bar);
-            else
-                mbar_arrive_expect_tx(bar, n_ok * INT4_TILE);
+        const int from = U * ix + lane % U;
+        const uint32_t tile = __shfl_sync(0xffffffffu, tile_c, from), n = __shfl_sync(0xffffffffu, n_c, from);
+        uint64_t* bar = &sm.bar[warp][ist];
+        if (lane < U) {
+            sm.ntok[warp][U * ist + lane] = (int)n;
+            if (n) bulk_g2s_hint(sm.ring[warp][U * ist + lane], a.cache + (size_t)tile * INT4_TILE, INT4_TILE, bar, policy);
         }
-        if constexpr (U > 1) __syncwarp();  // the expected bytes are set before any copy is issued
-        if (ok)
-            bulk_g2s_hint(sm.ring[warp][U * st + lane], a.cache + ((size_t)pid * a.H_kv + (hn >> 8)) * INT4_TILE, INT4_TILE,
-                          bar, policy);
+        __syncwarp();  // the counts are ordered before the arrive
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(ok_mask >> (U * ix) & ((1u << U) - 1)) * INT4_TILE);
         ++issued;
+        ++ix;
+        ist = ist + 1 == UNITS ? 0 : ist + 1;
     };
 #pragma unroll 1
     for (int k = 0; k < UNITS && issued < built; ++k) issue_next();
@@ -481,13 +484,15 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
 
     bool dead = false;  // a wait of this warp ran out: it takes part without data
     auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
         const bool ok = mbar_wait_bounded(bar, parity, WAIT_LIMIT_CYCLES);
         if (__any_sync(0xffffffffu, !ok)) {
             if (lane == 0) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_TIMEOUT);
             dead = true;
         }
     };
-    int done = 0;               // units consumed
+    int done = 0, st = 0;       // units consumed, the next one's ring group
+    uint32_t parity = 0;        // and the parity of its phase
     int end1 = 0, end2 = 0;     // `done` at the end of the last segment, of the one before
     int freed = 0;              // units whose ring groups may be issued into again
     auto refill = [&]() {
@@ -654,27 +659,33 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             // Waits for the unit in ring group st and clears, where a page is short, what the
             // slots past the context (or of no page) hold: any bytes, NaN too; with zero value
             // scales and mins, p = 0 meets finite factors.  Returns the pages' token counts.
+            // Only a warp's last unit of a segment can hold its end (`last`): the others are full,
+            // unless a bad id was seen.
             struct Counts {
                 int n[U];
             };
-            auto wait_unit = [&](int st) {
-                wait(&sm.bar[warp][st], (done / UNITS) & 1);
+            auto wait_unit = [&](bool last) {
                 Counts c;
-                int least = PAGE;
 #pragma unroll
-                for (int e = 0; e < U; ++e) {
-                    c.n[e] = sm.ntok[warp][U * st + e];
-                    least = min(least, c.n[e]);
-                }
-                if (least < PAGE && !dead) {  // warp-uniform
-                    for (int x = lane; x < U * 64; x += 32) {
-                        const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = sm.ntok[warp][U * st + e];
-                        const uint32_t keep = (2 * pair < n ? 0x0000ffffu : 0u) | (2 * pair + 1 < n ? 0xffff0000u : 0u);
-                        uint32_t* word = reinterpret_cast<uint32_t*>(sm.ring[warp][U * st + e] + O4_VS) + w;
-                        if (keep != 0xffffffffu) *word &= keep;
+                for (int e = 0; e < U; ++e) c.n[e] = PAGE;
+                wait(&sm.bar[warp][st], parity);
+                if (last || any_bad) {
+                    int least = PAGE;
+#pragma unroll
+                    for (int e = 0; e < U; ++e) {
+                        c.n[e] = sm.ntok[warp][U * st + e];
+                        least = min(least, c.n[e]);
                     }
-                    fence_proxy_async_smem();  // (written as ordinary memory: before the slots' next copies)
-                    __syncwarp();
+                    if (least < PAGE && !dead) {  // warp-uniform
+                        for (int x = lane; x < U * 64; x += 32) {
+                            const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = sm.ntok[warp][U * st + e];
+                            const uint32_t keep = (2 * pair < n ? 0x0000ffffu : 0u) | (2 * pair + 1 < n ? 0xffff0000u : 0u);
+                            uint32_t* word = reinterpret_cast<uint32_t*>(sm.ring[warp][U * st + e] + O4_VS) + w;
+                            if (keep != 0xffffffffu) *word &= keep;
+                        }
+                        fence_proxy_async_smem();  // (written as ordinary memory: before the slots' next copies)
+                        __syncwarp();
+                    }
                 }
                 return c;
             };
@@ -747,8 +758,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             // Pipelined by pages: the logits of the next page and the weighted sum of this
             // one share a block of code, so their latencies overlap.
             float lg[2][NT], p[2][NT];
-            int st = done % UNITS;
-            Counts nt = wait_unit(st);
+            Counts nt = wait_unit(n_units == 1);
             if (!dead) logits(0, U * st, 0, nt.n[0], lg);
 #pragma unroll 1
             for (int k = 0; k < n_units && !dead; ++k) {
@@ -762,16 +772,19 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                     softmax(lg, p);
                 }
                 ++done;
+                const int last = U * st + U - 1;
+                if (++st == UNITS) {
+                    st = 0;
+                    parity ^= 1u;
+                }
                 if (k + 1 == n_units) {
-                    pv_page(U * st + U - 1, p);
+                    pv_page(last, p);
                     break;
                 }
-                const int st1 = st + 1 == UNITS ? 0 : st + 1;
-                nt = wait_unit(st1);
+                nt = wait_unit(k + 2 == n_units);
                 if (dead) break;
-                logits(k + 1, U * st1, 0, nt.n[0], lg);
-                pv_page(U * st + U - 1, p);
-                st = st1;
+                logits(k + 1, U * st, 0, nt.n[0], lg);
+                pv_page(last, p);
                 __syncwarp();
                 // hand the group back, and the ones that the last segment's partial held
                 if (s > 0 && freed < end1) {
@@ -787,7 +800,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         // ---- this warp's partial, in its last ring group: channels 32 g + 4 r .. + 3 of
         // its head(s)
         const bool has = n_units > 0 && !dead;
-        const int at = (done - 1) % UNITS;
+        const int at = st == 0 ? UNITS - 1 : st - 1;
         if (has) {
             float* op = reinterpret_cast<float*>(sm.ring[warp][U * at]);
 #pragma unroll
@@ -1135,6 +1148,7 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: %d splits above %d", fn, num_splits, D4_MAX_SPLITS);
     if (!q || !cache || !block_table || !context_lens || !R_k || !R_v || !out || !workspace || (with_weights && !weights))
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (num_pages > (int64_t(1) << 32) / H_kv) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: num_pages * H_kv above 2^32", fn);
     for (const void* p : {q, cache, (const void*)R_k, (const void*)R_v, (const void*)out, (const void*)workspace})
         if (reinterpret_cast<uintptr_t>(p) % 16)
             return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: q, cache, R_k, R_v, out and workspace need 16-byte alignment", fn);
