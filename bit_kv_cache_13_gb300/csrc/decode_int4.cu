@@ -126,96 +126,114 @@ struct D4Args {
 
 // ------------------------------------------------------------------ 1: rotate
 
-// One CTA of 256 threads per KV head and run of `per` sequences; a thread
-// holds half a column of R_k in registers.
+// One CTA of 128 threads per KV head, group of 32 rotated channels and run of
+// `per` sequences (a group is two K steps and one column of the min term).  Thread
+// (channel, part) holds 32 rows of its column of R_k in registers.  The pre-scales
+// come from the norm of q, which bounds every rotated value: |q'| sigma stays below
+// 2^12 (fp16 ends at 2^16, so a matrix that is not quite a rotation has room) and
+// |S| sigma_s, S a sum of 32, below 2^12 sqrt(32) / 8.  The kernel also has L2 fetch
+// what the next two read first.
 template <int NT>
-__global__ void __launch_bounds__(256) rotate_int4_kernel(const __grid_constant__ D4Args a, int per) {
-    constexpr int MAXG = 4 * NT;
-    __shared__ __align__(16) float qin[MAXG][D], red[2][MAXG][D], qs[MAXG][D];
-    __shared__ float gsum[MAXG][NGROUP], sigma[MAXG], sigma_s[MAXG];
+__global__ void __launch_bounds__(128, 8) rotate_int4_kernel(const __grid_constant__ D4Args a, int per) {
+    constexpr int MAXG = 4 * NT, PARTS = 4, ROWS = D / PARTS;
+    __shared__ __align__(16) float qin[MAXG][D];
+    __shared__ float red[PARTS][MAXG][32], qs[MAXG][32], gsum[MAXG], sigma[MAXG];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
-    const int h = blockIdx.x, G = a.G, c = tid & (D - 1), half = tid >> 7;
-    const float* R = a.Rk + (size_t)h * D * D;
-    for (int i = tid; i < D * D / 32; i += 256) prefetch_l2(R + 32 * i);
+    const int h = blockIdx.x >> 2, g = blockIdx.x & 3, G = a.G;
+    const float* R = a.Rk + (size_t)h * D * D + 32 * g + (size_t)ROWS * warp * D + lane;
+    prefetch_l2(R - lane + (size_t)lane * D);
+    prefetch_l2_keep(a.Rv + (size_t)h * D * D + 4096 * g + 32 * tid);
     griddep_wait();
     griddep_launch_dependents();  // (after the wait: what the next kernel reads early is complete)
-    float rr[64];
+    float rr[ROWS];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) rr[i] = __ldg(R + (size_t)(64 * half + i) * D + c);
+    for (int i = 0; i < ROWS; ++i) rr[i] = __ldg(R + (size_t)i * D);
+    {
+        const int64_t x = 128 * ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) + tid;  // lines of the tables
+        if (x <= (a.B - 1) / 32) prefetch_l2(a.context_lens + 32 * x);
+        if (x <= ((int64_t)a.B * a.max_pages - 1) / 32) prefetch_l2(a.block_table + 32 * x);
+    }
     for (int b = blockIdx.y * per; b < min(a.B, (int)(blockIdx.y + 1) * per); ++b) {
         const __nv_bfloat16* qb = a.q + ((size_t)b * a.H_q + (size_t)h * G) * D;
-        for (int i = tid; i < MAXG * D; i += 256) qin[i / D][i % D] = i < G * D ? __bfloat162float(qb[i]) : 0.f;
+        uint2 raw[NT];
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {  // a warp per head (two for NT == 2): its values and their norm
+            const int j = warp + 4 * e;
+            raw[e] = j < G ? __ldg(reinterpret_cast<const uint2*>(qb + j * D) + lane) : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
+            const int j = warp + 4 * e;
+            const float4 x = make_float4(__uint_as_float(raw[e].x << 16), __uint_as_float(raw[e].x & 0xffff0000u),
+                                         __uint_as_float(raw[e].y << 16), __uint_as_float(raw[e].y & 0xffff0000u));
+            *reinterpret_cast<float4*>(&qin[j][4 * lane]) = x;
+            float n2 = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w)));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+            if (lane == 0) sigma[j] = d4_prescale(sqrtf(n2) * fabsf(a.scale_log2) * 8.f);
+        }
         __syncthreads();
         float acc[MAXG];
 #pragma unroll
         for (int j = 0; j < MAXG; ++j) acc[j] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 64; i += 4)
+        for (int i = 0; i < ROWS; i += 4)
 #pragma unroll
             for (int j = 0; j < MAXG; ++j) {
-                const float4 x = *reinterpret_cast<const float4*>(&qin[j][64 * half + i]);
+                const float4 x = *reinterpret_cast<const float4*>(&qin[j][ROWS * warp + i]);
                 acc[j] = fmaf(x.x, rr[i], fmaf(x.y, rr[i + 1], fmaf(x.z, rr[i + 2], fmaf(x.w, rr[i + 3], acc[j]))));
             }
 #pragma unroll
-        for (int j = 0; j < MAXG; ++j) red[half][j][c] = acc[j];
+        for (int j = 0; j < MAXG; ++j) red[warp][j][lane] = acc[j];
         __syncthreads();
-        // per head: the pre-scales (largest |q'| and |S| into [2^14, 2^15)) and the group sums
-        if (warp < MAXG) {
-            const int j = warp;
-            float mx = 0.f, ms = 0.f, gs[NGROUP];
 #pragma unroll
-            for (int g = 0; g < NGROUP; ++g) {
-                const int ch = 32 * g + lane;
-                const float x = (red[0][j][ch] + red[1][j][ch]) * a.scale_log2;
-                qs[j][ch] = x;
-                mx = fmaxf(mx, fabsf(x));
-                gs[g] = x;
-            }
+        for (int e = 0; e < NT; ++e) {
+            const int j = warp + 4 * e;
+            float x = ((red[0][j][lane] + red[1][j][lane]) + (red[2][j][lane] + red[3][j][lane])) * a.scale_log2;
+            qs[j][lane] = x;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-#pragma unroll
-                for (int g = 0; g < NGROUP; ++g) gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], o);
-            }
-#pragma unroll
-            for (int g = 0; g < NGROUP; ++g) ms = fmaxf(ms, fabsf(gs[g]));
-            if (lane == 0) {
-                sigma[j] = d4_prescale(mx);
-                sigma_s[j] = d4_prescale(ms);
-#pragma unroll
-                for (int g = 0; g < NGROUP; ++g) gsum[j][g] = gs[g];
-            }
+            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == 0) gsum[j] = x;
         }
         __syncthreads();
-        // K step s = 2 g + hs: b0 = channels 32 g + 8 t + 2 hs and + 4 (codes in the low
-        // nibble), b1 = the channels after those (the next nibble: 16 times the code)
+        // K step 2 g + hs: b0 = channels 32 g + 8 t + 2 hs and + 4 (codes in the low nibble),
+        // b1 = the channels after those (the next nibble: 16 times the code)
         auto parts = [](float v0, float v1, bool low) {
             const float h0 = __half2float(__float2half_rn(v0)), h1 = __half2float(__float2half_rn(v1));
             return low ? pack_half2(v0 - h0, v1 - h1) : pack_half2(h0, h1);
         };
         auto q_frag = [&](int j, int e, bool low) {
-            const int c0 = 32 * (warp >> 1) + 8 * t + 2 * (warp & 1) + e;
+            const int c0 = 8 * t + 2 * warp + e;
             const float f = sigma[j] * (e ? 0.0625f : 1.f);
             return parts(qs[j][c0] * f, qs[j][c0 + 4] * f, low);
         };
-        auto s_frag = [&](int j, bool low) {  // group sums 2 t, 2 t + 1 (t < 2)
-            return t >= 2 ? 0u : parts(gsum[j][2 * t] * sigma_s[j], gsum[j][2 * t + 1] * sigma_s[j], low);
-        };
         D4Query<NT>& out = static_cast<D4Query<NT>*>(a.query)[(size_t)b * a.H_kv + h];
-        if constexpr (NT == 1) {  // column r: head r / 2, high (r even) or low part
-            *reinterpret_cast<uint2*>(out.bq[warp][lane]) = make_uint2(q_frag(r >> 1, 0, r & 1), q_frag(r >> 1, 1, r & 1));
-            if (warp == 0) out.bs[lane][0] = s_frag(r >> 1, r & 1);
-        } else {                  // column r: head r
-            *reinterpret_cast<uint4*>(out.bq[warp][lane]) =
-                make_uint4(q_frag(r, 0, false), q_frag(r, 1, false), q_frag(r, 0, true), q_frag(r, 1, true));
-            if (warp == 0) *reinterpret_cast<uint2*>(out.bs[lane]) = make_uint2(s_frag(r, false), s_frag(r, true));
+        if (warp < 2) {
+            if constexpr (NT == 1)  // column r: head r / 2, high (r even) or low part
+                *reinterpret_cast<uint2*>(out.bq[2 * g + warp][lane]) = make_uint2(q_frag(r >> 1, 0, r & 1), q_frag(r >> 1, 1, r & 1));
+            else                    // column r: head r
+                *reinterpret_cast<uint4*>(out.bq[2 * g + warp][lane]) =
+                    make_uint4(q_frag(r, 0, false), q_frag(r, 1, false), q_frag(r, 0, true), q_frag(r, 1, true));
+        } else if (warp == 2 && t == (g >> 1)) {
+            // the min term's K index 2 t + e is group g: this CTA's half of lane (r, g / 2)
+            const int j = NT == 1 ? r >> 1 : r;
+            const float v = gsum[j] * sigma[j] * 0.125f, hi = __half2float(__float2half_rn(v));
+            __half* bs = reinterpret_cast<__half*>(out.bs[lane]) + (g & 1);
+            if constexpr (NT == 1) {
+                bs[0] = __float2half_rn(r & 1 ? v - hi : hi);
+            } else {
+                bs[0] = __float2half_rn(hi);
+                bs[2] = __float2half_rn(v - hi);
+            }
+        } else if (warp == 3 && g == 0) {
+            if (t >= 2)
+                for (int e = 0; e < NT; ++e) out.bs[lane][e] = 0u;
+            if (lane < MAXG) {
+                out.inv_q[lane] = 16777216.f / sigma[lane];
+                out.inv_s[lane] = 8.f / sigma[lane];
+            }
         }
-        if (tid < MAXG) {
-            out.inv_q[tid] = 16777216.f / sigma[tid];
-            out.inv_s[tid] = 1.f / sigma_s[tid];
-        }
-        // (the next round's first barrier comes before anything read here is overwritten,
-        // but for qin, last read before the second barrier above)
+        __syncthreads();  // sigma, qs and gsum are read above; the next round writes them
     }
 }
 
@@ -463,8 +481,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         ++ix;
         ist = ist + 1 == UNITS ? 0 : ist + 1;
     };
-#pragma unroll 1
-    for (int k = 0; k < UNITS && issued < built; ++k) issue_next();
+    if (built > 0) issue_next();
 
     griddep_wait();  // the rotated queries are there
     griddep_launch_dependents();
@@ -481,6 +498,9 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             fetch_query(w, 1);
         }
     }
+    // (the rest of the ring after the queries, which would queue behind it)
+#pragma unroll 1
+    while (issued < min(built, UNITS)) issue_next();
 
     bool dead = false;  // a wait of this warp ran out: it takes part without data
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -930,15 +950,15 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
 
 // ------------------------------------------------------------------ 3: finish
 
-// n_finish CTAs of 256 threads: RS of them per unit, D / RS rows of R_v each.
+// n_finish CTAs of 512 threads: RS of them per unit, D / RS rows of R_v each.
 // They merge the unit's partials (warp = head and every P-th partial), normalise
 // and rotate.  The others add weights: chunk x of a unit takes its tokens
-// 256 x .. + 255 and every chunks * 256 on.
+// 512 x .. + 511 and every chunks * 512 on.
 template <int RS, bool WTS>
-__global__ void __launch_bounds__(256) finish_int4_kernel(const __grid_constant__ D4Args a) {
-    constexpr int RW = D / RS / 8;  // rows of R_v a warp rotates
-    __shared__ __align__(16) float o[8][D], part[8][D];
-    __shared__ float pm[8][8], pl[8][8], Mh[8], inv[8];
+__global__ void __launch_bounds__(512) finish_int4_kernel(const __grid_constant__ D4Args a) {
+    constexpr int RW = D / RS / 16;  // rows of R_v a warp rotates
+    __shared__ __align__(16) float part[16][D], o[8][D];
+    __shared__ float Mh[8], inv[8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
     if (!WTS || (int)blockIdx.x < a.n_finish) {
         const size_t u = blockIdx.x / RS;
@@ -957,50 +977,67 @@ __global__ void __launch_bounds__(256) finish_int4_kernel(const __grid_constant_
             return;
         }
         const int2 info = __ldcg(a.info + u);
-        const int P = 8 / G, j = warp % G, p = warp / G;
+        const int P = 16 / G, j = warp % G, p = warp / G;
         if (p < P) {
-            constexpr int CH = 8;
             const float* ps = a.partials + (u + info.x) * (size_t)(G * PART_STRIDE) + (size_t)j * PART_STRIDE;
+            const size_t step = (size_t)G * PART_STRIDE;
+            // every warp of a head finds its M and L, a partial per lane; its own outputs are
+            // partials p, p + P, ... (32 partials at a time, four of its own in flight)
             float M = D4_NEG, L = 0.f;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int s0 = p; s0 < info.y; s0 += P * CH) {
-                float2 ml[CH];
+            for (int base = 0; base < info.y; base += 32) {
+                constexpr int CH = 4;
                 float4 ov[CH];
+                const int end = min(info.y, base + 32);
+                const float2 ml = base + lane < end ? __ldcg(reinterpret_cast<const float2*>(ps + (base + lane) * step))
+                                                    : make_float2(D4_NEG, 0.f);
+                float top = M;
+                for (int s0 = base + p; s0 < end; s0 += P * CH) {
 #pragma unroll
-                for (int x = 0; x < CH; ++x) {
-                    const int s = s0 + P * x;
-                    const float* q = ps + (size_t)s * G * PART_STRIDE;
-                    ml[x] = s < info.y ? __ldcg(reinterpret_cast<const float2*>(q)) : make_float2(D4_NEG, 0.f);
-                    ov[x] = s < info.y ? __ldcg(reinterpret_cast<const float4*>(q + 4 + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+                    for (int x = 0; x < CH; ++x)
+                        ov[x] = s0 + P * x < end ? __ldcg(reinterpret_cast<const float4*>(ps + (s0 + P * x) * step + 4 + 4 * lane))
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (s0 == base + p) {  // the running maximum, once the loads are out
+                        top = fmaxf(M, ml.x);
 #pragma unroll
-                for (int x = 0; x < CH; ++x) {
-                    const float Mn = fmaxf(M, ml[x].x), fo = d4_ex2(M - Mn), fn = d4_ex2(ml[x].x - Mn);
-                    L = fmaf(L, fo, ml[x].y * fn);
-                    O.x = fmaf(O.x, fo, ov[x].x * fn);
-                    O.y = fmaf(O.y, fo, ov[x].y * fn);
-                    O.z = fmaf(O.z, fo, ov[x].z * fn);
-                    O.w = fmaf(O.w, fo, ov[x].w * fn);
-                    M = Mn;
+                        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const float c = d4_ex2(M - top);
+                        O = make_float4(O.x * c, O.y * c, O.z * c, O.w * c);
+                    }
+                    const float f_own = d4_ex2(ml.x - top);
+#pragma unroll
+                    for (int x = 0; x < CH; ++x) {
+                        const float f = __shfl_sync(0xffffffffu, f_own, (s0 + P * x - base) & 31);  // (past the end: times zeros)
+                        O.x = fmaf(ov[x].x, f, O.x);
+                        O.y = fmaf(ov[x].y, f, O.y);
+                        O.z = fmaf(ov[x].z, f, O.z);
+                        O.w = fmaf(ov[x].w, f, O.w);
+                    }
                 }
+                if (base + p >= end) {  // no partial of its own here: only the maximum and the sum
+                    top = fmaxf(M, ml.x);
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    const float c = d4_ex2(M - top);
+                    O = make_float4(O.x * c, O.y * c, O.z * c, O.w * c);
+                }
+                float l = ml.y * d4_ex2(ml.x - top);
+#pragma unroll
+                for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                L = fmaf(L, d4_ex2(M - top), l);
+                M = top;
             }
-            *reinterpret_cast<float4*>(&part[warp][4 * lane]) = O;
-            if (lane == 0) {
-                pm[p][j] = M;
-                pl[p][j] = L;
-            }
+            const float inv_l = L > 0.f ? 1.f / L : (L == L ? 0.f : L);  // no token: 0; NaN stays NaN
+            *reinterpret_cast<float4*>(&part[warp][4 * lane]) = make_float4(O.x * inv_l, O.y * inv_l, O.z * inv_l, O.w * inv_l);
         }
         __syncthreads();
-        for (int i = tid; i < G * D; i += 256) {
-            const int jj = i / D, c = i % D;
-            float M = D4_NEG, L = 0.f, O = 0.f;
-            for (int x = 0; x < P; ++x) M = fmaxf(M, pm[x][jj]);
-            for (int x = 0; x < P; ++x) {
-                const float f = d4_ex2(pm[x][jj] - M);
-                L = fmaf(pl[x][jj], f, L);
-                O = fmaf(part[x * G + jj][c], f, O);
+        if (tid < G * 32) {
+            float4 x = *reinterpret_cast<const float4*>(&part[tid >> 5][4 * lane]);
+            for (int y = 1; y < P; ++y) {
+                const float4 z = *reinterpret_cast<const float4*>(&part[y * G + (tid >> 5)][4 * lane]);
+                x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
             }
-            o[jj][c] = O * (L > 0.f ? 1.f / L : (L == L ? 0.f : L));  // no token: 0; NaN stays NaN
+            *reinterpret_cast<float4*>(&o[tid >> 5][4 * lane]) = x;
         }
         __syncthreads();
         // out_i = sum_c o_c R_v[i][c]: a lane forms four columns of each of its warp's rows,
@@ -1033,7 +1070,7 @@ __global__ void __launch_bounds__(256) finish_int4_kernel(const __grid_constant_
         const int ctx = max(0, min(__ldg(a.context_lens + b), a.max_pages * PAGE));
         griddep_wait();
         griddep_launch_dependents();
-        if (chunk * 256 >= ctx) return;
+        if (chunk * 512 >= ctx) return;
         // the unit's maximum and 1 / sum of each head
         const int2 info = __ldcg(a.info + u);
         if (warp < G) {
@@ -1060,7 +1097,7 @@ __global__ void __launch_bounds__(256) finish_int4_kernel(const __grid_constant_
         __syncthreads();
         float* w = a.weights + (int64_t)u * a.wstride;
         const float* lg = a.logits + u * a.max_pages * PAGE * G;
-        for (int64_t s = (int64_t)chunk * 256 + tid; s < ctx; s += (int64_t)a.chunks * 256) {
+        for (int64_t s = (int64_t)chunk * 512 + tid; s < ctx; s += (int64_t)a.chunks * 512) {
             float p = 0.f;
             auto add = [&](float z, int j) {
                 // (a dropped token's logit is -inf: no weight, whatever the maximum)
@@ -1195,10 +1232,10 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const int nsm = kvq_device_sm_count();
     const int64_t units = (int64_t)B * H_kv;
     if (units > (1 << 24)) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: B * H_kv above 2^24", fn);
-    // 1: runs of sequences that give about one CTA per SM
-    const int per = (int)((units + nsm - 1) / nsm);
+    // 1: one sequence a CTA, up to eight CTAs per SM
+    const int per = (int)((4 * units + 8 * nsm - 1) / (8 * nsm));
     kvq_status st = kvq_check_cuda(launch_pdl(G <= 4 ? rotate_int4_kernel<1> : rotate_int4_kernel<2>,
-                                              dim3(H_kv, (B + per - 1) / per), dim3(256), 0, cs, a, per),
+                                              dim3(4 * H_kv, (B + per - 1) / per), dim3(128), 0, cs, a, per),
                                    "kvq_decode_attn_int4 rotate launch");
     if (st != KVQ_OK) return st;
     // 2
@@ -1213,18 +1250,18 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
                         "kvq_decode_attn_int4 launch");
     if (st != KVQ_OK) return st;
     // 3: few units are finished by four CTAs each (a quarter of R_v each), and
-    // about four CTAs per SM share the weights
+    // about two CTAs per SM share the weights
     const bool few = units * 4 <= nsm;
     a.n_finish = (int)(units * (few ? 4 : 1));
     a.chunks = 0;
     if (with_weights) {
-        const int64_t blocks = ((int64_t)max_pages * PAGE + 255) / 256, most = (4 * nsm + units - 1) / units;
+        const int64_t blocks = ((int64_t)max_pages * PAGE + 511) / 512, most = (2 * nsm + units - 1) / units;
         a.chunks = (int)(blocks < most ? blocks : most);
     }
     const dim3 grid((unsigned)(a.n_finish + units * a.chunks));
     st = kvq_check_cuda(launch_pdl(with_weights ? (few ? finish_int4_kernel<4, true> : finish_int4_kernel<1, true>)
                                                 : (few ? finish_int4_kernel<4, false> : finish_int4_kernel<1, false>),
-                                   grid, dim3(256), 0, cs, a),
+                                   grid, dim3(512), 0, cs, a),
                         "kvq_decode_attn_int4 finish launch");
     return st;
 }
