@@ -44,21 +44,24 @@
 // pages of all (sequence, KV head) units are laid end to end and every CTA takes
 // an equal share, so a ragged batch or a short context in a long table stays
 // balanced.
+#include <cstddef>
 #include <mutex>
 
 #include "int4_common.cuh"
 
 namespace kvq {
 
-// NW warps of a CTA, U pages per unit of a warp's ring (one mbarrier phase, one
-// refill), UNITS units in the ring.  Up to four heads fit 128 registers, four warps
-// per scheduler; eight take 168 and three.
+// NW warps of a CTA (three per scheduler at 168 registers), U pages per unit of a
+// warp's ring (one mbarrier phase, one refill), UNITS units in the ring.  At 128K,
+// 32 q / 8 KV heads, batch 1: 12 warps with units of two pages 41.3 us, of one page
+// 48.4 us, 16 warps (128 registers, one page) 49.4 us, 8 warps with units of three
+// 41.0 us and of two 47.2 us.
 template <int NT>
 struct D4Cfg {
-    static constexpr int NW = NT == 1 ? 12 : 12, U = NT == 1 ? 2 : 2, UNITS = NT == 1 ? 3 : 3;
+    static constexpr int NW = 12, U = 2, UNITS = 3;
 };
 constexpr int D4_MAX_SPLITS = 254;
-constexpr int D4_MIN_PAGES = 16;   // pages a CTA takes at least when the split is automatic
+constexpr int D4_MIN_PAGES = 24;   // pages per CTA below which an automatic split goes no further: a unit a warp
 constexpr int D4_SEG_PAGES = 40;   // what starting another unit costs a CTA, in pages streamed
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
 
@@ -86,6 +89,12 @@ __device__ __forceinline__ void d4_mma0(float (&d)[4], const uint32_t (&a)[4], u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Two values' high fp16 parts, or what those leave of them.
+__device__ __forceinline__ uint32_t d4_part(float v0, float v1, bool low) {
+    const float h0 = __half2float(__float2half_rn(v0)), h1 = __half2float(__float2half_rn(v1));
+    return low ? pack_half2(v0 - h0, v1 - h1) : pack_half2(h0, h1);
 }
 
 // The rotated queries of a unit as the stream kernel takes them: QK operands of
@@ -198,14 +207,10 @@ __global__ void __launch_bounds__(128, 8) rotate_int4_kernel(const __grid_consta
         __syncthreads();
         // K step 2 g + hs: b0 = channels 32 g + 8 t + 2 hs and + 4 (codes in the low nibble),
         // b1 = the channels after those (the next nibble: 16 times the code)
-        auto parts = [](float v0, float v1, bool low) {
-            const float h0 = __half2float(__float2half_rn(v0)), h1 = __half2float(__float2half_rn(v1));
-            return low ? pack_half2(v0 - h0, v1 - h1) : pack_half2(h0, h1);
-        };
         auto q_frag = [&](int j, int e, bool low) {
             const int c0 = 8 * t + 2 * warp + e;
             const float f = sigma[j] * (e ? 0.0625f : 1.f);
-            return parts(qs[j][c0] * f, qs[j][c0 + 4] * f, low);
+            return d4_part(qs[j][c0] * f, qs[j][c0 + 4] * f, low);
         };
         D4Query<NT>& out = static_cast<D4Query<NT>*>(a.query)[(size_t)b * a.H_kv + h];
         if (warp < 2) {
@@ -235,6 +240,29 @@ __global__ void __launch_bounds__(128, 8) rotate_int4_kernel(const __grid_consta
         }
         __syncthreads();  // sigma, qs and gsum are read above; the next round writes them
     }
+}
+
+// out_i = sum_c x_c R[i][c] for a warp's RW rows of R_v: a lane forms four columns
+// of each, and a reduce-scatter leaves row lane % RW in each lane.
+template <int RW>
+__device__ __forceinline__ void d4_rotate_rows(float4 x, const float4 (&rr)[RW], int lane, __nv_bfloat16* out) {
+    float v[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        v[i] = fmaf(x.x, rr[i].x, fmaf(x.y, rr[i].y, fmaf(x.z, rr[i].z, x.w * rr[i].w)));
+#pragma unroll
+        for (int off = 16; off >= RW; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    }
+#pragma unroll
+    for (int off = RW / 2; off >= 1; off >>= 1) {
+        const bool upper = lane & off;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float send = upper ? v[i] : v[i + off], hold = upper ? v[i + off] : v[i];
+            v[i] = hold + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    }
+    if (lane < RW) out[lane] = __float2bfloat16_rn(v[0]);
 }
 
 // ------------------------------------------------------------------ 2: stream
@@ -286,13 +314,26 @@ struct __align__(128) D4Smem {
     int64_t scan[NW];
     int scan_max[NW], scan_n[NW];
     int64_t base0;
-    int b0;
+    int b0, is_last;
+    // one sequence: the query's rotation and the unit's end, in this kernel
+    __align__(16) float qin[4 * NT][D];  // (these three are read as float4)
+    __align__(16) float red[3][4 * NT][D];
+    __align__(16) float qs[4 * NT][D];
+    float gsum[4 * NT][NGROUP], sigma[4 * NT];
 };
+static_assert(offsetof(D4Smem<1>, qin) % 16 == 0 && offsetof(D4Smem<1>, red) % 16 == 0 && offsetof(D4Smem<1>, qs) % 16 == 0 &&
+                  offsetof(D4Smem<2>, qin) % 16 == 0 && offsetof(D4Smem<2>, red) % 16 == 0 && offsetof(D4Smem<2>, qs) % 16 == 0 &&
+                  offsetof(D4Smem<1>, query) % 16 == 0 && offsetof(D4Smem<2>, query) % 16 == 0 && offsetof(D4Smem<1>, bar) % 8 == 0 &&
+                  offsetof(D4Smem<2>, bar) % 8 == 0,
+              "wide accesses to shared memory are aligned");
 static_assert(sizeof(D4Smem<1>) <= 227 * 1024 && sizeof(D4Smem<2>) <= 227 * 1024, "decode shared memory above 227 KB");
 static_assert(4 * D * 4 <= D4Cfg<1>::U * INT4_TILE && 8 * D * 4 <= D4Cfg<2>::U * INT4_TILE, "a warp's partial fits one ring group");
 
-// NT = 1: up to four query heads per KV head, NT = 2: up to eight.
-template <int NT, bool WTS>
+// NT = 1: up to four query heads per KV head, NT = 2: up to eight.  ONE: the form
+// for one sequence, whole in this kernel: every CTA works on one KV head, rotates
+// its queries itself (before its first copies are out, so the rotation does not wait
+// behind them) and the last CTA of a head finishes it.
+template <int NT, bool WTS, bool ONE>
 __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(const __grid_constant__ D4Args a) {
     constexpr int NW = D4Cfg<NT>::NW, U = D4Cfg<NT>::U, UNITS = D4Cfg<NT>::UNITS;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -309,14 +350,31 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         }
         fence_mbar_init();
     }
+    __syncwarp();  // (a warp's ring is its own)
 
     // ---- the split: pages of all sequences (a thread sums a run of them), the
     // CTAs that take part, and where this one's share begins.  Context lengths,
     // block table and cache are read before the dependency wait: the rotate kernel
     // let this one start only after its own wait, when everything before it was done.
-    int64_t V, g0;
-    int Ceff, share, extra = 0;  // extra: pages without work after each unit's, for the cost of starting it
-    {
+    int64_t V = 0, g0 = 0;
+    int Ceff = 0, share = 0, extra = 0;  // extra: pages without work after each unit's, for the cost of starting it
+    D4Walk cs;  // what this warp consumes
+    if constexpr (ONE) {
+        griddep_wait();  // (no rotate kernel ran before)
+        cs.b = cs.left = 0;
+        cs.np = d4_pages(a, 0);
+        if (cs.np == 0) {
+            for (int i = cta * NW * 32 + tid; i < a.H_q * D; i += gridDim.x * NW * 32) a.out[i] = __float2bfloat16_rn(0.f);
+            return;
+        }
+        // a whole number of CTAs per head
+        Ceff = min((int)gridDim.x / a.H_kv, (cs.np + D4_MIN_PAGES - 1) / D4_MIN_PAGES);  // per head
+        cs.h = cta / Ceff;
+        if (cs.h >= a.H_kv) return;
+        const int part = cta % Ceff;
+        cs.pa = (int)((int64_t)part * cs.np / Ceff);
+        cs.pb = cs.end = (int)((int64_t)(part + 1) * cs.np / Ceff);
+    } else {
         const int per = (a.B + (NW * 32) - 1) / (NW * 32), s0 = min(a.B, tid * per), s1 = min(a.B, s0 + per);
         int64_t own = 0;
         int mx = 0, own_ne = 0;
@@ -400,8 +458,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         }
         __syncthreads();
     }
-    D4Walk cs;  // what this warp consumes
-    {
+    if constexpr (!ONE) {
         cs.b = sm.b0;
         cs.np = d4_pages(a, cs.b);
         const int64_t in = g0 - sm.base0;
@@ -413,6 +470,22 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 return;
             }
             cs.next(a, extra);
+        }
+    }
+
+    // ONE: the head's R_k and queries are asked for before the pages
+    constexpr int MAXG = 4 * NT, ROWS = ONE ? 44 : 1;  // 44 + 44 + 40 rows, four at a time
+    float rr[ROWS], qv[ONE ? (MAXG * D + NW * 32 - 1) / (NW * 32) : 1];
+    if constexpr (ONE) {
+        const float* R = a.Rk + (size_t)cs.h * D * D + (tid & (D - 1));
+        const int i0 = (tid >> 7) * ROWS;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) rr[i] = i0 + i < D ? __ldg(R + (size_t)(i0 + i) * D) : 0.f;
+        const __nv_bfloat16* qb = a.q + (size_t)cs.h * G * D;
+#pragma unroll
+        for (int i = 0; i < (MAXG * D + NW * 32 - 1) / (NW * 32); ++i) {
+            const int x = tid + i * NW * 32;
+            qv[i] = x < G * D ? __bfloat162float(qb[x]) : 0.f;
         }
     }
 
@@ -483,14 +556,16 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     };
     if (built > 0) issue_next();
 
-    griddep_wait();  // the rotated queries are there
-    griddep_launch_dependents();
+    if constexpr (!ONE) {
+        griddep_wait();  // the rotated queries are there
+        griddep_launch_dependents();
+    }
     auto fetch_query = [&](const D4Walk& w, int buf) {  // one thread
         mbar_arrive_expect_tx(&sm.qbar[buf], sizeof(D4Query<NT>));
         bulk_g2s(&sm.query[buf], static_cast<const D4Query<NT>*>(a.query) + ((size_t)w.b * a.H_kv + w.h), sizeof(D4Query<NT>),
                  &sm.qbar[buf]);
     };
-    if (tid == 0) {
+    if (!ONE && tid == 0) {
         fetch_query(cs, 0);
         if (cs.left > 0) {
             D4Walk w = cs;
@@ -501,6 +576,73 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     // (the rest of the ring after the queries, which would queue behind it)
 #pragma unroll 1
     while (issued < min(built, UNITS)) issue_next();
+    if constexpr (ONE) {
+        // q' = q R_k * scale * log2(e), as the rotate kernel has it, into query[0]
+#pragma unroll
+        for (int i = 0; i < (MAXG * D + NW * 32 - 1) / (NW * 32); ++i) {
+            const int x = tid + i * NW * 32;
+            if (x < MAXG * D) sm.qin[x / D][x % D] = qv[i];
+        }
+        __syncthreads();
+        const int c = tid & (D - 1), part = tid >> 7, i0 = part * ROWS;
+        float acc[MAXG];
+#pragma unroll
+        for (int j = 0; j < MAXG; ++j) acc[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < ROWS; i += 4)
+            if (i0 + i < D) {
+#pragma unroll
+                for (int j = 0; j < MAXG; ++j) {
+                    const float4 x = *reinterpret_cast<const float4*>(&sm.qin[j][i0 + i]);
+                    acc[j] = fmaf(x.x, rr[i], fmaf(x.y, rr[i + 1], fmaf(x.z, rr[i + 2], fmaf(x.w, rr[i + 3], acc[j]))));
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < MAXG; ++j) sm.red[part][j][c] = acc[j];
+        if (warp < MAXG) {
+            const float4 x = *reinterpret_cast<const float4*>(&sm.qin[warp][4 * lane]);
+            float n2 = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w)));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+            if (lane == 0) sm.sigma[warp] = d4_prescale(sqrtf(n2) * fabsf(a.scale_log2) * 8.f);
+        }
+        __syncthreads();
+        for (int x = warp; x < MAXG * NGROUP; x += NW) {
+            const int j = x / NGROUP, g = x % NGROUP, ch = 32 * g + lane;
+            float y = ((sm.red[0][j][ch] + sm.red[1][j][ch]) + sm.red[2][j][ch]) * a.scale_log2;
+            sm.qs[j][ch] = y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            if (lane == 0) sm.gsum[j][g] = y;
+        }
+        __syncthreads();
+        D4Query<NT>& out = sm.query[0];
+        auto q_frag = [&](int j, int e, bool low) {
+            const int c0 = 32 * (warp >> 1) + 8 * t + 2 * (warp & 1) + e;
+            const float f = sm.sigma[j] * (e ? 0.0625f : 1.f);
+            return d4_part(sm.qs[j][c0] * f, sm.qs[j][c0 + 4] * f, low);
+        };
+        auto s_frag = [&](int j, bool low) {
+            const float f = sm.sigma[j] * 0.125f;
+            return t >= 2 ? 0u : d4_part(sm.gsum[j][2 * t] * f, sm.gsum[j][2 * t + 1] * f, low);
+        };
+        if (warp < 8) {
+            if constexpr (NT == 1)
+                *reinterpret_cast<uint2*>(out.bq[warp][lane]) = make_uint2(q_frag(r >> 1, 0, r & 1), q_frag(r >> 1, 1, r & 1));
+            else
+                *reinterpret_cast<uint4*>(out.bq[warp][lane]) =
+                    make_uint4(q_frag(r, 0, false), q_frag(r, 1, false), q_frag(r, 0, true), q_frag(r, 1, true));
+        } else if (warp == 8) {
+            if constexpr (NT == 1)
+                out.bs[lane][0] = s_frag(r >> 1, r & 1);
+            else
+                *reinterpret_cast<uint2*>(out.bs[lane]) = make_uint2(s_frag(r, false), s_frag(r, true));
+        } else if (warp == 9 && lane < MAXG) {
+            out.inv_q[lane] = 16777216.f / sm.sigma[lane];
+            out.inv_s[lane] = 8.f / sm.sigma[lane];
+        }
+        __syncthreads();
+    }
 
     bool dead = false;  // a wait of this warp ran out: it takes part without data
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -545,7 +687,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             lsum[e] = 0.f;
         }
         if (n_units > 0) {
-            wait(&sm.qbar[buf], (s >> 1) & 1);
+            if constexpr (!ONE) wait(&sm.qbar[buf], (s >> 1) & 1);
             const D4Query<NT>& qf = sm.query[buf];
             uint32_t bq[NT == 1 ? 8 : 1][2], bs[2];
             float inv_q[NT], inv_s[NT];  // NT == 1: head t; NT == 2: heads 2 t, 2 t + 1
@@ -856,6 +998,114 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             }
         }
         if (lane == 0) sm.part_at[buf][warp] = has ? at : -1;
+        if constexpr (ONE) {
+            // ---- the whole CTA merges its warps; with more CTAs on the head it publishes, and
+            // the last one merges those; then normalise, rotate by R_v^T, write
+            __syncthreads();
+            griddep_launch_dependents();
+            const size_t step = (size_t)G * PART_STRIDE;
+            float* slot = a.partials + (u + cta) * step;
+            for (int i = tid; i < G * (D / 4); i += NW * 32) {
+                const int j = i / (D / 4), c4 = 4 * (i % (D / 4));
+                float M = D4_NEG, L = 0.f;
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) M = fmaxf(M, sm.m_part[0][w][j]);
+#pragma unroll 4
+                for (int w = 0; w < NW; ++w) {
+                    const int at_w = sm.part_at[0][w];
+                    const float f = d4_ex2(sm.m_part[0][w][j] - M);
+                    if (at_w >= 0) {
+                        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w][U * at_w]) + j * D + c4);
+                        L = fmaf(sm.l_part[0][w][j], f, L);
+                        O.x = fmaf(x.x, f, O.x);
+                        O.y = fmaf(x.y, f, O.y);
+                        O.z = fmaf(x.z, f, O.z);
+                        O.w = fmaf(x.w, f, O.w);
+                    }
+                }
+                if (Ceff == 1) {
+                    const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+                    O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+                    *reinterpret_cast<float4*>(&sm.qs[j][c4]) = O;
+                } else {
+                    *reinterpret_cast<float4*>(slot + (size_t)j * PART_STRIDE + 4 + c4) = O;
+                }
+                if (c4 == 0) *reinterpret_cast<float2*>(slot + (size_t)j * PART_STRIDE) = make_float2(M, L);
+            }
+            if (WTS && tid == 0 && cta == cs.h * Ceff) a.info[u] = make_int2(cta, Ceff);
+            __syncthreads();
+            if (Ceff > 1) {
+                int32_t* ticket = reinterpret_cast<int32_t*>(a.ws + WS_HEADER) + u;
+                if (tid == 0) sm.is_last = atomic_add_acq_rel_gpu(ticket, 1) == Ceff - 1;
+                __syncthreads();
+                if (!sm.is_last) break;
+                if (tid == 0) *ticket = 0;
+                // warp (part, head): partials part, part + P, ..., four channels a lane
+                const int P = NW / G, j = warp % G, p = warp / G;
+                const float* ps = a.partials + (u + (size_t)cs.h * Ceff) * step + (size_t)j * PART_STRIDE;
+                if (p < P) {
+                    constexpr int CH = 8;
+                    float M = D4_NEG, L = 0.f;
+                    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int s0 = p; s0 < Ceff; s0 += P * CH) {
+                        float2 ml[CH];
+                        float4 ov[CH];
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) {
+                            const float* q = ps + (size_t)(s0 + P * x) * step;
+                            const bool in_range = s0 + P * x < Ceff;
+                            ml[x] = in_range ? __ldcg(reinterpret_cast<const float2*>(q)) : make_float2(D4_NEG, 0.f);
+                            ov[x] = in_range ? __ldcg(reinterpret_cast<const float4*>(q + 4 + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        float top = M;
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) top = fmaxf(top, ml[x].x);
+                        const float c = d4_ex2(M - top);
+                        L *= c;
+                        O = make_float4(O.x * c, O.y * c, O.z * c, O.w * c);
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) {
+                            const float f = d4_ex2(ml[x].x - top);
+                            L = fmaf(ml[x].y, f, L);
+                            O.x = fmaf(ov[x].x, f, O.x);
+                            O.y = fmaf(ov[x].y, f, O.y);
+                            O.z = fmaf(ov[x].z, f, O.z);
+                            O.w = fmaf(ov[x].w, f, O.w);
+                        }
+                        M = top;
+                    }
+                    *reinterpret_cast<float4*>(&(&sm.red[0][0][0])[warp * D + 4 * lane]) = O;
+                    if (lane == 0) {
+                        sm.m_part[0][p][j] = M;
+                        sm.l_part[0][p][j] = L;
+                    }
+                }
+                __syncthreads();
+                for (int i = tid; i < G * D; i += NW * 32) {
+                    const int jj = i / D, c = i % D;
+                    float M = D4_NEG, L = 0.f, O = 0.f;
+                    for (int x = 0; x < P; ++x) M = fmaxf(M, sm.m_part[0][x][jj]);
+                    for (int x = 0; x < P; ++x) {
+                        const float f = d4_ex2(sm.m_part[0][x][jj] - M);
+                        L = fmaf(sm.l_part[0][x][jj], f, L);
+                        O = fmaf((&sm.red[0][0][0])[(x * G + jj) * D + c], f, O);
+                    }
+                    sm.qs[jj][c] = O * (L > 0.f ? 1.f / L : (L == L ? 0.f : L));
+                }
+                __syncthreads();
+            }
+            if (warp < 8) {
+                const float* R = a.Rv + ((size_t)cs.h * D + 16 * warp) * D + 4 * lane;
+                float4 rv[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) rv[i] = __ldg(reinterpret_cast<const float4*>(R + (size_t)i * D));
+                __nv_bfloat16* o = a.out + (size_t)cs.h * G * D + 16 * warp;
+#pragma unroll 1
+                for (int jj = 0; jj < G; ++jj) d4_rotate_rows<16>(*reinterpret_cast<const float4*>(&sm.qs[jj][4 * lane]), rv, lane, o + (size_t)jj * D);
+            }
+            break;
+        }
         end2 = end1;
         end1 = done;
         __syncwarp();
@@ -982,11 +1232,11 @@ __global__ void __launch_bounds__(512) finish_int4_kernel(const __grid_constant_
             const float* ps = a.partials + (u + info.x) * (size_t)(G * PART_STRIDE) + (size_t)j * PART_STRIDE;
             const size_t step = (size_t)G * PART_STRIDE;
             // every warp of a head finds its M and L, a partial per lane; its own outputs are
-            // partials p, p + P, ... (32 partials at a time, four of its own in flight)
+            // partials p, p + P, ... (32 partials at a time, eight of its own in flight)
             float M = D4_NEG, L = 0.f;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int base = 0; base < info.y; base += 32) {
-                constexpr int CH = 4;
+                constexpr int CH = 8;
                 float4 ov[CH];
                 const int end = min(info.y, base + 32);
                 const float2 ml = base + lane < end ? __ldcg(reinterpret_cast<const float2*>(ps + (base + lane) * step))
@@ -1040,28 +1290,9 @@ __global__ void __launch_bounds__(512) finish_int4_kernel(const __grid_constant_
             *reinterpret_cast<float4*>(&o[tid >> 5][4 * lane]) = x;
         }
         __syncthreads();
-        // out_i = sum_c o_c R_v[i][c]: a lane forms four columns of each of its warp's rows,
-        // a reduce-scatter leaves row lane % RW in each lane
-#pragma unroll 2
+#pragma unroll 1
         for (int jj = 0; jj < G; ++jj) {
-            const float4 x = *reinterpret_cast<const float4*>(&o[jj][4 * lane]);
-            float v[RW];
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                v[i] = fmaf(x.x, rr[i].x, fmaf(x.y, rr[i].y, fmaf(x.z, rr[i].z, x.w * rr[i].w)));
-#pragma unroll
-                for (int off = 16; off >= RW; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-            }
-#pragma unroll
-            for (int off = RW / 2; off >= 1; off >>= 1) {
-                const bool upper = lane & off;
-#pragma unroll
-                for (int i = 0; i < off; ++i) {
-                    const float send = upper ? v[i] : v[i + off], hold = upper ? v[i + off] : v[i];
-                    v[i] = hold + __shfl_xor_sync(0xffffffffu, send, off);
-                }
-            }
-            if (lane < RW) out[(size_t)jj * D + lane] = __float2bfloat16_rn(v[0]);
+            d4_rotate_rows<RW>(*reinterpret_cast<const float4*>(&o[jj][4 * lane]), rr, lane, out + (size_t)jj * D);
         }
     } else {
         const int x = blockIdx.x - a.n_finish;
@@ -1135,7 +1366,7 @@ struct D4Layout {
 static D4Layout d4_layout(int B, int H_q, int H_kv, int max_pages, int64_t C, bool weights) {
     const size_t units = (size_t)B * H_kv, G = (size_t)(H_q / H_kv);
     D4Layout l;
-    l.query = WS_HEADER;
+    l.query = WS_HEADER + tickets_bytes(B, H_kv);
     l.info = align_up(l.query + units * (G <= 4 ? sizeof(D4Query<1>) : sizeof(D4Query<2>)), 256);
     l.partials = align_up(l.info + units * sizeof(int2), 256);
     l.logits = align_up(l.partials + (units + (size_t)C) * G * PART_STRIDE * 4, 256);  // a slot per (unit + CTA)
@@ -1155,7 +1386,7 @@ extern "C" size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pag
 // first call on each device only.
 static kvq_status d4_smem_once(const void* fn, int bytes, int which) {
     static std::mutex mu;
-    static bool done[64][4] = {};
+    static bool done[64][8] = {};
     int dev = 0;
     kvq_status st = kvq_check_cuda(cudaGetDevice(&dev), "kvq_decode_attn_int4: cudaGetDevice");
     if (st != KVQ_OK) return st;
@@ -1232,27 +1463,34 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const int nsm = kvq_device_sm_count();
     const int64_t units = (int64_t)B * H_kv;
     if (units > (1 << 24)) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: B * H_kv above 2^24", fn);
-    // 1: one sequence a CTA, up to eight CTAs per SM
-    const int per = (int)((4 * units + 8 * nsm - 1) / (8 * nsm));
-    kvq_status st = kvq_check_cuda(launch_pdl(G <= 4 ? rotate_int4_kernel<1> : rotate_int4_kernel<2>,
-                                              dim3(4 * H_kv, (B + per - 1) / per), dim3(128), 0, cs, a, per),
-                                   "kvq_decode_attn_int4 rotate launch");
-    if (st != KVQ_OK) return st;
+    // one sequence and a few heads: one kernel (the weights form: and the weights)
+    const bool one = num_splits == 0 && B == 1 && 4 * H_kv <= nsm;
+    kvq_status st;
+    if (!one) {
+        // 1: one sequence a CTA, up to eight CTAs per SM
+        const int per = (int)((4 * units + 8 * nsm - 1) / (8 * nsm));
+        st = kvq_check_cuda(launch_pdl(G <= 4 ? rotate_int4_kernel<1> : rotate_int4_kernel<2>,
+                                       dim3(4 * H_kv, (B + per - 1) / per), dim3(128), 0, cs, a, per),
+                            "kvq_decode_attn_int4 rotate launch");
+        if (st != KVQ_OK) return st;
+    }
     // 2
-    using Kern = decltype(&decode_int4_kernel<1, false>);
-    static const Kern kerns[4] = {decode_int4_kernel<1, false>, decode_int4_kernel<1, true>, decode_int4_kernel<2, false>,
-                                  decode_int4_kernel<2, true>};
-    const int which = (G <= 4 ? 0 : 2) + (with_weights ? 1 : 0);
+    using Kern = decltype(&decode_int4_kernel<1, false, false>);
+    static const Kern kerns[8] = {decode_int4_kernel<1, false, false>, decode_int4_kernel<1, true, false>,
+                                  decode_int4_kernel<2, false, false>, decode_int4_kernel<2, true, false>,
+                                  decode_int4_kernel<1, false, true>,  decode_int4_kernel<1, true, true>,
+                                  decode_int4_kernel<2, false, true>,  decode_int4_kernel<2, true, true>};
+    const int which = (G <= 4 ? 0 : 2) + (with_weights ? 1 : 0) + (one ? 4 : 0);
     const size_t smem = G <= 4 ? sizeof(D4Smem<1>) : sizeof(D4Smem<2>);
     st = d4_smem_once((const void*)kerns[which], (int)smem, which);
     if (st != KVQ_OK) return st;
     st = kvq_check_cuda(launch_pdl(kerns[which], dim3((unsigned)C), dim3(32 * (G <= 4 ? D4Cfg<1>::NW : D4Cfg<2>::NW)), smem, cs, a),
                         "kvq_decode_attn_int4 launch");
-    if (st != KVQ_OK) return st;
+    if (st != KVQ_OK || (one && !with_weights)) return st;
     // 3: few units are finished by four CTAs each (a quarter of R_v each), and
     // about two CTAs per SM share the weights
     const bool few = units * 4 <= nsm;
-    a.n_finish = (int)(units * (few ? 4 : 1));
+    a.n_finish = one ? 0 : (int)(units * (few ? 4 : 1));
     a.chunks = 0;
     if (with_weights) {
         const int64_t blocks = ((int64_t)max_pages * PAGE + 511) / 512, most = (2 * nsm + units - 1) / units;
