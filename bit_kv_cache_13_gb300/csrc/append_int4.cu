@@ -2,111 +2,540 @@
 //
 // z = (k - mu) R_k, w = v R_v, then 16 levels per group of 32 rotated channels
 // with an fp16 scale and min.  Codes, scales and mins are those of the exact
-// rotated vectors, whichever kernel writes them.
+// rotated vectors, whichever kernel writes them: each kernel forms the rotated
+// values to within a bound, and where a rounding or a threshold lies within that
+// bound of a value (a few groups in a hundred) it forms the value exactly.
+#include <mutex>
+
 #include "int4_common.cuh"
 
 namespace kvq {
 
-// One CTA of 256 threads per (token, KV head): thread j < 128 forms rotated
-// key channel j, thread 128 + j value channel j, as fp64 dot products of the
-// exact inputs (k - mu of a bf16 and an fp32 is exact in fp64).  Warp w is
-// group w % 4 of side w / 4, so a group's range is a warp reduction.
-__global__ void __launch_bounds__(256)
+// Writes code word w (8 codes: channels 32 g + 8 t + i of nibble i) of one token.
+__device__ __forceinline__ void store_word(uint8_t* tile, int side, int s, int g, int t, uint32_t w) {
+    if (!side) {
+        *reinterpret_cast<uint32_t*>(tile + O4_KC + 64 * s + 16 * t + 4 * g) = w;
+    } else {
+        uint8_t* p = tile + O4_VC + 128 * (s >> 1) + 32 * t + 4 * g + 2 * (s & 1);
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)w;
+        *reinterpret_cast<uint16_t*>(p + 16) = (uint16_t)(w >> 16);
+    }
+}
+
+__device__ __forceinline__ void store_meta(uint8_t* tile, int side, int s, int g, __half sh, __half mh) {
+    if (!side) {
+        *reinterpret_cast<__half*>(tile + O4_KM + 16 * s + 2 * g) = sh;
+        *reinterpret_cast<__half*>(tile + O4_KM + 16 * s + 8 + 2 * g) = mh;
+    } else {
+        *reinterpret_cast<__half*>(tile + O4_VS + int4_vmeta_off(s, g)) = sh;
+        *reinterpret_cast<__half*>(tile + O4_VM + int4_vmeta_off(s, g)) = mh;
+    }
+}
+
+// ------------------------------------------------------------ a few tokens
+//
+// One CTA of 512 threads per (token, KV head, side): thread (channel, quarter)
+// sums 32 products in an unevaluated pair of fp32 values, so the rotated values are
+// exact to about 46 bits and no second look is taken.  Bound by its chain of
+// latencies: one row of R_k per thread and quarter in flight.
+
+__global__ void __launch_bounds__(512)
 append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, int n_tok, int H_kv,
                    const int32_t* __restrict__ slot_mapping, const float* __restrict__ mu,
                    const float* __restrict__ Rk, const float* __restrict__ Rv, uint8_t* __restrict__ cache,
                    int64_t num_pages, int32_t* __restrict__ err_count, float clip) {
-    griddep_launch_dependents();
+    __shared__ float xs[D], xl[D], n2s[4];
+    __shared__ Dd part[4][D];
+    const int t = blockIdx.x, h = blockIdx.y, side = blockIdx.z, tid = threadIdx.x;
+    const int j = tid & (D - 1), quarter = tid >> 7, lane = tid & 31, g = (tid >> 5) & 3;
+    const float* R = (side ? Rv : Rk) + (size_t)h * D * D + (size_t)32 * quarter * D + j;
+    prefetch_l2(R - j + (size_t)(j >> 2) * D + 32 * (j & 3));  // the quarter's 32 rows, four lines each
     griddep_wait();
-    __shared__ double xs[2][D];
-    const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-    const int side = tid >> 7, j = tid & (D - 1), lane = tid & 31, g = (tid >> 5) & 3;
+    griddep_launch_dependents();
     const int slot = __ldg(slot_mapping + t);
-    if (slot == -1) return;
+    float rr[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) rr[i] = __ldg(R + (size_t)i * D);
     if (slot < 0 || (int64_t)slot >= num_pages * PAGE) {
-        if (tid == 0 && h == 0 && err_count) atomicAdd(err_count, 1);
+        if (slot != -1 && tid == 0 && h == 0 && side == 0 && err_count) atomicAdd(err_count, 1);
         return;
     }
-    const size_t row = ((size_t)t * H_kv + h) * D + j;
-    xs[side][j] = side ? (double)__bfloat162float(v[row])
-                       : (double)__bfloat162float(k[row]) - (double)__ldg(mu + (size_t)h * D + j);
+    if (quarter == 0) {
+        const size_t row = ((size_t)t * H_kv + h) * D + j;
+        const float x = __bfloat162float(side ? v[row] : k[row]);
+        const float m = side ? 0.f : __ldg(mu + (size_t)h * D + j);
+        float hi, lo;
+        two_sum(x, -m, hi, lo);  // (not finite: hi is, too, and lo does not matter)
+        xs[j] = hi;
+        xl[j] = isfinite(hi) ? lo : 0.f;
+        float n2 = fmaf(x, x, m * m);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+        if (lane == 0) n2s[g] = n2;
+    }
     __syncthreads();
-    const float* R = (side ? Rv : Rk) + (size_t)h * D * D + j;
-    double z = 0.0;
-#pragma unroll 8
-    for (int i = 0; i < D; ++i) z = fma(xs[side][i], (double)__ldg(R + (size_t)i * D), z);
-    double mn = z, mx = z;
-    const bool nan = !isfinite(z);
+    const bool wild = int4_wild(n2s[0] + n2s[1] + n2s[2] + n2s[3]);  // CTA-uniform
+    double z64 = 0.0;
+    if (!wild) {
+        // four chains, so that their latencies overlap
+        Dd acc[4] = {};
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dd_fma(acc[e], xs[32 * quarter + i + e], xl[32 * quarter + i + e], rr[i + e]);
+        dd_add(acc[0], acc[1]);
+        dd_add(acc[2], acc[3]);
+        dd_add(acc[0], acc[2]);
+        part[quarter][j] = acc[0];
+    }
+    __syncthreads();
+    if (quarter) return;
+    float z, eps = 0.f;
+    if (!wild) {
+        Dd a = part[0][j], b = part[2][j];
+        dd_add(a, part[1][j]);
+        dd_add(b, part[3][j]);
+        dd_add(a, b);
+        z64 = a.value();
+        z = __double2float_rn(z64);
+    } else {
+        const float* Rw = (side ? Rv : Rk) + (size_t)h * D * D + j;
+        for (int i = 0; i < D; ++i) z64 = fma((double)xs[i] + (double)xl[i], (double)__ldg(Rw + (size_t)i * D), z64);
+        z = (float)z64;
+    }
+    // the group's range: z within half an ulp of its exact value
+    float mn = z, mx = z;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        mn = fmin(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
-    if (__any_sync(0xffffffffu, nan)) mn = mx = CUDART_NAN;
+    eps = fmaxf(fabsf(mn), fabsf(mx)) * 0x1p-23f;
     __half sh, mh;
-    int4_params(mn, mx, (double)clip, sh, mh);
-    const int code = int4_code(z, sh, mh);
-    uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
-    const int s = slot % PAGE;
-    if (!side) {
-        // word (t = lane / 8, g): nibble lane % 8
-        uint32_t w = (uint32_t)code << (4 * (lane & 7));
-        w |= __shfl_xor_sync(0xffffffffu, w, 1);
-        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(tile + O4_KC + 64 * s + 16 * (lane >> 3) + 4 * g) = w;
-        if (lane == 0) {
-            *reinterpret_cast<__half*>(tile + O4_KM + 16 * s + 2 * g) = sh;
-            *reinterpret_cast<__half*>(tile + O4_KM + 16 * s + 8 + 2 * g) = mh;
+    if (int4_params_near(mn, mx, clip, eps, sh, mh) || wild) {  // warp-uniform
+        double lo = z64, hi = z64;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
+        if (__any_sync(0xffffffffu, !isfinite(z64))) lo = hi = CUDART_NAN;
+        int4_params(lo, hi, (double)clip, sh, mh);
+    }
+    const float s = __half2float(sh), m = __half2float(mh);
+    bool near;
+    int code = int4_code_near(z, s, s > 0.f ? 1.f / s : 0.f, m, eps, near);
+    if (near || wild) code = int4_code(z64, sh, mh);
+    // the eight codes of a word sit in eight neighbouring lanes
+    uint32_t w = (uint32_t)code << (4 * (lane & 7));
+    w |= __shfl_xor_sync(0xffffffffu, w, 1);
+    w |= __shfl_xor_sync(0xffffffffu, w, 2);
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
+    if ((lane & 7) == 0) store_word(tile, side, slot % PAGE, g, lane >> 3, w);
+    if (lane == 0) store_meta(tile, side, slot % PAGE, g, sh, mh);
+}
+
+// ------------------------------------------------------------ prefill
+//
+// The rotation on the tensor cores.  The inputs are bf16 and so exact operands; R
+// enters as three bf16 parts (its fp32 value to 2^-25), smallest first, into one
+// fp32 accumulator, and the centre is subtracted after the rotation (z = k R - mu R,
+// mu R formed once per CTA).  A warp owns one group of 32 rotated channels and keeps
+// its part of R in 192 registers; a tile is 16 tokens, whose rows all four warps
+// read.  With the columns of the product in the order channel 8 t + 2 i + e = column
+// 2 t + e of its eight columns' set i, the accumulators of a lane are the eight codes
+// of one word of the key record.
+//
+// |z - accumulated| <= PF_EPS (|k| + |mu|): the largest error seen was 2^-21.4 of the
+// norm (2^30 values), the bound leaves a factor of five.  Groups or codes that the
+// bound leaves open (about one group in twelve, two codes in ten thousand) take an
+// exact dot product by the whole warp.
+constexpr int PF_M = 16;                 // tokens of a tile
+constexpr float PF_EPS = 0x1p-19f;
+constexpr int PF_RT = D + 4, PF_A = D + 8;  // padded rows, in elements
+
+struct __align__(16) PrefillSmem {
+    float RT[D][PF_RT];                  // R transposed: RT[channel][input]
+    __nv_bfloat16 A[2][PF_M][PF_A];
+    float mu[D], c[D];                   // the centre (0 for values), and mu R
+    float n2[PF_M];                      // |x|^2 of the tile's rows
+    int slot[2][PF_M];
+    uint32_t word[PF_M][4][4];           // the tile's codes [token][t][g]
+    __half sc[PF_M][NGROUP], mn[PF_M][NGROUP];
+    double z[4][32];                     // scratch of a warp
+    float mu2;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// x = p0 + p1 + p2 + (less than 2^-25 of x), bf16 parts
+__device__ __forceinline__ float bf16_part(float& x) {
+    const float p = __bfloat162float(__float2bfloat16_rn(x));
+    x = x - p;  // exact
+    return p;
+}
+
+__global__ void __launch_bounds__(128, 2)
+append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, int n_tok, int H_kv,
+                           const int32_t* __restrict__ slot_mapping, const float* __restrict__ mu,
+                           const float* __restrict__ Rk, const float* __restrict__ Rv, uint8_t* __restrict__ cache,
+                           int64_t num_pages, int32_t* __restrict__ err_count, float clip) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    PrefillSmem& sm = *reinterpret_cast<PrefillSmem*>(smem_raw);
+    const int h = blockIdx.y, side = blockIdx.z, tid = threadIdx.x, g = tid >> 5, lane = tid & 31;
+    const int r = lane >> 2, t = lane & 3;
+    const float* R = (side ? Rv : Rk) + (size_t)h * D * D;
+    for (int l = tid; l < D * D / 32; l += 128) prefetch_l2(R + 32 * l);
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const int tiles = (n_tok + PF_M - 1) / PF_M;
+    const __nv_bfloat16* src = side ? v : k;
+    const int64_t n_slots = num_pages * PAGE;
+    auto fetch = [&](int x, int buf) {  // tile x: 256 pieces of 16 bytes, and its slots
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int p = tid + 128 * e, row = p >> 4, col = 8 * (p & 15);
+            const int64_t tok = min((int64_t)x * PF_M + row, (int64_t)n_tok - 1);  // (rows past the end repeat the last)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.A[buf][row][col])),
+                         "l"(src + ((size_t)tok * H_kv + h) * D + col)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (tid < PF_M) {
+            const int64_t tok = (int64_t)x * PF_M + tid;
+            int s = tok < n_tok ? __ldg(slot_mapping + tok) : -1;
+            if (s != -1 && (s < 0 || (int64_t)s >= n_slots)) {
+                if (h == 0 && side == 0 && err_count) atomicAdd(err_count, 1);
+                s = -1;
+            }
+            sm.slot[buf][tid] = s;
+        }
+    };
+    if ((int)blockIdx.x < tiles) fetch(blockIdx.x, 0);
+    // R transposed: thread = input row
+#pragma unroll 8
+    for (int c4 = 0; c4 < D; c4 += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(R + (size_t)tid * D + c4));
+        sm.RT[c4][tid] = x.x;
+        sm.RT[c4 + 1][tid] = x.y;
+        sm.RT[c4 + 2][tid] = x.z;
+        sm.RT[c4 + 3][tid] = x.w;
+    }
+    const float mu_own = side ? 0.f : __ldg(mu + (size_t)h * D + tid);
+    sm.mu[tid] = mu_own;
+    {
+        float m2 = mu_own * mu_own;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+        if (lane == 0) sm.z[0][g] = (double)m2;
+    }
+    __syncthreads();
+    if (tid == 0) sm.mu2 = (float)(sm.z[0][0] + sm.z[0][1] + sm.z[0][2] + sm.z[0][3]);
+    if (side == 0) {  // mu R: thread = channel
+        Dd acc[4] = {};
+#pragma unroll 4
+        for (int i = 0; i < D; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(&sm.RT[tid][i]);
+            dd_fma(acc[0], sm.mu[i], 0.f, x.x);
+            dd_fma(acc[1], sm.mu[i + 1], 0.f, x.y);
+            dd_fma(acc[2], sm.mu[i + 2], 0.f, x.z);
+            dd_fma(acc[3], sm.mu[i + 3], 0.f, x.w);
+        }
+        dd_add(acc[0], acc[1]);
+        dd_add(acc[2], acc[3]);
+        dd_add(acc[0], acc[2]);
+        sm.c[tid] = acc[0].hi + acc[0].lo;
     } else {
-        // half s % 2 of the word (r = lane / 4, g) of slot pair s / 2: nibble lane % 4
-        uint32_t w = (uint32_t)code << (4 * (lane & 3));
-        w |= __shfl_xor_sync(0xffffffffu, w, 1);
-        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        if ((lane & 3) == 0)
-            *reinterpret_cast<uint16_t*>(tile + O4_VC + 128 * (s >> 1) + 16 * (lane >> 2) + 4 * g + 2 * (s & 1)) =
-                (uint16_t)w;
-        if (lane == 0) {
-            *reinterpret_cast<__half*>(tile + O4_VS + int4_vmeta_off(s, g)) = sh;
-            *reinterpret_cast<__half*>(tile + O4_VM + int4_vmeta_off(s, g)) = mh;
+        sm.c[tid] = 0.f;
+    }
+    // this warp's channels of R as operands: column n of set i is channel 32 g + 8 (n / 2) + 2 i + n % 2
+    uint32_t bf[3][4][8][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float2 x = *reinterpret_cast<const float2*>(&sm.RT[32 * g + 8 * (r >> 1) + 2 * i + (r & 1)][16 * ks + 8 * e + 2 * t]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const float lo = bf16_part(x.x), hi = bf16_part(x.y);
+                    bf[p][i][ks][e] = pack_bf16(lo, hi);
+                }
+            }
+
+    int buf = 0;
+#pragma unroll 1
+    for (int x = blockIdx.x; x < tiles; x += gridDim.x, buf ^= 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the tile is there; the last one's words are written out
+        {   // norms: 8 threads a row
+            const int row = tid >> 3;
+            const uint4* p = reinterpret_cast<const uint4*>(&sm.A[buf][row][16 * (tid & 7)]);
+            float n2 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint4 q = p[e];
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float a = __uint_as_float(w[y] << 16), b = __uint_as_float(w[y] & 0xffff0000u);
+                    n2 = fmaf(a, a, fmaf(b, b, n2));
+                }
+            }
+            n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
+            n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
+            n2 += __shfl_xor_sync(0xffffffffu, n2, 4);
+            if ((tid & 7) == 0) sm.n2[row] = n2;
+        }
+        if (x + (int)gridDim.x < tiles) fetch(x + gridDim.x, buf ^ 1);
+
+        float acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+        const uint32_t a_addr = smem_u32(&sm.A[buf][lane & 15][8 * (lane >> 4)]);
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                uint32_t a[4];
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                             : "r"(a_addr + 32 * ks));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_bf16(acc[i], a, bf[p][i][ks][0], bf[p][i][ks][1]);
+            }
+        __syncthreads();  // the norms are there
+
+        // (k - mu) . R[:, ch] (or v . R) of a row, by the whole warp
+        auto exact = [&](int row, int ch) {
+            const uint2 raw = *reinterpret_cast<const uint2*>(&sm.A[buf][row][4 * lane]);
+            const float4 rv = *reinterpret_cast<const float4*>(&sm.RT[ch][4 * lane]);
+            const float4 m4 = *reinterpret_cast<const float4*>(&sm.mu[4 * lane]);
+            const float xv[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                                 __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
+            const float mv[4] = {m4.x, m4.y, m4.z, m4.w}, rw[4] = {rv.x, rv.y, rv.z, rv.w};
+            Dd s = {0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float hi, lo;
+                two_sum(xv[e], -mv[e], hi, lo);
+                dd_fma(s, hi, lo, rw[e]);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                Dd y;
+                y.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+                y.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+                dd_add(s, y);
+            }
+            // (the butterfly adds in another order in each lane: take one lane's)
+            s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
+            s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
+            return s.value();
+        };
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = r + 8 * e;
+            const bool live = sm.slot[buf][row] >= 0;
+            float z[8];
+            const float4 ca = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t]);
+            const float4 cb = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t + 4]);
+            const float cc[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = acc[i >> 1][2 * e + (i & 1)] - cc[i];
+            const float n2 = sm.n2[row] + sm.mu2;
+            const bool wild = live && int4_wild(n2);
+            const float eps = PF_EPS * (sqrtf(sm.n2[row]) + sqrtf(sm.mu2));
+            float mn = z[0], mx = z[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                mn = fminf(mn, z[i]);
+                mx = fmaxf(mx, z[i]);
+            }
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            __half sh, mh;
+            const bool open = int4_params_near(mn, mx, clip, eps, sh, mh) && live && !wild;
+            // ---- groups whose parameters are open: the exact ends (every value that could be one)
+            uint32_t rows = __ballot_sync(0xffffffffu, open);
+            while (rows) {
+                const int base = (__ffs(rows) - 1) & ~3;  // the four lanes of a row agree
+                uint32_t cand = 0;
+                if ((lane & ~3) == base) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) cand |= (uint32_t)(z[i] <= mn + 2.f * eps || z[i] >= mx - 2.f * eps) << i;
+                }
+                double lo = CUDART_INF, hi = -CUDART_INF;
+                uint32_t any = __ballot_sync(0xffffffffu, cand != 0);
+                while (any) {
+                    const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, cand, l)) - 1;
+                    const double y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
+                    lo = fmin(lo, y);
+                    hi = fmax(hi, y);
+                    if (lane == l) cand &= cand - 1;
+                    any = __ballot_sync(0xffffffffu, cand != 0);
+                }
+                if ((lane & ~3) == base) int4_params(lo, hi, (double)clip, sh, mh);
+                rows &= ~(0xfu << base);
+            }
+            // ---- codes
+            const float s = __half2float(sh), m = __half2float(mh), inv = s > 0.f ? 1.f / s : 0.f;
+            uint32_t w = 0, again = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                bool near;
+                w |= (uint32_t)int4_code_near(z[i], s, inv, m, eps, near) << (4 * i);
+                again |= (uint32_t)near << i;
+            }
+            if (!live || wild) again = 0;
+            uint32_t any = __ballot_sync(0xffffffffu, again != 0);
+            while (any) {
+                const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, again, l)) - 1;
+                const double y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
+                if (lane == l) {
+                    w = (w & ~(15u << (4 * i))) | (uint32_t)int4_code(y, sh, mh) << (4 * i);
+                    again &= again - 1;
+                }
+                any = __ballot_sync(0xffffffffu, again != 0);
+            }
+            // ---- rows outside fp32's comfortable range: all in fp64
+            rows = __ballot_sync(0xffffffffu, wild);
+            while (rows) {
+                const int base = (__ffs(rows) - 1) & ~3, rw = (base >> 2) + 8 * e;
+                double y = 0.0;  // lane = channel of the group
+                for (int i = 0; i < D; ++i)
+                    y = fma((double)__bfloat162float(sm.A[buf][rw][i]) - (double)sm.mu[i], (double)sm.RT[32 * g + lane][i], y);
+                double lo = y, hi = y;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                    hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+                }
+                if (__any_sync(0xffffffffu, !isfinite(y))) lo = hi = CUDART_NAN;
+                __half a, b;
+                int4_params(lo, hi, (double)clip, a, b);
+                uint32_t c = (uint32_t)int4_code(y, a, b) << (4 * (lane & 7));
+                c |= __shfl_xor_sync(0xffffffffu, c, 1);
+                c |= __shfl_xor_sync(0xffffffffu, c, 2);
+                c |= __shfl_xor_sync(0xffffffffu, c, 4);
+                c = __shfl_sync(0xffffffffu, c, 8 * t);  // the word of channels 8 t ..
+                if ((lane & ~3) == base) {
+                    w = c;
+                    sh = a;
+                    mh = b;
+                }
+                rows &= ~(0xfu << base);
+            }
+            sm.word[row][t][g] = w;
+            if (t == 0) {
+                sm.sc[row][g] = sh;
+                sm.mn[row][g] = mh;
+            }
+        }
+        __syncthreads();  // the tile's codes are there
+        if (!side) {
+            // a token's record: four pieces of codes and one of meta, 16 bytes each
+            if (tid < 5 * PF_M) {
+                const int row = tid / 5, piece = tid % 5, slot = sm.slot[buf][row];
+                if (slot >= 0) {
+                    uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
+                    const int s = slot % PAGE;
+                    if (piece < 4) {
+                        *reinterpret_cast<uint4*>(tile + O4_KC + 64 * s + 16 * piece) = *reinterpret_cast<const uint4*>(sm.word[row][piece]);
+                    } else {
+                        const uint2 a = *reinterpret_cast<const uint2*>(sm.sc[row]), b = *reinterpret_cast<const uint2*>(sm.mn[row]);
+                        *reinterpret_cast<uint4*>(tile + O4_KM + 16 * s) = make_uint4(a.x, a.y, b.x, b.y);
+                    }
+                }
+            }
+        } else {
+            // token pair (2 j, 2 j + 1) of the tile in the two slots of one pair: whole words
+            // (thread = eighth of a pair row: channels 32 g + 4 q ..); else halves
+            const int j = tid >> 4, q = tid & 15;
+            const int sa = sm.slot[buf][2 * j], sb = sm.slot[buf][2 * j + 1];
+            const bool pair = sa >= 0 && !(sa & 1) && sb == sa + 1;
+            if (pair) {
+                uint8_t* tile = cache + ((size_t)(sa / PAGE) * H_kv + h) * INT4_TILE;
+                const int s = (sa % PAGE) >> 1;
+                if (q < 8) {
+                    uint32_t out[4];
+                    const uint32_t sel = q & 1 ? 0x7632 : 0x5410;
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) out[gg] = prmt(sm.word[2 * j][q >> 1][gg], sm.word[2 * j + 1][q >> 1][gg], sel);
+                    *reinterpret_cast<uint4*>(tile + O4_VC + 128 * s + 16 * q) = make_uint4(out[0], out[1], out[2], out[3]);
+                } else if (q < 10) {
+                    const __half(*src2)[NGROUP] = q == 8 ? sm.sc : sm.mn;
+                    const uint2 a = *reinterpret_cast<const uint2*>(src2[2 * j]), b = *reinterpret_cast<const uint2*>(src2[2 * j + 1]);
+                    *reinterpret_cast<uint4*>(tile + (q == 8 ? O4_VS : O4_VM) + 16 * s) =
+                        make_uint4(prmt(a.x, b.x, 0x5410), prmt(a.x, b.x, 0x7632), prmt(a.y, b.y, 0x5410), prmt(a.y, b.y, 0x7632));
+                }
+            } else {
+                for (int e = 0; e < 2; ++e) {
+                    const int slot = e ? sb : sa, row = 2 * j + e;
+                    if (slot < 0) continue;
+                    uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
+                    store_word(tile, 1, slot % PAGE, q & 3, q >> 2, sm.word[row][q >> 2][q & 3]);
+                    if (q < NGROUP) store_meta(tile, 1, slot % PAGE, q, sm.sc[row][q], sm.mn[row][q]);
+                }
+            }
         }
     }
 }
 
-// Reads cached tokens back: one CTA per (token, KV head), thread j < 128 key
-// channel j, thread 128 + j value channel j; one fp32 fma, one rounding to bf16.
+// ------------------------------------------------------------ read-back
+//
+// Sixteen threads per (token, KV head, side), a word of eight channels each: one
+// fp32 fma and one rounding to bf16 per channel, a 16-byte store.
+
 __global__ void __launch_bounds__(256)
-dequant_int4_kernel(const uint8_t* __restrict__ cache, int64_t num_pages, int H_kv,
+dequant_int4_kernel(const uint8_t* __restrict__ cache, int64_t num_pages, int H_kv, int64_t rows,
                     const int32_t* __restrict__ slot_mapping, __nv_bfloat16* __restrict__ k_rot,
                     __nv_bfloat16* __restrict__ v_rot) {
     griddep_wait();
     griddep_launch_dependents();
-    const int t = blockIdx.x, h = blockIdx.y;
-    const int side = threadIdx.x >> 7, j = threadIdx.x & (D - 1);
+    const int64_t x = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // (token, head)
+    const int side = blockIdx.y, g = (threadIdx.x >> 2) & 3, t = threadIdx.x & 3;
     __nv_bfloat16* dst = side ? v_rot : k_rot;
-    if (!dst) return;
-    const int slot = __ldg(slot_mapping + t);
-    float val = 0.f;
+    if (!dst || x >= rows) return;
+    const int h = (int)(x % H_kv), slot = __ldg(slot_mapping + x / H_kv);
+    uint32_t out[4] = {0u, 0u, 0u, 0u};
     if (slot >= 0 && (int64_t)slot < num_pages * PAGE) {
-        const int s = slot % PAGE, g = j >> 5;
+        const int s = slot % PAGE;
         const uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
-        int code;
+        uint32_t w;
         const __half *ps, *pm;
         if (side) {
-            const int r = (j >> 2) & 7, i = j & 3;
-            code = *reinterpret_cast<const uint16_t*>(tile + O4_VC + 128 * (s >> 1) + 16 * r + 4 * g + 2 * (s & 1)) >> (4 * i);
+            const uint8_t* p = tile + O4_VC + 128 * (s >> 1) + 32 * t + 4 * g + 2 * (s & 1);
+            w = (uint32_t)*reinterpret_cast<const uint16_t*>(p) | (uint32_t)*reinterpret_cast<const uint16_t*>(p + 16) << 16;
             ps = reinterpret_cast<const __half*>(tile + O4_VS + int4_vmeta_off(s, g));
             pm = reinterpret_cast<const __half*>(tile + O4_VM + int4_vmeta_off(s, g));
         } else {
-            const int tt = (j >> 3) & 3, i = j & 7;
-            code = (int)(*reinterpret_cast<const uint32_t*>(tile + O4_KC + 64 * s + 16 * tt + 4 * g) >> (4 * i));
+            w = *reinterpret_cast<const uint32_t*>(tile + O4_KC + 64 * s + 16 * t + 4 * g);
             ps = reinterpret_cast<const __half*>(tile + O4_KM + 16 * s + 2 * g);
             pm = reinterpret_cast<const __half*>(tile + O4_KM + 16 * s + 8 + 2 * g);
         }
-        val = __fmaf_rn((float)(code & 15), __half2float(*ps), __half2float(*pm));
+        const float sc = __half2float(*ps), mn = __half2float(*pm);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[i] = pack_bf16(__fmaf_rn((float)((w >> (8 * i)) & 15), sc, mn), __fmaf_rn((float)((w >> (8 * i + 4)) & 15), sc, mn));
     }
-    dst[((size_t)t * H_kv + h) * D + j] = __float2bfloat16_rn(val);
+    *reinterpret_cast<uint4*>(dst + x * D + 32 * g + 8 * t) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 }  // namespace kvq
@@ -114,6 +543,24 @@ dequant_int4_kernel(const uint8_t* __restrict__ cache, int64_t num_pages, int H_
 using namespace kvq;
 
 extern "C" size_t kvq_int4_tile_bytes(int d) { return d == D ? (size_t)INT4_TILE : 0; }
+
+// Appends of at least this many tokens take the tensor-core kernel.
+static constexpr int PREFILL_MIN = 32;
+
+static kvq_status prefill_smem_once() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    kvq_status st = kvq_check_cuda(cudaGetDevice(&dev), "kvq_append_int4: cudaGetDevice");
+    if (st != KVQ_OK) return st;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < 64 && done[dev]) return KVQ_OK;
+    st = kvq_check_cuda(cudaFuncSetAttribute((const void*)append_int4_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sizeof(PrefillSmem)),
+                        "kvq_append_int4 smem attribute");
+    if (st == KVQ_OK && dev >= 0 && dev < 64) done[dev] = true;
+    return st;
+}
 
 extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, int H_kv, int d,
                                       const int32_t* slot_mapping, const float* mu_k, const float* R_k,
@@ -129,12 +576,23 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
     if (n_tok == 0) return KVQ_OK;
     if (!k || !v || !slot_mapping || !mu_k || !R_k || !R_v || !cache)
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_append_int4: null pointer");
-    if (reinterpret_cast<uintptr_t>(cache) % 16)
-        return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_append_int4: cache not 16-byte aligned");
-    return kvq_check_cuda(launch_pdl(append_int4_kernel, dim3(n_tok, H_kv), dim3(256), 0,
-                                     static_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(k),
-                                     static_cast<const __nv_bfloat16*>(v), n_tok, H_kv, slot_mapping, mu_k, R_k, R_v,
-                                     static_cast<uint8_t*>(cache), num_pages, err_count, clip),
+    for (const void* p : {k, v, (const void*)R_k, (const void*)R_v, (const void*)cache})
+        if (reinterpret_cast<uintptr_t>(p) % 16)
+            return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_append_int4: k, v, R_k, R_v and cache need to be 16-byte aligned");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const auto kb = static_cast<const __nv_bfloat16*>(k), vb = static_cast<const __nv_bfloat16*>(v);
+    uint8_t* const cb = static_cast<uint8_t*>(cache);
+    if (n_tok < PREFILL_MIN)
+        return kvq_check_cuda(launch_pdl(append_int4_kernel, dim3(n_tok, H_kv, 2), dim3(512), 0, st, kb, vb, n_tok, H_kv,
+                                         slot_mapping, mu_k, R_k, R_v, cb, num_pages, err_count, clip),
+                              "kvq_append_int4 launch");
+    const kvq_status sa = prefill_smem_once();
+    if (sa != KVQ_OK) return sa;
+    // two CTAs per SM in all, each with a stride of its (head, side)'s tiles
+    const int tiles = (n_tok + PF_M - 1) / PF_M, most = (2 * kvq_device_sm_count() + 2 * H_kv - 1) / (2 * H_kv);
+    return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(tiles < most ? tiles : most, H_kv, 2), dim3(128),
+                                     sizeof(PrefillSmem), st, kb, vb, n_tok, H_kv, slot_mapping, mu_k, R_k, R_v, cb, num_pages,
+                                     err_count, clip),
                           "kvq_append_int4 launch");
 }
 
@@ -147,11 +605,13 @@ extern "C" kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int
     if (n == 0) return KVQ_OK;
     if (!cache || !slot_mapping || (!k_rot && !v_rot))
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_dequant_int4: null pointer");
-    if (reinterpret_cast<uintptr_t>(cache) % 16)
-        return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_dequant_int4: cache not 16-byte aligned");
-    return kvq_check_cuda(launch_pdl(dequant_int4_kernel, dim3(n, H_kv), dim3(256), 0,
-                                     static_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(cache), num_pages,
-                                     H_kv, slot_mapping, static_cast<__nv_bfloat16*>(k_rot),
-                                     static_cast<__nv_bfloat16*>(v_rot)),
+    for (const void* p : {cache, (const void*)k_rot, (const void*)v_rot})
+        if (reinterpret_cast<uintptr_t>(p) % 16)
+            return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_dequant_int4: cache, k_rot and v_rot need to be 16-byte aligned");
+    const int64_t rows = (int64_t)n * H_kv, blocks = (rows + 15) / 16;
+    if (blocks > 0x7fffffff) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "kvq_dequant_int4: n * H_kv above 2^35");
+    return kvq_check_cuda(launch_pdl(dequant_int4_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                                     static_cast<const uint8_t*>(cache), num_pages, H_kv, rows, slot_mapping,
+                                     static_cast<__nv_bfloat16*>(k_rot), static_cast<__nv_bfloat16*>(v_rot)),
                           "kvq_dequant_int4 launch");
 }

@@ -323,7 +323,8 @@ size_t kvq_int4_tile_bytes(int d);
  * lower level); 0 when scale == 0.  A group holding a value that is not finite
  * is stored with NaN scale and min (it reads back as NaN).  Tokens with equal
  * slots race (last writer unspecified); what a token's bytes are does not
- * depend on the tokens appended with it. */
+ * depend on the tokens appended with it.  k, v, R_k, R_v and cache need 16-byte
+ * alignment. */
 kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, int H_kv, int d,
                            const int32_t* slot_mapping, const float* mu_k,
                            const float* R_k, const float* R_v, float clip,
@@ -331,8 +332,8 @@ kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, int H_kv, in
 
 /* Reads cached tokens back: min + code*scale of the tokens at
  * slot_mapping[0..n), still centred and rotated, rounded once to bf16.
- *   k_rot, v_rot  device bf16 [n][H_kv][d], either may be null; a slot outside
- *                 the cache gives zeros */
+ *   k_rot, v_rot  device bf16 [n][H_kv][d], 16-byte aligned, either may be null;
+ *                 a slot outside the cache gives zeros */
 kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int H_kv, int d,
                             const int32_t* slot_mapping, int n, void* k_rot, void* v_rot,
                             void* stream);
