@@ -75,7 +75,6 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
     }
     __syncthreads();
     const bool wild = int4_wild(n2s[0] + n2s[1] + n2s[2] + n2s[3]);  // CTA-uniform
-    double z64 = 0.0;
     if (!wild) {
         // four chains, so that their latencies overlap
         Dd acc[4] = {};
@@ -90,42 +89,41 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
     }
     __syncthreads();
     if (quarter) return;
-    float z, eps = 0.f;
-    if (!wild) {
-        Dd a = part[0][j], b = part[2][j];
-        dd_add(a, part[1][j]);
-        dd_add(b, part[3][j]);
-        dd_add(a, b);
-        z64 = a.value();
-        z = __double2float_rn(z64);
-    } else {
-        const float* Rw = (side ? Rv : Rk) + (size_t)h * D * D + j;
-        for (int i = 0; i < D; ++i) z64 = fma((double)xs[i] + (double)xl[i], (double)__ldg(Rw + (size_t)i * D), z64);
-        z = (float)z64;
-    }
-    // the group's range: z within half an ulp of its exact value
-    float mn = z, mx = z;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
-    eps = fmaxf(fabsf(mn), fabsf(mx)) * 0x1p-23f;
     __half sh, mh;
-    if (int4_params_near(mn, mx, clip, eps, sh, mh) || wild) {  // warp-uniform
-        double lo = z64, hi = z64;
+    int code;
+    if (!wild) {
+        Dd z = part[0][j], y = part[2][j];
+        dd_add(z, part[1][j]);
+        dd_add(y, part[3][j]);
+        dd_add(z, y);
+        z = dd_norm(z);
+        Dd mn = z, mx = z;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const Dd a = {__shfl_xor_sync(0xffffffffu, mn.hi, o), __shfl_xor_sync(0xffffffffu, mn.lo, o)};
+            const Dd b = {__shfl_xor_sync(0xffffffffu, mx.hi, o), __shfl_xor_sync(0xffffffffu, mx.lo, o)};
+            if (dd_less(a, mn)) mn = a;
+            if (dd_less(mx, b)) mx = b;
+        }
+        int4_params(mn, mx, clip, sh, mh);
+        const float s = __half2float(sh), m = __half2float(mh);
+        // the nearest threshold decides between two codes (past the ends, and for s = 0, the end)
+        const float q = s > 0.f ? fmaf(z.hi - m, 1.f / s, -0.5f) : -1.f;
+        code = q <= -0.5f ? 0 : q >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(z, s, m, (int)rintf(q));
+    } else {  // all in fp64
+        const float* Rw = (side ? Rv : Rk) + (size_t)h * D * D + j;
+        double z = 0.0;
+        for (int i = 0; i < D; ++i) z = fma((double)xs[i] + (double)xl[i], (double)__ldg(Rw + (size_t)i * D), z);
+        double lo = z, hi = z;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        if (__any_sync(0xffffffffu, !isfinite(z64))) lo = hi = CUDART_NAN;
+        if (__any_sync(0xffffffffu, !isfinite(z))) lo = hi = CUDART_NAN;
         int4_params(lo, hi, (double)clip, sh, mh);
+        code = int4_code(z, sh, mh);
     }
-    const float s = __half2float(sh), m = __half2float(mh);
-    bool near;
-    int code = int4_code_near(z, s, s > 0.f ? 1.f / s : 0.f, m, eps, near);
-    if (near || wild) code = int4_code(z64, sh, mh);
     // the eight codes of a word sit in eight neighbouring lanes
     uint32_t w = (uint32_t)code << (4 * (lane & 7));
     w |= __shfl_xor_sync(0xffffffffu, w, 1);
@@ -147,12 +145,14 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // 2 t + e of its eight columns' set i, the accumulators of a lane are the eight codes
 // of one word of the key record.
 //
-// |z - accumulated| <= PF_EPS (|k| + |mu|): the largest error seen was 2^-21.4 of the
-// norm (2^30 values), the bound leaves a factor of five.  Groups or codes that the
-// bound leaves open (about one group in twelve, two codes in ten thousand) take an
-// exact dot product by the whole warp.
+// |z - accumulated| <= PF_EPS (|k| + |mu|): the largest error seen was 2^-22.1 of the
+// norms (2 10^8 values of three distributions), the bound leaves a factor of four.
+// Groups or codes that the bound leaves open (about one group in twenty-five, one
+// code in ten thousand) take exact dot products by the whole warp, in pairs of fp32
+// values: fp64 is 64 times slower than fp32 here, and a first form of these second
+// looks in fp64 took most of the kernel's time (32K tokens 1.10 ms).
 constexpr int PF_M = 16;                 // tokens of a tile
-constexpr float PF_EPS = 0x1p-19f;
+constexpr float PF_EPS = 0x1p-20f;
 constexpr int PF_RT = D + 4, PF_A = D + 8;  // padded rows, in elements
 
 struct __align__(16) PrefillSmem {
@@ -345,7 +345,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             // (the butterfly adds in another order in each lane: take one lane's)
             s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
             s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
-            return s.value();
+            return dd_norm(s);
         };
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -381,17 +381,17 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
 #pragma unroll
                     for (int i = 0; i < 8; ++i) cand |= (uint32_t)(z[i] <= mn + 2.f * eps || z[i] >= mx - 2.f * eps) << i;
                 }
-                double lo = CUDART_INF, hi = -CUDART_INF;
+                Dd lo = {CUDART_INF_F, 0.f}, hi = {-CUDART_INF_F, 0.f};
                 uint32_t any = __ballot_sync(0xffffffffu, cand != 0);
                 while (any) {
                     const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, cand, l)) - 1;
-                    const double y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
-                    lo = fmin(lo, y);
-                    hi = fmax(hi, y);
+                    const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
+                    if (dd_less(y, lo)) lo = y;
+                    if (dd_less(hi, y)) hi = y;
                     if (lane == l) cand &= cand - 1;
                     any = __ballot_sync(0xffffffffu, cand != 0);
                 }
-                if ((lane & ~3) == base) int4_params(lo, hi, (double)clip, sh, mh);
+                if ((lane & ~3) == base) int4_params(lo, hi, clip, sh, mh);
                 rows &= ~(0xfu << base);
             }
             // ---- codes
@@ -407,9 +407,11 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             uint32_t any = __ballot_sync(0xffffffffu, again != 0);
             while (any) {
                 const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, again, l)) - 1;
-                const double y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
+                const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
                 if (lane == l) {
-                    w = (w & ~(15u << (4 * i))) | (uint32_t)int4_code(y, sh, mh) << (4 * i);
+                    // the threshold nearest to y
+                    const int n = max(0, min(INT4_LEVELS - 1, (int)rintf(fmaf(y.hi - m, inv, -0.5f))));
+                    w = (w & ~(15u << (4 * i))) | (uint32_t)int4_code(y, s, m, n) << (4 * i);
                     again &= again - 1;
                 }
                 any = __ballot_sync(0xffffffffu, again != 0);

@@ -80,6 +80,37 @@ __device__ __forceinline__ void dd_add(Dd& acc, Dd o) {
     acc.lo = __fadd_rn(acc.lo, __fadd_rn(t, o.lo));
 }
 
+// hi the nearest fp32 to the sum, so that pairs compare by hi, then lo
+__device__ __forceinline__ Dd dd_norm(Dd a) {
+    Dd r;
+    two_sum(a.hi, a.lo, r.hi, r.lo);
+    return r;
+}
+__device__ __forceinline__ bool dd_less(Dd a, Dd b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+
+// The parameters from exact ends in pairs: the quotient by 15 is refined by its
+// exact remainder, and the sum of the two parts is one rounding to fp32.
+__device__ __forceinline__ void int4_params(Dd mn, Dd mx, float clip, __half& sh, __half& mh) {
+    Dd d = {mx.hi, mx.lo};
+    dd_add(d, Dd{-mn.hi, -mn.lo});
+    d = dd_norm(d);
+    float p = __fmul_rn(clip, d.hi), e = __fmaf_rn(clip, d.lo, __fmaf_rn(clip, d.hi, -p));
+    const float q = __fdiv_rn(p, (float)INT4_LEVELS), rest = __fadd_rn(__fmaf_rn(-q, (float)INT4_LEVELS, p), e);
+    sh = f16_sat_nan(__fadd_rn(q, __fdiv_rn(rest, (float)INT4_LEVELS)));
+    p = __fmul_rn(clip, mn.hi);
+    e = __fmaf_rn(clip, mn.lo, __fmaf_rn(clip, mn.hi, -p));
+    mh = f16_sat_nan(__fadd_rn(p, e));
+}
+
+// code of z near threshold n (code n or n + 1): min + (n + 1/2) scale is a sum of
+// two fp32 values exactly, and z minus it has the right sign.
+__device__ __forceinline__ int int4_code(Dd z, float s, float m, int n) {
+    float th, tl, d, e;
+    two_sum(m, ((float)n + 0.5f) * s, th, tl);
+    two_sum(z.hi, -th, d, e);
+    return n + (__fadd_rn(d, __fadd_rn(e, __fsub_rn(z.lo, tl))) > 0.f);
+}
+
 // Sums of squares outside this range (and not 0) leave the fp32 paths: products
 // would lose bits below the smallest fp32 or leave its range.
 __device__ __forceinline__ bool int4_wild(float n2) { return !(n2 == 0.f || (n2 > 0x1p-80f && n2 < 0x1p100f)); }
