@@ -503,41 +503,56 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
 // ------------------------------------------------------------ read-back
 //
 // Sixteen threads per (token, KV head, side), a word of eight channels each: one
-// fp32 fma and one rounding to bf16 per channel, a 16-byte store.
+// fp32 fma and one rounding to bf16 per channel, a 16-byte store.  A thread takes
+// four tokens, whose loads are in flight together.
+
+constexpr int DQ_TOK = 4;
 
 __global__ void __launch_bounds__(256)
-dequant_int4_kernel(const uint8_t* __restrict__ cache, int64_t num_pages, int H_kv, int64_t rows,
+dequant_int4_kernel(const uint8_t* __restrict__ cache, int64_t num_pages, int H_kv, int n,
                     const int32_t* __restrict__ slot_mapping, __nv_bfloat16* __restrict__ k_rot,
                     __nv_bfloat16* __restrict__ v_rot) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t x = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // (token, head)
-    const int side = blockIdx.y, g = (threadIdx.x >> 2) & 3, t = threadIdx.x & 3;
+    const int side = blockIdx.z, h = blockIdx.y, g = (threadIdx.x >> 2) & 3, t = threadIdx.x & 3;
     __nv_bfloat16* dst = side ? v_rot : k_rot;
-    if (!dst || x >= rows) return;
-    const int h = (int)(x % H_kv), slot = __ldg(slot_mapping + x / H_kv);
-    uint32_t out[4] = {0u, 0u, 0u, 0u};
-    if (slot >= 0 && (int64_t)slot < num_pages * PAGE) {
-        const int s = slot % PAGE;
-        const uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
-        uint32_t w;
-        const __half *ps, *pm;
-        if (side) {
-            const uint8_t* p = tile + O4_VC + 128 * (s >> 1) + 32 * t + 4 * g + 2 * (s & 1);
-            w = (uint32_t)*reinterpret_cast<const uint16_t*>(p) | (uint32_t)*reinterpret_cast<const uint16_t*>(p + 16) << 16;
-            ps = reinterpret_cast<const __half*>(tile + O4_VS + int4_vmeta_off(s, g));
-            pm = reinterpret_cast<const __half*>(tile + O4_VM + int4_vmeta_off(s, g));
-        } else {
-            w = *reinterpret_cast<const uint32_t*>(tile + O4_KC + 64 * s + 16 * t + 4 * g);
-            ps = reinterpret_cast<const __half*>(tile + O4_KM + 16 * s + 2 * g);
-            pm = reinterpret_cast<const __half*>(tile + O4_KM + 16 * s + 8 + 2 * g);
+    if (!dst) return;
+    const int64_t first = (int64_t)blockIdx.x * 16 * DQ_TOK + (threadIdx.x >> 4);
+    uint32_t w[DQ_TOK];
+    __half sc[DQ_TOK], mn[DQ_TOK];
+    int slot[DQ_TOK];
+#pragma unroll
+    for (int e = 0; e < DQ_TOK; ++e) slot[e] = first + 16 * e < n ? __ldg(slot_mapping + first + 16 * e) : -1;
+#pragma unroll
+    for (int e = 0; e < DQ_TOK; ++e) {
+        w[e] = 0u;
+        sc[e] = mn[e] = __ushort_as_half(0);
+        if (slot[e] >= 0 && (int64_t)slot[e] < num_pages * PAGE) {
+            const int s = slot[e] % PAGE;
+            const uint8_t* tile = cache + ((size_t)(slot[e] / PAGE) * H_kv + h) * INT4_TILE;
+            if (side) {
+                const uint8_t* p = tile + O4_VC + 128 * (s >> 1) + 32 * t + 4 * g + 2 * (s & 1);
+                w[e] = (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p)) | (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p + 16)) << 16;
+                sc[e] = *reinterpret_cast<const __half*>(tile + O4_VS + int4_vmeta_off(s, g));
+                mn[e] = *reinterpret_cast<const __half*>(tile + O4_VM + int4_vmeta_off(s, g));
+            } else {
+                w[e] = __ldg(reinterpret_cast<const uint32_t*>(tile + O4_KC + 64 * s + 16 * t + 4 * g));
+                sc[e] = *reinterpret_cast<const __half*>(tile + O4_KM + 16 * s + 2 * g);
+                mn[e] = *reinterpret_cast<const __half*>(tile + O4_KM + 16 * s + 8 + 2 * g);
+            }
         }
-        const float sc = __half2float(*ps), mn = __half2float(*pm);
+    }
+#pragma unroll
+    for (int e = 0; e < DQ_TOK; ++e) {
+        if (first + 16 * e >= n) break;
+        const float s = __half2float(sc[e]), m = __half2float(mn[e]);
+        uint32_t out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            out[i] = pack_bf16(__fmaf_rn((float)((w >> (8 * i)) & 15), sc, mn), __fmaf_rn((float)((w >> (8 * i + 4)) & 15), sc, mn));
+            out[i] = pack_bf16(__fmaf_rn((float)((w[e] >> (8 * i)) & 15), s, m), __fmaf_rn((float)((w[e] >> (8 * i + 4)) & 15), s, m));
+        *reinterpret_cast<uint4*>(dst + ((size_t)(first + 16 * e) * H_kv + h) * D + 32 * g + 8 * t) =
+            make_uint4(out[0], out[1], out[2], out[3]);
     }
-    *reinterpret_cast<uint4*>(dst + x * D + 32 * g + 8 * t) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 }  // namespace kvq
@@ -610,10 +625,9 @@ extern "C" kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int
     for (const void* p : {cache, (const void*)k_rot, (const void*)v_rot})
         if (reinterpret_cast<uintptr_t>(p) % 16)
             return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_dequant_int4: cache, k_rot and v_rot need to be 16-byte aligned");
-    const int64_t rows = (int64_t)n * H_kv, blocks = (rows + 15) / 16;
-    if (blocks > 0x7fffffff) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "kvq_dequant_int4: n * H_kv above 2^35");
-    return kvq_check_cuda(launch_pdl(dequant_int4_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, static_cast<cudaStream_t>(stream),
-                                     static_cast<const uint8_t*>(cache), num_pages, H_kv, rows, slot_mapping,
+    const int blocks = (int)(((int64_t)n + 16 * DQ_TOK - 1) / (16 * DQ_TOK));
+    return kvq_check_cuda(launch_pdl(dequant_int4_kernel, dim3(blocks, H_kv, 2), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                                     static_cast<const uint8_t*>(cache), num_pages, H_kv, n, slot_mapping,
                                      static_cast<__nv_bfloat16*>(k_rot), static_cast<__nv_bfloat16*>(v_rot)),
                           "kvq_dequant_int4 launch");
 }

@@ -1,11 +1,15 @@
 // Eviction from the INT4 cache by accumulated attention weight: the selection
 // of the tokens each (sequence, KV head) keeps, and the move of the kept
 // tokens into other pages.
+#include <mutex>
+
 #include "int4_common.cuh"
 
 namespace kvq {
 
-constexpr int SEL_THREADS = 1024;
+constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_BINS = 2048;                       // bins of a digit (11, 11 and 10 bits)
+constexpr int SEL_KEYS = 48 * 1024;                  // keys a CTA holds in shared memory
 
 // Order-preserving key of a weight: larger weight, larger key; -0 as 0, NaN as -inf.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -14,80 +18,188 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, KV head).  Candidates are the tokens [sinks, n -
-// recent); the k-th largest key is found by a radix search, eight bits a pass
-// over the row, and the kept indices are written in order by a running count.
+struct SelectSmem {
+    int hist[3][SEL_BINS];
+    int warp_sum[SEL_WARPS], warp_gt[SEL_WARPS], warp_eq[SEL_WARPS];
+    int total_gt, total_eq, digit, above;
+};
+
+// The same shared variable of CTA `rank` of the cluster.
+__device__ __forceinline__ int cluster_load(const int* p, int rank) {
+    uint32_t addr;
+    int v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A cluster of CS CTAs per (sequence, KV head), each with a contiguous run of the
+// tokens; candidates are the tokens [sinks, n - recent).  Radix selection of the
+// k-th largest key in three digits: a CTA counts its keys in shared memory, the
+// cluster's counts are added by reading them from one another's shared memory, and
+// the row is read from global memory once (its keys stay in shared memory, up to
+// SEL_KEYS per CTA).  Then the kept indices are written in order: every warp counts
+// what it keeps of its run, a prefix sum over warps and CTAs gives it its place.
+// A row of 128K is bound by these steps' latencies (one CTA per row took 300 us).
+template <int CS>
 __global__ void __launch_bounds__(SEL_THREADS)
 evict_select_kernel(const float* __restrict__ weights, int64_t stride, int H_kv, int max_tokens,
                     const int32_t* __restrict__ context_lens, int budget, int sinks, int recent,
-                    int32_t* __restrict__ keep, int32_t* __restrict__ new_lens) {
+                    int32_t* __restrict__ keep, int32_t* __restrict__ new_lens, int in_smem) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_raw);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem_raw + sizeof(SelectSmem));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CS > 1 ? blockIdx.x % CS : 0, h = (int)(blockIdx.x / CS), b = blockIdx.y;
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ int hist[256], warp_eq[32], warp_kept[32];
-    __shared__ uint32_t s_digit;
-    __shared__ int s_above;
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = max(0, min(__ldg(context_lens + b), max_tokens));
     int32_t* out = keep + ((size_t)b * H_kv + h) * budget;
-    if (h == 0 && tid == 0) new_lens[b] = min(n, budget);
-    if (n <= budget) {
-        for (int i = tid; i < budget; i += SEL_THREADS) out[i] = i < n ? i : -1;
+    if (h == 0 && rank == 0 && tid == 0) new_lens[b] = min(n, budget);
+    if (n <= budget) {  // (uniform over the cluster)
+        for (int i = rank * SEL_THREADS + tid; i < budget; i += CS * SEL_THREADS) out[i] = i < n ? i : -1;
         return;
     }
     const float* w = weights + ((size_t)b * H_kv + h) * stride;
-    const int c0 = sinks, c1 = n - recent, k = budget - sinks - recent;  // 0 <= k < c1 - c0
+    const int c0 = sinks, c1 = n - recent;  // 0 <= budget - sinks - recent < c1 - c0
+    // this CTA's tokens, and each warp's run of them (whole 32s)
+    const int per_cta = (n + CS - 1) / CS, t0 = min(n, rank * per_cta), t1 = min(n, t0 + per_cta);
+    const int per_warp = ((t1 - t0 + SEL_THREADS - 1) / SEL_THREADS) * 32;
+    const int w0 = min(t1, t0 + warp * per_warp), w1 = min(t1, w0 + per_warp);
+    for (int i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&sm.hist[0][0])[i] = 0;
+    __syncthreads();
+    auto key_of = [&](int i) { return in_smem ? keys[i - t0] : weight_key(__ldg(w + i)); };
+    auto count = [&](int* hist, int bin, bool in) {
+        // a warp whose keys share a bin (ties) adds them at once
+        const uint32_t m = __ballot_sync(0xffffffffu, in);
+        if (!m) return;
+        const int lead = __ffs(m) - 1, first = __shfl_sync(0xffffffffu, bin, lead);
+        if (__all_sync(0xffffffffu, !in || bin == first)) {
+            if (lane == lead) atomicAdd(&hist[first], __popc(m));
+        } else if (in) {
+            atomicAdd(&hist[bin], 1);
+        }
+    };
+    // ---- first digit, while the keys come in
+#pragma unroll 4
+    for (int i = w0 + lane; i < ((w1 - w0 + 31) & ~31) + w0; i += 32) {
+        const uint32_t key = i < w1 ? weight_key(__ldg(w + i)) : 0u;
+        if (in_smem && i < w1) keys[i - t0] = key;
+        count(sm.hist[0], (int)(key >> 21), i < w1 && i >= c0 && i < c1);
+    }
     uint32_t prefix = 0;
-    int need = k;
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        if (tid < 256) hist[tid] = 0;
+    int need = budget - sinks - recent;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        if (pass > 0) {
+            const int shift = pass == 1 ? 10 : 0;
+            const uint32_t mask = pass == 1 ? 2047u : 1023u;
+#pragma unroll 4
+            for (int i = w0 + lane; i < ((w1 - w0 + 31) & ~31) + w0; i += 32) {
+                const uint32_t key = i < w1 ? key_of(i) : 0u;
+                const bool in = i < w1 && i >= c0 && i < c1 && (pass == 1 ? key >> 21 : key >> 10) == prefix;
+                count(sm.hist[pass], (int)(key >> shift & mask), in);
+            }
+        }
+        if (CS > 1)
+            cluster_barrier();
+        else
+            __syncthreads();
+        // thread t: bins 2047 - 2 t and the one below, so that a prefix sum counts from the top
+        const int hi_bin = SEL_BINS - 1 - 2 * tid;
+        int x = 0, y = 0;
+        if (CS > 1) {
+#pragma unroll
+            for (int q = 0; q < CS; ++q) {
+                x += cluster_load(&sm.hist[pass][hi_bin], q);
+                y += cluster_load(&sm.hist[pass][hi_bin - 1], q);
+            }
+        } else {
+            x = sm.hist[pass][hi_bin];
+            y = sm.hist[pass][hi_bin - 1];
+        }
+        int inc = x + y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += z;
+        }
+        if (lane == 31) sm.warp_sum[warp] = inc;
         __syncthreads();
-        for (int i = c0 + tid; i < c1; i += SEL_THREADS) {
-            const uint32_t key = weight_key(__ldg(w + i));
-            if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+        int before = inc - x - y, lower = lane < warp ? sm.warp_sum[lane] : 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) lower += __shfl_xor_sync(0xffffffffu, lower, o);
+        before += lower;  // keys in higher bins than this thread's
+        // the digit: the highest bin with need or more keys from the top down to it (for
+        // need = 0, the top: nothing lies above it, and nothing equal to it is taken)
+        if (need > before && need <= before + x) {
+            sm.digit = hi_bin;
+            sm.above = before;
+        } else if (need > before + x && need <= before + x + y) {
+            sm.digit = hi_bin - 1;
+            sm.above = before + x;
+        } else if (need == 0 && tid == 0) {
+            sm.digit = pass == 2 ? 1023 : SEL_BINS - 1;
+            sm.above = 0;
         }
         __syncthreads();
+        prefix = pass == 2 ? prefix << 10 | (uint32_t)sm.digit : prefix << 11 | (uint32_t)sm.digit;
+        need -= sm.above;
+        __syncthreads();  // (the next pass writes digit, above and warp_sum)
+    }
+    // ---- kept: the protected, keys above `prefix`, and the first `need` equal to it
+    auto look = [&](int i, bool& gt, bool& eq) {  // gt: kept whatever the ties
+        const bool in = i < w1, cand = in && i >= c0 && i < c1;
+        const uint32_t key = cand ? key_of(i) : 0u;
+        gt = in && (!cand || key > prefix);
+        eq = cand && key == prefix;
+    };
+    int n_gt = 0, n_eq = 0;
+    const int end = ((w1 - w0 + 31) & ~31) + w0;
+    for (int i = w0 + lane; i < end; i += 32) {
+        bool gt, eq;
+        look(i, gt, eq);
+        n_gt += __popc(__ballot_sync(0xffffffffu, gt));
+        n_eq += __popc(__ballot_sync(0xffffffffu, eq));
+    }
+    if (lane == 0) {
+        sm.warp_gt[warp] = n_gt;
+        sm.warp_eq[warp] = n_eq;
+    }
+    __syncthreads();
+    int g = sm.warp_gt[lane], e = sm.warp_eq[lane], g_before = lane < warp ? g : 0, e_before = lane < warp ? e : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        g += __shfl_xor_sync(0xffffffffu, g, o);
+        e += __shfl_xor_sync(0xffffffffu, e, o);
+        g_before += __shfl_xor_sync(0xffffffffu, g_before, o);
+        e_before += __shfl_xor_sync(0xffffffffu, e_before, o);
+    }
+    if (CS > 1) {
         if (tid == 0) {
-            int above = 0, dgt = 255;
-            for (; dgt > 0 && above + hist[dgt] < need; --dgt) above += hist[dgt];
-            s_digit = (uint32_t)dgt;
-            s_above = above;
+            sm.total_gt = g;
+            sm.total_eq = e;
         }
-        __syncthreads();
-        prefix = (prefix << 8) | s_digit;
-        need -= s_above;
-        __syncthreads();
+        cluster_barrier();
+        for (int q = 0; q < rank; ++q) {
+            g_before += cluster_load(&sm.total_gt, q);
+            e_before += cluster_load(&sm.total_eq, q);
+        }
     }
-    // kept candidates: keys above `prefix`, and the first `need` equal to it
-    int base_kept = 0, base_eq = 0;
-    for (int i0 = 0; i0 < n; i0 += SEL_THREADS) {
-        const int i = i0 + tid;
-        const bool cand = i >= c0 && i < c1, prot = i < n && !cand;
-        const uint32_t key = cand ? weight_key(__ldg(w + i)) : 0u;
-        const bool eq = cand && key == prefix;
-        const uint32_t meq = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) warp_eq[warp] = __popc(meq);
-        __syncthreads();
-        int eq_before = base_eq + __popc(meq & ((1u << lane) - 1));
-        int eq_all = 0;
-        for (int x = 0; x < 32; ++x) {
-            if (x < warp) eq_before += warp_eq[x];
-            eq_all += warp_eq[x];
-        }
-        const bool kept = prot || (cand && key > prefix) || (eq && eq_before < need);
-        const uint32_t mk = __ballot_sync(0xffffffffu, kept);
-        if (lane == 0) warp_kept[warp] = __popc(mk);
-        __syncthreads();
-        int at = base_kept + __popc(mk & ((1u << lane) - 1)), all = 0;
-        for (int x = 0; x < 32; ++x) {
-            if (x < warp) at += warp_kept[x];
-            all += warp_kept[x];
-        }
-        if (kept && at < budget) out[at] = i;
-        base_kept += all;
-        base_eq += eq_all;
-        __syncthreads();
+    for (int i = w0 + lane; i < end; i += 32) {
+        bool gt, eq;
+        look(i, gt, eq);
+        const uint32_t below = (1u << lane) - 1, mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+        const int e_at = e_before + __popc(me & below);
+        const int at = g_before + __popc(mg & below) + min(e_at, need);
+        if ((gt || (eq && e_at < need)) && at < budget) out[at] = i;
+        g_before += __popc(mg);
+        e_before += __popc(me);
     }
+    if (CS > 1) cluster_barrier();  // (shared memory is read from the other CTAs until here)
 }
 
 // One warp per (destination page, KV head).  The keys' codes and meta are
@@ -158,6 +270,22 @@ evict_gather_int4_kernel(const uint8_t* cache, int64_t num_pages, const int32_t*
 
 using namespace kvq;
 
+// The shared memory opt-in, once per kernel and device.
+static kvq_status select_smem_once(const void* fn, int which) {
+    static std::mutex mu;
+    static bool done[64][4] = {};
+    int dev = 0;
+    kvq_status st = kvq_check_cuda(cudaGetDevice(&dev), "kvq_evict_select: cudaGetDevice");
+    if (st != KVQ_OK) return st;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < 64 && done[dev][which]) return KVQ_OK;
+    st = kvq_check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(sizeof(SelectSmem) + SEL_KEYS * 4)),
+                        "kvq_evict_select smem attribute");
+    if (st == KVQ_OK && dev >= 0 && dev < 64) done[dev][which] = true;
+    return st;
+}
+
 extern "C" kvq_status kvq_evict_select(const float* weights, int64_t weights_stride, int B, int H_kv, int max_tokens,
                                        const int32_t* context_lens, int budget, int sinks, int recent, int32_t* keep,
                                        int32_t* new_lens, void* stream) {
@@ -168,14 +296,39 @@ extern "C" kvq_status kvq_evict_select(const float* weights, int64_t weights_str
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_evict_select: sinks %d + recent %d above the budget %d", sinks, recent,
                              budget);
     if (B > 65535 || H_kv > 65535) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "kvq_evict_select: B or H_kv above 65535");
+    if (max_tokens > (1 << 30)) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "kvq_evict_select: max_tokens %d above 2^30", max_tokens);
     if (weights_stride < max_tokens)
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_evict_select: weights_stride %lld below max_tokens %d",
                              (long long)weights_stride, max_tokens);
     if (!weights || !context_lens || !keep || !new_lens)
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_evict_select: null pointer");
-    return kvq_check_cuda(launch_pdl(evict_select_kernel, dim3(H_kv, B), dim3(SEL_THREADS), 0,
-                                     static_cast<cudaStream_t>(stream), weights, weights_stride, H_kv, max_tokens,
-                                     context_lens, budget, sinks, recent, keep, new_lens),
+    // CTAs per row: up to eight (a cluster) while they find an SM each and 2048 tokens or more
+    const int64_t rows = (int64_t)B * H_kv;
+    const int nsm = kvq_device_sm_count();
+    int cs = 1;
+    while (cs < 8 && rows * cs * 2 <= nsm && max_tokens / (cs * 2) >= 2048) cs *= 2;
+    const int64_t seg = ((int64_t)max_tokens + cs - 1) / cs;
+    const int in_smem = seg <= SEL_KEYS;
+    const size_t smem = sizeof(SelectSmem) + (in_smem ? (size_t)seg * 4 : 0);
+    using Kern = decltype(&evict_select_kernel<1>);
+    const Kern kern = cs == 8 ? evict_select_kernel<8> : cs == 4 ? evict_select_kernel<4> : cs == 2 ? evict_select_kernel<2> : evict_select_kernel<1>;
+    const kvq_status sa = select_smem_once((const void*)kern, cs == 8 ? 3 : cs >> 1);
+    if (sa != KVQ_OK) return sa;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(H_kv * cs, B);
+    cfg.blockDim = dim3(SEL_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    return kvq_check_cuda(cudaLaunchKernelEx(&cfg, kern, weights, weights_stride, H_kv, max_tokens, context_lens, budget, sinks,
+                                             recent, keep, new_lens, in_smem),
                           "kvq_evict_select launch");
 }
 
