@@ -240,30 +240,56 @@ evict_gather_int4_kernel(const uint8_t* cache, int64_t num_pages, const int32_t*
     const int64_t stile = ((int64_t)sid * H_kv + h) * INT4_TILE;
     const int sslot = src & (PAGE - 1);
     uint8_t* dt = dst + ((size_t)__shfl_sync(0xffffffffu, did, 0) * H_kv + h) * INT4_TILE;  // (token 0 is there if any is)
-#pragma unroll
-    for (int c0 = 0; c0 < 96; c0 += 32) {
-        const int c = c0 + lane, tok = min(c / 5, 15), piece = c % 5;
+    // ---- everything is asked for before anything is written
+    uint4 kp[3];           // keys: piece c % 5 (four of codes, one of meta) of token c / 5
+    uint16_t va[8], vb[8]; // value codes: word `lane` of each slot pair, its two sources' halves
+    uint16_t ma[2], mb[2]; // value meta: word x % 8 (four of scales, four of mins) of pair x / 8
+    auto half = [&](int tok, int base, int stride) {  // the source half of a token's word
         const int64_t st = __shfl_sync(0xffffffffu, stile, tok);
         const int ss = __shfl_sync(0xffffffffu, sslot, tok);
-        if (c < 80 && (okm >> tok & 1)) {
-            const int so = piece < 4 ? O4_KC + 64 * ss + 16 * piece : O4_KM + 16 * ss;
-            const int to = piece < 4 ? O4_KC + 64 * tok + 16 * piece : O4_KM + 16 * tok;
-            *reinterpret_cast<uint4*>(dt + to) = *reinterpret_cast<const uint4*>(cache + st + so);
-        }
+        return okm >> tok & 1 ? __ldg(reinterpret_cast<const uint16_t*>(cache + st + base + stride * (ss >> 1) + 2 * (ss & 1)))
+                              : (uint16_t)0;
+    };
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        const int c = 32 * x + lane, tok = min(c / 5, 15), piece = c % 5;
+        const int64_t st = __shfl_sync(0xffffffffu, stile, tok);
+        const int ss = __shfl_sync(0xffffffffu, sslot, tok);
+        kp[x] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < 80 && (okm >> tok & 1))
+            kp[x] = __ldg(reinterpret_cast<const uint4*>(cache + st + (piece < 4 ? O4_KC + 64 * ss + 16 * piece : O4_KM + 16 * ss)));
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int64_t sa = __shfl_sync(0xffffffffu, stile, 2 * j), sb = __shfl_sync(0xffffffffu, stile, 2 * j + 1);
-        const int la = __shfl_sync(0xffffffffu, sslot, 2 * j), lb = __shfl_sync(0xffffffffu, sslot, 2 * j + 1);
-        const bool oa = okm >> (2 * j) & 1, ob = okm >> (2 * j + 1) & 1;
-        // 32 words of codes, then 4 scale and 4 min words
-        for (int w = lane; w < 40; w += 32) {
-            const int base = w < 32 ? O4_VC + 4 * w : (w < 36 ? O4_VS : O4_VM) + 4 * (w & 3), stride = w < 32 ? 128 : 16;
-            uint16_t* d16 = reinterpret_cast<uint16_t*>(dt + base + stride * j);
-            if (oa) d16[0] = *reinterpret_cast<const uint16_t*>(cache + sa + base + stride * (la >> 1) + 2 * (la & 1));
-            if (ob) d16[1] = *reinterpret_cast<const uint16_t*>(cache + sb + base + stride * (lb >> 1) + 2 * (lb & 1));
-        }
+        va[j] = half(2 * j, O4_VC + 4 * lane, 128);
+        vb[j] = half(2 * j + 1, O4_VC + 4 * lane, 128);
     }
+    const int mbase = (lane & 7) < 4 ? O4_VS + 4 * (lane & 3) : O4_VM + 4 * (lane & 3);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int j = 4 * x + (lane >> 3);
+        ma[x] = half(2 * j, mbase, 16);
+        mb[x] = half(2 * j + 1, mbase, 16);
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        const int c = 32 * x + lane, tok = min(c / 5, 15), piece = c % 5;
+        if (c < 80 && (okm >> tok & 1))
+            *reinterpret_cast<uint4*>(dt + (piece < 4 ? O4_KC + 64 * tok + 16 * piece : O4_KM + 16 * tok)) = kp[x];
+    }
+    auto put = [&](int j, int at, uint16_t x, uint16_t y) {  // a slot pair's word, or the half that is there
+        const uint32_t two = okm >> (2 * j) & 3;
+        if (two == 3)
+            *reinterpret_cast<uint32_t*>(dt + at) = (uint32_t)x | (uint32_t)y << 16;
+        else if (two == 1)
+            *reinterpret_cast<uint16_t*>(dt + at) = x;
+        else if (two == 2)
+            *reinterpret_cast<uint16_t*>(dt + at + 2) = y;
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) put(j, O4_VC + 128 * j + 4 * lane, va[j], vb[j]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) put(4 * x + (lane >> 3), mbase + 16 * (4 * x + (lane >> 3)), ma[x], mb[x]);
 }
 
 }  // namespace kvq
