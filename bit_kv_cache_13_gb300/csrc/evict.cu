@@ -18,7 +18,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct SelectSmem {
+struct __align__(16) SelectSmem {
     int hist[3][SEL_BINS];
     int warp_sum[SEL_WARPS], warp_gt[SEL_WARPS], warp_eq[SEL_WARPS];
     int total_gt, total_eq, digit, above;
@@ -32,6 +32,13 @@ __device__ __forceinline__ int cluster_load(const int* p, int rank) {
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ int4 cluster_load4(const int* p, int rank) {
+    uint32_t addr;
+    int4 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -43,7 +50,9 @@ __device__ __forceinline__ void cluster_barrier() {
 // the row is read from global memory once (its keys stay in shared memory, up to
 // SEL_KEYS per CTA).  Then the kept indices are written in order: every warp counts
 // what it keeps of its run, a prefix sum over warps and CTAs gives it its place.
-// A row of 128K is bound by these steps' latencies (one CTA per row took 300 us).
+// A lane takes four neighbouring keys at a time.  A row of 128K is bound by these
+// steps' latencies: one CTA per row took 300 us, and reading the clusters' counts a
+// word at a time 5 us a digit.
 template <int CS>
 __global__ void __launch_bounds__(SEL_THREADS)
 evict_select_kernel(const float* __restrict__ weights, int64_t stride, int H_kv, int max_tokens,
@@ -65,63 +74,91 @@ evict_select_kernel(const float* __restrict__ weights, int64_t stride, int H_kv,
     }
     const float* w = weights + ((size_t)b * H_kv + h) * stride;
     const int c0 = sinks, c1 = n - recent;  // 0 <= budget - sinks - recent < c1 - c0
-    // this CTA's tokens, and each warp's run of them (whole 32s)
-    const int per_cta = (n + CS - 1) / CS, t0 = min(n, rank * per_cta), t1 = min(n, t0 + per_cta);
-    const int per_warp = ((t1 - t0 + SEL_THREADS - 1) / SEL_THREADS) * 32;
-    const int w0 = min(t1, t0 + warp * per_warp), w1 = min(t1, w0 + per_warp);
+    // this CTA's tokens, and each warp's run of them (whole 128s)
+    const int per_cta = ((n + CS - 1) / CS + 3) & ~3, t0 = min(n, rank * per_cta), t1 = min(n, t0 + per_cta);
+    const int per_warp = ((t1 - t0 + 128 * SEL_WARPS - 1) / (128 * SEL_WARPS)) * 128;
+    const int w0 = min(t1, t0 + warp * per_warp), w1 = min(t1, w0 + per_warp), end = w0 + ((w1 - w0 + 127) & ~127);
     for (int i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&sm.hist[0][0])[i] = 0;
     __syncthreads();
-    auto key_of = [&](int i) { return in_smem ? keys[i - t0] : weight_key(__ldg(w + i)); };
-    auto count = [&](int* hist, int bin, bool in) {
-        // a warp whose keys share a bin (ties) adds them at once
-        const uint32_t m = __ballot_sync(0xffffffffu, in);
-        if (!m) return;
-        const int lead = __ffs(m) - 1, first = __shfl_sync(0xffffffffu, bin, lead);
-        if (__all_sync(0xffffffffu, !in || bin == first)) {
-            if (lane == lead) atomicAdd(&hist[first], __popc(m));
-        } else if (in) {
-            atomicAdd(&hist[bin], 1);
+    // keys i .. i + 3 (0 past the run's end, which no candidate's key is below)
+    auto load4 = [&](int i, uint32_t (&key)[4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) key[q] = i + q < w1 ? weight_key(__ldg(w + i + q)) : 0u;
+    };
+    auto keys4 = [&](int i, uint32_t (&key)[4]) {
+        if (in_smem) {  // (the room behind a run's end holds what the load left there: zeros)
+            const uint4 x = *reinterpret_cast<const uint4*>(keys + (i - t0));
+            key[0] = x.x;
+            key[1] = x.y;
+            key[2] = x.z;
+            key[3] = x.w;
+        } else {
+            load4(i, key);
         }
     };
+    auto candidate = [&](int i) { return i >= c0 && i < c1 && i < w1; };
     // ---- first digit, while the keys come in
-#pragma unroll 4
-    for (int i = w0 + lane; i < ((w1 - w0 + 31) & ~31) + w0; i += 32) {
-        const uint32_t key = i < w1 ? weight_key(__ldg(w + i)) : 0u;
-        if (in_smem && i < w1) keys[i - t0] = key;
-        count(sm.hist[0], (int)(key >> 21), i < w1 && i >= c0 && i < c1);
+#pragma unroll 2
+    for (int i = w0 + 4 * lane; i < end; i += 128) {
+        uint32_t key[4];
+        load4(i, key);
+        if (in_smem && i < w1) *reinterpret_cast<uint4*>(keys + (i - t0)) = make_uint4(key[0], key[1], key[2], key[3]);
+        const uint32_t first = __shfl_sync(0xffffffffu, key[0] >> 21, 0);
+        const bool whole = candidate(i) && candidate(i + 3);
+        if (__all_sync(0xffffffffu, whole && key[0] >> 21 == first && key[1] >> 21 == first && key[2] >> 21 == first && key[3] >> 21 == first)) {
+            if (lane == 0) atomicAdd(&sm.hist[0][first], 128);  // (ties: a warp's 128 keys at once)
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (candidate(i + q)) atomicAdd(&sm.hist[0][key[q] >> 21], 1);
+        }
     }
     uint32_t prefix = 0;
     int need = budget - sinks - recent;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         if (pass > 0) {
-            const int shift = pass == 1 ? 10 : 0;
+            const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
             const uint32_t mask = pass == 1 ? 2047u : 1023u;
-#pragma unroll 4
-            for (int i = w0 + lane; i < ((w1 - w0 + 31) & ~31) + w0; i += 32) {
-                const uint32_t key = i < w1 ? key_of(i) : 0u;
-                const bool in = i < w1 && i >= c0 && i < c1 && (pass == 1 ? key >> 21 : key >> 10) == prefix;
-                count(sm.hist[pass], (int)(key >> shift & mask), in);
+#pragma unroll 2
+            for (int i = w0 + 4 * lane; i < end; i += 128) {
+                uint32_t key[4];
+                keys4(min(i, w1 - 1) & ~3, key);
+                bool in[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) in[q] = key[q] >> above == prefix && candidate(i + q);
+                const uint32_t m = __ballot_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3]);
+                if (!m) continue;
+                const uint32_t first = __shfl_sync(0xffffffffu, key[0] >> shift & mask, 0);
+                bool same = true;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) same = same && in[q] && (key[q] >> shift & mask) == first;
+                if (__all_sync(0xffffffffu, same)) {
+                    if (lane == 0) atomicAdd(&sm.hist[pass][first], 128);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (in[q]) atomicAdd(&sm.hist[pass][key[q] >> shift & mask], 1);
+                }
             }
         }
         if (CS > 1)
             cluster_barrier();
         else
             __syncthreads();
-        // thread t: bins 2047 - 2 t and the one below, so that a prefix sum counts from the top
-        const int hi_bin = SEL_BINS - 1 - 2 * tid;
-        int x = 0, y = 0;
-        if (CS > 1) {
+        // thread t < 512: bins 2047 - 4 t and the three below, so that a prefix sum counts from the top
+        const int hi_bin = SEL_BINS - 1 - 4 * tid;
+        int4 v = make_int4(0, 0, 0, 0);
+        if (tid < SEL_BINS / 4) {
 #pragma unroll
             for (int q = 0; q < CS; ++q) {
-                x += cluster_load(&sm.hist[pass][hi_bin], q);
-                y += cluster_load(&sm.hist[pass][hi_bin - 1], q);
+                const int* p = &sm.hist[pass][hi_bin - 3];
+                const int4 x = CS > 1 ? cluster_load4(p, q) : *reinterpret_cast<const int4*>(p);
+                v = make_int4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
             }
-        } else {
-            x = sm.hist[pass][hi_bin];
-            y = sm.hist[pass][hi_bin - 1];
         }
-        int inc = x + y;
+        const int sum = v.x + v.y + v.z + v.w;
+        int inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int z = __shfl_up_sync(0xffffffffu, inc, o);
@@ -129,18 +166,18 @@ evict_select_kernel(const float* __restrict__ weights, int64_t stride, int H_kv,
         }
         if (lane == 31) sm.warp_sum[warp] = inc;
         __syncthreads();
-        int before = inc - x - y, lower = lane < warp ? sm.warp_sum[lane] : 0;
+        int before = inc - sum, lower = lane < warp ? sm.warp_sum[lane] : 0;
 #pragma unroll
         for (int o = 16; o; o >>= 1) lower += __shfl_xor_sync(0xffffffffu, lower, o);
         before += lower;  // keys in higher bins than this thread's
         // the digit: the highest bin with need or more keys from the top down to it (for
         // need = 0, the top: nothing lies above it, and nothing equal to it is taken)
-        if (need > before && need <= before + x) {
-            sm.digit = hi_bin;
+        if (need > before && need <= before + sum) {
+            const int c[4] = {v.w, v.z, v.y, v.x};
+            int q = 0;
+            while (before + c[q] < need) before += c[q++];
+            sm.digit = hi_bin - q;
             sm.above = before;
-        } else if (need > before + x && need <= before + x + y) {
-            sm.digit = hi_bin - 1;
-            sm.above = before + x;
         } else if (need == 0 && tid == 0) {
             sm.digit = pass == 2 ? 1023 : SEL_BINS - 1;
             sm.above = 0;
@@ -151,19 +188,28 @@ evict_select_kernel(const float* __restrict__ weights, int64_t stride, int H_kv,
         __syncthreads();  // (the next pass writes digit, above and warp_sum)
     }
     // ---- kept: the protected, keys above `prefix`, and the first `need` equal to it
-    auto look = [&](int i, bool& gt, bool& eq) {  // gt: kept whatever the ties
-        const bool in = i < w1, cand = in && i >= c0 && i < c1;
-        const uint32_t key = cand ? key_of(i) : 0u;
-        gt = in && (!cand || key > prefix);
-        eq = cand && key == prefix;
+    auto look = [&](int i, uint32_t& gt, uint32_t& eq) {  // bits of keys i .. i + 3; gt: kept whatever the ties
+        uint32_t key[4];
+        keys4(min(i, w1 - 1) & ~3, key);
+        gt = eq = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool cand = candidate(i + q);
+            gt |= (uint32_t)(i + q < w1 && (!cand || key[q] > prefix)) << q;
+            eq |= (uint32_t)(cand && key[q] == prefix) << q;
+        }
     };
     int n_gt = 0, n_eq = 0;
-    const int end = ((w1 - w0 + 31) & ~31) + w0;
-    for (int i = w0 + lane; i < end; i += 32) {
-        bool gt, eq;
+    for (int i = w0 + 4 * lane; i < end; i += 128) {
+        uint32_t gt, eq;
         look(i, gt, eq);
-        n_gt += __popc(__ballot_sync(0xffffffffu, gt));
-        n_eq += __popc(__ballot_sync(0xffffffffu, eq));
+        n_gt += __popc(gt);
+        n_eq += __popc(eq);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        n_gt += __shfl_xor_sync(0xffffffffu, n_gt, o);
+        n_eq += __shfl_xor_sync(0xffffffffu, n_eq, o);
     }
     if (lane == 0) {
         sm.warp_gt[warp] = n_gt;
@@ -189,15 +235,37 @@ evict_select_kernel(const float* __restrict__ weights, int64_t stride, int H_kv,
             e_before += cluster_load(&sm.total_eq, q);
         }
     }
-    for (int i = w0 + lane; i < end; i += 32) {
-        bool gt, eq;
+    const uint32_t below = (1u << lane) - 1;
+    for (int i = w0 + 4 * lane; i < end; i += 128) {
+        uint32_t gt, eq;
         look(i, gt, eq);
-        const uint32_t below = (1u << lane) - 1, mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        const int e_at = e_before + __popc(me & below);
-        const int at = g_before + __popc(mg & below) + min(e_at, need);
-        if ((gt || (eq && e_at < need)) && at < budget) out[at] = i;
-        g_before += __popc(mg);
-        e_before += __popc(me);
+        // what the lanes below keep and tie, and the warp
+        int g_low = 0, e_low = 0, g_all = 0, e_all = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t m = __ballot_sync(0xffffffffu, gt >> q & 1);
+            g_low += __popc(m & below);
+            g_all += __popc(m);
+        }
+        if (__any_sync(0xffffffffu, eq)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t m = __ballot_sync(0xffffffffu, eq >> q & 1);
+                e_low += __popc(m & below);
+                e_all += __popc(m);
+            }
+        }
+        int g_at = g_before + g_low, e_at = e_before + e_low;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool is_gt = gt >> q & 1, is_eq = eq >> q & 1;
+            const int at = g_at + min(e_at, need);
+            if ((is_gt || (is_eq && e_at < need)) && at < budget) out[at] = i + q;
+            g_at += is_gt;
+            e_at += is_eq;
+        }
+        g_before += g_all;
+        e_before += e_all;
     }
     if (CS > 1) cluster_barrier();  // (shared memory is read from the other CTAs until here)
 }
@@ -333,7 +401,7 @@ extern "C" kvq_status kvq_evict_select(const float* weights, int64_t weights_str
     const int nsm = kvq_device_sm_count();
     int cs = 1;
     while (cs < 8 && rows * cs * 2 <= nsm && max_tokens / (cs * 2) >= 2048) cs *= 2;
-    const int64_t seg = ((int64_t)max_tokens + cs - 1) / cs;
+    const int64_t seg = (((int64_t)max_tokens + cs - 1) / cs + 3) & ~int64_t(3);
     const int in_smem = seg <= SEL_KEYS;
     const size_t smem = sizeof(SelectSmem) + (in_smem ? (size_t)seg * 4 : 0);
     using Kern = decltype(&evict_select_kernel<1>);
