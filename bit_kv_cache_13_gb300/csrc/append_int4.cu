@@ -5,7 +5,9 @@
 // rotated vectors, whichever kernel writes them: each kernel forms the rotated
 // values to within a bound, and where a rounding or a threshold lies within that
 // bound of a value (a few groups in a hundred) it forms the value exactly.
+#include <cstddef>
 #include <mutex>
+#include <type_traits>
 
 #include "int4_common.cuh"
 
@@ -153,19 +155,28 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // looks in fp64 took most of the kernel's time (32K tokens 1.10 ms).
 constexpr int PF_M = 16;                 // tokens of a tile
 constexpr float PF_EPS = 0x1p-20f;
+constexpr int PF_LIST = 192;             // exact values of a tile (a full one sends its groups the slow way)
 constexpr int PF_RT = D + 4, PF_A = D + 8;  // padded rows, in elements
 
 struct __align__(16) PrefillSmem {
-    float RT[D][PF_RT];                  // R transposed: RT[channel][input]
-    __nv_bfloat16 A[2][PF_M][PF_A];
-    float mu[D], c[D];                   // the centre (0 for values), and mu R
-    float n2[PF_M];                      // |x|^2 of the tile's rows
+    __align__(16) float RT[D][PF_RT];    // R transposed: RT[channel][input]
+    __align__(16) __nv_bfloat16 A[2][PF_M][PF_A];
+    __align__(16) float mu[D];           // the centre (0 for values)
+    __align__(16) float c[D];            // mu R
+    __align__(16) uint32_t word[PF_M][4][4];  // the tile's codes [token][t][g]
+    __align__(16) __half sc[PF_M][NGROUP];
+    __align__(16) __half mn[PF_M][NGROUP];
+    __align__(16) Dd found[PF_LIST];     // exact values, of
+    uint16_t item[PF_LIST];              // row << 7 | channel
+    float eps[PF_M];                     // the bound on the rows' errors; -1: a row for fp64
     int slot[2][PF_M];
-    uint32_t word[PF_M][4][4];           // the tile's codes [token][t][g]
-    __half sc[PF_M][NGROUP], mn[PF_M][NGROUP];
-    double z[4][32];                     // scratch of a warp
-    float mu2;
+    float m2[4], mu2;
+    int n_item;
 };
+static_assert(offsetof(PrefillSmem, RT) % 16 == 0 && offsetof(PrefillSmem, A) % 16 == 0 && offsetof(PrefillSmem, mu) % 16 == 0 &&
+                  offsetof(PrefillSmem, c) % 16 == 0 && offsetof(PrefillSmem, word) % 16 == 0 && offsetof(PrefillSmem, sc) % 8 == 0 &&
+                  offsetof(PrefillSmem, mn) % 8 == 0 && (PF_RT * 4) % 16 == 0 && (PF_A * 2) % 16 == 0,
+              "wide accesses to shared memory are aligned");
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -238,10 +249,10 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         float m2 = mu_own * mu_own;
 #pragma unroll
         for (int o = 16; o; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-        if (lane == 0) sm.z[0][g] = (double)m2;
+        if (lane == 0) sm.m2[g] = m2;
     }
     __syncthreads();
-    if (tid == 0) sm.mu2 = (float)(sm.z[0][0] + sm.z[0][1] + sm.z[0][2] + sm.z[0][3]);
+    if (tid == 0) sm.mu2 = (sm.m2[0] + sm.m2[1]) + (sm.m2[2] + sm.m2[3]);
     if (side == 0) {  // mu R: thread = channel
         Dd acc[4] = {};
 #pragma unroll 4
@@ -297,7 +308,8 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
             n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
             n2 += __shfl_xor_sync(0xffffffffu, n2, 4);
-            if ((tid & 7) == 0) sm.n2[row] = n2;
+            if ((tid & 7) == 0) sm.eps[row] = int4_wild(n2 + sm.mu2) ? -1.f : PF_EPS * (sqrtf(n2) + sqrtf(sm.mu2));
+            if (tid == 0) sm.n_item = 0;
         }
         if (x + (int)gridDim.x < tiles) fetch(x + gridDim.x, buf ^ 1);
 
@@ -318,106 +330,188 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mma_bf16(acc[i], a, bf[p][i][ks][0], bf[p][i][ks][1]);
             }
-        __syncthreads();  // the norms are there
+        __syncthreads();  // the bounds are there
 
-        // (k - mu) . R[:, ch] (or v . R) of a row, by the whole warp
-        auto exact = [&](int row, int ch) {
-            const uint2 raw = *reinterpret_cast<const uint2*>(&sm.A[buf][row][4 * lane]);
-            const float4 rv = *reinterpret_cast<const float4*>(&sm.RT[ch][4 * lane]);
-            const float4 m4 = *reinterpret_cast<const float4*>(&sm.mu[4 * lane]);
-            const float xv[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                                 __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
-            const float mv[4] = {m4.x, m4.y, m4.z, m4.w}, rw[4] = {rv.x, rv.y, rv.z, rv.w};
-            Dd s = {0.f, 0.f};
+        // (k - mu) . R[:, ch] (or v . R) of a row: the threads of a group of 2^LOG lanes
+        // take four inputs at a time; every lane of the group gets the sum
+        auto exact = [&](int row, int ch, auto log) {
+            constexpr int LANES = 1 << decltype(log)::value;
+            const int q = lane & (LANES - 1);
+            Dd s[2] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float hi, lo;
-                two_sum(xv[e], -mv[e], hi, lo);
-                dd_fma(s, hi, lo, rw[e]);
+            for (int x = 0; x < 32 / LANES; ++x) {
+                const int at = 4 * (LANES * x + q);
+                const uint2 raw = *reinterpret_cast<const uint2*>(&sm.A[buf][row][at]);
+                const float4 rv = *reinterpret_cast<const float4*>(&sm.RT[ch][at]);
+                const float xv[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                                     __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
+                const float rw[4] = {rv.x, rv.y, rv.z, rv.w};
+                if (side) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dd_fma(s[e & 1], xv[e], 0.f, rw[e]);
+                } else {
+                    const float4 m4 = *reinterpret_cast<const float4*>(&sm.mu[at]);
+                    const float mv[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float hi, lo;
+                        two_sum(xv[e], -mv[e], hi, lo);
+                        dd_fma(s[e & 1], hi, lo, rw[e]);
+                    }
+                }
             }
+            dd_add(s[0], s[1]);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) {
+            for (int o = LANES / 2; o; o >>= 1) {
                 Dd y;
-                y.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
-                y.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-                dd_add(s, y);
+                y.hi = __shfl_xor_sync(0xffffffffu, s[0].hi, o);
+                y.lo = __shfl_xor_sync(0xffffffffu, s[0].lo, o);
+                dd_add(s[0], y);
             }
-            // (the butterfly adds in another order in each lane: take one lane's)
-            s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
-            s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
-            return dd_norm(s);
+            // (the butterfly adds in another order in each lane: take the group's first)
+            s[0].hi = __shfl_sync(0xffffffffu, s[0].hi, lane & ~(LANES - 1));
+            s[0].lo = __shfl_sync(0xffffffffu, s[0].lo, lane & ~(LANES - 1));
+            return dd_norm(s[0]);
         };
+        auto z_of = [&](int i, int e) { return acc[i >> 1][2 * e + (i & 1)]; };
+        if (side == 0) {
+            const float4 ca = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t]), cb = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t + 4]);
+            const float cc[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i >> 1][2 * e + (i & 1)] -= cc[i];
+        }
+        // ---- each row's parameters; the candidates of open ones go on the CTA's list
+        float mn[2], mx[2];
+        __half sh[2], mh[2];
+        uint32_t cand[2];
+        int at[2];
+        bool slow[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mn[e] = mx[e] = z_of(0, e);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                mn[e] = fminf(mn[e], z_of(i, e));
+                mx[e] = fmaxf(mx[e], z_of(i, e));
+            }
+            mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], 1));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+            mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], 2));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+            const float eps = sm.eps[r + 8 * e];
+            const bool open = int4_params_near(mn[e], mx[e], clip, eps, sh[e], mh[e]) && eps >= 0.f && sm.slot[buf][r + 8 * e] >= 0;
+            cand[e] = 0;
+            at[e] = 0;
+            slow[e] = false;
+            if (__any_sync(0xffffffffu, open)) {
+                if (open) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        cand[e] |= (uint32_t)(z_of(i, e) <= mn[e] + 2.f * eps || z_of(i, e) >= mx[e] - 2.f * eps) << i;
+                }
+                int n = __popc(cand[e]), inc = n, base = 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                if (lane == 31) base = atomicAdd(&sm.n_item, inc);
+                base = __shfl_sync(0xffffffffu, base, 31);
+                slow[e] = base + __shfl_sync(0xffffffffu, inc, 31) > PF_LIST;  // (warp-uniform)
+                at[e] = base + inc - n;
+                if (!slow[e]) {
+                    int x = at[e];
+                    for (uint32_t c = cand[e]; c; c &= c - 1) sm.item[x++] = (uint16_t)((r + 8 * e) << 7 | (32 * g + 8 * t + __ffs(c) - 1));
+                } else {
+                    for (int x = max(base, 0) + lane; x < PF_LIST; x += 32) sm.item[x] = 0;  // (the list's end stays readable)
+                }
+            }
+        }
+        __syncthreads();  // the list is complete
+        const int n_item = min(sm.n_item, PF_LIST);
+        if (n_item > 0) {
+            for (int x0 = 0; x0 < n_item; x0 += 16) {  // eight threads an item
+                const int x = x0 + (tid >> 3), it = sm.item[min(x, n_item - 1)];
+                const Dd y = exact(it >> 7, it & 127, std::integral_constant<int, 3>());
+                if (x < n_item && (lane & 7) == 0) sm.found[x] = y;
+            }
+            __syncthreads();
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = r + 8 * e;
             const bool live = sm.slot[buf][row] >= 0;
-            float z[8];
-            const float4 ca = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t]);
-            const float4 cb = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t + 4]);
-            const float cc[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = acc[i >> 1][2 * e + (i & 1)] - cc[i];
-            const float n2 = sm.n2[row] + sm.mu2;
-            const bool wild = live && int4_wild(n2);
-            const float eps = PF_EPS * (sqrtf(sm.n2[row]) + sqrtf(sm.mu2));
-            float mn = z[0], mx = z[0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) {
-                mn = fminf(mn, z[i]);
-                mx = fmaxf(mx, z[i]);
-            }
-            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            __half sh, mh;
-            const bool open = int4_params_near(mn, mx, clip, eps, sh, mh) && live && !wild;
-            // ---- groups whose parameters are open: the exact ends (every value that could be one)
-            uint32_t rows = __ballot_sync(0xffffffffu, open);
-            while (rows) {
-                const int base = (__ffs(rows) - 1) & ~3;  // the four lanes of a row agree
-                uint32_t cand = 0;
-                if ((lane & ~3) == base) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) cand |= (uint32_t)(z[i] <= mn + 2.f * eps || z[i] >= mx - 2.f * eps) << i;
-                }
+            const float eps = sm.eps[row];
+            const bool wild = live && eps < 0.f;
+            if (__any_sync(0xffffffffu, cand[e] != 0)) {
+                // the exact ends of the open groups: every value that could be one was looked at
                 Dd lo = {CUDART_INF_F, 0.f}, hi = {-CUDART_INF_F, 0.f};
-                uint32_t any = __ballot_sync(0xffffffffu, cand != 0);
-                while (any) {
-                    const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, cand, l)) - 1;
-                    const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
-                    if (dd_less(y, lo)) lo = y;
-                    if (dd_less(hi, y)) hi = y;
-                    if (lane == l) cand &= cand - 1;
-                    any = __ballot_sync(0xffffffffu, cand != 0);
+                if (!slow[e]) {
+                    for (int x = 0, n = __popc(cand[e]); x < n; ++x) {
+                        const Dd y = sm.found[at[e] + x];
+                        if (dd_less(y, lo)) lo = y;
+                        if (dd_less(hi, y)) hi = y;
+                    }
+                } else {  // the list is full: the warp takes its own candidates one by one
+                    uint32_t left = cand[e], any;
+                    while ((any = __ballot_sync(0xffffffffu, left != 0)) != 0) {
+                        const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, left, l)) - 1;
+                        const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
+                        if (lane == l) {
+                            if (dd_less(y, lo)) lo = y;
+                            if (dd_less(hi, y)) hi = y;
+                            left &= left - 1;
+                        }
+                    }
                 }
-                if ((lane & ~3) == base) int4_params(lo, hi, clip, sh, mh);
-                rows &= ~(0xfu << base);
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    const Dd a = {__shfl_xor_sync(0xffffffffu, lo.hi, o), __shfl_xor_sync(0xffffffffu, lo.lo, o)};
+                    const Dd b = {__shfl_xor_sync(0xffffffffu, hi.hi, o), __shfl_xor_sync(0xffffffffu, hi.lo, o)};
+                    if (dd_less(a, lo)) lo = a;
+                    if (dd_less(hi, b)) hi = b;
+                }
+                if (lo.hi <= hi.hi) int4_params(lo, hi, clip, sh[e], mh[e]);  // (the rows that were not open saw none)
             }
-            // ---- codes
-            const float s = __half2float(sh), m = __half2float(mh), inv = s > 0.f ? 1.f / s : 0.f;
-            uint32_t w = 0, again = 0;
+            // ---- codes: the nearest integer to (z - min) / scale within [0, 15], by adding 1.5 2^23;
+            // what it leaves of the quotient says how near a threshold is
+            const float s = __half2float(sh[e]), m = __half2float(mh[e]), inv = s > 0.f ? 1.f / s : 0.f, off = -m * inv;
+            const float most = 0.5f - inv * (eps + 0x1p-20f * (fmaxf(fabsf(mn[e]), fabsf(mx[e])) + fabsf(m) + 16.f * s));
+            constexpr float MAGIC = 12582912.f;
+            uint32_t w = 0;
+            float far = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                bool near;
-                w |= (uint32_t)int4_code_near(z[i], s, inv, m, eps, near) << (4 * i);
-                again |= (uint32_t)near << i;
+                const float y = fminf(fmaxf(fmaf(z_of(i, e), inv, off), 0.f), (float)INT4_LEVELS), n = y + MAGIC;
+                far = fmaxf(far, fabsf(y - (n - MAGIC)));
+                w |= (__float_as_uint(n) & 15u) << (4 * i);
             }
-            if (!live || wild) again = 0;
-            uint32_t any = __ballot_sync(0xffffffffu, again != 0);
-            while (any) {
-                const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, again, l)) - 1;
-                const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i);
-                if (lane == l) {
-                    // the threshold nearest to y
-                    const int n = max(0, min(INT4_LEVELS - 1, (int)rintf(fmaf(y.hi - m, inv, -0.5f))));
-                    w = (w & ~(15u << (4 * i))) | (uint32_t)int4_code(y, s, m, n) << (4 * i);
-                    again &= again - 1;
+            uint32_t any = __ballot_sync(0xffffffffu, live && !wild && s > 0.f && !(far < most));
+            if (any) {
+                uint32_t again = 0;
+                if (any >> lane & 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float y = fminf(fmaxf(fmaf(z_of(i, e), inv, off), 0.f), (float)INT4_LEVELS);
+                        again |= (uint32_t)!(fabsf(y - (y + MAGIC - MAGIC)) < most) << i;
+                    }
                 }
-                any = __ballot_sync(0xffffffffu, again != 0);
+                while ((any = __ballot_sync(0xffffffffu, again != 0)) != 0) {
+                    const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, again, l)) - 1;
+                    const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
+                    if (lane == l) {
+                        // the nearest threshold decides
+                        const float q = fmaf(y.hi - m, inv, -0.5f);
+                        const int c = q <= -0.5f ? 0 : q >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(y, s, m, (int)rintf(q));
+                        w = (w & ~(15u << (4 * i))) | (uint32_t)c << (4 * i);
+                        again &= again - 1;
+                    }
+                }
             }
             // ---- rows outside fp32's comfortable range: all in fp64
-            rows = __ballot_sync(0xffffffffu, wild);
+            uint32_t rows = __ballot_sync(0xffffffffu, wild);
             while (rows) {
                 const int base = (__ffs(rows) - 1) & ~3, rw = (base >> 2) + 8 * e;
                 double y = 0.0;  // lane = channel of the group
@@ -439,15 +533,15 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 c = __shfl_sync(0xffffffffu, c, 8 * t);  // the word of channels 8 t ..
                 if ((lane & ~3) == base) {
                     w = c;
-                    sh = a;
-                    mh = b;
+                    sh[e] = a;
+                    mh[e] = b;
                 }
                 rows &= ~(0xfu << base);
             }
             sm.word[row][t][g] = w;
             if (t == 0) {
-                sm.sc[row][g] = sh;
-                sm.mn[row][g] = mh;
+                sm.sc[row][g] = sh[e];
+                sm.mn[row][g] = mh[e];
             }
         }
         __syncthreads();  // the tile's codes are there

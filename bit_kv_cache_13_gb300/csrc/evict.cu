@@ -23,6 +23,7 @@ struct __align__(16) SelectSmem {
     int warp_sum[SEL_WARPS], warp_gt[SEL_WARPS], warp_eq[SEL_WARPS];
     int total_gt, total_eq, digit, above;
 };
+static_assert(sizeof(SelectSmem) % 16 == 0, "the keys behind it are read sixteen bytes at a time");
 
 // The same shared variable of CTA `rank` of the cluster.
 __device__ __forceinline__ int cluster_load(const int* p, int rank) {

@@ -37,25 +37,17 @@ __device__ __forceinline__ int int4_code(double z, __half sh, __half mh) {
     return c > 0.0 ? (c < (double)INT4_LEVELS ? (int)c : INT4_LEVELS) : 0;
 }
 
-// The same from fp32 values known to within eps (in absolute terms): the
-// parameters and codes, and whether an exact value could have decided otherwise.
-// Rounding to fp32 and then to fp16 is monotone, so a parameter is certain when
-// both ends of its interval round alike.
+// The parameters from fp32 ends known to within eps (in absolute terms), and
+// whether the exact ends could give others.  Rounding to fp32 and then to fp16 is
+// monotone, so they are certain when both ends of their intervals round alike (what
+// saturates counts as open).
 __device__ __forceinline__ bool int4_params_near(float mn, float mx, float clip, float eps, __half& sh, __half& mh) {
     const float s = clip * (mx - mn) * (1.f / INT4_LEVELS), m = clip * mn;
-    const float ds = clip * eps * (2.f / INT4_LEVELS) + fabsf(s) * 0x1p-21f, dm = clip * eps + fabsf(m) * 0x1p-22f;
-    sh = f16_sat_nan(s - ds);
-    mh = f16_sat_nan(m - dm);
-    return __half_as_ushort(sh) != __half_as_ushort(f16_sat_nan(s + ds)) ||
-           __half_as_ushort(mh) != __half_as_ushort(f16_sat_nan(m + dm));
-}
-
-// code of v; near: a threshold lies within eps of v.  inv = 1 / s (0 for s = 0).
-__device__ __forceinline__ int int4_code_near(float v, float s, float inv, float m, float eps, bool& near) {
-    const float q = fmaf(v - m, inv, -0.5f), n = rintf(q);
-    near = n >= 0.f && n < (float)INT4_LEVELS && fabsf(q - n) * s <= eps + (fabsf(v) + fabsf(m) + 16.f * s) * 0x1p-21f && s > 0.f;
-    const float c = fminf(fmaxf(ceilf(q), 0.f), (float)INT4_LEVELS);
-    return s > 0.f ? (int)c : 0;
+    const float ds = fmaf(clip * (2.f / INT4_LEVELS), eps, s * 0x1p-21f), dm = fmaf(clip, eps, fabsf(m) * 0x1p-22f);
+    const __half2 lo = __floats2half2_rn(s - ds, m - dm), hi = __floats2half2_rn(s + ds, m + dm);
+    sh = __low2half(lo);
+    mh = __high2half(lo);
+    return h2_as_u32(lo) != h2_as_u32(hi) || !(s + ds < 65504.f && fabsf(m) + dm < 65504.f);
 }
 
 // Unevaluated sums hi + lo of two fp32 values (about 46 bits).
