@@ -139,44 +139,50 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // ------------------------------------------------------------ prefill
 //
 // The rotation on the tensor cores.  The inputs are bf16 and so exact operands; R
-// enters as three bf16 parts (its fp32 value to 2^-25), smallest first, into one
-// fp32 accumulator, and the centre is subtracted after the rotation (z = k R - mu R,
-// mu R formed once per CTA).  A warp owns one group of 32 rotated channels and keeps
-// its part of R in 192 registers; a tile is 16 tokens, whose rows all four warps
-// read.  With the columns of the product in the order channel 8 t + 2 i + e = column
-// 2 t + e of its eight columns' set i, the accumulators of a lane are the eight codes
-// of one word of the key record.
+// enters as three bf16 parts (8 bits each: its fp32 value, exactly), smallest first,
+// into one fp32 accumulator, and the centre is subtracted after the rotation (z = k R
+// - mu R, mu R formed once per CTA).  The parts stand in shared memory in operand
+// order; one CTA per SM holds those of one (KV head, side), and its four workers of
+// four warps go their own ways through tiles of 32 tokens: warp g of a worker forms
+// group g's 32 channels of them.  With the columns of the product in the order
+// channel 8 t + 2 i + e = column 2 t + e of its eight columns' set i, the accumulators
+// of a lane are the eight codes of one word of the key record.
 //
 // |z - accumulated| <= PF_EPS (|k| + |mu|): the largest error seen was 2^-22.1 of the
 // norms (2 10^8 values of three distributions), the bound leaves a factor of four.
 // Groups or codes that the bound leaves open (about one group in twenty-five, one
-// code in ten thousand) take exact dot products by the whole warp, in pairs of fp32
-// values: fp64 is 64 times slower than fp32 here, and a first form of these second
-// looks in fp64 took most of the kernel's time (32K tokens 1.10 ms).
-constexpr int PF_M = 16;                 // tokens of a tile
+// code in ten thousand) take exact dot products in pairs of fp32 values, a worker's
+// together in one list: fp64 is 64 times slower than fp32 here, and a first form of
+// these second looks in fp64 took most of the kernel's time.
+constexpr int PF_WORKERS = 4, PF_M = 32;  // tokens of a worker's tile
 constexpr float PF_EPS = 0x1p-20f;
-constexpr int PF_LIST = 192;             // exact values of a tile (a full one sends its groups the slow way)
-constexpr int PF_RT = D + 4, PF_A = D + 8;  // padded rows, in elements
+constexpr int PF_LIST = 96;               // exact values of a tile (a full list sends its groups the slow way)
+constexpr int PF_A = D + 8;               // padded rows, in elements
 
-struct __align__(16) PrefillSmem {
-    __align__(16) float RT[D][PF_RT];    // R transposed: RT[channel][input]
+struct __align__(16) PrefillWorker {
     __align__(16) __nv_bfloat16 A[2][PF_M][PF_A];
-    __align__(16) float mu[D];           // the centre (0 for values)
-    __align__(16) float c[D];            // mu R
     __align__(16) uint32_t word[PF_M][4][4];  // the tile's codes [token][t][g]
     __align__(16) __half sc[PF_M][NGROUP];
     __align__(16) __half mn[PF_M][NGROUP];
-    __align__(16) Dd found[PF_LIST];     // exact values, of
-    uint16_t item[PF_LIST];              // row << 7 | channel
-    float eps[PF_M];                     // the bound on the rows' errors; -1: a row for fp64
+    __align__(16) Dd found[PF_LIST];          // exact values, of
+    uint16_t item[PF_LIST];                   // row << 7 | channel
+    float eps[PF_M];                          // the bound on the rows' errors; -1: a row for fp64
     int slot[2][PF_M];
-    float m2[4], mu2;
     int n_item;
 };
-static_assert(offsetof(PrefillSmem, RT) % 16 == 0 && offsetof(PrefillSmem, A) % 16 == 0 && offsetof(PrefillSmem, mu) % 16 == 0 &&
-                  offsetof(PrefillSmem, c) % 16 == 0 && offsetof(PrefillSmem, word) % 16 == 0 && offsetof(PrefillSmem, sc) % 8 == 0 &&
-                  offsetof(PrefillSmem, mn) % 8 == 0 && (PF_RT * 4) % 16 == 0 && (PF_A * 2) % 16 == 0,
+struct __align__(16) PrefillSmem {
+    __align__(16) uint2 R[3][NGROUP][4][8][32];  // parts as operands: [part][group][set][K step][lane]
+    __align__(16) float mu[D];                // the centre (0 for values)
+    __align__(16) float c[D];                 // mu R
+    float m2[4], mu2;
+    PrefillWorker w[PF_WORKERS];
+};
+static_assert(offsetof(PrefillSmem, R) % 16 == 0 && offsetof(PrefillSmem, mu) % 16 == 0 && offsetof(PrefillSmem, c) % 16 == 0 &&
+                  offsetof(PrefillSmem, w) % 16 == 0 && sizeof(PrefillWorker) % 16 == 0 && offsetof(PrefillWorker, A) % 16 == 0 &&
+                  offsetof(PrefillWorker, word) % 16 == 0 && offsetof(PrefillWorker, sc) % 8 == 0 &&
+                  offsetof(PrefillWorker, mn) % 8 == 0 && (PF_A * 2) % 16 == 0,
               "wide accesses to shared memory are aligned");
+static_assert(sizeof(PrefillSmem) <= 227 * 1024, "prefill shared memory above 227 KB");
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -188,37 +194,41 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&x);
 }
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// x = p0 + p1 + p2 + (less than 2^-25 of x), bf16 parts
+// Takes the nearest bf16 value off x.
 __device__ __forceinline__ float bf16_part(float& x) {
     const float p = __bfloat162float(__float2bfloat16_rn(x));
     x = x - p;  // exact
     return p;
 }
 
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(PF_WORKERS * 128, 1)
 append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, int n_tok, int H_kv,
                            const int32_t* __restrict__ slot_mapping, const float* __restrict__ mu,
                            const float* __restrict__ Rk, const float* __restrict__ Rv, uint8_t* __restrict__ cache,
                            int64_t num_pages, int32_t* __restrict__ err_count, float clip) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     PrefillSmem& sm = *reinterpret_cast<PrefillSmem*>(smem_raw);
-    const int h = blockIdx.y, side = blockIdx.z, tid = threadIdx.x, g = tid >> 5, lane = tid & 31;
-    const int r = lane >> 2, t = lane & 3;
+    const int h = blockIdx.y, side = blockIdx.z, worker = threadIdx.x >> 7, tid = threadIdx.x & 127;
+    const int g = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
+    PrefillWorker& wk = sm.w[worker];
     const float* R = (side ? Rv : Rk) + (size_t)h * D * D;
-    for (int l = tid; l < D * D / 32; l += 128) prefetch_l2(R + 32 * l);
+    prefetch_l2(R + 32 * threadIdx.x);  // (512 lines)
     griddep_wait();
     griddep_launch_dependents();
 
-    const int tiles = (n_tok + PF_M - 1) / PF_M;
+    const int tiles = (n_tok + PF_M - 1) / PF_M, stride = gridDim.x * PF_WORKERS;
     const __nv_bfloat16* src = side ? v : k;
     const int64_t n_slots = num_pages * PAGE;
-    auto fetch = [&](int x, int buf) {  // tile x: 256 pieces of 16 bytes, and its slots
+    auto worker_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(worker + 1) : "memory"); };
+    auto fetch = [&](int x, int buf) {  // tile x: 512 pieces of 16 bytes, and its slots
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 4; ++e) {
             const int p = tid + 128 * e, row = p >> 4, col = 8 * (p & 15);
             const int64_t tok = min((int64_t)x * PF_M + row, (int64_t)n_tok - 1);  // (rows past the end repeat the last)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.A[buf][row][col])),
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&wk.A[buf][row][col])),
                          "l"(src + ((size_t)tok * H_kv + h) * D + col)
                          : "memory");
         }
@@ -230,142 +240,139 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 if (h == 0 && side == 0 && err_count) atomicAdd(err_count, 1);
                 s = -1;
             }
-            sm.slot[buf][tid] = s;
+            wk.slot[buf][tid] = s;
         }
     };
-    if ((int)blockIdx.x < tiles) fetch(blockIdx.x, 0);
-    // R transposed: thread = input row
-#pragma unroll 8
-    for (int c4 = 0; c4 < D; c4 += 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(R + (size_t)tid * D + c4));
-        sm.RT[c4][tid] = x.x;
-        sm.RT[c4 + 1][tid] = x.y;
-        sm.RT[c4 + 2][tid] = x.z;
-        sm.RT[c4 + 3][tid] = x.w;
+    const int x_first = blockIdx.x * PF_WORKERS + worker;
+    if (x_first < tiles) fetch(x_first, 0);
+    // R's parts as operands: column n of set i of a group is channel 8 (n / 2) + 2 i + n % 2 of it
+#pragma unroll 2
+    for (int y = threadIdx.x; y < NGROUP * 4 * 8 * 32; y += PF_WORKERS * 128) {
+        const int ks = (y >> 5) & 7, i = (y >> 8) & 3, gg = y >> 10;  // (r, t: this lane's column and rows)
+        const float* p = R + (size_t)(16 * ks + 2 * t) * D + 32 * gg + 8 * (r >> 1) + 2 * i + (r & 1);
+        float a = __ldg(p), b = __ldg(p + D), c = __ldg(p + 8 * D), d = __ldg(p + 9 * D);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const float a0 = bf16_part(a), b0 = bf16_part(b), c0 = bf16_part(c), d0 = bf16_part(d);
+            sm.R[q][gg][i][ks][lane] = make_uint2(pack_bf16(a0, b0), pack_bf16(c0, d0));
+        }
     }
-    const float mu_own = side ? 0.f : __ldg(mu + (size_t)h * D + tid);
-    sm.mu[tid] = mu_own;
-    {
-        float m2 = mu_own * mu_own;
+    if (threadIdx.x < D) {
+        const float m = side ? 0.f : __ldg(mu + (size_t)h * D + threadIdx.x);
+        sm.mu[threadIdx.x] = m;
+        float m2 = m * m;
 #pragma unroll
         for (int o = 16; o; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
         if (lane == 0) sm.m2[g] = m2;
     }
     __syncthreads();
-    if (tid == 0) sm.mu2 = (sm.m2[0] + sm.m2[1]) + (sm.m2[2] + sm.m2[3]);
-    if (side == 0) {  // mu R: thread = channel
-        Dd acc[4] = {};
-#pragma unroll 4
-        for (int i = 0; i < D; i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(&sm.RT[tid][i]);
-            dd_fma(acc[0], sm.mu[i], 0.f, x.x);
-            dd_fma(acc[1], sm.mu[i + 1], 0.f, x.y);
-            dd_fma(acc[2], sm.mu[i + 2], 0.f, x.z);
-            dd_fma(acc[3], sm.mu[i + 3], 0.f, x.w);
+    // inputs 16 ks + 2 q, + 1, + 8, + 9 of channel ch's column of R, from its parts: exact sums
+    auto column = [&](int ch, int ks, int q) {
+        const int c = ch & 31, at = 4 * (2 * (c >> 3) + (c & 1)) + q;
+        const uint2 a = sm.R[0][ch >> 5][(c >> 1) & 3][ks][at], b = sm.R[1][ch >> 5][(c >> 1) & 3][ks][at],
+                    d = sm.R[2][ch >> 5][(c >> 1) & 3][ks][at];
+        return make_float4((bf16_lo(a.x) + bf16_lo(b.x)) + bf16_lo(d.x), (bf16_hi(a.x) + bf16_hi(b.x)) + bf16_hi(d.x),
+                           (bf16_lo(a.y) + bf16_lo(b.y)) + bf16_lo(d.y), (bf16_hi(a.y) + bf16_hi(b.y)) + bf16_hi(d.y));
+    };
+    if (threadIdx.x == 0) sm.mu2 = (sm.m2[0] + sm.m2[1]) + (sm.m2[2] + sm.m2[3]);
+    if (side == 0) {  // mu R: four neighbouring threads a channel
+        const int ch = threadIdx.x >> 2, q = threadIdx.x & 3;
+        Dd s[2] = {};
+#pragma unroll 2
+        for (int ks = 0; ks < 8; ++ks) {
+            const float4 x = column(ch, ks, q);
+            dd_fma(s[0], sm.mu[16 * ks + 2 * q], 0.f, x.x);
+            dd_fma(s[1], sm.mu[16 * ks + 2 * q + 1], 0.f, x.y);
+            dd_fma(s[0], sm.mu[16 * ks + 2 * q + 8], 0.f, x.z);
+            dd_fma(s[1], sm.mu[16 * ks + 2 * q + 9], 0.f, x.w);
         }
-        dd_add(acc[0], acc[1]);
-        dd_add(acc[2], acc[3]);
-        dd_add(acc[0], acc[2]);
-        sm.c[tid] = acc[0].hi + acc[0].lo;
-    } else {
-        sm.c[tid] = 0.f;
+        dd_add(s[0], s[1]);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            const Dd y = {__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)};
+            dd_add(s[0], y);
+        }
+        if (q == 0) sm.c[ch] = s[0].hi + s[0].lo;
     }
-    // this warp's channels of R as operands: column n of set i is channel 32 g + 8 (n / 2) + 2 i + n % 2
-    uint32_t bf[3][4][8][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float2 x = *reinterpret_cast<const float2*>(&sm.RT[32 * g + 8 * (r >> 1) + 2 * i + (r & 1)][16 * ks + 8 * e + 2 * t]);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    const float lo = bf16_part(x.x), hi = bf16_part(x.y);
-                    bf[p][i][ks][e] = pack_bf16(lo, hi);
-                }
-            }
+    __syncthreads();  // the last barrier of the whole CTA
 
     int buf = 0;
 #pragma unroll 1
-    for (int x = blockIdx.x; x < tiles; x += gridDim.x, buf ^= 1) {
+    for (int x = x_first; x < tiles; x += stride, buf ^= 1) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();  // the tile is there; the last one's words are written out
-        {   // norms: 8 threads a row
-            const int row = tid >> 3;
-            const uint4* p = reinterpret_cast<const uint4*>(&sm.A[buf][row][16 * (tid & 7)]);
+        worker_sync();  // the tile is there; the last one's words are written out
+        {   // norms: 4 threads a row
+            const int row = tid >> 2;
+            const uint4* p = reinterpret_cast<const uint4*>(&wk.A[buf][row][0]);
             float n2 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint4 q = p[e];
+            for (int e = 0; e < 4; ++e) {
+                const uint4 q = p[4 * e + (tid & 3)];
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float a = __uint_as_float(w[y] << 16), b = __uint_as_float(w[y] & 0xffff0000u);
-                    n2 = fmaf(a, a, fmaf(b, b, n2));
-                }
+                for (int y = 0; y < 4; ++y) n2 = fmaf(bf16_lo(w[y]), bf16_lo(w[y]), fmaf(bf16_hi(w[y]), bf16_hi(w[y]), n2));
             }
             n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
             n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
-            n2 += __shfl_xor_sync(0xffffffffu, n2, 4);
-            if ((tid & 7) == 0) sm.eps[row] = int4_wild(n2 + sm.mu2) ? -1.f : PF_EPS * (sqrtf(n2) + sqrtf(sm.mu2));
-            if (tid == 0) sm.n_item = 0;
+            if ((tid & 3) == 0) wk.eps[row] = int4_wild(n2 + sm.mu2) ? -1.f : PF_EPS * (sqrtf(n2) + sqrtf(sm.mu2));
+            if (tid == 0) wk.n_item = 0;
         }
-        if (x + (int)gridDim.x < tiles) fetch(x + gridDim.x, buf ^ 1);
+        if (x + stride < tiles) fetch(x + stride, buf ^ 1);
 
-        float acc[4][4];
+        float acc[2][4][4];  // [16 tokens][set][..]
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-        const uint32_t a_addr = smem_u32(&sm.A[buf][lane & 15][8 * (lane >> 4)]);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.f;
+        const uint32_t a_addr = smem_u32(&wk.A[buf][lane & 15][8 * (lane >> 4)]);
+#pragma unroll 1
         for (int p = 2; p >= 0; --p)
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
-                uint32_t a[4];
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
-                             : "r"(a_addr + 32 * ks));
+                uint32_t a[2][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma_bf16(acc[i], a, bf[p][i][ks][0], bf[p][i][ks][1]);
+                for (int m = 0; m < 2; ++m)
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(a[m][0]), "=r"(a[m][1]), "=r"(a[m][2]), "=r"(a[m][3])
+                                 : "r"(a_addr + 32 * ks + 16 * PF_A * 2 * m));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint2 f = sm.R[p][g][i][ks][lane];
+                    mma_bf16(acc[0][i], a[0], f.x, f.y);
+                    mma_bf16(acc[1][i], a[1], f.x, f.y);
+                }
             }
-        __syncthreads();  // the bounds are there
+        worker_sync();  // the bounds are there
 
-        // (k - mu) . R[:, ch] (or v . R) of a row: the threads of a group of 2^LOG lanes
-        // take four inputs at a time; every lane of the group gets the sum
+        // (k - mu) . R[:, ch] (or v . R) of a row: a group of 2^LOG lanes takes four inputs
+        // a lane at a time; every lane of the group gets the sum
         auto exact = [&](int row, int ch, auto log) {
             constexpr int LANES = 1 << decltype(log)::value;
-            const int q = lane & (LANES - 1);
             Dd s[2] = {};
 #pragma unroll
-            for (int x = 0; x < 32 / LANES; ++x) {
-                const int at = 4 * (LANES * x + q);
-                const uint2 raw = *reinterpret_cast<const uint2*>(&sm.A[buf][row][at]);
-                const float4 rv = *reinterpret_cast<const float4*>(&sm.RT[ch][at]);
-                const float xv[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                                     __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
-                const float rw[4] = {rv.x, rv.y, rv.z, rv.w};
-                if (side) {
+            for (int y = 0; y < 32 / LANES; ++y) {
+                const int e = LANES * y + (lane & (LANES - 1)), i0 = 16 * (e >> 2) + 2 * (e & 3);
+                const uint32_t xa = *reinterpret_cast<const uint32_t*>(&wk.A[buf][row][i0]);
+                const uint32_t xb = *reinterpret_cast<const uint32_t*>(&wk.A[buf][row][i0 + 8]);
+                const float4 rv = column(ch, e >> 2, e & 3);
+                const float xv[4] = {bf16_lo(xa), bf16_hi(xa), bf16_lo(xb), bf16_hi(xb)}, rw[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dd_fma(s[e & 1], xv[e], 0.f, rw[e]);
-                } else {
-                    const float4 m4 = *reinterpret_cast<const float4*>(&sm.mu[at]);
-                    const float mv[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                for (int q = 0; q < 4; ++q) {
+                    if (side) {
+                        dd_fma(s[q & 1], xv[q], 0.f, rw[q]);
+                    } else {
                         float hi, lo;
-                        two_sum(xv[e], -mv[e], hi, lo);
-                        dd_fma(s[e & 1], hi, lo, rw[e]);
+                        two_sum(xv[q], -sm.mu[i0 + (q & 1) + 8 * (q >> 1)], hi, lo);
+                        dd_fma(s[q & 1], hi, lo, rw[q]);
                     }
                 }
             }
             dd_add(s[0], s[1]);
 #pragma unroll
             for (int o = LANES / 2; o; o >>= 1) {
-                Dd y;
-                y.hi = __shfl_xor_sync(0xffffffffu, s[0].hi, o);
-                y.lo = __shfl_xor_sync(0xffffffffu, s[0].lo, o);
+                const Dd y = {__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)};
                 dd_add(s[0], y);
             }
             // (the butterfly adds in another order in each lane: take the group's first)
@@ -373,95 +380,97 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             s[0].lo = __shfl_sync(0xffffffffu, s[0].lo, lane & ~(LANES - 1));
             return dd_norm(s[0]);
         };
-        auto z_of = [&](int i, int e) { return acc[i >> 1][2 * e + (i & 1)]; };
+        // row set q = 2 m + e: rows 16 m + 8 e + r; its channel 32 g + 8 t + i of this lane
+        auto row_of = [&](int q) { return 16 * (q >> 1) + 8 * (q & 1) + r; };
+        auto z_of = [&](int i, int q) -> float& { return acc[q >> 1][i >> 1][2 * (q & 1) + (i & 1)]; };
         if (side == 0) {
             const float4 ca = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t]), cb = *reinterpret_cast<const float4*>(&sm.c[32 * g + 8 * t + 4]);
             const float cc[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i >> 1][2 * e + (i & 1)] -= cc[i];
+                for (int i = 0; i < 8; ++i) z_of(i, q) -= cc[i];
         }
-        // ---- each row's parameters; the candidates of open ones go on the CTA's list
-        float mn[2], mx[2];
-        __half sh[2], mh[2];
-        uint32_t cand[2];
-        int at[2];
-        bool slow[2];
+        // ---- each row's parameters; the candidates of open ones go on the worker's list
+        float top[4];            // largest magnitude of the group
+        uint32_t par[4], cand[4];  // scale and min; candidate bits, and their place on the list << 8
+        bool slow = false;       // (warp-uniform) a list that was full
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            mn[e] = mx[e] = z_of(0, e);
+        for (int q = 0; q < 4; ++q) {
+            float mn = z_of(0, q), mx = mn;
 #pragma unroll
             for (int i = 1; i < 8; ++i) {
-                mn[e] = fminf(mn[e], z_of(i, e));
-                mx[e] = fmaxf(mx[e], z_of(i, e));
+                mn = fminf(mn, z_of(i, q));
+                mx = fmaxf(mx, z_of(i, q));
             }
-            mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-            mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], 2));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-            const float eps = sm.eps[r + 8 * e];
-            const bool open = int4_params_near(mn[e], mx[e], clip, eps, sh[e], mh[e]) && eps >= 0.f && sm.slot[buf][r + 8 * e] >= 0;
-            cand[e] = 0;
-            at[e] = 0;
-            slow[e] = false;
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            top[q] = fmaxf(fabsf(mn), fabsf(mx));
+            const float eps = wk.eps[row_of(q)];
+            __half sh, mh;
+            const bool open = int4_params_near(mn, mx, clip, eps, sh, mh) && eps >= 0.f && wk.slot[buf][row_of(q)] >= 0;
+            par[q] = (uint32_t)__half_as_ushort(sh) | (uint32_t)__half_as_ushort(mh) << 16;
+            cand[q] = 0;
             if (__any_sync(0xffffffffu, open)) {
+                uint32_t c = 0;
                 if (open) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        cand[e] |= (uint32_t)(z_of(i, e) <= mn[e] + 2.f * eps || z_of(i, e) >= mx[e] - 2.f * eps) << i;
+                    for (int i = 0; i < 8; ++i) c |= (uint32_t)(z_of(i, q) <= mn + 2.f * eps || z_of(i, q) >= mx - 2.f * eps) << i;
                 }
-                int n = __popc(cand[e]), inc = n, base = 0;
+                const int n = __popc(c);
+                int inc = n, base = 0;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int y = __shfl_up_sync(0xffffffffu, inc, o);
                     if (lane >= o) inc += y;
                 }
-                if (lane == 31) base = atomicAdd(&sm.n_item, inc);
+                if (lane == 31) base = atomicAdd(&wk.n_item, inc);
                 base = __shfl_sync(0xffffffffu, base, 31);
-                slow[e] = base + __shfl_sync(0xffffffffu, inc, 31) > PF_LIST;  // (warp-uniform)
-                at[e] = base + inc - n;
-                if (!slow[e]) {
-                    int x = at[e];
-                    for (uint32_t c = cand[e]; c; c &= c - 1) sm.item[x++] = (uint16_t)((r + 8 * e) << 7 | (32 * g + 8 * t + __ffs(c) - 1));
-                } else {
-                    for (int x = max(base, 0) + lane; x < PF_LIST; x += 32) sm.item[x] = 0;  // (the list's end stays readable)
+                slow |= base + __shfl_sync(0xffffffffu, inc, 31) > PF_LIST;
+                const int at = base + inc - n;
+                cand[q] = c | (uint32_t)at << 8;
+                for (int y = 0; y < n && at + y < PF_LIST; ++y) {
+                    wk.item[at + y] = (uint16_t)(row_of(q) << 7 | (32 * g + 8 * t + __ffs(c) - 1));
+                    c &= c - 1;
                 }
             }
         }
-        __syncthreads();  // the list is complete
-        const int n_item = min(sm.n_item, PF_LIST);
+        worker_sync();  // the list is complete
+        const int n_item = min(wk.n_item, PF_LIST);
         if (n_item > 0) {
-            for (int x0 = 0; x0 < n_item; x0 += 16) {  // eight threads an item
-                const int x = x0 + (tid >> 3), it = sm.item[min(x, n_item - 1)];
-                const Dd y = exact(it >> 7, it & 127, std::integral_constant<int, 3>());
-                if (x < n_item && (lane & 7) == 0) sm.found[x] = y;
+            for (int x0 = 0; x0 < n_item; x0 += 8) {  // sixteen threads an item
+                const int y = x0 + (tid >> 4), it = wk.item[min(y, n_item - 1)];
+                const Dd z = exact(it >> 7, it & 127, std::integral_constant<int, 4>());
+                if (y < n_item && (lane & 15) == 0) wk.found[y] = z;
             }
-            __syncthreads();
+            worker_sync();
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = r + 8 * e;
-            const bool live = sm.slot[buf][row] >= 0;
-            const float eps = sm.eps[row];
+        for (int q = 0; q < 4; ++q) {
+            const int row = row_of(q);
+            const bool live = wk.slot[buf][row] >= 0;
+            const float eps = wk.eps[row];
             const bool wild = live && eps < 0.f;
-            if (__any_sync(0xffffffffu, cand[e] != 0)) {
+            __half sh = __ushort_as_half((unsigned short)par[q]), mh = __ushort_as_half((unsigned short)(par[q] >> 16));
+            if (__any_sync(0xffffffffu, (cand[q] & 255) != 0)) {
                 // the exact ends of the open groups: every value that could be one was looked at
                 Dd lo = {CUDART_INF_F, 0.f}, hi = {-CUDART_INF_F, 0.f};
-                if (!slow[e]) {
-                    for (int x = 0, n = __popc(cand[e]); x < n; ++x) {
-                        const Dd y = sm.found[at[e] + x];
-                        if (dd_less(y, lo)) lo = y;
-                        if (dd_less(hi, y)) hi = y;
+                if (!slow) {
+                    for (int y = 0, n = __popc(cand[q] & 255); y < n; ++y) {
+                        const Dd z = wk.found[(cand[q] >> 8) + y];
+                        if (dd_less(z, lo)) lo = z;
+                        if (dd_less(hi, z)) hi = z;
                     }
-                } else {  // the list is full: the warp takes its own candidates one by one
-                    uint32_t left = cand[e], any;
+                } else {  // the warp takes its own candidates one by one
+                    uint32_t left = cand[q] & 255, any;
                     while ((any = __ballot_sync(0xffffffffu, left != 0)) != 0) {
                         const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, left, l)) - 1;
-                        const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
+                        const Dd z = exact(row - r + (l >> 2), 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
                         if (lane == l) {
-                            if (dd_less(y, lo)) lo = y;
-                            if (dd_less(hi, y)) hi = y;
+                            if (dd_less(z, lo)) lo = z;
+                            if (dd_less(hi, z)) hi = z;
                             left &= left - 1;
                         }
                     }
@@ -473,18 +482,18 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                     if (dd_less(a, lo)) lo = a;
                     if (dd_less(hi, b)) hi = b;
                 }
-                if (lo.hi <= hi.hi) int4_params(lo, hi, clip, sh[e], mh[e]);  // (the rows that were not open saw none)
+                if (lo.hi <= hi.hi) int4_params(lo, hi, clip, sh, mh);  // (the rows that were not open saw none)
             }
             // ---- codes: the nearest integer to (z - min) / scale within [0, 15], by adding 1.5 2^23;
             // what it leaves of the quotient says how near a threshold is
-            const float s = __half2float(sh[e]), m = __half2float(mh[e]), inv = s > 0.f ? 1.f / s : 0.f, off = -m * inv;
-            const float most = 0.5f - inv * (eps + 0x1p-20f * (fmaxf(fabsf(mn[e]), fabsf(mx[e])) + fabsf(m) + 16.f * s));
+            const float s = __half2float(sh), m = __half2float(mh), inv = s > 0.f ? 1.f / s : 0.f, off = -m * inv;
+            const float most = 0.5f - inv * (eps + 0x1p-20f * (top[q] + fabsf(m) + 16.f * s));
             constexpr float MAGIC = 12582912.f;
             uint32_t w = 0;
             float far = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float y = fminf(fmaxf(fmaf(z_of(i, e), inv, off), 0.f), (float)INT4_LEVELS), n = y + MAGIC;
+                const float y = fminf(fmaxf(fmaf(z_of(i, q), inv, off), 0.f), (float)INT4_LEVELS), n = y + MAGIC;
                 far = fmaxf(far, fabsf(y - (n - MAGIC)));
                 w |= (__float_as_uint(n) & 15u) << (4 * i);
             }
@@ -494,17 +503,17 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 if (any >> lane & 1) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float y = fminf(fmaxf(fmaf(z_of(i, e), inv, off), 0.f), (float)INT4_LEVELS);
+                        const float y = fminf(fmaxf(fmaf(z_of(i, q), inv, off), 0.f), (float)INT4_LEVELS);
                         again |= (uint32_t)!(fabsf(y - (y + MAGIC - MAGIC)) < most) << i;
                     }
                 }
                 while ((any = __ballot_sync(0xffffffffu, again != 0)) != 0) {
                     const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, again, l)) - 1;
-                    const Dd y = exact((l >> 2) + 8 * e, 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
+                    const Dd y = exact(row - r + (l >> 2), 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
                     if (lane == l) {
                         // the nearest threshold decides
-                        const float q = fmaf(y.hi - m, inv, -0.5f);
-                        const int c = q <= -0.5f ? 0 : q >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(y, s, m, (int)rintf(q));
+                        const float z = fmaf(y.hi - m, inv, -0.5f);
+                        const int c = z <= -0.5f ? 0 : z >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(y, s, m, (int)rintf(z));
                         w = (w & ~(15u << (4 * i))) | (uint32_t)c << (4 * i);
                         again &= again - 1;
                     }
@@ -513,10 +522,17 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             // ---- rows outside fp32's comfortable range: all in fp64
             uint32_t rows = __ballot_sync(0xffffffffu, wild);
             while (rows) {
-                const int base = (__ffs(rows) - 1) & ~3, rw = (base >> 2) + 8 * e;
+                const int base = (__ffs(rows) - 1) & ~3, rw = row - r + (base >> 2);
                 double y = 0.0;  // lane = channel of the group
-                for (int i = 0; i < D; ++i)
-                    y = fma((double)__bfloat162float(sm.A[buf][rw][i]) - (double)sm.mu[i], (double)sm.RT[32 * g + lane][i], y);
+#pragma unroll 1
+                for (int e = 0; e < 32; ++e) {
+                    const float4 rv = column(32 * g + lane, e >> 2, e & 3);
+                    const int i0 = 16 * (e >> 2) + 2 * (e & 3);
+                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0]) - (double)sm.mu[i0], (double)rv.x, y);
+                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0 + 1]) - (double)sm.mu[i0 + 1], (double)rv.y, y);
+                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0 + 8]) - (double)sm.mu[i0 + 8], (double)rv.z, y);
+                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0 + 9]) - (double)sm.mu[i0 + 9], (double)rv.w, y);
+                }
                 double lo = y, hi = y;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) {
@@ -533,61 +549,62 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 c = __shfl_sync(0xffffffffu, c, 8 * t);  // the word of channels 8 t ..
                 if ((lane & ~3) == base) {
                     w = c;
-                    sh[e] = a;
-                    mh[e] = b;
+                    sh = a;
+                    mh = b;
                 }
                 rows &= ~(0xfu << base);
             }
-            sm.word[row][t][g] = w;
+            wk.word[row][t][g] = w;
             if (t == 0) {
-                sm.sc[row][g] = sh[e];
-                sm.mn[row][g] = mh[e];
+                wk.sc[row][g] = sh;
+                wk.mn[row][g] = mh;
             }
         }
-        __syncthreads();  // the tile's codes are there
+        worker_sync();  // the tile's codes are there
         if (!side) {
             // a token's record: four pieces of codes and one of meta, 16 bytes each
-            if (tid < 5 * PF_M) {
-                const int row = tid / 5, piece = tid % 5, slot = sm.slot[buf][row];
-                if (slot >= 0) {
-                    uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
-                    const int s = slot % PAGE;
-                    if (piece < 4) {
-                        *reinterpret_cast<uint4*>(tile + O4_KC + 64 * s + 16 * piece) = *reinterpret_cast<const uint4*>(sm.word[row][piece]);
-                    } else {
-                        const uint2 a = *reinterpret_cast<const uint2*>(sm.sc[row]), b = *reinterpret_cast<const uint2*>(sm.mn[row]);
-                        *reinterpret_cast<uint4*>(tile + O4_KM + 16 * s) = make_uint4(a.x, a.y, b.x, b.y);
-                    }
+            for (int y = tid; y < 5 * PF_M; y += 128) {
+                const int row = y / 5, piece = y % 5, slot = wk.slot[buf][row];
+                if (slot < 0) continue;
+                uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
+                const int s = slot % PAGE;
+                if (piece < 4) {
+                    *reinterpret_cast<uint4*>(tile + O4_KC + 64 * s + 16 * piece) = *reinterpret_cast<const uint4*>(wk.word[row][piece]);
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2*>(wk.sc[row]), b = *reinterpret_cast<const uint2*>(wk.mn[row]);
+                    *reinterpret_cast<uint4*>(tile + O4_KM + 16 * s) = make_uint4(a.x, a.y, b.x, b.y);
                 }
             }
         } else {
             // token pair (2 j, 2 j + 1) of the tile in the two slots of one pair: whole words
             // (thread = eighth of a pair row: channels 32 g + 4 q ..); else halves
-            const int j = tid >> 4, q = tid & 15;
-            const int sa = sm.slot[buf][2 * j], sb = sm.slot[buf][2 * j + 1];
-            const bool pair = sa >= 0 && !(sa & 1) && sb == sa + 1;
-            if (pair) {
-                uint8_t* tile = cache + ((size_t)(sa / PAGE) * H_kv + h) * INT4_TILE;
-                const int s = (sa % PAGE) >> 1;
-                if (q < 8) {
-                    uint32_t out[4];
-                    const uint32_t sel = q & 1 ? 0x7632 : 0x5410;
 #pragma unroll
-                    for (int gg = 0; gg < 4; ++gg) out[gg] = prmt(sm.word[2 * j][q >> 1][gg], sm.word[2 * j + 1][q >> 1][gg], sel);
-                    *reinterpret_cast<uint4*>(tile + O4_VC + 128 * s + 16 * q) = make_uint4(out[0], out[1], out[2], out[3]);
-                } else if (q < 10) {
-                    const __half(*src2)[NGROUP] = q == 8 ? sm.sc : sm.mn;
-                    const uint2 a = *reinterpret_cast<const uint2*>(src2[2 * j]), b = *reinterpret_cast<const uint2*>(src2[2 * j + 1]);
-                    *reinterpret_cast<uint4*>(tile + (q == 8 ? O4_VS : O4_VM) + 16 * s) =
-                        make_uint4(prmt(a.x, b.x, 0x5410), prmt(a.x, b.x, 0x7632), prmt(a.y, b.y, 0x5410), prmt(a.y, b.y, 0x7632));
-                }
-            } else {
-                for (int e = 0; e < 2; ++e) {
-                    const int slot = e ? sb : sa, row = 2 * j + e;
-                    if (slot < 0) continue;
-                    uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
-                    store_word(tile, 1, slot % PAGE, q & 3, q >> 2, sm.word[row][q >> 2][q & 3]);
-                    if (q < NGROUP) store_meta(tile, 1, slot % PAGE, q, sm.sc[row][q], sm.mn[row][q]);
+            for (int rep = 0; rep < 2; ++rep) {
+                const int j = 8 * rep + (tid >> 4), q = tid & 15;
+                const int sa = wk.slot[buf][2 * j], sb = wk.slot[buf][2 * j + 1];
+                if (sa >= 0 && !(sa & 1) && sb == sa + 1) {
+                    uint8_t* tile = cache + ((size_t)(sa / PAGE) * H_kv + h) * INT4_TILE;
+                    const int s = (sa % PAGE) >> 1;
+                    if (q < 8) {
+                        uint32_t out[4];
+                        const uint32_t sel = q & 1 ? 0x7632 : 0x5410;
+#pragma unroll
+                        for (int gg = 0; gg < 4; ++gg) out[gg] = prmt(wk.word[2 * j][q >> 1][gg], wk.word[2 * j + 1][q >> 1][gg], sel);
+                        *reinterpret_cast<uint4*>(tile + O4_VC + 128 * s + 16 * q) = make_uint4(out[0], out[1], out[2], out[3]);
+                    } else if (q < 10) {
+                        const __half(*from)[NGROUP] = q == 8 ? wk.sc : wk.mn;
+                        const uint2 a = *reinterpret_cast<const uint2*>(from[2 * j]), b = *reinterpret_cast<const uint2*>(from[2 * j + 1]);
+                        *reinterpret_cast<uint4*>(tile + (q == 8 ? O4_VS : O4_VM) + 16 * s) =
+                            make_uint4(prmt(a.x, b.x, 0x5410), prmt(a.x, b.x, 0x7632), prmt(a.y, b.y, 0x5410), prmt(a.y, b.y, 0x7632));
+                    }
+                } else {
+                    for (int e = 0; e < 2; ++e) {
+                        const int slot = e ? sb : sa, row = 2 * j + e;
+                        if (slot < 0) continue;
+                        uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
+                        store_word(tile, 1, slot % PAGE, q & 3, q >> 2, wk.word[row][q >> 2][q & 3]);
+                        if (q < NGROUP) store_meta(tile, 1, slot % PAGE, q, wk.sc[row][q], wk.mn[row][q]);
+                    }
                 }
             }
         }
@@ -699,9 +716,11 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
                               "kvq_append_int4 launch");
     const kvq_status sa = prefill_smem_once();
     if (sa != KVQ_OK) return sa;
-    // two CTAs per SM in all, each with a stride of its (head, side)'s tiles
-    const int tiles = (n_tok + PF_M - 1) / PF_M, most = (2 * kvq_device_sm_count() + 2 * H_kv - 1) / (2 * H_kv);
-    return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(tiles < most ? tiles : most, H_kv, 2), dim3(128),
+    // one CTA per SM in all, each with a stride of its (head, side)'s tiles
+    const int tiles = (n_tok + PF_M - 1) / PF_M, want = (tiles + PF_WORKERS - 1) / PF_WORKERS;
+    int most = kvq_device_sm_count() / (2 * H_kv);
+    most = most < 1 ? 1 : most;
+    return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(want < most ? want : most, H_kv, 2), dim3(PF_WORKERS * 128),
                                      sizeof(PrefillSmem), st, kb, vb, n_tok, H_kv, slot_mapping, mu_k, R_k, R_v, cb, num_pages,
                                      err_count, clip),
                           "kvq_append_int4 launch");
