@@ -204,6 +204,72 @@ __device__ __forceinline__ float bf16_part(float& x) {
     return p;
 }
 
+// Inputs 16 ks + 2 q, + 1, + 8, + 9 of channel ch's column of R, from its parts: exact sums.
+__device__ __forceinline__ float4 prefill_column(const PrefillSmem& sm, int ch, int ks, int q) {
+    const int c = ch & 31, at = 4 * (2 * (c >> 3) + (c & 1)) + q;
+    const uint2 a = sm.R[0][ch >> 5][(c >> 1) & 3][ks][at], b = sm.R[1][ch >> 5][(c >> 1) & 3][ks][at],
+                d = sm.R[2][ch >> 5][(c >> 1) & 3][ks][at];
+    return make_float4((bf16_lo(a.x) + bf16_lo(b.x)) + bf16_lo(d.x), (bf16_hi(a.x) + bf16_hi(b.x)) + bf16_hi(d.x),
+                       (bf16_lo(a.y) + bf16_lo(b.y)) + bf16_lo(d.y), (bf16_hi(a.y) + bf16_hi(b.y)) + bf16_hi(d.y));
+}
+
+// (k - mu) . R[:, ch] (or v . R) of a row A: sixteen lanes, two times four inputs each;
+// all of them get the sum.  (Not inlined: the kernel's loop has to stay within the
+// instruction cache.  With these sums and the fp64 path unrolled into it, a warp waited
+// 4.4 cycles for each instruction's fetch.)
+__device__ __noinline__ Dd prefill_exact(const PrefillSmem& sm, const __nv_bfloat16* A, int ch, bool centred) {
+    const int lane = threadIdx.x & 31;
+    Dd s[2] = {};
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int e = 16 * y + (lane & 15), i0 = 16 * (e >> 2) + 2 * (e & 3);
+        const uint32_t xa = *reinterpret_cast<const uint32_t*>(A + i0), xb = *reinterpret_cast<const uint32_t*>(A + i0 + 8);
+        const float4 rv = prefill_column(sm, ch, e >> 2, e & 3);
+        const float xv[4] = {bf16_lo(xa), bf16_hi(xa), bf16_lo(xb), bf16_hi(xb)}, rw[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float hi = xv[q], lo = 0.f;
+            if (centred) two_sum(xv[q], -sm.mu[i0 + (q & 1) + 8 * (q >> 1)], hi, lo);
+            dd_fma(s[q & 1], hi, lo, rw[q]);
+        }
+    }
+    dd_add(s[0], s[1]);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+        const Dd y = {__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)};
+        dd_add(s[0], y);
+    }
+    // (the butterfly adds in another order in each lane: take the group's first)
+    s[0].hi = __shfl_sync(0xffffffffu, s[0].hi, lane & 16);
+    s[0].lo = __shfl_sync(0xffffffffu, s[0].lo, lane & 16);
+    return dd_norm(s[0]);
+}
+
+// A row all in fp64, lane = channel of group g: its code, scale and min.
+__device__ __noinline__ int prefill_wild(const PrefillSmem& sm, const __nv_bfloat16* A, int g, float clip, __half& sh, __half& mh) {
+    double y = 0.0;
+#pragma unroll 1
+    for (int e = 0; e < 32; ++e) {
+        const float4 rv = prefill_column(sm, 32 * g + (threadIdx.x & 31), e >> 2, e & 3);
+        const int i0 = 16 * (e >> 2) + 2 * (e & 3);
+        const float rw[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + (q & 1) + 8 * (q >> 1);
+            y = fma((double)__bfloat162float(A[i]) - (double)sm.mu[i], (double)rw[q], y);
+        }
+    }
+    double lo = y, hi = y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    if (__any_sync(0xffffffffu, !isfinite(y))) lo = hi = CUDART_NAN;
+    int4_params(lo, hi, (double)clip, sh, mh);
+    return int4_code(y, sh, mh);
+}
+
 __global__ void __launch_bounds__(PF_WORKERS * 128, 1)
 append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, int n_tok, int H_kv,
                            const int32_t* __restrict__ slot_mapping, const float* __restrict__ mu,
@@ -266,21 +332,13 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         if (lane == 0) sm.m2[g] = m2;
     }
     __syncthreads();
-    // inputs 16 ks + 2 q, + 1, + 8, + 9 of channel ch's column of R, from its parts: exact sums
-    auto column = [&](int ch, int ks, int q) {
-        const int c = ch & 31, at = 4 * (2 * (c >> 3) + (c & 1)) + q;
-        const uint2 a = sm.R[0][ch >> 5][(c >> 1) & 3][ks][at], b = sm.R[1][ch >> 5][(c >> 1) & 3][ks][at],
-                    d = sm.R[2][ch >> 5][(c >> 1) & 3][ks][at];
-        return make_float4((bf16_lo(a.x) + bf16_lo(b.x)) + bf16_lo(d.x), (bf16_hi(a.x) + bf16_hi(b.x)) + bf16_hi(d.x),
-                           (bf16_lo(a.y) + bf16_lo(b.y)) + bf16_lo(d.y), (bf16_hi(a.y) + bf16_hi(b.y)) + bf16_hi(d.y));
-    };
     if (threadIdx.x == 0) sm.mu2 = (sm.m2[0] + sm.m2[1]) + (sm.m2[2] + sm.m2[3]);
     if (side == 0) {  // mu R: four neighbouring threads a channel
         const int ch = threadIdx.x >> 2, q = threadIdx.x & 3;
         Dd s[2] = {};
 #pragma unroll 2
         for (int ks = 0; ks < 8; ++ks) {
-            const float4 x = column(ch, ks, q);
+            const float4 x = prefill_column(sm, ch, ks, q);
             dd_fma(s[0], sm.mu[16 * ks + 2 * q], 0.f, x.x);
             dd_fma(s[1], sm.mu[16 * ks + 2 * q + 1], 0.f, x.y);
             dd_fma(s[0], sm.mu[16 * ks + 2 * q + 8], 0.f, x.z);
@@ -346,40 +404,6 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             }
         worker_sync();  // the bounds are there
 
-        // (k - mu) . R[:, ch] (or v . R) of a row: a group of 2^LOG lanes takes four inputs
-        // a lane at a time; every lane of the group gets the sum
-        auto exact = [&](int row, int ch, auto log) {
-            constexpr int LANES = 1 << decltype(log)::value;
-            Dd s[2] = {};
-#pragma unroll
-            for (int y = 0; y < 32 / LANES; ++y) {
-                const int e = LANES * y + (lane & (LANES - 1)), i0 = 16 * (e >> 2) + 2 * (e & 3);
-                const uint32_t xa = *reinterpret_cast<const uint32_t*>(&wk.A[buf][row][i0]);
-                const uint32_t xb = *reinterpret_cast<const uint32_t*>(&wk.A[buf][row][i0 + 8]);
-                const float4 rv = column(ch, e >> 2, e & 3);
-                const float xv[4] = {bf16_lo(xa), bf16_hi(xa), bf16_lo(xb), bf16_hi(xb)}, rw[4] = {rv.x, rv.y, rv.z, rv.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (side) {
-                        dd_fma(s[q & 1], xv[q], 0.f, rw[q]);
-                    } else {
-                        float hi, lo;
-                        two_sum(xv[q], -sm.mu[i0 + (q & 1) + 8 * (q >> 1)], hi, lo);
-                        dd_fma(s[q & 1], hi, lo, rw[q]);
-                    }
-                }
-            }
-            dd_add(s[0], s[1]);
-#pragma unroll
-            for (int o = LANES / 2; o; o >>= 1) {
-                const Dd y = {__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)};
-                dd_add(s[0], y);
-            }
-            // (the butterfly adds in another order in each lane: take the group's first)
-            s[0].hi = __shfl_sync(0xffffffffu, s[0].hi, lane & ~(LANES - 1));
-            s[0].lo = __shfl_sync(0xffffffffu, s[0].lo, lane & ~(LANES - 1));
-            return dd_norm(s[0]);
-        };
         // row set q = 2 m + e: rows 16 m + 8 e + r; its channel 32 g + 8 t + i of this lane
         auto row_of = [&](int q) { return 16 * (q >> 1) + 8 * (q & 1) + r; };
         auto z_of = [&](int i, int q) -> float& { return acc[q >> 1][i >> 1][2 * (q & 1) + (i & 1)]; };
@@ -392,9 +416,9 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 for (int i = 0; i < 8; ++i) z_of(i, q) -= cc[i];
         }
         // ---- each row's parameters; the candidates of open ones go on the worker's list
-        float top[4];            // largest magnitude of the group
-        uint32_t par[4], cand[4];  // scale and min; candidate bits, and their place on the list << 8
-        bool slow = false;       // (warp-uniform) a list that was full
+        float top[4];                 // largest magnitude of the group
+        uint32_t cands = 0, places = 0;  // candidate bits and their place on the list (255: not on it), a byte per row set
+        bool any_open = false;        // (warp-uniform)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float mn = z_of(0, q), mx = mn;
@@ -411,8 +435,10 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             const float eps = wk.eps[row_of(q)];
             __half sh, mh;
             const bool open = int4_params_near(mn, mx, clip, eps, sh, mh) && eps >= 0.f && wk.slot[buf][row_of(q)] >= 0;
-            par[q] = (uint32_t)__half_as_ushort(sh) | (uint32_t)__half_as_ushort(mh) << 16;
-            cand[q] = 0;
+            if (t == 0) {
+                wk.sc[row_of(q)][g] = sh;
+                wk.mn[row_of(q)][g] = mh;
+            }
             if (__any_sync(0xffffffffu, open)) {
                 uint32_t c = 0;
                 if (open) {
@@ -428,9 +454,10 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 }
                 if (lane == 31) base = atomicAdd(&wk.n_item, inc);
                 base = __shfl_sync(0xffffffffu, base, 31);
-                slow |= base + __shfl_sync(0xffffffffu, inc, 31) > PF_LIST;
+                any_open = true;
                 const int at = base + inc - n;
-                cand[q] = c | (uint32_t)at << 8;
+                cands |= c << (8 * q);
+                places |= (uint32_t)(at + n <= PF_LIST ? at : 255) << (8 * q);
                 for (int y = 0; y < n && at + y < PF_LIST; ++y) {
                     wk.item[at + y] = (uint16_t)(row_of(q) << 7 | (32 * g + 8 * t + __ffs(c) - 1));
                     c &= c - 1;
@@ -440,53 +467,61 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         worker_sync();  // the list is complete
         const int n_item = min(wk.n_item, PF_LIST);
         if (n_item > 0) {
+#pragma unroll 1
             for (int x0 = 0; x0 < n_item; x0 += 8) {  // sixteen threads an item
                 const int y = x0 + (tid >> 4), it = wk.item[min(y, n_item - 1)];
-                const Dd z = exact(it >> 7, it & 127, std::integral_constant<int, 4>());
+                const Dd z = prefill_exact(sm, wk.A[buf][it >> 7], it & 127, !side);
                 if (y < n_item && (lane & 15) == 0) wk.found[y] = z;
             }
             worker_sync();
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int row = row_of(q);
-            const bool live = wk.slot[buf][row] >= 0;
-            const float eps = wk.eps[row];
-            const bool wild = live && eps < 0.f;
-            __half sh = __ushort_as_half((unsigned short)par[q]), mh = __ushort_as_half((unsigned short)(par[q] >> 16));
-            if (__any_sync(0xffffffffu, (cand[q] & 255) != 0)) {
-                // the exact ends of the open groups: every value that could be one was looked at
+        if (any_open) {  // the exact ends of the open groups: every value that could be one was looked at
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t c = cands >> (8 * q) & 255;
+                const int place = places >> (8 * q) & 255, row0 = row_of(q) - r;
+                if (!__any_sync(0xffffffffu, c != 0)) continue;
                 Dd lo = {CUDART_INF_F, 0.f}, hi = {-CUDART_INF_F, 0.f};
-                if (!slow) {
-                    for (int y = 0, n = __popc(cand[q] & 255); y < n; ++y) {
-                        const Dd z = wk.found[(cand[q] >> 8) + y];
+                if (place != 255)
+                    for (int y = 0, n = __popc(c); y < n; ++y) {
+                        const Dd z = wk.found[place + y];
                         if (dd_less(z, lo)) lo = z;
                         if (dd_less(hi, z)) hi = z;
                     }
-                } else {  // the warp takes its own candidates one by one
-                    uint32_t left = cand[q] & 255, any;
-                    while ((any = __ballot_sync(0xffffffffu, left != 0)) != 0) {
-                        const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, left, l)) - 1;
-                        const Dd z = exact(row - r + (l >> 2), 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
-                        if (lane == l) {
-                            if (dd_less(z, lo)) lo = z;
-                            if (dd_less(hi, z)) hi = z;
-                            left &= left - 1;
-                        }
+                uint32_t left = place == 255 ? c : 0, any;  // not on the list: the warp takes them one by one
+                while ((any = __ballot_sync(0xffffffffu, left != 0)) != 0) {
+                    const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, left, l)) - 1;
+                    const Dd z = prefill_exact(sm, wk.A[buf][row0 + (l >> 2)], 32 * g + 8 * (l & 3) + i, !side);
+                    if (lane == l) {
+                        if (dd_less(z, lo)) lo = z;
+                        if (dd_less(hi, z)) hi = z;
+                        left &= left - 1;
                     }
                 }
 #pragma unroll
                 for (int o = 1; o < 4; o <<= 1) {
-                    const Dd a = {__shfl_xor_sync(0xffffffffu, lo.hi, o), __shfl_xor_sync(0xffffffffu, lo.lo, o)};
-                    const Dd b = {__shfl_xor_sync(0xffffffffu, hi.hi, o), __shfl_xor_sync(0xffffffffu, hi.lo, o)};
-                    if (dd_less(a, lo)) lo = a;
-                    if (dd_less(hi, b)) hi = b;
+                    const Dd x = {__shfl_xor_sync(0xffffffffu, lo.hi, o), __shfl_xor_sync(0xffffffffu, lo.lo, o)};
+                    const Dd y = {__shfl_xor_sync(0xffffffffu, hi.hi, o), __shfl_xor_sync(0xffffffffu, hi.lo, o)};
+                    if (dd_less(x, lo)) lo = x;
+                    if (dd_less(hi, y)) hi = y;
                 }
-                if (lo.hi <= hi.hi) int4_params(lo, hi, clip, sh, mh);  // (the rows that were not open saw none)
+                if (t == 0 && lo.hi <= hi.hi) {  // (the rows that were not open saw none)
+                    __half sh, mh;
+                    int4_params(lo, hi, clip, sh, mh);
+                    wk.sc[row0 + r][g] = sh;
+                    wk.mn[row0 + r][g] = mh;
+                }
             }
+        }
+        __syncwarp();  // (a warp's parameters are its own)
+        uint32_t agains = 0, wilds = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int row = row_of(q);
+            const float eps = wk.eps[row];
             // ---- codes: the nearest integer to (z - min) / scale within [0, 15], by adding 1.5 2^23;
             // what it leaves of the quotient says how near a threshold is
-            const float s = __half2float(sh), m = __half2float(mh), inv = s > 0.f ? 1.f / s : 0.f, off = -m * inv;
+            const float s = __half2float(wk.sc[row][g]), m = __half2float(wk.mn[row][g]), inv = s > 0.f ? 1.f / s : 0.f, off = -m * inv;
             const float most = 0.5f - inv * (eps + 0x1p-20f * (top[q] + fabsf(m) + 16.f * s));
             constexpr float MAGIC = 12582912.f;
             uint32_t w = 0;
@@ -497,67 +532,48 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 far = fmaxf(far, fabsf(y - (n - MAGIC)));
                 w |= (__float_as_uint(n) & 15u) << (4 * i);
             }
-            uint32_t any = __ballot_sync(0xffffffffu, live && !wild && s > 0.f && !(far < most));
-            if (any) {
-                uint32_t again = 0;
-                if (any >> lane & 1) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float y = fminf(fmaxf(fmaf(z_of(i, q), inv, off), 0.f), (float)INT4_LEVELS);
-                        again |= (uint32_t)!(fabsf(y - (y + MAGIC - MAGIC)) < most) << i;
-                    }
-                }
-                while ((any = __ballot_sync(0xffffffffu, again != 0)) != 0) {
-                    const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, again, l)) - 1;
-                    const Dd y = exact(row - r + (l >> 2), 32 * g + 8 * (l & 3) + i, std::integral_constant<int, 5>());
-                    if (lane == l) {
-                        // the nearest threshold decides
-                        const float z = fmaf(y.hi - m, inv, -0.5f);
-                        const int c = z <= -0.5f ? 0 : z >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(y, s, m, (int)rintf(z));
-                        w = (w & ~(15u << (4 * i))) | (uint32_t)c << (4 * i);
-                        again &= again - 1;
-                    }
-                }
-            }
-            // ---- rows outside fp32's comfortable range: all in fp64
-            uint32_t rows = __ballot_sync(0xffffffffu, wild);
-            while (rows) {
-                const int base = (__ffs(rows) - 1) & ~3, rw = row - r + (base >> 2);
-                double y = 0.0;  // lane = channel of the group
-#pragma unroll 1
-                for (int e = 0; e < 32; ++e) {
-                    const float4 rv = column(32 * g + lane, e >> 2, e & 3);
-                    const int i0 = 16 * (e >> 2) + 2 * (e & 3);
-                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0]) - (double)sm.mu[i0], (double)rv.x, y);
-                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0 + 1]) - (double)sm.mu[i0 + 1], (double)rv.y, y);
-                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0 + 8]) - (double)sm.mu[i0 + 8], (double)rv.z, y);
-                    y = fma((double)__bfloat162float(wk.A[buf][rw][i0 + 9]) - (double)sm.mu[i0 + 9], (double)rv.w, y);
-                }
-                double lo = y, hi = y;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                    hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                }
-                if (__any_sync(0xffffffffu, !isfinite(y))) lo = hi = CUDART_NAN;
-                __half a, b;
-                int4_params(lo, hi, (double)clip, a, b);
-                uint32_t c = (uint32_t)int4_code(y, a, b) << (4 * (lane & 7));
-                c |= __shfl_xor_sync(0xffffffffu, c, 1);
-                c |= __shfl_xor_sync(0xffffffffu, c, 2);
-                c |= __shfl_xor_sync(0xffffffffu, c, 4);
-                c = __shfl_sync(0xffffffffu, c, 8 * t);  // the word of channels 8 t ..
-                if ((lane & ~3) == base) {
-                    w = c;
-                    sh = a;
-                    mh = b;
-                }
-                rows &= ~(0xfu << base);
-            }
             wk.word[row][t][g] = w;
-            if (t == 0) {
-                wk.sc[row][g] = sh;
-                wk.mn[row][g] = mh;
+            const bool live = wk.slot[buf][row] >= 0;
+            wilds |= (uint32_t)(live && eps < 0.f) << q;
+            if (live && eps >= 0.f && s > 0.f && !(far < most)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = fminf(fmaxf(fmaf(z_of(i, q), inv, off), 0.f), (float)INT4_LEVELS);
+                    agains |= (uint32_t)!(fabsf(y - (y + MAGIC - MAGIC)) < most) << (8 * q + i);
+                }
+            }
+        }
+        // ---- codes that a threshold is near to: the exact value and the nearest threshold
+        uint32_t any;
+#pragma unroll 1
+        while ((any = __ballot_sync(0xffffffffu, agains != 0)) != 0) {
+            const int l = __ffs(any) - 1, bit = __ffs(__shfl_sync(0xffffffffu, agains, l)) - 1, q = bit >> 3, i = bit & 7;
+            const int row = row_of(q) - r + (l >> 2);
+            const Dd y = prefill_exact(sm, wk.A[buf][row], 32 * g + 8 * (l & 3) + i, !side);
+            if (lane == l) {
+                const float s = __half2float(wk.sc[row][g]), m = __half2float(wk.mn[row][g]), z = fmaf(y.hi - m, 1.f / s, -0.5f);
+                const int c = z <= -0.5f ? 0 : z >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(y, s, m, (int)rintf(z));
+                wk.word[row][t][g] = (wk.word[row][t][g] & ~(15u << (4 * i))) | (uint32_t)c << (4 * i);
+                agains &= agains - 1;
+            }
+        }
+        // ---- rows outside fp32's comfortable range: all in fp64
+#pragma unroll 1
+        while ((any = __ballot_sync(0xffffffffu, wilds != 0)) != 0) {
+            const int l = __ffs(any) - 1, q = __ffs(__shfl_sync(0xffffffffu, wilds, l)) - 1, row = row_of(q) - r + (l >> 2);
+            __half sh, mh;
+            uint32_t c = (uint32_t)prefill_wild(sm, wk.A[buf][row], g, clip, sh, mh) << (4 * (lane & 7));
+            c |= __shfl_xor_sync(0xffffffffu, c, 1);
+            c |= __shfl_xor_sync(0xffffffffu, c, 2);
+            c |= __shfl_xor_sync(0xffffffffu, c, 4);
+            c = __shfl_sync(0xffffffffu, c, 8 * t);  // the word of channels 8 t ..
+            if ((lane >> 2) == (l >> 2)) {
+                wk.word[row][t][g] = c;
+                if (t == 0) {
+                    wk.sc[row][g] = sh;
+                    wk.mn[row][g] = mh;
+                }
+                wilds &= ~(1u << q);
             }
         }
         worker_sync();  // the tile's codes are there
