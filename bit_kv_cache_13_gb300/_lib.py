@@ -90,8 +90,8 @@ def _check(status: int):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # (the handle itself: making a Stream object of it costs 2.5 us, as much as a launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -233,10 +233,35 @@ def kvq_workspace_status(workspace, stream=None) -> int:
 
 
 # ------------------------------------------------------------------- INT4
+#
+# These calls take a few microseconds on the device for a single token, so each
+# tensor is checked in one expression; what fails it is looked at again to say why.
 
-def _shape(x, shape, name: str):
-    if x is not None and tuple(x.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(x.shape)}")
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+
+
+def _ptr(x, dtype, shape, dev: int, name: str):
+    """x's device pointer: a contiguous tensor of this dtype and shape (None: any) on device dev, the current one."""
+    if x is None:
+        return None
+    if x.dtype is dtype and x.get_device() == dev and (shape is None or x.shape == shape) and x.is_contiguous():
+        return x.data_ptr()
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    _dev(x, dtype, name)
+    raise ValueError(f"tensors must be on the current device cuda:{torch.cuda.current_device()}, "
+                     f"{name} is on {x.device}")
+
+
+def _here(x) -> int:
+    """The current device, whose stream the call is enqueued on (-1 for a tensor that is not on a GPU)."""
+    return torch.cuda.current_device() if x.is_cuda else -1
+
+
+def _call(fn, dev: int, args, stream):
+    if dev < 0:
+        raise ValueError("the call's tensors must be CUDA tensors")
+    _check(fn(*args, _stream(stream)))
 
 
 def _pool(cache, num_pages: int, h_kv: int, name: str):
@@ -245,12 +270,17 @@ def _pool(cache, num_pages: int, h_kv: int, name: str):
         raise ValueError(f"{name} holds {cache.numel()} bytes, below {num_pages} pages x {h_kv} heads x 2560")
 
 
-def _one_device(*tensors):
-    """The call's tensors live on the current device, whose stream it is enqueued on."""
-    dev = torch.cuda.current_device()
-    for x in tensors:
-        if x is not None and x.is_cuda and x.get_device() != dev:
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {x.device}")
+def _rows(x, lead, name: str, last: str):
+    """The last extent of x, whose others are lead."""
+    if x.shape[:-1] != lead or x.dim() != len(lead) + 1:
+        raise ValueError(f"{name} must have shape ({', '.join(map(str, lead))}, {last}), got {tuple(x.shape)}")
+    return x.shape[-1]
+
+
+def _count(x, dev: int):
+    if x is not None and x.numel() == 0:
+        raise ValueError("err_count must have an element")
+    return _ptr(x, _I32, None, dev, "err_count")
 
 
 def kvq_int4_tile_bytes(d: int = 128) -> int:
@@ -260,33 +290,24 @@ def kvq_int4_tile_bytes(d: int = 128) -> int:
 def kvq_append_int4(k, v, slot_mapping, mu_k, R_k, R_v, cache, num_pages: int, clip: float = 1.0, err_count=None,
                     stream=None):
     """Quantise-on-append of k, v [n, H_kv, d] bf16 into the INT4 cache."""
-    n_tok, h_kv, d = k.shape
-    _shape(v, (n_tok, h_kv, d), "v")
-    _shape(slot_mapping, (n_tok,), "slot_mapping")
-    _shape(mu_k, (h_kv, d), "mu_k")
-    _shape(R_k, (h_kv, d, d), "R_k")
-    _shape(R_v, (h_kv, d, d), "R_v")
+    n_tok, h_kv, d = shape = k.shape
+    dev = _here(k)
     _pool(cache, num_pages, h_kv, "cache")
-    args = (_dev(k, torch.bfloat16, "k"), _dev(v, torch.bfloat16, "v"), n_tok, h_kv, d,
-            _dev(slot_mapping, torch.int32, "slot_mapping"), _dev(mu_k, torch.float32, "mu_k"),
-            _dev(R_k, torch.float32, "R_k"), _dev(R_v, torch.float32, "R_v"), float(clip),
-            _dev(cache, torch.uint8, "cache"), int(num_pages), _dev(err_count, torch.int32, "err_count"))
-    _one_device(k, v, slot_mapping, mu_k, R_k, R_v, cache, err_count)
-    _check(load().kvq_append_int4(*args, _stream(stream)))
+    _call(load().kvq_append_int4, dev, (
+        _ptr(k, _BF16, shape, dev, "k"), _ptr(v, _BF16, shape, dev, "v"), n_tok, h_kv, d,
+        _ptr(slot_mapping, _I32, (n_tok,), dev, "slot_mapping"), _ptr(mu_k, _F32, (h_kv, d), dev, "mu_k"),
+        _ptr(R_k, _F32, (h_kv, d, d), dev, "R_k"), _ptr(R_v, _F32, (h_kv, d, d), dev, "R_v"), float(clip),
+        _ptr(cache, _U8, None, dev, "cache"), int(num_pages), _count(err_count, dev)), stream)
 
 
 def kvq_dequant_int4(cache, num_pages: int, H_kv: int, slot_mapping, k_rot=None, v_rot=None, stream=None):
     """Dequantised rotated vectors [n, H_kv, d] bf16 of the cached tokens at slot_mapping [n]."""
-    n = slot_mapping.shape[0]
-    _shape(slot_mapping, (n,), "slot_mapping")
-    _shape(k_rot, (n, H_kv, 128), "k_rot")
-    _shape(v_rot, (n, H_kv, 128), "v_rot")
+    n, dev = slot_mapping.shape[0], _here(cache)
     _pool(cache, num_pages, H_kv, "cache")
-    args = (_dev(cache, torch.uint8, "cache"), int(num_pages), H_kv, 128,
-            _dev(slot_mapping, torch.int32, "slot_mapping"), n, _dev(k_rot, torch.bfloat16, "k_rot"),
-            _dev(v_rot, torch.bfloat16, "v_rot"))
-    _one_device(cache, slot_mapping, k_rot, v_rot)
-    _check(load().kvq_dequant_int4(*args, _stream(stream)))
+    _call(load().kvq_dequant_int4, dev, (
+        _ptr(cache, _U8, None, dev, "cache"), int(num_pages), H_kv, 128,
+        _ptr(slot_mapping, _I32, (n,), dev, "slot_mapping"), n,
+        _ptr(k_rot, _BF16, (n, H_kv, 128), dev, "k_rot"), _ptr(v_rot, _BF16, (n, H_kv, 128), dev, "v_rot")), stream)
 
 
 def kvq_int4_workspace_bytes(B: int, H_q: int, H_kv: int, max_pages_per_seq: int, num_splits: int = 0,
@@ -294,56 +315,47 @@ def kvq_int4_workspace_bytes(B: int, H_q: int, H_kv: int, max_pages_per_seq: int
     return load().kvq_int4_workspace_bytes(B, H_q, H_kv, max_pages_per_seq, num_splits, int(weights))
 
 
-def _decode_int4_args(q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out):
-    B, H_q, d = q.shape
+def _decode_int4_args(dev, q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out):
+    B, H_q, d = shape = q.shape
     h_kv = R_k.shape[0]
-    _shape(R_k, (h_kv, d, d), "R_k")
-    _shape(R_v, (h_kv, d, d), "R_v")
-    _shape(context_lens, (B,), "context_lens")
-    _shape(out, (B, H_q, d), "out")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must have shape ({B}, max_pages), got {tuple(block_table.shape)}")
+    pages = _rows(block_table, (B,), "block_table", "max_pages")
     _pool(cache, num_pages, h_kv, "cache")
-    return (_dev(q, torch.bfloat16, "q"), B, H_q, h_kv, d, _dev(cache, torch.uint8, "cache"), int(num_pages),
-            _dev(block_table, torch.int32, "block_table"), block_table.shape[1],
-            _dev(context_lens, torch.int32, "context_lens"), _dev(R_k, torch.float32, "R_k"),
-            _dev(R_v, torch.float32, "R_v"), float(scale), _dev(out, torch.bfloat16, "out"))
+    return (_ptr(q, _BF16, None, dev, "q"), B, H_q, h_kv, d, _ptr(cache, _U8, None, dev, "cache"), int(num_pages),
+            _ptr(block_table, _I32, None, dev, "block_table"), pages,
+            _ptr(context_lens, _I32, (B,), dev, "context_lens"), _ptr(R_k, _F32, (h_kv, d, d), dev, "R_k"),
+            _ptr(R_v, _F32, (h_kv, d, d), dev, "R_v"), float(scale), _ptr(out, _BF16, shape, dev, "out"))
 
 
 def kvq_decode_attn_int4(q, cache, num_pages: int, block_table, context_lens, R_k, R_v, scale: float, out, workspace,
                          num_splits: int = 0, stream=None):
     """Decode attention of q [B, H_q, d] bf16 over the INT4 cache into out [B, H_q, d] bf16."""
-    args = _decode_int4_args(q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out)
-    ws = _dev(workspace, torch.uint8, "workspace")
-    _one_device(q, cache, block_table, context_lens, R_k, R_v, out, workspace)
-    _check(load().kvq_decode_attn_int4(*args, ws, workspace.numel(), int(num_splits), _stream(stream)))
+    dev = _here(q)
+    _call(load().kvq_decode_attn_int4, dev, (
+        *_decode_int4_args(dev, q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out),
+        _ptr(workspace, _U8, None, dev, "workspace"), workspace.numel(), int(num_splits)), stream)
 
 
 def kvq_decode_attn_int4_weights(q, cache, num_pages: int, block_table, context_lens, R_k, R_v, scale: float, out,
                                  weights, decay: float, workspace, num_splits: int = 0, stream=None):
     """kvq_decode_attn_int4 that also adds each token's attention weight, summed over the query heads of its KV head,
     to weights [B, H_kv, >= 16 max_pages] fp32 (scaled by decay first)."""
-    if weights.dim() != 3 or tuple(weights.shape[:2]) != (q.shape[0], R_k.shape[0]):
-        raise ValueError(f"weights must have shape ({q.shape[0]}, {R_k.shape[0]}, tokens), got {tuple(weights.shape)}")
-    args = _decode_int4_args(q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out)
-    w, ws = _dev(weights, torch.float32, "weights"), _dev(workspace, torch.uint8, "workspace")
-    _one_device(q, cache, block_table, context_lens, R_k, R_v, out, weights, workspace)
-    _check(load().kvq_decode_attn_int4_weights(*args, w, weights.shape[2], float(decay), ws, workspace.numel(),
-                                               int(num_splits), _stream(stream)))
+    dev = _here(q)
+    tokens = _rows(weights, (q.shape[0], R_k.shape[0]), "weights", "tokens")
+    _call(load().kvq_decode_attn_int4_weights, dev, (
+        *_decode_int4_args(dev, q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out),
+        _ptr(weights, _F32, None, dev, "weights"), tokens, float(decay), _ptr(workspace, _U8, None, dev, "workspace"),
+        workspace.numel(), int(num_splits)), stream)
 
 
 def kvq_evict_select(weights, context_lens, budget: int, sinks: int, recent: int, keep, new_lens, stream=None):
     """Chooses the tokens each (sequence, KV head) keeps by weights [B, H_kv, max_tokens] fp32: their indices, ascending,
     into keep [B, H_kv, budget] int32 (-1 past them) and min(length, budget) into new_lens [B] int32."""
     B, h_kv, max_tokens = weights.shape
-    _shape(context_lens, (B,), "context_lens")
-    _shape(new_lens, (B,), "new_lens")
-    _shape(keep, (B, h_kv, budget), "keep")
-    args = (_dev(weights, torch.float32, "weights"), max_tokens, B, h_kv, max_tokens,
-            _dev(context_lens, torch.int32, "context_lens"), int(budget), int(sinks), int(recent),
-            _dev(keep, torch.int32, "keep"), _dev(new_lens, torch.int32, "new_lens"))
-    _one_device(weights, context_lens, keep, new_lens)
-    _check(load().kvq_evict_select(*args, _stream(stream)))
+    dev = _here(weights)
+    _call(load().kvq_evict_select, dev, (
+        _ptr(weights, _F32, None, dev, "weights"), max_tokens, B, h_kv, max_tokens,
+        _ptr(context_lens, _I32, (B,), dev, "context_lens"), int(budget), int(sinks), int(recent),
+        _ptr(keep, _I32, (B, h_kv, budget), dev, "keep"), _ptr(new_lens, _I32, (B,), dev, "new_lens")), stream)
 
 
 def kvq_evict_gather_int4(cache, num_pages: int, block_table, keep, new_lens, dst_cache, dst_num_pages: int,
@@ -351,26 +363,23 @@ def kvq_evict_gather_int4(cache, num_pages: int, block_table, keep, new_lens, ds
     """Moves the tokens of keep [B, H_kv, budget] from the pages of block_table into those of dst_block_table (and their
     weights [B, H_kv, tokens] into weights_out, whose rows are zero past them)."""
     B, h_kv, budget = keep.shape
-    _shape(new_lens, (B,), "new_lens")
-    for x, name in ((block_table, "block_table"), (dst_block_table, "dst_block_table")):
-        if x.dim() != 2 or x.shape[0] != B:
-            raise ValueError(f"{name} must have shape ({B}, pages), got {tuple(x.shape)}")
+    dev = _here(cache)
+    src_pages = _rows(block_table, (B,), "block_table", "pages")
+    dst_pages = _rows(dst_block_table, (B,), "dst_block_table", "pages")
     if (weights is None) != (weights_out is None):
         raise ValueError("weights and weights_out go together")
-    for x, name in ((weights, "weights"), (weights_out, "weights_out")):
-        if x is not None and (x.dim() != 3 or tuple(x.shape[:2]) != (B, h_kv)):
-            raise ValueError(f"{name} must have shape ({B}, {h_kv}, tokens), got {tuple(x.shape)}")
+    w_row, o_row = (0 if x is None else _rows(x, (B, h_kv), name, "tokens")
+                    for x, name in ((weights, "weights"), (weights_out, "weights_out")))
     _pool(cache, num_pages, h_kv, "cache")
     _pool(dst_cache, dst_num_pages, h_kv, "dst_cache")
-    args = (_dev(cache, torch.uint8, "cache"), int(num_pages), _dev(block_table, torch.int32, "block_table"),
-            block_table.shape[1], _dev(keep, torch.int32, "keep"), budget, _dev(new_lens, torch.int32, "new_lens"),
-            B, h_kv, 128, _dev(dst_cache, torch.uint8, "dst_cache"), int(dst_num_pages),
-            _dev(dst_block_table, torch.int32, "dst_block_table"), dst_block_table.shape[1],
-            _dev(weights, torch.float32, "weights"), 0 if weights is None else weights.shape[2],
-            _dev(weights_out, torch.float32, "weights_out"), 0 if weights_out is None else weights_out.shape[2],
-            _dev(err_count, torch.int32, "err_count"))
-    _one_device(cache, block_table, keep, new_lens, dst_cache, dst_block_table, weights, weights_out, err_count)
-    _check(load().kvq_evict_gather_int4(*args, _stream(stream)))
+    _call(load().kvq_evict_gather_int4, dev, (
+        _ptr(cache, _U8, None, dev, "cache"), int(num_pages),
+        _ptr(block_table, _I32, None, dev, "block_table"), src_pages,
+        _ptr(keep, _I32, None, dev, "keep"), budget, _ptr(new_lens, _I32, (B,), dev, "new_lens"), B, h_kv, 128,
+        _ptr(dst_cache, _U8, None, dev, "dst_cache"), int(dst_num_pages),
+        _ptr(dst_block_table, _I32, None, dev, "dst_block_table"), dst_pages, _ptr(weights, _F32, None, dev, "weights"),
+        w_row, _ptr(weights_out, _F32, None, dev, "weights_out"), o_row,
+        _count(err_count, dev)), stream)
 
 
 # -------------------------------------------------------------- Block-GTQ
