@@ -148,14 +148,18 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // channel 8 t + 2 i + e = column 2 t + e of its eight columns' set i, the accumulators
 // of a lane are the eight codes of one word of the key record.
 //
-// |z - accumulated| <= PF_EPS (|k| + |mu|): the largest error seen was 2^-22.1 of the
-// norms (2 10^8 values of three distributions), the bound leaves a factor of four.
-// Groups or codes that the bound leaves open (about one group in twenty-five, one
+// |z - accumulated| <= PF_EPS |R_j| (|k| + |mu|), R_j the largest column: an MMA cuts
+// its sum to 24 bits once, by less than 2^-23 of a partial sum that the norms bound.
+// The largest part's eight steps go as two chains of four (4 2^-23 for both; one chain
+// of eight was seen 2^-20.2 off on inputs along a column, sorted to grow at once, two
+// chains 2^-21.8, normal inputs 2^-23.8), the smaller parts' 2^-8 of that; adding the
+// chains, rounding mu R and subtracting it make 3 2^-24; the rest of 6 2^-23 is room.
+// Groups or codes that the bound leaves open (a few groups in a hundred, one
 // code in ten thousand) take exact dot products in pairs of fp32 values, a worker's
 // together in one list: fp64 is 64 times slower than fp32 here, and a first form of
 // these second looks in fp64 took most of the kernel's time.
 constexpr int PF_WORKERS = 4, PF_M = 32;  // tokens of a worker's tile
-constexpr float PF_EPS = 0x1p-20f;
+constexpr float PF_EPS = 0x1.8p-21f;
 constexpr int PF_LIST = 96;               // exact values of a tile (a full list sends its groups the slow way)
 constexpr int PF_A = D + 8;               // padded rows, in elements
 
@@ -174,7 +178,7 @@ struct __align__(16) PrefillSmem {
     __align__(16) uint2 R[3][NGROUP][4][8][32];  // parts as operands: [part][group][set][K step][lane]
     __align__(16) float mu[D];                // the centre (0 for values)
     __align__(16) float c[D];                 // mu R
-    float m2[4], mu2;
+    float m2[4], col2[PF_WORKERS * 4], mu_norm, bound;  // bound: PF_EPS times the largest column's norm
     PrefillWorker w[PF_WORKERS];
 };
 static_assert(offsetof(PrefillSmem, R) % 16 == 0 && offsetof(PrefillSmem, mu) % 16 == 0 && offsetof(PrefillSmem, c) % 16 == 0 &&
@@ -219,7 +223,7 @@ __device__ __forceinline__ float4 prefill_column(const PrefillSmem& sm, int ch, 
 // 4.4 cycles for each instruction's fetch.)
 __device__ __noinline__ Dd prefill_exact(const PrefillSmem& sm, const __nv_bfloat16* A, int ch, bool centred) {
     const int lane = threadIdx.x & 31;
-    Dd s[2] = {};
+    Dd s[4] = {};  // (chains)
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const int e = 16 * y + (lane & 15), i0 = 16 * (e >> 2) + 2 * (e & 3);
@@ -230,10 +234,12 @@ __device__ __noinline__ Dd prefill_exact(const PrefillSmem& sm, const __nv_bfloa
         for (int q = 0; q < 4; ++q) {
             float hi = xv[q], lo = 0.f;
             if (centred) two_sum(xv[q], -sm.mu[i0 + (q & 1) + 8 * (q >> 1)], hi, lo);
-            dd_fma(s[q & 1], hi, lo, rw[q]);
+            dd_fma(s[q], hi, lo, rw[q]);
         }
     }
     dd_add(s[0], s[1]);
+    dd_add(s[2], s[3]);
+    dd_add(s[0], s[2]);
 #pragma unroll
     for (int o = 8; o; o >>= 1) {
         const Dd y = {__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)};
@@ -332,13 +338,15 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         if (lane == 0) sm.m2[g] = m2;
     }
     __syncthreads();
-    if (threadIdx.x == 0) sm.mu2 = (sm.m2[0] + sm.m2[1]) + (sm.m2[2] + sm.m2[3]);
-    if (side == 0) {  // mu R: four neighbouring threads a channel
+    {   // the columns' norms and mu R: four neighbouring threads a channel
         const int ch = threadIdx.x >> 2, q = threadIdx.x & 3;
         Dd s[2] = {};
+        float n2 = 0.f;
 #pragma unroll 2
         for (int ks = 0; ks < 8; ++ks) {
             const float4 x = prefill_column(sm, ch, ks, q);
+            n2 = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, n2))));
+            if (side) continue;
             dd_fma(s[0], sm.mu[16 * ks + 2 * q], 0.f, x.x);
             dd_fma(s[1], sm.mu[16 * ks + 2 * q + 1], 0.f, x.y);
             dd_fma(s[0], sm.mu[16 * ks + 2 * q + 8], 0.f, x.z);
@@ -351,6 +359,18 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             dd_add(s[0], y);
         }
         if (q == 0) sm.c[ch] = s[0].hi + s[0].lo;
+        n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
+        n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
+#pragma unroll
+        for (int o = 16; o >= 4; o >>= 1) n2 = fmaxf(n2, __shfl_xor_sync(0xffffffffu, n2, o));
+        if (lane == 0) sm.col2[threadIdx.x >> 5] = n2;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            n2 = sm.col2[0];
+            for (int w = 1; w < PF_WORKERS * 4; ++w) n2 = fmaxf(n2, sm.col2[w]);
+            sm.bound = PF_EPS * sqrtf(n2);
+            sm.mu_norm = sqrtf((sm.m2[0] + sm.m2[1]) + (sm.m2[2] + sm.m2[3]));
+        }
     }
     __syncthreads();  // the last barrier of the whole CTA
 
@@ -372,36 +392,48 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             }
             n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
             n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
-            if ((tid & 3) == 0) wk.eps[row] = int4_wild(n2 + sm.mu2) ? -1.f : PF_EPS * (sqrtf(n2) + sqrtf(sm.mu2));
+            if ((tid & 3) == 0) wk.eps[row] = int4_wild(n2 + sm.mu_norm * sm.mu_norm) ? -1.f : sm.bound * (sqrtf(n2) + sm.mu_norm);
             if (tid == 0) wk.n_item = 0;
         }
         if (x + stride < tiles) fetch(x + stride, buf ^ 1);
 
-        float acc[2][4][4];  // [16 tokens][set][..]
+        float acc[2][4][4], acc2[2][4][4];  // [16 tokens][set][..]; acc2: the largest part's second half
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[m][i][e] = acc2[m][i][e] = 0.f;
         const uint32_t a_addr = smem_u32(&wk.A[buf][lane & 15][8 * (lane >> 4)]);
-#pragma unroll 1
-        for (int p = 2; p >= 0; --p)
+        auto step = [&](int p, int ks, float (&to)[2][4][4]) {
+            uint32_t a[2][4];
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                uint32_t a[2][4];
+            for (int m = 0; m < 2; ++m)
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(a[m][0]), "=r"(a[m][1]), "=r"(a[m][2]), "=r"(a[m][3])
+                             : "r"(a_addr + 32 * ks + 16 * PF_A * 2 * m));
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(a[m][0]), "=r"(a[m][1]), "=r"(a[m][2]), "=r"(a[m][3])
-                                 : "r"(a_addr + 32 * ks + 16 * PF_A * 2 * m));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint2 f = sm.R[p][g][i][ks][lane];
-                    mma_bf16(acc[0][i], a[0], f.x, f.y);
-                    mma_bf16(acc[1][i], a[1], f.x, f.y);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const uint2 f = sm.R[p][g][i][ks][lane];
+                mma_bf16(to[0][i], a[0], f.x, f.y);
+                mma_bf16(to[1][i], a[1], f.x, f.y);
             }
+        };
+#pragma unroll 1
+        for (int p = 2; p >= 1; --p)
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) step(p, ks, acc);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            step(0, ks, acc);
+            step(0, ks + 4, acc2);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][i][e] += acc2[m][i][e];
         worker_sync();  // the bounds are there
 
         // row set q = 2 m + e: rows 16 m + 8 e + r; its channel 32 g + 8 t + i of this lane

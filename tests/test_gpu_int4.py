@@ -377,3 +377,25 @@ def test_prefill_then_decode_through_the_layer():
             assert np.linalg.norm(f(out)[b, j] - ref[b, j]) <= 2.0 ** -7 * np.linalg.norm(ref[b, j])
     # 16 heads of two sequences, each with weights that add up to 1 (two calls of one step: only the first accumulates)
     assert abs(float(layer.weights.double().sum()) - 2 * 16) <= 32 * 2.0 ** -15
+
+
+def _grown(R, n, g):
+    """Inputs along columns of R, from its rows in the order of the first column's magnitudes down: products of one sign
+    whose partial sums stay near the bound that the norms give, where a sum that is cut to 24 bits at each step errs most."""
+    x = R[:, np.where(np.arange(n) % 2, 0, g.integers(0, 128, n))].T * g.uniform(0.5, 2.0, (n, 1))
+    return (x * (1.0 + 0.1 * g.standard_normal(x.shape)))[:, None]
+
+
+@pytest.mark.parametrize("norm", [1.0, 3.0])
+def test_append_of_inputs_along_a_column(norm):
+    """A whole prefill's bytes are the oracle's, also where the columns of the matrix have another norm than 1."""
+    rng = np.random.default_rng(77)
+    R = _rot(rng, 1)[0]
+    R = (norm * R[np.argsort(-np.abs(R[:, 0]))]).astype(np.float32)
+    n = 4096
+    k, v = _bf(_grown(R, n, rng)), _bf(_grown(R, n, rng))
+    mu = np.zeros((1, 128), np.float32)
+    cache, want = torch.zeros((n // 16, 1, 2560), dtype=torch.uint8, device="cuda"), int4.new_cache(n // 16, 1)
+    assert _append(k, v, np.arange(n), mu, R[None], R[None], cache) == 0
+    int4.append(want, k.double().numpy(), v.double().numpy(), np.arange(n), mu, R[None], R[None])
+    assert np.array_equal(cache.cpu().numpy(), want)
