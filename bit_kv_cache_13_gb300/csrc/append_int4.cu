@@ -160,7 +160,7 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // these second looks in fp64 took most of the kernel's time.
 constexpr int PF_WORKERS = 4, PF_M = 32;  // tokens of a worker's tile
 constexpr float PF_EPS = 0x1.8p-21f;
-constexpr int PF_LIST = 96;               // exact values of a tile (a full list sends its groups the slow way)
+constexpr int PF_LIST = 96;               // exact values of a tile (below 127; a full list sends its groups the slow way)
 constexpr int PF_A = D + 8;               // padded rows, in elements
 
 struct __align__(16) PrefillWorker {
@@ -177,7 +177,8 @@ struct __align__(16) PrefillWorker {
 struct __align__(16) PrefillSmem {
     __align__(16) uint2 R[3][NGROUP][4][8][32];  // parts as operands: [part][group][set][K step][lane]
     __align__(16) float mu[D];                // the centre (0 for values)
-    __align__(16) float c[D];                 // mu R
+    __align__(16) float c[D];                 // mu R (0 for values)
+    __align__(16) Dd c_exact[D];
     float m2[4], col2[PF_WORKERS * 4], mu_norm, bound;  // bound: PF_EPS times the largest column's norm
     PrefillWorker w[PF_WORKERS];
 };
@@ -217,29 +218,24 @@ __device__ __forceinline__ float4 prefill_column(const PrefillSmem& sm, int ch, 
                        (bf16_lo(a.y) + bf16_lo(b.y)) + bf16_lo(d.y), (bf16_hi(a.y) + bf16_hi(b.y)) + bf16_hi(d.y));
 }
 
-// (k - mu) . R[:, ch] (or v . R) of a row A: sixteen lanes, two times four inputs each;
-// all of them get the sum.  (Not inlined: the kernel's loop has to stay within the
-// instruction cache.  With these sums and the fp64 path unrolled into it, a warp waited
-// 4.4 cycles for each instruction's fetch.)
-__device__ __noinline__ Dd prefill_exact(const PrefillSmem& sm, const __nv_bfloat16* A, int ch, bool centred) {
+// k . R[:, ch] - (mu R)[ch] (or v . R[:, ch]) of a row A: sixteen lanes, two times four
+// inputs each; all of them get the sum.  (Not inlined: the kernel's loop has to stay
+// within the instruction cache.  With these sums and the fp64 path unrolled into it, a
+// warp waited 4.4 cycles for each instruction's fetch.)
+__device__ __noinline__ Dd prefill_exact(const PrefillSmem& sm, const __nv_bfloat16* A, int ch) {
     const int lane = threadIdx.x & 31;
-    Dd s[4] = {};  // (chains)
+    Dd s[2] = {};
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const int e = 16 * y + (lane & 15), i0 = 16 * (e >> 2) + 2 * (e & 3);
         const uint32_t xa = *reinterpret_cast<const uint32_t*>(A + i0), xb = *reinterpret_cast<const uint32_t*>(A + i0 + 8);
         const float4 rv = prefill_column(sm, ch, e >> 2, e & 3);
-        const float xv[4] = {bf16_lo(xa), bf16_hi(xa), bf16_lo(xb), bf16_hi(xb)}, rw[4] = {rv.x, rv.y, rv.z, rv.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float hi = xv[q], lo = 0.f;
-            if (centred) two_sum(xv[q], -sm.mu[i0 + (q & 1) + 8 * (q >> 1)], hi, lo);
-            dd_fma(s[q], hi, lo, rw[q]);
-        }
+        dd_fma(s[0], bf16_lo(xa), 0.f, rv.x);
+        dd_fma(s[1], bf16_hi(xa), 0.f, rv.y);
+        dd_fma(s[0], bf16_lo(xb), 0.f, rv.z);
+        dd_fma(s[1], bf16_hi(xb), 0.f, rv.w);
     }
     dd_add(s[0], s[1]);
-    dd_add(s[2], s[3]);
-    dd_add(s[0], s[2]);
 #pragma unroll
     for (int o = 8; o; o >>= 1) {
         const Dd y = {__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)};
@@ -248,6 +244,8 @@ __device__ __noinline__ Dd prefill_exact(const PrefillSmem& sm, const __nv_bfloa
     // (the butterfly adds in another order in each lane: take the group's first)
     s[0].hi = __shfl_sync(0xffffffffu, s[0].hi, lane & 16);
     s[0].lo = __shfl_sync(0xffffffffu, s[0].lo, lane & 16);
+    const Dd c = sm.c_exact[ch];
+    dd_add(s[0], Dd{-c.hi, -c.lo});
     return dd_norm(s[0]);
 }
 
@@ -358,7 +356,10 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             const Dd y = {__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)};
             dd_add(s[0], y);
         }
-        if (q == 0) sm.c[ch] = s[0].hi + s[0].lo;
+        if (q == 0) {
+            sm.c[ch] = s[0].hi + s[0].lo;
+            sm.c_exact[ch] = dd_norm(s[0]);
+        }
         n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
         n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
 #pragma unroll
@@ -449,7 +450,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         }
         // ---- each row's parameters; the candidates of open ones go on the worker's list
         float top[4];                 // largest magnitude of the group
-        uint32_t cands = 0, places = 0;  // candidate bits and their place on the list (255: not on it), a byte per row set
+        uint32_t cands = 0, places = 0;  // a byte per row set: candidates; place on the list (127: not on it), bit 7 an open scale
         bool any_open = false;        // (warp-uniform)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -466,30 +467,23 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             top[q] = fmaxf(fabsf(mn), fabsf(mx));
             const float eps = wk.eps[row_of(q)];
             __half sh, mh;
-            const bool open = int4_params_near(mn, mx, clip, eps, sh, mh) && eps >= 0.f && wk.slot[buf][row_of(q)] >= 0;
+            const int near = int4_params_near(mn, mx, clip, eps, sh, mh);
+            const bool open = near && eps >= 0.f && wk.slot[buf][row_of(q)] >= 0;
             if (t == 0) {
                 wk.sc[row_of(q)][g] = sh;
                 wk.mn[row_of(q)][g] = mh;
             }
             if (__any_sync(0xffffffffu, open)) {
                 uint32_t c = 0;
-                if (open) {
+                if (open) {  // (the largest values only where the scale is open)
+                    const float low = mn + 2.f * eps, high = near > 1 ? mx - 2.f * eps : CUDART_INF_F;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) c |= (uint32_t)(z_of(i, q) <= mn + 2.f * eps || z_of(i, q) >= mx - 2.f * eps) << i;
+                    for (int i = 0; i < 8; ++i) c |= (uint32_t)(z_of(i, q) <= low || z_of(i, q) >= high) << i;
                 }
-                const int n = __popc(c);
-                int inc = n, base = 0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                if (lane == 31) base = atomicAdd(&wk.n_item, inc);
-                base = __shfl_sync(0xffffffffu, base, 31);
+                const int n = __popc(c), at = n ? atomicAdd(&wk.n_item, n) : 0;
                 any_open = true;
-                const int at = base + inc - n;
                 cands |= c << (8 * q);
-                places |= (uint32_t)(at + n <= PF_LIST ? at : 255) << (8 * q);
+                places |= (uint32_t)((at + n <= PF_LIST ? at : 127) | (near > 1 ? 128 : 0)) << (8 * q);
                 for (int y = 0; y < n && at + y < PF_LIST; ++y) {
                     wk.item[at + y] = (uint16_t)(row_of(q) << 7 | (32 * g + 8 * t + __ffs(c) - 1));
                     c &= c - 1;
@@ -502,7 +496,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
 #pragma unroll 1
             for (int x0 = 0; x0 < n_item; x0 += 8) {  // sixteen threads an item
                 const int y = x0 + (tid >> 4), it = wk.item[min(y, n_item - 1)];
-                const Dd z = prefill_exact(sm, wk.A[buf][it >> 7], it & 127, !side);
+                const Dd z = prefill_exact(sm, wk.A[buf][it >> 7], it & 127);
                 if (y < n_item && (lane & 15) == 0) wk.found[y] = z;
             }
             worker_sync();
@@ -511,19 +505,19 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 const uint32_t c = cands >> (8 * q) & 255;
-                const int place = places >> (8 * q) & 255, row0 = row_of(q) - r;
+                const int place = places >> (8 * q) & 127, row0 = row_of(q) - r;
                 if (!__any_sync(0xffffffffu, c != 0)) continue;
                 Dd lo = {CUDART_INF_F, 0.f}, hi = {-CUDART_INF_F, 0.f};
-                if (place != 255)
+                if (place != 127)
                     for (int y = 0, n = __popc(c); y < n; ++y) {
                         const Dd z = wk.found[place + y];
                         if (dd_less(z, lo)) lo = z;
                         if (dd_less(hi, z)) hi = z;
                     }
-                uint32_t left = place == 255 ? c : 0, any;  // not on the list: the warp takes them one by one
+                uint32_t left = place == 127 ? c : 0, any;  // not on the list: the warp takes them one by one
                 while ((any = __ballot_sync(0xffffffffu, left != 0)) != 0) {
                     const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, left, l)) - 1;
-                    const Dd z = prefill_exact(sm, wk.A[buf][row0 + (l >> 2)], 32 * g + 8 * (l & 3) + i, !side);
+                    const Dd z = prefill_exact(sm, wk.A[buf][row0 + (l >> 2)], 32 * g + 8 * (l & 3) + i);
                     if (lane == l) {
                         if (dd_less(z, lo)) lo = z;
                         if (dd_less(hi, z)) hi = z;
@@ -540,7 +534,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 if (t == 0 && lo.hi <= hi.hi) {  // (the rows that were not open saw none)
                     __half sh, mh;
                     int4_params(lo, hi, clip, sh, mh);
-                    wk.sc[row0 + r][g] = sh;
+                    if (places >> (8 * q + 7) & 1) wk.sc[row0 + r][g] = sh;
                     wk.mn[row0 + r][g] = mh;
                 }
             }
@@ -581,7 +575,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         while ((any = __ballot_sync(0xffffffffu, agains != 0)) != 0) {
             const int l = __ffs(any) - 1, bit = __ffs(__shfl_sync(0xffffffffu, agains, l)) - 1, q = bit >> 3, i = bit & 7;
             const int row = row_of(q) - r + (l >> 2);
-            const Dd y = prefill_exact(sm, wk.A[buf][row], 32 * g + 8 * (l & 3) + i, !side);
+            const Dd y = prefill_exact(sm, wk.A[buf][row], 32 * g + 8 * (l & 3) + i);
             if (lane == l) {
                 const float s = __half2float(wk.sc[row][g]), m = __half2float(wk.mn[row][g]), z = fmaf(y.hi - m, 1.f / s, -0.5f);
                 const int c = z <= -0.5f ? 0 : z >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(y, s, m, (int)rintf(z));

@@ -38,22 +38,22 @@ __device__ __forceinline__ int int4_code(double z, __half sh, __half mh) {
 }
 
 // The parameters from fp32 ends known to within eps (in absolute terms), and
-// whether the exact ends could give others.  Rounding to fp32 and then to fp16 is
-// monotone, so they are certain when both ends of their intervals round alike (what
-// saturates counts as open).
-__device__ __forceinline__ bool int4_params_near(float mn, float mx, float clip, float eps, __half& sh, __half& mh) {
+// whether the exact ends could give others: bit 0 another min, bit 1 another scale.
+// Rounding to fp32 and then to fp16 is monotone, so they are certain when both ends
+// of their intervals round alike (what saturates counts as open).
+__device__ __forceinline__ int int4_params_near(float mn, float mx, float clip, float eps, __half& sh, __half& mh) {
     const float s = clip * (mx - mn) * (1.f / INT4_LEVELS), m = clip * mn;
     const float ds = fmaf(clip * (2.f / INT4_LEVELS), eps, s * 0x1p-21f), dm = fmaf(clip, eps, fabsf(m) * 0x1p-22f);
     const __half2 lo = __floats2half2_rn(s - ds, m - dm), hi = __floats2half2_rn(s + ds, m + dm);
     sh = __low2half(lo);
     mh = __high2half(lo);
-    return h2_as_u32(lo) != h2_as_u32(hi) || !(s + ds < 65504.f && fabsf(m) + dm < 65504.f);
+    const uint32_t diff = h2_as_u32(lo) ^ h2_as_u32(hi);
+    return (diff >> 16 != 0 || !(fabsf(m) + dm < 65504.f)) | ((diff & 0xffff) != 0 || !(s + ds < 65504.f)) << 1;
 }
 
 // Unevaluated sums hi + lo of two fp32 values (about 46 bits).
 struct Dd {
     float hi, lo;
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
 };
 
 // acc + (x + xl) r
