@@ -160,7 +160,6 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // these second looks in fp64 took most of the kernel's time.
 constexpr int PF_WORKERS = 4, PF_M = 32;  // tokens of a worker's tile
 constexpr float PF_EPS = 0x1.8p-21f;
-constexpr int PF_LIST = 96;               // exact values of a tile (below 127; a full list sends its groups the slow way)
 constexpr int PF_A = D + 8;               // padded rows, in elements
 
 struct __align__(16) PrefillWorker {
@@ -168,11 +167,11 @@ struct __align__(16) PrefillWorker {
     __align__(16) uint32_t word[PF_M][4][4];  // the tile's codes [token][t][g]
     __align__(16) __half sc[PF_M][NGROUP];
     __align__(16) __half mn[PF_M][NGROUP];
-    __align__(16) Dd found[PF_LIST];          // exact values, of
-    uint16_t item[PF_LIST];                   // row << 7 | channel
+    uint32_t open_cand[PF_M * NGROUP];        // groups whose parameters are open: channels to look at, and
+    uint16_t open_id[PF_M * NGROUP];          // row << 4 | group << 2 | what is open
     float eps[PF_M];                          // the bound on the rows' errors; -1: a row for fp64
     int slot[2][PF_M];
-    int n_item;
+    int n_open;
 };
 struct __align__(16) PrefillSmem {
     __align__(16) uint2 R[3][NGROUP][4][8][32];  // parts as operands: [part][group][set][K step][lane]
@@ -394,7 +393,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
             n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
             if ((tid & 3) == 0) wk.eps[row] = int4_wild(n2 + sm.mu_norm * sm.mu_norm) ? -1.f : sm.bound * (sqrtf(n2) + sm.mu_norm);
-            if (tid == 0) wk.n_item = 0;
+            if (tid == 0) wk.n_open = 0;
         }
         if (x + stride < tiles) fetch(x + stride, buf ^ 1);
 
@@ -448,10 +447,8 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z_of(i, q) -= cc[i];
         }
-        // ---- each row's parameters; the candidates of open ones go on the worker's list
-        float top[4];                 // largest magnitude of the group
-        uint32_t cands = 0, places = 0;  // a byte per row set: candidates; place on the list (127: not on it), bit 7 an open scale
-        bool any_open = false;        // (warp-uniform)
+        // ---- each row's parameters; open ones go on the worker's list
+        float top[4];  // largest magnitude of the group
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float mn = z_of(0, q), mx = mn;
@@ -474,98 +471,84 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 wk.mn[row_of(q)][g] = mh;
             }
             if (__any_sync(0xffffffffu, open)) {
+                // every value that could be the smallest (the largest, where the scale is open)
+                const float low = mn + 2.f * eps, high = near > 1 ? mx - 2.f * eps : CUDART_INF_F;
                 uint32_t c = 0;
-                if (open) {  // (the largest values only where the scale is open)
-                    const float low = mn + 2.f * eps, high = near > 1 ? mx - 2.f * eps : CUDART_INF_F;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) c |= (uint32_t)(z_of(i, q) <= low || z_of(i, q) >= high) << i;
-                }
-                const int n = __popc(c), at = n ? atomicAdd(&wk.n_item, n) : 0;
-                any_open = true;
-                cands |= c << (8 * q);
-                places |= (uint32_t)((at + n <= PF_LIST ? at : 127) | (near > 1 ? 128 : 0)) << (8 * q);
-                for (int y = 0; y < n && at + y < PF_LIST; ++y) {
-                    wk.item[at + y] = (uint16_t)(row_of(q) << 7 | (32 * g + 8 * t + __ffs(c) - 1));
-                    c &= c - 1;
+                for (int i = 0; i < 8; ++i) c |= (uint32_t)(z_of(i, q) <= low || z_of(i, q) >= high) << i;
+                c <<= 8 * t;
+                c |= __shfl_xor_sync(0xffffffffu, c, 1);
+                c |= __shfl_xor_sync(0xffffffffu, c, 2);
+                if (open && t == 0) {
+                    const int at = atomicAdd(&wk.n_open, 1);
+                    wk.open_cand[at] = c;
+                    wk.open_id[at] = (uint16_t)(row_of(q) << 4 | g << 2 | near);
                 }
             }
         }
         worker_sync();  // the list is complete
-        const int n_item = min(wk.n_item, PF_LIST);
-        if (n_item > 0) {
+        const int n_open = wk.n_open;
+        if (n_open > 0) {
+            // a warp takes a group at a time, two values at a time
 #pragma unroll 1
-            for (int x0 = 0; x0 < n_item; x0 += 8) {  // sixteen threads an item
-                const int y = x0 + (tid >> 4), it = wk.item[min(y, n_item - 1)];
-                const Dd z = prefill_exact(sm, wk.A[buf][it >> 7], it & 127);
-                if (y < n_item && (lane & 15) == 0) wk.found[y] = z;
+            for (int y = g; y < n_open; y += 4) {
+                uint32_t c = wk.open_cand[y];
+                const int id = wk.open_id[y], row = id >> 4, gg = id >> 2 & 3;
+                Dd lo = {CUDART_INF_F, 0.f}, hi = {-CUDART_INF_F, 0.f};
+#pragma unroll 1
+                while (c) {
+                    const int first = __ffs(c) - 1;
+                    c &= c - 1;
+                    const int second = c ? __ffs(c) - 1 : first;
+                    c &= c - 1;
+                    const Dd z = prefill_exact(sm, wk.A[buf][row], 32 * gg + (lane < 16 ? first : second));
+                    if (dd_less(z, lo)) lo = z;
+                    if (dd_less(hi, z)) hi = z;
+                }
+                const Dd l2 = {__shfl_xor_sync(0xffffffffu, lo.hi, 16), __shfl_xor_sync(0xffffffffu, lo.lo, 16)};
+                const Dd h2 = {__shfl_xor_sync(0xffffffffu, hi.hi, 16), __shfl_xor_sync(0xffffffffu, hi.lo, 16)};
+                if (dd_less(l2, lo)) lo = l2;
+                if (dd_less(hi, h2)) hi = h2;
+                __half sh, mh;
+                int4_params(lo, hi, clip, sh, mh);
+                if (lane == 0) {
+                    if (id & 2) wk.sc[row][gg] = sh;
+                    wk.mn[row][gg] = mh;
+                }
             }
             worker_sync();
+        } else {
+            __syncwarp();  // (a warp's parameters are its own)
         }
-        if (any_open) {  // the exact ends of the open groups: every value that could be one was looked at
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t c = cands >> (8 * q) & 255;
-                const int place = places >> (8 * q) & 127, row0 = row_of(q) - r;
-                if (!__any_sync(0xffffffffu, c != 0)) continue;
-                Dd lo = {CUDART_INF_F, 0.f}, hi = {-CUDART_INF_F, 0.f};
-                if (place != 127)
-                    for (int y = 0, n = __popc(c); y < n; ++y) {
-                        const Dd z = wk.found[place + y];
-                        if (dd_less(z, lo)) lo = z;
-                        if (dd_less(hi, z)) hi = z;
-                    }
-                uint32_t left = place == 127 ? c : 0, any;  // not on the list: the warp takes them one by one
-                while ((any = __ballot_sync(0xffffffffu, left != 0)) != 0) {
-                    const int l = __ffs(any) - 1, i = __ffs(__shfl_sync(0xffffffffu, left, l)) - 1;
-                    const Dd z = prefill_exact(sm, wk.A[buf][row0 + (l >> 2)], 32 * g + 8 * (l & 3) + i);
-                    if (lane == l) {
-                        if (dd_less(z, lo)) lo = z;
-                        if (dd_less(hi, z)) hi = z;
-                        left &= left - 1;
-                    }
-                }
-#pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    const Dd x = {__shfl_xor_sync(0xffffffffu, lo.hi, o), __shfl_xor_sync(0xffffffffu, lo.lo, o)};
-                    const Dd y = {__shfl_xor_sync(0xffffffffu, hi.hi, o), __shfl_xor_sync(0xffffffffu, hi.lo, o)};
-                    if (dd_less(x, lo)) lo = x;
-                    if (dd_less(hi, y)) hi = y;
-                }
-                if (t == 0 && lo.hi <= hi.hi) {  // (the rows that were not open saw none)
-                    __half sh, mh;
-                    int4_params(lo, hi, clip, sh, mh);
-                    if (places >> (8 * q + 7) & 1) wk.sc[row0 + r][g] = sh;
-                    wk.mn[row0 + r][g] = mh;
-                }
-            }
-        }
-        __syncwarp();  // (a warp's parameters are its own)
         uint32_t agains = 0, wilds = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int row = row_of(q);
             const float eps = wk.eps[row];
-            // ---- codes: the nearest integer to (z - min) / scale within [0, 15], by adding 1.5 2^23;
-            // what it leaves of the quotient says how near a threshold is
-            const float s = __half2float(wk.sc[row][g]), m = __half2float(wk.mn[row][g]), inv = s > 0.f ? 1.f / s : 0.f, off = -m * inv;
-            const float most = 0.5f - inv * (eps + 0x1p-20f * (top[q] + fabsf(m) + 16.f * s));
+            // ---- codes: 15 times z's place in [min, min + 15 scale], rounded by adding 1.5 2^23; what
+            // that leaves says how near a threshold is (2^-21 of the terms and 2^-19: twice what the
+            // roundings of the place and its product make)
+            const float s = __half2float(wk.sc[row][g]), m = __half2float(wk.mn[row][g]), inv = s > 0.f ? 1.f / s : 0.f;
+            const float inv15 = inv * (1.f / INT4_LEVELS), off15 = -m * inv15;
+            const float most = 0.5f - 0x1p-19f - inv * (eps + 0x1p-21f * (top[q] + fabsf(m)));
             constexpr float MAGIC = 12582912.f;
             uint32_t w = 0;
             float far = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float y = fminf(fmaxf(fmaf(z_of(i, q), inv, off), 0.f), (float)INT4_LEVELS), n = y + MAGIC;
-                far = fmaxf(far, fabsf(y - (n - MAGIC)));
-                w |= (__float_as_uint(n) & 15u) << (4 * i);
+                const float y = __saturatef(fmaf(z_of(i, q), inv15, off15)), n = fmaf(y, (float)INT4_LEVELS, MAGIC);
+                far = fmaxf(far, fabsf(fmaf(y, (float)INT4_LEVELS, MAGIC - n)));
+                w += __float_as_uint(n) << (4 * i);  // (MAGIC's bits come off below)
             }
+            w -= 0x4b400000u * 0x11111111u;  // (1.5 2^23 as bits, times 16^0 + .. + 16^7)
             wk.word[row][t][g] = w;
             const bool live = wk.slot[buf][row] >= 0;
             wilds |= (uint32_t)(live && eps < 0.f) << q;
             if (live && eps >= 0.f && s > 0.f && !(far < most)) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float y = fminf(fmaxf(fmaf(z_of(i, q), inv, off), 0.f), (float)INT4_LEVELS);
-                    agains |= (uint32_t)!(fabsf(y - (y + MAGIC - MAGIC)) < most) << (8 * q + i);
+                    const float y = __saturatef(fmaf(z_of(i, q), inv15, off15)), n = fmaf(y, (float)INT4_LEVELS, MAGIC);
+                    agains |= (uint32_t)!(fabsf(fmaf(y, (float)INT4_LEVELS, MAGIC - n)) < most) << (8 * q + i);
                 }
             }
         }
