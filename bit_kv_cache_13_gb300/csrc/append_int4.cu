@@ -5,6 +5,7 @@
 // rotated vectors, whichever kernel writes them: each kernel forms the rotated
 // values to within a bound, and where a rounding or a threshold lies within that
 // bound of a value (a few groups in a hundred) it forms the value exactly.
+#include <algorithm>
 #include <cstddef>
 #include <mutex>
 #include <type_traits>
@@ -160,6 +161,7 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // these second looks in fp64 took most of the kernel's time.
 constexpr int PF_WORKERS = 4, PF_M = 32;  // tokens of a worker's tile
 constexpr float PF_EPS = 0x1.8p-21f;
+constexpr int PF_KEY_COST = 5, PF_VALUE_COST = 4;  // of a tile's time (more keys are looked at twice: the centre is in their bound)
 constexpr int PF_A = D + 8;               // padded rows, in elements
 
 struct __align__(16) PrefillWorker {
@@ -277,10 +279,10 @@ __global__ void __launch_bounds__(PF_WORKERS * 128, 1)
 append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, int n_tok, int H_kv,
                            const int32_t* __restrict__ slot_mapping, const float* __restrict__ mu,
                            const float* __restrict__ Rk, const float* __restrict__ Rv, uint8_t* __restrict__ cache,
-                           int64_t num_pages, int32_t* __restrict__ err_count, float clip) {
+                           int64_t num_pages, int32_t* __restrict__ err_count, float clip, int key_ctas) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     PrefillSmem& sm = *reinterpret_cast<PrefillSmem*>(smem_raw);
-    const int h = blockIdx.y, side = blockIdx.z, worker = threadIdx.x >> 7, tid = threadIdx.x & 127;
+    const int h = blockIdx.y, side = blockIdx.x >= key_ctas, worker = threadIdx.x >> 7, tid = threadIdx.x & 127;
     const int g = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
     PrefillWorker& wk = sm.w[worker];
     const float* R = (side ? Rv : Rk) + (size_t)h * D * D;
@@ -288,7 +290,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
     griddep_wait();
     griddep_launch_dependents();
 
-    const int tiles = (n_tok + PF_M - 1) / PF_M, stride = gridDim.x * PF_WORKERS;
+    const int tiles = (n_tok + PF_M - 1) / PF_M, stride = (side ? gridDim.x - key_ctas : key_ctas) * PF_WORKERS;
     const __nv_bfloat16* src = side ? v : k;
     const int64_t n_slots = num_pages * PAGE;
     auto worker_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(worker + 1) : "memory"); };
@@ -312,7 +314,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             wk.slot[buf][tid] = s;
         }
     };
-    const int x_first = blockIdx.x * PF_WORKERS + worker;
+    const int x_first = (blockIdx.x - (side ? key_ctas : 0)) * PF_WORKERS + worker;
     if (x_first < tiles) fetch(x_first, 0);
     // R's parts as operands: column n of set i of a group is channel 8 (n / 2) + 2 i + n % 2 of it
 #pragma unroll 2
@@ -741,13 +743,28 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
                               "kvq_append_int4 launch");
     const kvq_status sa = prefill_smem_once();
     if (sa != KVQ_OK) return sa;
-    // one CTA per SM in all, each with a stride of its (head, side)'s tiles
-    const int tiles = (n_tok + PF_M - 1) / PF_M, want = (tiles + PF_WORKERS - 1) / PF_WORKERS;
-    int most = kvq_device_sm_count() / (2 * H_kv);
-    most = most < 1 ? 1 : most;
-    return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(want < most ? want : most, H_kv, 2), dim3(PF_WORKERS * 128),
+    // One CTA per SM in all, each with a stride of its (head, side)'s tiles; a head's are
+    // split between its sides so that the later of them ends soonest, in rounds of a tile
+    // per worker (32K tokens, 8 heads, with read-back: 317 us for equal halves, 290 us).
+    const int tiles = (n_tok + PF_M - 1) / PF_M, most = kvq_device_sm_count() / H_kv;
+    auto rounds = [&](int ctas) { return (int)((tiles + (int64_t)ctas * PF_WORKERS - 1) / ((int64_t)ctas * PF_WORKERS)); };
+    int nk = 1, nv = 1;
+    int64_t best = INT64_MAX;
+    for (int x = 1; x < most; ++x) {
+        const int64_t cost = std::max((int64_t)PF_KEY_COST * rounds(x), (int64_t)PF_VALUE_COST * rounds(most - x));
+        if (cost < best) {
+            best = cost;
+            nk = x;
+            nv = most - x;
+        }
+    }
+    // (no more CTAs than those rounds need)
+    auto trim = [&](int ctas) { return (int)((tiles + (int64_t)rounds(ctas) * PF_WORKERS - 1) / ((int64_t)rounds(ctas) * PF_WORKERS)); };
+    nk = trim(nk);
+    nv = trim(nv);
+    return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(nk + nv, H_kv), dim3(PF_WORKERS * 128),
                                      sizeof(PrefillSmem), st, kb, vb, n_tok, H_kv, slot_mapping, mu_k, R_k, R_v, cb, num_pages,
-                                     err_count, clip),
+                                     err_count, clip, nk),
                           "kvq_append_int4 launch");
 }
 
