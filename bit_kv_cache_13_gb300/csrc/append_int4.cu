@@ -699,8 +699,12 @@ using namespace kvq;
 
 extern "C" size_t kvq_int4_tile_bytes(int d) { return d == D ? (size_t)INT4_TILE : 0; }
 
-// Appends of at least this many tokens take the tensor-core kernel.
-static constexpr int PREFILL_MIN = 32;
+// Token-heads from which on the tensor-core kernel is taken, for each wave of its CTAs:
+// it starts in about 12 us a wave (R's operand parts), the few-token kernel takes 0.03 us a
+// token-head.  With the read-back: 33 tokens of 8 heads 14.5 against 11.2 us, 64 tokens of
+// one head 13.4 against 5.2, 128 of two 18.0 against 11.6, 64 of 8 15.4 against 17.8, 128 of
+// 8 19.5 against 30.8.
+static constexpr int PREFILL_MIN = 400;
 
 static kvq_status prefill_smem_once() {
     static std::mutex mu;
@@ -737,7 +741,8 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const auto kb = static_cast<const __nv_bfloat16*>(k), vb = static_cast<const __nv_bfloat16*>(v);
     uint8_t* const cb = static_cast<uint8_t*>(cache);
-    if (n_tok < PREFILL_MIN)
+    const int nsm = kvq_device_sm_count(), waves = (2 * H_kv + nsm - 1) / nsm;
+    if ((int64_t)n_tok * H_kv < (int64_t)PREFILL_MIN * waves)
         return kvq_check_cuda(launch_pdl(append_int4_kernel, dim3(n_tok, H_kv, 2), dim3(512), 0, st, kb, vb, n_tok, H_kv,
                                          slot_mapping, mu_k, R_k, R_v, cb, num_pages, err_count, clip),
                               "kvq_append_int4 launch");
@@ -746,7 +751,7 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
     // One CTA per SM in all, each with a stride of its (head, side)'s tiles; a head's are
     // split between its sides so that the later of them ends soonest, in rounds of a tile
     // per worker (32K tokens, 8 heads, with read-back: 317 us for equal halves, 290 us).
-    const int tiles = (n_tok + PF_M - 1) / PF_M, most = kvq_device_sm_count() / H_kv;
+    const int tiles = (n_tok + PF_M - 1) / PF_M, most = nsm / H_kv;
     auto rounds = [&](int ctas) { return (int)((tiles + (int64_t)ctas * PF_WORKERS - 1) / ((int64_t)ctas * PF_WORKERS)); };
     int nk = 1, nv = 1;
     int64_t best = INT64_MAX;

@@ -42,7 +42,7 @@ def _append(k, v, slots, mu, rk, rv, cache, **kw):
 
 
 @pytest.mark.parametrize("n,h_kv,clip", [(1, 1, 1.0), (3, 8, 1.0), (17, 2, 0.9), (100, 1, 1.0), (255, 3, 1.0), (256, 1, 0.75),
-                                         (300, 2, 1.0), (1031, 1, 1.0)])
+                                         (300, 2, 1.0), (1031, 1, 1.0), (501, 1, 0.75), (64, 9, 1.0), (3, 200, 1.0)])
 def test_append_bytes_and_read_back(n, h_kv, clip):
     rng = np.random.default_rng(n)
     big = np.where(rng.random((h_kv, 128)) < 0.03, 20.0, 1.0)
@@ -72,7 +72,7 @@ def test_append_bytes_and_read_back(n, h_kv, clip):
 def test_append_adversarial_groups():
     """Identity rotation: exact midpoints, constant groups, saturating and vanishing scales, signed zeros."""
     eye = np.eye(128, dtype=np.float32)[None]
-    for n in (40, 300):
+    for n in (40, 500):
         k = torch.randn(n, 1, 128, generator=torch.Generator().manual_seed(0)) * 3
         k[0, 0, :32] = 1.5
         k[1, 0, :32] = torch.tensor([0.0, 15.0] + [i + 0.5 for i in range(15)] * 2)
@@ -84,7 +84,7 @@ def test_append_adversarial_groups():
         k[7] = torch.randint(0, 31, (128,), generator=torch.Generator().manual_seed(2)) * 0.5   # many midpoints
         k, v = k.to(torch.bfloat16), (-k).to(torch.bfloat16)
         mu = np.zeros((1, 128), np.float32)
-        cache, want = torch.zeros((19, 1, 2560), dtype=torch.uint8, device="cuda"), int4.new_cache(19, 1)
+        cache, want = torch.zeros((32, 1, 2560), dtype=torch.uint8, device="cuda"), int4.new_cache(32, 1)
         assert _append(k, v, np.arange(n), mu, eye, eye, cache) == 0
         int4.append(want, k.double().numpy(), v.double().numpy(), np.arange(n), mu, eye, eye)
         assert np.array_equal(cache.cpu().numpy(), want)
@@ -93,12 +93,12 @@ def test_append_adversarial_groups():
 def test_append_with_a_large_centre_and_huge_values():
     """Key minus centre cancels to a thousandth of either; values up to the end of the type's range."""
     rng = np.random.default_rng(6)
-    for n in (5, 300):
+    for n in (5, 500):
         mu = (300 * rng.standard_normal((1, 128))).astype(np.float32)
         k = _bf(mu[None] + rng.standard_normal((n, 1, 128)))
         v = _bf(rng.standard_normal((n, 1, 128)) * 10.0 ** rng.uniform(-37, 37, (n, 1, 1)))
         rk, rv = _rot(rng, 1), _rot(rng, 1)
-        cache, want = torch.zeros((19, 1, 2560), dtype=torch.uint8, device="cuda"), int4.new_cache(19, 1)
+        cache, want = torch.zeros((32, 1, 2560), dtype=torch.uint8, device="cuda"), int4.new_cache(32, 1)
         _append(k, v, np.arange(n), mu, rk, rv, cache)
         int4.append(want, k.double().numpy(), v.double().numpy(), np.arange(n), mu, rk, rv)
         assert np.array_equal(cache.cpu().numpy(), want)
@@ -112,12 +112,12 @@ def test_token_bytes_do_not_depend_on_their_company():
     mu, rk, rv = rng.standard_normal((h, 128)).astype(np.float32), _rot(rng, h), _rot(rng, h)
     slots = np.arange(n, dtype=np.int32)
     got = []
-    for cuts in ([0, n], [0, 333, n], list(range(0, 64)) + [64, n]):
+    for cuts in ([0, n], [0, 333, n], list(range(0, 64)) + [64, n], [0, 150, 300, 450, 600, n]):
         cache = torch.zeros((44, h, 2560), dtype=torch.uint8, device="cuda")
         for a, b in zip(cuts, cuts[1:]):
             _append(k[a:b], v[a:b], slots[a:b], mu, rk, rv, cache)
         got.append(cache.cpu().numpy())
-    assert np.array_equal(got[0], got[1]) and np.array_equal(got[0], got[2])
+    assert all(np.array_equal(got[0], x) for x in got[1:])
 
 
 @pytest.mark.parametrize("n", [2, 400])
