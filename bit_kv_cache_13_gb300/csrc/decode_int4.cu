@@ -1374,11 +1374,28 @@ static D4Layout d4_layout(int B, int H_q, int H_kv, int max_pages, int64_t C, bo
     return l;
 }
 
+// What the arguments that the workspace depends on are refused for (null: nothing).
+static const char* d4_refusal(int B, int H_q, int H_kv, int max_pages, int num_splits, kvq_status& st) {
+    st = KVQ_ERR_INVALID_ARG;
+    if (B <= 0 || H_kv <= 0 || H_q <= 0 || H_q % H_kv || max_pages <= 0 || num_splits < 0) return "sizes";
+    if (num_splits > D4_MAX_SPLITS) return "num_splits above 254";
+    st = KVQ_ERR_UNSUPPORTED;
+    if (H_q / H_kv > 8) return "GQA group above 8";
+    if (B > 65535 || H_kv > 65535) return "B or H_kv above 65535";
+    if (max_pages >= (1 << 27)) return "max_pages_per_seq not below 2^27";
+    const int64_t units = (int64_t)B * H_kv;
+    if (units > (1 << 24)) return "B * H_kv above 2^24";
+    // (a CTA's index times the batch's pages stays within 64 bits, a CTA's share within 32)
+    if (units * max_pages > (int64_t(1) << 36)) return "B * H_kv * max_pages_per_seq above 2^36";
+    if (units * num_splits > (1 << 22)) return "more than 2^22 CTAs";
+    st = KVQ_OK;
+    return nullptr;
+}
+
 extern "C" size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq, int num_splits,
                                            int weights) {
-    if (B <= 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv || max_pages_per_seq <= 0 || max_pages_per_seq >= (1 << 27) ||
-        num_splits < 0 || num_splits > D4_MAX_SPLITS || B > 65535 || H_kv > 65535)
-        return 0;
+    kvq_status st;
+    if (d4_refusal(B, H_q, H_kv, max_pages_per_seq, num_splits, st)) return 0;
     return d4_layout(B, H_q, H_kv, max_pages_per_seq, d4_ctas(B, H_kv, num_splits), weights != 0).total;
 }
 
@@ -1404,16 +1421,12 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
                               bool with_weights, float* weights, int64_t weights_stride, float decay, void* workspace,
                               size_t workspace_bytes, int num_splits, void* stream) {
     if (d != D) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: d=%d (only 128)", fn, d);
-    if (B <= 0 || H_kv <= 0 || H_q <= 0 || H_q % H_kv || max_pages <= 0 || num_pages <= 0 || num_splits < 0)
-        return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: B=%d H_q=%d H_kv=%d max_pages=%d num_pages=%lld splits=%d", fn,
-                             B, H_q, H_kv, max_pages, (long long)num_pages, num_splits);
+    kvq_status st;
+    if (const char* why = d4_refusal(B, H_q, H_kv, max_pages, num_splits, st))
+        return kvq_set_error(st, "%s: %s (B=%d H_q=%d H_kv=%d max_pages=%d splits=%d)", fn, why, B, H_q, H_kv, max_pages,
+                             num_splits);
+    if (num_pages <= 0) return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: num_pages=%lld", fn, (long long)num_pages);
     const int G = H_q / H_kv;
-    if (G > 8) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: GQA group %d > 8", fn, G);
-    if (B > 65535 || H_kv > 65535) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: B or H_kv above 65535", fn);
-    if (max_pages >= (1 << 27))
-        return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: max_pages_per_seq %d not below 2^27", fn, max_pages);
-    if (num_splits > D4_MAX_SPLITS)
-        return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: %d splits above %d", fn, num_splits, D4_MAX_SPLITS);
     if (!q || !cache || !block_table || !context_lens || !R_k || !R_v || !out || !workspace || (with_weights && !weights))
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (num_pages > (int64_t(1) << 32) / H_kv) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: num_pages * H_kv above 2^32", fn);
@@ -1428,9 +1441,6 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
             return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: decay %g is not finite and >= 0", fn, (double)decay);
     }
     const int64_t C = d4_ctas(B, H_kv, num_splits);
-    // (a CTA's index times the batch's pages stays within 64 bits, a CTA's share within 32)
-    if (C > (1 << 22) || (int64_t)B * H_kv * max_pages > (int64_t(1) << 36))
-        return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: %lld CTAs above 2^22, or B * H_kv * max_pages above 2^36", fn, (long long)C);
     const D4Layout lay = d4_layout(B, H_q, H_kv, max_pages, C, with_weights);
     if (workspace_bytes < lay.total)
         return kvq_set_error(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, lay.total);
@@ -1462,10 +1472,8 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int nsm = kvq_device_sm_count();
     const int64_t units = (int64_t)B * H_kv;
-    if (units > (1 << 24)) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: B * H_kv above 2^24", fn);
     // one sequence and a few heads: one kernel (the weights form: and the weights)
     const bool one = num_splits == 0 && B == 1 && 4 * H_kv <= nsm;
-    kvq_status st;
     if (!one) {
         // 1: one sequence a CTA, up to eight CTAs per SM
         const int per = (int)((4 * units + 8 * nsm - 1) / (8 * nsm));

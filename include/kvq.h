@@ -324,7 +324,7 @@ size_t kvq_int4_tile_bytes(int d);
  * is stored with NaN scale and min (it reads back as NaN).  Tokens with equal
  * slots race (last writer unspecified); what a token's bytes are does not
  * depend on the tokens appended with it.  k, v, R_k, R_v and cache need 16-byte
- * alignment. */
+ * alignment; R_k and R_v need not be orthogonal here. */
 kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, int H_kv, int d,
                            const int32_t* slot_mapping, const float* mu_k,
                            const float* R_k, const float* R_v, float clip,
@@ -343,8 +343,8 @@ kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int H_kv, int 
  * logits of every query head, 64 * H_q * B * max_pages_per_seq bytes).
  * num_splits as passed to the call (0 = automatic on the current device).  The
  * workspace must be zero-filled once before its first use.  Calls (and captured
- * graphs) that may overlap on the GPU need a workspace each.  Its error word is read by kvq_workspace_status.
- * Returns 0 for invalid sizes. */
+ * graphs) that may overlap on the GPU need a workspace each.  Its error word is
+ * read by kvq_workspace_status.  Returns 0 for sizes that the call refuses. */
 size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq, int num_splits,
                                 int weights);
 
@@ -352,9 +352,19 @@ size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq,
  *   o = softmax(<q R_k, K^> * scale) V^ R_v^T,  K^, V^ the cached values.
  *   q    device bf16 [B][H_q][d]
  *   out  device bf16 [B][H_q][d], rounded once (zeros for an empty context)
- * Other arguments, the split of the work, and the treatment of block-table
- * entries outside [0, num_pages) as kvq_decode_attn_int2.  q and out need
- * 16-byte alignment. */
+ *   R_k, R_v  device fp32 [H_kv][d][d], rotations (q R_k may be up to 15 times
+ *             as long as q; beyond that its fp16 operands can overflow)
+ *   num_splits  CTAs per (sequence, KV head), at most 254; 0: one CTA per SM in
+ *             all, or fewer for a short batch.  The pages that the context
+ *             lengths name are shared out evenly among them on the device, so
+ *             the result's last bits depend on num_splits, the lengths and the
+ *             number of SMs, and on nothing else
+ * Other arguments and the treatment of block-table entries outside
+ * [0, num_pages) as kvq_decode_attn_int2; context_lens is clamped to
+ * [0, 16 * max_pages_per_seq].  q, cache, R_k, R_v, out and workspace need
+ * 16-byte alignment.  H_q / H_kv <= 8, B and H_kv <= 65535, B * H_kv <= 2^24,
+ * max_pages_per_seq < 2^27, B * H_kv * max_pages_per_seq <= 2^36,
+ * num_splits * B * H_kv <= 2^22, num_pages * H_kv <= 2^32. */
 kvq_status kvq_decode_attn_int4(const void* q, int B, int H_q, int H_kv, int d,
                                 const void* cache, int64_t num_pages,
                                 const int32_t* block_table, int max_pages_per_seq,
@@ -391,7 +401,8 @@ kvq_status kvq_decode_attn_int4_weights(const void* q, int B, int H_q, int H_kv,
  *   keep      device int32 [B][H_kv][budget], written: the kept indices in
  *             ascending order, then -1
  *   new_lens  device int32 [B], written: min(n, budget)
- * 1 <= budget, 0 <= sinks, 0 <= recent, sinks + recent <= budget. */
+ * 1 <= budget, 0 <= sinks, 0 <= recent, sinks + recent <= budget,
+ * max_tokens <= 2^30, B and H_kv <= 65535. */
 kvq_status kvq_evict_select(const float* weights, int64_t weights_stride, int B, int H_kv, int max_tokens,
                             const int32_t* context_lens, int budget, int sinks, int recent,
                             int32_t* keep, int32_t* new_lens, void* stream);

@@ -29,6 +29,7 @@ def _refused(lib, st, status, text):
     (dict(H_kv=70000), UNSUPPORTED, "too large"), (dict(num_pages=0), INVALID, "num_pages=0"),
     (dict(clip=0.0), INVALID, "clip"), (dict(clip=1.01), INVALID, "clip"), (dict(clip=float("nan")), INVALID, "clip"),
     (dict(k=None), INVALID, "null"), (dict(cache=MIS), INVALID, "aligned"),
+    (dict(k=MIS), INVALID, "aligned"),
 ])
 def test_append_refuses(lib, kw, status, text):
     a = dict(k=A, n=4, H_kv=1, d=128, clip=1.0, cache=A, num_pages=4) | kw
@@ -47,8 +48,9 @@ def test_empty_append_and_read_are_no_ops(lib):
 @host_only
 @pytest.mark.parametrize("kw,status,text", [
     (dict(d=64), UNSUPPORTED, "d=64"), (dict(B=0), INVALID, "B=0"), (dict(H_q=6, H_kv=4), INVALID, "H_q=6"),
-    (dict(H_q=9), UNSUPPORTED, "group 9"), (dict(max_pages=1 << 27), UNSUPPORTED, "2^27"),
-    (dict(splits=255), INVALID, "255"), (dict(splits=-1), INVALID, "splits=-1"), (dict(q=None), INVALID, "null"),
+    (dict(H_q=9), UNSUPPORTED, "group above 8"), (dict(max_pages=1 << 27), UNSUPPORTED, "2^27"),
+    (dict(splits=255), INVALID, "above 254"), (dict(B=60000, H_kv=300, H_q=300), UNSUPPORTED, "2^24"),
+    (dict(B=60000, splits=100), UNSUPPORTED, "2^22"), (dict(B=60000, max_pages=1 << 26), UNSUPPORTED, "2^36"), (dict(splits=-1), INVALID, "splits=-1"), (dict(q=None), INVALID, "null"),
     (dict(out=MIS), INVALID, "alignment"), (dict(ws=MIS), INVALID, "alignment"), (dict(ws_bytes=64), WORKSPACE, "workspace"),
     (dict(B=70000), UNSUPPORTED, "65535"), (dict(w=None), INVALID, "null"), (dict(stride=63), INVALID, "weights_stride"),
     (dict(decay=-0.5), INVALID, "decay"), (dict(decay=float("nan")), INVALID, "decay"),
@@ -70,7 +72,8 @@ def test_workspace_bytes(lib):
     # the weights form holds 16 * 100 logits of every query head more
     assert _lib.kvq_int4_workspace_bytes(1, 8, 2, 100, 3, True) >= _lib.kvq_int4_workspace_bytes(1, 8, 2, 100, 3) + 4 * 8 * 1600
     for bad in ((0, 8, 2, 100, 0), (1, 7, 2, 100, 0), (1, 8, 2, 0, 0), (1, 8, 2, 100, -1), (1, 8, 2, 100, 255),
-                (1, 8, 2, 1 << 27, 0)):
+                (1, 8, 2, 1 << 27, 0), (1, 9, 1, 100, 0), (60000, 300, 300, 1, 0), (60000, 1, 1, 1, 100),
+                (60000, 1, 1, 1 << 26, 0), (70000, 1, 1, 1, 0)):
         assert _lib.kvq_int4_workspace_bytes(*bad) == 0
     assert _lib.kvq_int4_tile_bytes(128) == 2560 and _lib.kvq_int4_tile_bytes(64) == 0
 
@@ -81,6 +84,7 @@ def test_workspace_bytes(lib):
     (dict(recent=-2), INVALID, "recent=-2"), (dict(sinks=5, recent=4), INVALID, "above the budget"),
     (dict(sinks=2**31 - 1, recent=2**31 - 1), INVALID, "above the budget"), (dict(stride=99), INVALID, "weights_stride"),
     (dict(w=None), INVALID, "null"), (dict(B=70000), UNSUPPORTED, "65535"),
+    (dict(T=(1 << 30) + 1, stride=1 << 31), UNSUPPORTED, "2^30"),
 ])
 def test_select_refuses(lib, kw, status, text):
     a = dict(w=A, stride=100, B=1, H_kv=1, T=100, budget=8, sinks=1, recent=1) | kw
@@ -126,6 +130,8 @@ def test_binding_checks_shapes_types_and_device():
             _lib.kvq_decode_attn_int4(*args)
     with pytest.raises(ValueError, match="weights must have shape"):
         _lib.kvq_decode_attn_int4_weights(q, cache, 4, bt, lens, R, R, 0.1, out, _t(1, 1, 64), 1.0, ws)
+    with pytest.raises(ValueError, match="err_count must have"):
+        _lib.kvq_append_int4(k, k, slots, mu, R, R, cache, 4, 1.0, _t(0, dtype=i32))
     with pytest.raises(ValueError, match="keep"):
         _lib.kvq_evict_select(_t(1, 2, 64), lens, 8, 0, 0, _t(1, 2, 9, dtype=i32), lens)
     keep = _t(1, 2, 8, dtype=i32)
