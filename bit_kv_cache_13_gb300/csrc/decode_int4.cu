@@ -419,11 +419,13 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         V = P * a.H_kv;
         int64_t C = gridDim.x;
         if (a.automatic) {
-            C = min(C, (V + D4_MIN_PAGES - 1) / D4_MIN_PAGES);
+            const int64_t units = (int64_t)ne * a.H_kv;
+            // (a CTA for each unit if there are as many: 19 sequences of one page in one CTA
+            // took 88 us, a unit after the other)
+            C = min(C, max((V + D4_MIN_PAGES - 1) / D4_MIN_PAGES, units));
             extra = D4_SEG_PAGES;
             // sequences of one length: a whole number of CTAs per unit, each in one
             // unit only, where that streams little more than equal shares would
-            const int64_t units = (int64_t)ne * a.H_kv;
             if (units > 0 && units <= C && (int64_t)ne * mx == P) {
                 const int64_t k = C / units;
                 if ((mx + k - 1) / k <= V / C + D4_SEG_PAGES) {
