@@ -35,7 +35,8 @@
 //              launch turn the logits that the stream left into token weights
 // Rotating inside the streaming CTAs cost each (sequence, KV head) that a CTA
 // touches about 7 us during which it streamed nothing (32 ragged sequences up to
-// 4K, 8 KV heads: 166 us).  The stream kernel's warps never wait for one another:
+// 4K, 8 KV heads: 166 us); where each CTA has one unit only, all three steps in one
+// kernel are quicker instead (below, ONE).  The stream kernel's warps never wait for one another:
 // each walks the CTA's units by itself, its ring running ahead into the next
 // unit's pages; the last warp to leave a unit merges its warps' partials, which
 // stand in ring slots of their own until then.
@@ -63,6 +64,7 @@ struct D4Cfg {
 constexpr int D4_MAX_SPLITS = 254;
 constexpr int D4_MIN_PAGES = 24;   // pages per CTA below which an automatic split goes no further: a unit a warp
 constexpr int D4_SEG_PAGES = 40;   // what starting another unit costs a CTA, in pages streamed
+constexpr int D4_ONE_PAGES = 96;   // pages per CTA up to which a few sequences go without an even split
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
 
 __device__ __forceinline__ float d4_ex2(float x) {
@@ -315,7 +317,7 @@ struct __align__(128) D4Smem {
     int scan_max[NW], scan_n[NW];
     int64_t base0;
     int b0, is_last;
-    // one sequence: the query's rotation and the unit's end, in this kernel
+    // ONE: the query's rotation and the unit's end, in this kernel
     __align__(16) float qin[4 * NT][D];  // (these three are read as float4)
     __align__(16) float red[3][4 * NT][D];
     __align__(16) float qs[4 * NT][D];
@@ -330,9 +332,9 @@ static_assert(sizeof(D4Smem<1>) <= 227 * 1024 && sizeof(D4Smem<2>) <= 227 * 1024
 static_assert(4 * D * 4 <= D4Cfg<1>::U * INT4_TILE && 8 * D * 4 <= D4Cfg<2>::U * INT4_TILE, "a warp's partial fits one ring group");
 
 // NT = 1: up to four query heads per KV head, NT = 2: up to eight.  ONE: the form
-// for one sequence, whole in this kernel: every CTA works on one KV head, rotates
+// for one or a few sequences, whole in this kernel: every CTA works on one unit, rotates
 // its queries itself (before its first copies are out, so the rotation does not wait
-// behind them) and the last CTA of a head finishes it.
+// behind them) and the last CTA of a unit finishes it.
 template <int NT, bool WTS, bool ONE>
 __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(const __grid_constant__ D4Args a) {
     constexpr int NW = D4Cfg<NT>::NW, U = D4Cfg<NT>::U, UNITS = D4Cfg<NT>::UNITS;
@@ -357,21 +359,23 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     // block table and cache are read before the dependency wait: the rotate kernel
     // let this one start only after its own wait, when everything before it was done.
     int64_t V = 0, g0 = 0;
-    int Ceff = 0, share = 0, extra = 0;  // extra: pages without work after each unit's, for the cost of starting it
+    int Ceff = 0, share = 0, part = 0, extra = 0;  // extra: pages without work after each unit's, for the cost of starting it
     D4Walk cs;  // what this warp consumes
     if constexpr (ONE) {
         griddep_wait();  // (no rotate kernel ran before)
-        cs.b = cs.left = 0;
-        cs.np = d4_pages(a, 0);
+        // a whole number of CTAs per unit, as many of them as its pages deserve
+        const int most = gridDim.x / (a.B * a.H_kv), unit = cta / most;
+        part = cta % most;
+        cs.b = unit / a.H_kv;
+        cs.h = unit % a.H_kv;
+        cs.left = 0;
+        cs.np = d4_pages(a, cs.b);
         if (cs.np == 0) {
-            for (int i = cta * NW * 32 + tid; i < a.H_q * D; i += gridDim.x * NW * 32) a.out[i] = __float2bfloat16_rn(0.f);
+            for (int i = tid; i < G * D && part == 0; i += NW * 32) a.out[(size_t)unit * G * D + i] = __float2bfloat16_rn(0.f);
             return;
         }
-        // a whole number of CTAs per head
-        Ceff = min((int)gridDim.x / a.H_kv, (cs.np + D4_MIN_PAGES - 1) / D4_MIN_PAGES);  // per head
-        cs.h = cta / Ceff;
-        if (cs.h >= a.H_kv) return;
-        const int part = cta % Ceff;
+        Ceff = min(most, (cs.np + D4_MIN_PAGES - 1) / D4_MIN_PAGES);  // of the unit
+        if (part >= Ceff) return;
         cs.pa = (int)((int64_t)part * cs.np / Ceff);
         cs.pb = cs.end = (int)((int64_t)(part + 1) * cs.np / Ceff);
     } else {
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         const int i0 = (tid >> 7) * ROWS;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) rr[i] = i0 + i < D ? __ldg(R + (size_t)(i0 + i) * D) : 0.f;
-        const __nv_bfloat16* qb = a.q + (size_t)cs.h * G * D;
+        const __nv_bfloat16* qb = a.q + ((size_t)cs.b * a.H_kv + cs.h) * G * D;
 #pragma unroll
         for (int i = 0; i < (MAXG * D + NW * 32 - 1) / (NW * 32); ++i) {
             const int x = tid + i * NW * 32;
@@ -1035,7 +1039,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 }
                 if (c4 == 0) *reinterpret_cast<float2*>(slot + (size_t)j * PART_STRIDE) = make_float2(M, L);
             }
-            if (WTS && tid == 0 && cta == cs.h * Ceff) a.info[u] = make_int2(cta, Ceff);
+            if (WTS && tid == 0 && part == 0) a.info[u] = make_int2(cta, Ceff);
             __syncthreads();
             if (Ceff > 1) {
                 int32_t* ticket = reinterpret_cast<int32_t*>(a.ws + WS_HEADER) + u;
@@ -1045,7 +1049,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 if (tid == 0) *ticket = 0;
                 // warp (part, head): partials part, part + P, ..., four channels a lane
                 const int P = NW / G, j = warp % G, p = warp / G;
-                const float* ps = a.partials + (u + (size_t)cs.h * Ceff) * step + (size_t)j * PART_STRIDE;
+                const float* ps = a.partials + (u + cta - part) * step + (size_t)j * PART_STRIDE;
                 if (p < P) {
                     constexpr int CH = 8;
                     float M = D4_NEG, L = 0.f;
@@ -1102,7 +1106,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 float4 rv[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) rv[i] = __ldg(reinterpret_cast<const float4*>(R + (size_t)i * D));
-                __nv_bfloat16* o = a.out + (size_t)cs.h * G * D + 16 * warp;
+                __nv_bfloat16* o = a.out + u * G * D + 16 * warp;
 #pragma unroll 1
                 for (int jj = 0; jj < G; ++jj) d4_rotate_rows<16>(*reinterpret_cast<const float4*>(&sm.qs[jj][4 * lane]), rv, lane, o + (size_t)jj * D);
             }
@@ -1474,8 +1478,17 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int nsm = kvq_device_sm_count();
     const int64_t units = (int64_t)B * H_kv;
-    // one sequence and a few heads: one kernel (the weights form: and the weights)
-    const bool one = num_splits == 0 && B == 1 && 4 * H_kv <= nsm;
+    // A few units: one kernel (in the weights form, and the weights' one), whose CTAs have one
+    // unit each.  Lengths differ, so of several sequences none may have more than
+    // D4_ONE_PAGES pages for each of its CTAs.  8 sequences of 300 tokens, 8 KV heads: 8.7 us
+    // against 12.5 in three kernels, 16 of up to 1500 16.7 against 23.9; 3 of up to 8000
+    // (84 pages a CTA) 15.5 against 14.1.  In the weights form, where the third kernel runs
+    // anyway and would have merged the partials, only up to two CTAs per unit: 8 of 700 tokens
+    // 14.0 against 16.0 us, but one of 2048 13.9 against 13.0.
+    const int per_unit = (int)(nsm / units);
+    const bool small = max_pages <= (int64_t)D4_ONE_PAGES * per_unit;
+    const bool one = num_splits == 0 && per_unit >= 1 &&
+                     (with_weights ? small && per_unit <= 2 : small || (B == 1 && per_unit >= 4));
     if (!one) {
         // 1: one sequence a CTA, up to eight CTAs per SM
         const int per = (int)((4 * units + 8 * nsm - 1) / (8 * nsm));
@@ -1494,7 +1507,7 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const size_t smem = G <= 4 ? sizeof(D4Smem<1>) : sizeof(D4Smem<2>);
     st = d4_smem_once((const void*)kerns[which], (int)smem, which);
     if (st != KVQ_OK) return st;
-    st = kvq_check_cuda(launch_pdl(kerns[which], dim3((unsigned)C), dim3(32 * (G <= 4 ? D4Cfg<1>::NW : D4Cfg<2>::NW)), smem, cs, a),
+    st = kvq_check_cuda(launch_pdl(kerns[which], dim3(one ? (unsigned)(units * per_unit) : (unsigned)C), dim3(32 * (G <= 4 ? D4Cfg<1>::NW : D4Cfg<2>::NW)), smem, cs, a),
                         "kvq_decode_attn_int4 launch");
     if (st != KVQ_OK || (one && !with_weights)) return st;
     // 3: few units are finished by four CTAs each (a quarter of R_v each), and

@@ -356,9 +356,10 @@ size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq,
  *             as long as q; beyond that its fp16 operands can overflow)
  *   num_splits  CTAs per (sequence, KV head), at most 254; 0: one CTA per SM in
  *             all, or fewer for a short batch.  The pages that the context
- *             lengths name are shared out evenly among them on the device, so
- *             the result's last bits depend on num_splits, the lengths and the
- *             number of SMs, and on nothing else
+ *             lengths name are shared out among them on the device.  A call
+ *             repeated gives the same bits; another num_splits, batch, table
+ *             width, number of SMs or (with 0) form of the call may round its
+ *             sums in another order
  * Other arguments and the treatment of block-table entries outside
  * [0, num_pages) as kvq_decode_attn_int2; context_lens is clamped to
  * [0, 16 * max_pages_per_seq].  q, cache, R_k, R_v, out and workspace need

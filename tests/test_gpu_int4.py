@@ -243,6 +243,32 @@ def test_weights_match_oracle(h_q, h_kv, ctxs, splits, decay):
     c.check(got, w, decay)
 
 
+# batches on both sides of where one kernel's CTAs have a unit each: 160 units; 80 with up to 128 pages; 48 of one page;
+# two heads of a long and two short sequences; 152 units (a CTA each)
+BATCHES = [(16, 8, [(37 * i) % 130 for i in range(20)]), (8, 4, [(811 * i) % 2047 for i in range(20)]),
+           (6, 6, [1 + i % 16 for i in range(8)]), (10, 2, [20000, 17, 0]), (38, 19, [3, 90, 16, 0, 40, 1, 17, 200])]
+
+
+@pytest.mark.parametrize("h_q,h_kv,ctxs", BATCHES)
+@pytest.mark.parametrize("decay", [None, 1.0])
+def test_batches_match_oracle(h_q, h_kv, ctxs, decay):
+    c = _Case(h_q, h_kv, ctxs, seed=2)
+    got, w = c.run(0, decay)
+    assert c.status == 0
+    c.check(got, w, decay or 1.0)
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("g", [4, 8])
+def test_bad_pages_in_a_given_split(g, splits):
+    c = _Case(2 * g, 2, [500, 40, 20])
+    bt = c.bt.copy()
+    bt[0, 3], bt[0, 31], bt[1, :], bt[2, 1] = -1, c.num_pages, 1 << 30, -7   # sequence 1 loses every page
+    got, w = c.run(splits, 1.0, bt=bt)
+    assert c.status == -5
+    c.check(got, w, bt=bt)
+
+
 @pytest.mark.parametrize("g", [4, 8])
 def test_bad_pages_are_dropped_and_reported(g):
     c = _Case(2 * g, 2, [500, 40, 20])
@@ -360,9 +386,13 @@ def test_prefill_then_decode_through_the_layer():
     q, out = layer.queries(), torch.empty((2, 16, 128), dtype=torch.bfloat16, device="cuda")
     ws = layer.workspace()
     layer.decode(q, out, ws, decay=1.0)
-    plain = torch.empty_like(out)
+    plain, split, split_w = (torch.empty_like(out) for _ in range(3))
     layer.decode(q, plain, ws)
-    assert torch.equal(out, plain)
+    keep, ws2 = layer.weights.clone(), layer.workspace(2)
+    layer.decode(q, split, ws2, 2)
+    layer.decode(q, split_w, ws2, 2, decay=1.0)
+    layer.weights = keep
+    assert torch.equal(split, split_w)  # (the same split: the same sums)
     f = lambda x: x.cpu().double().numpy()  # noqa: E731
     cache = int4.new_cache(layer.num_pages, 2)
     for b in range(2):
@@ -374,7 +404,8 @@ def test_prefill_then_decode_through_the_layer():
     for b in range(2):
         for j in range(16):
             # 2^-8 for bf16, 2^-10 of terms that are a few times the result
-            assert np.linalg.norm(f(out)[b, j] - ref[b, j]) <= 2.0 ** -7 * np.linalg.norm(ref[b, j])
+            for o in (out, plain, split):
+                assert np.linalg.norm(f(o)[b, j] - ref[b, j]) <= 2.0 ** -7 * np.linalg.norm(ref[b, j])
     # 16 heads of two sequences, each with weights that add up to 1 (two calls of one step: only the first accumulates)
     assert abs(float(layer.weights.double().sum()) - 2 * 16) <= 32 * 2.0 ** -15
 
