@@ -290,7 +290,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
     griddep_wait();
     griddep_launch_dependents();
 
-    const int tiles = (n_tok + PF_M - 1) / PF_M, stride = (side ? gridDim.x - key_ctas : key_ctas) * PF_WORKERS;
+    const int tiles = (n_tok + PF_M - 1) / PF_M, ctas = side ? gridDim.x - key_ctas : key_ctas, stride = ctas * PF_WORKERS;
     const __nv_bfloat16* src = side ? v : k;
     const int64_t n_slots = num_pages * PAGE;
     auto worker_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(worker + 1) : "memory"); };
@@ -314,7 +314,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             wk.slot[buf][tid] = s;
         }
     };
-    const int x_first = (blockIdx.x - (side ? key_ctas : 0)) * PF_WORKERS + worker;
+    const int x_first = blockIdx.x - (side ? key_ctas : 0) + worker * ctas;  // (few tiles: on as many SMs as there are)
     if (x_first < tiles) fetch(x_first, 0);
     // R's parts as operands: column n of set i of a group is channel 8 (n / 2) + 2 i + n % 2 of it
 #pragma unroll 2
@@ -702,7 +702,7 @@ extern "C" size_t kvq_int4_tile_bytes(int d) { return d == D ? (size_t)INT4_TILE
 // Token-heads from which on the tensor-core kernel is taken, for each wave of its CTAs:
 // it starts in about 12 us a wave (R's operand parts), the few-token kernel takes 0.03 us a
 // token-head.  With the read-back: 33 tokens of 8 heads 14.5 against 11.2 us, 64 tokens of
-// one head 13.4 against 5.2, 128 of two 18.0 against 11.6, 64 of 8 15.4 against 17.8, 128 of
+// one head 13.4 against 5.2, 128 of two 18.0 against 11.6, 64 of 8 14.2 against 17.8, 128 of
 // 8 19.5 against 30.8.
 static constexpr int PREFILL_MIN = 400;
 
@@ -753,20 +753,20 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
     // per worker (32K tokens, 8 heads, with read-back: 317 us for equal halves, 290 us).
     const int tiles = (n_tok + PF_M - 1) / PF_M, most = nsm / H_kv;
     auto rounds = [&](int ctas) { return (int)((tiles + (int64_t)ctas * PF_WORKERS - 1) / ((int64_t)ctas * PF_WORKERS)); };
-    int nk = 1, nv = 1;
+    int nk = 1;
     int64_t best = INT64_MAX;
+    float best_even = 0.f;
     for (int x = 1; x < most; ++x) {
         const int64_t cost = std::max((int64_t)PF_KEY_COST * rounds(x), (int64_t)PF_VALUE_COST * rounds(most - x));
-        if (cost < best) {
+        const float even = std::max((float)PF_KEY_COST / x, (float)PF_VALUE_COST / (most - x));
+        if (cost < best || (cost == best && even < best_even)) {
             best = cost;
+            best_even = even;
             nk = x;
-            nv = most - x;
         }
     }
-    // (no more CTAs than those rounds need)
-    auto trim = [&](int ctas) { return (int)((tiles + (int64_t)rounds(ctas) * PF_WORKERS - 1) / ((int64_t)rounds(ctas) * PF_WORKERS)); };
-    nk = trim(nk);
-    nv = trim(nv);
+    const int nv = std::min(tiles, std::max(1, most - nk));
+    nk = std::min(tiles, nk);
     return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(nk + nv, H_kv), dim3(PF_WORKERS * 128),
                                      sizeof(PrefillSmem), st, kb, vb, n_tok, H_kv, slot_mapping, mu_k, R_k, R_v, cb, num_pages,
                                      err_count, clip, nk),
