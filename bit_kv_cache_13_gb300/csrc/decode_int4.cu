@@ -4,7 +4,9 @@
 //   q' = q R_k;  a_s = <q', K^_s> scale;  p = softmax(a);  o = (sum_s p_s V^_s) R_v^T
 //
 // Bound by the 160 bytes of packed cache per token-head, if the instructions
-// that unpack them fit under the stream: one CTA of 12 or 16 warps per SM, every warp
+// that unpack them fit under the stream (32 q / 8 KV heads, batch 1, 128K: 34 us, 5.0 TB/s;
+// batch 8, 32K: 65.6 us, 5.1 TB/s; from 128K to 256K tokens another 24 us, 6.9 TB/s: the
+// rest is the launch, the rotations, the merge).  One CTA of 12 warps per SM, every warp
 // streaming pages through a ring of its own (bulk copies, one mbarrier per unit
 // of one or two pages), all products on mma.sync m16n8k16 with the codes as operands.
 //
@@ -44,7 +46,9 @@
 // The work is split over the CTAs on the device, by the real page counts: the
 // pages of all (sequence, KV head) units are laid end to end and every CTA takes
 // an equal share, so a ragged batch or a short context in a long table stays
-// balanced.
+// balanced.  With eight heads to a KV head the instructions bound it: 32 ragged
+// sequences of up to 4K, 64 q / 8 KV heads, 47.5 us for 84 MB, of which the pages 20 us
+// (62 % issue), the start of the chain 10, merging and finishing 12.
 #include <cstddef>
 #include <mutex>
 
@@ -1483,12 +1487,14 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     // D4_ONE_PAGES pages for each of its CTAs.  8 sequences of 300 tokens, 8 KV heads: 8.7 us
     // against 12.5 in three kernels, 16 of up to 1500 16.7 against 23.9; 3 of up to 8000
     // (84 pages a CTA) 15.5 against 14.1.  In the weights form, where the third kernel runs
-    // anyway and would have merged the partials, only up to two CTAs per unit: 8 of 700 tokens
-    // 14.0 against 16.0 us, but one of 2048 13.9 against 13.0.
+    // anyway and would have merged the partials, only up to two CTAs per unit (8 of 700 tokens
+    // 14.0 against 16.0 us, but 4 of up to 1959 with 4 heads 17.2 against 15.5) and for a single
+    // sequence (2048 tokens: 13.9 against 13.0 us in a graph, but 14.9 against 16.7 when each
+    // launch is paid for on the host).
     const int per_unit = (int)(nsm / units);
     const bool small = max_pages <= (int64_t)D4_ONE_PAGES * per_unit;
     const bool one = num_splits == 0 && per_unit >= 1 &&
-                     (with_weights ? small && per_unit <= 2 : small || (B == 1 && per_unit >= 4));
+                     ((small && (!with_weights || per_unit <= 2)) || (B == 1 && per_unit >= 4));
     if (!one) {
         // 1: one sequence a CTA, up to eight CTAs per SM
         const int per = (int)((4 * units + 8 * nsm - 1) / (8 * nsm));
