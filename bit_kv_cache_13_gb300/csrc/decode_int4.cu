@@ -1370,13 +1370,17 @@ static int64_t d4_ctas(int B, int H_kv, int num_splits) {
     return num_splits > 0 ? (int64_t)num_splits * B * H_kv : kvq_device_sm_count();
 }
 
+// (The tickets stand at one place whatever the shape, so that what a call of another
+// shape left in the workspace is never taken for one.)
+constexpr int D4_TICKETS = 1024;
+
 struct D4Layout {
     size_t query, info, partials, logits, total;
 };
 static D4Layout d4_layout(int B, int H_q, int H_kv, int max_pages, int64_t C, bool weights) {
     const size_t units = (size_t)B * H_kv, G = (size_t)(H_q / H_kv);
     D4Layout l;
-    l.query = WS_HEADER + tickets_bytes(B, H_kv);
+    l.query = WS_HEADER + D4_TICKETS * 4;
     l.info = align_up(l.query + units * (G <= 4 ? sizeof(D4Query<1>) : sizeof(D4Query<2>)), 256);
     l.partials = align_up(l.info + units * sizeof(int2), 256);
     l.logits = align_up(l.partials + (units + (size_t)C) * G * PART_STRIDE * 4, 256);  // a slot per (unit + CTA)
@@ -1493,7 +1497,7 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     // launch is paid for on the host).
     const int per_unit = (int)(nsm / units);
     const bool small = max_pages <= (int64_t)D4_ONE_PAGES * per_unit;
-    const bool one = num_splits == 0 && per_unit >= 1 &&
+    const bool one = num_splits == 0 && per_unit >= 1 && units <= D4_TICKETS &&
                      ((small && (!with_weights || per_unit <= 2)) || (B == 1 && per_unit >= 4));
     if (!one) {
         // 1: one sequence a CTA, up to eight CTAs per SM

@@ -344,7 +344,9 @@ kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int H_kv, int 
  * num_splits as passed to the call (0 = automatic on the current device).  The
  * workspace must be zero-filled once before its first use.  Calls (and captured
  * graphs) that may overlap on the GPU need a workspace each.  Its error word is
- * read by kvq_workspace_status.  Returns 0 for sizes that the call refuses. */
+ * read by kvq_workspace_status.  A workspace may serve calls of any shape and form
+ * that it is large enough for, one after another.  Returns 0 for sizes that the
+ * call refuses. */
 size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq, int num_splits,
                                 int weights);
 

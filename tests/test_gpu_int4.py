@@ -164,10 +164,11 @@ class _Case:
         self.q = _bf(rng.standard_normal((self.B, h_q, 128)) * q_scale)
         self.w0 = rng.random((self.B, h_kv, self.P * 16 + 5)).astype(np.float32)
 
-    def run(self, splits=0, decay=None, ctx=None, bt=None):
+    def run(self, splits=0, decay=None, ctx=None, bt=None, ws=None):
         out = torch.full((self.B, self.h_q, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
-        ws = torch.zeros(_lib.kvq_int4_workspace_bytes(self.B, self.h_q, self.h_kv, self.P, splits, decay is not None),
-                         dtype=torch.uint8, device="cuda")
+        if ws is None:
+            ws = torch.zeros(_lib.kvq_int4_workspace_bytes(self.B, self.h_q, self.h_kv, self.P, splits, decay is not None),
+                             dtype=torch.uint8, device="cuda")
         args = (self.q.cuda(), _dev(self.gpu), self.num_pages, _dev(self.bt if bt is None else bt),
                 _dev(self.ctx if ctx is None else ctx), _dev(self.rk), _dev(self.rv), SCALE, out)
         w = None
@@ -375,6 +376,22 @@ def test_repeated_calls_give_the_same_bits():
         for _ in range(3):
             b, wb = c.run(0, 1.0)
             assert np.array_equal(a, b) and np.array_equal(wa, wb)
+
+
+def test_one_workspace_serves_calls_of_every_shape():
+    """Batches that grow and shrink, with and without weights and a given split, in one workspace: each call's bits are
+    those of a call with a workspace of its own."""
+    cases = [(_Case(8, 1, [100], seed=6), 3), (_Case(32, 8, [40] * 19, seed=6), 0), (_Case(16, 8, [50] * 30, seed=6), 0),
+             (_Case(32, 8, [70] * 9, seed=6), 0), (_Case(8, 1, [900], seed=6), 0), (_Case(64, 8, [33] * 12, seed=6), 0)]
+    size = lambda c, s, w: _lib.kvq_int4_workspace_bytes(c.B, c.h_q, c.h_kv, c.P, s, w)  # noqa: E731
+    ws = torch.zeros(max(size(c, s, True) for c, s in cases), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for c, splits in cases:
+            for decay in (None, 1.0):
+                want, w_want = c.run(splits, decay)
+                got, w_got = c.run(splits, decay, ws=ws)
+                assert c.status == 0 and np.array_equal(got, want)
+                assert decay is None or np.array_equal(w_got, w_want)
 
 
 def test_prefill_then_decode_through_the_layer():
