@@ -369,6 +369,37 @@ def test_inputs_written_by_the_kernel_just_before():
         c.check(out.double().cpu().numpy(), buf[6].double().cpu().numpy())
 
 
+@pytest.mark.parametrize("n", [30, 900])
+@pytest.mark.parametrize("splits", [0, 2])
+def test_a_chain_of_calls_without_a_pause(n, splits):
+    """Append, decode, append over the same slots, decode: each call sees the one before, on a stream of its own too."""
+    rng = np.random.default_rng(n)
+    h, P = 2, (n + 15) // 16
+    mu, rk, rv = _dev(rng.standard_normal((h, 128)).astype(np.float32)), _dev(_rot(rng, h)), _dev(_rot(rng, h))
+    kv = [(_bf(rng.standard_normal((n, h, 128))).cuda(), _bf(rng.standard_normal((n, h, 128))).cuda()) for _ in range(2)]
+    q, slots = _bf(2 * rng.standard_normal((1, 8, 128))).cuda(), torch.arange(n, dtype=torch.int32, device="cuda")
+    bt, ctx = torch.arange(P, dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda")
+    cache = torch.zeros((P, h, 2560), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(_lib.kvq_int4_workspace_bytes(1, 8, h, P, splits), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((1, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+
+    def run(outs, pause, stream=None):
+        for i, out in enumerate(outs):
+            _lib.kvq_append_int4(*kv[i % 2], slots, mu, rk, rv, cache, P, stream=stream)
+            pause()
+            _lib.kvq_decode_attn_int4(q, cache, P, bt, ctx, rk, rv, SCALE, out, ws, splits, stream=stream)
+            pause()
+
+    run(outs[:2], torch.cuda.synchronize)
+    own = torch.cuda.Stream()
+    run(outs[2:6], lambda: None, own)
+    own.synchronize()
+    run(outs[6:], lambda: None)
+    torch.cuda.synchronize()
+    assert not torch.equal(outs[0], outs[1])
+    assert all(torch.equal(x, outs[i % 2]) for i, x in enumerate(outs))
+
+
 def test_repeated_calls_give_the_same_bits():
     for h_q in (32, 64):
         c = _Case(h_q, 8, [1500, 700], seed=4)
