@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <cstddef>
 #include <mutex>
-#include <type_traits>
 
 #include "int4_common.cuh"
 

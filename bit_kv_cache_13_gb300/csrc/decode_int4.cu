@@ -4,8 +4,8 @@
 //   q' = q R_k;  a_s = <q', K^_s> scale;  p = softmax(a);  o = (sum_s p_s V^_s) R_v^T
 //
 // Bound by the 160 bytes of packed cache per token-head, if the instructions
-// that unpack them fit under the stream (32 q / 8 KV heads, batch 1, 128K: 34 us, 5.0 TB/s;
-// batch 8, 32K: 65.6 us, 5.1 TB/s; from 128K to 256K tokens another 24 us, 6.9 TB/s: the
+// that unpack them fit under the stream (32 q / 8 KV heads, batch 1, 128K: 34 us, 4.9 TB/s;
+// batch 8, 32K: 64.6 us, 5.2 TB/s; from 128K to 256K tokens another 24 us, 6.9 TB/s: the
 // rest is the launch, the rotations, the merge).  One CTA of 12 warps per SM, every warp
 // streaming pages through a ring of its own (bulk copies, one mbarrier per unit
 // of one or two pages), all products on mma.sync m16n8k16 with the codes as operands.
@@ -67,7 +67,10 @@ struct D4Cfg {
 };
 constexpr int D4_MAX_SPLITS = 254;
 constexpr int D4_MIN_PAGES = 24;   // pages per CTA below which an automatic split goes no further: a unit a warp
-constexpr int D4_SEG_PAGES = 40;   // what starting another unit costs a CTA, in pages streamed
+// What starting another unit costs a CTA, in pages streamed.  30 ragged sequences of up to
+// 8000 tokens, 64 q / 8 KV heads: 87 us for 10, 76 for 20, 64.2 for 40, 60.7 for 60, 62.2 for
+// 110; 32 of up to 4000, 32 q heads: 54.8, 46.6, 37.1, 36.9, 38.2.
+constexpr int D4_SEG_PAGES = 60;
 constexpr int D4_ONE_PAGES = 96;   // pages per CTA up to which a few sequences go without an even split
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
 
