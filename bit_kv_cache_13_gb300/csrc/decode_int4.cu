@@ -20,13 +20,21 @@
 //           low part (22 bits): for up to four heads the parts sit side by side in the
 //           eight columns, for up to eight they are two MMAs into one accumulator.
 //   softmax base 2, against the running maximum of each head; the maximum is
-//           raised (and the accumulators rescaled) only when a logit exceeds it, which
+//           raised (and the weights rescaled) only when a logit exceeds it, which
 //           one vote per unit decides.  Sums are fp32 of the unrounded p.
 //   PV      rows = 16 channels, K = 16 tokens, columns = heads; the second operand is
-//           fp16(fp16(p) * scale_{token, group}): two roundings of 2^-11 of a term, below
-//           the output's bf16 rounding; p transposes from the QK layout by movmatrix.
-//           Up to four heads fill the eight columns as (tokens 0..7, tokens 8..15) of
-//           each head, which the end adds.  The mins are one more MMA.
+//           fp16(fp16(P) * scale_{token, group} / size): two roundings of 2^-11 of a term,
+//           below the output's bf16 rounding.  A token's size is a power of two next
+//           below the largest of its four scales and |mins|, and P = p * size * F, F such
+//           that the largest P so far stays within [2^11, 2^13] (each head's F falls
+//           when a P exceeds 2^13, and rises when the running maximum does).  So no
+//           operand overflows, and what fp16 cuts off below 2^-24 is 2^-31 of the context's
+//           largest term, however small or large the weights are or the values (6e-5 and
+//           up; smaller sizes count as that): a sink with small values, or none, does not
+//           take the other tokens' digits.  P transposes from
+//           the QK layout by movmatrix.  Up to four heads fill the eight columns as
+//           (tokens 0..7, tokens 8..15) of each head, which the end adds.  The mins are
+//           one more MMA.
 //
 // Three kernels, chained by programmatic dependent launch so that each one's
 // start overlaps the end of the one before:
@@ -73,6 +81,7 @@ constexpr int D4_MIN_PAGES = 24;   // pages per CTA below which an automatic spl
 constexpr int D4_SEG_PAGES = 60;
 constexpr int D4_ONE_PAGES = 96;   // pages per CTA up to which a few sequences go without an even split
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
+constexpr float D4_PV_FACTOR = 0x1p100f;  // the PV weights' largest factor, where it starts
 
 __device__ __forceinline__ float d4_ex2(float x) {
     float y;
@@ -689,7 +698,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             }
         }
         const int n_units = dead ? 0 : cs.units<NW, U>(warp);
-        float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT];
+        float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT], fpv[NT];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -698,6 +707,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         for (int e = 0; e < NT; ++e) {
             mrun[e] = D4_NEG;
             lsum[e] = 0.f;
+            fpv[e] = D4_PV_FACTOR;
         }
         if (n_units > 0) {
             if constexpr (!ONE) wait(&sm.qbar[buf], (s >> 1) & 1);
@@ -784,36 +794,60 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 }
             };
 
-            auto pv_page = [&](int slot, const float (&p)[2][NT]) {
+            // The token sizes of the unit's two pages, two fp16 powers of two a lane: lane 16 e + 2 j
+            // (and the next) those of tokens 2 j, 2 j + 1 of page e.  They are 2^-14 at least, so
+            // that what divides by them is finite, but 0 where the values are.
+            static_assert(U == 2, "half a warp a page");
+            auto unit_sizes = [&](int group) {
+                const uint8_t* at = sm.ring[warp][U * group + (lane >> 4)] + 8 * (lane & 15);
+                const uint2 sc = lds64(at + O4_VS), mn = lds64(at + O4_VM);
+                __half2 m = __hmax2(__hmax2(__habs2(u32_as_h2(sc.x)), __habs2(u32_as_h2(sc.y))),
+                                    __hmax2(__habs2(u32_as_h2(mn.x)), __habs2(u32_as_h2(mn.y))));
+                m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                const uint32_t size = h2_as_u32(__hmax2(m, u32_as_h2(0x04000400u))) & 0x7c007c00u;
+                return h2_as_u32(__hmin2(u32_as_h2(size), __hmul2(m, u32_as_h2(0x78007800u))));
+            };
+            // Those of tokens r, r + 8 of page e.
+            auto page_sizes = [&](uint32_t unit, int e) {
+                const int from = 16 * e + ((lane >> 2) & 6);
+                return prmt(__shfl_sync(0xffffffffu, unit, from), __shfl_sync(0xffffffffu, unit, from + 8), r & 1 ? 0x7632 : 0x5410);
+            };
+
+            auto pv_page = [&](int slot, uint32_t size, const uint32_t (&p)[NT]) {
                 const uint8_t* tile = sm.ring[warp][slot];
+                // 2 / size of tokens 2 t + 8 (r & 1) and the next, transposed like p
+                const uint32_t f = movmatrix(0x7c007c00u - h2_as_u32(__hmax2(u32_as_h2(size), u32_as_h2(0x04000400u))));
+                const bool odd = r & 1;
                 uint32_t pb0, pb1;  // p in the operand's layout: tokens 2 t, 2 t + 1 and 2 t + 8, 2 t + 9
                 uint32_t s0[4], s1[4];
                 if constexpr (NT == 1) {
                     // column r: head r / 2, tokens 0..7 (r even) or 8..15 (r odd); the other half is zero
-                    const uint32_t y = movmatrix(pack_half2(p[0][0], p[1][0]));
-                    pb0 = r & 1 ? 0u : y;
-                    pb1 = r & 1 ? y : 0u;
+                    const uint32_t y = movmatrix(p[0]);
+                    pb0 = odd ? 0u : y;
+                    pb1 = odd ? y : 0u;
                     const uint4 sc = lds128(tile + O4_VS + 16 * (t + 4 * (r & 1)));
-                    s0[0] = s1[0] = sc.x;
-                    s0[1] = s1[1] = sc.y;
-                    s0[2] = s1[2] = sc.z;
-                    s0[3] = s1[3] = sc.w;
+                    s0[0] = s1[0] = h2_as_u32(__hmul2(u32_as_h2(sc.x), u32_as_h2(f)));
+                    s0[1] = s1[1] = h2_as_u32(__hmul2(u32_as_h2(sc.y), u32_as_h2(f)));
+                    s0[2] = s1[2] = h2_as_u32(__hmul2(u32_as_h2(sc.z), u32_as_h2(f)));
+                    s0[3] = s1[3] = h2_as_u32(__hmul2(u32_as_h2(sc.w), u32_as_h2(f)));
                 } else {
-                    pb0 = movmatrix(pack_half2(p[0][0], p[0][1]));
-                    pb1 = movmatrix(pack_half2(p[1][0], p[1][1]));
+                    pb0 = movmatrix(prmt(p[0], p[1], 0x5410));
+                    pb1 = movmatrix(prmt(p[0], p[1], 0x7632));
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, f, 4);
+                    const __half2 fa = u32_as_h2(odd ? other : f), fb = u32_as_h2(odd ? f : other);
                     const uint4 sA = lds128(tile + O4_VS + 16 * t), sB = lds128(tile + O4_VS + 16 * (t + 4));
-                    s0[0] = sA.x;
-                    s0[1] = sA.y;
-                    s0[2] = sA.z;
-                    s0[3] = sA.w;
-                    s1[0] = sB.x;
-                    s1[1] = sB.y;
-                    s1[2] = sB.z;
-                    s1[3] = sB.w;
+                    s0[0] = h2_as_u32(__hmul2(u32_as_h2(sA.x), fa));
+                    s0[1] = h2_as_u32(__hmul2(u32_as_h2(sA.y), fa));
+                    s0[2] = h2_as_u32(__hmul2(u32_as_h2(sA.z), fa));
+                    s0[3] = h2_as_u32(__hmul2(u32_as_h2(sA.w), fa));
+                    s1[0] = h2_as_u32(__hmul2(u32_as_h2(sB.x), fb));
+                    s1[1] = h2_as_u32(__hmul2(u32_as_h2(sB.y), fb));
+                    s1[2] = h2_as_u32(__hmul2(u32_as_h2(sB.z), fb));
+                    s1[3] = h2_as_u32(__hmul2(u32_as_h2(sB.w), fb));
                 }
-                {   // min term: row r holds group r & 3
-                    const uint32_t am[4] = {lds32(tile + O4_VM + 16 * t + 4 * (r & 3)), 0u,
-                                            lds32(tile + O4_VM + 16 * (t + 4) + 4 * (r & 3)), 0u};
+                {   // min term: row r holds group r / 2, tokens 0..7 (r even) or 8..15 (r odd)
+                    const uint32_t m = h2_as_u32(__hmul2(u32_as_h2(lds32(tile + O4_VM + 16 * (t + 4 * (r & 1)) + 4 * (r >> 1))), u32_as_h2(f)));
+                    const uint32_t am[4] = {odd ? 0u : m, 0u, odd ? m : 0u, 0u};
                     mma_f16_16816(cmin, am, pb0, pb1);
                 }
                 const uint4 va = lds128(tile + O4_VC + 128 * t + 16 * r), vb = lds128(tile + O4_VC + 128 * (t + 4) + 16 * r);
@@ -889,24 +923,63 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                     }
                 }
             };
-            // Raises the running maxima to the page's logits where one is larger.
-            auto raise = [&](const float (&lg)[2][NT]) {
-                float top[NT];
-                bool grow = false;
+            // Rescales the value accumulators of this lane's head x.
+            auto rescale = [&](int x, float c) {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    oacc[m][x] *= c;
+                    oacc[m][x + 2] *= c;
+                    if (NT == 1) {
+                        oacc[m][1] *= c;
+                        oacc[m][3] *= c;
+                    }
+                }
+                cmin[x] *= c;
+                if (NT == 1) cmin[1] *= c;
+            };
+            // The softmax weights of a page's tokens (of these sizes) into the sums, and their PV
+            // weights P, tokens r and r + 8 in one word.  Where a logit exceeds the running maximum
+            // or a P what it may be (one vote), the maximum is raised, and the weights' factor with
+            // it (up to the largest factor the accumulators stay), or the factor brought down.
+            auto softmax = [&](const float (&lg)[2][NT], uint32_t size, uint32_t (&p)[NT]) {
+                const float2 z = __half22float2(u32_as_h2(size));
+                float w[2][NT];
+                bool rare = false;
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    top[x] = fmaxf(lg[0][x], lg[1][x]);
-                    grow |= top[x] > mrun[x];
+                    w[0][x] = d4_ex2(lg[0][x] - mrun[x]);
+                    w[1][x] = d4_ex2(lg[1][x] - mrun[x]);
+                    p[x] = pack_half2(w[0][x] * (fpv[x] * z.x), w[1][x] * (fpv[x] * z.y));
+                    rare |= fmaxf(lg[0][x], lg[1][x]) > mrun[x] || !__hble2(u32_as_h2(p[x]), u32_as_h2(0x70007000u));  // 2^13
                 }
-                if (__any_sync(0xffffffffu, grow)) {
+                if (__any_sync(0xffffffffu, rare)) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
-                        top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 4));
-                        top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 8));
-                        top[x] = fmaxf(fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 16)), mrun[x]);
-                        const float c = d4_ex2(mrun[x] - top[x]);
-                        mrun[x] = top[x];
+                        float top = fmaxf(lg[0][x], lg[1][x]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), mrun[x]);
+                        float c = d4_ex2(mrun[x] - top);
+                        const float f = fpv[x] * d4_ex2(top - mrun[x]);
+                        mrun[x] = top;
                         lsum[x] *= c;
+                        c = f <= D4_PV_FACTOR ? 1.f : c * __fdividef(D4_PV_FACTOR, fpv[x]);  // of the accumulators
+                        fpv[x] = fminf(f, D4_PV_FACTOR);
+                        w[0][x] = d4_ex2(lg[0][x] - mrun[x]);
+                        w[1][x] = d4_ex2(lg[1][x] - mrun[x]);
+                        float P0 = w[0][x] * (fpv[x] * z.x), P1 = w[1][x] * (fpv[x] * z.y);
+                        top = fmaxf(P0, P1);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        if (top > 8192.f) {  // to [2^11, 2^12), by a power of two
+                            const float down = __uint_as_float((265u - (__float_as_uint(top) >> 23)) << 23);
+                            fpv[x] *= down;
+                            P0 *= down;
+                            P1 *= down;
+                            c *= down;
+                        }
+                        p[x] = pack_half2(P0, P1);
 #pragma unroll
                         for (int m = 0; m < 8; ++m) {
                             oacc[m][x] *= c;
@@ -920,31 +993,29 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                         if (NT == 1) cmin[1] *= c;
                     }
                 }
-            };
-            auto softmax = [&](const float (&lg)[2][NT], float (&p)[2][NT]) {
 #pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    p[0][x] = d4_ex2(lg[0][x] - mrun[x]);
-                    p[1][x] = d4_ex2(lg[1][x] - mrun[x]);
-                    lsum[x] += p[0][x] + p[1][x];
-                }
+                for (int x = 0; x < NT; ++x) lsum[x] += w[0][x] + w[1][x];
             };
 
             // Pipelined by pages: the logits of the next page and the weighted sum of this
             // one share a block of code, so their latencies overlap.
-            float lg[2][NT], p[2][NT];
+            float lg[2][NT];
+            uint32_t p[NT], sizes = 0, size = 0;  // sizes: of the unit's pages; size: of the page whose weights p holds
             Counts nt = wait_unit(n_units == 1);
-            if (!dead) logits(0, U * st, 0, nt.n[0], lg);
+            if (!dead) {
+                logits(0, U * st, 0, nt.n[0], lg);
+                sizes = unit_sizes(st);
+            }
 #pragma unroll 1
             for (int k = 0; k < n_units && !dead; ++k) {
-                raise(lg);
-                softmax(lg, p);
+                size = page_sizes(sizes, 0);
+                softmax(lg, size, p);
 #pragma unroll
                 for (int e = 1; e < U; ++e) {
                     logits(k, U * st + e, e, nt.n[e], lg);
-                    pv_page(U * st + e - 1, p);
-                    raise(lg);
-                    softmax(lg, p);
+                    pv_page(U * st + e - 1, size, p);
+                    size = page_sizes(sizes, e);
+                    softmax(lg, size, p);
                 }
                 ++done;
                 const int last = U * st + U - 1;
@@ -953,13 +1024,14 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                     parity ^= 1u;
                 }
                 if (k + 1 == n_units) {
-                    pv_page(last, p);
+                    pv_page(last, size, p);
                     break;
                 }
                 nt = wait_unit(k + 2 == n_units);
                 if (dead) break;
                 logits(k + 1, U * st, 0, nt.n[0], lg);
-                pv_page(last, p);
+                sizes = unit_sizes(st);
+                pv_page(last, size, p);
                 __syncwarp();
                 // hand the group back, and the ones that the last segment's partial held
                 if (s > 0 && freed < end1) {
@@ -978,22 +1050,30 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         const int at = st == 0 ? UNITS - 1 : st - 1;
         if (has) {
             float* op = reinterpret_cast<float*>(sm.ring[warp][U * at]);
+            auto min_of = [&](float c, int g) { return __shfl_sync(0xffffffffu, c, 8 * g + t) + __shfl_sync(0xffffffffu, c, 8 * g + 4 + t); };
+            float inv[NT], lo[NT], hi[NT];  // 1 / (2 F), and what the codes' places (2^-24, 2^-20) make of it
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                inv[x] = __fdividef(0.5f, fpv[x]);
+                lo[x] = 16777216.f * inv[x];
+                hi[x] = 1048576.f * inv[x];
+            }
 #pragma unroll
             for (int gg = 0; gg < NGROUP; ++gg) {
                 if constexpr (NT == 1) {
-                    const float mt = __shfl_sync(0xffffffffu, cmin[0] + cmin[1], 4 * gg + t);
+                    const float mt = min_of(cmin[0] + cmin[1], gg) * inv[0];
                     *reinterpret_cast<float4*>(op + t * D + 32 * gg + 4 * r) =
-                        make_float4(fmaf(oacc[2 * gg][0] + oacc[2 * gg][1], 16777216.f, mt),
-                                    fmaf(oacc[2 * gg][2] + oacc[2 * gg][3], 1048576.f, mt),
-                                    fmaf(oacc[2 * gg + 1][0] + oacc[2 * gg + 1][1], 16777216.f, mt),
-                                    fmaf(oacc[2 * gg + 1][2] + oacc[2 * gg + 1][3], 1048576.f, mt));
+                        make_float4(fmaf(oacc[2 * gg][0] + oacc[2 * gg][1], lo[0], mt),
+                                    fmaf(oacc[2 * gg][2] + oacc[2 * gg][3], hi[0], mt),
+                                    fmaf(oacc[2 * gg + 1][0] + oacc[2 * gg + 1][1], lo[0], mt),
+                                    fmaf(oacc[2 * gg + 1][2] + oacc[2 * gg + 1][3], hi[0], mt));
                 } else {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float mt = __shfl_sync(0xffffffffu, cmin[x], 4 * gg + t);
+                        const float mt = min_of(cmin[x], gg) * inv[x];
                         *reinterpret_cast<float4*>(op + (2 * t + x) * D + 32 * gg + 4 * r) =
-                            make_float4(fmaf(oacc[2 * gg][x], 16777216.f, mt), fmaf(oacc[2 * gg][2 + x], 1048576.f, mt),
-                                        fmaf(oacc[2 * gg + 1][x], 16777216.f, mt), fmaf(oacc[2 * gg + 1][2 + x], 1048576.f, mt));
+                            make_float4(fmaf(oacc[2 * gg][x], lo[x], mt), fmaf(oacc[2 * gg][2 + x], hi[x], mt),
+                                        fmaf(oacc[2 * gg + 1][x], lo[x], mt), fmaf(oacc[2 * gg + 1][2 + x], hi[x], mt));
                     }
                 }
             }
