@@ -94,12 +94,13 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
     if (quarter) return;
     __half sh, mh;
     int code;
-    if (!wild) {
-        Dd z = part[0][j], y = part[2][j];
-        dd_add(z, part[1][j]);
-        dd_add(y, part[3][j]);
-        dd_add(z, y);
-        z = dd_norm(z);
+    Dd z = part[0][j], y = part[2][j];
+    dd_add(z, part[1][j]);
+    dd_add(y, part[3][j]);
+    dd_add(z, y);
+    z = dd_norm(z);
+    // (a matrix's large entries can take the pairs out of range, or hold what is not finite)
+    if (!wild && __all_sync(0xffffffffu, isfinite(z.hi))) {
         Dd mn = z, mx = z;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -115,17 +116,17 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
         code = q <= -0.5f ? 0 : q >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(z, s, m, (int)rintf(q));
     } else {  // all in fp64
         const float* Rw = (side ? Rv : Rk) + (size_t)h * D * D + j;
-        double z = 0.0;
-        for (int i = 0; i < D; ++i) z = fma((double)xs[i] + (double)xl[i], (double)__ldg(Rw + (size_t)i * D), z);
-        double lo = z, hi = z;
+        double w = 0.0;
+        for (int i = 0; i < D; ++i) w = fma((double)xs[i] + (double)xl[i], (double)__ldg(Rw + (size_t)i * D), w);
+        double lo = w, hi = w;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        if (__any_sync(0xffffffffu, !isfinite(z))) lo = hi = CUDART_NAN;
+        if (__any_sync(0xffffffffu, !isfinite(w))) lo = hi = CUDART_NAN;
         int4_params(lo, hi, (double)clip, sh, mh);
-        code = int4_code(z, sh, mh);
+        code = int4_code(w, sh, mh);
     }
     // the eight codes of a word sit in eight neighbouring lanes
     uint32_t w = (uint32_t)code << (4 * (lane & 7));
@@ -195,7 +196,7 @@ struct __align__(16) PrefillSmem {
     __align__(16) float c[D];                 // mu R (0 for values)
     __align__(16) Dd c_exact[D];
     float m2[4], col2[PF_WORKERS * 4], col_most[PF_WORKERS * 4], mu_norm;
-    float bound, bound_most;                  // PF_NORM times the largest column's norm, PF_MOST times the largest entry
+    float bound, bound_most;                  // PF_NORM times the largest column's norm (-1: fp64), PF_MOST times the largest entry
     PrefillWorker w[PF_WORKERS];
 };
 static_assert(offsetof(PrefillSmem, R) % 16 == 0 && offsetof(PrefillSmem, mu) % 16 == 0 && offsetof(PrefillSmem, c) % 16 == 0 &&
@@ -279,20 +280,13 @@ __device__ __noinline__ Dd prefill_exact(const PrefillSmem& sm, const __nv_bfloa
     return dd_norm(s[0]);
 }
 
-// A row all in fp64, lane = channel of group g: its code, scale and min.
-__device__ __noinline__ int prefill_wild(const PrefillSmem& sm, const __nv_bfloat16* A, int g, float clip, __half& sh, __half& mh) {
+// A row all in fp64, lane = channel of group g: its code, scale and min.  (From R itself:
+// a bf16 part of its largest numbers would be infinite.)
+__device__ __noinline__ int prefill_wild(const PrefillSmem& sm, const float* R, const __nv_bfloat16* A, int g, float clip, __half& sh, __half& mh) {
     double y = 0.0;
-#pragma unroll 1
-    for (int e = 0; e < 32; ++e) {
-        const float4 rv = prefill_column(sm, 32 * g + (threadIdx.x & 31), e >> 2, e & 3);
-        const int i0 = 16 * (e >> 2) + 2 * (e & 3);
-        const float rw[4] = {rv.x, rv.y, rv.z, rv.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = i0 + (q & 1) + 8 * (q >> 1);
-            y = fma((double)__bfloat162float(A[i]) - (double)sm.mu[i], (double)rw[q], y);
-        }
-    }
+#pragma unroll 4
+    for (int i = 0; i < D; ++i)
+        y = fma((double)__bfloat162float(A[i]) - (double)sm.mu[i], (double)__ldg(R + (size_t)i * D + 32 * g + (threadIdx.x & 31)), y);
     double lo = y, hi = y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -393,6 +387,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         }
         n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
         n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
+        const int wild = __syncthreads_or(!(n2 < 0x1p100f));  // large numbers, or NaN: all rows in fp64
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             n2 = fmaxf(n2, __shfl_xor_sync(0xffffffffu, n2, o));
@@ -408,7 +403,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
                 n2 = fmaxf(n2, sm.col2[w]);
                 most = fmaxf(most, sm.col_most[w]);
             }
-            sm.bound = PF_NORM * sqrtf(n2);
+            sm.bound = wild ? -1.f : PF_NORM * sqrtf(n2);
             sm.bound_most = PF_MOST * most;
             sm.mu_norm = sqrtf((sm.m2[0] + sm.m2[1]) + (sm.m2[2] + sm.m2[3]));
         }
@@ -444,7 +439,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             most += __shfl_xor_sync(0xffffffffu, most, 1);
             most += __shfl_xor_sync(0xffffffffu, most, 2);
             if (q == 0)
-                wk.eps[row] = int4_wild(n2 + sm.mu_norm * sm.mu_norm) ? -1.f : fmaf(sm.bound, sqrtf(n2) + sm.mu_norm, sm.bound_most * most);
+                wk.eps[row] = sm.bound < 0.f || int4_wild(n2 + sm.mu_norm * sm.mu_norm) ? -1.f : fmaf(sm.bound, sqrtf(n2) + sm.mu_norm, sm.bound_most * most);
             if (tid == 0) wk.n_open = 0;
         }
         if (x + stride < tiles) fetch(x + stride, buf ^ 1);
@@ -634,7 +629,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         while ((any = __ballot_sync(0xffffffffu, wilds != 0)) != 0) {
             const int l = __ffs(any) - 1, q = __ffs(__shfl_sync(0xffffffffu, wilds, l)) - 1, row = row_of(q) - r + (l >> 2);
             __half sh, mh;
-            uint32_t c = (uint32_t)prefill_wild(sm, wk.A[buf][row], g, clip, sh, mh) << (4 * (lane & 7));
+            uint32_t c = (uint32_t)prefill_wild(sm, R, wk.A[buf][row], g, clip, sh, mh) << (4 * (lane & 7));
             c |= __shfl_xor_sync(0xffffffffu, c, 1);
             c |= __shfl_xor_sync(0xffffffffu, c, 2);
             c |= __shfl_xor_sync(0xffffffffu, c, 4);

@@ -30,7 +30,8 @@ def quant_params(z, clip: float = 1.0):
     c = float(np.float32(clip))
     fine = np.isfinite(z).all(axis=-1)   # a group with a value that is not finite is NaN
     lo, hi = np.where(fine, c * z.min(axis=-1), np.nan), np.where(fine, c * z.max(axis=-1), np.nan)
-    return f16_rn_sat(((hi - lo) / TOP).astype(np.float32)), f16_rn_sat(lo.astype(np.float32))
+    f32 = lambda x: np.clip(x, -np.finfo(np.float32).max, np.finfo(np.float32).max).astype(np.float32)  # noqa: E731
+    return f16_rn_sat(f32((hi - lo) / TOP)), f16_rn_sat(f32(lo))   # (past fp32's range: saturated too)
 
 
 def quant_codes(z, scale_h, min_h):

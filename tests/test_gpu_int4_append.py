@@ -62,3 +62,38 @@ def test_a_min_next_to_a_rounding_boundary_under_a_dominant_product(sign, units)
     int4.append(want, x.double().numpy(), x.double().numpy(), np.arange(n), mu, R, R)
     got = cache.cpu().numpy()
     assert np.array_equal(got, want), np.count_nonzero((got != want).any(-1))
+
+
+@pytest.mark.parametrize("n", [3, 600])
+@pytest.mark.parametrize("kind", ["nan", "inf", "huge", "largest", "overflowing sum"])
+def test_matrices_with_numbers_that_are_huge_or_not_finite(n, kind):
+    """Groups that a matrix entry makes infinite or NaN are NaN in whole, the others are as ever; finite results past fp32
+    saturate.  Both kernels write the same bytes."""
+    rng = np.random.default_rng(5)
+    R = _rot(rng, 1)
+    if kind == "nan":
+        R[0, 17, 40] = np.nan
+    elif kind == "inf":
+        R[0, 17, 40] = -np.inf
+    elif kind == "huge":
+        R[0, :, 40] *= 1e25
+    elif kind == "largest":
+        R[0, 17, 40] = 3.4e38            # (the nearest bf16 number is infinite)
+    else:
+        R[0, :, 40] = 3e38 * np.where(np.arange(128) % 2, 1, -1)
+    k, v = _bf(rng.standard_normal((n, 1, 128))), _bf(rng.standard_normal((n, 1, 128)) * (1e18 if kind == "huge" else 1.0))
+    mu = rng.standard_normal((1, 128)).astype(np.float32)
+    pages = (n + 15) // 16
+    cache, want = torch.zeros((pages, 1, 2560), dtype=torch.uint8, device="cuda"), int4.new_cache(pages, 1)
+    assert _append(k, v, np.arange(n), mu, R, R, cache) == 0
+    int4.append(want, k.double().numpy(), v.double().numpy(), np.arange(n), mu, R, R)
+    got = cache.cpu().numpy()
+    for side in (0, 1):
+        a, b = int4.values(got, side).reshape(-1, 128)[:n], int4.values(want, side).reshape(-1, 128)[:n]
+        assert np.array_equal(a, b, equal_nan=True)
+        assert np.isnan(a[:, 32:64]).all() == (kind in ("nan", "inf")) and np.isfinite(np.delete(a, np.s_[32:64], 1)).all()
+    few = torch.zeros_like(cache)
+    for i in range(min(n, 40)):
+        _append(k[i:i + 1], v[i:i + 1], [i], mu, R, R, few)
+    done = min(n, 40) // 16
+    assert np.array_equal(few.cpu().numpy()[:done], got[:done])
