@@ -369,6 +369,11 @@ evict_gather_int4_kernel(const uint8_t* cache, int64_t num_pages, const int32_t*
 
 using namespace kvq;
 
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
 // The shared memory opt-in, once per kernel and device.
 static kvq_status select_smem_once(const void* fn, int which) {
     static std::mutex mu;
@@ -401,8 +406,16 @@ extern "C" kvq_status kvq_evict_select(const float* weights, int64_t weights_str
                              (long long)weights_stride, max_tokens);
     if (!weights || !context_lens || !keep || !new_lens)
         return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_evict_select: null pointer");
-    // CTAs per row: up to eight (a cluster) while they find an SM each and 2048 tokens or more
+    // What is written while other CTAs still read: a late reader of an overwritten length would
+    // keep other tokens, and threads that disagree on it would part before a barrier.
     const int64_t rows = (int64_t)B * H_kv;
+    const size_t lens_bytes = (size_t)B * 4, keep_bytes = (size_t)rows * budget * 4;
+    const size_t weights_bytes = ((size_t)(rows - 1) * weights_stride + max_tokens) * 4;
+    if (overlap(new_lens, lens_bytes, context_lens, lens_bytes) || overlap(new_lens, lens_bytes, weights, weights_bytes) ||
+        overlap(keep, keep_bytes, context_lens, lens_bytes) || overlap(keep, keep_bytes, weights, weights_bytes) ||
+        overlap(keep, keep_bytes, new_lens, lens_bytes))
+        return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_evict_select: keep and new_lens must not overlap another argument");
+    // CTAs per row: up to eight (a cluster) while they find an SM each and 2048 tokens or more
     const int nsm = kvq_device_sm_count();
     int cs = 1;
     while (cs < 8 && rows * cs * 2 <= nsm && max_tokens / (cs * 2) >= 2048) cs *= 2;

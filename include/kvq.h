@@ -404,6 +404,8 @@ kvq_status kvq_decode_attn_int4_weights(const void* q, int B, int H_q, int H_kv,
  *   keep      device int32 [B][H_kv][budget], written: the kept indices in
  *             ascending order, then -1
  *   new_lens  device int32 [B], written: min(n, budget)
+ * keep and new_lens must not overlap each other, weights (rows and what lies
+ * between them) or context_lens: a call on the lengths in place is refused.
  * 1 <= budget, 0 <= sinks, 0 <= recent, sinks + recent <= budget,
  * max_tokens <= 2^30, B and H_kv <= 65535. */
 kvq_status kvq_evict_select(const float* weights, int64_t weights_stride, int B, int H_kv, int max_tokens,
