@@ -123,6 +123,17 @@ class Int4Layer(Int2Layer):
                 self.append(k[s:e].contiguous(), v[s:e].contiguous(), sl[s:e].contiguous())
             del k, v
 
+    def new_slots(self) -> torch.Tensor:
+        """Slot of position context_lens[b] - 1 of every sequence: of the
+        step's new token, which context_lens counts (after an eviction, raise
+        context_lens first).  -1, which an append skips, for an empty
+        sequence; a position past the block table is an IndexError."""
+        out = torch.full((self.spec.batch,), -1, dtype=torch.int32)
+        for b, n in enumerate(self.context_lens.tolist()):
+            if n > 0:
+                out[b] = inputs.slot_mapping(self.block_table[b].cpu(), torch.tensor([n - 1]))[0]
+        return out.to(self.device)
+
     def workspace(self, num_splits: int = 0, weights: bool = True) -> torch.Tensor:
         n = _lib.kvq_int4_workspace_bytes(self.spec.batch, self.spec.h_q, self.spec.h_kv, self.block_table.shape[1],
                                           num_splits, weights)
