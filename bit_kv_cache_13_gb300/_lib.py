@@ -221,7 +221,7 @@ def kvq_decode_attn_int2_noalloc(q, cache, num_pages: int, block_table, context_
 
 
 def kvq_debug_drop_next_copy() -> None:
-    """Test hook: the next INT2 decode launch leaves one bulk copy unissued
+    """Test hook: the next INT2 or INT4 decode launch leaves one bulk copy unissued
     so a bounded wait runs out (the call then reports KVQ_ERR_CUDA)."""
     load().kvq_debug_drop_next_copy()
 

@@ -1160,11 +1160,13 @@ extern "C" size_t kvq_decode_workspace_bytes(int B, int H_q, int H_kv, int max_p
     return int2_workspace_bytes(B, H_q, H_kv, slots);
 }
 
-// Test hook: makes the next INT2 decode launch on this process drop one bulk
+// Test hook: makes the next INT2 or INT4 decode launch on this process drop one bulk
 // copy so that a bounded wait runs out (kvq_debug_drop_next_copy).
 static std::atomic<int> g_debug_flags{0};
 
 extern "C" void kvq_debug_drop_next_copy(void) { g_debug_flags.store(DBG_DROP_FIRST_COPY); }
+
+bool kvq_take_drop_next_copy() { return g_debug_flags.exchange(0) != 0; }
 
 // A validated INT2 decode launch.
 struct Int2Plan {

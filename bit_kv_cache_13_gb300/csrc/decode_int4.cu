@@ -82,6 +82,7 @@ constexpr int D4_SEG_PAGES = 60;
 constexpr int D4_ONE_PAGES = 96;   // pages per CTA up to which a few sequences go without an even split
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
 constexpr float D4_PV_FACTOR = 0x1p100f;  // the PV weights' largest factor, where it starts
+constexpr long long D4_SHORT_WAIT_CYCLES = 2000000LL;  // about a millisecond: a wait's limit under the test hook
 
 __device__ __forceinline__ float d4_ex2(float x) {
     float y;
@@ -144,6 +145,7 @@ struct D4Args {
     float* partials;   // [unit + CTA][G][PART_STRIDE]
     float* logits;     // [unit][16 max_pages][G], base 2 (weights form)
     int automatic;     // the split is the kernel's choice (else the grid's)
+    int drop;          // test hook: the first copy of CTA 0 is left out, and waits are short
     // weights form
     float* weights;
     int64_t wstride;
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     int ist = 0, ix = 0;      // ring group and batch place of the next unit
     // Lanes e < U issue page e of the next unit.  (The copies may land before their
     // bytes are announced: the phase is open until lane 0 arrives.)
-    auto issue_next = [&]() {
+    auto issue_next = [&](bool drop) {
         if (ix == BATCH) {
             turn();
             ix = 0;
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         uint64_t* bar = &sm.bar[warp][ist];
         if (lane < U) {
             sm.ntok[warp][U * ist + lane] = (int)n;
-            if (n) bulk_g2s_hint(sm.ring[warp][U * ist + lane], a.cache + (size_t)tile * INT4_TILE, INT4_TILE, bar, policy);
+            if (n && !(drop && lane == 0)) bulk_g2s_hint(sm.ring[warp][U * ist + lane], a.cache + (size_t)tile * INT4_TILE, INT4_TILE, bar, policy);
         }
         __syncwarp();  // the counts are ordered before the arrive
         if (lane == 0) mbar_arrive_expect_tx(bar, __popc(ok_mask >> (U * ix) & ((1u << U) - 1)) * INT4_TILE);
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         ++ix;
         ist = ist + 1 == UNITS ? 0 : ist + 1;
     };
-    if (built > 0) issue_next();
+    if (built > 0) issue_next(a.drop && tid < 32 && cta == 0);
 
     if constexpr (!ONE) {
         griddep_wait();  // the rotated queries are there
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     }
     // (the rest of the ring after the queries, which would queue behind it)
 #pragma unroll 1
-    while (issued < min(built, UNITS)) issue_next();
+    while (issued < min(built, UNITS)) issue_next(false);
     if constexpr (ONE) {
         // q' = q R_k * scale * log2(e), as the rotate kernel has it, into query[0]
 #pragma unroll
@@ -669,7 +671,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     bool dead = false;  // a wait of this warp ran out: it takes part without data
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
-        const bool ok = mbar_wait_bounded(bar, parity, WAIT_LIMIT_CYCLES);
+        const bool ok = mbar_wait_bounded(bar, parity, a.drop ? D4_SHORT_WAIT_CYCLES : WAIT_LIMIT_CYCLES);
         if (__any_sync(0xffffffffu, !ok)) {
             if (lane == 0) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_TIMEOUT);
             dead = true;
@@ -681,9 +683,10 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     int freed = 0;              // units whose ring groups may be issued into again
     auto refill = [&]() {
 #pragma unroll 1
-        while (issued < min(built, freed + UNITS) && !dead) issue_next();
+        while (issued < min(built, freed + UNITS) && !dead) issue_next(false);
     };
-    for (int s = 0;; ++s) {
+    int s = 0;
+    for (;; ++s) {
         // ================ segment s: pages [pa, pb) of unit (b, h)
         const size_t u = (size_t)cs.b * a.H_kv + cs.h;
         const int buf = s & 1;
@@ -1043,6 +1046,12 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             }
             __syncwarp();
         }
+        if constexpr (WTS) {
+            if (dead) {  // no logit of this warp's pages (what it wrote of them counts for nothing without its partial)
+                for (int page = cs.pa + warp; page < cs.pb; page += NW)
+                    for (int x = lane; x < PAGE * G; x += 32) a.logits[(u * a.max_pages + page) * PAGE * G + x] = -CUDART_INF_F;
+            }
+        }
 
         // ---- this warp's partial, in its last ring group: channels 32 g + 4 r .. + 3 of
         // its head(s)
@@ -1286,9 +1295,12 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         if (cs.left == 0) break;
         cs.next(a, extra);
     }
-    if (dead)  // copies in flight land before the block ends
+    if (dead) {  // copies in flight land before the block ends, the last segments' queries too
         for (int v = done; v < issued; ++v)
             (void)mbar_wait_bounded(&sm.bar[warp][v % UNITS], (v / UNITS) & 1, 1000000LL);
+        if constexpr (!ONE)
+            for (int v = max(0, s - 1); v <= s; ++v) (void)mbar_wait_bounded(&sm.qbar[v & 1], (v >> 1) & 1, 1000000LL);
+    }
 }
 
 // ------------------------------------------------------------------ 3: finish
@@ -1563,6 +1575,7 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     a.partials = reinterpret_cast<float*>(ws + lay.partials);
     a.logits = with_weights ? reinterpret_cast<float*>(ws + lay.logits) : nullptr;
     a.automatic = num_splits == 0;
+    a.drop = kvq_take_drop_next_copy();
     a.weights = weights;
     a.wstride = weights_stride;
     a.decay = decay;

@@ -61,6 +61,9 @@ int bgtq_decode_auto_splits(int B, int H_q, int H_kv, int max_pages_per_seq);
 // Streaming multiprocessors of the current device (host; 152 without one).
 int kvq_device_sm_count();
 
+// Whether kvq_debug_drop_next_copy was called since the last decode launch (host; once).
+bool kvq_take_drop_next_copy();
+
 // The INT2 decode with every argument validated before `prepare` is called
 // to clear (`zeroed` bytes) and return the scratch it runs in (host; used by
 // the allocation-free entry point).

@@ -283,8 +283,8 @@ kvq_status kvq_decode_attn_int2_noalloc(const void* q, int B, int H_q, int H_kv,
                                         const float* R_k, const float* R_v, float scale,
                                         float* out, int num_splits, void* stream);
 
-/* Test hook, not for production use: the next INT2 decode launch in this
- * process leaves the bulk copy of its first page unissued (the page's bytes
+/* Test hook, not for production use: the next INT2 or INT4 decode launch in
+ * this process leaves the bulk copy of its first page unissued (the page's bytes
  * are still expected) and gives its waits a limit of about a millisecond, so
  * that wait runs out: the kernel records the timeout, lets its other copies
  * land, finishes without the missing page and returns, and
