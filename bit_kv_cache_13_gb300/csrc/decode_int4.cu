@@ -25,13 +25,12 @@
 //   PV      rows = 16 channels, K = 16 tokens, columns = heads; the second operand is
 //           fp16(fp16(P) * scale_{token, group} / size): two roundings of 2^-11 of a term,
 //           below the output's bf16 rounding.  A token's size is a power of two next
-//           below the largest of its four scales and |mins|, and P = p * size * F, F such
-//           that the largest P so far stays within [2^11, 2^13] (each head's F falls
-//           when a P exceeds 2^13, and rises when the running maximum does).  So no
-//           operand overflows, and what fp16 cuts off below 2^-24 is 2^-31 of the context's
-//           largest term, however small or large the weights are or the values (6e-5 and
-//           up; smaller sizes count as that): a sink with small values, or none, does not
-//           take the other tokens' digits.  P transposes from
+//           below the largest of its four scales and |mins|, and P = p * size relative to
+//           a reference of its own, so that the largest P so far lies within 2^10 and 2^13.
+//           So no operand overflows, and what fp16 cuts off below 2^-24 is 2^-29 of the
+//           context's largest term, however small or large the weights are or the values
+//           (6e-5 and up; smaller sizes count as that): a sink with small values, or none,
+//           does not take the other tokens' digits.  P transposes from
 //           the QK layout by movmatrix.  Up to four heads fill the eight columns as
 //           (tokens 0..7, tokens 8..15) of each head, which the end adds.  The mins are
 //           one more MMA.
@@ -81,13 +80,32 @@ constexpr int D4_MIN_PAGES = 24;   // pages per CTA below which an automatic spl
 constexpr int D4_SEG_PAGES = 60;
 constexpr int D4_ONE_PAGES = 96;   // pages per CTA up to which a few sequences go without an even split
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
-constexpr float D4_PV_FACTOR = 0x1p100f;  // the PV weights' largest factor, where it starts
+// PV weights P are at most 2^D4_PV_MOST (with scales below 4, products below 2^15); where one is
+// above that, their reference moves, and the largest is 2^D4_PV_TOP or up to a bit less.
+constexpr float D4_PV_MOST = 13.f, D4_PV_TOP = 11.f;
+constexpr float D4_WHOLE = 12582912.f;  // 1.5 2^23: a sum with it is a whole number
 constexpr long long D4_SHORT_WAIT_CYCLES = 2000000LL;  // about a millisecond: a wait's limit under the test hook
 
 __device__ __forceinline__ float d4_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Base-2 logarithm to 2^-22; -inf of 0.
+__device__ __forceinline__ float d4_lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a + b, two fp32 sums in one instruction.
+__device__ __forceinline__ float2 d4_add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 // Power of two that brings x into [2^14, 2^15) (1 for 0 and what is not
@@ -701,7 +719,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             }
         }
         const int n_units = dead ? 0 : cs.units<NW, U>(warp);
-        float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT], fpv[NT];
+        float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT], vref[NT];  // vref: the logit plus log2 size at which P is 1, plus D4_WHOLE
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -710,7 +728,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         for (int e = 0; e < NT; ++e) {
             mrun[e] = D4_NEG;
             lsum[e] = 0.f;
-            fpv[e] = D4_PV_FACTOR;
+            vref[e] = D4_NEG;
         }
         if (n_units > 0) {
             if constexpr (!ONE) wait(&sm.qbar[buf], (s >> 1) & 1);
@@ -797,29 +815,25 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 }
             };
 
-            // The token sizes of the unit's two pages, two fp16 powers of two a lane: lane 16 e + 2 j
-            // (and the next) those of tokens 2 j, 2 j + 1 of page e.  They are 2^-14 at least, so
-            // that what divides by them is finite, but 0 where the values are.
+            // Of the unit's two pages: log2 of the size of token lane & 15 of page lane >> 4, plus
+            // D4_WHOLE, and the inverses of its slot pair's two sizes.  Sizes are powers of two within
+            // 2^-14 and 2^14, so that both they and their inverses are fp16 numbers; of a token whose
+            // values are 0 the logarithm is -inf.
             static_assert(U == 2, "half a warp a page");
-            auto unit_sizes = [&](int group) {
-                const uint8_t* at = sm.ring[warp][U * group + (lane >> 4)] + 8 * (lane & 15);
+            auto unit_sizes = [&](int group, float& logs, uint32_t& inv) {
+                const uint8_t* at = sm.ring[warp][U * group + (lane >> 4)] + 8 * (lane & 15);  // groups 2 (lane & 1), + 1 of the pair
                 const uint2 sc = lds64(at + O4_VS), mn = lds64(at + O4_VM);
                 __half2 m = __hmax2(__hmax2(__habs2(u32_as_h2(sc.x)), __habs2(u32_as_h2(sc.y))),
                                     __hmax2(__habs2(u32_as_h2(mn.x)), __habs2(u32_as_h2(mn.y))));
                 m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                const uint32_t size = h2_as_u32(__hmax2(m, u32_as_h2(0x04000400u))) & 0x7c007c00u;
-                return h2_as_u32(__hmin2(u32_as_h2(size), __hmul2(m, u32_as_h2(0x78007800u))));
-            };
-            // Those of tokens r, r + 8 of page e.
-            auto page_sizes = [&](uint32_t unit, int e) {
-                const int from = 16 * e + ((lane >> 2) & 6);
-                return prmt(__shfl_sync(0xffffffffu, unit, from), __shfl_sync(0xffffffffu, unit, from + 8), r & 1 ? 0x7632 : 0x5410);
+                const uint32_t size = h2_as_u32(__hmin2(__hmax2(m, u32_as_h2(0x04000400u)), u32_as_h2(0x74007400u))) & 0x7c007c00u;
+                inv = 0x78007800u - size;
+                const __half2 z = __hmin2(u32_as_h2(size), __hmul2(m, u32_as_h2(0x78007800u)));
+                logs = d4_lg2(__half2float(lane & 1 ? __high2half(z) : __low2half(z))) + D4_WHOLE;
             };
 
-            auto pv_page = [&](int slot, uint32_t size, const uint32_t (&p)[NT]) {
+            auto pv_page = [&](int slot, uint32_t f, const uint32_t (&p)[NT]) {
                 const uint8_t* tile = sm.ring[warp][slot];
-                // 2 / size of tokens 2 t + 8 (r & 1) and the next, transposed like p
-                const uint32_t f = movmatrix(0x7c007c00u - h2_as_u32(__hmax2(u32_as_h2(size), u32_as_h2(0x04000400u))));
                 const bool odd = r & 1;
                 uint32_t pb0, pb1;  // p in the operand's layout: tokens 2 t, 2 t + 1 and 2 t + 8, 2 t + 9
                 uint32_t s0[4], s1[4];
@@ -834,8 +848,8 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                     s0[2] = s1[2] = h2_as_u32(__hmul2(u32_as_h2(sc.z), u32_as_h2(f)));
                     s0[3] = s1[3] = h2_as_u32(__hmul2(u32_as_h2(sc.w), u32_as_h2(f)));
                 } else {
-                    pb0 = movmatrix(prmt(p[0], p[1], 0x5410));
-                    pb1 = movmatrix(prmt(p[0], p[1], 0x7632));
+                    pb0 = movmatrix(p[0]);
+                    pb1 = movmatrix(p[1]);
                     const uint32_t other = __shfl_xor_sync(0xffffffffu, f, 4);
                     const __half2 fa = u32_as_h2(odd ? other : f), fb = u32_as_h2(odd ? f : other);
                     const uint4 sA = lds128(tile + O4_VS + 16 * t), sB = lds128(tile + O4_VS + 16 * (t + 4));
@@ -940,85 +954,88 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 cmin[x] *= c;
                 if (NT == 1) cmin[1] *= c;
             };
-            // The softmax weights of a page's tokens (of these sizes) into the sums, and their PV
-            // weights P, tokens r and r + 8 in one word.  Where a logit exceeds the running maximum
-            // or a P what it may be (one vote), the maximum is raised, and the weights' factor with
-            // it (up to the largest factor the accumulators stay), or the factor brought down.
-            auto softmax = [&](const float (&lg)[2][NT], uint32_t size, uint32_t (&p)[NT]) {
-                const float2 z = __half22float2(u32_as_h2(size));
-                float w[2][NT];
+            // The softmax weights of a page's tokens (their sizes' logarithms in log_z) into the sums, and their PV
+            // weights P: tokens r and r + 8 in one word, or (NT == 2) a word each of both heads.
+            // Where a logit exceeds the running maximum or a P what it may be (one vote), the one
+            // or the other reference is raised.
+            auto softmax = [&](const float (&lg)[2][NT], float2 log_z, uint32_t (&p)[NT]) {
+                float2 P[NT];  // first their logarithms
                 bool rare = false;
+                auto relate = [&](int x) {  // (whole numbers first: what a reference moves by cancels exactly)
+                    P[x] = d4_add2(make_float2(lg[0][x], lg[1][x]), d4_add2(log_z, make_float2(-vref[x], -vref[x])));
+                };
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    w[0][x] = d4_ex2(lg[0][x] - mrun[x]);
-                    w[1][x] = d4_ex2(lg[1][x] - mrun[x]);
-                    p[x] = pack_half2(w[0][x] * (fpv[x] * z.x), w[1][x] * (fpv[x] * z.y));
-                    rare |= fmaxf(lg[0][x], lg[1][x]) > mrun[x] || !__hble2(u32_as_h2(p[x]), u32_as_h2(0x70007000u));  // 2^13
+                    relate(x);
+                    rare |= fmaxf(lg[0][x], lg[1][x]) > mrun[x] || fmaxf(P[x].x, P[x].y) > D4_PV_MOST;
                 }
                 if (__any_sync(0xffffffffu, rare)) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
-                        float top = fmaxf(lg[0][x], lg[1][x]);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), mrun[x]);
-                        float c = d4_ex2(mrun[x] - top);
-                        const float f = fpv[x] * d4_ex2(top - mrun[x]);
-                        mrun[x] = top;
-                        lsum[x] *= c;
-                        c = f <= D4_PV_FACTOR ? 1.f : c * __fdividef(D4_PV_FACTOR, fpv[x]);  // of the accumulators
-                        fpv[x] = fminf(f, D4_PV_FACTOR);
-                        w[0][x] = d4_ex2(lg[0][x] - mrun[x]);
-                        w[1][x] = d4_ex2(lg[1][x] - mrun[x]);
-                        float P0 = w[0][x] * (fpv[x] * z.x), P1 = w[1][x] * (fpv[x] * z.y);
-                        top = fmaxf(P0, P1);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        if (top > 8192.f) {  // to [2^11, 2^12), by a power of two
-                            const float down = __uint_as_float((265u - (__float_as_uint(top) >> 23)) << 23);
-                            fpv[x] *= down;
-                            P0 *= down;
-                            P1 *= down;
-                            c *= down;
-                        }
-                        p[x] = pack_half2(P0, P1);
+                        float top = fmaxf(lg[0][x], lg[1][x]), vtop = fmaxf(P[x].x, P[x].y) > D4_PV_MOST ? fmaxf(lg[0][x] + (log_z.x - D4_WHOLE), lg[1][x] + (log_z.y - D4_WHOLE)) : D4_NEG;
 #pragma unroll
-                        for (int m = 0; m < 8; ++m) {
-                            oacc[m][x] *= c;
-                            oacc[m][x + 2] *= c;
-                            if (NT == 1) {
-                                oacc[m][1] *= c;
-                                oacc[m][3] *= c;
-                            }
+                        for (int o = 4; o <= 16; o <<= 1) {
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
                         }
-                        cmin[x] *= c;
-                        if (NT == 1) cmin[1] *= c;
+                        top = fmaxf(top, mrun[x]);
+                        lsum[x] *= d4_ex2(mrun[x] - top);
+                        mrun[x] = top;
+                        if (vtop > D4_NEG) {  // (in some lane, of all that have the head)
+                            const float to = ceilf(vtop) - D4_PV_TOP + D4_WHOLE, c = d4_ex2(vref[x] - to);
+                            vref[x] = to;
+                            relate(x);
+#pragma unroll
+                            for (int m = 0; m < 8; ++m) {
+                                oacc[m][x] *= c;
+                                oacc[m][x + 2] *= c;
+                                if (NT == 1) {
+                                    oacc[m][1] *= c;
+                                    oacc[m][3] *= c;
+                                }
+                            }
+                            cmin[x] *= c;
+                            if (NT == 1) cmin[1] *= c;
+                        }
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < NT; ++x) lsum[x] += w[0][x] + w[1][x];
+                for (int x = 0; x < NT; ++x) {
+                    const float2 w = d4_add2(make_float2(lg[0][x], lg[1][x]), make_float2(-mrun[x], -mrun[x]));
+                    P[x] = make_float2(d4_ex2(P[x].x), d4_ex2(P[x].y));
+                    lsum[x] += d4_ex2(w.x) + d4_ex2(w.y);
+                }
+                if constexpr (NT == 1) {
+                    p[0] = pack_half2(P[0].x, P[0].y);
+                } else {
+                    p[0] = pack_half2(P[0].x, P[1].x);
+                    p[1] = pack_half2(P[0].y, P[1].y);
+                }
             };
 
             // Pipelined by pages: the logits of the next page and the weighted sum of this
             // one share a block of code, so their latencies overlap.
             float lg[2][NT];
-            uint32_t p[NT], sizes = 0, size = 0;  // sizes: of the unit's pages; size: of the page whose weights p holds
+            uint32_t p[NT], invs = 0, f = 0, next = 0;  // f: 1 / size of tokens 2 t + 8 (r & 1) and the next, of the page whose weights p holds
+            float logs = 0.f;
+            auto page_logs = [&](int e) { return make_float2(__shfl_sync(0xffffffffu, logs, 16 * e + r), __shfl_sync(0xffffffffu, logs, 16 * e + r + 8)); };
+            auto page_inv = [&](int e) { return __shfl_sync(0xffffffffu, invs, 16 * e + 2 * t + 8 * (r & 1)); };
             Counts nt = wait_unit(n_units == 1);
             if (!dead) {
                 logits(0, U * st, 0, nt.n[0], lg);
-                sizes = unit_sizes(st);
+                unit_sizes(st, logs, invs);
+                f = page_inv(0);
             }
 #pragma unroll 1
             for (int k = 0; k < n_units && !dead; ++k) {
-                size = page_sizes(sizes, 0);
-                softmax(lg, size, p);
+                softmax(lg, page_logs(0), p);
 #pragma unroll
                 for (int e = 1; e < U; ++e) {
                     logits(k, U * st + e, e, nt.n[e], lg);
-                    pv_page(U * st + e - 1, size, p);
-                    size = page_sizes(sizes, e);
-                    softmax(lg, size, p);
+                    next = page_inv(e);
+                    pv_page(U * st + e - 1, f, p);
+                    f = next;
+                    softmax(lg, page_logs(e), p);
                 }
                 ++done;
                 const int last = U * st + U - 1;
@@ -1027,14 +1044,16 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                     parity ^= 1u;
                 }
                 if (k + 1 == n_units) {
-                    pv_page(last, size, p);
+                    pv_page(last, f, p);
                     break;
                 }
                 nt = wait_unit(k + 2 == n_units);
                 if (dead) break;
                 logits(k + 1, U * st, 0, nt.n[0], lg);
-                sizes = unit_sizes(st);
-                pv_page(last, size, p);
+                unit_sizes(st, logs, invs);
+                next = page_inv(0);
+                pv_page(last, f, p);
+                f = next;
                 __syncwarp();
                 // hand the group back, and the ones that the last segment's partial held
                 if (s > 0 && freed < end1) {
@@ -1060,10 +1079,12 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         if (has) {
             float* op = reinterpret_cast<float*>(sm.ring[warp][U * at]);
             auto min_of = [&](float c, int g) { return __shfl_sync(0xffffffffu, c, 8 * g + t) + __shfl_sync(0xffffffffu, c, 8 * g + 4 + t); };
-            float inv[NT], lo[NT], hi[NT];  // 1 / (2 F), and what the codes' places (2^-24, 2^-20) make of it
+            // p size / P, and what the codes' places (2^-24, 2^-20) make of it
+            float inv[NT], lo[NT], hi[NT];
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                inv[x] = __fdividef(0.5f, fpv[x]);
+                const float whole = rintf(mrun[x]);
+                inv[x] = d4_ex2(whole - mrun[x]) * d4_ex2((vref[x] - D4_WHOLE) - whole);
                 lo[x] = 16777216.f * inv[x];
                 hi[x] = 1048576.f * inv[x];
             }
