@@ -90,8 +90,11 @@ def _check(status: int):
 
 
 def _stream(stream) -> int:
-    if stream is None:  # (the handle itself: making a Stream object of it costs 2.5 us, as much as a launch)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        dev = torch.cuda.current_device()
+        # the handle itself, where torch has a name for it: making a Stream object of it costs 2.5 us, as much as a launch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
