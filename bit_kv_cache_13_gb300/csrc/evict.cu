@@ -472,6 +472,13 @@ extern "C" kvq_status kvq_evict_gather_int4(const void* cache, int64_t num_pages
             return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: weights strides %lld, %lld below 16 * pages per sequence", fn,
                                  (long long)weights_stride, (long long)weights_out_stride);
         if (weights == weights_out) return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: weights_out is weights", fn);
+        // rows of the one between rows of the other are fine, a common float is read by one CTA and written by another
+        const size_t last = (size_t)B * H_kv - 1, from = (size_t)max_pages_per_seq * PAGE, to = (size_t)dst_max_pages * PAGE;
+        if (overlap(weights, (last * weights_stride + from) * 4, weights_out, (last * weights_out_stride + to) * 4)) {
+            const int64_t floats = weights_out - weights, at = ((floats % weights_stride) + weights_stride) % weights_stride;
+            if (last == 0 || weights_stride != weights_out_stride || at < (int64_t)from || at + (int64_t)to > weights_stride)
+                return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: weights_out must not overlap weights", fn);
+        }
     }
     // pages past the budget only have weights to clear
     const int pages = weights ? dst_max_pages : (budget + PAGE - 1) / PAGE;

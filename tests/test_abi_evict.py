@@ -1,4 +1,4 @@
-"""Refusals of kvq_evict_select on the host (no GPU) where what it writes overlaps what it reads."""
+"""Refusals of the eviction calls on the host (no GPU) where what they write overlaps what they read."""
 import os
 
 import pytest
@@ -40,3 +40,23 @@ def test_neighbours_are_not(lib, kw):
     a = dict(new=NEW, keep=KEEP) | kw
     lib.kvq_evict_select(W, STRIDE, B, H, T, LENS, BUDGET, 1, 1, a["keep"], a["new"], None)
     assert "overlap" not in lib.kvq_last_error().decode()   # (it goes on to the device, of which there is none)
+
+
+# rows of 64 floats (4 source pages) in, of 32 (2 destination pages) out
+def _gather(lib, wo, stride, wo_stride, rows=(3, 2)):
+    a, b = 0x800000, 0x900000
+    lib.kvq_evict_gather_int4(a, 4, LENS, 4, KEEP, 20, NEW, *rows, 128, b, 4, LENS, 2, W, stride, wo, wo_stride, None, None)
+    return "must not overlap weights" in lib.kvq_last_error().decode()
+
+
+@host_only
+@pytest.mark.parametrize("floats,stride,wo_stride", [(1, 64, 32), (5 * 64 + 63, 64, 32), (-5 * 32 - 31, 64, 32), (63, 96, 96), (65, 96, 96),
+                                                     (64, 100, 96), (64 - 96, 95, 95)])
+def test_weights_out_over_weights_is_refused(lib, floats, stride, wo_stride):
+    assert _gather(lib, W + 4 * floats, stride, wo_stride)
+
+
+@host_only
+@pytest.mark.parametrize("floats,stride,wo_stride", [(6 * 64, 64, 32), (-6 * 32, 64, 32), (64, 96, 96), (64 - 2 * 96, 96, 96), (70, 128, 128)])
+def test_weights_out_beside_or_between_rows_is_not(lib, floats, stride, wo_stride):
+    assert not _gather(lib, W + 4 * floats, stride, wo_stride)
