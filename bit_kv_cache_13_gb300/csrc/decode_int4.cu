@@ -30,10 +30,13 @@
 //           So no operand overflows, and what fp16 cuts off below 2^-24 is 2^-29 of the
 //           context's largest term, however small or large the weights are or the values
 //           (6e-5 and up; smaller sizes count as that): a sink with small values, or none,
-//           does not take the other tokens' digits.  P transposes from
-//           the QK layout by movmatrix.  Up to four heads fill the eight columns as
-//           (tokens 0..7, tokens 8..15) of each head, which the end adds.  The mins are
-//           one more MMA.
+//           does not take the other tokens' digits.  P transposes from the QK layout by
+//           movmatrix.  Up to four heads fill the eight columns as (tokens 0..7, tokens
+//           8..15) of each head, which the end adds.  The mins are one more MMA.  A page's
+//           products start from zero and are added in fp32, to nearest: an MMA cuts its
+//           terms off toward zero, at 2^-25 of its accumulator, and the codes' and the
+//           mins' sums, each of one sign, would drift apart (equal weights of 128K tokens
+//           of values around zero in one CTA: 0.9 % of the output, 0.19 % so).
 //
 // Three kernels, chained by programmatic dependent launch so that each one's
 // start overlaps the end of the one before:
@@ -865,7 +868,11 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 {   // min term: row r holds group r / 2, tokens 0..7 (r even) or 8..15 (r odd)
                     const uint32_t m = h2_as_u32(__hmul2(u32_as_h2(lds32(tile + O4_VM + 16 * (t + 4 * (r & 1)) + 4 * (r >> 1))), u32_as_h2(f)));
                     const uint32_t am[4] = {odd ? 0u : m, 0u, odd ? m : 0u, 0u};
-                    mma_f16_16816(cmin, am, pb0, pb1);
+                    float d[4];
+                    d4_mma0(d, am, pb0, pb1);
+                    const float2 c = d4_add2(make_float2(cmin[0], cmin[1]), make_float2(d[0], d[1]));
+                    cmin[0] = c.x;
+                    cmin[1] = c.y;
                 }
                 const uint4 va = lds128(tile + O4_VC + 128 * t + 16 * r), vb = lds128(tile + O4_VC + 128 * (t + 4) + 16 * r);
                 const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
@@ -877,7 +884,14 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                     for (int hs = 0; hs < 2; ++hs) {
                         const uint32_t A = hs ? wa[gg] >> 8 : wa[gg], Bw = hs ? wb[gg] >> 8 : wb[gg];
                         const uint32_t af[4] = {A & 0x000f000fu, A & 0x00f000f0u, Bw & 0x000f000fu, Bw & 0x00f000f0u};
-                        mma_f16_16816(oacc[2 * gg + hs], af, h0, h1);
+                        float d[4];
+                        d4_mma0(d, af, h0, h1);
+                        float (&o)[4] = oacc[2 * gg + hs];
+                        const float2 lo = d4_add2(make_float2(o[0], o[1]), make_float2(d[0], d[1])), hi = d4_add2(make_float2(o[2], o[3]), make_float2(d[2], d[3]));
+                        o[0] = lo.x;
+                        o[1] = lo.y;
+                        o[2] = hi.x;
+                        o[3] = hi.y;
                     }
                 }
             };
