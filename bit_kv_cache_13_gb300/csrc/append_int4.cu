@@ -170,13 +170,12 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
 // together in one list: fp64 is 64 times slower than fp32 here, and a first form of
 // these second looks in fp64 took most of the kernel's time.
 //
-// 32K tokens of eight heads: 255 us, bound by the instructions of the epilogue and the
-// second looks (47 % issue, four warps per scheduler at 126 registers, the tensor pipe
-// 33 %); without the second looks it takes 190 us, with one part of R in place of three
-// another 50 less.
+// 32K tokens of eight heads: 263 us, bound by the instructions of the epilogue and the
+// second looks (50 % issue, four warps per scheduler at 128 registers, the tensor pipe
+// 30 %).
 constexpr int PF_WORKERS = 4, PF_M = 32;  // tokens of a worker's tile
 constexpr float PF_NORM = 4.625f * 0x1p-23f, PF_MOST = 4.125f * 0x1p-23f;
-constexpr int PF_KEY_COST = 5, PF_VALUE_COST = 4;  // of a tile's time (more keys are looked at twice: the centre is in their bound)
+constexpr int PF_KEY_COST = 6, PF_VALUE_COST = 5;  // of a tile's time (more keys are looked at twice: the centre is in their bound)
 constexpr int PF_A = D + 8;               // padded rows, in elements
 
 struct __align__(16) PrefillWorker {
@@ -758,9 +757,9 @@ extern "C" size_t kvq_int4_tile_bytes(int d) { return d == D ? (size_t)INT4_TILE
 
 // Token-heads from which on the tensor-core kernel is taken, for each wave of its CTAs:
 // it starts in about 12 us a wave (R's operand parts), the few-token kernel takes 0.03 us a
-// token-head.  With the read-back: 33 tokens of 8 heads 14.5 against 11.2 us, 64 tokens of
-// one head 13.4 against 5.2, 128 of two 18.0 against 11.6, 64 of 8 14.2 against 17.8, 128 of
-// 8 19.5 against 30.8.
+// token-head.  With the read-back: 33 tokens of 8 heads 13.9 against 11.2 us, 64 tokens of
+// one head 13.1 against 5.2, 128 of two 14.5 against 11.6, 64 of 8 14.4 against 17.9, 128 of
+// 8 15.1 against 30.8.
 static constexpr int PREFILL_MIN = 400;
 
 static kvq_status prefill_smem_once() {
@@ -807,7 +806,8 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
     if (sa != KVQ_OK) return sa;
     // One CTA per SM in all, each with a stride of its (head, side)'s tiles; a head's are
     // split between its sides so that the later of them ends soonest, in rounds of a tile
-    // per worker (32K tokens, 8 heads, with read-back: 317 us for equal halves, 290 us).
+    // per worker (32K tokens, 8 heads, with read-back: 326 us for equal halves, 306 for 5 to 4,
+    // 298 for 6 to 5).
     const int tiles = (n_tok + PF_M - 1) / PF_M, most = nsm / H_kv;
     auto rounds = [&](int ctas) { return (int)((tiles + (int64_t)ctas * PF_WORKERS - 1) / ((int64_t)ctas * PF_WORKERS)); };
     int nk = 1;

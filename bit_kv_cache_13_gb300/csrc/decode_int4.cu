@@ -4,8 +4,8 @@
 //   q' = q R_k;  a_s = <q', K^_s> scale;  p = softmax(a);  o = (sum_s p_s V^_s) R_v^T
 //
 // Bound by the 160 bytes of packed cache per token-head, if the instructions
-// that unpack them fit under the stream (32 q / 8 KV heads, batch 1, 128K: 34 us, 4.9 TB/s;
-// batch 8, 32K: 64.6 us, 5.2 TB/s; from 128K to 256K tokens another 24 us, 6.9 TB/s: the
+// that unpack them fit under the stream (32 q / 8 KV heads, batch 1, 128K: 37 us, 4.5 TB/s;
+// batch 8, 32K: 70.4 us, 4.8 TB/s; from 128K to 256K tokens another 25 us, 6.6 TB/s: the
 // rest is the launch, the rotations, the merge).  One CTA of 12 warps per SM, every warp
 // streaming pages through a ring of its own (bulk copies, one mbarrier per unit
 // of one or two pages), all products on mma.sync m16n8k16 with the codes as operands.
@@ -57,8 +57,7 @@
 // pages of all (sequence, KV head) units are laid end to end and every CTA takes
 // an equal share, so a ragged batch or a short context in a long table stays
 // balanced.  With eight heads to a KV head the instructions bound it: 32 ragged
-// sequences of up to 4K, 64 q / 8 KV heads, 47.5 us for 84 MB, of which the pages 20 us
-// (62 % issue), the start of the chain 10, merging and finishing 12.
+// sequences of up to 4K, 64 q / 8 KV heads, 53 us for 84 MB (12.5 at the copy rate).
 #include <cstddef>
 #include <mutex>
 
@@ -67,10 +66,10 @@
 namespace kvq {
 
 // NW warps of a CTA (three per scheduler at 168 registers), U pages per unit of a
-// warp's ring (one mbarrier phase, one refill), UNITS units in the ring.  At 128K,
-// 32 q / 8 KV heads, batch 1: 12 warps with units of two pages 41.3 us, of one page
-// 48.4 us, 16 warps (128 registers, one page) 49.4 us, 8 warps with units of three
-// 41.0 us and of two 47.2 us.
+// warp's ring (one mbarrier phase, one refill), UNITS units in the ring.  Batch 8 at 32K,
+// 32 q / 8 KV heads: 12 warps with three units 70.4 us, 8 warps with four 76; 128K, batch 1:
+// 37.3 and 40.0.  (In a first form of the kernel, 128K: 12 warps with units of two pages
+// 41.3 us, of one page 48.4, 16 warps with one page 49.4.)
 template <int NT>
 struct D4Cfg {
     static constexpr int NW = 12, U = 2, UNITS = 3;
@@ -78,8 +77,8 @@ struct D4Cfg {
 constexpr int D4_MAX_SPLITS = 254;
 constexpr int D4_MIN_PAGES = 24;   // pages per CTA below which an automatic split goes no further: a unit a warp
 // What starting another unit costs a CTA, in pages streamed.  30 ragged sequences of up to
-// 8000 tokens, 64 q / 8 KV heads: 87 us for 10, 76 for 20, 64.2 for 40, 60.7 for 60, 62.2 for
-// 110; 32 of up to 4000, 32 q heads: 54.8, 46.6, 37.1, 36.9, 38.2.
+// 8000 tokens, 64 q / 8 KV heads: 84 us for 20, 69.7 for 40, 68.8 for 60, 70.8 for 110; 32 of
+// up to 4000, 32 q heads: 49.4, 39.5, 39.5, 41.0.
 constexpr int D4_SEG_PAGES = 60;
 constexpr int D4_ONE_PAGES = 96;   // pages per CTA up to which a few sequences go without an even split
 constexpr float D4_NEG = -3e38f;   // running maximum before any token
@@ -539,7 +538,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     // (0: past the warp's pages).  The next batch's ids load while this one is issued.
     D4Walk is = cs;
     int ik = 0, in = is.units<NW, U>(warp), issued = 0, built = 0;
-    constexpr int BATCH = 32 / U;  // (for U = 3, lanes 30 and 31 hold nothing)
+    constexpr int BATCH = 32 / U;
     auto build = [&](int& pid, int& hn) {  // the units after the first `built`
         pid = hn = 0;
         int x = 0;
@@ -1619,13 +1618,13 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const int64_t units = (int64_t)B * H_kv;
     // A few units: one kernel (in the weights form, and the weights' one), whose CTAs have one
     // unit each.  Lengths differ, so of several sequences none may have more than
-    // D4_ONE_PAGES pages for each of its CTAs.  8 sequences of 300 tokens, 8 KV heads: 8.7 us
-    // against 12.5 in three kernels, 16 of up to 1500 16.7 against 23.9; 3 of up to 8000
-    // (84 pages a CTA) 15.5 against 14.1.  In the weights form, where the third kernel runs
-    // anyway and would have merged the partials, only up to two CTAs per unit (8 of 700 tokens
-    // 14.0 against 16.0 us, but 4 of up to 1959 with 4 heads 17.2 against 15.5) and for a single
-    // sequence (2048 tokens: 13.9 against 13.0 us in a graph, but 14.9 against 16.7 when each
-    // launch is paid for on the host).
+    // D4_ONE_PAGES pages for each of its CTAs.  8 sequences of 300 tokens, 8 KV heads: 9.3 us
+    // against 12.8 in three kernels, 16 of 1500 14.2 against 20.2; 3 of up to 8000 (84 pages a
+    // CTA) 16.5 against 14.7.  In the weights form, where the third kernel runs anyway and
+    // would have merged the partials, only up to two CTAs per unit (8 of 700 tokens 14.4
+    // against 15.5 us, but 4 of up to 1959 with 4 heads 14.4 against 13.7) and for a single
+    // sequence (2048 tokens: 14.3 against 13.6 us in a graph, but one launch fewer to pay for
+    // on the host).
     const int per_unit = (int)(nsm / units);
     const bool small = max_pages <= (int64_t)D4_ONE_PAGES * per_unit;
     const bool one = num_splits == 0 && per_unit >= 1 && units <= D4_TICKETS &&
