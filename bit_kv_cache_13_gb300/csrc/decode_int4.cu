@@ -19,7 +19,7 @@
 //           is one more MMA over the four groups.  q' and S enter as an fp16 high and
 //           low part (22 bits): for up to four heads the parts sit side by side in the
 //           eight columns, for up to eight they are two MMAs into one accumulator.
-//   softmax base 2, against the running maximum of each head; the maximum is
+//   softmax base 2, against the running maximum of each head, rounded up; the maximum is
 //           raised (and the weights rescaled) only when a logit exceeds it, which
 //           one vote per unit decides.  Sums are fp32 of the unrounded p.
 //   PV      rows = 16 channels, K = 16 tokens, columns = heads; the second operand is
@@ -85,7 +85,7 @@ constexpr float D4_NEG = -3e38f;   // running maximum before any token
 // PV weights P are at most 2^D4_PV_MOST (with scales below 4, products below 2^15); where one is
 // above that, their reference moves, and the largest is 2^D4_PV_TOP or up to a bit less.
 constexpr float D4_PV_MOST = 13.f, D4_PV_TOP = 11.f;
-constexpr float D4_WHOLE = 12582912.f;  // 1.5 2^23: a sum with it is a whole number
+constexpr float D4_WHOLE = 12582912.f;  // 1.5 2^23: small numbers are rounded to whole ones by adding it
 constexpr long long D4_SHORT_WAIT_CYCLES = 2000000LL;  // about a millisecond: a wait's limit under the test hook
 
 __device__ __forceinline__ float d4_ex2(float x) {
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             }
         }
         const int n_units = dead ? 0 : cs.units<NW, U>(warp);
-        float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT], vref[NT];  // vref: the logit plus log2 size at which P is 1, plus D4_WHOLE
+        float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT], vref[NT];  // whole numbers; vref: log2 of p * size where P is 1
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         for (int e = 0; e < NT; ++e) {
             mrun[e] = D4_NEG;
             lsum[e] = 0.f;
-            vref[e] = D4_NEG;
+            vref[e] = 0.f;
         }
         if (n_units > 0) {
             if constexpr (!ONE) wait(&sm.qbar[buf], (s >> 1) & 1);
@@ -817,8 +817,8 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 }
             };
 
-            // Of the unit's two pages: log2 of the size of token lane & 15 of page lane >> 4, plus
-            // D4_WHOLE, and the inverses of its slot pair's two sizes.  Sizes are powers of two within
+            // Of the unit's two pages: log2 of the size of token lane & 15 of page lane >> 4, a whole
+            // number, and the inverses of its slot pair's two sizes.  Sizes are powers of two within
             // 2^-14 and 2^14, so that both they and their inverses are fp16 numbers; of a token whose
             // values are 0 the logarithm is -inf.
             static_assert(U == 2, "half a warp a page");
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 const uint32_t size = h2_as_u32(__hmin2(__hmax2(m, u32_as_h2(0x04000400u)), u32_as_h2(0x74007400u))) & 0x7c007c00u;
                 inv = 0x78007800u - size;
                 const __half2 z = __hmin2(u32_as_h2(size), __hmul2(m, u32_as_h2(0x78007800u)));
-                logs = d4_lg2(__half2float(lane & 1 ? __high2half(z) : __low2half(z))) + D4_WHOLE;
+                logs = (d4_lg2(__half2float(lane & 1 ? __high2half(z) : __low2half(z))) + D4_WHOLE) - D4_WHOLE;
             };
 
             auto pv_page = [&](int slot, uint32_t f, const uint32_t (&p)[NT]) {
@@ -972,10 +972,11 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             // Where a logit exceeds the running maximum or a P what it may be (one vote), the one
             // or the other reference is raised.
             auto softmax = [&](const float (&lg)[2][NT], float2 log_z, uint32_t (&p)[NT]) {
-                float2 P[NT];  // first their logarithms
+                float2 w[NT], P[NT];  // first their logarithms
                 bool rare = false;
                 auto relate = [&](int x) {  // (whole numbers first: what a reference moves by cancels exactly)
-                    P[x] = d4_add2(make_float2(lg[0][x], lg[1][x]), d4_add2(log_z, make_float2(-vref[x], -vref[x])));
+                    w[x] = d4_add2(make_float2(lg[0][x], lg[1][x]), make_float2(-mrun[x], -mrun[x]));
+                    P[x] = d4_add2(w[x], d4_add2(log_z, make_float2(-vref[x], -vref[x])));
                 };
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
@@ -985,19 +986,21 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 if (__any_sync(0xffffffffu, rare)) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
-                        float top = fmaxf(lg[0][x], lg[1][x]), vtop = fmaxf(P[x].x, P[x].y) > D4_PV_MOST ? fmaxf(lg[0][x] + (log_z.x - D4_WHOLE), lg[1][x] + (log_z.y - D4_WHOLE)) : D4_NEG;
+                        float top = fmaxf(lg[0][x], lg[1][x]), vtop = fmaxf(lg[0][x] + log_z.x, lg[1][x] + log_z.y);
 #pragma unroll
                         for (int o = 4; o <= 16; o <<= 1) {
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                             vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
                         }
-                        top = fmaxf(top, mrun[x]);
-                        lsum[x] *= d4_ex2(mrun[x] - top);
+                        top = fmaxf(ceilf(top), mrun[x]);
+                        const float up = top - mrun[x];
+                        lsum[x] *= d4_ex2(-up);
                         mrun[x] = top;
-                        if (vtop > D4_NEG) {  // (in some lane, of all that have the head)
-                            const float to = ceilf(vtop) - D4_PV_TOP + D4_WHOLE, c = d4_ex2(vref[x] - to);
-                            vref[x] = to;
-                            relate(x);
+                        vref[x] -= up;  // (the values' sums stay)
+                        vtop = ceilf((vtop - top) + fabsf(top) * 0x1p-22f);  // (with what its sum's rounding may have cost)
+                        if (vtop - vref[x] > D4_PV_MOST) {
+                            const float c = d4_ex2(vref[x] - (vtop - D4_PV_TOP));
+                            vref[x] = vtop - D4_PV_TOP;
 #pragma unroll
                             for (int m = 0; m < 8; ++m) {
                                 oacc[m][x] *= c;
@@ -1010,13 +1013,13 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                             cmin[x] *= c;
                             if (NT == 1) cmin[1] *= c;
                         }
+                        relate(x);
                     }
                 }
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    const float2 w = d4_add2(make_float2(lg[0][x], lg[1][x]), make_float2(-mrun[x], -mrun[x]));
                     P[x] = make_float2(d4_ex2(P[x].x), d4_ex2(P[x].y));
-                    lsum[x] += d4_ex2(w.x) + d4_ex2(w.y);
+                    lsum[x] += d4_ex2(w[x].x) + d4_ex2(w[x].y);
                 }
                 if constexpr (NT == 1) {
                     p[0] = pack_half2(P[0].x, P[0].y);
@@ -1096,8 +1099,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             float inv[NT], lo[NT], hi[NT];
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                const float whole = rintf(mrun[x]);
-                inv[x] = d4_ex2(whole - mrun[x]) * d4_ex2((vref[x] - D4_WHOLE) - whole);
+                inv[x] = d4_ex2(vref[x]);
                 lo[x] = 16777216.f * inv[x];
                 hi[x] = 1048576.f * inv[x];
             }

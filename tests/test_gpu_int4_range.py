@@ -106,3 +106,33 @@ def test_values_times_a_power_of_two(g, splits):
         d.gpu[..., 2304:] = (meta * np.float16(2.0 ** power)).view(np.uint8)
         got, _ = d.run(splits)
         assert np.array_equal(got, want * 2.0 ** power)
+
+
+@pytest.mark.parametrize("g", [4, 8])
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("size", [2e4, 1e5, 3e5])   # of the keys: logits of a million and more
+def test_logits_of_millions(g, splits, size):
+    """Far apart logits: one token has all the weight, and the output is its values, of whatever size."""
+    for v_size in (1e-3, 2e-3, 1.0, 2.0, 1e3, 2e3):
+        c = _Range(2 * g, 2, [900, 100], v_size, q_scale=200.0, seed=6)
+        meta = c.gpu[..., 1024:1280].copy().view(np.float16)
+        c.gpu[..., 1024:1280] = np.clip(meta.astype(np.float64) * size / 10, -65504, 65504).astype(np.float16).view(np.uint8)
+        tiles = c.cache[c.bt[0, :56], 0]
+        a = int4.values(tiles, 0).reshape(-1, 128) @ (c.q[0, 0].double().numpy() @ c.rk[0].astype(np.float64)) * SCALE
+        assert abs(a).max() > 25 * size
+        got, _ = c.run(splits)
+        assert c.status == 0 and np.isfinite(got).all()
+        for b in range(2):
+            for h in range(2):
+                n = int(c.ctx[b])
+                tiles = c.cache[c.bt[b, : (n + 15) // 16], h]
+                k, v = (int4.values(tiles, side).reshape(-1, 128)[:n] for side in (0, 1))
+                for j in range(h * g, (h + 1) * g):
+                    a = k @ (c.q[b, j].double().numpy() @ c.rk[h].astype(np.float64)) * SCALE
+                    order = np.argsort(a)
+                    if a[order[-1]] - a[order[-2]] < 2.0 ** -15 * abs(a).max() + 20:   # (logits are fp32 numbers)
+                        continue
+                    want = v[order[-1]] @ c.rv[h].astype(np.float64).T
+                    # bf16 2^-8, the two fp16 roundings of the one weight and its products, fp32 sums
+                    spread = np.abs(v[order[-1]]).max() * 128 ** 0.5 * 2
+                    assert np.linalg.norm(got[b, j] - want) <= 2.0 ** -8 * np.linalg.norm(want) + (2.0 ** -10 + 2.0 ** -16) * spread
