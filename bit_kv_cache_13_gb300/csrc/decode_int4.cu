@@ -5,7 +5,7 @@
 //
 // Bound by the 160 bytes of packed cache per token-head, if the instructions
 // that unpack them fit under the stream (32 q / 8 KV heads, batch 1, 128K: 37 us, 4.5 TB/s;
-// batch 8, 32K: 70.4 us, 4.8 TB/s; from 128K to 256K tokens another 25 us, 6.6 TB/s: the
+// batch 8, 32K: 70.0 us, 4.8 TB/s; from 128K to 256K tokens another 25 us, 6.6 TB/s: the
 // rest is the launch, the rotations, the merge).  One CTA of 12 warps per SM, every warp
 // streaming pages through a ring of its own (bulk copies, one mbarrier per unit
 // of one or two pages), all products on mma.sync m16n8k16 with the codes as operands.
@@ -67,7 +67,7 @@ namespace kvq {
 
 // NW warps of a CTA (three per scheduler at 168 registers), U pages per unit of a
 // warp's ring (one mbarrier phase, one refill), UNITS units in the ring.  Batch 8 at 32K,
-// 32 q / 8 KV heads: 12 warps with three units 70.4 us, 8 warps with four 76; 128K, batch 1:
+// 32 q / 8 KV heads: 12 warps with three units 70.4 us, 8 warps with four 76.0; 128K, batch 1:
 // 37.3 and 40.0.  (In a first form of the kernel, 128K: 12 warps with units of two pages
 // 41.3 us, of one page 48.4, 16 warps with one page 49.4.)
 template <int NT>
