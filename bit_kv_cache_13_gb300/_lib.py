@@ -45,6 +45,10 @@ _SIGS = {
     "kvq_decode_attn_int4_weights": ([P, I, I, I, I, P, I64, P, I, P, P, P, F, P, P, I64, F, P, SZ, I, P], I),
     "kvq_evict_select": ([P, I64, I, I, I, P, I, I, I, P, P, P], I),
     "kvq_evict_gather_int4": ([P, I64, P, I, P, I, P, I, I, I, P, I64, P, I, P, I64, P, I64, P, P], I),
+    "kvq_append_rope_int4": ([P, I64, P, I64, P, I64, I, I, I, I, P, P, I, I, I, P, P, D, P, P, P, P, F, P, I64, P, P, P, P], I),
+    "kvq_decode_attn_int4_sliding": ([P, I, I, I, I, P, I64, P, I, P, P, P, F, I, I, P, P, SZ, I, P], I),
+    "kvq_chunk_workspace_bytes": ([I, I, I, I], SZ),
+    "kvq_chunk_attn_int4": ([P, I, P, I, I, I, I, P, I64, P, I, P, P, P, F, I, I, P, P, SZ, P], I),
     "bgtq_lloyd_max_codebook": ([I, P], I),
     "bgtq_allocate": ([P, I, I, I, I64, P], I),
     "bgtq_tile_bytes": ([I, I], SZ),
@@ -303,6 +307,43 @@ def kvq_append_int4(k, v, slot_mapping, mu_k, R_k, R_v, cache, num_pages: int, c
         _ptr(cache, _U8, None, dev, "cache"), int(num_pages), _count(err_count, dev)), stream)
 
 
+def _heads(x, n_tok, dev: int, name: str):
+    """Device pointer and token stride of x [n_tok, heads, 128], each token's heads one behind the other."""
+    if x.dim() != 3 or x.shape[0] != n_tok:
+        raise ValueError(f"{name} must have shape ({n_tok}, heads, d), got {tuple(x.shape)}")
+    if x.dtype is not _BF16 or x.get_device() != dev:
+        _ptr(x, _BF16, None, dev, name)
+    _, s1, s2 = x.stride()
+    if x.numel() and ((s2 != 1 and x.shape[2] > 1) or (s1 != x.shape[2] and x.shape[1] > 1)):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return x.data_ptr(), x.stride(0) if n_tok > 1 else x.shape[1] * x.shape[2]
+
+
+def kvq_append_rope_int4(q, k, v, positions, rope, slot_mapping, mu_k, R_k, R_v, cache, num_pages: int, q_out, k_out,
+                         q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, clip: float = 1.0,
+                         err_count=None, stream=None):
+    """From a projection's q [n, H_q, d], k and v [n, H_kv, d] bf16 (views with a token stride of their own) to the INT4
+    cache: the heads' norms of q and k (with q_weight, k_weight [d] bf16), the rotation by positions [n] through the table
+    rope [max_pos, rot_dim] fp32 (cosines, then sines), the results in q_out and k_out, and kvq_append_int4 of k_out and v."""
+    n_tok, h_q, d = q.shape
+    h_kv, dev = k.shape[1], _here(q)
+    _pool(cache, num_pages, h_kv, "cache")
+    max_pos, rot = rope.shape
+    q_at, q_stride = _heads(q, n_tok, dev, "q")
+    k_at, k_stride = _heads(k, n_tok, dev, "k")
+    v_at, v_stride = _heads(v, n_tok, dev, "v")
+    if v.shape != k.shape or k.shape[2] != d:
+        raise ValueError(f"k and v must have shape ({n_tok}, heads, {d}), got {tuple(k.shape)} and {tuple(v.shape)}")
+    _call(load().kvq_append_rope_int4, dev, (
+        q_at, q_stride, k_at, k_stride, v_at, v_stride, n_tok, h_q, h_kv, d,
+        _ptr(positions, _I32, (n_tok,), dev, "positions"), _ptr(rope, _F32, None, dev, "rope"), max_pos, rot, int(interleaved),
+        _ptr(q_weight, _BF16, (d,), dev, "q_weight"), _ptr(k_weight, _BF16, (d,), dev, "k_weight"), float(eps),
+        _ptr(slot_mapping, _I32, (n_tok,), dev, "slot_mapping"), _ptr(mu_k, _F32, (h_kv, d), dev, "mu_k"),
+        _ptr(R_k, _F32, (h_kv, d, d), dev, "R_k"), _ptr(R_v, _F32, (h_kv, d, d), dev, "R_v"), float(clip),
+        _ptr(cache, _U8, None, dev, "cache"), int(num_pages), _ptr(q_out, _BF16, (n_tok, h_q, d), dev, "q_out"),
+        _ptr(k_out, _BF16, (n_tok, h_kv, d), dev, "k_out"), _count(err_count, dev)), stream)
+
+
 def kvq_dequant_int4(cache, num_pages: int, H_kv: int, slot_mapping, k_rot=None, v_rot=None, stream=None):
     """Dequantised rotated vectors [n, H_kv, d] bf16 of the cached tokens at slot_mapping [n]."""
     n, dev = slot_mapping.shape[0], _here(cache)
@@ -348,6 +389,38 @@ def kvq_decode_attn_int4_weights(q, cache, num_pages: int, block_table, context_
         *_decode_int4_args(dev, q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out),
         _ptr(weights, _F32, None, dev, "weights"), tokens, float(decay), _ptr(workspace, _U8, None, dev, "workspace"),
         workspace.numel(), int(num_splits)), stream)
+
+
+def kvq_decode_attn_int4_sliding(q, cache, num_pages: int, block_table, context_lens, R_k, R_v, scale: float, window: int,
+                                 sinks: int, out, workspace, num_splits: int = 0, stream=None):
+    """kvq_decode_attn_int4 over the last `window` tokens of each sequence and its first `sinks`."""
+    dev = _here(q)
+    *args, out_at = _decode_int4_args(dev, q, cache, num_pages, block_table, context_lens, R_k, R_v, scale, out)
+    _call(load().kvq_decode_attn_int4_sliding, dev, (
+        *args, int(window), int(sinks), out_at, _ptr(workspace, _U8, None, dev, "workspace"), workspace.numel(),
+        int(num_splits)), stream)
+
+
+def kvq_chunk_workspace_bytes(n_tok: int, B: int, H_q: int, H_kv: int) -> int:
+    return load().kvq_chunk_workspace_bytes(n_tok, B, H_q, H_kv)
+
+
+def kvq_chunk_attn_int4(q, q_start, cache, num_pages: int, block_table, context_lens, R_k, R_v, scale: float, out, workspace,
+                        window: int = 0, sinks: int = 0, stream=None):
+    """Attention of each sequence's last tokens over the INT4 cache, causal: rows q_start[b] .. q_start[b + 1] - 1 of q
+    [n, H_q, d] bf16 are the tokens at the end of sequence b's context_lens[b]; out [n, H_q, d] bf16.  window > 0: only the
+    last `window` tokens up to each, and the first `sinks`."""
+    dev = _here(q)
+    n_tok, h_q, d = shape = q.shape
+    h_kv, B = R_k.shape[0], context_lens.shape[0]
+    pages = _rows(block_table, (B,), "block_table", "max_pages")
+    _pool(cache, num_pages, h_kv, "cache")
+    _call(load().kvq_chunk_attn_int4, dev, (
+        _ptr(q, _BF16, None, dev, "q"), n_tok, _ptr(q_start, _I32, (B + 1,), dev, "q_start"), B, h_q, h_kv, d,
+        _ptr(cache, _U8, None, dev, "cache"), int(num_pages), _ptr(block_table, _I32, None, dev, "block_table"), pages,
+        _ptr(context_lens, _I32, (B,), dev, "context_lens"), _ptr(R_k, _F32, (h_kv, d, d), dev, "R_k"),
+        _ptr(R_v, _F32, (h_kv, d, d), dev, "R_v"), float(scale), int(window), int(sinks), _ptr(out, _BF16, shape, dev, "out"),
+        _ptr(workspace, _U8, None, dev, "workspace"), workspace.numel()), stream)
 
 
 def kvq_evict_select(weights, context_lens, budget: int, sinks: int, recent: int, keep, new_lens, stream=None):

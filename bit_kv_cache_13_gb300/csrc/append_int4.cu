@@ -34,6 +34,15 @@ __device__ __forceinline__ void store_meta(uint8_t* tile, int side, int s, int g
     }
 }
 
+// Token t's slot; -1 to skip it, -2 for one that is skipped and counted.
+__device__ __forceinline__ int append_slot(const AppendInt4& a, int64_t t) {
+    const int slot = __ldg(a.slot_mapping + t);
+    if (slot == -1) return -1;
+    bool ok = slot >= 0 && (int64_t)slot < a.num_pages * PAGE;
+    if (a.positions) ok = ok && (unsigned)__ldg(a.positions + t) < (unsigned)a.max_pos;
+    return ok ? slot : -2;
+}
+
 // ------------------------------------------------------------ a few tokens
 //
 // One CTA of 512 threads per (token, KV head, side): thread (channel, quarter)
@@ -43,30 +52,27 @@ __device__ __forceinline__ void store_meta(uint8_t* tile, int side, int s, int g
 // with the read-back in a second kernel, 4.5 us).
 
 __global__ void __launch_bounds__(512)
-append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, int n_tok, int H_kv,
-                   const int32_t* __restrict__ slot_mapping, const float* __restrict__ mu,
-                   const float* __restrict__ Rk, const float* __restrict__ Rv, uint8_t* __restrict__ cache,
-                   int64_t num_pages, int32_t* __restrict__ err_count, float clip) {
+append_int4_kernel(const __grid_constant__ AppendInt4 a) {
     __shared__ float xs[D], xl[D], n2s[4];
     __shared__ Dd part[4][D];
     const int t = blockIdx.x, h = blockIdx.y, side = blockIdx.z, tid = threadIdx.x;
     const int j = tid & (D - 1), quarter = tid >> 7, lane = tid & 31, g = (tid >> 5) & 3;
-    const float* R = (side ? Rv : Rk) + (size_t)h * D * D + (size_t)32 * quarter * D + j;
+    const float* R = (side ? a.R_v : a.R_k) + (size_t)h * D * D + (size_t)32 * quarter * D + j;
     prefetch_l2(R - j + (size_t)(j >> 2) * D + 32 * (j & 3));  // the quarter's 32 rows, four lines each
     griddep_wait();
     griddep_launch_dependents();
-    const int slot = __ldg(slot_mapping + t);
+    const int slot = append_slot(a, t);
     float rr[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) rr[i] = __ldg(R + (size_t)i * D);
-    if (slot < 0 || (int64_t)slot >= num_pages * PAGE) {
-        if (slot != -1 && tid == 0 && h == 0 && side == 0 && err_count) atomicAdd(err_count, 1);
+    if (slot < 0) {
+        if (slot != -1 && tid == 0 && h == 0 && side == 0 && a.err_count) atomicAdd(a.err_count, 1);
         return;
     }
     if (quarter == 0) {
-        const size_t row = ((size_t)t * H_kv + h) * D + j;
-        const float x = __bfloat162float(side ? v[row] : k[row]);
-        const float m = side ? 0.f : __ldg(mu + (size_t)h * D + j);
+        const size_t row = (size_t)t * (side ? a.v_stride : a.k_stride) + h * D + j;
+        const float x = __bfloat162float((side ? a.v : a.k)[row]);
+        const float m = side ? 0.f : __ldg(a.mu_k + (size_t)h * D + j);
         float hi, lo;
         two_sum(x, -m, hi, lo);  // (not finite: hi is, too, and lo does not matter)
         xs[j] = hi;
@@ -109,13 +115,13 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
             if (dd_less(a, mn)) mn = a;
             if (dd_less(mx, b)) mx = b;
         }
-        int4_params(mn, mx, clip, sh, mh);
+        int4_params(mn, mx, a.clip, sh, mh);
         const float s = __half2float(sh), m = __half2float(mh);
         // the nearest threshold decides between two codes (past the ends, and for s = 0, the end)
         const float q = s > 0.f ? fmaf(z.hi - m, 1.f / s, -0.5f) : -1.f;
         code = q <= -0.5f ? 0 : q >= INT4_LEVELS - 0.5f ? INT4_LEVELS : int4_code(z, s, m, (int)rintf(q));
     } else {  // all in fp64
-        const float* Rw = (side ? Rv : Rk) + (size_t)h * D * D + j;
+        const float* Rw = (side ? a.R_v : a.R_k) + (size_t)h * D * D + j;
         double w = 0.0;
         for (int i = 0; i < D; ++i) w = fma((double)xs[i] + (double)xl[i], (double)__ldg(Rw + (size_t)i * D), w);
         double lo = w, hi = w;
@@ -125,7 +131,7 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
             hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
         if (__any_sync(0xffffffffu, !isfinite(w))) lo = hi = CUDART_NAN;
-        int4_params(lo, hi, (double)clip, sh, mh);
+        int4_params(lo, hi, (double)a.clip, sh, mh);
         code = int4_code(w, sh, mh);
     }
     // the eight codes of a word sit in eight neighbouring lanes
@@ -133,7 +139,7 @@ append_int4_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __r
     w |= __shfl_xor_sync(0xffffffffu, w, 1);
     w |= __shfl_xor_sync(0xffffffffu, w, 2);
     w |= __shfl_xor_sync(0xffffffffu, w, 4);
-    uint8_t* tile = cache + ((size_t)(slot / PAGE) * H_kv + h) * INT4_TILE;
+    uint8_t* tile = a.cache + ((size_t)(slot / PAGE) * a.H_kv + h) * INT4_TILE;
     if ((lane & 7) == 0) store_word(tile, side, slot % PAGE, g, lane >> 3, w);
     if (lane == 0) store_meta(tile, side, slot % PAGE, g, sh, mh);
 }
@@ -298,23 +304,23 @@ __device__ __noinline__ int prefill_wild(const PrefillSmem& sm, const float* R, 
 }
 
 __global__ void __launch_bounds__(PF_WORKERS * 128, 1)
-append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, int n_tok, int H_kv,
-                           const int32_t* __restrict__ slot_mapping, const float* __restrict__ mu,
-                           const float* __restrict__ Rk, const float* __restrict__ Rv, uint8_t* __restrict__ cache,
-                           int64_t num_pages, int32_t* __restrict__ err_count, float clip, int key_ctas) {
+append_int4_prefill_kernel(const __grid_constant__ AppendInt4 args, int key_ctas) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     PrefillSmem& sm = *reinterpret_cast<PrefillSmem*>(smem_raw);
     const int h = blockIdx.y, side = blockIdx.x >= key_ctas, worker = threadIdx.x >> 7, tid = threadIdx.x & 127;
     const int g = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
     PrefillWorker& wk = sm.w[worker];
-    const float* R = (side ? Rv : Rk) + (size_t)h * D * D;
+    const float* R = (side ? args.R_v : args.R_k) + (size_t)h * D * D;
     prefetch_l2(R + 32 * threadIdx.x);  // (512 lines)
     griddep_wait();
     griddep_launch_dependents();
 
-    const int tiles = (n_tok + PF_M - 1) / PF_M, ctas = side ? gridDim.x - key_ctas : key_ctas, stride = ctas * PF_WORKERS;
-    const __nv_bfloat16* src = side ? v : k;
-    const int64_t n_slots = num_pages * PAGE;
+    const int n_tok = args.n_tok, tiles = (n_tok + PF_M - 1) / PF_M, ctas = side ? gridDim.x - key_ctas : key_ctas, stride = ctas * PF_WORKERS;
+    const __nv_bfloat16* src = (side ? args.v : args.k) + h * D;
+    const int64_t src_stride = side ? args.v_stride : args.k_stride;
+    const float clip = args.clip;
+    uint8_t* const cache = args.cache;
+    const int H_kv = args.H_kv;
     auto worker_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(worker + 1) : "memory"); };
     auto fetch = [&](int x, int buf) {  // tile x: 512 pieces of 16 bytes, and its slots
 #pragma unroll
@@ -322,15 +328,15 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
             const int p = tid + 128 * e, row = p >> 4, col = 8 * (p & 15);
             const int64_t tok = min((int64_t)x * PF_M + row, (int64_t)n_tok - 1);  // (rows past the end repeat the last)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&wk.A[buf][row][col])),
-                         "l"(src + ((size_t)tok * H_kv + h) * D + col)
+                         "l"(src + tok * src_stride + col)
                          : "memory");
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (tid < PF_M) {
             const int64_t tok = (int64_t)x * PF_M + tid;
-            int s = tok < n_tok ? __ldg(slot_mapping + tok) : -1;
-            if (s != -1 && (s < 0 || (int64_t)s >= n_slots)) {
-                if (h == 0 && side == 0 && err_count) atomicAdd(err_count, 1);
+            int s = tok < n_tok ? append_slot(args, tok) : -1;
+            if (s < -1) {
+                if (h == 0 && side == 0 && args.err_count) atomicAdd(args.err_count, 1);
                 s = -1;
             }
             wk.slot[buf][tid] = s;
@@ -351,7 +357,7 @@ append_int4_prefill_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloa
         }
     }
     if (threadIdx.x < D) {
-        const float m = side ? 0.f : __ldg(mu + (size_t)h * D + threadIdx.x);
+        const float m = side ? 0.f : __ldg(args.mu_k + (size_t)h * D + threadIdx.x);
         sm.mu[threadIdx.x] = m;
         float m2 = m * m;
 #pragma unroll
@@ -777,31 +783,28 @@ static kvq_status prefill_smem_once() {
     return st;
 }
 
-extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, int H_kv, int d,
-                                      const int32_t* slot_mapping, const float* mu_k, const float* R_k,
-                                      const float* R_v, float clip, void* cache, int64_t num_pages,
-                                      int32_t* err_count, void* stream) {
-    if (d != D) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "kvq_append_int4: d=%d (only 128)", d);
-    if (n_tok < 0 || H_kv <= 0 || num_pages <= 0)
-        return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_append_int4: n_tok=%d H_kv=%d num_pages=%lld", n_tok, H_kv,
-                             (long long)num_pages);
-    if (H_kv > 65535) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "kvq_append_int4: H_kv=%d too large", H_kv);
-    if (!(clip > 0.f && clip <= 1.f))
-        return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_append_int4: clip ratio %g outside (0, 1]", (double)clip);
-    if (n_tok == 0) return KVQ_OK;
-    if (!k || !v || !slot_mapping || !mu_k || !R_k || !R_v || !cache)
-        return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_append_int4: null pointer");
-    for (const void* p : {k, v, (const void*)R_k, (const void*)R_v, (const void*)cache})
+kvq_status kvq_append_int4_args(const char* fn, const AppendInt4& a, int d) {
+    if (d != D) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: d=%d (only 128)", fn, d);
+    if (a.n_tok < 0 || a.H_kv <= 0 || a.num_pages <= 0)
+        return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: n_tok=%d H_kv=%d num_pages=%lld", fn, a.n_tok, a.H_kv,
+                             (long long)a.num_pages);
+    if (a.H_kv > 65535) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: H_kv=%d too large", fn, a.H_kv);
+    if (!(a.clip > 0.f && a.clip <= 1.f))
+        return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: clip ratio %g outside (0, 1]", fn, (double)a.clip);
+    if (a.n_tok == 0) return KVQ_OK;
+    if (!a.k || !a.v || !a.slot_mapping || !a.mu_k || !a.R_k || !a.R_v || !a.cache)
+        return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: null pointer", fn);
+    for (const void* p : {(const void*)a.k, (const void*)a.v, (const void*)a.R_k, (const void*)a.R_v, (const void*)a.cache})
         if (reinterpret_cast<uintptr_t>(p) % 16)
-            return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_append_int4: k, v, R_k, R_v and cache need to be 16-byte aligned");
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const auto kb = static_cast<const __nv_bfloat16*>(k), vb = static_cast<const __nv_bfloat16*>(v);
-    uint8_t* const cb = static_cast<uint8_t*>(cache);
+            return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: k, v, R_k, R_v and cache need to be 16-byte aligned", fn);
+    return KVQ_OK;
+}
+
+kvq_status kvq_append_int4_launch(const char* fn, const AppendInt4& a, cudaStream_t st) {
+    const int n_tok = a.n_tok, H_kv = a.H_kv;
     const int nsm = kvq_device_sm_count(), waves = (2 * H_kv + nsm - 1) / nsm;
     if ((int64_t)n_tok * H_kv < (int64_t)PREFILL_MIN * waves)
-        return kvq_check_cuda(launch_pdl(append_int4_kernel, dim3(n_tok, H_kv, 2), dim3(512), 0, st, kb, vb, n_tok, H_kv,
-                                         slot_mapping, mu_k, R_k, R_v, cb, num_pages, err_count, clip),
-                              "kvq_append_int4 launch");
+        return kvq_check_cuda(launch_pdl(append_int4_kernel, dim3(n_tok, H_kv, 2), dim3(512), 0, st, a), fn);
     const kvq_status sa = prefill_smem_once();
     if (sa != KVQ_OK) return sa;
     // One CTA per SM in all, each with a stride of its (head, side)'s tiles; a head's are
@@ -824,10 +827,32 @@ extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, i
     }
     const int nv = std::min(tiles, std::max(1, most - nk));
     nk = std::min(tiles, nk);
-    return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(nk + nv, H_kv), dim3(PF_WORKERS * 128),
-                                     sizeof(PrefillSmem), st, kb, vb, n_tok, H_kv, slot_mapping, mu_k, R_k, R_v, cb, num_pages,
-                                     err_count, clip, nk),
-                          "kvq_append_int4 launch");
+    return kvq_check_cuda(launch_pdl(append_int4_prefill_kernel, dim3(nk + nv, H_kv), dim3(PF_WORKERS * 128), sizeof(PrefillSmem),
+                                     st, a, nk),
+                          fn);
+}
+
+extern "C" kvq_status kvq_append_int4(const void* k, const void* v, int n_tok, int H_kv, int d,
+                                      const int32_t* slot_mapping, const float* mu_k, const float* R_k,
+                                      const float* R_v, float clip, void* cache, int64_t num_pages,
+                                      int32_t* err_count, void* stream) {
+    AppendInt4 a = {};
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.k_stride = a.v_stride = (int64_t)H_kv * D;
+    a.n_tok = n_tok;
+    a.H_kv = H_kv;
+    a.slot_mapping = slot_mapping;
+    a.mu_k = mu_k;
+    a.R_k = R_k;
+    a.R_v = R_v;
+    a.clip = clip;
+    a.cache = static_cast<uint8_t*>(cache);
+    a.num_pages = num_pages;
+    a.err_count = err_count;
+    const kvq_status st = kvq_append_int4_args("kvq_append_int4", a, d);
+    if (st != KVQ_OK || n_tok == 0) return st;
+    return kvq_append_int4_launch("kvq_append_int4 launch", a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int H_kv, int d,

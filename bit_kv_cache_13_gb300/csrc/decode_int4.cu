@@ -58,6 +58,7 @@
 // an equal share, so a ragged batch or a short context in a long table stays
 // balanced.  With eight heads to a KV head the instructions bound it: 32 ragged
 // sequences of up to 4K, 64 q / 8 KV heads, 53 us for 84 MB (12.5 at the copy rate).
+#include <algorithm>
 #include <cstddef>
 #include <mutex>
 
@@ -171,6 +172,8 @@ struct D4Args {
     int64_t wstride;
     float decay;
     int n_finish, chunks;
+    // sliding form (window 0: all tokens): the last `window` tokens and the first `sinks`
+    int window, sinks;
 };
 
 // ------------------------------------------------------------------ 1: rotate
@@ -307,13 +310,27 @@ __device__ __forceinline__ void d4_rotate_rows(float4 x, const float4 (&rr)[RW],
 
 // ------------------------------------------------------------------ 2: stream
 
+// In the sliding form a sequence's pages are those with a sink, then those of the window:
+// page x of the list is page x of the sequence below `sinks`, and page x + skip from there on.
+struct D4List {
+    int n, sinks, skip, first;  // pages; first: the first token in the window
+};
+__device__ __forceinline__ D4List d4_list(const D4Args& a, int c) {  // c > 0
+    const int ctx = (int)min((int64_t)c, (int64_t)a.max_pages * PAGE), first = max(0, ctx - a.window), fp = first / PAGE;
+    const int sp = min(fp, (int)((min((int64_t)a.sinks, (int64_t)ctx) + PAGE - 1) / PAGE));
+    return {(ctx - 1) / PAGE + 1 - fp + sp, sp, fp - sp, first};
+}
+
+template <bool SLIDE = false>
 __device__ __forceinline__ int d4_pages(const D4Args& a, int b) {
     const int c = __ldg(a.context_lens + b);
+    if constexpr (SLIDE) return c <= 0 ? 0 : d4_list(a, c).n;
     return c <= 0 ? 0 : min((int)(((int64_t)c + PAGE - 1) / PAGE), a.max_pages);
 }
 
 // A CTA's walk over its share: pages [pa, pb) of unit (b, h), which has np (and
 // `extra` without work after them), and `left` pages of the share after them.
+template <bool SLIDE>
 struct D4Walk {
     int b, h, np, pa, pb, end, left;  // end: where the share leaves the unit, work-free pages counted
     // Takes [pa, ..) of the unit out of `share` pages; false if only work-free ones are left of it.
@@ -326,7 +343,7 @@ struct D4Walk {
     __device__ __forceinline__ void next(const D4Args& a, int extra) {  // needs left > 0
         if (++h == a.H_kv) {
             h = 0;
-            do np = d4_pages(a, ++b);
+            do np = d4_pages<SLIDE>(a, ++b);
             while (np == 0);
         }
         pa = 0;
@@ -347,7 +364,7 @@ struct __align__(128) D4Smem {
     uint8_t ring[NW][U * UNITS][INT4_TILE];  // pages in flight; a unit's last slots keep the warp's o' [4 NT][D]
     D4Query<NT> query[2];                       // of segments s, s + 1
     uint64_t bar[NW][UNITS], qbar[2], free_bar[2];
-    int ntok[NW][U * UNITS];                 // valid tokens of the page in each slot
+    int ntok[NW][U * UNITS];                 // valid tokens of the page in each slot (SLIDE: one bit each)
     float m_part[2][NW][4 * NT], l_part[2][NW][4 * NT];
     int part_at[2][NW];                      // ring group that holds the warp's o', -1: no pages
     int arrived[2];
@@ -373,9 +390,12 @@ static_assert(4 * D * 4 <= D4Cfg<1>::U * INT4_TILE && 8 * D * 4 <= D4Cfg<2>::U *
 // for one or a few sequences, whole in this kernel: every CTA works on one unit, rotates
 // its queries itself (before its first copies are out, so the rotation does not wait
 // behind them) and the last CTA of a unit finishes it.
-template <int NT, bool WTS, bool ONE>
+// SLIDE: the sliding form, whose pages' valid tokens are a mask of 16 bits instead of their number.
+template <int NT, bool WTS, bool ONE, bool SLIDE>
 __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(const __grid_constant__ D4Args a) {
     constexpr int NW = D4Cfg<NT>::NW, U = D4Cfg<NT>::U, UNITS = D4Cfg<NT>::UNITS;
+    constexpr int ALL = SLIDE ? 0xffff : PAGE, TOKENS = SLIDE ? 0xffff : 255, HEAD = SLIDE ? 16 : 8;  // of a page's word
+    static_assert(!(WTS && SLIDE), "the weights form has no window");
     extern __shared__ __align__(128) uint8_t smem_raw[];
     D4Smem<NT>& sm = *reinterpret_cast<D4Smem<NT>*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -398,7 +418,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     // let this one start only after its own wait, when everything before it was done.
     int64_t V = 0, g0 = 0;
     int Ceff = 0, share = 0, part = 0, extra = 0;  // extra: pages without work after each unit's, for the cost of starting it
-    D4Walk cs;  // what this warp consumes
+    D4Walk<SLIDE> cs;  // what this warp consumes
     if constexpr (ONE) {
         griddep_wait();  // (no rotate kernel ran before)
         // a whole number of CTAs per unit, as many of them as its pages deserve
@@ -407,7 +427,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         cs.b = unit / a.H_kv;
         cs.h = unit % a.H_kv;
         cs.left = 0;
-        cs.np = d4_pages(a, cs.b);
+        cs.np = d4_pages<SLIDE>(a, cs.b);
         if (cs.np == 0) {
             for (int i = tid; i < G * D && part == 0; i += NW * 32) a.out[(size_t)unit * G * D + i] = __float2bfloat16_rn(0.f);
             return;
@@ -421,7 +441,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         int64_t own = 0;
         int mx = 0, own_ne = 0;
         for (int b = s0; b < s1; ++b) {
-            const int p = d4_pages(a, b);
+            const int p = d4_pages<SLIDE>(a, b);
             own += p;
             mx = max(mx, p);
             own_ne += p > 0;
@@ -492,7 +512,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         if (g0 >= first && g0 < first + own * a.H_kv) {
             int b = s0;
             for (; b < s1; ++b) {
-                const int np = d4_pages(a, b);
+                const int np = d4_pages<SLIDE>(a, b);
                 const int64_t n = (int64_t)(np ? np + extra : 0) * a.H_kv;
                 if (g0 < first + n) break;
                 first += n;
@@ -504,7 +524,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     }
     if constexpr (!ONE) {
         cs.b = sm.b0;
-        cs.np = d4_pages(a, cs.b);
+        cs.np = d4_pages<SLIDE>(a, cs.b);
         const int64_t in = g0 - sm.base0;
         cs.h = (int)(in / (cs.np + extra));
         cs.pa = (int)(in - (int64_t)cs.h * (cs.np + extra));
@@ -536,8 +556,8 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     // ---- what it issues, up to UNITS units ahead, across segments.  Lane U x + e
     // of a batch holds page e of the batch's unit x: its id, KV head and valid tokens
     // (0: past the warp's pages).  The next batch's ids load while this one is issued.
-    D4Walk is = cs;
-    int ik = 0, in = is.units<NW, U>(warp), issued = 0, built = 0;
+    D4Walk<SLIDE> is = cs;
+    int ik = 0, in = is.template units<NW, U>(warp), issued = 0, built = 0;
     constexpr int BATCH = 32 / U;
     auto build = [&](int& pid, int& hn) {  // the units after the first `built`
         pid = hn = 0;
@@ -547,14 +567,23 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 if (is.left == 0) break;
                 is.next(a, extra);
                 ik = 0;
-                in = is.units<NW, U>(warp);
+                in = is.template units<NW, U>(warp);
                 continue;
             }
             const int take = min(BATCH - x, in - ik), y = lane / U - x;
-            const int page = is.pa + warp + NW * (U * (ik + y) + lane % U);
+            int page = is.pa + warp + NW * (U * (ik + y) + lane % U);
             if (y >= 0 && y < take && lane < U * BATCH && page < is.pb) {
+                if constexpr (SLIDE) {
+                    const int ctx = __ldg(a.context_lens + is.b);
+                    const D4List list = d4_list(a, ctx);
+                    if (page >= list.sinks) page += list.skip;
+                    const int t0 = page * PAGE, low = max(0, list.first - t0);  // (below 16 on a page of the window)
+                    const uint32_t valid = 0xffffu >> (PAGE - min(PAGE, ctx - t0)), sink = (1u << min(PAGE, max(0, a.sinks - t0))) - 1u;
+                    hn = (int)((uint32_t)is.h << HEAD | (valid & ((low < PAGE ? 0xffffu << low : 0u) | sink)));
+                } else {
+                    hn = is.h << HEAD | (page + 1 < is.np ? PAGE : min(PAGE, __ldg(a.context_lens + is.b) - page * PAGE));
+                }
                 pid = __ldg(a.block_table + (size_t)is.b * a.max_pages + page);
-                hn = is.h << 8 | (page + 1 < is.np ? PAGE : min(PAGE, __ldg(a.context_lens + is.b) - page * PAGE));
             }
             ik += take;
             x += take;
@@ -564,13 +593,13 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     int pid_n, hn_n;          // of the next batch: as loaded
     uint32_t tile_c, n_c;     // of this one: (page, KV head) tile, valid tokens (0: no page, or a bad id)
     uint32_t ok_mask = 0;     // lanes of this batch that hold a page
-    bool any_bad = false;     // a bad id was seen: token counts are read back for every unit from then on
+    bool any_bad = SLIDE;     // a bad id was seen, or pages are short anywhere: token counts are read back for every unit from then on
     auto turn = [&]() {       // the next batch becomes this one
-        const bool page = hn_n & 255, ok = page && pid_n >= 0 && (int64_t)pid_n < a.num_pages;
+        const bool page = hn_n & TOKENS, ok = page && pid_n >= 0 && (int64_t)pid_n < a.num_pages;
         if (page && !ok) atomicOr(reinterpret_cast<uint32_t*>(a.ws), ERR_BAD_PAGE);
         any_bad |= __any_sync(0xffffffffu, page && !ok);
-        tile_c = ok ? (uint32_t)pid_n * (uint32_t)a.H_kv + (uint32_t)(hn_n >> 8) : 0u;
-        n_c = ok ? hn_n & 255 : 0;
+        tile_c = ok ? (uint32_t)pid_n * (uint32_t)a.H_kv + ((uint32_t)hn_n >> HEAD) : 0u;
+        n_c = ok ? hn_n & TOKENS : 0;
         ok_mask = __ballot_sync(0xffffffffu, ok);
         build(pid_n, hn_n);
     };
@@ -604,7 +633,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
         griddep_wait();  // the rotated queries are there
         griddep_launch_dependents();
     }
-    auto fetch_query = [&](const D4Walk& w, int buf) {  // one thread
+    auto fetch_query = [&](const D4Walk<SLIDE>& w, int buf) {  // one thread
         mbar_arrive_expect_tx(&sm.qbar[buf], sizeof(D4Query<NT>));
         bulk_g2s(&sm.query[buf], static_cast<const D4Query<NT>*>(a.query) + ((size_t)w.b * a.H_kv + w.h), sizeof(D4Query<NT>),
                  &sm.qbar[buf]);
@@ -612,7 +641,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
     if (!ONE && tid == 0) {
         fetch_query(cs, 0);
         if (cs.left > 0) {
-            D4Walk w = cs;
+            D4Walk<SLIDE> w = cs;
             w.next(a, extra);
             fetch_query(w, 1);
         }
@@ -720,7 +749,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
                 refill();
             }
         }
-        const int n_units = dead ? 0 : cs.units<NW, U>(warp);
+        const int n_units = dead ? 0 : cs.template units<NW, U>(warp);
         float oacc[8][4], cmin[4] = {0.f, 0.f, 0.f, 0.f}, mrun[NT], lsum[NT], vref[NT];  // whole numbers; vref: log2 of p * size where P is 1
 #pragma unroll
         for (int m = 0; m < 8; ++m)
@@ -906,19 +935,20 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             auto wait_unit = [&](bool last) {
                 Counts c;
 #pragma unroll
-                for (int e = 0; e < U; ++e) c.n[e] = PAGE;
+                for (int e = 0; e < U; ++e) c.n[e] = ALL;
                 wait(&sm.bar[warp][st], parity);
                 if (last || any_bad) {
-                    int least = PAGE;
+                    int least = ALL;
 #pragma unroll
                     for (int e = 0; e < U; ++e) {
                         c.n[e] = sm.ntok[warp][U * st + e];
                         least = min(least, c.n[e]);
                     }
-                    if (least < PAGE && !dead) {  // warp-uniform
+                    if (least < ALL && !dead) {  // warp-uniform
                         for (int x = lane; x < U * 64; x += 32) {
                             const int e = x >> 6, w = x & 63, pair = (w & 31) >> 2, n = sm.ntok[warp][U * st + e];
-                            const uint32_t keep = (2 * pair < n ? 0x0000ffffu : 0u) | (2 * pair + 1 < n ? 0xffff0000u : 0u);
+                            const bool even = SLIDE ? n >> (2 * pair) & 1 : 2 * pair < n, odd = SLIDE ? n >> (2 * pair + 1) & 1 : 2 * pair + 1 < n;
+                            const uint32_t keep = (even ? 0x0000ffffu : 0u) | (odd ? 0xffff0000u : 0u);
                             uint32_t* word = reinterpret_cast<uint32_t*>(sm.ring[warp][U * st + e] + O4_VS) + w;
                             if (keep != 0xffffffffu) *word &= keep;
                         }
@@ -931,11 +961,11 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             // Logits of page e of unit k (n valid tokens); the weights form stores them.
             auto logits = [&](int k, int slot, int e, int n, float (&lg)[2][NT]) {
                 qk_page(slot, lg);
-                if (n < PAGE) {  // warp-uniform
+                if (n < ALL) {  // warp-uniform
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
-                        if (r >= n) lg[0][x] = -CUDART_INF_F;
-                        if (r + 8 >= n) lg[1][x] = -CUDART_INF_F;
+                        if (SLIDE ? !(n >> r & 1) : r >= n) lg[0][x] = -CUDART_INF_F;
+                        if (SLIDE ? !(n >> (r + 8) & 1) : r + 8 >= n) lg[1][x] = -CUDART_INF_F;
                     }
                 }
                 if constexpr (WTS) {
@@ -1316,7 +1346,7 @@ __global__ void __launch_bounds__(D4Cfg<NT>::NW * 32, 1) decode_int4_kernel(cons
             if (lane == 0) {
                 // everyone is done with this segment's queries: fetch those of segment s + 2
                 if (cs.left > 0) {
-                    D4Walk w = cs;
+                    D4Walk<SLIDE> w = cs;
                     w.next(a, extra);
                     if (w.left > 0) {
                         w.next(a, extra);
@@ -1548,7 +1578,7 @@ extern "C" size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pag
 // first call on each device only.
 static kvq_status d4_smem_once(const void* fn, int bytes, int which) {
     static std::mutex mu;
-    static bool done[64][8] = {};
+    static bool done[64][12] = {};
     int dev = 0;
     kvq_status st = kvq_check_cuda(cudaGetDevice(&dev), "kvq_decode_attn_int4: cudaGetDevice");
     if (st != KVQ_OK) return st;
@@ -1563,8 +1593,8 @@ static kvq_status d4_smem_once(const void* fn, int bytes, int which) {
 static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int H_kv, int d, const void* cache,
                               int64_t num_pages, const int32_t* block_table, int max_pages,
                               const int32_t* context_lens, const float* R_k, const float* R_v, float scale, void* out,
-                              bool with_weights, float* weights, int64_t weights_stride, float decay, void* workspace,
-                              size_t workspace_bytes, int num_splits, void* stream) {
+                              bool with_weights, float* weights, int64_t weights_stride, float decay, int window, int sinks,
+                              void* workspace, size_t workspace_bytes, int num_splits, void* stream) {
     if (d != D) return kvq_set_error(KVQ_ERR_UNSUPPORTED, "%s: d=%d (only 128)", fn, d);
     kvq_status st;
     if (const char* why = d4_refusal(B, H_q, H_kv, max_pages, num_splits, st))
@@ -1615,6 +1645,8 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     a.weights = weights;
     a.wstride = weights_stride;
     a.decay = decay;
+    a.window = window;
+    a.sinks = sinks;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int nsm = kvq_device_sm_count();
     const int64_t units = (int64_t)B * H_kv;
@@ -1628,7 +1660,10 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     // sequence (2048 tokens: 14.3 against 13.6 us in a graph, but one launch fewer to pay for
     // on the host).
     const int per_unit = (int)(nsm / units);
-    const bool small = max_pages <= (int64_t)D4_ONE_PAGES * per_unit;
+    // (in the sliding form: pages of a window wherever it begins, and the sinks')
+    const int64_t most_pages = window ? std::min((int64_t)max_pages, ((int64_t)window + PAGE - 2) / PAGE + 1 + ((int64_t)sinks + PAGE - 1) / PAGE)
+                                      : max_pages;
+    const bool small = most_pages <= (int64_t)D4_ONE_PAGES * per_unit;
     const bool one = num_splits == 0 && per_unit >= 1 && units <= D4_TICKETS &&
                      ((small && (!with_weights || per_unit <= 2)) || (B == 1 && per_unit >= 4));
     if (!one) {
@@ -1640,12 +1675,14 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
         if (st != KVQ_OK) return st;
     }
     // 2
-    using Kern = decltype(&decode_int4_kernel<1, false, false>);
-    static const Kern kerns[8] = {decode_int4_kernel<1, false, false>, decode_int4_kernel<1, true, false>,
-                                  decode_int4_kernel<2, false, false>, decode_int4_kernel<2, true, false>,
-                                  decode_int4_kernel<1, false, true>,  decode_int4_kernel<1, true, true>,
-                                  decode_int4_kernel<2, false, true>,  decode_int4_kernel<2, true, true>};
-    const int which = (G <= 4 ? 0 : 2) + (with_weights ? 1 : 0) + (one ? 4 : 0);
+    using Kern = decltype(&decode_int4_kernel<1, false, false, false>);
+    static const Kern kerns[12] = {decode_int4_kernel<1, false, false, false>, decode_int4_kernel<1, true, false, false>,
+                                   decode_int4_kernel<2, false, false, false>, decode_int4_kernel<2, true, false, false>,
+                                   decode_int4_kernel<1, false, true, false>,  decode_int4_kernel<1, true, true, false>,
+                                   decode_int4_kernel<2, false, true, false>,  decode_int4_kernel<2, true, true, false>,
+                                   decode_int4_kernel<1, false, false, true>,  decode_int4_kernel<2, false, false, true>,
+                                   decode_int4_kernel<1, false, true, true>,   decode_int4_kernel<2, false, true, true>};
+    const int which = window ? 8 + (G <= 4 ? 0 : 1) + (one ? 2 : 0) : (G <= 4 ? 0 : 2) + (with_weights ? 1 : 0) + (one ? 4 : 0);
     const size_t smem = G <= 4 ? sizeof(D4Smem<1>) : sizeof(D4Smem<2>);
     st = d4_smem_once((const void*)kerns[which], (int)smem, which);
     if (st != KVQ_OK) return st;
@@ -1675,8 +1712,22 @@ extern "C" kvq_status kvq_decode_attn_int4(const void* q, int B, int H_q, int H_
                                            float scale, void* out, void* workspace, size_t workspace_bytes,
                                            int num_splits, void* stream) {
     return decode_int4("kvq_decode_attn_int4", q, B, H_q, H_kv, d, cache, num_pages, block_table, max_pages_per_seq,
-                       context_lens, R_k, R_v, scale, out, false, nullptr, 0, 0.f, workspace, workspace_bytes,
+                       context_lens, R_k, R_v, scale, out, false, nullptr, 0, 0.f, 0, 0, workspace, workspace_bytes,
                        num_splits, stream);
+}
+
+extern "C" kvq_status kvq_decode_attn_int4_sliding(const void* q, int B, int H_q, int H_kv, int d, const void* cache,
+                                                   int64_t num_pages, const int32_t* block_table,
+                                                   int max_pages_per_seq, const int32_t* context_lens,
+                                                   const float* R_k, const float* R_v, float scale, int window,
+                                                   int sinks, void* out, void* workspace, size_t workspace_bytes,
+                                                   int num_splits, void* stream) {
+    if (window <= 0 || sinks < 0)
+        return kvq_set_error(KVQ_ERR_INVALID_ARG, "kvq_decode_attn_int4_sliding: window=%d (at least 1) sinks=%d (at least 0)",
+                             window, sinks);
+    return decode_int4("kvq_decode_attn_int4_sliding", q, B, H_q, H_kv, d, cache, num_pages, block_table,
+                       max_pages_per_seq, context_lens, R_k, R_v, scale, out, false, nullptr, 0, 0.f, window, sinks,
+                       workspace, workspace_bytes, num_splits, stream);
 }
 
 extern "C" kvq_status kvq_decode_attn_int4_weights(const void* q, int B, int H_q, int H_kv, int d, const void* cache,
@@ -1687,6 +1738,6 @@ extern "C" kvq_status kvq_decode_attn_int4_weights(const void* q, int B, int H_q
                                                    void* workspace, size_t workspace_bytes, int num_splits,
                                                    void* stream) {
     return decode_int4("kvq_decode_attn_int4_weights", q, B, H_q, H_kv, d, cache, num_pages, block_table,
-                       max_pages_per_seq, context_lens, R_k, R_v, scale, out, true, weights, weights_stride, decay,
+                       max_pages_per_seq, context_lens, R_k, R_v, scale, out, true, weights, weights_stride, decay, 0, 0,
                        workspace, workspace_bytes, num_splits, stream);
 }

@@ -107,4 +107,23 @@ __device__ __forceinline__ int int4_code(Dd z, float s, float m, int n) {
 // would lose bits below the smallest fp32 or leave its range.
 __device__ __forceinline__ bool int4_wild(float n2) { return !(n2 == 0.f || (n2 > 0x1p-80f && n2 < 0x1p100f)); }
 
+// An append to the INT4 cache: k, v rows of H_kv heads, `stride` elements from token to token.  With
+// positions, a token whose position lies outside [0, max_pos) is skipped and counted as one with a bad slot is.
+struct AppendInt4 {
+    const __nv_bfloat16 *k, *v;
+    int64_t k_stride, v_stride;
+    int n_tok, H_kv;
+    const int32_t *slot_mapping, *positions;
+    int max_pos;
+    const float *mu_k, *R_k, *R_v;
+    float clip;
+    uint8_t* cache;
+    int64_t num_pages;
+    int32_t* err_count;
+};
+
 }  // namespace kvq
+
+// The append's refusals and its kernels (host).
+kvq_status kvq_append_int4_args(const char* fn, const kvq::AppendInt4& a, int d);
+kvq_status kvq_append_int4_launch(const char* what, const kvq::AppendInt4& a, cudaStream_t stream);

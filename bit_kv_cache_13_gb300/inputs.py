@@ -229,6 +229,15 @@ def query_params(spec: Spec, layer: int, head_kv: int):
 # RoPE (input preparation: the kernels consume post-RoPE keys)
 # --------------------------------------------------------------------------
 
+def rope_table(max_pos: int, rot_dim: int, theta: float, factor: float = 1.0) -> torch.Tensor:
+    """[max_pos, rot_dim] fp32: cosines, then sines of the angles
+    pos / factor * theta^(-2 i / rot_dim), i < rot_dim / 2, formed in fp64
+    (factor > 1: positions interpolated for longer contexts)."""
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    ang = torch.arange(max_pos, dtype=torch.float64)[:, None] / factor * theta ** (-2.0 * i / rot_dim)
+    return torch.cat([torch.cos(ang), torch.sin(ang)], -1).float().contiguous()
+
+
 def rope_apply(x: torch.Tensor, positions: torch.Tensor, theta: float) -> torch.Tensor:
     """Rotate-half RoPE: block i pairs dims (i, i + d/2) and turns by
     pos * theta^(-2i/d).  x: [..., n, d] float, positions: [n]."""

@@ -2,8 +2,9 @@
  * kvq.h - C ABI of the rotated low-bit KV-cache library (libkvq.so).
  *
  * Three cache formats, each with a quantise-on-append call and a fused
- * packed-cache decode-attention call, eviction for the INT4 one, and two
- * host-only helpers:
+ * packed-cache decode-attention call; for the INT4 one eviction, an append
+ * that norms and rotates the heads on the way, attention of more than one new
+ * token and a sliding window; and two host-only helpers:
  *
  *   INT2     "Output-Aware Rotation for INT2 KV-Cache Quantization":
  *            keys centred per head (§1, attention-equivalent
@@ -393,6 +394,84 @@ kvq_status kvq_decode_attn_int4_weights(const void* q, int B, int H_q, int H_kv,
                                         void* out, float* weights, int64_t weights_stride, float decay,
                                         void* workspace, size_t workspace_bytes,
                                         int num_splits, void* stream);
+
+/* kvq_decode_attn_int4 over a sliding window with sinks: query b, at position
+ * n - 1 of its n = context_lens[b] tokens, sees token s when s >= n - window or
+ * s < sinks (s < n).  Only the pages that hold such a token are read, and only
+ * their block-table entries.
+ *   window >= 1, sinks >= 0
+ * Other arguments, workspace and limits as kvq_decode_attn_int4. */
+kvq_status kvq_decode_attn_int4_sliding(const void* q, int B, int H_q, int H_kv, int d,
+                                        const void* cache, int64_t num_pages,
+                                        const int32_t* block_table, int max_pages_per_seq,
+                                        const int32_t* context_lens,
+                                        const float* R_k, const float* R_v, float scale,
+                                        int window, int sinks, void* out,
+                                        void* workspace, size_t workspace_bytes,
+                                        int num_splits, void* stream);
+
+/* From a projection's output to the INT4 cache in one call: the heads' norms of
+ * queries and keys, the rotation by the tokens' positions, and
+ * kvq_append_int4 of the resulting keys and of v.
+ *   q, k, v     device bf16, token t's heads [H_q][d] (k, v: [H_kv][d]) at
+ *               x + t * x_stride; strides in elements, a multiple of 8, at least a
+ *               token's heads (so the three may be views of one projection's output)
+ *   positions   device int32 [n_tok]
+ *   rope        device fp32 [max_pos][rot_dim]: of each position rot_dim/2 cosines,
+ *               then rot_dim/2 sines, whatever scaling of the angles they hold
+ *   rot_dim     the first rot_dim channels of a head rotate (a multiple of 16, 16..128)
+ *   interleaved 0: channel j pairs with j + rot_dim/2; else 2j with 2j + 1
+ *   q_weight, k_weight  nullable device bf16 [d]: with it the heads of q (of k)
+ *               are normed, y = x * weight / sqrt(mean(x^2) + eps); eps >= 0
+ *   q_out, k_out  device bf16 [n_tok][H_q][d], [n_tok][H_kv][d], written: with
+ *               (a, b) a pair of y, a cos - b sin and b cos + a sin.  The real
+ *               numbers, rounded once (they are formed as far as that takes).  Each
+ *               may be its input, where that is dense; else no overlap.
+ *   other arguments as kvq_append_int4, whose cache bytes for (k_out, v) these are
+ * A token whose position lies outside [0, max_pos) gets zeros in q_out and k_out;
+ * it is not appended and counts in err_count as one with a bad slot does (once;
+ * not with slot -1: padded tokens may hold any position).  q, k, v, rope, the
+ * weights, q_out, k_out, R_k, R_v and cache need 16-byte alignment. */
+kvq_status kvq_append_rope_int4(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, int n_tok, int H_q, int H_kv, int d,
+                                const int32_t* positions, const float* rope, int max_pos, int rot_dim,
+                                int interleaved, const void* q_weight, const void* k_weight, double eps,
+                                const int32_t* slot_mapping, const float* mu_k,
+                                const float* R_k, const float* R_v, float clip,
+                                void* cache, int64_t num_pages, void* q_out, void* k_out,
+                                int32_t* err_count, void* stream);
+
+/* Bytes of workspace for kvq_chunk_attn_int4.  It must be zero-filled once before
+ * its first use; calls (and captured graphs) that may overlap on the GPU need one
+ * each.  A workspace may serve calls of any shape that it is large enough for, one
+ * after another.  Returns 0 for sizes that the call refuses. */
+size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
+
+/* Attention of each sequence's last tokens over the INT4 cache, causal among
+ * themselves (a piece of a prompt, a whole one, drafted tokens to verify).  Rows
+ * q_start[b] .. q_start[b+1]-1 of q and out belong to sequence b; row q_start[b] + i
+ * of its n_b stands at position p = context_lens[b] - n_b + i, and sees the cached
+ * tokens t <= p (the chunk's own among them: append them first) with
+ * window == 0, or t > p - window, or t < sinks:
+ *   o = softmax(<q R_k, K^> * scale) V^ R_v^T,  K^, V^ the cached values
+ *   q, out   device bf16 [n_tok][H_q][d]; out may be q.  Rows outside
+ *            [q_start[0], q_start[B]) are left as they were; a row that sees
+ *            nothing (p < 0 among them) gets zeros
+ *   q_start  device int32 [B+1], ascending within 0..n_tok; a sequence whose two
+ *            entries are not has no rows, and kvq_workspace_status reports
+ *            KVQ_ERR_INVALID_ARG
+ *   window   0: all tokens; sinks >= 0 (without a window it makes no difference)
+ * context_lens is clamped to [0, 16 * max_pages_per_seq]; block-table entries
+ * outside [0, num_pages) as kvq_decode_attn_int4, where a token that a row sees lies
+ * on them.  A call repeated gives the same bits.  q, cache, R_k, R_v, out and
+ * workspace need 16-byte alignment.  H_q / H_kv <= 64, B and H_kv <= 65535,
+ * n_tok * H_q <= 2^30, max_pages_per_seq < 2^27, num_pages * H_kv <= 2^32. */
+kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_t* q_start, int B, int H_q, int H_kv,
+                               int d, const void* cache, int64_t num_pages,
+                               const int32_t* block_table, int max_pages_per_seq,
+                               const int32_t* context_lens, const float* R_k, const float* R_v, float scale,
+                               int window, int sinks, void* out, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /* Chooses the tokens each (sequence, KV head) keeps.  With n = context_lens[b]
  * (clamped to [0, max_tokens]): all of them when n <= budget; else tokens

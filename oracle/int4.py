@@ -204,3 +204,74 @@ def gather(cache, block_table, keep, new_lens, dst, dst_block_table, weights=Non
                 if wo is not None:
                     wo[b, h, i] = weights[b, h, s]
     return wo
+
+
+# ------------------------------------------------------------------ norms and rotation, more than one new token
+
+def norm_rope(x, positions, table, weight=None, eps: float = 1e-6, interleaved: bool = False):
+    """Heads x [n, H, 128] normed (with a weight [128]) and their first channels rotated by positions through table
+    [max_pos, rot] (rot/2 cosines, then sines); zeros for a position outside the table.  Not rounded."""
+    y = np.array(x, np.float64)
+    if weight is not None:
+        y = y * np.asarray(weight, np.float64) / np.sqrt((y * y).mean(-1, keepdims=True) + eps)
+    table = np.asarray(table, np.float32).astype(np.float64)
+    half = table.shape[1] // 2
+    pos = np.asarray(positions, np.int64)
+    ok = (pos >= 0) & (pos < table.shape[0])
+    cos, sin = np.split(table[np.where(ok, pos, 0)][:, None], 2, -1)
+    j = np.arange(half)
+    first, second = (2 * j, 2 * j + 1) if interleaved else (j, j + half)
+    a, b = y[..., first], y[..., second]
+    y[..., first], y[..., second] = a * cos - b * sin, b * cos + a * sin
+    return np.where(ok[:, None, None], y, 0.0)
+
+
+def to_bf16(y):
+    """fp64 to the nearest bf16 value, ties to even, in one rounding (normal range)."""
+    y = np.asarray(y, np.float64)
+    ulp = np.ldexp(1.0, np.frexp(y)[1] - 8)
+    return np.round(y / ulp) * ulp
+
+
+def chunk(q, q_start, cache, block_table, ctx_lens, rk32, rv32, scale, window: int = 0, sinks: int = 0):
+    """Attention of each sequence's last tokens: row q_start[b] + i at position ctx - n_b + i sees cached tokens t <= it
+    (window > 0: t > it - window or t < sinks); pages outside the pool are dropped.  Returns out [n, H_q, d] and the bound
+    [n, H_q] on the 2-norm of what rounding the rotated queries, the cached keys and values and the weights to fp16 once
+    each does to it: products' roundings are independent and taken at six standard deviations, weights and values at 2^-11."""
+    q = np.asarray(q, np.float64)
+    h_q, d = q.shape[1:]
+    h_kv = cache.shape[1]
+    g = h_q // h_kv
+    out, bound = np.zeros(q.shape), np.zeros(q.shape[:2])
+    sc = float(np.float32(scale))
+    for b, ctx in enumerate(np.clip(np.asarray(ctx_lens, np.int64), 0, PAGE * block_table.shape[1])):
+        n = int(q_start[b + 1] - q_start[b])
+        if n <= 0 or ctx == 0:
+            continue
+        pages = np.asarray(block_table[b][: -(-int(ctx) // PAGE)], np.int64)
+        ok = (pages >= 0) & (pages < cache.shape[0])
+        t, p = np.arange(ctx), ctx - n + np.arange(n)[:, None]
+        see = (t <= p) & np.repeat(ok, PAGE)[:ctx]
+        if window:
+            see &= (t > p - window) | (t < sinks)
+        rows = slice(int(q_start[b]), int(q_start[b]) + n)
+        any_row = see.any(1)
+        for h in range(h_kv):
+            tiles = cache[np.where(ok, pages, 0), h]
+            k, v = (values(tiles, side).reshape(-1, d)[:ctx] for side in (0, 1))
+            used = see.any(0)
+            k, v = np.where(used[:, None], k, 0.0), np.where(used[:, None], v, 0.0)
+            size = np.linalg.norm(v, axis=1)
+            rk, rv = (np.asarray(r[h], np.float32).astype(np.float64) for r in (rk32, rv32))
+            for j in range(h * g, (h + 1) * g):
+                qr = q[rows, j] @ rk
+                a = np.where(see, qr @ k.T * sc, -np.inf)
+                top = np.where(any_row, a.max(1, initial=-np.inf), 0.0)[:, None]
+                w = np.where(see, np.exp(a - top), 0.0)
+                w /= np.where(any_row, w.sum(1), 1.0)[:, None]
+                o = w @ v
+                out[rows, j] = o @ rv.T
+                e = 6 * np.sqrt(2 / 3) * 2.0 ** -11 * abs(sc) * np.sqrt((qr * qr) @ (k * k).T) + 2.0 ** -11
+                e = np.where(see, e, 0.0)
+                bound[rows, j] = (w * e) @ size + 2.0 ** -11 * (w @ size) + (w * e).sum(1) * np.linalg.norm(o, axis=1) + 1e-6 * size.max(initial=0.0)
+    return out, bound
