@@ -5,13 +5,42 @@
 //   q' = q R_k;  a_t = <q', K^_t> scale over the tokens that the query's position sees;
 //   o = (sum_t softmax(a)_t V^_t) R_v^T
 //
-// Rows of 32 (token, head) pairs of one KV head per CTA, a page of 16 tokens at a time,
-// all in fp32: four threads a row, four tokens' logits and 32 channels of the output each.
+// Three kernels, chained by programmatic dependent launch:
+//   1 rotate   q' of every row (a token and one of its heads) as fp16, and the plan: the
+//              row blocks with the tiles of tokens that they see
+//   2 stream   a persistent CTA per SM takes an equal share of all blocks' tiles; the
+//              products on tcgen05, the cache unpacked to fp16 in shared memory on the way
+//   3 finish   merges the shares' partial sums, normalises, rotates by R_v^T
+#include <algorithm>
 #include <cstddef>
+#include <mutex>
 
 #include "int4_common.cuh"
 
 namespace kvq {
+
+constexpr int CK_ROWS = 256;       // rows of a block: two row tiles of 128
+constexpr int CK_TILE = 128;       // cached tokens of a tile: eight pages
+constexpr int CK_UNIT_COST = 6;    // what starting a block costs, in tiles of one row tile
+constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
+constexpr float CK_STALE = 8.f;    // a row's reference stays while its logits are at most 2^8 above it
+constexpr float CK_LIFT = 7.f;     // weights are carried 2^7 times as large: they use fp16 from 2^15 down
+constexpr long long CK_SHORT_WAIT_CYCLES = 2000000LL;
+
+// Rows [r0, r0 + rows) of sequence b (row = token * G + head of the group), and the pages
+// that one of them sees: page x of the list is page x of the sequence below `sinks`, and
+// page x + skip from there on.
+struct __align__(16) CkBlock {
+    int64_t start;   // of the blocks before it, per KV head: their cost
+    int cost, tiles;
+    int b, q0, n, ctx;
+    int r0, rows, pages, sinks;
+    int skip, index_in_b, pad0, pad1;
+};
+struct CkPlan {
+    int blocks, ctas;
+    int64_t total;  // cost of all heads
+};
 
 struct ChunkArgs {
     const __nv_bfloat16* q;
@@ -28,12 +57,23 @@ struct ChunkArgs {
     int window, sinks;
     __nv_bfloat16* out;
     uint32_t* error;
+    CkPlan* plan;
+    CkBlock* block;       // [max_blocks]
+    int max_blocks;
+    __half* rot;          // q' [H_kv][n_tok * G][D], channels in the order of the unpacked keys
+    float* row_scale;     // [H_kv][n_tok * G]: logit = product * row_scale
+    float* main;          // [H_kv * n_tok * G][PART_STRIDE] partials of the shares that begin a block
+    float* second;        // of their second stream (blocks of one row tile)
+    int64_t second_rows;  // rows of `second` per sequence and KV head (0: as in main)
+    float* extra;         // [ctas][CK_ROWS][PART_STRIDE] of the shares that begin within one
+    int ctas;
+    int drop;
 };
 
-constexpr int CH_ROWS = 32;
+// ------------------------------------------------------------------ plan
 
 // New tokens of sequence b: first row and count (0 where q_start is not what it should be).
-__device__ __forceinline__ int2 chunk_rows(const ChunkArgs& a, int b) {
+__device__ __forceinline__ int2 ck_tokens(const ChunkArgs& a, int b) {
     const int s = __ldg(a.q_start + b), e = __ldg(a.q_start + b + 1);
     if (s < 0 || e < s || e > a.n_tok) {
         atomicOr(a.error, ERR_BAD_ROWS);
@@ -41,97 +81,895 @@ __device__ __forceinline__ int2 chunk_rows(const ChunkArgs& a, int b) {
     }
     return make_int2(s, e - s);
 }
+__device__ __forceinline__ int ck_blocks(int n, int G) { return (int)(((int64_t)n * G + CK_ROWS - 1) / CK_ROWS); }
 
-__global__ void __launch_bounds__(128) chunk_int4_kernel(const __grid_constant__ ChunkArgs a) {
-    __shared__ __align__(16) float qs[CH_ROWS][D + 4], K[PAGE][D + 4], V[PAGE][D + 4];
-    const int tid = threadIdx.x, row = tid >> 2, part = tid & 3, h = blockIdx.y, G = a.G;
+__device__ __forceinline__ int ck_weight(int rows) { return rows > CK_TILE ? 2 : 1; }
+
+template <typename T>
+__device__ __forceinline__ T ck_scan(T own, T* warp_sums, T& total) {  // exclusive, over the CTA's 256 threads
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    T before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) before += warp_sums[w];
+        total += warp_sums[w];
+    }
+    return before + inc - own;
+}
+
+// One CTA of 256 threads: a thread takes a run of sequences, then a block at a time.
+__device__ void ck_make_plan(const ChunkArgs& a) {
+    __shared__ int64_t sums[8];
+    __shared__ int sums32[8];
+    const int tid = threadIdx.x, per = (a.B + 255) / 256, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int own = 0, n_blocks;
+    for (int b = b0; b < b1; ++b) own += ck_blocks(ck_tokens(a, b).y, a.G);
+    int at = ck_scan(own, sums32, n_blocks);
+    for (int b = b0; b < b1; ++b) {
+        const int2 t = ck_tokens(a, b);
+        const int ctx = (int)min((int64_t)max(0, __ldg(a.context_lens + b)), (int64_t)a.max_pages * PAGE);
+        for (int x = 0, n = ck_blocks(t.y, a.G); x < n && at < a.max_blocks; ++x, ++at) {
+            CkBlock& k = a.block[at];
+            k.b = b;
+            k.q0 = t.x;
+            k.n = t.y;
+            k.ctx = ctx;
+            k.index_in_b = x;
+        }
+    }
+    __syncthreads();
+    n_blocks = min(n_blocks, a.max_blocks);
+    int64_t base = 0;
+    for (int e0 = 0; e0 < n_blocks; e0 += 256) {
+        const int e = e0 + tid;
+        CkBlock k = {};
+        if (e < n_blocks) {
+            k = a.block[e];
+            k.r0 = k.index_in_b * CK_ROWS;
+            k.rows = (int)min((int64_t)CK_ROWS, (int64_t)k.n * a.G - k.r0);
+            const int first = k.ctx - k.n + k.r0 / a.G, last = k.ctx - k.n + (k.r0 + k.rows - 1) / a.G;  // positions
+            k.pages = k.sinks = k.skip = k.tiles = k.cost = 0;
+            if (last >= 0) {
+                const int low = a.window ? max(0, first - min(first, a.window - 1)) : 0;  // (first < 0: from 0 on)
+                const int fp = (first < 0 ? 0 : low) / PAGE;
+                k.sinks = min(fp, (min(a.sinks, last + 1) + PAGE - 1) / PAGE);
+                k.skip = fp - k.sinks;
+                k.pages = last / PAGE + 1 - k.skip;
+                k.tiles = (k.pages + CK_TILE / PAGE - 1) / (CK_TILE / PAGE);
+                k.cost = ck_weight(k.rows) * k.tiles + CK_UNIT_COST;
+            }
+        }
+        int64_t total;
+        k.start = base + ck_scan((int64_t)k.cost, sums, total);
+        if (e < n_blocks) a.block[e] = k;
+        base += total;
+    }
+    if (tid == 0) {
+        a.plan->blocks = n_blocks;
+        a.plan->total = base * a.H_kv;
+        a.plan->ctas = (int)min((int64_t)a.ctas, base * a.H_kv);
+    }
+}
+
+// A share: tiles [from, to) of head h of a block, out of cost [pos, end).
+struct CkWalk {
+    int64_t pos, end;
+    int e, h, from, to;
+    CkBlock k;
+    __device__ __forceinline__ void read(const ChunkArgs& a) {
+        const int4* p = reinterpret_cast<const int4*>(a.block + e);
+        int4* q = reinterpret_cast<int4*>(&k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = __ldcg(p + i);
+    }
+    // The next share with tiles; false at the end.  (e, h) name the unit that holds pos.
+    __device__ __forceinline__ bool next(const ChunkArgs& a) {
+        while (pos < end) {
+            read(a);
+            if (k.cost == 0) {
+                ++e;
+                continue;
+            }
+            const int64_t unit = k.start * a.H_kv + (int64_t)h * k.cost;
+            const int x0 = (int)(pos - unit), x1 = (int)min(end - unit, (int64_t)k.cost), w = ck_weight(k.rows);
+            from = (x0 + w - 1) / w;
+            to = min(k.tiles, (x1 + w - 1) / w);
+            pos = unit + x1;
+            last_h = h;
+            if (x1 == k.cost && ++h == a.H_kv) {
+                h = 0;
+                ++e;
+            }
+            if (from < to) return true;
+        }
+        return false;
+    }
+    int last_h;  // head of the share that next() found
+};
+
+// Where the cost axis is cut for CTA c of C.
+__device__ __forceinline__ int64_t ck_cut(int64_t total, int c, int C) { return (int64_t)c * total / C; }
+
+// ------------------------------------------------------------------ 1: rotate
+
+__device__ __forceinline__ void ck_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t ck_pack(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+// Two values' bf16 parts: what rounds, and what that leaves.
+__device__ __forceinline__ void ck_parts(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = ck_pack(x, y);
+    lo = ck_pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+
+// A matrix as the B operand of m16n8k16, in two bf16 parts: [K step][8 columns][lane] of (b0, b1) of the high part, then
+// of the low one.  at(k, n) is its entry.
+struct __align__(16) CkMatrix {
+    uint4 f[8][16][32];
+};
+template <typename At>
+__device__ __forceinline__ void ck_stage_matrix(CkMatrix& m, At at) {
+    for (int x = threadIdx.x; x < 8 * 16 * 32; x += blockDim.x) {
+        const int lane = x & 31, nt = (x >> 5) & 15, ks = x >> 9, n = 8 * nt + (lane >> 2), k = 16 * ks + 2 * (lane & 3);
+        uint4 f;
+        ck_parts(at(k, n), at(k + 1, n), f.x, f.z);
+        ck_parts(at(k + 8, n), at(k + 9, n), f.y, f.w);
+        m.f[ks][nt][lane] = f;
+    }
+}
+
+// Position of a key channel in the unpacked keys: a word's eight channels come as (0, 4), (1, 5), (2, 6), (3, 7).
+__host__ __device__ constexpr int ck_key_at(int ch) { return (ch & ~7) | (ch & 3) << 1 | (ch >> 2 & 1); }
+// Position of a value channel 32 g + 4 r + i in the unpacked values: 32 g + 8 i + r.
+__host__ __device__ constexpr int ck_value_channel(int at) { return (at & ~31) | (at & 7) << 2 | (at >> 3 & 3); }
+
+// CTAs of 256 threads, 128 rows each (a warp 16); the last CTA of a head's row makes the plan.
+__global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant__ ChunkArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    CkMatrix& R = *reinterpret_cast<CkMatrix*>(smem_raw);
     griddep_wait();
     griddep_launch_dependents();
-    int b = 0, first = 0;
-    int2 rows;
-    int64_t block = blockIdx.x;
-    for (; b < a.B; ++b) {
-        rows = chunk_rows(a, b);
-        const int64_t blocks = ((int64_t)rows.y * G + CH_ROWS - 1) / CH_ROWS;
-        if (block < blocks) break;
-        block -= blocks;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y == 0) ck_make_plan(a);
+        return;
     }
-    if (b == a.B) return;
-    first = (int)(block * CH_ROWS);
-    const int n_rows = (int)min((int64_t)CH_ROWS, (int64_t)rows.y * G - first);
-    const int ctx = (int)min((int64_t)max(0, __ldg(a.context_lens + b)), (int64_t)a.max_pages * PAGE);
-    const bool live = row < n_rows;
-    const int tok = (first + (live ? row : 0)) / G, head = h * G + (first + (live ? row : 0)) % G;
-    const int pos = ctx - rows.y + tok;
-    // q' into qs
-    const __nv_bfloat16* q = a.q + ((size_t)(rows.x + tok) * a.H_q + head) * D;
-    float acc[32];
-    for (int c = 0; c < 32; ++c) acc[c] = 0.f;
-    for (int i = 0; i < D; ++i) {
-        const float x = __bfloat162float(q[i]) * a.scale_log2;
-        for (int c = 0; c < 32; ++c) acc[c] = fmaf(x, __ldg(a.Rk + ((size_t)h * D + i) * D + 32 * part + c), acc[c]);
-    }
-    for (int c = 0; c < 32; ++c) qs[row][32 * part + c] = live ? acc[c] : 0.f;
-    float m = -CUDART_INF_F, l = 0.f;
-    for (int c = 0; c < 32; ++c) acc[c] = 0.f;
-    const int last = ctx - rows.y + (first + n_rows - 1) / G, p0 = ctx - rows.y + first / G;  // positions
-    const int low = a.window ? max(0, p0 - a.window + 1) : 0;
-    for (int page = 0; page * PAGE <= last; ++page) {
-        if (page * PAGE >= a.sinks && (page + 1) * PAGE <= low) continue;
-        const int id = __ldg(a.block_table + (size_t)b * a.max_pages + page);
-        const bool ok = id >= 0 && (int64_t)id < a.num_pages;
-        if (!ok && tid == 0) atomicOr(a.error, ERR_BAD_PAGE);
-        if (!ok) continue;
-        __syncthreads();
-        const uint8_t* tile = a.cache + ((size_t)id * a.H_kv + h) * INT4_TILE;
-        for (int x = tid; x < PAGE * D; x += 128) {
-            const int s = x / D, ch = x % D, g = ch / 32, kt = ch % 32 / 8, ki = ch % 8, vr = ch % 32 / 4, vi = ch % 4;
-            const int kc = tile[O4_KC + 64 * s + 16 * kt + 4 * g + ki / 2] >> (4 * (ki & 1)) & 15;
-            const int vc = tile[O4_VC + 128 * (s / 2) + 16 * vr + 4 * g + 2 * (s & 1) + vi / 2] >> (4 * (vi & 1)) & 15;
-            auto half_at = [&](int at) { return __half2float(*reinterpret_cast<const __half*>(tile + at)); };
-            const bool there = page * PAGE + s < ctx;
-            K[s][ch] = there ? fmaf((float)kc, half_at(O4_KM + 16 * s + 2 * g), half_at(O4_KM + 16 * s + 8 + 2 * g)) : 0.f;
-            V[s][ch] = there ? fmaf((float)vc, half_at(O4_VS + int4_vmeta_off(s, g)), half_at(O4_VM + int4_vmeta_off(s, g))) : 0.f;
-        }
-        __syncthreads();
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = 0; c < D; ++c)
-            for (int e = 0; e < 4; ++e) x[e] = fmaf(qs[row][c], K[4 * part + e][c], x[e]);
-        float top = m;
-        for (int e = 0; e < 4; ++e) {
-            const int t = page * PAGE + 4 * part + e;
-            if (!(t <= pos && (!a.window || t > pos - a.window || t < a.sinks))) x[e] = -CUDART_INF_F;
-            top = fmaxf(top, x[e]);
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float c0 = m == -CUDART_INF_F ? 0.f : exp2f(m - top);
-        l *= c0;
-        for (int c = 0; c < 32; ++c) acc[c] *= c0;
-        m = top;
-        float p[4];
-        for (int e = 0; e < 4; ++e) {
-            p[e] = x[e] == -CUDART_INF_F ? 0.f : exp2f(x[e] - m);
-            l += p[e];
-        }
-        for (int s = 0; s < PAGE; ++s) {
-            const float w = __shfl_sync(0xffffffffu, p[s & 3], (tid & 28) | (s >> 2));
-            if (w == 0.f) continue;
-            for (int c = 0; c < 32; ++c) acc[c] = fmaf(w, V[s][32 * part + c], acc[c]);
-        }
-    }
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    const float* Rk = a.Rk + (size_t)h * D * D;
+    // columns of the product in the order of the unpacked keys: column position n holds channel c with ck_key_at(c) == n
+    ck_stage_matrix(R, [&](int k, int n) { return __ldg(Rk + k * D + ((n & ~7) | (n >> 1 & 3) | (n & 1) << 2)); });
     __syncthreads();
-    for (int c = 0; c < 32; ++c) qs[row][32 * part + c] = acc[c] * inv;
+    const int64_t rows = (int64_t)a.n_tok * a.G;
+    for (int64_t r0 = (int64_t)blockIdx.x * 128 + 16 * warp; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 128) {
+        const __nv_bfloat16* q[2];
+        uint32_t x[8][4];
+        float n2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t row = min(r0 + r + 8 * e, rows - 1);
+            q[e] = a.q + ((row / a.G) * a.H_q + (int64_t)h * a.G + row % a.G) * D;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[ks][e] = __ldg(reinterpret_cast<const uint32_t*>(q[e & 1] + 16 * ks + 8 * (e >> 1) + 2 * t));
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float lo = __uint_as_float(x[ks][e] << 16), hi = __uint_as_float(x[ks][e] & 0xffff0000u);
+                n2[e & 1] = fmaf(lo, lo, fmaf(hi, hi, n2[e & 1]));
+            }
+        // |q'| sigma lies within 2^7 and 2^8, so its entries are far from both ends of fp16; keys are carried at 2^-4
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            n2[e] += __shfl_xor_sync(0xffffffffu, n2[e], 1);
+            n2[e] += __shfl_xor_sync(0xffffffffu, n2[e], 2);
+            const float size = sqrtf(n2[e]) * fabsf(a.scale_log2);
+            const float sigma = size > 0.f && size < CUDART_INF_F ? ldexpf(1.f, max(-100, min(100, 7 - ilogbf(size)))) : 1.f;
+            f[e] = a.scale_log2 * sigma;
+            const int64_t row = r0 + r + 8 * e;
+            if (t == 0 && row < rows) a.row_scale[(int64_t)h * rows + row] = 16.f / sigma;
+        }
+#pragma unroll 2
+        for (int nt = 0; nt < 16; ++nt) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint4 b = R.f[ks][nt][lane];
+                ck_mma(c, x[ks], b.z, b.w);
+                ck_mma(c, x[ks], b.x, b.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t row = r0 + r + 8 * e;
+                if (row < rows)
+                    *reinterpret_cast<uint32_t*>(a.rot + ((int64_t)h * rows + row) * D + 8 * nt + 2 * t) =
+                        pack_half2(c[2 * e] * f[e], c[2 * e + 1] * f[e]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ 2: stream
+//
+// Twenty warps: two warpgroups of softmax (a thread a row of its row tile), one that
+// unpacks keys, one that unpacks values, a warp that issues the products and one that
+// fetches pages.  A block of more than 128 rows has two row tiles, whose warpgroups both take
+// every tile of tokens; a block of up to 128 has one, and the warpgroups take every other tile
+// of tokens of it (two streams, each with sums of its own).  In either case the products of
+// one stream run while the other one's softmax does.
+//
+//   TMEM     S0, S1 (a stream's logits, and over them its weights P as fp16), O0, O1
+//   shared   Q [stream], K and V [2 stages] as K-major operands in the 128-byte swizzle (V
+//            transposed: rows are channels), three raw stages of four pages
+constexpr int CK_OPERAND = 128 * 128 * 2, CK_HALF = CK_OPERAND / 2;  // 64 columns of 128 rows each
+constexpr int CK_RAW_PAGES = 4, CK_RAW = CK_RAW_PAGES * INT4_TILE, CK_RAW_STAGES = 3;
+constexpr int CK_THREADS = 640;
+
+struct __align__(16) CkInfo {  // of a tile of tokens, written with its values
+    int base[2][4];        // first position of each page, -1 without one
+    uint32_t poison[2][4]; // [half][warp]: tokens whose values are not finite, 32 of them per warp
+    uint32_t special[2];   // [half]: bit t: stream t's rows do not all see all of it
+};
+struct __align__(1024) CkSmem {
+    uint8_t q[2][CK_OPERAND], k[2][CK_OPERAND], v[2][CK_OPERAND];
+    uint8_t raw[CK_RAW_STAGES][CK_RAW];
+    __align__(16) CkInfo info[2];
+    __align__(16) int raw_base[CK_RAW_STAGES][4];
+    uint64_t raw_full[CK_RAW_STAGES], raw_free[CK_RAW_STAGES], k_full[2], k_free[2], v_full[2], v_free[2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint32_t tmem;
+    int dead, e0, h0;
+    uint32_t stages;  // raw stages fetched
+};
+static_assert(sizeof(CkSmem) + 1024 <= 227 * 1024, "chunk shared memory above 227 KB");
+
+__device__ __forceinline__ uint64_t ck_desc(const void* p) {  // K-major, 128-byte swizzle: atoms of 8 rows, 1024 bytes apart
+    return (uint64_t)((smem_u32(p) & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp32 accumulators, fp16 operands, both K-major, 128 x 128
+constexpr uint32_t CK_IDESC = 1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24;
+
+__device__ __forceinline__ void ck_mma_ss(uint32_t d, uint64_t a, uint64_t b, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
+        "r"(CK_IDESC), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint64_t b, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
+        "r"(CK_IDESC), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void ck_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void ck_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void ck_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void ck_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// What was loaded is used after the wait only.
+template <int N>
+__device__ __forceinline__ void ck_loaded(uint32_t (&x)[N]) {
+    ck_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i]));
+}
+__device__ __forceinline__ void ck_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define CK_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define CK_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+__device__ __forceinline__ void ck_tmem_ld32(uint32_t* x, uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : CK_R8(x, 0), CK_R8(x, 8), CK_R8(x, 16), CK_R8(x, 24)
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void ck_tmem_st32(const uint32_t* x, uint32_t at) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::CK_W8(x, 0),
+        CK_W8(x, 8), CK_W8(x, 16), CK_W8(x, 24), "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ float ck_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 ck_fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n fma.rn.f32x2 x, x, y, z;\n"
+        " mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 ck_add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Codes of a word as fp16 numbers, two at a time: nibbles (0, 4), (1, 5), (2, 6), (3, 7).  1024 + c by its bits, less 1024.
+__device__ __forceinline__ void ck_codes(uint32_t w, __half2 (&c)[4]) {
+    const __half2 one = u32_as_h2(0xe400e400u), sixteenth = u32_as_h2(0x2c002c00u), back = u32_as_h2(0xd400d400u);  // -1024, 1/16, -64
+    const uint32_t v = w >> 8;
+    c[0] = __hadd2(u32_as_h2((w & 0x000f000fu) | 0x64006400u), one);
+    c[1] = __hfma2(u32_as_h2((w & 0x00f000f0u) | 0x64006400u), sixteenth, back);
+    c[2] = __hadd2(u32_as_h2((v & 0x000f000fu) | 0x64006400u), one);
+    c[3] = __hfma2(u32_as_h2((v & 0x00f000f0u) | 0x64006400u), sixteenth, back);
+}
+
+__global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __grid_constant__ ChunkArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    CkSmem& sm = *reinterpret_cast<CkSmem*>(smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2;
+    if (tid == 0) {
+        for (int i = 0; i < CK_RAW_STAGES; ++i) {
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_free[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.k_full[i], 8);  // four warps, two halves
+            mbar_init(&sm.v_full[i], 8);
+            mbar_init(&sm.k_free[i], 1);
+            mbar_init(&sm.v_free[i], 1);
+            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_full[i], 1);
+        }
+        mbar_init(&sm.drained, 1);
+        sm.dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 16) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    const int C = __ldcg(&a.plan->ctas), cta = blockIdx.x, n_blocks = __ldcg(&a.plan->blocks);
+    const int64_t total = __ldcg(&a.plan->total);
+    const bool idle = cta >= C;
+    CkWalk start;
+    start.pos = idle ? 0 : ck_cut(total, cta, C);
+    start.end = idle ? 0 : ck_cut(total, cta + 1, C);
+    if (warp == 17 && !idle) {  // the block that holds pos: 33 cuts of the range at a time
+        int lo = 0, hi = n_blocks;  // start[lo] * H <= pos, start[hi] * H > pos
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 32) / 33, x = lo + (lane + 1) * step;
+            const bool below = x < hi && __ldcg(&a.block[x].start) * a.H_kv <= start.pos;
+            const int n = __popc(__ballot_sync(0xffffffffu, below));
+            hi = min(hi, lo + (n + 1) * step);
+            lo += n * step;
+        }
+        if (lane == 0) {
+            // (of blocks with one start only the last costs anything, and the search ends there)
+            const int cost = __ldcg(&a.block[lo].cost);
+            sm.e0 = lo;
+            sm.h0 = (int)((start.pos - __ldcg(&a.block[lo].start) * a.H_kv) / max(1, cost));
+        }
+    }
+    ck_fence_before();
     __syncthreads();
-    if (!live) return;
-    __nv_bfloat16* out = a.out + ((size_t)(rows.x + tok) * a.H_q + head) * D;
-    for (int i = 32 * part; i < 32 * part + 32; ++i) {
-        float x = 0.f;
-        for (int c = 0; c < D; ++c) x = fmaf(qs[row][c], __ldg(a.Rv + ((size_t)h * D + i) * D + c), x);
-        out[i] = __float2bfloat16_rn(x);
+    ck_fence_after();
+    start.e = sm.e0;
+    start.h = sm.h0;
+    const uint32_t tmem = sm.tmem;
+    const long long limit = a.drop ? CK_SHORT_WAIT_CYCLES : WAIT_LIMIT_CYCLES;
+    auto spin = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        const long long t0 = clock64();
+        while (true) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (*(volatile int*)&sm.dead) return false;
+            if (clock64() - t0 > limit) {
+                *(volatile int*)&sm.dead = 1;
+                atomicOr(a.error, ERR_TIMEOUT);
+                return false;
+            }
+        }
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, spin(bar, parity)); };  // a whole warp
+
+    if (group == 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (warp == 16 && lane == 0 && !idle) {
+            // ---- products
+            CkWalk w = start;
+            uint32_t tile0 = 0, steps[2] = {0, 0}, seg = 0;  // tiles before this share, steps of each stream
+            bool ok = true;
+            while (ok && w.next(a)) {
+                const int n = w.to - w.from, two = w.k.rows > CK_TILE;
+                const int ns[2] = {two ? n : (n + 1) / 2, two ? n : n / 2};
+                auto qk = [&](int t, int j) {
+                    const uint32_t x = tile0 + (two ? j : 2 * j + t), st = x & 1;
+                    if (!(ok = ok && spin(&sm.k_full[st], x >> 1 & 1))) return;
+                    ck_fence_after();
+                    const uint64_t qd = ck_desc(sm.q[t]), kd = ck_desc(sm.k[st]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4);
+                        ck_mma_ss(tmem + 128 * t, qd + at, kd + at, i > 0);
+                    }
+                    ck_commit(&sm.s_full[t]);
+                    if (!two || t == 1) ck_commit(&sm.k_free[st]);
+                };
+                auto pv = [&](int t, int j) {
+                    const uint32_t x = tile0 + (two ? j : 2 * j + t), st = x & 1;
+                    if (!(ok = ok && spin(&sm.v_full[st], x >> 1 & 1) && spin(&sm.p_full[t], (steps[t] + j) & 1))) return;
+                    ck_fence_after();
+                    const uint64_t vd = ck_desc(sm.v[st]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        ck_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, vd + (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4), j > 0 || i > 0);
+                    if (!two || t == 1) ck_commit(&sm.v_free[st]);
+                    if (j + 1 == ns[t]) ck_commit(&sm.o_full[t]);
+                };
+                for (int t = 0; t < 2; ++t)
+                    if (ok && (ok = spin(&sm.q_full[t], seg & 1)) && ns[t] > 0) qk(t, 0);
+                for (int j = 0; j < ns[0] && ok; ++j)
+                    for (int t = 0; t < 2 && ok; ++t)
+                        if (j < ns[t]) {
+                            pv(t, j);
+                            if (ok && j + 1 < ns[t]) qk(t, j + 1);
+                        }
+                tile0 += n;
+                steps[0] += ns[0];
+                steps[1] += ns[1];
+                ++seg;
+            }
+            // everything issued is done before TMEM is freed
+            ck_commit(&sm.drained);
+            (void)mbar_wait_bounded(&sm.drained, 0, 100000000LL);
+        } else if (warp == 17 && !idle) {
+            // ---- pages
+            CkWalk w = start;
+            uint32_t stage = 0;
+            bool ok = true;
+            while (ok && w.next(a)) {
+                const int p1 = min(w.k.pages, 8 * w.to), n = 2 * (w.to - w.from);
+                const int32_t* table = a.block_table + (size_t)w.k.b * a.max_pages;
+                auto ids = [&](int p0) {
+                    const int p = p0 + lane;
+                    return p < p1 ? __ldg(table + p + (p < w.k.sinks ? 0 : w.k.skip)) : 0;
+                };
+                int id = ids(8 * w.from), next_id = 0;
+                for (int s = 0; s < n && ok; ++s, ++stage) {
+                    if ((s & 7) == 0) {
+                        if (s) id = next_id;
+                        next_id = ids(8 * w.from + 4 * s + 32);
+                    }
+                    const uint32_t slot = stage % CK_RAW_STAGES;
+                    if (stage >= CK_RAW_STAGES && !(ok = wait(&sm.raw_free[slot], (stage / CK_RAW_STAGES - 1) & 1))) break;
+                    const int mine = __shfl_sync(0xffffffffu, id, 4 * (s & 7) + (lane & 3)), p = 8 * w.from + 4 * s + (lane & 3);
+                    const bool there = p < p1, good = there && mine >= 0 && (int64_t)mine < a.num_pages;
+                    const uint32_t copies = __popc(__ballot_sync(0xffffffffu, good) & 15u);
+                    if (lane < 4) {
+                        sm.raw_base[slot][lane] = good ? PAGE * (p + (p < w.k.sinks ? 0 : w.k.skip)) : -1;
+                        if (there && !good) atomicOr(a.error, ERR_BAD_PAGE);
+                        if (good && !(a.drop && stage == 0 && lane == 0 && cta == 0))
+                            bulk_g2s(sm.raw[slot] + lane * INT4_TILE, a.cache + ((size_t)mine * a.H_kv + w.last_h) * INT4_TILE, INT4_TILE, &sm.raw_full[slot]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[slot], copies * INT4_TILE);
+                }
+            }
+            if (lane == 0) sm.stages = stage;
+        }
+    } else if (group == 2) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ---- keys: a thread takes a token's words t of all groups, twice a stage
+        CkWalk w = start;
+        uint32_t tile = 0;
+        bool ok = !idle;
+        const int t = lane & 3, tok0 = 8 * (warp & 3) + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
+        while (ok && w.next(a))
+            for (int i = w.from; i < w.to && ok; ++i, ++tile) {
+                const uint32_t st = tile & 1;
+                if (tile >= 2 && !(ok = wait(&sm.k_free[st], (tile / 2 - 1) & 1))) break;
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t raw = 2 * tile + half, slot = raw % CK_RAW_STAGES;
+                    if (!(ok = wait(&sm.raw_full[slot], (raw / CK_RAW_STAGES) & 1))) break;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int tok = tok0 + 32 * e, row = 64 * half + tok;
+                        const uint8_t* page = sm.raw[slot] + (tok >> 4) * INT4_TILE;
+                        const uint4 codes = lds128(page + O4_KC + 64 * (tok & 15) + 16 * t), meta = lds128(page + O4_KM + 16 * (tok & 15));
+                        const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
+                        const __half2 tiny = u32_as_h2(0x2c002c00u);  // 1/16: with it no key leaves fp16
+                        const __half2 s01 = __hmul2(u32_as_h2(meta.x), tiny), s23 = __hmul2(u32_as_h2(meta.y), tiny);
+                        const __half2 m01 = __hmul2(u32_as_h2(meta.z), tiny), m23 = __hmul2(u32_as_h2(meta.w), tiny);
+                        uint8_t* out = sm.k[st] + row * 128;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const __half2 s = g & 1 ? __high2half2(g < 2 ? s01 : s23) : __low2half2(g < 2 ? s01 : s23);
+                            const __half2 m = g & 1 ? __high2half2(g < 2 ? m01 : m23) : __low2half2(g < 2 ? m01 : m23);
+                            __half2 c[4];
+                            ck_codes(word[g], c);
+                            const uint4 x = make_uint4(h2_as_u32(__hfma2(c[0], s, m)), h2_as_u32(__hfma2(c[1], s, m)),
+                                                       h2_as_u32(__hfma2(c[2], s, m)), h2_as_u32(__hfma2(c[3], s, m)));
+                            *reinterpret_cast<uint4*>(out + (g >> 1) * CK_HALF + (((4 * (g & 1) + t) ^ (row & 7)) << 4)) = x;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.raw_free[slot]);
+                        mbar_arrive(&sm.k_full[st]);
+                    }
+                }
+            }
+    } else if (group == 3) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ---- values: a thread takes the words r of eight tokens and two groups
+        CkWalk w = start;
+        uint32_t tile = 0;
+        bool ok = !idle;
+        const int wg = warp & 3, r = lane & 7, oct = 4 * (wg & 1) + (lane >> 3), g0 = 2 * (wg >> 1);
+        while (ok && w.next(a)) {
+            // positions of the streams' first and last rows
+            int first[2], last[2];
+            for (int t = 0; t < 2; ++t) {
+                const int r0 = w.k.r0 + (w.k.rows > CK_TILE ? CK_TILE * t : 0), r1 = min(w.k.r0 + w.k.rows, r0 + CK_TILE) - 1;
+                first[t] = w.k.ctx - w.k.n + r0 / a.G;
+                last[t] = w.k.ctx - w.k.n + r1 / a.G;
+            }
+            for (int i = w.from; i < w.to && ok; ++i, ++tile) {
+                const uint32_t st = tile & 1;
+                if (tile >= 2 && !(ok = wait(&sm.v_free[st], (tile / 2 - 1) & 1))) break;
+                CkInfo& info = sm.info[st];
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t raw = 2 * tile + half, slot = raw % CK_RAW_STAGES;
+                    if (!(ok = wait(&sm.raw_full[slot], (raw / CK_RAW_STAGES) & 1))) break;
+                    const uint8_t* page = sm.raw[slot] + (oct >> 1) * INT4_TILE;
+                    const int base = sm.raw_base[slot][oct >> 1], pair0 = 4 * (oct & 1);
+                    // tokens of the octet within the context, none without a page
+                    const int valid = base < 0 ? 0 : min(8, max(0, w.k.ctx - base - 2 * pair0));
+                    uint2 code[4], sc[4], mn[4];
+                    __half2 most = u32_as_h2(0u);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        code[p] = lds64(page + O4_VC + 128 * (pair0 + p) + 16 * r + 4 * g0);
+                        sc[p] = lds64(page + O4_VS + 16 * (pair0 + p) + 4 * g0);
+                        mn[p] = lds64(page + O4_VM + 16 * (pair0 + p) + 4 * g0);
+                    }
+                    {   // a lane looks at one pair's two groups of scales or mins: those from 2^11 or 2^15 up, and NaN, take the long way
+                        const uint2 look = lds64(page + (r & 4 ? O4_VM : O4_VS) + 16 * (pair0 + (r & 3)) + 4 * g0);
+                        most = __hmax2_nan(__habs2(u32_as_h2(look.x)), __habs2(u32_as_h2(look.y)));
+                    }
+                    const float edge = r & 4 ? 32768.f : 2048.f;
+                    const bool plain = valid == 8 && __low2float(most) < edge && __high2float(most) < edge;
+                    uint32_t poison = 0u;
+                    uint8_t* out = sm.v[st] + half * CK_HALF + r * 128 + ((oct ^ r) << 4);
+                    if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t x[4][4];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                __half2 c[4];
+                                ck_codes(g ? code[p].y : code[p].x, c);
+                                const __half2 s = u32_as_h2(g ? sc[p].y : sc[p].x), m = u32_as_h2(g ? mn[p].y : mn[p].x);
+#pragma unroll
+                                for (int n = 0; n < 4; ++n) x[n][p] = h2_as_u32(__hfma2(c[n], s, m));
+                            }
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                *reinterpret_cast<uint4*>(out + (32 * (g0 + g) + 8 * n) * 128) = make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
+                        }
+                    } else {
+                        // in fp32, cut off at fp16's ends; tokens past the context are 0, and so are those that hold what is not
+                        // finite, whose logits the softmax makes NaN instead (a weight of 0 would not hide it from other rows)
+                        uint32_t bad = 0u;  // of the octet's tokens
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float2 s0 = __half22float2(u32_as_h2(sc[p].x)), s1 = __half22float2(u32_as_h2(sc[p].y));
+                                const float2 m0 = __half22float2(u32_as_h2(mn[p].x)), m1 = __half22float2(u32_as_h2(mn[p].y));
+                                const float all = e ? (s0.y - s0.y) + (s1.y - s1.y) + (m0.y - m0.y) + (m1.y - m1.y)
+                                                    : (s0.x - s0.x) + (s1.x - s1.x) + (m0.x - m0.x) + (m1.x - m1.x);
+                                if (all != 0.f && 2 * p + e < valid) bad |= 1u << (2 * p + e);
+                            }
+                        const uint32_t keep = (1u << valid) - 1u & ~bad;
+#pragma unroll 1
+                        for (int x = 0; x < 8; ++x) {
+                            const int g = x >> 2, n = x & 3;
+                            uint32_t y[4];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const uint32_t c = (g ? code[p].y : code[p].x) >> (4 * n);
+                                const float2 s = __half22float2(u32_as_h2(g ? sc[p].y : sc[p].x)), m = __half22float2(u32_as_h2(g ? mn[p].y : mn[p].x));
+                                const float lo = fminf(fmaxf(fmaf((float)(c & 15), s.x, m.x), -65504.f), 65504.f);
+                                const float hi = fminf(fmaxf(fmaf((float)(c >> 16 & 15), s.y, m.y), -65504.f), 65504.f);
+                                y[p] = pack_half2(keep >> (2 * p) & 1 ? lo : 0.f, keep >> (2 * p + 1) & 1 ? hi : 0.f);
+                            }
+                            *reinterpret_cast<uint4*>(out + (32 * (g0 + g) + 8 * n) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                        poison = bad << (8 * (lane >> 3));
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) poison |= __shfl_xor_sync(0xffffffffu, poison, o);
+                    }
+                    if (lane == 0) info.poison[half][wg] = poison;
+                    if (wg == 0) {
+                        const int at = sm.raw_base[slot][lane & 3];
+                        bool part[2];
+                        for (int t = 0; t < 2; ++t)
+                            part[t] = at < 0 || at + PAGE - 1 > first[t] || (a.window && at <= last[t] - a.window && at + PAGE > a.sinks);
+                        const uint32_t s0 = __any_sync(0xffffffffu, part[0]), s1 = __any_sync(0xffffffffu, part[1]);
+                        if (lane < 4) info.base[half][lane] = at;
+                        if (lane == 0) info.special[half] = s0 | s1 << 1;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.raw_free[slot]);
+                        mbar_arrive(&sm.v_full[st]);
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        // ---- softmax of stream t: a thread a row
+        CkWalk w = start;
+        const int t = group, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
+        uint32_t tile0 = 0, step = 0, parts = 0;
+        bool ok = !idle;
+        while (ok && w.next(a)) {
+            const int two = w.k.rows > CK_TILE, n = w.to - w.from, ns = two ? n : (n + 1 - t) / 2;
+            const int in_block = (two ? CK_TILE * t : 0) + row;
+            const bool live = in_block < w.k.rows;
+            const int in_seq = w.k.r0 + (live ? in_block : 0);
+            const int64_t grow = (int64_t)w.k.q0 * a.G + in_seq;                       // of all rows
+            const int64_t at = (int64_t)w.last_h * a.n_tok * a.G + grow;
+            const int pos = w.k.ctx - w.k.n + in_seq / a.G;
+            {   // the row's queries (the stream's last product with the ones before is done: its logits were read)
+                const uint4* src = reinterpret_cast<const uint4*>(a.rot + at * D);
+                uint8_t* dst = sm.q[t] + row * 128;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * CK_HALF + (((c & 7) ^ (row & 7)) << 4)) = __ldcg(src + c);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_full[t]);
+            }
+            const float f = __ldcg(a.row_scale + at);
+            float ref = CK_NEG, l = 0.f;
+            for (int j = 0; j < ns && ok; ++j, ++step) {
+                const uint32_t tile = tile0 + (two ? j : 2 * j + t), st = tile & 1;
+                if (!(ok = wait(&sm.v_full[st], tile >> 1 & 1) && wait(&sm.s_full[t], step & 1))) break;
+                ck_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ck_tmem_ld32(s + 32 * c, s_at + 32 * c);
+                const CkInfo& info = sm.info[st];
+                const uint4 pa = lds128(info.poison[0]), pb = lds128(info.poison[1]);
+                const uint32_t poisoned = pa.x | pa.y | pa.z | pa.w | pb.x | pb.y | pb.z | pb.w;
+                const bool special = ((info.special[0] | info.special[1]) >> t & 1) || poisoned;
+                ck_loaded(s);
+                if (special) {
+#pragma unroll
+                    for (int pg = 0; pg < 8; ++pg) {
+                        const int base = info.base[pg >> 2][pg & 3];
+                        uint32_t see = base < 0 ? 0u : (1u << min(PAGE, max(0, pos - base + 1))) - 1u;
+                        if (a.window) {
+                            const int low = min(PAGE, max(0, pos - a.window + 1 - base)), sink = min(PAGE, max(0, a.sinks - base));
+                            see &= ~((1u << low) - 1u) | ((1u << sink) - 1u);
+                        }
+                        const uint32_t w0 = info.poison[pg >> 2][pg >> 1 & 1] | info.poison[pg >> 2][2 + (pg >> 1 & 1)];
+                        const uint32_t bad = w0 >> (16 * (pg & 1));
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            if (bad >> c & 1) s[16 * pg + c] = 0x7fffffffu;
+                            if (!(see >> c & 1)) s[16 * pg + c] = 0xff800000u;
+                        }
+                    }
+                }
+                float m0 = __uint_as_float(s[0]), m1 = __uint_as_float(s[1]);
+#pragma unroll
+                for (int c = 2; c < 126; c += 4) {
+                    m0 = fmaxf(fmaxf(m0, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                    m1 = fmaxf(fmaxf(m1, __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
+                }
+                const float top = fmaxf(fmaxf(m0, m1), fmaxf(__uint_as_float(s[126]), __uint_as_float(s[127]))) * f;
+                if (__any_sync(0xffffffffu, top > ref + CK_STALE)) {
+                    const float up = top > ref + CK_STALE ? ceilf(top) : ref, c0 = ck_ex2(ref - up);
+                    ref = up;
+                    l *= c0;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[16];
+                            asm volatile(
+                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                                : CK_R8(o, 0), CK_R8(o, 8)
+                                : "r"(o_at + 16 * c)
+                                : "memory");
+                            ck_loaded(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c0);
+                            asm volatile(
+                                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::CK_W8(o, 0),
+                                CK_W8(o, 8), "r"(o_at + 16 * c)
+                                : "memory");
+                        }
+                    }
+                }
+                const float2 f2 = make_float2(f, f), off = make_float2(CK_LIFT - ref, CK_LIFT - ref);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    float2 x = ck_fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), f2, off);
+                    x = make_float2(ck_ex2(x.x), ck_ex2(x.y));
+                    sum[c & 1] = ck_add2(sum[c & 1], x);
+                    s[c] = pack_half2(x.x, x.y);
+                    if (c == 31) ck_tmem_st32(s, s_at);
+                }
+                ck_tmem_st32(s + 32, s_at + 32);
+                sum[0] = ck_add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+                ck_wait_st();
+                ck_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[t]);
+            }
+            tile0 += n;
+            if (ok && ns > 0) {
+                if (!(ok = wait(&sm.o_full[t], parts & 1))) break;
+                ++parts;
+                ck_fence_after();
+                float* out = w.from > 0   ? a.extra + ((size_t)cta * CK_ROWS + CK_TILE * t + row) * PART_STRIDE
+                             : two || !t  ? a.main + at * PART_STRIDE
+                             : a.second_rows ? a.second + (((int64_t)w.k.b * a.H_kv + w.last_h) * a.second_rows + row) * PART_STRIDE
+                                             : a.second + at * PART_STRIDE;
+                if (live) *reinterpret_cast<float2*>(out) = make_float2(ref - CK_LIFT, l);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    ck_tmem_ld32(o, o_at + 32 * c);
+                    ck_loaded(o);
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<uint4*>(out + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                }
+                ck_fence_before();
+            }
+        }
+    }
+    __syncwarp();
+    ck_fence_before();
+    __syncthreads();
+    if (sm.dead && warp == 17 && !idle)  // copies in flight land before the block ends
+        for (uint32_t n = sm.stages, s = n > CK_RAW_STAGES ? n - CK_RAW_STAGES : 0; s < n; ++s)
+            (void)mbar_wait_bounded(&sm.raw_full[s % CK_RAW_STAGES], (s / CK_RAW_STAGES) & 1, 1000000LL);
+    if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ------------------------------------------------------------------ 3: finish
+
+// CTAs of 256 threads per (row tile, KV head): the rows' partials merged (a warp 16 rows, a lane
+// four channels), normalised, rotated by R_v^T.
+struct __align__(16) CkFinish {
+    CkMatrix R;
+    __align__(16) __nv_bfloat16 o[2][CK_TILE][D + 8];  // high and low parts
+};
+__global__ void __launch_bounds__(256) chunk_finish_kernel(const __grid_constant__ ChunkArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    CkFinish& sm = *reinterpret_cast<CkFinish*>(smem_raw);
+    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    const float* Rv = a.Rv + (size_t)h * D * D;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int C = __ldcg(&a.plan->ctas), n_blocks = __ldcg(&a.plan->blocks);
+    const int64_t total = __ldcg(&a.plan->total);
+    bool staged = false;
+    for (int x = blockIdx.x; x < 2 * n_blocks; x += gridDim.x) {
+        CkWalk w;
+        w.e = x >> 1;
+        w.read(a);
+        const int tile = x & 1, r0 = CK_TILE * tile, two = w.k.rows > CK_TILE;
+        if (r0 >= w.k.rows) continue;
+        if (!staged) {
+            // B: k = position of the unpacked values, n = output channel
+            ck_stage_matrix(sm.R, [&](int k, int n) { return __ldg(Rv + (size_t)n * D + ck_value_channel(k)); });
+            staged = true;
+        }
+        __syncthreads();
+        const int rows = min(CK_TILE, w.k.rows - r0), wt = ck_weight(w.k.rows);
+        const int64_t unit = w.k.start * a.H_kv + (int64_t)h * w.k.cost;
+        const int c0 = w.k.tiles ? (int)(((unit + 1) * C - 1) / total) : 0, c1 = w.k.tiles ? (int)(((unit + (int64_t)wt * (w.k.tiles - 1) + 1) * C - 1) / total) : -1;
+        for (int i = warp; i < CK_TILE; i += 8) {
+            float M = CK_NEG, L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < rows) {
+                const int64_t at = (int64_t)h * a.n_tok * a.G + (int64_t)w.k.q0 * a.G + w.k.r0 + r0 + i;
+                auto merge = [&](const float* p) {
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
+                    const float4 o = __ldcg(reinterpret_cast<const float4*>(p + 4 + 4 * lane));
+                    const float top = fmaxf(M, ml.x), f = ck_ex2(M - top), g = ck_ex2(ml.x - top);
+                    L = fmaf(L, f, ml.y * g);
+                    O = make_float4(fmaf(O.x, f, o.x * g), fmaf(O.y, f, o.y * g), fmaf(O.z, f, o.z * g), fmaf(O.w, f, o.w * g));
+                    M = top;
+                };
+                for (int c = c0; c <= c1; ++c) {
+                    const int64_t b0 = max(ck_cut(total, c, C), unit), b1 = min(ck_cut(total, c + 1, C), unit + w.k.cost);
+                    const int from = (int)((b0 - unit + wt - 1) / wt), n = min(w.k.tiles, (int)((b1 - unit + wt - 1) / wt)) - from;
+                    if (n <= 0) continue;
+                    const float* e = a.extra + ((size_t)c * CK_ROWS + (two ? r0 : 0) + i) * PART_STRIDE;
+                    merge(from > 0 ? e : a.main + at * PART_STRIDE);
+                    if (!two && n > 1)
+                        merge(from > 0         ? e + (size_t)CK_TILE * PART_STRIDE
+                              : a.second_rows ? a.second + (((int64_t)w.k.b * a.H_kv + h) * a.second_rows + i) * PART_STRIDE
+                                              : a.second + at * PART_STRIDE);
+                }
+            }
+            const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);  // no token: 0; NaN stays NaN
+            uint2 hi, lo;
+            ck_parts(O.x * inv, O.y * inv, hi.x, lo.x);
+            ck_parts(O.z * inv, O.w * inv, hi.y, lo.y);
+            *reinterpret_cast<uint2*>(&sm.o[0][i][4 * lane]) = hi;
+            *reinterpret_cast<uint2*>(&sm.o[1][i][4 * lane]) = lo;
+        }
+        __syncthreads();
+        if (16 * warp < rows) {
+            uint32_t hi[8][4], lo[8][4];
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 16 * warp + r + 8 * (e & 1), c = 16 * ks + 8 * (e >> 1) + 2 * t;
+                    hi[ks][e] = *reinterpret_cast<const uint32_t*>(&sm.o[0][i][c]);
+                    lo[ks][e] = *reinterpret_cast<const uint32_t*>(&sm.o[1][i][c]);
+                }
+#pragma unroll 1
+            for (int nt = 0; nt < 16; ++nt) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint4 b = sm.R.f[ks][nt][lane];
+                    ck_mma(c, lo[ks], b.x, b.y);
+                    ck_mma(c, hi[ks], b.z, b.w);
+                    ck_mma(c, hi[ks], b.x, b.y);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 16 * warp + r + 8 * e;
+                    if (i >= rows) continue;
+                    const int in_seq = w.k.r0 + r0 + i;
+                    __nv_bfloat16* out = a.out + ((int64_t)(w.k.q0 + in_seq / a.G) * a.H_q + (int64_t)h * a.G + in_seq % a.G) * D;
+                    *reinterpret_cast<uint32_t*>(out + 8 * nt + 2 * t) = ck_pack(c[2 * e], c[2 * e + 1]);
+                }
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -151,9 +989,56 @@ static const char* chunk_refusal(int n_tok, int B, int H_q, int H_kv, kvq_status
     return nullptr;
 }
 
+struct ChunkLayout {
+    size_t plan, block, scale, rot, main, second, extra, total;
+    int max_blocks;
+    int64_t second_rows;
+};
+static ChunkLayout chunk_layout(int n_tok, int B, int H_q, int H_kv) {
+    const int64_t G = H_q / H_kv, rows = (int64_t)n_tok * H_q, part = PART_STRIDE * 4;
+    // second streams: of blocks of one row tile, at most one per sequence
+    const bool few = (int64_t)B * H_kv * CK_TILE < rows;
+    ChunkLayout l;
+    l.max_blocks = (int)((int64_t)n_tok * G / CK_ROWS + B);
+    l.second_rows = few ? CK_TILE : 0;
+    l.plan = WS_HEADER;
+    l.block = align_up(l.plan + sizeof(CkPlan), 256);
+    l.scale = align_up(l.block + (size_t)l.max_blocks * sizeof(CkBlock), 256);
+    l.rot = align_up(l.scale + (size_t)rows * 4, 256);
+    l.main = align_up(l.rot + (size_t)rows * D * 2, 256);
+    l.second = align_up(l.main + (size_t)(rows * part), 256);
+    l.extra = align_up(l.second + (size_t)((few ? (int64_t)B * H_kv * CK_TILE : rows) * part), 256);
+    l.total = l.extra + (size_t)kvq_device_sm_count() * CK_ROWS * part;
+    return l;
+}
+
 extern "C" size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv) {
     kvq_status st;
-    return chunk_refusal(n_tok, B, H_q, H_kv, st) ? 0 : (size_t)WS_HEADER;
+    return chunk_refusal(n_tok, B, H_q, H_kv, st) ? 0 : chunk_layout(n_tok, B, H_q, H_kv).total;
+}
+
+// The shared memory opt-ins, once on each device.
+static kvq_status chunk_smem_once() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    kvq_status st = kvq_check_cuda(cudaGetDevice(&dev), "kvq_chunk_attn_int4: cudaGetDevice");
+    if (st != KVQ_OK) return st;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < 64 && done[dev]) return KVQ_OK;
+    const struct {
+        const void* fn;
+        size_t bytes;
+    } need[3] = {{(const void*)chunk_rotate_kernel, sizeof(CkMatrix)},
+                 {(const void*)chunk_stream_kernel, sizeof(CkSmem) + 1024},
+                 {(const void*)chunk_finish_kernel, sizeof(CkFinish)}};
+    for (const auto& x : need) {
+        st = kvq_check_cuda(cudaFuncSetAttribute(x.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.bytes),
+                            "kvq_chunk_attn_int4 smem attribute");
+        if (st != KVQ_OK) return st;
+    }
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return KVQ_OK;
 }
 
 extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_t* q_start, int B, int H_q, int H_kv, int d,
@@ -177,9 +1062,10 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     for (const void* p : {q, cache, (const void*)R_k, (const void*)R_v, (const void*)out, (const void*)workspace})
         if (reinterpret_cast<uintptr_t>(p) % 16)
             return kvq_set_error(KVQ_ERR_INVALID_ARG, "%s: q, cache, R_k, R_v, out and workspace need 16-byte alignment", fn);
-    if (workspace_bytes < kvq_chunk_workspace_bytes(n_tok, B, H_q, H_kv))
-        return kvq_set_error(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
-                             kvq_chunk_workspace_bytes(n_tok, B, H_q, H_kv));
+    const ChunkLayout l = chunk_layout(n_tok, B, H_q, H_kv);
+    if (workspace_bytes < l.total)
+        return kvq_set_error(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, l.total);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     ChunkArgs a;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.n_tok = n_tok;
@@ -199,8 +1085,29 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     a.window = window;
     a.sinks = window ? sinks : 0;
     a.out = static_cast<__nv_bfloat16*>(out);
-    a.error = static_cast<uint32_t*>(workspace);
-    const int64_t blocks = ((int64_t)n_tok * a.G + CH_ROWS - 1) / CH_ROWS + B;
-    return kvq_check_cuda(launch_pdl(chunk_int4_kernel, dim3((unsigned)blocks, H_kv), dim3(128), 0, static_cast<cudaStream_t>(stream), a),
-                          "kvq_chunk_attn_int4 launch");
+    a.error = reinterpret_cast<uint32_t*>(ws);
+    a.plan = reinterpret_cast<CkPlan*>(ws + l.plan);
+    a.block = reinterpret_cast<CkBlock*>(ws + l.block);
+    a.max_blocks = l.max_blocks;
+    a.row_scale = reinterpret_cast<float*>(ws + l.scale);
+    a.rot = reinterpret_cast<__half*>(ws + l.rot);
+    a.main = reinterpret_cast<float*>(ws + l.main);
+    a.second = reinterpret_cast<float*>(ws + l.second);
+    a.second_rows = l.second_rows;
+    a.extra = reinterpret_cast<float*>(ws + l.extra);
+    a.ctas = kvq_device_sm_count();
+    a.drop = kvq_take_drop_next_copy();
+    st = chunk_smem_once();
+    if (st != KVQ_OK) return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int64_t row_tiles = ((int64_t)n_tok * a.G + CK_TILE - 1) / CK_TILE;
+    auto capped = [&](int64_t want) { return (unsigned)std::min(want, std::max<int64_t>(1, 4 * a.ctas / H_kv)); };  // CTAs per head
+    st = kvq_check_cuda(launch_pdl(chunk_rotate_kernel, dim3(capped(row_tiles) + 1, H_kv), dim3(256), sizeof(CkMatrix), cs, a),
+                        "kvq_chunk_attn_int4 rotate launch");
+    if (st != KVQ_OK) return st;
+    st = kvq_check_cuda(launch_pdl(chunk_stream_kernel, dim3(a.ctas), dim3(CK_THREADS), sizeof(CkSmem) + 1024, cs, a),
+                        "kvq_chunk_attn_int4 launch");
+    if (st != KVQ_OK) return st;
+    return kvq_check_cuda(launch_pdl(chunk_finish_kernel, dim3(capped(2 * (int64_t)l.max_blocks), H_kv), dim3(256), sizeof(CkFinish), cs, a),
+                          "kvq_chunk_attn_int4 finish launch");
 }
