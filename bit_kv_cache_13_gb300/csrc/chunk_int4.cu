@@ -23,7 +23,6 @@ constexpr int CK_ROWS = 256;       // rows of a block: two row tiles of 128
 constexpr int CK_TILE = 128;       // cached tokens of a tile: eight pages
 constexpr int CK_UNIT_COST = 6;    // what starting a block costs, in tiles of one row tile
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
-constexpr float CK_STALE = 8.f;    // a row's reference stays while its logits are at most 2^8 above it
 constexpr float CK_LIFT = 7.f;     // weights are carried 2^7 times as large: they use fp16 from 2^15 down
 constexpr long long CK_SHORT_WAIT_CYCLES = 2000000LL;
 
@@ -218,30 +217,23 @@ __device__ __forceinline__ void ck_parts(float x, float y, uint32_t& hi, uint32_
 }
 
 // A matrix as the B operand of m16n8k16, in two bf16 parts: [K step][8 columns][lane] of (b0, b1) of the high part, then
-// of the low one.  at(k, n) is its entry.
+// of the low one.
 struct __align__(16) CkMatrix {
     uint4 f[8][16][32];
 };
-template <typename At>
-__device__ __forceinline__ void ck_stage_matrix(CkMatrix& m, At at) {
-    for (int x = threadIdx.x; x < 8 * 16 * 32; x += blockDim.x) {
-        const int lane = x & 31, nt = (x >> 5) & 15, ks = x >> 9, n = 8 * nt + (lane >> 2), k = 16 * ks + 2 * (lane & 3);
-        uint4 f;
-        ck_parts(at(k, n), at(k + 1, n), f.x, f.z);
-        ck_parts(at(k + 8, n), at(k + 9, n), f.y, f.w);
-        m.f[ks][nt][lane] = f;
-    }
-}
 
 // Position of a key channel in the unpacked keys: a word's eight channels come as (0, 4), (1, 5), (2, 6), (3, 7).
 __host__ __device__ constexpr int ck_key_at(int ch) { return (ch & ~7) | (ch & 3) << 1 | (ch >> 2 & 1); }
-// Position of a value channel 32 g + 4 r + i in the unpacked values: 32 g + 8 i + r.
-__host__ __device__ constexpr int ck_value_channel(int at) { return (at & ~31) | (at & 7) << 2 | (at >> 3 & 3); }
+// (A value channel 32 g + 4 r + i stands at 32 g + 8 i + r.)
 
 // CTAs of 256 threads, 128 rows each (a warp 16); the last CTA of a head's row makes the plan.
+struct __align__(16) CkRotate {
+    CkMatrix R;
+    __align__(16) __half out[8][16][D + 8];
+};
 __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    CkMatrix& R = *reinterpret_cast<CkMatrix*>(smem_raw);
+    CkRotate& sm = *reinterpret_cast<CkRotate*>(smem_raw);
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x == gridDim.x - 1) {
@@ -250,14 +242,9 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
     }
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
     const float* Rk = a.Rk + (size_t)h * D * D;
-    // columns of the product in the order of the unpacked keys: column position n holds channel c with ck_key_at(c) == n
-    ck_stage_matrix(R, [&](int k, int n) { return __ldg(Rk + k * D + ((n & ~7) | (n >> 1 & 3) | (n & 1) << 2)); });
-    __syncthreads();
     const int64_t rows = (int64_t)a.n_tok * a.G;
-    for (int64_t r0 = (int64_t)blockIdx.x * 128 + 16 * warp; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 128) {
+    auto fetch = [&](int64_t r0, uint32_t (&x)[8][4]) {
         const __nv_bfloat16* q[2];
-        uint32_t x[8][4];
-        float n2[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int64_t row = min(r0 + r + 8 * e, rows - 1);
@@ -267,6 +254,30 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
         for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[ks][e] = __ldg(reinterpret_cast<const uint32_t*>(q[e & 1] + 16 * ks + 8 * (e >> 1) + 2 * t));
+    };
+    uint32_t x[8][4];
+    int64_t r0 = (int64_t)blockIdx.x * 128 + 16 * warp;
+    if (r0 < rows) fetch(r0, x);
+    // Columns of the product in the order of the unpacked keys: position n holds channel c with ck_key_at(c) == n.
+    // A thread takes four channels (low or high half of eight: positions 2 i or 2 i + 1) of rows k, k + 1, k + 8, k + 9.
+#pragma unroll
+    for (int y = threadIdx.x; y < 8 * 4 * 32; y += 256) {
+        const int c4 = y & 31, tt = (y >> 5) & 3, ks = y >> 7;
+        const float* p = Rk + (size_t)(16 * ks + 2 * tt) * D + 4 * c4;
+        const float4 v0 = __ldg(reinterpret_cast<const float4*>(p)), v1 = __ldg(reinterpret_cast<const float4*>(p + D));
+        const float4 v8 = __ldg(reinterpret_cast<const float4*>(p + 8 * D)), v9 = __ldg(reinterpret_cast<const float4*>(p + 9 * D));
+        const float k0[4] = {v0.x, v0.y, v0.z, v0.w}, k1[4] = {v1.x, v1.y, v1.z, v1.w}, k8[4] = {v8.x, v8.y, v8.z, v8.w}, k9[4] = {v9.x, v9.y, v9.z, v9.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 f;
+            ck_parts(k0[i], k1[i], f.x, f.z);
+            ck_parts(k8[i], k9[i], f.y, f.w);
+            sm.R.f[ks][c4 >> 1][4 * (2 * i + (c4 & 1)) + tt] = f;
+        }
+    }
+    __syncthreads();
+    for (; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 128) {
+        float n2[2] = {0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
@@ -288,21 +299,28 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
         }
 #pragma unroll 2
         for (int nt = 0; nt < 16; ++nt) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
-                const uint4 b = R.f[ks][nt][lane];
-                ck_mma(c, x[ks], b.z, b.w);
+                const uint4 b = sm.R.f[ks][nt][lane];
+                ck_mma(d, x[ks], b.z, b.w);
                 ck_mma(c, x[ks], b.x, b.y);
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int64_t row = r0 + r + 8 * e;
-                if (row < rows)
-                    *reinterpret_cast<uint32_t*>(a.rot + ((int64_t)h * rows + row) * D + 8 * nt + 2 * t) =
-                        pack_half2(c[2 * e] * f[e], c[2 * e + 1] * f[e]);
-            }
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<uint32_t*>(&sm.out[warp][r + 8 * e][8 * nt + 2 * t]) =
+                    pack_half2((c[2 * e] + d[2 * e]) * f[e], (c[2 * e + 1] + d[2 * e + 1]) * f[e]);
         }
+        const int64_t next = r0 + (int64_t)(gridDim.x - 1) * 128;
+        if (next < rows) fetch(next, x);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // two rows at a time, 16 bytes a lane
+            const int y = 2 * i + (lane >> 4);
+            if (r0 + y < rows)
+                *reinterpret_cast<uint4*>(a.rot + ((int64_t)h * rows + r0 + y) * D + 8 * (lane & 15)) = lds128(&sm.out[warp][y][8 * (lane & 15)]);
+        }
+        __syncwarp();
     }
 }
 
@@ -320,42 +338,62 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
 //            transposed: rows are channels), three raw stages of four pages
 constexpr int CK_OPERAND = 128 * 128 * 2, CK_HALF = CK_OPERAND / 2;  // 64 columns of 128 rows each
 constexpr int CK_RAW_PAGES = 4, CK_RAW = CK_RAW_PAGES * INT4_TILE, CK_RAW_STAGES = 3;
+// (registers: 640 threads of 96 at launch; 152 for softmax, 64 for unpacking and 40 for the rest are 60416 of those 61440)
 constexpr int CK_THREADS = 640;
 
-struct __align__(16) CkInfo {  // of a tile of tokens, written with its values
+constexpr int CK_INFOS = 4, CK_SHARES = 4;
+
+struct __align__(16) CkInfo {  // of a tile of tokens, written with its keys
     int base[2][4];        // first position of each page, -1 without one
-    uint32_t poison[2][4]; // [half][warp]: tokens whose values are not finite, 32 of them per warp
+    uint32_t poison[2][4]; // tokens of each page whose values are not finite
     uint32_t special[2];   // [half]: bit t: stream t's rows do not all see all of it
+};
+struct __align__(16) CkShare {  // what the roles need of a share
+    int n, two, from, rows;     // tiles; two row tiles
+    int r0, pos0, ctx, b;       // pos0: position of the sequence's first new token
+    int first[2], last[2];      // positions of the streams' first and last rows
+    int64_t row0;               // the sequence's first row among all of a head's
+    int h, end;
 };
 struct __align__(1024) CkSmem {
     uint8_t q[2][CK_OPERAND], k[2][CK_OPERAND], v[2][CK_OPERAND];
     uint8_t raw[CK_RAW_STAGES][CK_RAW];
-    __align__(16) CkInfo info[2];
+    CkInfo info[CK_INFOS];
+    CkShare share[CK_SHARES];
     __align__(16) int raw_base[CK_RAW_STAGES][4];
     uint64_t raw_full[CK_RAW_STAGES], raw_free[CK_RAW_STAGES], k_full[2], k_free[2], v_full[2], v_free[2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained, share_full[CK_SHARES], share_free[CK_SHARES];
     uint32_t tmem;
-    int dead, e0, h0;
+    int dead;
     uint32_t stages;  // raw stages fetched
 };
 static_assert(sizeof(CkSmem) + 1024 <= 227 * 1024, "chunk shared memory above 227 KB");
 
-__device__ __forceinline__ uint64_t ck_desc(const void* p) {  // K-major, 128-byte swizzle: atoms of 8 rows, 1024 bytes apart
-    return (uint64_t)((smem_u32(p) & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Descriptor of an operand, K-major in the 128-byte swizzle: atoms of 8 rows, 1024 bytes apart.  Its low word holds the
+// address in 16-byte units.
+__device__ __forceinline__ uint32_t ck_desc_lo(const void* p) { return (smem_u32(p) & 0x3ffff) >> 4 | 1u << 16; }
+constexpr uint32_t CK_DESC_HI = (1024 >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ bool ck_elect() {
+    uint32_t x;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+    return x != 0;
 }
 // fp32 accumulators, fp16 operands, both K-major, 128 x 128
 constexpr uint32_t CK_IDESC = 1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24;
 
-__device__ __forceinline__ void ck_mma_ss(uint32_t d, uint64_t a, uint64_t b, bool add) {
+__device__ __forceinline__ void ck_mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
-        "r"(CK_IDESC), "r"((uint32_t)add)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(CK_IDESC), "r"((uint32_t)add),
+        "r"(CK_DESC_HI)
         : "memory");
 }
-__device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint64_t b, bool add) {
+__device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
-        "r"(CK_IDESC), "r"((uint32_t)add)
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(CK_IDESC), "r"((uint32_t)add),
+        "r"(CK_DESC_HI)
         : "memory");
 }
 __device__ __forceinline__ void ck_commit(uint64_t* bar) {
@@ -441,116 +479,169 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_full[i], 1);
         }
+        for (int i = 0; i < CK_SHARES; ++i) {
+            mbar_init(&sm.share_full[i], 1);
+            mbar_init(&sm.share_free[i], 17);  // the warps but the loader
+        }
         mbar_init(&sm.drained, 1);
         sm.dead = 0;
+        sm.stages = 0;
         fence_mbar_init();
     }
     if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    griddep_wait();
-    griddep_launch_dependents();
-    const int C = __ldcg(&a.plan->ctas), cta = blockIdx.x, n_blocks = __ldcg(&a.plan->blocks);
-    const int64_t total = __ldcg(&a.plan->total);
-    const bool idle = cta >= C;
-    CkWalk start;
-    start.pos = idle ? 0 : ck_cut(total, cta, C);
-    start.end = idle ? 0 : ck_cut(total, cta + 1, C);
-    if (warp == 17 && !idle) {  // the block that holds pos: 33 cuts of the range at a time
-        int lo = 0, hi = n_blocks;  // start[lo] * H <= pos, start[hi] * H > pos
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 32) / 33, x = lo + (lane + 1) * step;
-            const bool below = x < hi && __ldcg(&a.block[x].start) * a.H_kv <= start.pos;
-            const int n = __popc(__ballot_sync(0xffffffffu, below));
-            hi = min(hi, lo + (n + 1) * step);
-            lo += n * step;
-        }
-        if (lane == 0) {
-            // (of blocks with one start only the last costs anything, and the search ends there)
-            const int cost = __ldcg(&a.block[lo].cost);
-            sm.e0 = lo;
-            sm.h0 = (int)((start.pos - __ldcg(&a.block[lo].start) * a.H_kv) / max(1, cost));
-        }
-    }
     ck_fence_before();
     __syncthreads();
     ck_fence_after();
-    start.e = sm.e0;
-    start.h = sm.h0;
+    griddep_wait();
+    griddep_launch_dependents();
     const uint32_t tmem = sm.tmem;
     const long long limit = a.drop ? CK_SHORT_WAIT_CYCLES : WAIT_LIMIT_CYCLES;
-    auto spin = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // a whole warp
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        bool ok = true;
         const long long t0 = clock64();
-        while (true) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if (*(volatile int*)&sm.dead) return false;
+        while (!mbar_try_wait(bar, parity)) {
+            if (*(volatile int*)&sm.dead) {
+                ok = false;
+                break;
+            }
             if (clock64() - t0 > limit) {
                 *(volatile int*)&sm.dead = 1;
                 atomicOr(a.error, ERR_TIMEOUT);
-                return false;
+                ok = false;
+                break;
             }
         }
+        return (bool)__all_sync(0xffffffffu, ok);
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, spin(bar, parity)); };  // a whole warp
+    // the shares, as the loader finds them; false at the end
+    uint32_t n_share = 0;
+    auto next_share = [&]() {
+        if (n_share) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.share_free[(n_share - 1) % CK_SHARES]);
+        }
+        const bool ok = wait(&sm.share_full[n_share % CK_SHARES], (n_share / CK_SHARES) & 1) && !sm.share[n_share % CK_SHARES].end;
+        ++n_share;
+        return ok;
+    };
 
     if (group == 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-        if (warp == 16 && lane == 0 && !idle) {
-            // ---- products
-            CkWalk w = start;
-            uint32_t tile0 = 0, steps[2] = {0, 0}, seg = 0;  // tiles before this share, steps of each stream
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 16) {
+            // ---- products: the whole warp goes along, so that descriptors stay in uniform registers; one lane issues
+            uint32_t tile0 = 0, done0 = 0, done1 = 0;  // tiles before this share, weights taken of each stream
             bool ok = true;
-            while (ok && w.next(a)) {
-                const int n = w.to - w.from, two = w.k.rows > CK_TILE;
-                const int ns[2] = {two ? n : (n + 1) / 2, two ? n : n / 2};
-                auto qk = [&](int t, int j) {
+            const bool leader = ck_elect();
+            const uint32_t q_lo = ck_desc_lo(sm.q[0]), k_lo = ck_desc_lo(sm.k[0]), v_lo = ck_desc_lo(sm.v[0]);
+            while (ok && next_share()) {
+                const CkShare& g = sm.share[(n_share - 1) % CK_SHARES];
+                const int n = __shfl_sync(0xffffffffu, g.n, 0), two = __shfl_sync(0xffffffffu, g.two, 0);
+                const int n0 = two ? n : (n + 1) / 2, n1 = two ? n : n / 2;
+                auto qk = [&](int t, int j) {  // (t a constant at each call)
                     const uint32_t x = tile0 + (two ? j : 2 * j + t), st = x & 1;
-                    if (!(ok = ok && spin(&sm.k_full[st], x >> 1 & 1))) return;
+                    if (!(ok = wait(&sm.k_full[st], x >> 1 & 1))) return;
                     ck_fence_after();
-                    const uint64_t qd = ck_desc(sm.q[t]), kd = ck_desc(sm.k[st]);
+                    if (leader) {
+                        const uint32_t qd = q_lo + t * (CK_OPERAND >> 4), kd = k_lo + st * (CK_OPERAND >> 4);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int at = (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4);
-                        ck_mma_ss(tmem + 128 * t, qd + at, kd + at, i > 0);
-                    }
-                    ck_commit(&sm.s_full[t]);
-                    if (!two || t == 1) ck_commit(&sm.k_free[st]);
-                };
-                auto pv = [&](int t, int j) {
-                    const uint32_t x = tile0 + (two ? j : 2 * j + t), st = x & 1;
-                    if (!(ok = ok && spin(&sm.v_full[st], x >> 1 & 1) && spin(&sm.p_full[t], (steps[t] + j) & 1))) return;
-                    ck_fence_after();
-                    const uint64_t vd = ck_desc(sm.v[st]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        ck_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, vd + (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4), j > 0 || i > 0);
-                    if (!two || t == 1) ck_commit(&sm.v_free[st]);
-                    if (j + 1 == ns[t]) ck_commit(&sm.o_full[t]);
-                };
-                for (int t = 0; t < 2; ++t)
-                    if (ok && (ok = spin(&sm.q_full[t], seg & 1)) && ns[t] > 0) qk(t, 0);
-                for (int j = 0; j < ns[0] && ok; ++j)
-                    for (int t = 0; t < 2 && ok; ++t)
-                        if (j < ns[t]) {
-                            pv(t, j);
-                            if (ok && j + 1 < ns[t]) qk(t, j + 1);
+                        for (int i = 0; i < 8; ++i) {
+                            const int at = (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4);
+                            ck_mma_ss(tmem + 128 * t, qd + at, kd + at, i > 0);
                         }
+                        ck_commit(&sm.s_full[t]);
+                        if (!two || t == 1) ck_commit(&sm.k_free[st]);
+                    }
+                    __syncwarp();
+                };
+                auto pv = [&](int t, int j, bool last) {
+                    const uint32_t x = tile0 + (two ? j : 2 * j + t), st = x & 1;
+                    uint32_t& done = t ? done1 : done0;
+                    if (!(ok = wait(&sm.v_full[st], x >> 1 & 1) && wait(&sm.p_full[t], done & 1))) return;
+                    ++done;
+                    ck_fence_after();
+                    if (leader) {
+                        const uint32_t vd = v_lo + st * (CK_OPERAND >> 4);
+                        ck_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t, vd, j > 0);
+#pragma unroll
+                        for (int i = 1; i < 8; ++i)
+                            ck_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, vd + (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4), true);
+                        if (!two || t == 1) ck_commit(&sm.v_free[st]);
+                        if (last) ck_commit(&sm.o_full[t]);
+                    }
+                    __syncwarp();
+                };
+                ok = wait(&sm.q_full[0], (n_share - 1) & 1);
+                if (ok) qk(0, 0);
+                if (ok) ok = wait(&sm.q_full[1], (n_share - 1) & 1);
+                if (ok && n1 > 0) qk(1, 0);
+                for (int j = 0; j < n0 && ok; ++j) {
+                    pv(0, j, j + 1 == n0);
+                    if (ok && j + 1 < n0) qk(0, j + 1);
+                    if (ok && j < n1) pv(1, j, j + 1 == n1);
+                    if (ok && j + 1 < n1) qk(1, j + 1);
+                }
                 tile0 += n;
-                steps[0] += ns[0];
-                steps[1] += ns[1];
-                ++seg;
             }
             // everything issued is done before TMEM is freed
-            ck_commit(&sm.drained);
-            (void)mbar_wait_bounded(&sm.drained, 0, 100000000LL);
-        } else if (warp == 17 && !idle) {
-            // ---- pages
-            CkWalk w = start;
+            if (leader) {
+                ck_commit(&sm.drained);
+                (void)mbar_wait_bounded(&sm.drained, 0, 100000000LL);
+            }
+        } else if (warp == 17) {
+            // ---- shares and pages
+            const int C = __ldcg(&a.plan->ctas), cta = blockIdx.x, n_blocks = __ldcg(&a.plan->blocks);
+            const int64_t total = __ldcg(&a.plan->total);
+            CkWalk w;
+            w.pos = w.end = 0;
+            w.e = w.h = 0;
+            if (cta < C) {  // the block that holds pos: 33 cuts of the range at a time
+                w.pos = ck_cut(total, cta, C);
+                w.end = ck_cut(total, cta + 1, C);
+                int lo = 0, hi = n_blocks;  // start[lo] * H <= pos, start[hi] * H > pos
+                while (hi - lo > 1) {
+                    const int step = (hi - lo + 32) / 33, x = lo + (lane + 1) * step;
+                    const bool below = x < hi && __ldcg(&a.block[x].start) * a.H_kv <= w.pos;
+                    const int n = __popc(__ballot_sync(0xffffffffu, below));
+                    hi = min(hi, lo + (n + 1) * step);
+                    lo += n * step;
+                }
+                // (of blocks with one start only the last costs anything, and the search ends there)
+                w.e = lo;
+                w.h = (int)((w.pos - __ldcg(&a.block[lo].start) * a.H_kv) / max(1, __ldcg(&a.block[lo].cost)));
+            }
             uint32_t stage = 0;
             bool ok = true;
-            while (ok && w.next(a)) {
+            for (uint32_t x = 0; ok; ++x) {
+                const bool have = w.next(a);
+                if (x >= CK_SHARES && !(ok = wait(&sm.share_free[x % CK_SHARES], (x / CK_SHARES - 1) & 1))) break;
+                if (lane == 0) {
+                    CkShare& g = sm.share[x % CK_SHARES];
+                    g.end = !have;
+                    if (have) {
+                        g.n = w.to - w.from;
+                        g.two = w.k.rows > CK_TILE;
+                        g.from = w.from;
+                        g.rows = w.k.rows;
+                        g.r0 = w.k.r0;
+                        g.pos0 = w.k.ctx - w.k.n;
+                        g.ctx = w.k.ctx;
+                        g.b = w.k.b;
+                        g.h = w.last_h;
+                        g.row0 = (int64_t)w.k.q0 * a.G;
+                        for (int t = 0; t < 2; ++t) {
+                            const int r0 = w.k.r0 + (g.two ? CK_TILE * t : 0), r1 = min(w.k.r0 + w.k.rows, r0 + CK_TILE) - 1;
+                            g.first[t] = g.pos0 + r0 / a.G;
+                            g.last[t] = g.pos0 + r1 / a.G;
+                        }
+                    }
+                    mbar_arrive(&sm.share_full[x % CK_SHARES]);
+                }
+                __syncwarp();
+                if (!have) break;
                 const int p1 = min(w.k.pages, 8 * w.to), n = 2 * (w.to - w.from);
                 const int32_t* table = a.block_table + (size_t)w.k.b * a.max_pages;
                 auto ids = [&](int p0) {
@@ -558,7 +649,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     return p < p1 ? __ldg(table + p + (p < w.k.sinks ? 0 : w.k.skip)) : 0;
                 };
                 int id = ids(8 * w.from), next_id = 0;
-                for (int s = 0; s < n && ok; ++s, ++stage) {
+                for (int s = 0; s < n; ++s, ++stage) {
                     if ((s & 7) == 0) {
                         if (s) id = next_id;
                         next_id = ids(8 * w.from + 4 * s + 32);
@@ -583,14 +674,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
     } else if (group == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         // ---- keys: a thread takes a token's words t of all groups, twice a stage
-        CkWalk w = start;
         uint32_t tile = 0;
-        bool ok = !idle;
-        const int t = lane & 3, tok0 = 8 * (warp & 3) + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
-        while (ok && w.next(a))
-            for (int i = w.from; i < w.to && ok; ++i, ++tile) {
+        bool ok = true;
+        const int t = lane & 3, wk = warp & 3, tok0 = 8 * wk + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
+        while (ok && next_share()) {
+            const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
+            for (int i = share.n; i > 0 && ok; --i, ++tile) {
                 const uint32_t st = tile & 1;
                 if (tile >= 2 && !(ok = wait(&sm.k_free[st], (tile / 2 - 1) & 1))) break;
+                CkInfo& info = sm.info[tile % CK_INFOS];
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const uint32_t raw = 2 * tile + half, slot = raw % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], (raw / CK_RAW_STAGES) & 1))) break;
@@ -615,6 +708,28 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             *reinterpret_cast<uint4*>(out + (g >> 1) * CK_HALF + (((4 * (g & 1) + t) ^ (row & 7)) << 4)) = x;
                         }
                     }
+                    {   // values that are not finite: a warp looks at its page's scales and mins, a slot pair of either a lane
+                        const uint4 y = lds128(sm.raw[slot] + wk * INT4_TILE + O4_VS + 16 * (lane & 15));
+                        const __half2 top = __hmax2_nan(__hmax2_nan(__habs2(u32_as_h2(y.x)), __habs2(u32_as_h2(y.y))),
+                                                        __hmax2_nan(__habs2(u32_as_h2(y.z)), __habs2(u32_as_h2(y.w))));
+                        uint32_t bad = (__half2float(__low2half(top)) < CUDART_INF_F ? 0u : 1u) | (__half2float(__high2half(top)) < CUDART_INF_F ? 0u : 2u);
+                        if (__any_sync(0xffffffffu, bad)) {
+                            bad <<= 2 * (lane & 7);
+#pragma unroll
+                            for (int o = 8; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+                        }
+                        if (lane == 0) info.poison[half][wk] = sm.raw_base[slot][wk] < 0 ? 0u : bad;
+                    }
+                    if (wk == 0) {
+                        const int at = sm.raw_base[slot][lane & 3];
+                        bool part[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            part[x] = at < 0 || at + PAGE - 1 > share.first[x] || (a.window && at <= share.last[x] - a.window && at + PAGE > a.sinks);
+                        const uint32_t s0 = __any_sync(0xffffffffu, part[0]), s1 = __any_sync(0xffffffffu, part[1]);
+                        if (lane < 4) info.base[half][lane] = at;
+                        if (lane == 0) info.special[half] = s0 | s1 << 1;
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -623,48 +738,39 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     }
                 }
             }
+        }
     } else if (group == 3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         // ---- values: a thread takes the words r of eight tokens and two groups
-        CkWalk w = start;
         uint32_t tile = 0;
-        bool ok = !idle;
-        const int wg = warp & 3, r = lane & 7, oct = 4 * (wg & 1) + (lane >> 3), g0 = 2 * (wg >> 1);
-        while (ok && w.next(a)) {
-            // positions of the streams' first and last rows
-            int first[2], last[2];
-            for (int t = 0; t < 2; ++t) {
-                const int r0 = w.k.r0 + (w.k.rows > CK_TILE ? CK_TILE * t : 0), r1 = min(w.k.r0 + w.k.rows, r0 + CK_TILE) - 1;
-                first[t] = w.k.ctx - w.k.n + r0 / a.G;
-                last[t] = w.k.ctx - w.k.n + r1 / a.G;
-            }
-            for (int i = w.from; i < w.to && ok; ++i, ++tile) {
+        bool ok = true;
+        const int wg = warp & 3, r = lane & 7, oct = 4 * (wg & 1) + (lane >> 3), g0 = 2 * (wg >> 1), pair0 = 4 * (oct & 1);
+        while (ok && next_share()) {
+            const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
+            for (int i = share.n; i > 0 && ok; --i, ++tile) {
                 const uint32_t st = tile & 1;
                 if (tile >= 2 && !(ok = wait(&sm.v_free[st], (tile / 2 - 1) & 1))) break;
-                CkInfo& info = sm.info[st];
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const uint32_t raw = 2 * tile + half, slot = raw % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], (raw / CK_RAW_STAGES) & 1))) break;
                     const uint8_t* page = sm.raw[slot] + (oct >> 1) * INT4_TILE;
-                    const int base = sm.raw_base[slot][oct >> 1], pair0 = 4 * (oct & 1);
+                    const int base = sm.raw_base[slot][oct >> 1];
                     // tokens of the octet within the context, none without a page
-                    const int valid = base < 0 ? 0 : min(8, max(0, w.k.ctx - base - 2 * pair0));
+                    const int valid = base < 0 ? 0 : min(8, max(0, share.ctx - base - 2 * pair0));
                     uint2 code[4], sc[4], mn[4];
-                    __half2 most = u32_as_h2(0u);
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         code[p] = lds64(page + O4_VC + 128 * (pair0 + p) + 16 * r + 4 * g0);
                         sc[p] = lds64(page + O4_VS + 16 * (pair0 + p) + 4 * g0);
                         mn[p] = lds64(page + O4_VM + 16 * (pair0 + p) + 4 * g0);
                     }
-                    {   // a lane looks at one pair's two groups of scales or mins: those from 2^11 or 2^15 up, and NaN, take the long way
-                        const uint2 look = lds64(page + (r & 4 ? O4_VM : O4_VS) + 16 * (pair0 + (r & 3)) + 4 * g0);
-                        most = __hmax2_nan(__habs2(u32_as_h2(look.x)), __habs2(u32_as_h2(look.y)));
-                    }
+                    // a lane looks at one pair's two groups of scales or mins: those from 2^11 or 2^15 up, and NaN, take the long way
+                    const uint2 look = lds64(page + (r & 4 ? O4_VM : O4_VS) + 16 * (pair0 + (r & 3)) + 4 * g0);
+                    const __half2 most = __hmax2_nan(__habs2(u32_as_h2(look.x)), __habs2(u32_as_h2(look.y)));
                     const float edge = r & 4 ? 32768.f : 2048.f;
                     const bool plain = valid == 8 && __low2float(most) < edge && __high2float(most) < edge;
-                    uint32_t poison = 0u;
-                    uint8_t* out = sm.v[st] + half * CK_HALF + r * 128 + ((oct ^ r) << 4);
+                    uint8_t* out = sm.v[st] + half * CK_HALF + r * 128 + ((oct ^ r) << 4) + 32 * g0 * 128;
                     if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
@@ -679,23 +785,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             }
 #pragma unroll
                             for (int n = 0; n < 4; ++n)
-                                *reinterpret_cast<uint4*>(out + (32 * (g0 + g) + 8 * n) * 128) = make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
+                                *reinterpret_cast<uint4*>(out + (32 * g + 8 * n) * 128) = make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
                         }
                     } else {
                         // in fp32, cut off at fp16's ends; tokens past the context are 0, and so are those that hold what is not
                         // finite, whose logits the softmax makes NaN instead (a weight of 0 would not hide it from other rows)
-                        uint32_t bad = 0u;  // of the octet's tokens
-#pragma unroll
-                        for (int p = 0; p < 4; ++p)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float2 s0 = __half22float2(u32_as_h2(sc[p].x)), s1 = __half22float2(u32_as_h2(sc[p].y));
-                                const float2 m0 = __half22float2(u32_as_h2(mn[p].x)), m1 = __half22float2(u32_as_h2(mn[p].y));
-                                const float all = e ? (s0.y - s0.y) + (s1.y - s1.y) + (m0.y - m0.y) + (m1.y - m1.y)
-                                                    : (s0.x - s0.x) + (s1.x - s1.x) + (m0.x - m0.x) + (m1.x - m1.x);
-                                if (all != 0.f && 2 * p + e < valid) bad |= 1u << (2 * p + e);
-                            }
-                        const uint32_t keep = (1u << valid) - 1u & ~bad;
 #pragma unroll 1
                         for (int x = 0; x < 8; ++x) {
                             const int g = x >> 2, n = x & 3;
@@ -704,25 +798,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             for (int p = 0; p < 4; ++p) {
                                 const uint32_t c = (g ? code[p].y : code[p].x) >> (4 * n);
                                 const float2 s = __half22float2(u32_as_h2(g ? sc[p].y : sc[p].x)), m = __half22float2(u32_as_h2(g ? mn[p].y : mn[p].x));
-                                const float lo = fminf(fmaxf(fmaf((float)(c & 15), s.x, m.x), -65504.f), 65504.f);
-                                const float hi = fminf(fmaxf(fmaf((float)(c >> 16 & 15), s.y, m.y), -65504.f), 65504.f);
-                                y[p] = pack_half2(keep >> (2 * p) & 1 ? lo : 0.f, keep >> (2 * p + 1) & 1 ? hi : 0.f);
+                                const float lo = fmaf((float)(c & 15), s.x, m.x), hi = fmaf((float)(c >> 16 & 15), s.y, m.y);
+                                const bool lo_ok = 2 * p < valid && isfinite(s.x) && isfinite(m.x), hi_ok = 2 * p + 1 < valid && isfinite(s.y) && isfinite(m.y);
+                                y[p] = pack_half2(lo_ok ? fminf(fmaxf(lo, -65504.f), 65504.f) : 0.f, hi_ok ? fminf(fmaxf(hi, -65504.f), 65504.f) : 0.f);
                             }
-                            *reinterpret_cast<uint4*>(out + (32 * (g0 + g) + 8 * n) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(out + (32 * g + 8 * n) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
-                        poison = bad << (8 * (lane >> 3));
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) poison |= __shfl_xor_sync(0xffffffffu, poison, o);
-                    }
-                    if (lane == 0) info.poison[half][wg] = poison;
-                    if (wg == 0) {
-                        const int at = sm.raw_base[slot][lane & 3];
-                        bool part[2];
-                        for (int t = 0; t < 2; ++t)
-                            part[t] = at < 0 || at + PAGE - 1 > first[t] || (a.window && at <= last[t] - a.window && at + PAGE > a.sinks);
-                        const uint32_t s0 = __any_sync(0xffffffffu, part[0]), s1 = __any_sync(0xffffffffu, part[1]);
-                        if (lane < 4) info.base[half][lane] = at;
-                        if (lane == 0) info.special[half] = s0 | s1 << 1;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -734,22 +815,20 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         // ---- softmax of stream t: a thread a row
-        CkWalk w = start;
         const int t = group, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
         uint32_t tile0 = 0, step = 0, parts = 0;
-        bool ok = !idle;
-        while (ok && w.next(a)) {
-            const int two = w.k.rows > CK_TILE, n = w.to - w.from, ns = two ? n : (n + 1 - t) / 2;
+        bool ok = true;
+        while (ok && next_share()) {
+            const CkShare& g = sm.share[(n_share - 1) % CK_SHARES];
+            const int two = g.two, n = g.n, ns = two ? n : (n + 1 - t) / 2;
             const int in_block = (two ? CK_TILE * t : 0) + row;
-            const bool live = in_block < w.k.rows;
-            const int in_seq = w.k.r0 + (live ? in_block : 0);
-            const int64_t grow = (int64_t)w.k.q0 * a.G + in_seq;                       // of all rows
-            const int64_t at = (int64_t)w.last_h * a.n_tok * a.G + grow;
-            const int pos = w.k.ctx - w.k.n + in_seq / a.G;
-            {   // the row's queries (the stream's last product with the ones before is done: its logits were read)
+            const bool live = in_block < g.rows;
+            const int in_seq = g.r0 + (live ? in_block : 0), pos = g.pos0 + in_seq / a.G;
+            const int64_t at = (int64_t)g.h * a.n_tok * a.G + g.row0 + in_seq;  // the row among all
+            {   // the row's queries (the stream's last product with the ones before is done: its sums were read)
                 const uint4* src = reinterpret_cast<const uint4*>(a.rot + at * D);
                 uint8_t* dst = sm.q[t] + row * 128;
 #pragma unroll
@@ -761,79 +840,87 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             }
             const float f = __ldcg(a.row_scale + at);
             float ref = CK_NEG, l = 0.f;
-            for (int j = 0; j < ns && ok; ++j, ++step) {
-                const uint32_t tile = tile0 + (two ? j : 2 * j + t), st = tile & 1;
-                if (!(ok = wait(&sm.v_full[st], tile >> 1 & 1) && wait(&sm.s_full[t], step & 1))) break;
+            for (int j = 0; j < ns; ++j, ++step) {
+                if (!(ok = wait(&sm.s_full[t], step & 1))) break;
                 ck_fence_after();
-                uint32_t s[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) ck_tmem_ld32(s + 32 * c, s_at + 32 * c);
-                const CkInfo& info = sm.info[st];
+                const CkInfo& info = sm.info[(tile0 + (two ? j : 2 * j + t)) % CK_INFOS];
                 const uint4 pa = lds128(info.poison[0]), pb = lds128(info.poison[1]);
-                const uint32_t poisoned = pa.x | pa.y | pa.z | pa.w | pb.x | pb.y | pb.z | pb.w;
-                const bool special = ((info.special[0] | info.special[1]) >> t & 1) || poisoned;
-                ck_loaded(s);
-                if (special) {
+                const bool special = ((info.special[0] | info.special[1]) >> t & 1) | ((pa.x | pa.y | pa.z | pa.w | pb.x | pb.y | pb.z | pb.w) != 0);
+                // 32 tokens, two pages: what the row does not see is -inf, what is not finite NaN
+                auto mask = [&](uint32_t (&s)[32], int c) {
 #pragma unroll
-                    for (int pg = 0; pg < 8; ++pg) {
-                        const int base = info.base[pg >> 2][pg & 3];
+                    for (int pg = 0; pg < 2; ++pg) {
+                        const int base = info.base[c >> 1][2 * (c & 1) + pg];
                         uint32_t see = base < 0 ? 0u : (1u << min(PAGE, max(0, pos - base + 1))) - 1u;
                         if (a.window) {
                             const int low = min(PAGE, max(0, pos - a.window + 1 - base)), sink = min(PAGE, max(0, a.sinks - base));
                             see &= ~((1u << low) - 1u) | ((1u << sink) - 1u);
                         }
-                        const uint32_t w0 = info.poison[pg >> 2][pg >> 1 & 1] | info.poison[pg >> 2][2 + (pg >> 1 & 1)];
-                        const uint32_t bad = w0 >> (16 * (pg & 1));
+                        const uint32_t bad = info.poison[c >> 1][2 * (c & 1) + pg];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            if (bad >> c & 1) s[16 * pg + c] = 0x7fffffffu;
-                            if (!(see >> c & 1)) s[16 * pg + c] = 0xff800000u;
+                        for (int i = 0; i < 16; ++i) {
+                            if (bad >> i & 1) s[16 * pg + i] = 0x7fffffffu;
+                            if (!(see >> i & 1)) s[16 * pg + i] = 0xff800000u;
                         }
                     }
-                }
-                float m0 = __uint_as_float(s[0]), m1 = __uint_as_float(s[1]);
-#pragma unroll
-                for (int c = 2; c < 126; c += 4) {
-                    m0 = fmaxf(fmaxf(m0, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
-                    m1 = fmaxf(fmaxf(m1, __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
-                }
-                const float top = fmaxf(fmaxf(m0, m1), fmaxf(__uint_as_float(s[126]), __uint_as_float(s[127]))) * f;
-                if (__any_sync(0xffffffffu, top > ref + CK_STALE)) {
-                    const float up = top > ref + CK_STALE ? ceilf(top) : ref, c0 = ck_ex2(ref - up);
-                    ref = up;
-                    l *= c0;
-                    if (j > 0) {
+                };
+                bool raise = j == 0;
+                uint32_t p[64];
+                float total;
+                while (true) {
+                    if (raise) {  // the row's largest logit, and its reference up to it
+                        float top = -CUDART_INF_F;
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            uint32_t o[16];
-                            asm volatile(
-                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                                : CK_R8(o, 0), CK_R8(o, 8)
-                                : "r"(o_at + 16 * c)
-                                : "memory");
-                            ck_loaded(o);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t s[32];
+                            ck_tmem_ld32(s, s_at + 32 * c);
+                            ck_loaded(s);
+                            if (special) mask(s, c);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c0);
-                            asm volatile(
-                                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::CK_W8(o, 0),
-                                CK_W8(o, 8), "r"(o_at + 16 * c)
-                                : "memory");
+                            for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+                        }
+                        top *= f;
+                        const float up = top > ref ? ceilf(top) : ref, c0 = ck_ex2(ref - up);
+                        ref = up;
+                        l *= c0;
+                        if (j > 0) {
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t o[32];
+                                ck_tmem_ld32(o, o_at + 32 * c);
+                                ck_loaded(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c0);
+                                ck_tmem_st32(o, o_at + 32 * c);
+                            }
                         }
                     }
-                }
-                const float2 f2 = make_float2(f, f), off = make_float2(CK_LIFT - ref, CK_LIFT - ref);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float2 f2 = make_float2(f, f), off = make_float2(CK_LIFT - ref, CK_LIFT - ref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t s[2][32];
+                    ck_tmem_ld32(s[0], s_at);
 #pragma unroll
-                for (int c = 0; c < 64; ++c) {
-                    float2 x = ck_fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), f2, off);
-                    x = make_float2(ck_ex2(x.x), ck_ex2(x.y));
-                    sum[c & 1] = ck_add2(sum[c & 1], x);
-                    s[c] = pack_half2(x.x, x.y);
-                    if (c == 31) ck_tmem_st32(s, s_at);
+                    for (int c = 0; c < 4; ++c) {
+                        ck_loaded(s[c & 1]);
+                        if (c < 3) ck_tmem_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));
+                        if (special) mask(s[c & 1], c);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = ck_fma2(make_float2(__uint_as_float(s[c & 1][2 * i]), __uint_as_float(s[c & 1][2 * i + 1])), f2, off);
+                            x = make_float2(ck_ex2(x.x), ck_ex2(x.y));
+                            sum[i & 1] = ck_add2(sum[i & 1], x);
+                            p[16 * c + i] = pack_half2(x.x, x.y);
+                        }
+                    }
+                    sum[0] = ck_add2(sum[0], sum[1]);
+                    total = sum[0].x + sum[0].y;
+                    // (a sum that fp16 holds is one of weights that it holds)
+                    if (raise || !__any_sync(0xffffffffu, total > 65504.f)) break;
+                    raise = true;
                 }
-                ck_tmem_st32(s + 32, s_at + 32);
-                sum[0] = ck_add2(sum[0], sum[1]);
-                l += sum[0].x + sum[0].y;
+                l += total;
+                ck_tmem_st32(p, s_at);
+                ck_tmem_st32(p + 32, s_at + 32);
                 ck_wait_st();
                 ck_fence_before();
                 __syncwarp();
@@ -844,12 +931,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 if (!(ok = wait(&sm.o_full[t], parts & 1))) break;
                 ++parts;
                 ck_fence_after();
-                float* out = w.from > 0   ? a.extra + ((size_t)cta * CK_ROWS + CK_TILE * t + row) * PART_STRIDE
-                             : two || !t  ? a.main + at * PART_STRIDE
-                             : a.second_rows ? a.second + (((int64_t)w.k.b * a.H_kv + w.last_h) * a.second_rows + row) * PART_STRIDE
+                float* out = g.from > 0      ? a.extra + ((size_t)blockIdx.x * CK_ROWS + CK_TILE * t + row) * PART_STRIDE
+                             : two || !t     ? a.main + at * PART_STRIDE
+                             : a.second_rows ? a.second + (((int64_t)g.b * a.H_kv + g.h) * a.second_rows + row) * PART_STRIDE
                                              : a.second + at * PART_STRIDE;
                 if (live) *reinterpret_cast<float2*>(out) = make_float2(ref - CK_LIFT, l);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
                     ck_tmem_ld32(o, o_at + 32 * c);
@@ -867,7 +954,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
     __syncwarp();
     ck_fence_before();
     __syncthreads();
-    if (sm.dead && warp == 17 && !idle)  // copies in flight land before the block ends
+    if (sm.dead && warp == 17)  // copies in flight land before the block ends
         for (uint32_t n = sm.stages, s = n > CK_RAW_STAGES ? n - CK_RAW_STAGES : 0; s < n; ++s)
             (void)mbar_wait_bounded(&sm.raw_full[s % CK_RAW_STAGES], (s / CK_RAW_STAGES) & 1, 1000000LL);
     if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -875,101 +962,138 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
 
 // ------------------------------------------------------------------ 3: finish
 
-// CTAs of 256 threads per (row tile, KV head): the rows' partials merged (a warp 16 rows, a lane
-// four channels), normalised, rotated by R_v^T.
-struct __align__(16) CkFinish {
-    CkMatrix R;
-    __align__(16) __nv_bfloat16 o[2][CK_TILE][D + 8];  // high and low parts
-};
-__global__ void __launch_bounds__(256) chunk_finish_kernel(const __grid_constant__ ChunkArgs a) {
+// CTAs of 256 threads take row tiles of a KV head, a warp 16 rows: their partials are merged in the layout of the A
+// operand (a lane has eight times four values of two rows), normalised and rotated by R_v^T.
+__global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    CkFinish& sm = *reinterpret_cast<CkFinish*>(smem_raw);
+    CkMatrix& R = *reinterpret_cast<CkMatrix*>(smem_raw);
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    // B: k = position of the unpacked values, n = output channel.  Positions 32 g + 8 i + 2 t and + 1 are channels
+    // 32 g + 8 t + i and + 4; the next eight positions those after them.  (Read before the wait: the kernel that started
+    // this one did so after its own.)
     const float* Rv = a.Rv + (size_t)h * D * D;
+#pragma unroll 4
+    for (int y = threadIdx.x; y < D * 4 * 4; y += 256) {
+        const int tt = y & 3, g = (y >> 2) & 3, n = y >> 4;
+        const float4* p = reinterpret_cast<const float4*>(Rv + (size_t)n * D + 32 * g + 8 * tt);
+        const float4 u = __ldg(p), v = __ldg(p + 1);
+        uint4 f;
+        ck_parts(u.x, v.x, f.x, f.z);
+        ck_parts(u.y, v.y, f.y, f.w);
+        R.f[2 * g][n >> 3][4 * (n & 7) + tt] = f;
+        ck_parts(u.z, v.z, f.x, f.z);
+        ck_parts(u.w, v.w, f.y, f.w);
+        R.f[2 * g + 1][n >> 3][4 * (n & 7) + tt] = f;
+    }
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
     const int C = __ldcg(&a.plan->ctas), n_blocks = __ldcg(&a.plan->blocks);
     const int64_t total = __ldcg(&a.plan->total);
-    bool staged = false;
-    for (int x = blockIdx.x; x < 2 * n_blocks; x += gridDim.x) {
+    // a warp at a time, its 16 rows of row tile x / 8
+    for (int x = blockIdx.x * 8 + warp; x < 16 * n_blocks; x += gridDim.x * 8) {
         CkWalk w;
-        w.e = x >> 1;
+        w.e = x >> 4;
         w.read(a);
-        const int tile = x & 1, r0 = CK_TILE * tile, two = w.k.rows > CK_TILE;
-        if (r0 >= w.k.rows) continue;
-        if (!staged) {
-            // B: k = position of the unpacked values, n = output channel
-            ck_stage_matrix(sm.R, [&](int k, int n) { return __ldg(Rv + (size_t)n * D + ck_value_channel(k)); });
-            staged = true;
-        }
-        __syncthreads();
-        const int rows = min(CK_TILE, w.k.rows - r0), wt = ck_weight(w.k.rows);
+        const int two = w.k.rows > CK_TILE, i0 = 16 * (x & 15);  // in the block
+        if (i0 >= w.k.rows) continue;
+        const int wt = ck_weight(w.k.rows);
         const int64_t unit = w.k.start * a.H_kv + (int64_t)h * w.k.cost;
-        const int c0 = w.k.tiles ? (int)(((unit + 1) * C - 1) / total) : 0, c1 = w.k.tiles ? (int)(((unit + (int64_t)wt * (w.k.tiles - 1) + 1) * C - 1) / total) : -1;
-        for (int i = warp; i < CK_TILE; i += 8) {
-            float M = CK_NEG, L = 0.f;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < rows) {
-                const int64_t at = (int64_t)h * a.n_tok * a.G + (int64_t)w.k.q0 * a.G + w.k.r0 + r0 + i;
-                auto merge = [&](const float* p) {
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
-                    const float4 o = __ldcg(reinterpret_cast<const float4*>(p + 4 + 4 * lane));
-                    const float top = fmaxf(M, ml.x), f = ck_ex2(M - top), g = ck_ex2(ml.x - top);
-                    L = fmaf(L, f, ml.y * g);
-                    O = make_float4(fmaf(O.x, f, o.x * g), fmaf(O.y, f, o.y * g), fmaf(O.z, f, o.z * g), fmaf(O.w, f, o.w * g));
-                    M = top;
-                };
-                for (int c = c0; c <= c1; ++c) {
-                    const int64_t b0 = max(ck_cut(total, c, C), unit), b1 = min(ck_cut(total, c + 1, C), unit + w.k.cost);
-                    const int from = (int)((b0 - unit + wt - 1) / wt), n = min(w.k.tiles, (int)((b1 - unit + wt - 1) / wt)) - from;
-                    if (n <= 0) continue;
-                    const float* e = a.extra + ((size_t)c * CK_ROWS + (two ? r0 : 0) + i) * PART_STRIDE;
-                    merge(from > 0 ? e : a.main + at * PART_STRIDE);
-                    if (!two && n > 1)
-                        merge(from > 0         ? e + (size_t)CK_TILE * PART_STRIDE
-                              : a.second_rows ? a.second + (((int64_t)w.k.b * a.H_kv + h) * a.second_rows + i) * PART_STRIDE
-                                              : a.second + at * PART_STRIDE);
-                }
-            }
-            const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);  // no token: 0; NaN stays NaN
-            uint2 hi, lo;
-            ck_parts(O.x * inv, O.y * inv, hi.x, lo.x);
-            ck_parts(O.z * inv, O.w * inv, hi.y, lo.y);
-            *reinterpret_cast<uint2*>(&sm.o[0][i][4 * lane]) = hi;
-            *reinterpret_cast<uint2*>(&sm.o[1][i][4 * lane]) = lo;
-        }
-        __syncthreads();
-        if (16 * warp < rows) {
-            uint32_t hi[8][4], lo[8][4];
+        const int c0 = w.k.tiles ? (int)(((unit + 1) * C - 1) / total) : 0;
+        const int c1 = w.k.tiles ? (int)(((unit + (int64_t)wt * (w.k.tiles - 1) + 1) * C - 1) / total) : -1;
+        float M[2] = {CK_NEG, CK_NEG}, L[2] = {0.f, 0.f};
+        float2 o[8][4];  // [K step][row, + 8; the next eight positions]
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[ks][e] = make_float2(0.f, 0.f);
+        const int ra = min(i0 + r, w.k.rows - 1), rb = min(i0 + r + 8, w.k.rows - 1);  // in the block
+        const int64_t at = (int64_t)h * a.n_tok * a.G + (int64_t)w.k.q0 * a.G + w.k.r0;
+        auto merge = [&](const float* base) {  // partials of the block's rows from base on
+            const float* p[2] = {base + (int64_t)ra * PART_STRIDE, base + (int64_t)rb * PART_STRIDE};
+            float keep[2], take[2];
+            float2 y[8][4];
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 16 * warp + r + 8 * (e & 1), c = 16 * ks + 8 * (e >> 1) + 2 * t;
-                    hi[ks][e] = *reinterpret_cast<const uint32_t*>(&sm.o[0][i][c]);
-                    lo[ks][e] = *reinterpret_cast<const uint32_t*>(&sm.o[1][i][c]);
-                }
+                for (int e = 0; e < 4; ++e) y[ks][e] = __ldcg(reinterpret_cast<const float2*>(p[e & 1] + 4 + 16 * ks + 8 * (e >> 1) + 2 * t));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p[e]));
+                const float top = fmaxf(M[e], ml.x);
+                keep[e] = ck_ex2(M[e] - top);
+                take[e] = ck_ex2(ml.x - top);
+                L[e] = fmaf(L[e], keep[e], ml.y * take[e]);
+                M[e] = top;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[ks][e] = make_float2(fmaf(o[ks][e].x, keep[e & 1], y[ks][e].x * take[e & 1]), fmaf(o[ks][e].y, keep[e & 1], y[ks][e].y * take[e & 1]));
+        };
 #pragma unroll 1
-            for (int nt = 0; nt < 16; ++nt) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t b0 = max(ck_cut(total, c, C), unit), b1 = min(ck_cut(total, c + 1, C), unit + w.k.cost);
+            const int from = (int)((b0 - unit + wt - 1) / wt), n = min(w.k.tiles, (int)((b1 - unit + wt - 1) / wt)) - from;
+            if (n <= 0) continue;
+            const float* extra = a.extra + (size_t)c * CK_ROWS * PART_STRIDE;
+#pragma unroll 1
+            for (int s = 0; s < (two || n == 1 ? 1 : 2); ++s)  // (one row tile: a second stream, if there was a second tile)
+                merge(from > 0         ? extra + (size_t)s * CK_TILE * PART_STRIDE
+                      : !s            ? a.main + at * PART_STRIDE
+                      : a.second_rows ? a.second + ((int64_t)w.k.b * a.H_kv + h) * a.second_rows * PART_STRIDE
+                                      : a.second + at * PART_STRIDE);
+        }
+        uint32_t hi[8][4], lo[8][4];
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint4 b = sm.R.f[ks][nt][lane];
-                    ck_mma(c, lo[ks], b.x, b.y);
-                    ck_mma(c, hi[ks], b.z, b.w);
-                    ck_mma(c, hi[ks], b.x, b.y);
-                }
+        for (int e = 0; e < 2; ++e) L[e] = L[e] > 0.f ? 1.f / L[e] : (L[e] == L[e] ? 0.f : L[e]);  // no token: 0; NaN stays NaN
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = 16 * warp + r + 8 * e;
-                    if (i >= rows) continue;
-                    const int in_seq = w.k.r0 + r0 + i;
-                    __nv_bfloat16* out = a.out + ((int64_t)(w.k.q0 + in_seq / a.G) * a.H_q + (int64_t)h * a.G + in_seq % a.G) * D;
-                    *reinterpret_cast<uint32_t*>(out + 8 * nt + 2 * t) = ck_pack(c[2 * e], c[2 * e + 1]);
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ck_parts(o[ks][e].x * L[e & 1], o[ks][e].y * L[e & 1], hi[ks][e], lo[ks][e]);
+        __nv_bfloat16* out[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int in_seq = w.k.r0 + (e ? rb : ra);
+            out[e] = a.out + ((int64_t)(w.k.q0 + in_seq / a.G) * a.H_q + (int64_t)h * a.G + in_seq % a.G) * D;
+        }
+#pragma unroll 1
+        for (int nt = 0; nt < 16; nt += 4) {
+            float c[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[j][e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 b = R.f[ks][nt + j][lane];
+                    ck_mma(c[j], lo[ks], b.x, b.y);
+                    ck_mma(c[j], hi[ks], b.z, b.w);
+                    ck_mma(c[j], hi[ks], b.x, b.y);
                 }
+            // a lane's two columns of four sets become eight of one: lane t gets set nt + t
+            uint32_t z[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[e][j] = ck_pack(c[j][2 * e], c[j][2 * e + 1]);
+#pragma unroll
+                for (int k = 1; k < 4; k <<= 1) {  // transpose of the four lanes' four words
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (!(j & k)) {
+                            const uint32_t send = t & k ? z[e][j] : z[e][j | k];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, send, k);
+                            if (t & k) z[e][j] = got;
+                            else z[e][j | k] = got;
+                        }
+                }
+                if (i0 + r + 8 * e < w.k.rows) *reinterpret_cast<uint4*>(out[e] + 8 * (nt + t)) = make_uint4(z[e][0], z[e][1], z[e][2], z[e][3]);
             }
         }
-        __syncthreads();
     }
 }
 
@@ -1029,9 +1153,9 @@ static kvq_status chunk_smem_once() {
     const struct {
         const void* fn;
         size_t bytes;
-    } need[3] = {{(const void*)chunk_rotate_kernel, sizeof(CkMatrix)},
+    } need[3] = {{(const void*)chunk_rotate_kernel, sizeof(CkRotate)},
                  {(const void*)chunk_stream_kernel, sizeof(CkSmem) + 1024},
-                 {(const void*)chunk_finish_kernel, sizeof(CkFinish)}};
+                 {(const void*)chunk_finish_kernel, sizeof(CkMatrix)}};
     for (const auto& x : need) {
         st = kvq_check_cuda(cudaFuncSetAttribute(x.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.bytes),
                             "kvq_chunk_attn_int4 smem attribute");
@@ -1102,12 +1226,12 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int64_t row_tiles = ((int64_t)n_tok * a.G + CK_TILE - 1) / CK_TILE;
     auto capped = [&](int64_t want) { return (unsigned)std::min(want, std::max<int64_t>(1, 4 * a.ctas / H_kv)); };  // CTAs per head
-    st = kvq_check_cuda(launch_pdl(chunk_rotate_kernel, dim3(capped(row_tiles) + 1, H_kv), dim3(256), sizeof(CkMatrix), cs, a),
+    st = kvq_check_cuda(launch_pdl(chunk_rotate_kernel, dim3(capped(row_tiles) + 1, H_kv), dim3(256), sizeof(CkRotate), cs, a),
                         "kvq_chunk_attn_int4 rotate launch");
     if (st != KVQ_OK) return st;
     st = kvq_check_cuda(launch_pdl(chunk_stream_kernel, dim3(a.ctas), dim3(CK_THREADS), sizeof(CkSmem) + 1024, cs, a),
                         "kvq_chunk_attn_int4 launch");
     if (st != KVQ_OK) return st;
-    return kvq_check_cuda(launch_pdl(chunk_finish_kernel, dim3(capped(2 * (int64_t)l.max_blocks), H_kv), dim3(256), sizeof(CkFinish), cs, a),
+    return kvq_check_cuda(launch_pdl(chunk_finish_kernel, dim3(capped(2 * (int64_t)l.max_blocks), H_kv), dim3(256), sizeof(CkMatrix), cs, a),
                           "kvq_chunk_attn_int4 finish launch");
 }
