@@ -20,8 +20,9 @@
 namespace kvq {
 
 constexpr int CK_ROWS = 256;       // rows of a block: two row tiles of 128
-constexpr int CK_TILE = 128;       // cached tokens of a tile: eight pages
-constexpr int CK_UNIT_COST = 6;    // what starting a block costs, in tiles of one row tile
+constexpr int CK_ROW_TILE = 128;
+constexpr int CK_PAGES = 4, CK_TILE = CK_PAGES * PAGE;  // pages and cached tokens of a tile
+constexpr int CK_UNIT_COST = 24;   // what starting a block costs, in tiles of one row tile
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 constexpr float CK_LIFT = 7.f;     // weights are carried 2^7 times as large: they use fp16 from 2^15 down
 constexpr long long CK_SHORT_WAIT_CYCLES = 2000000LL;
@@ -57,6 +58,7 @@ struct ChunkArgs {
     __nv_bfloat16* out;
     uint32_t* error;
     CkPlan* plan;
+    int64_t* cut;         // [ctas + 1]: where the cost of all heads is cut into shares
     CkBlock* block;       // [max_blocks]
     int max_blocks;
     __half* rot;          // q' [H_kv][n_tok * G][D], channels in the order of the unpacked keys
@@ -82,7 +84,7 @@ __device__ __forceinline__ int2 ck_tokens(const ChunkArgs& a, int b) {
 }
 __device__ __forceinline__ int ck_blocks(int n, int G) { return (int)(((int64_t)n * G + CK_ROWS - 1) / CK_ROWS); }
 
-__device__ __forceinline__ int ck_weight(int rows) { return rows > CK_TILE ? 2 : 1; }
+__device__ __forceinline__ int ck_weight(int rows) { return rows > CK_ROW_TILE ? 2 : 1; }
 
 template <typename T>
 __device__ __forceinline__ T ck_scan(T own, T* warp_sums, T& total) {  // exclusive, over the CTA's 256 threads
@@ -144,7 +146,7 @@ __device__ void ck_make_plan(const ChunkArgs& a) {
                 k.sinks = min(fp, (min(a.sinks, last + 1) + PAGE - 1) / PAGE);
                 k.skip = fp - k.sinks;
                 k.pages = last / PAGE + 1 - k.skip;
-                k.tiles = (k.pages + CK_TILE / PAGE - 1) / (CK_TILE / PAGE);
+                k.tiles = (k.pages + CK_PAGES - 1) / CK_PAGES;
                 k.cost = ck_weight(k.rows) * k.tiles + CK_UNIT_COST;
             }
         }
@@ -153,10 +155,12 @@ __device__ void ck_make_plan(const ChunkArgs& a) {
         if (e < n_blocks) a.block[e] = k;
         base += total;
     }
+    const int64_t total = base * a.H_kv, C = min((int64_t)a.ctas, total);
+    for (int c = tid; c <= C; c += 256) a.cut[c] = C ? c * total / C : 0;
     if (tid == 0) {
         a.plan->blocks = n_blocks;
-        a.plan->total = base * a.H_kv;
-        a.plan->ctas = (int)min((int64_t)a.ctas, base * a.H_kv);
+        a.plan->total = total;
+        a.plan->ctas = (int)C;
     }
 }
 
@@ -196,30 +200,21 @@ struct CkWalk {
     int last_h;  // head of the share that next() found
 };
 
-// Where the cost axis is cut for CTA c of C.
-__device__ __forceinline__ int64_t ck_cut(int64_t total, int c, int C) { return (int64_t)c * total / C; }
-
 // ------------------------------------------------------------------ 1: rotate
 
-__device__ __forceinline__ void ck_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+// The rotations take one fp16 product each: a rotation's entries, the queries (8 bits of their own) and the outputs, each
+// row brought to a power of two by its largest value, keep 11 bits, as do the rotated queries in any case, and an output
+// is rounded to 8.  (With both factors in parts, three products, a prompt of 4K tokens and 32 heads took 57 us to finish.)
 __device__ __forceinline__ uint32_t ck_pack(float lo, float hi) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&x);
 }
-// Two values' bf16 parts: what rounds, and what that leaves.
-__device__ __forceinline__ void ck_parts(float x, float y, uint32_t& hi, uint32_t& lo) {
-    hi = ck_pack(x, y);
-    lo = ck_pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-}
+// Power of two that brings x into [2^7, 2^8) (1 for 0 and what is not finite).
+__device__ __forceinline__ float ck_scale(float x) { return x > 0.f && x < CUDART_INF_F ? ldexpf(1.f, max(-100, min(100, 7 - ilogbf(x)))) : 1.f; }
 
-// A matrix as the B operand of m16n8k16, in two bf16 parts: [K step][8 columns][lane] of (b0, b1) of the high part, then
-// of the low one.
+// A matrix as the B operand of m16n8k16: [K step][8 columns][lane].
 struct __align__(16) CkMatrix {
-    uint4 f[8][16][32];
+    uint2 f[8][16][32];
 };
 
 // Position of a key channel in the unpacked keys: a word's eight channels come as (0, 4), (1, 5), (2, 6), (3, 7).
@@ -243,6 +238,7 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
     const float* Rk = a.Rk + (size_t)h * D * D;
     const int64_t rows = (int64_t)a.n_tok * a.G;
+    const float unit = a.scale_log2 < 0.f ? -1.f : a.scale_log2 > 0.f ? 1.f : 0.f;
     auto fetch = [&](int64_t r0, uint32_t (&x)[8][4]) {
         const __nv_bfloat16* q[2];
 #pragma unroll
@@ -269,47 +265,45 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
         const float k0[4] = {v0.x, v0.y, v0.z, v0.w}, k1[4] = {v1.x, v1.y, v1.z, v1.w}, k8[4] = {v8.x, v8.y, v8.z, v8.w}, k9[4] = {v9.x, v9.y, v9.z, v9.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint4 f;
-            ck_parts(k0[i], k1[i], f.x, f.z);
-            ck_parts(k8[i], k9[i], f.y, f.w);
-            sm.R.f[ks][c4 >> 1][4 * (2 * i + (c4 & 1)) + tt] = f;
+            sm.R.f[ks][c4 >> 1][4 * (2 * i + (c4 & 1)) + tt] = make_uint2(pack_half2(k0[i], k1[i]), pack_half2(k8[i], k9[i]));
         }
     }
     __syncthreads();
     for (; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 128) {
-        float n2[2] = {0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float lo = __uint_as_float(x[ks][e] << 16), hi = __uint_as_float(x[ks][e] & 0xffff0000u);
-                n2[e & 1] = fmaf(lo, lo, fmaf(hi, hi, n2[e & 1]));
-            }
-        // |q'| sigma lies within 2^7 and 2^8, so its entries are far from both ends of fp16; keys are carried at 2^-4
+        // a row's largest value to 2^7..2^8: its rotated ones stay within 2^12 and far from fp16's other end; keys are
+        // carried at 2^-4 (the sign of the logits' scale goes into the queries, so that row_scale is positive)
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            n2[e] += __shfl_xor_sync(0xffffffffu, n2[e], 1);
-            n2[e] += __shfl_xor_sync(0xffffffffu, n2[e], 2);
-            const float size = sqrtf(n2[e]) * fabsf(a.scale_log2);
-            const float sigma = size > 0.f && size < CUDART_INF_F ? ldexpf(1.f, max(-100, min(100, 7 - ilogbf(size)))) : 1.f;
-            f[e] = a.scale_log2 * sigma;
-            const int64_t row = r0 + r + 8 * e;
-            if (t == 0 && row < rows) a.row_scale[(int64_t)h * rows + row] = 16.f / sigma;
-        }
-#pragma unroll 2
-        for (int nt = 0; nt < 16; ++nt) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+            __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
-                const uint4 b = sm.R.f[ks][nt][lane];
-                ck_mma(d, x[ks], b.z, b.w);
-                ck_mma(c, x[ks], b.x, b.y);
+                m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[ks][e])));
+                m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[ks][e + 2])));
+            }
+            float top = fmaxf(__low2float(m), __high2float(m));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float sigma = ck_scale(top);
+            f[e] = unit * sigma;
+            const int64_t row = r0 + r + 8 * e;
+            if (t == 0 && row < rows) a.row_scale[(int64_t)h * rows + row] = unit == 0.f ? 1.f : fmaxf(16.f * fabsf(a.scale_log2) / sigma, 1e-30f);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[ks][e] = pack_half2(__uint_as_float(x[ks][e] << 16) * f[e & 1], __uint_as_float(x[ks][e] & 0xffff0000u) * f[e & 1]);
+#pragma unroll 4
+        for (int nt = 0; nt < 16; ++nt) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint2 b = sm.R.f[ks][nt][lane];
+                mma_f16_16816(c, x[ks], b.x, b.y);
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<uint32_t*>(&sm.out[warp][r + 8 * e][8 * nt + 2 * t]) =
-                    pack_half2((c[2 * e] + d[2 * e]) * f[e], (c[2 * e + 1] + d[2 * e + 1]) * f[e]);
+            for (int e = 0; e < 2; ++e) *reinterpret_cast<uint32_t*>(&sm.out[warp][r + 8 * e][8 * nt + 2 * t]) = pack_half2(c[2 * e], c[2 * e + 1]);
         }
         const int64_t next = r0 + (int64_t)(gridDim.x - 1) * 128;
         if (next < rows) fetch(next, x);
@@ -326,27 +320,26 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ 2: stream
 //
-// Twenty warps: two warpgroups of softmax (a thread a row of its row tile), one that
-// unpacks keys, one that unpacks values, a warp that issues the products and one that
-// fetches pages.  A block of more than 128 rows has two row tiles, whose warpgroups both take
-// every tile of tokens; a block of up to 128 has one, and the warpgroups take every other tile
-// of tokens of it (two streams, each with sums of its own).  In either case the products of
-// one stream run while the other one's softmax does.
+// Two warpgroups of softmax (a thread a row of its row tile), four that unpack, two warps that
+// issue products and one that fetches pages.  A block of more than 128 rows has two row
+// tiles, whose warpgroups both take every tile of tokens; a block of up to 128 has one, and
+// the warpgroups take every other tile of tokens of it (two streams, each with sums of its
+// own).  In either case the products of one stream run while the other one's softmax does.
 //
-//   TMEM     S0, S1 (a stream's logits, and over them its weights P as fp16), O0, O1
-//   shared   Q [stream], K and V [2 stages] as K-major operands in the 128-byte swizzle (V
-//            transposed: rows are channels), three raw stages of four pages
-constexpr int CK_OPERAND = 128 * 128 * 2, CK_HALF = CK_OPERAND / 2;  // 64 columns of 128 rows each
-constexpr int CK_RAW_PAGES = 4, CK_RAW = CK_RAW_PAGES * INT4_TILE, CK_RAW_STAGES = 3;
-// (registers: 640 threads of 96 at launch; 152 for softmax, 64 for unpacking and 40 for the rest are 60416 of those 61440)
-constexpr int CK_THREADS = 640;
-
-constexpr int CK_INFOS = 4, CK_SHARES = 4;
+//   TMEM     S [stream][2 buffers] (the logits of a tile, and over them its weights P as
+//            fp16), O [stream]
+//   shared   Q [stream], K and V [4 stages] as K-major operands in the 128-byte swizzle (V
+//            transposed: rows are channels), three raw stages
+constexpr int CK_QUERIES = CK_ROW_TILE * D * 2, CK_OPERAND = CK_TILE * D * 2;  // bytes
+constexpr int CK_RAW = CK_PAGES * INT4_TILE, CK_RAW_STAGES = 3, CK_STAGES = 4, CK_INFOS = 8, CK_SHARES = 4;
+constexpr int CK_SOFTMAX = 8, CK_UNPACK = 16;  // warps
+// (Registers: 896 threads of 72 at launch; 128 for softmax, 48 for unpacking and 56 for the rest are those 64512.)
+constexpr int CK_THREADS = 32 * (CK_SOFTMAX + CK_UNPACK + 4);
 
 struct __align__(16) CkInfo {  // of a tile of tokens, written with its keys
-    int base[2][4];        // first position of each page, -1 without one
-    uint32_t poison[2][4]; // tokens of each page whose values are not finite
-    uint32_t special[2];   // [half]: bit t: stream t's rows do not all see all of it
+    int base[4];          // first position of each page, -1 without one
+    uint32_t poison[4];   // tokens of each page whose values are not finite
+    uint32_t special;     // bit t: stream t's rows do not all see all of it
 };
 struct __align__(16) CkShare {  // what the roles need of a share
     int n, two, from, rows;     // tiles; two row tiles
@@ -356,13 +349,13 @@ struct __align__(16) CkShare {  // what the roles need of a share
     int h, end;
 };
 struct __align__(1024) CkSmem {
-    uint8_t q[2][CK_OPERAND], k[2][CK_OPERAND], v[2][CK_OPERAND];
+    uint8_t q[2][CK_QUERIES], k[CK_STAGES][CK_OPERAND], v[CK_STAGES][CK_OPERAND];
     uint8_t raw[CK_RAW_STAGES][CK_RAW];
     CkInfo info[CK_INFOS];
     CkShare share[CK_SHARES];
-    __align__(16) int raw_base[CK_RAW_STAGES][4];
-    uint64_t raw_full[CK_RAW_STAGES], raw_free[CK_RAW_STAGES], k_full[2], k_free[2], v_full[2], v_free[2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained, share_full[CK_SHARES], share_free[CK_SHARES];
+    __align__(16) int raw_base[CK_RAW_STAGES][CK_PAGES];
+    uint64_t raw_full[CK_RAW_STAGES], raw_free[CK_RAW_STAGES], k_full[CK_STAGES], k_free[CK_STAGES], v_full[CK_STAGES], v_free[CK_STAGES];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
     uint32_t tmem;
     int dead;
     uint32_t stages;  // raw stages fetched
@@ -379,20 +372,20 @@ __device__ __forceinline__ bool ck_elect() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
     return x != 0;
 }
-// fp32 accumulators, fp16 operands, both K-major, 128 x 128
-constexpr uint32_t CK_IDESC = 1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24;
+// fp32 accumulators, fp16 operands, both K-major, 128 rows, 128 columns or 64
+constexpr uint32_t CK_IDESC = 1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24, CK_IDESC_QK = 1u << 4 | (64u >> 3) << 17 | (128u >> 4) << 24;
 
-__device__ __forceinline__ void ck_mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add) {
+__device__ __forceinline__ void ck_mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add, uint32_t idesc) {
     asm volatile(
         "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(CK_IDESC), "r"((uint32_t)add),
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add),
         "r"(CK_DESC_HI)
         : "memory");
 }
-__device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
+__device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add, uint32_t idesc) {
     asm volatile(
         "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(CK_IDESC), "r"((uint32_t)add),
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add),
         "r"(CK_DESC_HI)
         : "memory");
 }
@@ -401,13 +394,11 @@ __device__ __forceinline__ void ck_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void ck_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void ck_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void ck_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// What was loaded is used after the wait only.
-template <int N>
-__device__ __forceinline__ void ck_loaded(uint32_t (&x)[N]) {
-    ck_wait_ld();
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i]));
+// What was loaded is used after the wait only (it passes through it).
+#define CK_T8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+__device__ __forceinline__ void ck_loaded16(uint32_t* x) { asm volatile("tcgen05.wait::ld.sync.aligned;" : CK_T8(x, 0), CK_T8(x, 8)::"memory"); }
+__device__ __forceinline__ void ck_loaded32(uint32_t* x) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : CK_T8(x, 0), CK_T8(x, 8), CK_T8(x, 16), CK_T8(x, 24)::"memory");
 }
 __device__ __forceinline__ void ck_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -421,6 +412,13 @@ __device__ __forceinline__ void ck_tmem_ld32(uint32_t* x, uint32_t at) {
         : "r"(at)
         : "memory");
 }
+__device__ __forceinline__ void ck_tmem_ld16(uint32_t* x, uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : CK_R8(x, 0), CK_R8(x, 8)
+        : "r"(at)
+        : "memory");
+}
 __device__ __forceinline__ void ck_tmem_st32(const uint32_t* x, uint32_t at) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -428,7 +426,12 @@ __device__ __forceinline__ void ck_tmem_st32(const uint32_t* x, uint32_t at) {
         CK_W8(x, 8), CK_W8(x, 16), CK_W8(x, 24), "r"(at)
         : "memory");
 }
-
+__device__ __forceinline__ void ck_tmem_st16(const uint32_t* x, uint32_t at) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::CK_W8(x, 0),
+        CK_W8(x, 8), "r"(at)
+        : "memory");
+}
 __device__ __forceinline__ float ck_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -451,44 +454,62 @@ __device__ __forceinline__ float2 ck_add2(float2 a, float2 b) {
 }
 
 // Codes of a word as fp16 numbers, two at a time: nibbles (0, 4), (1, 5), (2, 6), (3, 7).  1024 + c by its bits, less 1024.
-__device__ __forceinline__ void ck_codes(uint32_t w, __half2 (&c)[4]) {
-    const __half2 one = u32_as_h2(0xe400e400u), sixteenth = u32_as_h2(0x2c002c00u), back = u32_as_h2(0xd400d400u);  // -1024, 1/16, -64
-    const uint32_t v = w >> 8;
-    c[0] = __hadd2(u32_as_h2((w & 0x000f000fu) | 0x64006400u), one);
-    c[1] = __hfma2(u32_as_h2((w & 0x00f000f0u) | 0x64006400u), sixteenth, back);
-    c[2] = __hadd2(u32_as_h2((v & 0x000f000fu) | 0x64006400u), one);
-    c[3] = __hfma2(u32_as_h2((v & 0x00f000f0u) | 0x64006400u), sixteenth, back);
-}
+// (The constants stand in registers that the compiler does not see through: otherwise it takes two instructions for an AND
+// and an OR with two immediates, and moves the others again for each word.)
+struct CkConst {
+    uint32_t low, high, magic, one, sixteenth, back;
+    __device__ __forceinline__ CkConst() {
+        asm volatile("mov.b32 %0, 0x000f000f;\n mov.b32 %1, 0x00f000f0;\n mov.b32 %2, 0x64006400;\n mov.b32 %3, 0xe400e400;\n mov.b32 %4, 0x2c002c00;\n mov.b32 %5, 0xd400d400;"
+                     : "=r"(low), "=r"(high), "=r"(magic), "=r"(one), "=r"(sixteenth), "=r"(back));  // .. 1024, -1024, 1/16, -64
+    }
+    __device__ __forceinline__ __half2 take(uint32_t w, uint32_t mask) const {
+        uint32_t x;
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "r"(mask), "r"(magic));
+        return u32_as_h2(x);
+    }
+    __device__ __forceinline__ void codes(uint32_t w, __half2 (&c)[4]) const {
+        const uint32_t v = w >> 8;
+        c[0] = __hadd2(take(w, low), u32_as_h2(one));
+        c[1] = __hfma2(take(w, high), u32_as_h2(sixteenth), u32_as_h2(back));
+        c[2] = __hadd2(take(v, low), u32_as_h2(one));
+        c[3] = __hfma2(take(v, high), u32_as_h2(sixteenth), u32_as_h2(back));
+    }
+};
 
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ uint8_t smem_raw[];
     CkSmem& sm = *reinterpret_cast<CkSmem*>(smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < CK_RAW_STAGES; ++i) {
             mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_free[i], 8);
+            mbar_init(&sm.raw_free[i], CK_UNPACK);
+        }
+        for (int i = 0; i < CK_STAGES; ++i) {
+            mbar_init(&sm.k_full[i], CK_UNPACK / 2);
+            mbar_init(&sm.v_full[i], CK_UNPACK / 2);
+            mbar_init(&sm.k_free[i], 2);
+            mbar_init(&sm.v_free[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.k_full[i], 8);  // four warps, two halves
-            mbar_init(&sm.v_full[i], 8);
-            mbar_init(&sm.k_free[i], 1);
-            mbar_init(&sm.v_free[i], 1);
             mbar_init(&sm.q_full[i], 4);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sm.s_full[i][h], 1);
+                mbar_init(&sm.p_full[i][h], 4);
+            }
+            mbar_init(&sm.o_done[i], 1);
             mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.drained[i], 1);
         }
         for (int i = 0; i < CK_SHARES; ++i) {
             mbar_init(&sm.share_full[i], 1);
-            mbar_init(&sm.share_free[i], 17);  // the warps but the loader
+            mbar_init(&sm.share_free[i], CK_SOFTMAX + CK_UNPACK + 2);  // the warps but the loader
         }
-        mbar_init(&sm.drained, 1);
         sm.dead = 0;
         sm.stages = 0;
         fence_mbar_init();
     }
-    if (warp == 16) {
+    if (warp == CK_SOFTMAX + CK_UNPACK) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -529,78 +550,75 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
         return ok;
     };
 
-    if (group == 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 16) {
-            // ---- products: the whole warp goes along, so that descriptors stay in uniform registers; one lane issues
-            uint32_t tile0 = 0, done0 = 0, done1 = 0;  // tiles before this share, weights taken of each stream
+    if (warp >= CK_SOFTMAX + CK_UNPACK) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (!(warp & 1)) {
+            // ---- products of stream t.  Its logits stand in two buffers: the next tile's are formed while the softmax works
+            // on this one's.  (Two warps: the tensor core takes few products in advance, so one warp's waits between two
+            // streams' products left it idle.)  The whole warp goes along, so that descriptors stay in uniform registers;
+            // one lane issues.
+            const int t = __shfl_sync(0xffffffffu, warp >> 1 & 1, 0);
+            uint32_t tile0 = 0, done = 0;  // tiles before this share, of this stream
             bool ok = true;
             const bool leader = ck_elect();
-            const uint32_t q_lo = ck_desc_lo(sm.q[0]), k_lo = ck_desc_lo(sm.k[0]), v_lo = ck_desc_lo(sm.v[0]);
+            const uint32_t q_lo = ck_desc_lo(sm.q[t]), k_lo = ck_desc_lo(sm.k[0]), v_lo = ck_desc_lo(sm.v[0]);
+            const uint32_t s_at = tmem + 128 * t, o_at = tmem + 256 + 128 * t;
             while (ok && next_share()) {
                 const CkShare& g = sm.share[(n_share - 1) % CK_SHARES];
-                const int n = __shfl_sync(0xffffffffu, g.n, 0), two = __shfl_sync(0xffffffffu, g.two, 0);
-                const int n0 = two ? n : (n + 1) / 2, n1 = two ? n : n / 2;
-                auto qk = [&](int t, int j) {  // (t a constant at each call)
-                    const uint32_t x = tile0 + (two ? j : 2 * j + t), st = x & 1;
-                    if (!(ok = wait(&sm.k_full[st], x >> 1 & 1))) return;
-                    ck_fence_after();
-                    if (leader) {
-                        const uint32_t qd = q_lo + t * (CK_OPERAND >> 4), kd = k_lo + st * (CK_OPERAND >> 4);
+                const int n = __shfl_sync(0xffffffffu, g.n, 0), two = __shfl_sync(0xffffffffu, g.two, 0), ns = two ? n : (n + 1 - t) / 2;
+                ok = wait(&sm.q_full[t], (n_share - 1) & 1);
+#pragma unroll 1
+                for (int x = 0; x < ns + 2 && ok; ++x) {
+                    if (x >= 2) {  // the weighted sum of tile x - 2
+                        const uint32_t tile = tile0 + (two ? x - 2 : 2 * (x - 2) + t), st = tile % CK_STAGES, step = done + x - 2;
+                        if (!(ok = wait(&sm.v_full[st], tile / CK_STAGES & 1) && wait(&sm.p_full[t][step & 1], step >> 1 & 1))) break;
+                        ck_fence_after();
+                        if (leader) {
+                            const uint32_t vd = v_lo + st * (CK_OPERAND >> 4), p_at = s_at + 64 * (step & 1);
+                            ck_mma_ts(o_at, p_at, vd, x > 2, CK_IDESC);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int at = (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4);
-                            ck_mma_ss(tmem + 128 * t, qd + at, kd + at, i > 0);
+                            for (int i = 1; i < 4; ++i) ck_mma_ts(o_at, p_at + 8 * i, vd + 2 * i, true, CK_IDESC);
+                            ck_commit(&sm.o_done[t]);
+                            if (x == ns + 1) ck_commit(&sm.o_full[t]);
+                            ck_commit(&sm.v_free[st]);
+                            if (!two) ck_commit(&sm.v_free[st]);
                         }
-                        ck_commit(&sm.s_full[t]);
-                        if (!two || t == 1) ck_commit(&sm.k_free[st]);
+                        __syncwarp();
                     }
-                    __syncwarp();
-                };
-                auto pv = [&](int t, int j, bool last) {
-                    const uint32_t x = tile0 + (two ? j : 2 * j + t), st = x & 1;
-                    uint32_t& done = t ? done1 : done0;
-                    if (!(ok = wait(&sm.v_full[st], x >> 1 & 1) && wait(&sm.p_full[t], done & 1))) return;
-                    ++done;
-                    ck_fence_after();
-                    if (leader) {
-                        const uint32_t vd = v_lo + st * (CK_OPERAND >> 4);
-                        ck_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t, vd, j > 0);
+                    if (x < ns) {  // the logits of tile x
+                        const uint32_t tile = tile0 + (two ? x : 2 * x + t), st = tile % CK_STAGES, step = done + x;
+                        if (!(ok = wait(&sm.k_full[st], tile / CK_STAGES & 1))) break;
+                        ck_fence_after();
+                        if (leader) {
+                            const uint32_t kd = k_lo + st * (CK_OPERAND >> 4);
 #pragma unroll
-                        for (int i = 1; i < 8; ++i)
-                            ck_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, vd + (i & 3) * 2 + (i >> 2) * (CK_HALF >> 4), true);
-                        if (!two || t == 1) ck_commit(&sm.v_free[st]);
-                        if (last) ck_commit(&sm.o_full[t]);
+                            for (int i = 0; i < 8; ++i)
+                                ck_mma_ss(s_at + 64 * (step & 1), q_lo + (i & 3) * 2 + (i >> 2) * (CK_QUERIES >> 5), kd + (i & 3) * 2 + (i >> 2) * (CK_OPERAND >> 5),
+                                          i > 0, CK_IDESC_QK);
+                            ck_commit(&sm.s_full[t][step & 1]);
+                            ck_commit(&sm.k_free[st]);
+                            if (!two) ck_commit(&sm.k_free[st]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                };
-                ok = wait(&sm.q_full[0], (n_share - 1) & 1);
-                if (ok) qk(0, 0);
-                if (ok) ok = wait(&sm.q_full[1], (n_share - 1) & 1);
-                if (ok && n1 > 0) qk(1, 0);
-                for (int j = 0; j < n0 && ok; ++j) {
-                    pv(0, j, j + 1 == n0);
-                    if (ok && j + 1 < n0) qk(0, j + 1);
-                    if (ok && j < n1) pv(1, j, j + 1 == n1);
-                    if (ok && j + 1 < n1) qk(1, j + 1);
                 }
                 tile0 += n;
+                done += ns;
             }
             // everything issued is done before TMEM is freed
             if (leader) {
-                ck_commit(&sm.drained);
-                (void)mbar_wait_bounded(&sm.drained, 0, 100000000LL);
+                ck_commit(&sm.drained[t]);
+                (void)mbar_wait_bounded(&sm.drained[t], 0, 100000000LL);
             }
-        } else if (warp == 17) {
+        } else if (warp == CK_SOFTMAX + CK_UNPACK + 1) {
             // ---- shares and pages
             const int C = __ldcg(&a.plan->ctas), cta = blockIdx.x, n_blocks = __ldcg(&a.plan->blocks);
-            const int64_t total = __ldcg(&a.plan->total);
             CkWalk w;
             w.pos = w.end = 0;
             w.e = w.h = 0;
             if (cta < C) {  // the block that holds pos: 33 cuts of the range at a time
-                w.pos = ck_cut(total, cta, C);
-                w.end = ck_cut(total, cta + 1, C);
+                w.pos = __ldcg(a.cut + cta);
+                w.end = __ldcg(a.cut + cta + 1);
                 int lo = 0, hi = n_blocks;  // start[lo] * H <= pos, start[hi] * H > pos
                 while (hi - lo > 1) {
                     const int step = (hi - lo + 32) / 33, x = lo + (lane + 1) * step;
@@ -615,6 +633,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             }
             uint32_t stage = 0;
             bool ok = true;
+            const bool leader = ck_elect();
             for (uint32_t x = 0; ok; ++x) {
                 const bool have = w.next(a);
                 if (x >= CK_SHARES && !(ok = wait(&sm.share_free[x % CK_SHARES], (x / CK_SHARES - 1) & 1))) break;
@@ -623,7 +642,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     g.end = !have;
                     if (have) {
                         g.n = w.to - w.from;
-                        g.two = w.k.rows > CK_TILE;
+                        g.two = w.k.rows > CK_ROW_TILE;
                         g.from = w.from;
                         g.rows = w.k.rows;
                         g.r0 = w.k.r0;
@@ -633,7 +652,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         g.h = w.last_h;
                         g.row0 = (int64_t)w.k.q0 * a.G;
                         for (int t = 0; t < 2; ++t) {
-                            const int r0 = w.k.r0 + (g.two ? CK_TILE * t : 0), r1 = min(w.k.r0 + w.k.rows, r0 + CK_TILE) - 1;
+                            const int r0 = w.k.r0 + (g.two ? CK_ROW_TILE * t : 0), r1 = min(w.k.r0 + w.k.rows, r0 + CK_ROW_TILE) - 1;
                             g.first[t] = g.pos0 + r0 / a.G;
                             g.last[t] = g.pos0 + r1 / a.G;
                         }
@@ -642,74 +661,85 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 }
                 __syncwarp();
                 if (!have) break;
-                const int p1 = min(w.k.pages, 8 * w.to), n = 2 * (w.to - w.from);
+                // a lane's page of the next eight tiles' 32: its first position (-1: none, or a bad entry) and where it stands
+                const int p0 = CK_PAGES * w.from, p1 = min(w.k.pages, CK_PAGES * w.to), n = w.to - w.from, sinks = w.k.sinks, skip = w.k.skip;
                 const int32_t* table = a.block_table + (size_t)w.k.b * a.max_pages;
-                auto ids = [&](int p0) {
-                    const int p = p0 + lane;
-                    return p < p1 ? __ldg(table + p + (p < w.k.sinks ? 0 : w.k.skip)) : 0;
+                auto ids = [&](int first) {
+                    const int p = first + lane;
+                    return p < p1 ? __ldg(table + p + (p < sinks ? 0 : skip)) : 0;
                 };
-                int id = ids(8 * w.from), next_id = 0;
+                int next_id = ids(p0), base = -1;
+                uint64_t from = 0;
                 for (int s = 0; s < n; ++s, ++stage) {
                     if ((s & 7) == 0) {
-                        if (s) id = next_id;
-                        next_id = ids(8 * w.from + 4 * s + 32);
+                        const int p = p0 + CK_PAGES * s + lane;
+                        const bool good = p < p1 && next_id >= 0 && (int64_t)next_id < a.num_pages;
+                        if (p < p1 && !good) atomicOr(a.error, ERR_BAD_PAGE);
+                        base = good ? PAGE * (p + (p < sinks ? 0 : skip)) : -1;
+                        from = reinterpret_cast<uint64_t>(a.cache + ((size_t)(good ? next_id : 0) * a.H_kv + w.last_h) * INT4_TILE);
+                        next_id = ids(p0 + CK_PAGES * s + 32);
                     }
                     const uint32_t slot = stage % CK_RAW_STAGES;
+                    int at[CK_PAGES];
+                    uint64_t src[CK_PAGES];
+                    uint32_t bytes = 0;
+#pragma unroll
+                    for (int i = 0; i < CK_PAGES; ++i) {
+                        at[i] = __shfl_sync(0xffffffffu, base, 4 * (s & 7) + i);
+                        src[i] = __shfl_sync(0xffffffffu, from, 4 * (s & 7) + i);
+                        bytes += at[i] >= 0 ? INT4_TILE : 0;
+                    }
                     if (stage >= CK_RAW_STAGES && !(ok = wait(&sm.raw_free[slot], (stage / CK_RAW_STAGES - 1) & 1))) break;
-                    const int mine = __shfl_sync(0xffffffffu, id, 4 * (s & 7) + (lane & 3)), p = 8 * w.from + 4 * s + (lane & 3);
-                    const bool there = p < p1, good = there && mine >= 0 && (int64_t)mine < a.num_pages;
-                    const uint32_t copies = __popc(__ballot_sync(0xffffffffu, good) & 15u);
-                    if (lane < 4) {
-                        sm.raw_base[slot][lane] = good ? PAGE * (p + (p < w.k.sinks ? 0 : w.k.skip)) : -1;
-                        if (there && !good) atomicOr(a.error, ERR_BAD_PAGE);
-                        if (good && !(a.drop && stage == 0 && lane == 0 && cta == 0))
-                            bulk_g2s(sm.raw[slot] + lane * INT4_TILE, a.cache + ((size_t)mine * a.H_kv + w.last_h) * INT4_TILE, INT4_TILE, &sm.raw_full[slot]);
+                    if (leader) {
+                        *reinterpret_cast<int4*>(sm.raw_base[slot]) = make_int4(at[0], at[1], at[2], at[3]);
+                        mbar_arrive_expect_tx(&sm.raw_full[slot], bytes);
+#pragma unroll
+                        for (int i = 0; i < CK_PAGES; ++i)
+                            if (at[i] >= 0 && !(a.drop && stage == 0 && i == 0 && cta == 0))
+                                bulk_g2s(sm.raw[slot] + i * INT4_TILE, reinterpret_cast<const void*>(src[i]), INT4_TILE, &sm.raw_full[slot]);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[slot], copies * INT4_TILE);
                 }
             }
             if (lane == 0) sm.stages = stage;
         }
-    } else if (group == 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        // ---- keys: a thread takes a token's words t of all groups, twice a stage
+    } else if (warp >= CK_SOFTMAX) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        // (keys on two of the four schedulers and values on the others: with both, and the softmax, on each, warps waited
+        // for instructions more than for anything else)
+        const int part = (warp & 1) | ((warp - CK_SOFTMAX) >> 1 & ~1);  // of eight warps
         uint32_t tile = 0;
         bool ok = true;
-        const int t = lane & 3, wk = warp & 3, tok0 = 8 * wk + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
-        while (ok && next_share()) {
-            const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
-            for (int i = share.n; i > 0 && ok; --i, ++tile) {
-                const uint32_t st = tile & 1;
-                if (tile >= 2 && !(ok = wait(&sm.k_free[st], (tile / 2 - 1) & 1))) break;
-                CkInfo& info = sm.info[tile % CK_INFOS];
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t raw = 2 * tile + half, slot = raw % CK_RAW_STAGES;
-                    if (!(ok = wait(&sm.raw_full[slot], (raw / CK_RAW_STAGES) & 1))) break;
+        const CkConst cc;
+        if (!(warp & 2)) {
+            // ---- keys: a thread takes a token's words t of all groups
+            const int t = lane & 3, tok = 8 * part + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
+            const uint32_t from = (tok >> 4) * INT4_TILE + O4_KC + 64 * (tok & 15) + 16 * t, meta_from = (tok >> 4) * INT4_TILE + O4_KM + 16 * (tok & 15);
+            const uint32_t to0 = tok * 128 + ((t ^ (tok & 7)) << 4), to1 = tok * 128 + (((4 + t) ^ (tok & 7)) << 4);
+            while (ok && next_share()) {
+                const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
+                for (int i = share.n; i > 0; --i, ++tile) {
+                    const uint32_t st = tile % CK_STAGES, slot = tile % CK_RAW_STAGES;
+                    if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
+                    if (tile >= CK_STAGES && !(ok = wait(&sm.k_free[st], (tile / CK_STAGES - 1) & 1))) break;
+                    const uint4 codes = lds128(sm.raw[slot] + from), meta = lds128(sm.raw[slot] + meta_from);
+                    const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
+                    const __half2 tiny = u32_as_h2(cc.sixteenth);  // with it no key leaves fp16
+                    const __half2 s01 = __hmul2(u32_as_h2(meta.x), tiny), s23 = __hmul2(u32_as_h2(meta.y), tiny);
+                    const __half2 m01 = __hmul2(u32_as_h2(meta.z), tiny), m23 = __hmul2(u32_as_h2(meta.w), tiny);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int tok = tok0 + 32 * e, row = 64 * half + tok;
-                        const uint8_t* page = sm.raw[slot] + (tok >> 4) * INT4_TILE;
-                        const uint4 codes = lds128(page + O4_KC + 64 * (tok & 15) + 16 * t), meta = lds128(page + O4_KM + 16 * (tok & 15));
-                        const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
-                        const __half2 tiny = u32_as_h2(0x2c002c00u);  // 1/16: with it no key leaves fp16
-                        const __half2 s01 = __hmul2(u32_as_h2(meta.x), tiny), s23 = __hmul2(u32_as_h2(meta.y), tiny);
-                        const __half2 m01 = __hmul2(u32_as_h2(meta.z), tiny), m23 = __hmul2(u32_as_h2(meta.w), tiny);
-                        uint8_t* out = sm.k[st] + row * 128;
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const __half2 s = g & 1 ? __high2half2(g < 2 ? s01 : s23) : __low2half2(g < 2 ? s01 : s23);
-                            const __half2 m = g & 1 ? __high2half2(g < 2 ? m01 : m23) : __low2half2(g < 2 ? m01 : m23);
-                            __half2 c[4];
-                            ck_codes(word[g], c);
-                            const uint4 x = make_uint4(h2_as_u32(__hfma2(c[0], s, m)), h2_as_u32(__hfma2(c[1], s, m)),
-                                                       h2_as_u32(__hfma2(c[2], s, m)), h2_as_u32(__hfma2(c[3], s, m)));
-                            *reinterpret_cast<uint4*>(out + (g >> 1) * CK_HALF + (((4 * (g & 1) + t) ^ (row & 7)) << 4)) = x;
-                        }
+                    for (int g = 0; g < 4; ++g) {
+                        const __half2 s = g & 1 ? __high2half2(g < 2 ? s01 : s23) : __low2half2(g < 2 ? s01 : s23);
+                        const __half2 m = g & 1 ? __high2half2(g < 2 ? m01 : m23) : __low2half2(g < 2 ? m01 : m23);
+                        __half2 c[4];
+                        cc.codes(word[g], c);
+                        *reinterpret_cast<uint4*>(sm.k[st] + (g >> 1) * (CK_OPERAND / 2) + (g & 1 ? to1 : to0)) =
+                            make_uint4(h2_as_u32(__hfma2(c[0], s, m)), h2_as_u32(__hfma2(c[1], s, m)), h2_as_u32(__hfma2(c[2], s, m)),
+                                       h2_as_u32(__hfma2(c[3], s, m)));
                     }
-                    {   // values that are not finite: a warp looks at its page's scales and mins, a slot pair of either a lane
-                        const uint4 y = lds128(sm.raw[slot] + wk * INT4_TILE + O4_VS + 16 * (lane & 15));
+                    CkInfo& info = sm.info[tile % CK_INFOS];
+                    if (part < CK_PAGES) {  // values that are not finite: a warp looks at a page's scales and mins, a slot pair of either a lane
+                        const uint4 y = lds128(sm.raw[slot] + part * INT4_TILE + O4_VS + 16 * (lane & 15));
                         const __half2 top = __hmax2_nan(__hmax2_nan(__habs2(u32_as_h2(y.x)), __habs2(u32_as_h2(y.y))),
                                                         __hmax2_nan(__habs2(u32_as_h2(y.z)), __habs2(u32_as_h2(y.w))));
                         uint32_t bad = (__half2float(__low2half(top)) < CUDART_INF_F ? 0u : 1u) | (__half2float(__high2half(top)) < CUDART_INF_F ? 0u : 2u);
@@ -718,17 +748,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
 #pragma unroll
                             for (int o = 8; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
                         }
-                        if (lane == 0) info.poison[half][wk] = sm.raw_base[slot][wk] < 0 ? 0u : bad;
-                    }
-                    if (wk == 0) {
+                        if (lane == 0) info.poison[part] = sm.raw_base[slot][part] < 0 ? 0u : bad;
+                    } else if (part == CK_PAGES) {
                         const int at = sm.raw_base[slot][lane & 3];
-                        bool part[2];
+                        bool cut[2];
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            part[x] = at < 0 || at + PAGE - 1 > share.first[x] || (a.window && at <= share.last[x] - a.window && at + PAGE > a.sinks);
-                        const uint32_t s0 = __any_sync(0xffffffffu, part[0]), s1 = __any_sync(0xffffffffu, part[1]);
-                        if (lane < 4) info.base[half][lane] = at;
-                        if (lane == 0) info.special[half] = s0 | s1 << 1;
+                            cut[x] = at < 0 || at + PAGE - 1 > share.first[x] || (a.window && at <= share.last[x] - a.window && at + PAGE > a.sinks);
+                        const uint32_t s0 = __any_sync(0xffffffffu, cut[0]), s1 = __any_sync(0xffffffffu, cut[1]);
+                        if (lane < 4) info.base[lane] = at;
+                        if (lane == 0) info.special = s0 | s1 << 1;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -738,73 +767,62 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     }
                 }
             }
-        }
-    } else if (group == 3) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        // ---- values: a thread takes the words r of eight tokens and two groups
-        uint32_t tile = 0;
-        bool ok = true;
-        const int wg = warp & 3, r = lane & 7, oct = 4 * (wg & 1) + (lane >> 3), g0 = 2 * (wg >> 1), pair0 = 4 * (oct & 1);
-        while (ok && next_share()) {
-            const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
-            for (int i = share.n; i > 0 && ok; --i, ++tile) {
-                const uint32_t st = tile & 1;
-                if (tile >= 2 && !(ok = wait(&sm.v_free[st], (tile / 2 - 1) & 1))) break;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t raw = 2 * tile + half, slot = raw % CK_RAW_STAGES;
-                    if (!(ok = wait(&sm.raw_full[slot], (raw / CK_RAW_STAGES) & 1))) break;
-                    const uint8_t* page = sm.raw[slot] + (oct >> 1) * INT4_TILE;
+        } else {
+            // ---- values: a thread takes the words r of eight tokens and a group
+            const int r = lane & 7, oct = 4 * (part & 1) + (lane >> 3), g = part >> 1, pair0 = 4 * (oct & 1);
+            const uint32_t from = (oct >> 1) * INT4_TILE + O4_VC + 128 * pair0 + 16 * r + 4 * g, meta_from = (oct >> 1) * INT4_TILE + O4_VS + 16 * pair0 + 4 * g;
+            const uint32_t to = (32 * g + r) * 128 + ((oct ^ r) << 4);
+            while (ok && next_share()) {
+                const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
+                for (int i = share.n; i > 0; --i, ++tile) {
+                    const uint32_t st = tile % CK_STAGES, slot = tile % CK_RAW_STAGES;
+                    if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
+                    if (tile >= CK_STAGES && !(ok = wait(&sm.v_free[st], (tile / CK_STAGES - 1) & 1))) break;
+                    const uint8_t *cp = sm.raw[slot] + from, *mp = sm.raw[slot] + meta_from;
+                    uint32_t code[4], sc[4], mn[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        code[p] = lds32(cp + 128 * p);
+                        sc[p] = lds32(mp + 16 * p);
+                        mn[p] = lds32(mp + 16 * p + (O4_VM - O4_VS));
+                    }
                     const int base = sm.raw_base[slot][oct >> 1];
                     // tokens of the octet within the context, none without a page
                     const int valid = base < 0 ? 0 : min(8, max(0, share.ctx - base - 2 * pair0));
-                    uint2 code[4], sc[4], mn[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        code[p] = lds64(page + O4_VC + 128 * (pair0 + p) + 16 * r + 4 * g0);
-                        sc[p] = lds64(page + O4_VS + 16 * (pair0 + p) + 4 * g0);
-                        mn[p] = lds64(page + O4_VM + 16 * (pair0 + p) + 4 * g0);
-                    }
-                    // a lane looks at one pair's two groups of scales or mins: those from 2^11 or 2^15 up, and NaN, take the long way
-                    const uint2 look = lds64(page + (r & 4 ? O4_VM : O4_VS) + 16 * (pair0 + (r & 3)) + 4 * g0);
-                    const __half2 most = __hmax2_nan(__habs2(u32_as_h2(look.x)), __habs2(u32_as_h2(look.y)));
+                    // a lane looks at one pair's scales or mins: those from 2^11 or 2^15 up, and NaN, take the long way
+                    const __half2 look = __habs2(u32_as_h2(lds32(mp + 16 * (r & 3) + (r & 4 ? O4_VM - O4_VS : 0))));
                     const float edge = r & 4 ? 32768.f : 2048.f;
-                    const bool plain = valid == 8 && __low2float(most) < edge && __high2float(most) < edge;
-                    uint8_t* out = sm.v[st] + half * CK_HALF + r * 128 + ((oct ^ r) << 4) + 32 * g0 * 128;
+                    const bool plain = valid == 8 && __low2float(look) < edge && __high2float(look) < edge;
+                    uint32_t x[4][4];
                     if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            uint32_t x[4][4];
+                        for (int p = 0; p < 4; ++p) {
+                            __half2 c[4];
+                            cc.codes(code[p], c);
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                __half2 c[4];
-                                ck_codes(g ? code[p].y : code[p].x, c);
-                                const __half2 s = u32_as_h2(g ? sc[p].y : sc[p].x), m = u32_as_h2(g ? mn[p].y : mn[p].x);
-#pragma unroll
-                                for (int n = 0; n < 4; ++n) x[n][p] = h2_as_u32(__hfma2(c[n], s, m));
-                            }
-#pragma unroll
-                            for (int n = 0; n < 4; ++n)
-                                *reinterpret_cast<uint4*>(out + (32 * g + 8 * n) * 128) = make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
+                            for (int n = 0; n < 4; ++n) x[n][p] = h2_as_u32(__hfma2(c[n], u32_as_h2(sc[p]), u32_as_h2(mn[p])));
                         }
                     } else {
                         // in fp32, cut off at fp16's ends; tokens past the context are 0, and so are those that hold what is not
                         // finite, whose logits the softmax makes NaN instead (a weight of 0 would not hide it from other rows)
 #pragma unroll 1
-                        for (int x = 0; x < 8; ++x) {
-                            const int g = x >> 2, n = x & 3;
-                            uint32_t y[4];
+                        for (int p = 0; p < 4; ++p) {
+                            const uint32_t c = lds32(cp + 128 * p);
+                            const float2 s = __half22float2(u32_as_h2(lds32(mp + 16 * p))), m = __half22float2(u32_as_h2(lds32(mp + 16 * p + (O4_VM - O4_VS))));
+                            const bool lo_ok = 2 * p < valid && isfinite(s.x) && isfinite(m.x), hi_ok = 2 * p + 1 < valid && isfinite(s.y) && isfinite(m.y);
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                const uint32_t c = (g ? code[p].y : code[p].x) >> (4 * n);
-                                const float2 s = __half22float2(u32_as_h2(g ? sc[p].y : sc[p].x)), m = __half22float2(u32_as_h2(g ? mn[p].y : mn[p].x));
-                                const float lo = fmaf((float)(c & 15), s.x, m.x), hi = fmaf((float)(c >> 16 & 15), s.y, m.y);
-                                const bool lo_ok = 2 * p < valid && isfinite(s.x) && isfinite(m.x), hi_ok = 2 * p + 1 < valid && isfinite(s.y) && isfinite(m.y);
-                                y[p] = pack_half2(lo_ok ? fminf(fmaxf(lo, -65504.f), 65504.f) : 0.f, hi_ok ? fminf(fmaxf(hi, -65504.f), 65504.f) : 0.f);
+                            for (int n = 0; n < 4; ++n) {
+                                const float lo = fmaf((float)(c >> (4 * n) & 15), s.x, m.x), hi = fmaf((float)(c >> (16 + 4 * n) & 15), s.y, m.y);
+                                const uint32_t y = pack_half2(lo_ok ? fminf(fmaxf(lo, -65504.f), 65504.f) : 0.f, hi_ok ? fminf(fmaxf(hi, -65504.f), 65504.f) : 0.f);
+#pragma unroll
+                                for (int pp = 0; pp < 4; ++pp)
+                                    if (pp == p) x[n][pp] = y;
                             }
-                            *reinterpret_cast<uint4*>(out + (32 * g + 8 * n) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        *reinterpret_cast<uint4*>(sm.v[st] + to + 8 * n * 128) = make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -815,16 +833,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         // ---- softmax of stream t: a thread a row
-        const int t = group, row = tid & 127;
+        const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
-        uint32_t tile0 = 0, step = 0, parts = 0;
+        uint32_t tile0 = 0, done = 0, parts = 0;
         bool ok = true;
         while (ok && next_share()) {
             const CkShare& g = sm.share[(n_share - 1) % CK_SHARES];
             const int two = g.two, n = g.n, ns = two ? n : (n + 1 - t) / 2;
-            const int in_block = (two ? CK_TILE * t : 0) + row;
+            const int in_block = (two ? CK_ROW_TILE * t : 0) + row;
             const bool live = in_block < g.rows;
             const int in_seq = g.r0 + (live ? in_block : 0), pos = g.pos0 + in_seq / a.G;
             const int64_t at = (int64_t)g.h * a.n_tok * a.G + g.row0 + in_seq;  // the row among all
@@ -833,30 +851,34 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 uint8_t* dst = sm.q[t] + row * 128;
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * CK_HALF + (((c & 7) ^ (row & 7)) << 4)) = __ldcg(src + c);
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * (CK_QUERIES / 2) + (((c & 7) ^ (row & 7)) << 4)) = __ldcg(src + c);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.q_full[t]);
             }
             const float f = __ldcg(a.row_scale + at);
             float ref = CK_NEG, l = 0.f;
-            for (int j = 0; j < ns; ++j, ++step) {
-                if (!(ok = wait(&sm.s_full[t], step & 1))) break;
+            for (int x = 0; x < ns; ++x, ++done) {
+                const uint32_t p_at = s_at + 64 * (done & 1);
+                if (!(ok = wait(&sm.s_full[t][done & 1], done >> 1 & 1))) break;
                 ck_fence_after();
-                const CkInfo& info = sm.info[(tile0 + (two ? j : 2 * j + t)) % CK_INFOS];
-                const uint4 pa = lds128(info.poison[0]), pb = lds128(info.poison[1]);
-                const bool special = ((info.special[0] | info.special[1]) >> t & 1) | ((pa.x | pa.y | pa.z | pa.w | pb.x | pb.y | pb.z | pb.w) != 0);
+                uint32_t s[64], p[32];
+                ck_tmem_ld32(s, p_at);
+                ck_tmem_ld32(s + 32, p_at + 32);
+                const CkInfo& info = sm.info[(tile0 + (two ? x : 2 * x + t)) % CK_INFOS];
+                const uint4 bad4 = lds128(info.poison);
+                const bool special = (info.special >> t & 1) | ((bad4.x | bad4.y | bad4.z | bad4.w) != 0);
                 // 32 tokens, two pages: what the row does not see is -inf, what is not finite NaN
-                auto mask = [&](uint32_t (&s)[32], int c) {
+                auto mask = [&](uint32_t* s, int c) {
 #pragma unroll
                     for (int pg = 0; pg < 2; ++pg) {
-                        const int base = info.base[c >> 1][2 * (c & 1) + pg];
+                        const int base = info.base[2 * c + pg];
                         uint32_t see = base < 0 ? 0u : (1u << min(PAGE, max(0, pos - base + 1))) - 1u;
                         if (a.window) {
                             const int low = min(PAGE, max(0, pos - a.window + 1 - base)), sink = min(PAGE, max(0, a.sinks - base));
                             see &= ~((1u << low) - 1u) | ((1u << sink) - 1u);
                         }
-                        const uint32_t bad = info.poison[c >> 1][2 * (c & 1) + pg];
+                        const uint32_t bad = info.poison[2 * c + pg];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             if (bad >> i & 1) s[16 * pg + i] = 0x7fffffffu;
@@ -864,74 +886,72 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         }
                     }
                 };
-                bool raise = j == 0;
-                uint32_t p[64];
-                float total;
+                ck_loaded32(s);
+                ck_loaded32(s + 32);
+                if (special) {
+                    mask(s, 0);
+                    mask(s + 32, 1);
+                }
+                float2 sum[2];
+                bool raise = x == 0;
                 while (true) {
-                    if (raise) {  // the row's largest logit, and its reference up to it
+                    if (raise) {  // the row's reference goes up to its largest logit here, what it has so far down by as much
                         float top = -CUDART_INF_F;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t s[32];
-                            ck_tmem_ld32(s, s_at + 32 * c);
-                            ck_loaded(s);
-                            if (special) mask(s, c);
+                        for (int c = 0; c < 2; ++c) {  // (read again: a rare path of its own)
+                            uint32_t z[32];
+                            ck_tmem_ld32(z, p_at + 32 * c);
+                            ck_loaded32(z);
+                            if (special) mask(z, c);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+                            for (int y = 0; y < 32; y += 2) top = fmaxf(fmaxf(top, __uint_as_float(z[y])), __uint_as_float(z[y + 1]));
                         }
                         top *= f;
                         const float up = top > ref ? ceilf(top) : ref, c0 = ck_ex2(ref - up);
                         ref = up;
                         l *= c0;
-                        if (j > 0) {
+                        if (x > 0) {
+                            if (!(ok = wait(&sm.o_done[t], (done - 1) & 1))) break;  // (the tile before is in the sums)
+                            ck_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t o[32];
-                                ck_tmem_ld32(o, o_at + 32 * c);
-                                ck_loaded(o);
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t o[16];
+                                ck_tmem_ld16(o, o_at + 16 * c);
+                                ck_loaded16(o);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c0);
-                                ck_tmem_st32(o, o_at + 32 * c);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c0);
+                                ck_tmem_st16(o, o_at + 16 * c);
                             }
                         }
                     }
                     const float2 f2 = make_float2(f, f), off = make_float2(CK_LIFT - ref, CK_LIFT - ref);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t s[2][32];
-                    ck_tmem_ld32(s[0], s_at);
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        ck_loaded(s[c & 1]);
-                        if (c < 3) ck_tmem_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));
-                        if (special) mask(s[c & 1], c);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float2 x = ck_fma2(make_float2(__uint_as_float(s[c & 1][2 * i]), __uint_as_float(s[c & 1][2 * i + 1])), f2, off);
-                            x = make_float2(ck_ex2(x.x), ck_ex2(x.y));
-                            sum[i & 1] = ck_add2(sum[i & 1], x);
-                            p[16 * c + i] = pack_half2(x.x, x.y);
-                        }
+                    for (int i = 0; i < 32; ++i) {
+                        float2 y = ck_fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f2, off);
+                        y = make_float2(ck_ex2(y.x), ck_ex2(y.y));
+                        sum[i & 1] = ck_add2(sum[i & 1], y);
+                        p[i] = pack_half2(y.x, y.y);
                     }
                     sum[0] = ck_add2(sum[0], sum[1]);
-                    total = sum[0].x + sum[0].y;
                     // (a sum that fp16 holds is one of weights that it holds)
-                    if (raise || !__any_sync(0xffffffffu, total > 65504.f)) break;
+                    if (raise || !__any_sync(0xffffffffu, sum[0].x + sum[0].y > 65504.f)) break;
                     raise = true;
                 }
-                l += total;
-                ck_tmem_st32(p, s_at);
-                ck_tmem_st32(p + 32, s_at + 32);
+                if (!ok) break;
+                l += sum[0].x + sum[0].y;
+                ck_tmem_st32(p, p_at);  // (over logits that were read)
                 ck_wait_st();
                 ck_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[t]);
+                if (lane == 0) mbar_arrive(&sm.p_full[t][done & 1]);
             }
             tile0 += n;
             if (ok && ns > 0) {
                 if (!(ok = wait(&sm.o_full[t], parts & 1))) break;
                 ++parts;
                 ck_fence_after();
-                float* out = g.from > 0      ? a.extra + ((size_t)blockIdx.x * CK_ROWS + CK_TILE * t + row) * PART_STRIDE
+                float* out = g.from > 0      ? a.extra + ((size_t)blockIdx.x * CK_ROWS + CK_ROW_TILE * t + row) * PART_STRIDE
                              : two || !t     ? a.main + at * PART_STRIDE
                              : a.second_rows ? a.second + (((int64_t)g.b * a.H_kv + g.h) * a.second_rows + row) * PART_STRIDE
                                              : a.second + at * PART_STRIDE;
@@ -940,7 +960,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
                     ck_tmem_ld32(o, o_at + 32 * c);
-                    ck_loaded(o);
+                    ck_loaded32(o);
                     if (live) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
@@ -954,10 +974,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
     __syncwarp();
     ck_fence_before();
     __syncthreads();
-    if (sm.dead && warp == 17)  // copies in flight land before the block ends
+    if (sm.dead && warp == CK_SOFTMAX + CK_UNPACK + 1)  // copies in flight land before the block ends
         for (uint32_t n = sm.stages, s = n > CK_RAW_STAGES ? n - CK_RAW_STAGES : 0; s < n; ++s)
             (void)mbar_wait_bounded(&sm.raw_full[s % CK_RAW_STAGES], (s / CK_RAW_STAGES) & 1, 1000000LL);
-    if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == CK_SOFTMAX + CK_UNPACK) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ------------------------------------------------------------------ 3: finish
@@ -972,18 +992,13 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
     // 32 g + 8 t + i and + 4; the next eight positions those after them.  (Read before the wait: the kernel that started
     // this one did so after its own.)
     const float* Rv = a.Rv + (size_t)h * D * D;
-#pragma unroll 4
+#pragma unroll
     for (int y = threadIdx.x; y < D * 4 * 4; y += 256) {
         const int tt = y & 3, g = (y >> 2) & 3, n = y >> 4;
         const float4* p = reinterpret_cast<const float4*>(Rv + (size_t)n * D + 32 * g + 8 * tt);
         const float4 u = __ldg(p), v = __ldg(p + 1);
-        uint4 f;
-        ck_parts(u.x, v.x, f.x, f.z);
-        ck_parts(u.y, v.y, f.y, f.w);
-        R.f[2 * g][n >> 3][4 * (n & 7) + tt] = f;
-        ck_parts(u.z, v.z, f.x, f.z);
-        ck_parts(u.w, v.w, f.y, f.w);
-        R.f[2 * g + 1][n >> 3][4 * (n & 7) + tt] = f;
+        R.f[2 * g][n >> 3][4 * (n & 7) + tt] = make_uint2(pack_half2(u.x, v.x), pack_half2(u.y, v.y));
+        R.f[2 * g + 1][n >> 3][4 * (n & 7) + tt] = make_uint2(pack_half2(u.z, v.z), pack_half2(u.w, v.w));
     }
     __syncthreads();
     griddep_wait();
@@ -995,12 +1010,17 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
         CkWalk w;
         w.e = x >> 4;
         w.read(a);
-        const int two = w.k.rows > CK_TILE, i0 = 16 * (x & 15);  // in the block
+        const int two = w.k.rows > CK_ROW_TILE, i0 = 16 * (x & 15);  // in the block
         if (i0 >= w.k.rows) continue;
         const int wt = ck_weight(w.k.rows);
         const int64_t unit = w.k.start * a.H_kv + (int64_t)h * w.k.cost;
-        const int c0 = w.k.tiles ? (int)(((unit + 1) * C - 1) / total) : 0;
-        const int c1 = w.k.tiles ? (int)(((unit + (int64_t)wt * (w.k.tiles - 1) + 1) * C - 1) / total) : -1;
+        // the share that holds the unit's first tile: a guess, put right by the cuts themselves
+        int c = 0;
+        if (w.k.tiles) {
+            c = min(C - 1, (int)((float)unit / (float)total * (float)C));
+            while (__ldcg(a.cut + c) > unit) --c;
+            while (__ldcg(a.cut + c + 1) <= unit) ++c;
+        }
         float M[2] = {CK_NEG, CK_NEG}, L[2] = {0.f, 0.f};
         float2 o[8][4];  // [K step][row, + 8; the next eight positions]
 #pragma unroll
@@ -1033,25 +1053,36 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
                     o[ks][e] = make_float2(fmaf(o[ks][e].x, keep[e & 1], y[ks][e].x * take[e & 1]), fmaf(o[ks][e].y, keep[e & 1], y[ks][e].y * take[e & 1]));
         };
 #pragma unroll 1
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t b0 = max(ck_cut(total, c, C), unit), b1 = min(ck_cut(total, c + 1, C), unit + w.k.cost);
-            const int from = (int)((b0 - unit + wt - 1) / wt), n = min(w.k.tiles, (int)((b1 - unit + wt - 1) / wt)) - from;
+        for (int from = 0, n; from < w.k.tiles; from += n, ++c) {
+            n = min(w.k.tiles, ((int)min(__ldcg(a.cut + c + 1) - unit, (int64_t)w.k.cost) + wt - 1) / wt) - from;
             if (n <= 0) continue;
             const float* extra = a.extra + (size_t)c * CK_ROWS * PART_STRIDE;
 #pragma unroll 1
             for (int s = 0; s < (two || n == 1 ? 1 : 2); ++s)  // (one row tile: a second stream, if there was a second tile)
-                merge(from > 0         ? extra + (size_t)s * CK_TILE * PART_STRIDE
+                merge(from > 0         ? extra + (size_t)s * CK_ROW_TILE * PART_STRIDE
                       : !s            ? a.main + at * PART_STRIDE
                       : a.second_rows ? a.second + ((int64_t)w.k.b * a.H_kv + h) * a.second_rows * PART_STRIDE
                                       : a.second + at * PART_STRIDE);
         }
-        uint32_t hi[8][4], lo[8][4];
+        uint32_t x16[8][4];
+        float back[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) L[e] = L[e] > 0.f ? 1.f / L[e] : (L[e] == L[e] ? 0.f : L[e]);  // no token: 0; NaN stays NaN
+        for (int e = 0; e < 2; ++e) {
+            float top = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+            for (int ks = 0; ks < 8; ++ks)
+                top = fmaxf(fmaxf(top, fmaxf(fabsf(o[ks][e].x), fabsf(o[ks][e].y))), fmaxf(fabsf(o[ks][e + 2].x), fabsf(o[ks][e + 2].y)));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float sigma = ck_scale(top);
+            // (no token: 0; NaN stays NaN)
+            back[e] = (L[e] > 0.f ? 1.f / L[e] : L[e] == L[e] ? 0.f : L[e]) / sigma;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ck_parts(o[ks][e].x * L[e & 1], o[ks][e].y * L[e & 1], hi[ks][e], lo[ks][e]);
+            for (int ks = 0; ks < 8; ++ks) {
+                x16[ks][e] = pack_half2(o[ks][e].x * sigma, o[ks][e].y * sigma);
+                x16[ks][e + 2] = pack_half2(o[ks][e + 2].x * sigma, o[ks][e + 2].y * sigma);
+            }
+        }
         __nv_bfloat16* out[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -1069,17 +1100,15 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
             for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint4 b = R.f[ks][nt + j][lane];
-                    ck_mma(c[j], lo[ks], b.x, b.y);
-                    ck_mma(c[j], hi[ks], b.z, b.w);
-                    ck_mma(c[j], hi[ks], b.x, b.y);
+                    const uint2 b = R.f[ks][nt + j][lane];
+                    mma_f16_16816(c[j], x16[ks], b.x, b.y);
                 }
             // a lane's two columns of four sets become eight of one: lane t gets set nt + t
             uint32_t z[2][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) z[e][j] = ck_pack(c[j][2 * e], c[j][2 * e + 1]);
+                for (int j = 0; j < 4; ++j) z[e][j] = ck_pack(c[j][2 * e] * back[e], c[j][2 * e + 1] * back[e]);
 #pragma unroll
                 for (int k = 1; k < 4; k <<= 1) {  // transpose of the four lanes' four words
 #pragma unroll
@@ -1114,24 +1143,25 @@ static const char* chunk_refusal(int n_tok, int B, int H_q, int H_kv, kvq_status
 }
 
 struct ChunkLayout {
-    size_t plan, block, scale, rot, main, second, extra, total;
+    size_t plan, cut, block, scale, rot, main, second, extra, total;
     int max_blocks;
     int64_t second_rows;
 };
 static ChunkLayout chunk_layout(int n_tok, int B, int H_q, int H_kv) {
     const int64_t G = H_q / H_kv, rows = (int64_t)n_tok * H_q, part = PART_STRIDE * 4;
     // second streams: of blocks of one row tile, at most one per sequence
-    const bool few = (int64_t)B * H_kv * CK_TILE < rows;
+    const bool few = (int64_t)B * H_kv * CK_ROW_TILE < rows;
     ChunkLayout l;
     l.max_blocks = (int)((int64_t)n_tok * G / CK_ROWS + B);
-    l.second_rows = few ? CK_TILE : 0;
+    l.second_rows = few ? CK_ROW_TILE : 0;
     l.plan = WS_HEADER;
-    l.block = align_up(l.plan + sizeof(CkPlan), 256);
+    l.cut = l.plan + 256;
+    l.block = align_up(l.cut + (size_t)(kvq_device_sm_count() + 1) * 8, 256);
     l.scale = align_up(l.block + (size_t)l.max_blocks * sizeof(CkBlock), 256);
     l.rot = align_up(l.scale + (size_t)rows * 4, 256);
     l.main = align_up(l.rot + (size_t)rows * D * 2, 256);
     l.second = align_up(l.main + (size_t)(rows * part), 256);
-    l.extra = align_up(l.second + (size_t)((few ? (int64_t)B * H_kv * CK_TILE : rows) * part), 256);
+    l.extra = align_up(l.second + (size_t)((few ? (int64_t)B * H_kv * CK_ROW_TILE : rows) * part), 256);
     l.total = l.extra + (size_t)kvq_device_sm_count() * CK_ROWS * part;
     return l;
 }
@@ -1211,6 +1241,7 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     a.out = static_cast<__nv_bfloat16*>(out);
     a.error = reinterpret_cast<uint32_t*>(ws);
     a.plan = reinterpret_cast<CkPlan*>(ws + l.plan);
+    a.cut = reinterpret_cast<int64_t*>(ws + l.cut);
     a.block = reinterpret_cast<CkBlock*>(ws + l.block);
     a.max_blocks = l.max_blocks;
     a.row_scale = reinterpret_cast<float*>(ws + l.scale);
@@ -1224,7 +1255,7 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     st = chunk_smem_once();
     if (st != KVQ_OK) return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const int64_t row_tiles = ((int64_t)n_tok * a.G + CK_TILE - 1) / CK_TILE;
+    const int64_t row_tiles = ((int64_t)n_tok * a.G + CK_ROW_TILE - 1) / CK_ROW_TILE;
     auto capped = [&](int64_t want) { return (unsigned)std::min(want, std::max<int64_t>(1, 4 * a.ctas / H_kv)); };  // CTAs per head
     st = kvq_check_cuda(launch_pdl(chunk_rotate_kernel, dim3(capped(row_tiles) + 1, H_kv), dim3(256), sizeof(CkRotate), cs, a),
                         "kvq_chunk_attn_int4 rotate launch");

@@ -236,8 +236,9 @@ def to_bf16(y):
 def chunk(q, q_start, cache, block_table, ctx_lens, rk32, rv32, scale, window: int = 0, sinks: int = 0):
     """Attention of each sequence's last tokens: row q_start[b] + i at position ctx - n_b + i sees cached tokens t <= it
     (window > 0: t > it - window or t < sinks); pages outside the pool are dropped.  Returns out [n, H_q, d] and the bound
-    [n, H_q] on the 2-norm of what rounding the rotated queries, the cached keys and values and the weights to fp16 once
-    each does to it: products' roundings are independent and taken at six standard deviations, weights and values at 2^-11."""
+    [n, H_q] on the 2-norm of what rounding to fp16 does to it: of the rotation's entries, the rotated queries and the cached
+    keys once each (each at most 2^-11 of a product's term, in standard deviation 2^-11 / sqrt(3); the three are independent
+    and taken at six standard deviations), of the weights, the values, the sums and the output rotation's entries at 2^-11."""
     q = np.asarray(q, np.float64)
     h_q, d = q.shape[1:]
     h_kv = cache.shape[1]
@@ -271,7 +272,7 @@ def chunk(q, q_start, cache, block_table, ctx_lens, rk32, rv32, scale, window: i
                 w /= np.where(any_row, w.sum(1), 1.0)[:, None]
                 o = w @ v
                 out[rows, j] = o @ rv.T
-                e = 6 * np.sqrt(2 / 3) * 2.0 ** -11 * abs(sc) * np.sqrt((qr * qr) @ (k * k).T) + 2.0 ** -11
+                e = 6 * 2.0 ** -11 * abs(sc) * np.sqrt((qr * qr) @ (k * k).T) + 2.0 ** -11
                 e = np.where(see, e, 0.0)
-                bound[rows, j] = (w * e) @ size + 2.0 ** -11 * (w @ size) + (w * e).sum(1) * np.linalg.norm(o, axis=1) + 1e-6 * size.max(initial=0.0)
+                bound[rows, j] = (w * e) @ size + 2.0 ** -11 * (w @ size) + 2.0 ** -10 * np.linalg.norm(o, axis=1) + (w * e).sum(1) * np.linalg.norm(o, axis=1) + 1e-6 * size.max(initial=0.0)
     return out, bound
