@@ -308,15 +308,17 @@ def kvq_append_int4(k, v, slot_mapping, mu_k, R_k, R_v, cache, num_pages: int, c
 
 
 def _heads(x, n_tok, dev: int, name: str):
-    """Device pointer and token stride of x [n_tok, heads, 128], each token's heads one behind the other."""
-    if x.dim() != 3 or x.shape[0] != n_tok:
-        raise ValueError(f"{name} must have shape ({n_tok}, heads, d), got {tuple(x.shape)}")
+    """Device pointer and token stride of x [n_tok, heads, d], each token's heads one behind the other."""
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != n_tok:
+        raise ValueError(f"{name} must have shape ({n_tok}, heads, d), got {tuple(shape)}")
     if x.dtype is not _BF16 or x.get_device() != dev:
         _ptr(x, _BF16, None, dev, name)
-    _, s1, s2 = x.stride()
-    if x.numel() and ((s2 != 1 and x.shape[2] > 1) or (s1 != x.shape[2] and x.shape[1] > 1)):
+        raise ValueError(f"{name} must be {_BF16} on the current device")
+    _, h, d = shape
+    if (strides[2] != 1 and d > 1) or (strides[1] != d and h > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return x.data_ptr(), x.stride(0) if n_tok > 1 else x.shape[1] * x.shape[2]
+    return x.data_ptr(), strides[0] if n_tok > 1 else h * d
 
 
 def kvq_append_rope_int4(q, k, v, positions, rope, slot_mapping, mu_k, R_k, R_v, cache, num_pages: int, q_out, k_out,
