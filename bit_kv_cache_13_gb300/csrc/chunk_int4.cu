@@ -24,7 +24,11 @@ constexpr int CK_ROW_TILE = 128;
 constexpr int CK_PAGES = 4, CK_TILE = CK_PAGES * PAGE;  // pages and cached tokens of a tile
 constexpr int CK_UNIT_COST = 24;   // what starting a block costs, in tiles of one row tile
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
-constexpr float CK_LIFT = 7.f;     // weights are carried 2^7 times as large: they use fp16 from 2^15 down
+// A weight is carried as 2^CK_LIFT times itself relative to the row's reference, its largest logit in the first tile, or
+// where the reference was last raised.  fp16 ends 13 powers of two above, and a weight 17 below keeps its 11 bits (one
+// further below, 2^-28 of the reference's).  Raising drains the stream's products: with 9 powers above, one tile in fifty
+// raised some row of a warp, and 2K tokens of 32K took 994 us instead of 954.
+constexpr float CK_LIFT = 3.f;
 constexpr long long CK_SHORT_WAIT_CYCLES = 2000000LL;
 
 // Rows [r0, r0 + rows) of sequence b (row = token * G + head of the group), and the pages
