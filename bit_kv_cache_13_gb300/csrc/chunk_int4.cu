@@ -228,9 +228,9 @@ __host__ __device__ constexpr int ck_key_at(int ch) { return (ch & ~7) | (ch & 3
 // CTAs of 256 threads, 128 rows each (a warp 16); the last CTA of a head's row makes the plan.
 struct __align__(16) CkRotate {
     CkMatrix R;
-    __align__(16) __half out[8][16][D + 8];
+    __align__(16) __half out[8][16][D / 2 + 8];  // half a row at a time, so that four CTAs share an SM
 };
-__global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     CkRotate& sm = *reinterpret_cast<CkRotate*>(smem_raw);
     griddep_wait();
@@ -298,27 +298,30 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const __grid_constant
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 x[ks][e] = pack_half2(__uint_as_float(x[ks][e] << 16) * f[e & 1], __uint_as_float(x[ks][e] & 0xffff0000u) * f[e & 1]);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
 #pragma unroll 4
-        for (int nt = 0; nt < 16; ++nt) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int nt = 0; nt < 8; ++nt) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint2 b = sm.R.f[ks][nt][lane];
-                mma_f16_16816(c, x[ks], b.x, b.y);
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint2 b = sm.R.f[ks][8 * part + nt][lane];
+                    mma_f16_16816(c, x[ks], b.x, b.y);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) *reinterpret_cast<uint32_t*>(&sm.out[warp][r + 8 * e][8 * nt + 2 * t]) = pack_half2(c[2 * e], c[2 * e + 1]);
             }
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 2; ++e) *reinterpret_cast<uint32_t*>(&sm.out[warp][r + 8 * e][8 * nt + 2 * t]) = pack_half2(c[2 * e], c[2 * e + 1]);
+            for (int i = 0; i < 4; ++i) {  // four rows at a time, 16 bytes a lane
+                const int y = 4 * i + (lane >> 3);
+                if (r0 + y < rows)
+                    *reinterpret_cast<uint4*>(a.rot + ((int64_t)h * rows + r0 + y) * D + 64 * part + 8 * (lane & 7)) = lds128(&sm.out[warp][y][8 * (lane & 7)]);
+            }
+            __syncwarp();
         }
         const int64_t next = r0 + (int64_t)(gridDim.x - 1) * 128;
         if (next < rows) fetch(next, x);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // two rows at a time, 16 bytes a lane
-            const int y = 2 * i + (lane >> 4);
-            if (r0 + y < rows)
-                *reinterpret_cast<uint4*>(a.rot + ((int64_t)h * rows + r0 + y) * D + 8 * (lane & 15)) = lds128(&sm.out[warp][y][8 * (lane & 15)]);
-        }
-        __syncwarp();
     }
 }
 
@@ -1260,13 +1263,13 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     if (st != KVQ_OK) return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int64_t row_tiles = ((int64_t)n_tok * a.G + CK_ROW_TILE - 1) / CK_ROW_TILE;
-    auto capped = [&](int64_t want) { return (unsigned)std::min(want, std::max<int64_t>(1, 4 * a.ctas / H_kv)); };  // CTAs per head
-    st = kvq_check_cuda(launch_pdl(chunk_rotate_kernel, dim3(capped(row_tiles) + 1, H_kv), dim3(256), sizeof(CkRotate), cs, a),
+    auto capped = [&](int64_t want, int per_sm) { return (unsigned)std::min(want, std::max<int64_t>(1, per_sm * a.ctas / H_kv)); };  // CTAs per head
+    st = kvq_check_cuda(launch_pdl(chunk_rotate_kernel, dim3(capped(row_tiles, 4) + 1, H_kv), dim3(256), sizeof(CkRotate), cs, a),
                         "kvq_chunk_attn_int4 rotate launch");
     if (st != KVQ_OK) return st;
     st = kvq_check_cuda(launch_pdl(chunk_stream_kernel, dim3(a.ctas), dim3(CK_THREADS), sizeof(CkSmem) + 1024, cs, a),
                         "kvq_chunk_attn_int4 launch");
     if (st != KVQ_OK) return st;
-    return kvq_check_cuda(launch_pdl(chunk_finish_kernel, dim3(capped(2 * (int64_t)l.max_blocks), H_kv), dim3(256), sizeof(CkMatrix), cs, a),
+    return kvq_check_cuda(launch_pdl(chunk_finish_kernel, dim3(capped(2 * (int64_t)l.max_blocks, 4), H_kv), dim3(256), sizeof(CkMatrix), cs, a),
                           "kvq_chunk_attn_int4 finish launch");
 }
