@@ -19,10 +19,13 @@
 
 namespace kvq {
 
-constexpr int CK_ROWS = 256;       // rows of a block: two row tiles of 128
+constexpr int CK_ROWS = 256;       // most rows of a block: two row tiles of 128
 constexpr int CK_ROW_TILE = 128;
 constexpr int CK_PAGES = 4, CK_TILE = CK_PAGES * PAGE;  // pages and cached tokens of a tile
-constexpr int CK_UNIT_COST = 24;   // what starting a block costs, in tiles of one row tile
+// What starting a block costs, in tiles of one row tile: its queries' way in, a pipeline filled and drained, its sums' way
+// out.  A 4K prompt: 484 us for 6, 334 for 16, 300 for 24, 301 for 32; 8 x 5 tokens at 32K, in blocks of one row tile:
+// 179 us for 6, 182 for 24.
+constexpr int CK_UNIT_COST = 24, CK_UNIT_COST_FEW = 6;
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // A weight is carried as 2^CK_LIFT times itself relative to the row's reference, its largest logit in the first tile, or
 // where the reference was last raised.  fp16 ends 13 powers of two above, and a weight 17 below keeps its 11 bits (one
@@ -64,7 +67,7 @@ struct ChunkArgs {
     CkPlan* plan;
     int64_t* cut;         // [ctas + 1]: where the cost of all heads is cut into shares
     CkBlock* block;       // [max_blocks]
-    int max_blocks;
+    int max_blocks, block_rows;
     __half* rot;          // q' [H_kv][n_tok * G][D], channels in the order of the unpacked keys
     float* row_scale;     // [H_kv][n_tok * G]: logit = product * row_scale
     float* main;          // [H_kv * n_tok * G][PART_STRIDE] partials of the shares that begin a block
@@ -86,7 +89,7 @@ __device__ __forceinline__ int2 ck_tokens(const ChunkArgs& a, int b) {
     }
     return make_int2(s, e - s);
 }
-__device__ __forceinline__ int ck_blocks(int n, int G) { return (int)(((int64_t)n * G + CK_ROWS - 1) / CK_ROWS); }
+__device__ __forceinline__ int ck_blocks(const ChunkArgs& a, int n) { return (int)(((int64_t)n * a.G + a.block_rows - 1) / a.block_rows); }
 
 __device__ __forceinline__ int ck_weight(int rows) { return rows > CK_ROW_TILE ? 2 : 1; }
 
@@ -118,12 +121,12 @@ __device__ void ck_make_plan(const ChunkArgs& a) {
     __shared__ int sums32[8];
     const int tid = threadIdx.x, per = (a.B + 255) / 256, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int own = 0, n_blocks;
-    for (int b = b0; b < b1; ++b) own += ck_blocks(ck_tokens(a, b).y, a.G);
+    for (int b = b0; b < b1; ++b) own += ck_blocks(a, ck_tokens(a, b).y);
     int at = ck_scan(own, sums32, n_blocks);
     for (int b = b0; b < b1; ++b) {
         const int2 t = ck_tokens(a, b);
         const int ctx = (int)min((int64_t)max(0, __ldg(a.context_lens + b)), (int64_t)a.max_pages * PAGE);
-        for (int x = 0, n = ck_blocks(t.y, a.G); x < n && at < a.max_blocks; ++x, ++at) {
+        for (int x = 0, n = ck_blocks(a, t.y); x < n && at < a.max_blocks; ++x, ++at) {
             CkBlock& k = a.block[at];
             k.b = b;
             k.q0 = t.x;
@@ -140,8 +143,8 @@ __device__ void ck_make_plan(const ChunkArgs& a) {
         CkBlock k = {};
         if (e < n_blocks) {
             k = a.block[e];
-            k.r0 = k.index_in_b * CK_ROWS;
-            k.rows = (int)min((int64_t)CK_ROWS, (int64_t)k.n * a.G - k.r0);
+            k.r0 = k.index_in_b * a.block_rows;
+            k.rows = (int)min((int64_t)a.block_rows, (int64_t)k.n * a.G - k.r0);
             const int first = k.ctx - k.n + k.r0 / a.G, last = k.ctx - k.n + (k.r0 + k.rows - 1) / a.G;  // positions
             k.pages = k.sinks = k.skip = k.tiles = k.cost = 0;
             if (last >= 0) {
@@ -151,7 +154,7 @@ __device__ void ck_make_plan(const ChunkArgs& a) {
                 k.skip = fp - k.sinks;
                 k.pages = last / PAGE + 1 - k.skip;
                 k.tiles = (k.pages + CK_PAGES - 1) / CK_PAGES;
-                k.cost = ck_weight(k.rows) * k.tiles + CK_UNIT_COST;
+                k.cost = ck_weight(k.rows) * k.tiles + (a.block_rows == CK_ROWS ? CK_UNIT_COST : CK_UNIT_COST_FEW);
             }
         }
         int64_t total;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
 //   shared   Q [stream], K and V [4 stages] as K-major operands in the 128-byte swizzle (V
 //            transposed: rows are channels), three raw stages
 constexpr int CK_QUERIES = CK_ROW_TILE * D * 2, CK_OPERAND = CK_TILE * D * 2;  // bytes
-constexpr int CK_RAW = CK_PAGES * INT4_TILE, CK_RAW_STAGES = 3, CK_STAGES = 4, CK_INFOS = 8, CK_SHARES = 4;
+constexpr int CK_RAW = CK_PAGES * INT4_TILE, CK_STAGES = 4, CK_INFOS = 8, CK_SHARES = 4;
 constexpr int CK_SOFTMAX = 8, CK_UNPACK = 16;  // warps
 // (Registers: 896 threads of 72 at launch; 128 for softmax, 48 for unpacking and 56 for the rest are those 64512.)
 constexpr int CK_THREADS = 32 * (CK_SOFTMAX + CK_UNPACK + 4);
@@ -355,19 +358,23 @@ struct __align__(16) CkShare {  // what the roles need of a share
     int64_t row0;               // the sequence's first row among all of a head's
     int h, end;
 };
+// FEW: blocks of one row tile only.  One copy of the queries serves both streams, and six raw stages instead of three
+// cover the cache's latency: such calls are bound by reading it (8 x 5 tokens at 32K: 208 us with three).
+template <bool FEW>
 struct __align__(1024) CkSmem {
-    uint8_t q[2][CK_QUERIES], k[CK_STAGES][CK_OPERAND], v[CK_STAGES][CK_OPERAND];
-    uint8_t raw[CK_RAW_STAGES][CK_RAW];
+    static constexpr int RAW_STAGES = FEW ? 6 : 3;
+    uint8_t q[FEW ? 1 : 2][CK_QUERIES], k[CK_STAGES][CK_OPERAND], v[CK_STAGES][CK_OPERAND];
+    uint8_t raw[RAW_STAGES][CK_RAW];
     CkInfo info[CK_INFOS];
     CkShare share[CK_SHARES];
-    __align__(16) int raw_base[CK_RAW_STAGES][CK_PAGES];
-    uint64_t raw_full[CK_RAW_STAGES], raw_free[CK_RAW_STAGES], k_full[CK_STAGES], k_free[CK_STAGES], v_full[CK_STAGES], v_free[CK_STAGES];
-    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
+    __align__(16) int raw_base[RAW_STAGES][CK_PAGES];
+    uint64_t raw_full[RAW_STAGES], raw_free[RAW_STAGES], k_full[CK_STAGES], k_free[CK_STAGES], v_full[CK_STAGES], v_free[CK_STAGES];
+    uint64_t q_full[2], q_free, s_full[2][2], p_full[2][2], o_done[2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
     uint32_t tmem;
     int dead;
     uint32_t stages;  // raw stages fetched
 };
-static_assert(sizeof(CkSmem) + 1024 <= 227 * 1024, "chunk shared memory above 227 KB");
+static_assert(sizeof(CkSmem<false>) + 1024 <= 227 * 1024 && sizeof(CkSmem<true>) + 1024 <= 227 * 1024, "chunk shared memory above 227 KB");
 
 // Descriptor of an operand, K-major in the 128-byte swizzle: atoms of 8 rows, 1024 bytes apart.  Its low word holds the
 // address in 16-byte units.
@@ -483,23 +490,26 @@ struct CkConst {
     }
 };
 
+template <bool FEW>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    CkSmem& sm = *reinterpret_cast<CkSmem*>(smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024);
+    constexpr int CK_RAW_STAGES = CkSmem<FEW>::RAW_STAGES;
+    CkSmem<FEW>& sm = *reinterpret_cast<CkSmem<FEW>*>(smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < CK_RAW_STAGES; ++i) {
             mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_free[i], CK_UNPACK);
+            mbar_init(&sm.raw_free[i], CK_UNPACK / 2);
         }
         for (int i = 0; i < CK_STAGES; ++i) {
-            mbar_init(&sm.k_full[i], CK_UNPACK / 2);
-            mbar_init(&sm.v_full[i], CK_UNPACK / 2);
+            mbar_init(&sm.k_full[i], CK_UNPACK / 4);
+            mbar_init(&sm.v_full[i], CK_UNPACK / 4);
             mbar_init(&sm.k_free[i], 2);
             mbar_init(&sm.v_free[i], 2);
         }
+        mbar_init(&sm.q_free, CK_SOFTMAX);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.q_full[i], FEW ? 8 : 4);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&sm.s_full[i][h], 1);
                 mbar_init(&sm.p_full[i][h], 4);
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             uint32_t tile0 = 0, done = 0;  // tiles before this share, of this stream
             bool ok = true;
             const bool leader = ck_elect();
-            const uint32_t q_lo = ck_desc_lo(sm.q[t]), k_lo = ck_desc_lo(sm.k[0]), v_lo = ck_desc_lo(sm.v[0]);
+            const uint32_t q_lo = ck_desc_lo(sm.q[FEW ? 0 : t]), k_lo = ck_desc_lo(sm.k[0]), v_lo = ck_desc_lo(sm.v[0]);
             const uint32_t s_at = tmem + 128 * t, o_at = tmem + 256 + 128 * t;
             while (ok && next_share()) {
                 const CkShare& g = sm.share[(n_share - 1) % CK_SHARES];
@@ -714,38 +724,45 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // (keys on two of the four schedulers and values on the others: with both, and the softmax, on each, warps waited
         // for instructions more than for anything else)
-        const int part = (warp & 1) | ((warp - CK_SOFTMAX) >> 1 & ~1);  // of eight warps
+        // Four warps take the even tiles of tokens and four the odd ones: a warp's chain of waits, loads and stores over one
+        // tile covers another's.
+        const int part = (warp & 1) | (warp - CK_SOFTMAX) >> 2 & 2;
+        const uint32_t odd = (warp - CK_SOFTMAX) >> 2 & 1;
         uint32_t tile = 0;
         bool ok = true;
         const CkConst cc;
         if (!(warp & 2)) {
-            // ---- keys: a thread takes a token's words t of all groups
-            const int t = lane & 3, tok = 8 * part + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
-            const uint32_t from = (tok >> 4) * INT4_TILE + O4_KC + 64 * (tok & 15) + 16 * t, meta_from = (tok >> 4) * INT4_TILE + O4_KM + 16 * (tok & 15);
+            // ---- keys: a thread takes the words t of all groups of two tokens
+            const int t = lane & 3, tok = 16 * part + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
+            const uint32_t from = part * INT4_TILE + O4_KC + 64 * (tok & 15) + 16 * t, meta_from = part * INT4_TILE + O4_KM + 16 * (tok & 15);
             const uint32_t to0 = tok * 128 + ((t ^ (tok & 7)) << 4), to1 = tok * 128 + (((4 + t) ^ (tok & 7)) << 4);
             while (ok && next_share()) {
                 const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
                 for (int i = share.n; i > 0; --i, ++tile) {
+                    if ((tile & 1) != odd) continue;
                     const uint32_t st = tile % CK_STAGES, slot = tile % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
                     if (tile >= CK_STAGES && !(ok = wait(&sm.k_free[st], (tile / CK_STAGES - 1) & 1))) break;
-                    const uint4 codes = lds128(sm.raw[slot] + from), meta = lds128(sm.raw[slot] + meta_from);
-                    const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
                     const __half2 tiny = u32_as_h2(cc.sixteenth);  // with it no key leaves fp16
-                    const __half2 s01 = __hmul2(u32_as_h2(meta.x), tiny), s23 = __hmul2(u32_as_h2(meta.y), tiny);
-                    const __half2 m01 = __hmul2(u32_as_h2(meta.z), tiny), m23 = __hmul2(u32_as_h2(meta.w), tiny);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const __half2 s = g & 1 ? __high2half2(g < 2 ? s01 : s23) : __low2half2(g < 2 ? s01 : s23);
-                        const __half2 m = g & 1 ? __high2half2(g < 2 ? m01 : m23) : __low2half2(g < 2 ? m01 : m23);
-                        __half2 c[4];
-                        cc.codes(word[g], c);
-                        *reinterpret_cast<uint4*>(sm.k[st] + (g >> 1) * (CK_OPERAND / 2) + (g & 1 ? to1 : to0)) =
-                            make_uint4(h2_as_u32(__hfma2(c[0], s, m)), h2_as_u32(__hfma2(c[1], s, m)), h2_as_u32(__hfma2(c[2], s, m)),
-                                       h2_as_u32(__hfma2(c[3], s, m)));
+                    for (int e = 0; e < 2; ++e) {  // tokens tok and tok + 8
+                        const uint4 codes = lds128(sm.raw[slot] + from + 512 * e), meta = lds128(sm.raw[slot] + meta_from + 128 * e);
+                        const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
+                        const __half2 s01 = __hmul2(u32_as_h2(meta.x), tiny), s23 = __hmul2(u32_as_h2(meta.y), tiny);
+                        const __half2 m01 = __hmul2(u32_as_h2(meta.z), tiny), m23 = __hmul2(u32_as_h2(meta.w), tiny);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const __half2 s = g & 1 ? __high2half2(g < 2 ? s01 : s23) : __low2half2(g < 2 ? s01 : s23);
+                            const __half2 m = g & 1 ? __high2half2(g < 2 ? m01 : m23) : __low2half2(g < 2 ? m01 : m23);
+                            __half2 c[4];
+                            cc.codes(word[g], c);
+                            *reinterpret_cast<uint4*>(sm.k[st] + (g >> 1) * (CK_OPERAND / 2) + (g & 1 ? to1 : to0) + 1024 * e) =
+                                make_uint4(h2_as_u32(__hfma2(c[0], s, m)), h2_as_u32(__hfma2(c[1], s, m)), h2_as_u32(__hfma2(c[2], s, m)),
+                                           h2_as_u32(__hfma2(c[3], s, m)));
+                        }
                     }
                     CkInfo& info = sm.info[tile % CK_INFOS];
-                    if (part < CK_PAGES) {  // values that are not finite: a warp looks at a page's scales and mins, a slot pair of either a lane
+                    {   // values that are not finite: a warp looks at a page's scales and mins, a slot pair of either a lane
                         const uint4 y = lds128(sm.raw[slot] + part * INT4_TILE + O4_VS + 16 * (lane & 15));
                         const __half2 top = __hmax2_nan(__hmax2_nan(__habs2(u32_as_h2(y.x)), __habs2(u32_as_h2(y.y))),
                                                         __hmax2_nan(__habs2(u32_as_h2(y.z)), __habs2(u32_as_h2(y.w))));
@@ -756,7 +773,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             for (int o = 8; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
                         }
                         if (lane == 0) info.poison[part] = sm.raw_base[slot][part] < 0 ? 0u : bad;
-                    } else if (part == CK_PAGES) {
+                    }
+                    if (part == 0) {
                         const int at = sm.raw_base[slot][lane & 3];
                         bool cut[2];
 #pragma unroll
@@ -775,61 +793,60 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 }
             }
         } else {
-            // ---- values: a thread takes the words r of eight tokens and a group
-            const int r = lane & 7, oct = 4 * (part & 1) + (lane >> 3), g = part >> 1, pair0 = 4 * (oct & 1);
-            const uint32_t from = (oct >> 1) * INT4_TILE + O4_VC + 128 * pair0 + 16 * r + 4 * g, meta_from = (oct >> 1) * INT4_TILE + O4_VS + 16 * pair0 + 4 * g;
-            const uint32_t to = (32 * g + r) * 128 + ((oct ^ r) << 4);
+            // ---- values: a thread takes the words r of eight tokens and two groups
+            const int r = lane & 7, oct = 4 * (part & 1) + (lane >> 3), g0 = part & 2, pair0 = 4 * (oct & 1);
+            const uint32_t from = (oct >> 1) * INT4_TILE + O4_VC + 128 * pair0 + 16 * r + 4 * g0, meta_from = (oct >> 1) * INT4_TILE + O4_VS + 16 * pair0 + 4 * g0;
+            const uint32_t to = (32 * g0 + r) * 128 + ((oct ^ r) << 4);
             while (ok && next_share()) {
                 const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
                 for (int i = share.n; i > 0; --i, ++tile) {
+                    if ((tile & 1) != odd) continue;
                     const uint32_t st = tile % CK_STAGES, slot = tile % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
                     if (tile >= CK_STAGES && !(ok = wait(&sm.v_free[st], (tile / CK_STAGES - 1) & 1))) break;
                     const uint8_t *cp = sm.raw[slot] + from, *mp = sm.raw[slot] + meta_from;
-                    uint32_t code[4], sc[4], mn[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        code[p] = lds32(cp + 128 * p);
-                        sc[p] = lds32(mp + 16 * p);
-                        mn[p] = lds32(mp + 16 * p + (O4_VM - O4_VS));
-                    }
                     const int base = sm.raw_base[slot][oct >> 1];
                     // tokens of the octet within the context, none without a page
                     const int valid = base < 0 ? 0 : min(8, max(0, share.ctx - base - 2 * pair0));
                     // a lane looks at one pair's scales or mins: those from 2^11 or 2^15 up, and NaN, take the long way
-                    const __half2 look = __habs2(u32_as_h2(lds32(mp + 16 * (r & 3) + (r & 4 ? O4_VM - O4_VS : 0))));
+                    const uint2 look = lds64(mp + 16 * (r & 3) + (r & 4 ? O4_VM - O4_VS : 0));
+                    const __half2 most = __hmax2_nan(__habs2(u32_as_h2(look.x)), __habs2(u32_as_h2(look.y)));
                     const float edge = r & 4 ? 32768.f : 2048.f;
-                    const bool plain = valid == 8 && __low2float(look) < edge && __high2float(look) < edge;
-                    uint32_t x[4][4];
-                    if (__all_sync(0xffffffffu, plain)) {
+                    const bool plain = valid == 8 && __low2float(most) < edge && __high2float(most) < edge, all = __all_sync(0xffffffffu, plain);
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            __half2 c[4];
-                            cc.codes(code[p], c);
+                    for (int g = 0; g < 2; ++g, cp += 4, mp += 4) {
+                        uint32_t x[4][4];
+                        if (all) {
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) x[n][p] = h2_as_u32(__hfma2(c[n], u32_as_h2(sc[p]), u32_as_h2(mn[p])));
-                        }
-                    } else {
-                        // in fp32, cut off at fp16's ends; tokens past the context are 0, and so are those that hold what is not
-                        // finite, whose logits the softmax makes NaN instead (a weight of 0 would not hide it from other rows)
+                            for (int p = 0; p < 4; ++p) {
+                                const uint32_t s = lds32(mp + 16 * p), m = lds32(mp + 16 * p + (O4_VM - O4_VS));
+                                __half2 c[4];
+                                cc.codes(lds32(cp + 128 * p), c);
+#pragma unroll
+                                for (int n = 0; n < 4; ++n) x[n][p] = h2_as_u32(__hfma2(c[n], u32_as_h2(s), u32_as_h2(m)));
+                            }
+                        } else {
+                            // in fp32, cut off at fp16's ends; tokens past the context are 0, and so are those that hold what is not
+                            // finite, whose logits the softmax makes NaN instead (a weight of 0 would not hide it from other rows)
 #pragma unroll 1
-                        for (int p = 0; p < 4; ++p) {
-                            const uint32_t c = lds32(cp + 128 * p);
-                            const float2 s = __half22float2(u32_as_h2(lds32(mp + 16 * p))), m = __half22float2(u32_as_h2(lds32(mp + 16 * p + (O4_VM - O4_VS))));
-                            const bool lo_ok = 2 * p < valid && isfinite(s.x) && isfinite(m.x), hi_ok = 2 * p + 1 < valid && isfinite(s.y) && isfinite(m.y);
+                            for (int p = 0; p < 4; ++p) {
+                                const uint32_t c = lds32(cp + 128 * p);
+                                const float2 s = __half22float2(u32_as_h2(lds32(mp + 16 * p))), m = __half22float2(u32_as_h2(lds32(mp + 16 * p + (O4_VM - O4_VS))));
+                                const bool lo_ok = 2 * p < valid && isfinite(s.x) && isfinite(m.x), hi_ok = 2 * p + 1 < valid && isfinite(s.y) && isfinite(m.y);
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                const float lo = fmaf((float)(c >> (4 * n) & 15), s.x, m.x), hi = fmaf((float)(c >> (16 + 4 * n) & 15), s.y, m.y);
-                                const uint32_t y = pack_half2(lo_ok ? fminf(fmaxf(lo, -65504.f), 65504.f) : 0.f, hi_ok ? fminf(fmaxf(hi, -65504.f), 65504.f) : 0.f);
+                                for (int n = 0; n < 4; ++n) {
+                                    const float lo = fmaf((float)(c >> (4 * n) & 15), s.x, m.x), hi = fmaf((float)(c >> (16 + 4 * n) & 15), s.y, m.y);
+                                    const uint32_t y = pack_half2(lo_ok ? fminf(fmaxf(lo, -65504.f), 65504.f) : 0.f, hi_ok ? fminf(fmaxf(hi, -65504.f), 65504.f) : 0.f);
 #pragma unroll
-                                for (int pp = 0; pp < 4; ++pp)
-                                    if (pp == p) x[n][pp] = y;
+                                    for (int pp = 0; pp < 4; ++pp)
+                                        if (pp == p) x[n][pp] = y;
+                                }
                             }
                         }
-                    }
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        *reinterpret_cast<uint4*>(sm.v[st] + to + 8 * n * 128) = make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
+                        for (int n = 0; n < 4; ++n)
+                            *reinterpret_cast<uint4*>(sm.v[st] + to + (32 * g + 8 * n) * 128) = make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -853,15 +870,22 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             const bool live = in_block < g.rows;
             const int in_seq = g.r0 + (live ? in_block : 0), pos = g.pos0 + in_seq / a.G;
             const int64_t at = (int64_t)g.h * a.n_tok * a.G + g.row0 + in_seq;  // the row among all
-            {   // the row's queries (the stream's last product with the ones before is done: its sums were read)
+            // the row's queries: the last product with the ones before is done (FEW: of both streams)
+            if (FEW && n_share > 1 && !(ok = wait(&sm.q_free, n_share & 1))) break;
+            {
                 const uint4* src = reinterpret_cast<const uint4*>(a.rot + at * D);
-                uint8_t* dst = sm.q[t] + row * 128;
+                uint8_t* dst = sm.q[FEW ? 0 : t] + row * 128;
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * (CK_QUERIES / 2) + (((c & 7) ^ (row & 7)) << 4)) = __ldcg(src + c);
+                for (int c = 0; c < (FEW ? 8 : 16); ++c) {  // (FEW: half the channels each)
+                    const int y = FEW ? 8 * t + c : c;
+                    *reinterpret_cast<uint4*>(dst + (y >> 3) * (CK_QUERIES / 2) + (((y & 7) ^ (row & 7)) << 4)) = __ldcg(src + y);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.q_full[t]);
+                if (lane == 0) {
+                    mbar_arrive(&sm.q_full[t]);
+                    if constexpr (FEW) mbar_arrive(&sm.q_full[t ^ 1]);
+                }
             }
             const float f = __ldcg(a.row_scale + at);
             float ref = CK_NEG, l = 0.f;
@@ -975,6 +999,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     }
                 }
                 ck_fence_before();
+            }
+            if constexpr (FEW) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_free);
             }
         }
     }
@@ -1151,15 +1179,17 @@ static const char* chunk_refusal(int n_tok, int B, int H_q, int H_kv, kvq_status
 
 struct ChunkLayout {
     size_t plan, cut, block, scale, rot, main, second, extra, total;
-    int max_blocks;
+    int max_blocks, block_rows;
     int64_t second_rows;
 };
 static ChunkLayout chunk_layout(int n_tok, int B, int H_q, int H_kv) {
     const int64_t G = H_q / H_kv, rows = (int64_t)n_tok * H_q, part = PART_STRIDE * 4;
-    // second streams: of blocks of one row tile, at most one per sequence
-    const bool few = (int64_t)B * H_kv * CK_ROW_TILE < rows;
+    // Blocks of one row tile where a sequence has no more rows than that on the average.  Second streams: of blocks of one
+    // row tile, of the others at most one per sequence
     ChunkLayout l;
-    l.max_blocks = (int)((int64_t)n_tok * G / CK_ROWS + B);
+    l.block_rows = (int64_t)n_tok * G <= (int64_t)B * CK_ROW_TILE ? CK_ROW_TILE : CK_ROWS;
+    const bool few = l.block_rows == CK_ROWS && (int64_t)B * H_kv * CK_ROW_TILE < rows;
+    l.max_blocks = (int)((int64_t)n_tok * G / l.block_rows + B);
     l.second_rows = few ? CK_ROW_TILE : 0;
     l.plan = WS_HEADER;
     l.cut = l.plan + 256;
@@ -1190,8 +1220,9 @@ static kvq_status chunk_smem_once() {
     const struct {
         const void* fn;
         size_t bytes;
-    } need[3] = {{(const void*)chunk_rotate_kernel, sizeof(CkRotate)},
-                 {(const void*)chunk_stream_kernel, sizeof(CkSmem) + 1024},
+    } need[4] = {{(const void*)chunk_rotate_kernel, sizeof(CkRotate)},
+                 {(const void*)chunk_stream_kernel<false>, sizeof(CkSmem<false>) + 1024},
+                 {(const void*)chunk_stream_kernel<true>, sizeof(CkSmem<true>) + 1024},
                  {(const void*)chunk_finish_kernel, sizeof(CkMatrix)}};
     for (const auto& x : need) {
         st = kvq_check_cuda(cudaFuncSetAttribute(x.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.bytes),
@@ -1251,6 +1282,7 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     a.cut = reinterpret_cast<int64_t*>(ws + l.cut);
     a.block = reinterpret_cast<CkBlock*>(ws + l.block);
     a.max_blocks = l.max_blocks;
+    a.block_rows = l.block_rows;
     a.row_scale = reinterpret_cast<float*>(ws + l.scale);
     a.rot = reinterpret_cast<__half*>(ws + l.rot);
     a.main = reinterpret_cast<float*>(ws + l.main);
@@ -1267,7 +1299,9 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     st = kvq_check_cuda(launch_pdl(chunk_rotate_kernel, dim3(capped(row_tiles, 4) + 1, H_kv), dim3(256), sizeof(CkRotate), cs, a),
                         "kvq_chunk_attn_int4 rotate launch");
     if (st != KVQ_OK) return st;
-    st = kvq_check_cuda(launch_pdl(chunk_stream_kernel, dim3(a.ctas), dim3(CK_THREADS), sizeof(CkSmem) + 1024, cs, a),
+    const bool one = l.block_rows == CK_ROW_TILE;
+    st = kvq_check_cuda(launch_pdl(one ? chunk_stream_kernel<true> : chunk_stream_kernel<false>, dim3(a.ctas), dim3(CK_THREADS),
+                                   (one ? sizeof(CkSmem<true>) : sizeof(CkSmem<false>)) + 1024, cs, a),
                         "kvq_chunk_attn_int4 launch");
     if (st != KVQ_OK) return st;
     return kvq_check_cuda(launch_pdl(chunk_finish_kernel, dim3(capped(2 * (int64_t)l.max_blocks, 4), H_kv), dim3(256), sizeof(CkMatrix), cs, a),

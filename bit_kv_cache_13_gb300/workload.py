@@ -139,14 +139,38 @@ class Int4Layer(Int2Layer):
                                           num_splits, weights)
         return torch.zeros(n, dtype=torch.uint8, device=self.device)
 
-    def decode(self, q, out, ws, num_splits: int = 0, decay: float | None = None):
+    def append_rope(self, q, k, v, positions, rope, slots, q_weight=None, k_weight=None, interleaved: bool = False,
+                    err_count=None):
+        """Norms and rotates the heads of q [n, H_q, d] and k [n, H_kv, d] and appends the keys and v; returns the
+        rotated queries and keys."""
+        q_out, k_out = (torch.empty(x.shape, dtype=torch.bfloat16, device=self.device) for x in (q, k))
+        _lib.kvq_append_rope_int4(q, k, v, positions, rope, slots, self.mu, self.R_k, self.R_v, self.cache, self.num_pages,
+                                  q_out, k_out, q_weight, k_weight, interleaved=interleaved, err_count=err_count)
+        return q_out, k_out
+
+    def chunk_workspace(self, n_tok: int) -> torch.Tensor:
+        n = _lib.kvq_chunk_workspace_bytes(n_tok, self.spec.batch, self.spec.h_q, self.spec.h_kv)
+        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    def chunk(self, q, q_start, out, ws, window: int = 0, sinks: int = 0):
+        """Attends the rows q_start[b] .. q_start[b + 1] - 1 of q, the last tokens of each sequence, over context_lens
+        tokens, causal (with a window: the last ones up to each, and the first `sinks`)."""
+        _lib.kvq_chunk_attn_int4(q, q_start, self.cache, self.num_pages, self.block_table, self.context_lens, self.R_k,
+                                 self.R_v, self.scale, out, ws, window=window, sinks=sinks)
+
+    def decode(self, q, out, ws, num_splits: int = 0, decay: float | None = None, window: int = 0, sinks: int = 0):
         """Attends over context_lens tokens; with decay given, accumulates
-        the tokens' attention weights too."""
-        args = (q, self.cache, self.num_pages, self.block_table, self.context_lens, self.R_k, self.R_v, self.scale, out)
-        if decay is None:
-            _lib.kvq_decode_attn_int4(*args, ws, num_splits)
+        the tokens' attention weights too; with a window, over the last
+        `window` tokens and the first `sinks`."""
+        args = (q, self.cache, self.num_pages, self.block_table, self.context_lens, self.R_k, self.R_v, self.scale)
+        if window:
+            if decay is not None:
+                raise ValueError("no accumulated weights with a window")
+            _lib.kvq_decode_attn_int4_sliding(*args, window, sinks, out, ws, num_splits)
+        elif decay is None:
+            _lib.kvq_decode_attn_int4(*args, out, ws, num_splits)
         else:
-            _lib.kvq_decode_attn_int4_weights(*args, self.weights, decay, ws, num_splits)
+            _lib.kvq_decode_attn_int4_weights(*args, out, self.weights, decay, ws, num_splits)
 
     def evict(self, budget: int, sinks: int, recent: int, dst_block_table) -> torch.Tensor:
         """Shrinks every sequence to at most `budget` tokens, moved into the

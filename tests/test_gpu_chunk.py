@@ -234,3 +234,131 @@ def test_sliding_skips_bad_pages_and_masks_nan():
     _lib.kvq_decode_attn_int4_sliding(q, *args, 100, 20, out, ws)
     assert _lib.load().kvq_workspace_status(ws.data_ptr(), None) == -5
     c.check(out.cpu())
+
+
+@pytest.mark.parametrize("new,ctx", [
+    ([100, 0, 0, 1], [333, 0, 7, 50]),              # few rows on the average, four blocks of them in one sequence
+    ([65, 1, 1], [65, 300, 129]),                   # the last block of a sequence one row past a tile
+    ([32, 32], [200, 32]), ([33, 32], [200, 32]),   # 128 rows on the average, and a token more
+    ([1] * 300, [int(x) for x in np.random.default_rng(0).integers(0, 200, 300)]),
+    ([3] * 90, [int(x) for x in np.random.default_rng(1).integers(3, 500, 90)]),
+])
+def test_block_sizes_and_wide_batches(new, ctx):
+    c = Case(3 + len(new), new, ctx, 4, 1)
+    c.check(c.run())
+    if len(new) < 10:
+        c = Case(4 + len(new), new, ctx, 8, 2, window=40, sinks=5)
+        c.check(c.run())
+
+
+def test_scales_zero_and_negative_and_queries_of_any_size():
+    for scale, peak in ((0.0, 2.5), (-SCALE, 2.5), (SCALE * 1e-6, 2.5e6), (SCALE * 1e30, 2.5e-30)):
+        c = Case(41, [70], [300], 4, 1, peak=peak)
+        args = list(c.device())
+        args[-1] = scale
+        out, ws = torch.empty_like(args[0]), c.workspace()
+        _lib.kvq_chunk_attn_int4(*args, out, ws)
+        want, bound = int4.chunk(c.q.double().numpy(), c.start, c.cache, c.bt, c.ctx, c.rk, c.rv, scale)
+        err = np.linalg.norm(out.double().cpu().numpy() - want, axis=-1)
+        assert (err <= bound + 2.0 ** -8 * np.linalg.norm(want, axis=-1)).all(), scale
+
+
+def test_a_late_largest_logit_raises_the_reference():
+    """Logits that grow along the context by far more than fp16 holds, slowly and at once, also within a tile."""
+    for at in (0, 70, 150, 299):
+        c = Case(50 + at, [40], [300], 4, 1, peak=1.0)
+        q = c.q.float().numpy()
+        for h in range(4):    # a key along the mean query at one token: its logit about 40 above the others
+            q[:, h] = q[:, 0]
+        q[:] = q[:1]
+        c.q = torch.as_tensor(q).bfloat16()
+        k = (c.q[0, 0].double().numpy() @ c.rk[0].astype(np.float64))
+        tile = c.cache[c.bt[0, at // 16], 0]
+        int4.write_tokens(tile, 0, at % 16, *int4.quantize(k * (40 / SCALE / (k @ k))))
+        c.check(c.run())
+    c = Case(60, [30], [1500], 4, 1, peak=1.0)
+    q = c.q.float().numpy()
+    q[:] = q[:1, :1]
+    c.q = torch.as_tensor(q).bfloat16()
+    k = c.q[0, 0].double().numpy() @ c.rk[0].astype(np.float64)
+    for t in range(0, 1500, 7):
+        int4.write_tokens(c.cache[c.bt[0, t // 16], 0], 0, t % 16, *int4.quantize(k * (0.1 * t / SCALE / (k @ k))))
+    c.check(c.run())
+
+
+def test_a_workspace_serves_calls_of_other_shapes():
+    big = Case(71, [200, 60], [700, 300], 8, 2)
+    ws = big.workspace()
+    for c in (big, Case(72, [3], [40], 4, 1), Case(73, [1] * 20, [100] * 20, 4, 1), big, Case(74, [90], [90], 8, 2)):
+        assert _lib.kvq_chunk_workspace_bytes(c.q.shape[0], len(c.new), c.h_q, c.h_kv) <= ws.numel()
+        c.check(c.run(ws))
+    small = torch.zeros(big.workspace().numel() - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(_lib.KvqError, match="workspace"):
+        big.run(small)
+
+
+def test_captured_and_replayed_on_another_stream_with_other_inputs():
+    c, d = Case(81, [50, 5], [400, 90], 8, 2), Case(82, [50, 5], [400, 90], 8, 2)
+    args, ws = list(c.device()), c.workspace()
+    out = torch.zeros_like(args[0])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _lib.kvq_chunk_attn_int4(*args, out, ws)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            _lib.kvq_chunk_attn_int4(*args, out, ws)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(out.cpu())
+    other = d.device()
+    for x, y in zip(args, other):
+        if torch.is_tensor(x):
+            x.copy_(y)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    d.check(out.cpu())
+    assert _lib.load().kvq_workspace_status(ws.data_ptr(), None) == 0
+
+
+def test_two_streams_at_once():
+    cases = [Case(91, [120], [900], 8, 2), Case(92, [4, 4, 4], [300, 800, 64], 8, 1)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    state = [(c.device(), c.workspace(), torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (args, ws, out) in zip(streams, state):
+            _lib.kvq_chunk_attn_int4(*args, out, ws, stream=s)
+    torch.cuda.synchronize()
+    for c, (_, _, out) in zip(cases, state):
+        c.check(out.cpu())
+
+
+def test_an_empty_call_and_refused_tensors():
+    c = Case(95, [4], [40], 4, 1)
+    q, start, *rest = c.device()
+    ws = c.workspace()
+    _lib.kvq_chunk_attn_int4(q[:0], start * 0, *rest, q[:0], ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        _lib.kvq_chunk_attn_int4(q.transpose(0, 1).contiguous().transpose(0, 1), start, *rest, torch.empty_like(q), ws)
+    with pytest.raises(ValueError, match="q_start"):
+        _lib.kvq_chunk_attn_int4(q, start[:1], *rest, torch.empty_like(q), ws)
+    with pytest.raises(ValueError, match="out"):
+        _lib.kvq_chunk_attn_int4(q, start, *rest, torch.empty_like(q)[:2], ws)
+    with pytest.raises(ValueError, match="bytes"):
+        _lib.kvq_chunk_attn_int4(q, start, rest[0], rest[1] + 1, *rest[2:], torch.empty_like(q), ws)
+
+
+def test_a_copy_that_never_comes_is_reported():
+    """The wait for it runs out, the call ends, the status says so, and the next call is right."""
+    for new, ctx in (([100], [700]), ([3, 3], [500, 90])):
+        c = Case(97 + len(new), new, ctx, 8, 2)
+        ws = c.workspace()
+        _lib.kvq_debug_drop_next_copy()
+        args = c.device()
+        _lib.kvq_chunk_attn_int4(*args, torch.empty_like(args[0]), ws)
+        torch.cuda.synchronize()
+        assert _lib.load().kvq_workspace_status(ws.data_ptr(), None) == -4
+        c.check(c.run(ws))
