@@ -338,10 +338,10 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
 //
 //   TMEM     S [stream][2 buffers] (the logits of a tile, and over them its weights P as
 //            fp16), O [stream]
-//   shared   Q [stream], K and V [4 stages] as K-major operands in the 128-byte swizzle (V
-//            transposed: rows are channels), three raw stages
+//   shared   Q [stream], K [2 stages] and V [4] as K-major operands in the 128-byte swizzle
+//            (V transposed: rows are channels), six raw stages
 constexpr int CK_QUERIES = CK_ROW_TILE * D * 2, CK_OPERAND = CK_TILE * D * 2;  // bytes
-constexpr int CK_RAW = CK_PAGES * INT4_TILE, CK_STAGES = 4, CK_INFOS = 8, CK_SHARES = 4;
+constexpr int CK_RAW = CK_PAGES * INT4_TILE, CK_INFOS = 8, CK_SHARES = 4;
 constexpr int CK_SOFTMAX = 8, CK_UNPACK = 16;  // warps
 // (Registers: 896 threads of 72 at launch; 128 for softmax, 48 for unpacking and 56 for the rest are those 64512.)
 constexpr int CK_THREADS = 32 * (CK_SOFTMAX + CK_UNPACK + 4);
@@ -358,18 +358,21 @@ struct __align__(16) CkShare {  // what the roles need of a share
     int64_t row0;               // the sequence's first row among all of a head's
     int h, end;
 };
-// FEW: blocks of one row tile only.  One copy of the queries serves both streams, and six raw stages instead of three
-// cover the cache's latency: such calls are bound by reading it (8 x 5 tokens at 32K: 208 us with three).
+// FEW: blocks of one row tile only.  One copy of the queries serves both streams, and more raw stages cover the
+// cache's latency, which bounds such calls (8 x 5 tokens at 32K: 208 us with three raw stages, 196 with six).
 template <bool FEW>
 struct __align__(1024) CkSmem {
-    static constexpr int RAW_STAGES = FEW ? 6 : 3;
-    uint8_t q[FEW ? 1 : 2][CK_QUERIES], k[CK_STAGES][CK_OPERAND], v[CK_STAGES][CK_OPERAND];
+    static constexpr int K_STAGES = 4, V_STAGES = FEW ? 4 : 2, RAW_STAGES = 6;
+    // (A tile's stages are its number modulo their count.  The warps of the even tiles never wait for an odd one's phase:
+    // with an odd count they could ask for a stage's next phase while the last one is open, and be let through.)
+    static_assert(RAW_STAGES % 2 == 0 && K_STAGES % 2 == 0 && V_STAGES % 2 == 0, "even and odd tiles have stages of their own");
+    uint8_t q[FEW ? 1 : 2][CK_QUERIES], k[K_STAGES][CK_OPERAND], v[V_STAGES][CK_OPERAND];
     uint8_t raw[RAW_STAGES][CK_RAW];
     CkInfo info[CK_INFOS];
     CkShare share[CK_SHARES];
     __align__(16) int raw_base[RAW_STAGES][CK_PAGES];
-    uint64_t raw_full[RAW_STAGES], raw_free[RAW_STAGES], k_full[CK_STAGES], k_free[CK_STAGES], v_full[CK_STAGES], v_free[CK_STAGES];
-    uint64_t q_full[2], q_free, s_full[2][2], p_full[2][2], o_done[2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
+    uint64_t raw_full[RAW_STAGES], raw_free[RAW_STAGES], k_full[K_STAGES], k_free[K_STAGES], v_full[V_STAGES], v_free[V_STAGES];
+    uint64_t q_full[CK_SHARES], q_free, s_full[2][2], p_full[2][2], o_done[2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
     uint32_t tmem;
     int dead;
     uint32_t stages;  // raw stages fetched
@@ -493,7 +496,7 @@ struct CkConst {
 template <bool FEW>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    constexpr int CK_RAW_STAGES = CkSmem<FEW>::RAW_STAGES;
+    constexpr int CK_RAW_STAGES = CkSmem<FEW>::RAW_STAGES, CK_K_STAGES = CkSmem<FEW>::K_STAGES, CK_V_STAGES = CkSmem<FEW>::V_STAGES;
     CkSmem<FEW>& sm = *reinterpret_cast<CkSmem<FEW>*>(smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -501,15 +504,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             mbar_init(&sm.raw_full[i], 1);
             mbar_init(&sm.raw_free[i], CK_UNPACK / 2);
         }
-        for (int i = 0; i < CK_STAGES; ++i) {
+        for (int i = 0; i < CK_K_STAGES; ++i) {
             mbar_init(&sm.k_full[i], CK_UNPACK / 4);
-            mbar_init(&sm.v_full[i], CK_UNPACK / 4);
             mbar_init(&sm.k_free[i], 2);
+        }
+        for (int i = 0; i < CK_V_STAGES; ++i) {
+            mbar_init(&sm.v_full[i], CK_UNPACK / 4);
             mbar_init(&sm.v_free[i], 2);
         }
         mbar_init(&sm.q_free, CK_SOFTMAX);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], FEW ? 8 : 4);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&sm.s_full[i][h], 1);
                 mbar_init(&sm.p_full[i][h], 4);
@@ -520,6 +524,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
         }
         for (int i = 0; i < CK_SHARES; ++i) {
             mbar_init(&sm.share_full[i], 1);
+            mbar_init(&sm.q_full[i], CK_SOFTMAX);
             mbar_init(&sm.share_free[i], CK_SOFTMAX + CK_UNPACK + 2);  // the warps but the loader
         }
         sm.dead = 0;
@@ -583,12 +588,14 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             while (ok && next_share()) {
                 const CkShare& g = sm.share[(n_share - 1) % CK_SHARES];
                 const int n = __shfl_sync(0xffffffffu, g.n, 0), two = __shfl_sync(0xffffffffu, g.two, 0), ns = two ? n : (n + 1 - t) / 2;
-                ok = wait(&sm.q_full[t], (n_share - 1) & 1);
+                // both streams' queries: then both are done with the shares before, and every phase of a stage that this
+                // stream's tiles have not been in is over
+                ok = wait(&sm.q_full[(n_share - 1) % CK_SHARES], (n_share - 1) / CK_SHARES & 1);
 #pragma unroll 1
                 for (int x = 0; x < ns + 2 && ok; ++x) {
                     if (x >= 2) {  // the weighted sum of tile x - 2
-                        const uint32_t tile = tile0 + (two ? x - 2 : 2 * (x - 2) + t), st = tile % CK_STAGES, step = done + x - 2;
-                        if (!(ok = wait(&sm.v_full[st], tile / CK_STAGES & 1) && wait(&sm.p_full[t][step & 1], step >> 1 & 1))) break;
+                        const uint32_t tile = tile0 + (two ? x - 2 : 2 * (x - 2) + t), st = tile % CK_V_STAGES, step = done + x - 2;
+                        if (!(ok = wait(&sm.v_full[st], tile / CK_V_STAGES & 1) && wait(&sm.p_full[t][step & 1], step >> 1 & 1))) break;
                         ck_fence_after();
                         if (leader) {
                             const uint32_t vd = v_lo + st * (CK_OPERAND >> 4), p_at = s_at + 64 * (step & 1);
@@ -603,8 +610,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         __syncwarp();
                     }
                     if (x < ns) {  // the logits of tile x
-                        const uint32_t tile = tile0 + (two ? x : 2 * x + t), st = tile % CK_STAGES, step = done + x;
-                        if (!(ok = wait(&sm.k_full[st], tile / CK_STAGES & 1))) break;
+                        const uint32_t tile = tile0 + (two ? x : 2 * x + t), st = tile % CK_K_STAGES, step = done + x;
+                        if (!(ok = wait(&sm.k_full[st], tile / CK_K_STAGES & 1))) break;
                         ck_fence_after();
                         if (leader) {
                             const uint32_t kd = k_lo + st * (CK_OPERAND >> 4);
@@ -740,11 +747,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
                 for (int i = share.n; i > 0; --i, ++tile) {
                     if ((tile & 1) != odd) continue;
-                    const uint32_t st = tile % CK_STAGES, slot = tile % CK_RAW_STAGES;
+                    const uint32_t st = tile % CK_K_STAGES, slot = tile % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
-                    if (tile >= CK_STAGES && !(ok = wait(&sm.k_free[st], (tile / CK_STAGES - 1) & 1))) break;
+                    if (tile >= CK_K_STAGES && !(ok = wait(&sm.k_free[st], (tile / CK_K_STAGES - 1) & 1))) break;
                     const __half2 tiny = u32_as_h2(cc.sixteenth);  // with it no key leaves fp16
-#pragma unroll
+#pragma unroll 1
                     for (int e = 0; e < 2; ++e) {  // tokens tok and tok + 8
                         const uint4 codes = lds128(sm.raw[slot] + from + 512 * e), meta = lds128(sm.raw[slot] + meta_from + 128 * e);
                         const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
@@ -801,9 +808,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 const CkShare& share = sm.share[(n_share - 1) % CK_SHARES];
                 for (int i = share.n; i > 0; --i, ++tile) {
                     if ((tile & 1) != odd) continue;
-                    const uint32_t st = tile % CK_STAGES, slot = tile % CK_RAW_STAGES;
+                    const uint32_t st = tile % CK_V_STAGES, slot = tile % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
-                    if (tile >= CK_STAGES && !(ok = wait(&sm.v_free[st], (tile / CK_STAGES - 1) & 1))) break;
+                    if (tile >= CK_V_STAGES && !(ok = wait(&sm.v_free[st], (tile / CK_V_STAGES - 1) & 1))) break;
                     const uint8_t *cp = sm.raw[slot] + from, *mp = sm.raw[slot] + meta_from;
                     const int base = sm.raw_base[slot][oct >> 1];
                     // tokens of the octet within the context, none without a page
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     const __half2 most = __hmax2_nan(__habs2(u32_as_h2(look.x)), __habs2(u32_as_h2(look.y)));
                     const float edge = r & 4 ? 32768.f : 2048.f;
                     const bool plain = valid == 8 && __low2float(most) < edge && __high2float(most) < edge, all = __all_sync(0xffffffffu, plain);
-#pragma unroll
+#pragma unroll 1
                     for (int g = 0; g < 2; ++g, cp += 4, mp += 4) {
                         uint32_t x[4][4];
                         if (all) {
@@ -882,10 +889,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.q_full[t]);
-                    if constexpr (FEW) mbar_arrive(&sm.q_full[t ^ 1]);
-                }
+                if (lane == 0) mbar_arrive(&sm.q_full[(n_share - 1) % CK_SHARES]);
             }
             const float f = __ldcg(a.row_scale + at);
             float ref = CK_NEG, l = 0.f;
