@@ -107,12 +107,15 @@ __device__ __noinline__ void rope_again(const float (&x)[8], const float (&a)[8]
                                         bool wild, uint32_t open, uint16_t (&out)[8]) {
     Dd r = {1.f, 0.f};
     double v = 1.0;
-    if (norm) {
+    if (__any_sync(0xffffffffu, norm)) {  // (the other half of the warp may hold a head without one)
         double n2 = 0.0;
         for (int e = 0; e < 8; ++e) n2 = fma((double)x[e], (double)x[e], n2);
         for (int o = 8; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-        v = n2 / D + eps;
-        r = rope_root(x, eps);
+        const Dd root = rope_root(x, eps);
+        if (norm) {
+            v = n2 / D + eps;
+            r = root;
+        }
     }
     for (int e = 0; e < 8; ++e) {
         if (!(open >> e & 1)) continue;
@@ -283,7 +286,10 @@ __global__ void __launch_bounds__(128, 6) rope_kernel(const __grid_constant__ Ro
                     if (open >> e & 1) lo[e >> 1] = e & 1 ? (lo[e >> 1] & 0xffffu) | (uint32_t)again[e] << 16 : (lo[e >> 1] & 0xffff0000u) | again[e];
             } else {  // of the products, which are exact, in pairs
                 Dd root = {1.f, 0.f};
-                if (norm) root = rope_root(x, a.eps);
+                if (__any_sync(0xffffffffu, norm)) {  // (of two heads one may have none, a query's last beside a key's first)
+                    const Dd y = rope_root(x, a.eps);
+                    if (norm) root = y;
+                }
                 while (open) {
                     const int e = __ffs(open) - 1;
                     open &= open - 1u;

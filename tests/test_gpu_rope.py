@@ -76,6 +76,16 @@ def test_one_norm_alone():
         s.check()
 
 
+@pytest.mark.parametrize("n,h_q,h_kv", [(40, 5, 1), (3, 7, 3), (500, 9, 3)])
+def test_one_norm_alone_where_a_query_shares_its_warp_with_a_key(n, h_q, h_kv):
+    """An odd number of query heads: the last one and the first key are one warp's two rows."""
+    for drop in ("qw", "kw"):
+        for scale in (None, 1e-25):
+            s = Setup(n, h_q, h_kv, scale=scale)
+            setattr(s, drop, None)
+            s.check(eps=EPS if scale is None else 0.0)
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-18, 1e-6, 1e8, 1e18, 1e30])
 @pytest.mark.parametrize("norm", [True, False])
 def test_values_of_any_size(scale, norm):
@@ -149,3 +159,43 @@ def test_bytes_do_not_depend_on_the_calls_size():
                                   b.q_out[sl], b.k_out[sl], b.qw, b.kw, EPS)
         at += n
     assert at == 600 and torch.equal(a.cache, b.cache) and torch.equal(a.q_out, b.q_out) and torch.equal(a.k_out, b.k_out)
+
+
+def test_captured_and_replayed_on_another_stream_with_other_inputs():
+    for n in (1, 70, 700):
+        a, b = Setup(n, 7, 3, seed=1), Setup(n, 7, 3, seed=2)
+        b.slots.copy_(a.slots)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            a.call()
+            side.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                a.call()
+        for x in ("qkv", "pos", "qw", "kw", "mu", "rk", "rv", "cache"):
+            getattr(a, x).copy_(getattr(b, x))
+        a.pos[n // 2] = b.pos[n // 2] = 10 ** 6      # a bad position in the replay
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        b.check()
+        assert torch.equal(a.q_out, b.q_out) and torch.equal(a.k_out, b.k_out) and torch.equal(a.cache, b.cache)
+        assert a.err.item() == 2 and b.err.item() == 1
+
+
+def test_two_streams_at_once():
+    s = [Setup(300, 8, 2, seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in s]
+    torch.cuda.synchronize()
+    start = [x.cache.clone() for x in s]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for x, stream in zip(s, streams):
+            with torch.cuda.stream(stream):
+                x.call()
+    torch.cuda.synchronize()
+    for x, y in zip(s, start):
+        got = x.q_out.clone(), x.k_out.clone(), x.cache.clone()
+        x.cache.copy_(y)
+        x.check()
+        assert torch.equal(got[0], x.q_out) and torch.equal(got[1], x.k_out) and torch.equal(got[2], x.cache)
