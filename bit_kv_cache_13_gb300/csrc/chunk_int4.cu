@@ -93,19 +93,18 @@ __device__ __forceinline__ int ck_blocks(const ChunkArgs& a, int n) { return (in
 
 __device__ __forceinline__ int ck_weight(int rows) { return rows > CK_ROW_TILE ? 2 : 1; }
 
-template <typename T>
-__device__ __forceinline__ T ck_scan(T own, T* warp_sums, T& total) {  // exclusive, over the CTA's 256 threads
+__device__ __forceinline__ int64_t ck_scan(int64_t own, int64_t* warp_sums, int64_t& total) {  // exclusive, over the CTA's 256 threads
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T inc = own;
+    int64_t inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T x = __shfl_up_sync(0xffffffffu, inc, o);
+        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
     __syncthreads();
     if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
-    T before = 0;
+    int64_t before = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
@@ -118,11 +117,11 @@ __device__ __forceinline__ T ck_scan(T own, T* warp_sums, T& total) {  // exclus
 // One CTA of 256 threads: a thread takes a run of sequences, then a block at a time.
 __device__ void ck_make_plan(const ChunkArgs& a) {
     __shared__ int64_t sums[8];
-    __shared__ int sums32[8];
     const int tid = threadIdx.x, per = (a.B + 255) / 256, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    int own = 0, n_blocks;
+    // (in 64 bits: where the row starts go up and down, the sequences' blocks are more than max_blocks, even than 2^31)
+    int64_t own = 0, all;
     for (int b = b0; b < b1; ++b) own += ck_blocks(a, ck_tokens(a, b).y);
-    int at = ck_scan(own, sums32, n_blocks);
+    int64_t at = ck_scan(own, sums, all);
     for (int b = b0; b < b1; ++b) {
         const int2 t = ck_tokens(a, b);
         const int ctx = (int)min((int64_t)max(0, __ldg(a.context_lens + b)), (int64_t)a.max_pages * PAGE);
@@ -136,7 +135,7 @@ __device__ void ck_make_plan(const ChunkArgs& a) {
         }
     }
     __syncthreads();
-    n_blocks = min(n_blocks, a.max_blocks);
+    const int n_blocks = (int)min(all, (int64_t)a.max_blocks);
     int64_t base = 0;
     for (int e0 = 0; e0 < n_blocks; e0 += 256) {
         const int e = e0 + tid;
@@ -1278,8 +1277,8 @@ extern "C" kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_
     a.Rk = R_k;
     a.Rv = R_v;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.window = window;
-    a.sinks = window ? sinks : 0;
+    a.window = window < (int64_t)max_pages_per_seq * PAGE ? window : 0;  // (a longer one holds every token)
+    a.sinks = a.window ? sinks : 0;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.error = reinterpret_cast<uint32_t*>(ws);
     a.plan = reinterpret_cast<CkPlan*>(ws + l.plan);

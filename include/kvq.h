@@ -284,9 +284,9 @@ kvq_status kvq_decode_attn_int2_noalloc(const void* q, int B, int H_q, int H_kv,
                                         const float* R_k, const float* R_v, float scale,
                                         float* out, int num_splits, void* stream);
 
-/* Test hook, not for production use: the next INT2 or INT4 decode launch in
- * this process leaves the bulk copy of its first page unissued (the page's bytes
- * are still expected) and gives its waits a limit of about a millisecond, so
+/* Test hook, not for production use: the next INT2 or INT4 decode or chunk
+ * attention launch in this process leaves the bulk copy of its first page
+ * unissued (the page's bytes are still expected) and gives its waits a limit of about a millisecond, so
  * that wait runs out: the kernel records the timeout, lets its other copies
  * land, finishes without the missing page and returns, and
  * kvq_workspace_status then reports KVQ_ERR_CUDA.  Nothing faults or hangs;
@@ -444,7 +444,8 @@ kvq_status kvq_append_rope_int4(const void* q, int64_t q_stride, const void* k, 
 /* Bytes of workspace for kvq_chunk_attn_int4.  It must be zero-filled once before
  * its first use; calls (and captured graphs) that may overlap on the GPU need one
  * each.  A workspace may serve calls of any shape that it is large enough for, one
- * after another.  Returns 0 for sizes that the call refuses. */
+ * after another, but no decode call besides: those count on zeros in theirs, where
+ * this one leaves sums.  Returns 0 for sizes that the call refuses. */
 size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
 
 /* Attention of each sequence's last tokens over the INT4 cache, causal among
@@ -459,11 +460,14 @@ size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
  *            nothing (p < 0 among them) gets zeros
  *   q_start  device int32 [B+1], ascending within 0..n_tok; a sequence whose two
  *            entries are not has no rows, and kvq_workspace_status reports
- *            KVQ_ERR_INVALID_ARG
+ *            KVQ_ERR_INVALID_ARG (rows that others then share hold either's result)
  *   window   0: all tokens; sinks >= 0 (without a window it makes no difference)
  * context_lens is clamped to [0, 16 * max_pages_per_seq]; block-table entries
  * outside [0, num_pages) as kvq_decode_attn_int4, where a token that a row sees lies
- * on them.  A call repeated gives the same bits.  q, cache, R_k, R_v, out and
+ * on them.  Products take fp16 operands with 11 bits each (rotations, rotated
+ * queries, cached keys and values, weights) and add in fp32; a cached value beyond
+ * +-65504 counts as that, a rotation's entries may not pass it.  A call repeated
+ * gives the same bits.  q, cache, R_k, R_v, out and
  * workspace need 16-byte alignment.  H_q / H_kv <= 64, B and H_kv <= 65535,
  * n_tok * H_q <= 2^30, max_pages_per_seq < 2^27, num_pages * H_kv <= 2^32. */
 kvq_status kvq_chunk_attn_int4(const void* q, int n_tok, const int32_t* q_start, int B, int H_q, int H_kv,

@@ -171,6 +171,55 @@ def test_bad_row_starts_are_reported():
     assert torch.equal(got[15:], torch.full_like(got[15:], 7.0))
 
 
+def test_row_starts_up_and_down_of_a_wide_batch():
+    """Every other sequence claims all the rows: far more blocks than the workspace has places for, none written behind it."""
+    rows, B = 3000, 40001
+    c = Case(20, [rows], [rows], 1, 1, extra=0)
+    start = torch.zeros(B + 1, dtype=torch.int32)
+    start[1::2] = rows
+    q, _, cache, pages, bt, _, rk, rv, scale = c.device()
+    n = _lib.kvq_chunk_workspace_bytes(rows, B, 1, 1)
+    ws = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    ws[n:] = 99
+    out = torch.empty_like(q)
+    ctx = torch.zeros(B, dtype=torch.int32)
+    _lib.kvq_chunk_attn_int4(q, start.cuda(), cache, pages, bt.expand(B, -1).contiguous(), ctx.cuda(), rk, rv, scale, out, ws[:n])
+    torch.cuda.synchronize()
+    assert _lib.load().kvq_workspace_status(ws.data_ptr(), None) == -1
+    assert (ws[n:] == 99).all()
+    assert not out.any()                            # no context: every row of the sequences that count sees nothing
+    ctx[0] = rows
+    _lib.kvq_chunk_attn_int4(q, torch.full((B + 1,), rows, dtype=torch.int32).index_fill_(0, torch.tensor([0]), 0).cuda(), cache, pages,
+                             bt.expand(B, -1).contiguous(), ctx.cuda(), rk, rv, scale, out, ws[:n])
+    c.check(out.cpu())
+    assert (ws[n:] == 99).all()
+
+
+def test_windows_of_the_largest_sizes():
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (100, 2 ** 31 - 1), (16 * 20 - 1, 1), (16 * 20, 1)):
+        c = Case(25, [30, 2], [300, 1], 4, 1, window=window, sinks=sinks)
+        c.check(c.run())
+
+
+def test_pages_past_four_gigabytes():
+    c = Case(26, [20, 3], [200, 90], 32, 8, window=64, sinks=20)
+    q, start, cache, _, bt, ctx, rk, rv, scale = c.device()
+    first = 2 ** 32 // (8 * 2560) + 5
+    far = torch.empty((first + cache.shape[0], 8, 2560), dtype=torch.uint8, device="cuda")
+    far[first:] = cache
+    bt = bt + first
+    out, ws = torch.full_like(q, 7.0), c.workspace()
+    _lib.kvq_chunk_attn_int4(q, start, far, far.shape[0], bt, ctx, rk, rv, scale, out, ws, window=64, sinks=20)
+    c.check(out.cpu())
+    # the sequences' last tokens alone, by the sliding decode
+    last = (start[1:] - 1).long()
+    one = torch.empty_like(q[last])
+    ws = torch.zeros(_lib.kvq_int4_workspace_bytes(2, 32, 8, bt.shape[1]), dtype=torch.uint8, device="cuda")
+    _lib.kvq_decode_attn_int4_sliding(q[last], far, far.shape[0], bt, ctx, rk, rv, scale, 64, 20, one, ws)
+    out[last] = one
+    c.check(out.cpu())
+
+
 def test_nan_in_tokens_that_some_rows_see():
     """A cached group of NaN makes the rows that see it NaN, and no other."""
     for side in (0, 1):
