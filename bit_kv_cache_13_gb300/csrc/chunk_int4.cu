@@ -227,7 +227,8 @@ struct __align__(16) CkMatrix {
 __host__ __device__ constexpr int ck_key_at(int ch) { return (ch & ~7) | (ch & 3) << 1 | (ch >> 2 & 1); }
 // (A value channel 32 g + 4 r + i stands at 32 g + 8 i + r.)
 
-// CTAs of 256 threads, 128 rows each (a warp 16); the last CTA of a head's row makes the plan.
+// CTAs of 256 threads, 128 rows each (a warp 16); the last CTA of a head's row makes the plan.  4096 tokens of 32 heads:
+// 35 us for 67 MB (10 at the copy rate), the matrix's way into the operands' layout and a tile or two behind it.
 struct __align__(16) CkRotate {
     CkMatrix R;
     __align__(16) __half out[8][16][D / 2 + 8];  // half a row at a time, so that four CTAs share an SM
@@ -334,6 +335,11 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
 // tiles, whose warpgroups both take every tile of tokens; a block of up to 128 has one, and
 // the warpgroups take every other tile of tokens of it (two streams, each with sums of its
 // own).  In either case the products of one stream run while the other one's softmax does.
+//
+// 2048 tokens of 32K, 32 q / 8 KV heads: 0.96 ms, 1.11 PFLOP/s, 0.56 of a library product's rate.  Bound by the roles'
+// instructions and their waits together: tensor pipe 40 %, issue 51 %, FMA 29 %; alone, the products took 783 us, the
+// softmax 802 and the unpacking 620.  (With 128 logit columns a product and one buffer a stream, for which tensor memory
+// has room, products alone took 637 us, and all of it 1164.)
 //
 //   TMEM     S [stream][2 buffers] (the logits of a tile, and over them its weights P as
 //            fp16), O [stream]
@@ -945,7 +951,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         ref = up;
                         l *= c0;
                         if (x > 0) {
-                            if (!(ok = wait(&sm.o_done[t], (done - 1) & 1))) break;  // (the tile before is in the sums)
+                            // the tile before is in the sums (the one before that was before these logits, whose product came after it)
+                            if (!(ok = wait(&sm.o_done[t], (done - 1) & 1))) break;
                             ck_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < 8; ++c) {
@@ -1021,7 +1028,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
 // ------------------------------------------------------------------ 3: finish
 
 // CTAs of 256 threads take row tiles of a KV head, a warp 16 rows: their partials are merged in the layout of the A
-// operand (a lane has eight times four values of two rows), normalised and rotated by R_v^T.
+// operand (a lane has eight times four values of two rows), normalised and rotated by R_v^T.  A 4K prompt of 32 heads: 42 us
+// for 69 MB of partials and 34 of output (15 at the copy rate), bound by latency with two CTAs an SM.
 __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     CkMatrix& R = *reinterpret_cast<CkMatrix*>(smem_raw);
