@@ -218,7 +218,8 @@ __device__ __forceinline__ uint32_t ck_pack(float lo, float hi) {
 // Power of two that brings x into [2^7, 2^8) (1 for 0 and what is not finite).
 __device__ __forceinline__ float ck_scale(float x) { return x > 0.f && x < CUDART_INF_F ? ldexpf(1.f, max(-100, min(100, 7 - ilogbf(x)))) : 1.f; }
 
-// A matrix as the B operand of m16n8k16: [K step][8 columns][lane].
+// A matrix as the B operand of m16n8k16: [K step][8 columns][lane].  What a product sums over may come in any order: that of
+// the K steps is such that lane t of a row's four loads its values of a step (or of two) at once.
 struct __align__(16) CkMatrix {
     uint2 f[8][16][32];
 };
@@ -254,26 +255,35 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
             q[e] = a.q + ((row / a.G) * a.H_q + (int64_t)h * a.G + row % a.G) * D;
         }
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int ks = 0; ks < 8; ks += 2)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[ks][e] = __ldg(reinterpret_cast<const uint32_t*>(q[e & 1] + 16 * ks + 8 * (e >> 1) + 2 * t));
+            for (int e = 0; e < 2; ++e) {  // channels 8 t .. 8 t + 7 of 32: four of a K step, then four of the next
+                const uint4 y = __ldg(reinterpret_cast<const uint4*>(q[e] + 16 * ks + 8 * t));
+                x[ks][e] = y.x;
+                x[ks][e + 2] = y.y;
+                x[ks + 1][e] = y.z;
+                x[ks + 1][e + 2] = y.w;
+            }
     };
     uint32_t x[8][4];
     int64_t r0 = (int64_t)blockIdx.x * 128 + 16 * warp;
     if (r0 < rows) fetch(r0, x);
     // Columns of the product in the order of the unpacked keys: position n holds channel c with ck_key_at(c) == n.
-    // A thread takes four channels (low or high half of eight: positions 2 i or 2 i + 1) of rows k, k + 1, k + 8, k + 9.
-#pragma unroll
+    // A thread takes four channels (low or high half of eight: positions 2 i or 2 i + 1) of four rows.  (A lane's place is
+    // turned by the column set, so that a warp's stores meet all banks.)
+#pragma unroll 2
     for (int y = threadIdx.x; y < 8 * 4 * 32; y += 256) {
-        const int c4 = y & 31, tt = (y >> 5) & 3, ks = y >> 7;
-        const float* p = Rk + (size_t)(16 * ks + 2 * tt) * D + 4 * c4;
-        const float4 v0 = __ldg(reinterpret_cast<const float4*>(p)), v1 = __ldg(reinterpret_cast<const float4*>(p + D));
-        const float4 v8 = __ldg(reinterpret_cast<const float4*>(p + 8 * D)), v9 = __ldg(reinterpret_cast<const float4*>(p + 9 * D));
-        const float k0[4] = {v0.x, v0.y, v0.z, v0.w}, k1[4] = {v1.x, v1.y, v1.z, v1.w}, k8[4] = {v8.x, v8.y, v8.z, v8.w}, k9[4] = {v9.x, v9.y, v9.z, v9.w};
+        const int c4 = (y & 7) | (y >> 2 & 0x18), tt = (y >> 3) & 3, ks = y >> 7;
+        const float* p = Rk + (size_t)(32 * (ks >> 1) + 8 * tt + 4 * (ks & 1)) * D + 4 * c4;
+        float k[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sm.R.f[ks][c4 >> 1][4 * (2 * i + (c4 & 1)) + tt] = make_uint2(pack_half2(k0[i], k1[i]), pack_half2(k8[i], k9[i]));
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p + j * D));
+            k[j][0] = v.x, k[j][1] = v.y, k[j][2] = v.z, k[j][3] = v.w;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sm.R.f[ks][c4 >> 1][(4 * (2 * i + (c4 & 1)) + tt) ^ 8 * (c4 >> 1 & 3)] = make_uint2(pack_half2(k[0][i], k[1][i]), pack_half2(k[2][i], k[3][i]));
     }
     __syncthreads();
     for (; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 128) {
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
-                    const uint2 b = sm.R.f[ks][8 * part + nt][lane];
+                    const uint2 b = sm.R.f[ks][8 * part + nt][lane ^ 8 * (nt & 3)];
                     mma_f16_16816(c, x[ks], b.x, b.y);
                 }
 #pragma unroll
@@ -1034,17 +1044,23 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
     extern __shared__ __align__(16) uint8_t smem_raw[];
     CkMatrix& R = *reinterpret_cast<CkMatrix*>(smem_raw);
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-    // B: k = position of the unpacked values, n = output channel.  Positions 32 g + 8 i + 2 t and + 1 are channels
-    // 32 g + 8 t + i and + 4; the next eight positions those after them.  (Read before the wait: the kernel that started
-    // this one did so after its own.)
+    // B: k = position of the unpacked values, n = output channel.  Lane t's four positions of a K step are 16 ks + 4 t and the
+    // three after it: channels 32 (ks / 2) + 16 (t & 1) + 2 (ks & 1) + (t / 2), and 4, 8 and 12 further.  (Read before the
+    // wait: the kernel that started this one did so after its own.)
     const float* Rv = a.Rv + (size_t)h * D * D;
 #pragma unroll
-    for (int y = threadIdx.x; y < D * 4 * 4; y += 256) {
-        const int tt = y & 3, g = (y >> 2) & 3, n = y >> 4;
-        const float4* p = reinterpret_cast<const float4*>(Rv + (size_t)n * D + 32 * g + 8 * tt);
-        const float4 u = __ldg(p), v = __ldg(p + 1);
-        R.f[2 * g][n >> 3][4 * (n & 7) + tt] = make_uint2(pack_half2(u.x, v.x), pack_half2(u.y, v.y));
-        R.f[2 * g + 1][n >> 3][4 * (n & 7) + tt] = make_uint2(pack_half2(u.z, v.z), pack_half2(u.w, v.w));
+    for (int y = threadIdx.x; y < D * 4 * 2; y += 256) {
+        const int half = y & 1, g = (y >> 1) & 3, n = y >> 3;
+        const float4* p = reinterpret_cast<const float4*>(Rv + (size_t)n * D + 32 * g + 16 * half);
+        float k[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = __ldg(p + j);
+            k[j][0] = v.x, k[j][1] = v.y, k[j][2] = v.z, k[j][3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            R.f[2 * g + (i >> 1)][n >> 3][(4 * (n & 7) + half + 2 * (i & 1)) ^ 8 * g] = make_uint2(pack_half2(k[0][i], k[1][i]), pack_half2(k[2][i], k[3][i]));
     }
     __syncthreads();
     griddep_wait();
@@ -1068,7 +1084,7 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
             while (__ldcg(a.cut + c + 1) <= unit) ++c;
         }
         float M[2] = {CK_NEG, CK_NEG}, L[2] = {0.f, 0.f};
-        float2 o[8][4];  // [K step][row, + 8; the next eight positions]
+        float2 o[8][4];  // [K step][row, + 8; the next two positions]
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
@@ -1082,7 +1098,11 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[ks][e] = __ldcg(reinterpret_cast<const float2*>(p[e & 1] + 4 + 16 * ks + 8 * (e >> 1) + 2 * t));
+                for (int e = 0; e < 2; ++e) {
+                    const float4 z = __ldcg(reinterpret_cast<const float4*>(p[e] + 4 + 16 * ks + 4 * t));
+                    y[ks][e] = make_float2(z.x, z.y);
+                    y[ks][e + 2] = make_float2(z.z, z.w);
+                }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(p[e]));
@@ -1146,7 +1166,7 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
             for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint2 b = R.f[ks][nt + j][lane];
+                    const uint2 b = R.f[ks][nt + j][lane ^ 8 * (ks >> 1)];
                     mma_f16_16816(c[j], x16[ks], b.x, b.y);
                 }
             // a lane's two columns of four sets become eight of one: lane t gets set nt + t
