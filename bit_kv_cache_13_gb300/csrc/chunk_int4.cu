@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             const CkShare& g = sm.share[(n_share - 1) % CK_SHARES];
             const int two = g.two, n = g.n, ns = two ? n : (n + 1 - t) / 2;
             const int in_block = (two ? CK_ROW_TILE * t : 0) + row;
-            const bool live = in_block < g.rows;
+            const bool live = in_block < g.rows, idle = FEW && in_block - lane >= g.rows;
             const int in_seq = g.r0 + (live ? in_block : 0), pos = g.pos0 + in_seq / a.G;
             const int64_t at = (int64_t)g.h * a.n_tok * a.G + g.row0 + in_seq;  // the row among all
             // the row's queries: the last product with the ones before is done (FEW: of both streams)
@@ -911,6 +911,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             for (int x = 0; x < ns; ++x, ++done) {
                 const uint32_t p_at = s_at + 64 * (done & 1);
                 if (!(ok = wait(&sm.s_full[t][done & 1], done >> 1 & 1))) break;
+                if (idle) {  // a warp without a row: whatever its lanes of P hold stays in them
+                    if (lane == 0) mbar_arrive(&sm.p_full[t][done & 1]);
+                    continue;
+                }
                 ck_fence_after();
                 uint32_t s[64], p[32];
                 ck_tmem_ld32(s, p_at);
@@ -1008,7 +1012,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                                              : a.second + at * PART_STRIDE;
                 if (live) *reinterpret_cast<float2*>(out) = make_float2(ref - CK_LIFT, l);
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 4 && !idle; ++c) {
                     uint32_t o[32];
                     ck_tmem_ld32(o, o_at + 32 * c);
                     ck_loaded32(o);
