@@ -883,6 +883,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
         // ---- softmax of stream t: a thread a row
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
+        // 16 bytes of row x of the warp's
+        auto q_slot = [&](int x, int y) { return sm.q[FEW ? 0 : t] + (32 * (warp & 3) + x) * 128 + (y >> 3) * (CK_QUERIES / 2) + (((y & 7) ^ (x & 7)) << 4); };
         uint32_t tile0 = 0, done = 0, parts = 0;
         bool ok = true;
         while (ok && next_share()) {
@@ -895,12 +897,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             // the row's queries: the last product with the ones before is done (FEW: of both streams)
             if (FEW && n_share > 1 && !(ok = wait(&sm.q_free, n_share & 1))) break;
             {
-                const uint4* src = reinterpret_cast<const uint4*>(a.rot + at * D);
-                uint8_t* dst = sm.q[FEW ? 0 : t] + row * 128;
+                const uint4* src = reinterpret_cast<const uint4*>(a.rot + (at - (live ? in_block : 0)) * D);  // of the block's first row
 #pragma unroll
-                for (int c = 0; c < (FEW ? 8 : 16); ++c) {  // (FEW: half the channels each)
-                    const int y = FEW ? 8 * t + c : c;
-                    *reinterpret_cast<uint4*>(dst + (y >> 3) * (CK_QUERIES / 2) + (((y & 7) ^ (row & 7)) << 4)) = __ldcg(src + y);
+                for (int i = 0; i < (FEW ? 8 : 16); ++i) {  // two rows at a time; FEW: four, half the channels each
+                    const int y = FEW ? 8 * t + (lane & 7) : lane & 15, x = FEW ? 4 * i + (lane >> 3) : 2 * i + (lane >> 4), from = in_block - lane + x;
+                    *reinterpret_cast<uint4*>(q_slot(x, y)) = __ldcg(src + (size_t)(from < g.rows ? from : 0) * (D / 8) + y);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1007,19 +1008,43 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 ++parts;
                 ck_fence_after();
                 float* out = g.from > 0      ? a.extra + ((size_t)blockIdx.x * CK_ROWS + CK_ROW_TILE * t + row) * PART_STRIDE
-                             : two || !t     ? a.main + at * PART_STRIDE
+                             : two || !t     ? a.main + (at + (live ? 0 : in_block)) * PART_STRIDE
                              : a.second_rows ? a.second + (((int64_t)g.b * a.H_kv + g.h) * a.second_rows + row) * PART_STRIDE
-                                             : a.second + at * PART_STRIDE;
+                                             : a.second + (at + (live ? 0 : in_block)) * PART_STRIDE;
                 if (live) *reinterpret_cast<float2*>(out) = make_float2(ref - CK_LIFT, l);
+                if constexpr (FEW) {
 #pragma unroll 1
-                for (int c = 0; c < 4 && !idle; ++c) {
-                    uint32_t o[32];
-                    ck_tmem_ld32(o, o_at + 32 * c);
-                    ck_loaded32(o);
-                    if (live) {
+                    for (int c = 0; c < 4 && !idle; ++c) {
+                        uint32_t o[32];
+                        ck_tmem_ld32(o, o_at + 32 * c);
+                        ck_loaded32(o);
+                        if (live) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4*>(out + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<uint4*>(out + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        }
+                    }
+                } else {
+                    // through the queries' place, which no product reads any more, so that a store covers two rows' 256 bytes
+                    // (a row a lane touched 32 lines: that and the queries' way in, likewise, made a block's start take 13 us)
+                    out -= (int64_t)lane * PART_STRIDE;  // of the warp's first row
+#pragma unroll 1
+                    for (int c = 0; c < 2 && in_block - lane < g.rows; ++c) {
+                        uint32_t o[64];
+                        ck_tmem_ld32(o, o_at + 64 * c);
+                        ck_tmem_ld32(o + 32, o_at + 64 * c + 32);
+                        ck_loaded32(o);
+                        ck_loaded32(o + 32);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(q_slot(lane, i)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int x = 2 * i + (lane >> 4);
+                            if (in_block - lane + x < g.rows)
+                                *reinterpret_cast<uint4*>(out + (int64_t)x * PART_STRIDE + 4 + 64 * c + 4 * (lane & 15)) = lds128(q_slot(x, lane & 15));
+                        }
+                        __syncwarp();
                     }
                 }
                 ck_fence_before();
