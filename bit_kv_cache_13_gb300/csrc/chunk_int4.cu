@@ -23,9 +23,9 @@ constexpr int CK_ROWS = 256;       // most rows of a block: two row tiles of 128
 constexpr int CK_ROW_TILE = 128;
 constexpr int CK_PAGES = 4, CK_TILE = CK_PAGES * PAGE;  // pages and cached tokens of a tile
 // What starting a block costs, in tiles of one row tile: its queries' way in, a pipeline filled and drained, its sums' way
-// out.  A 4K prompt: 484 us for 6, 334 for 16, 300 for 24, 301 for 32; 8 x 5 tokens at 32K, in blocks of one row tile:
-// 179 us for 6, 182 for 24.
-constexpr int CK_UNIT_COST = 24, CK_UNIT_COST_FEW = 6;
+// out.  A 4K prompt: 294 us for 8, 267 for 11, 245 for 14, 242 for 18, 249 for 24; 8 x 5 tokens at 32K, in blocks of one row
+// tile: 173 us for 4 and 6, 175 for 9.
+constexpr int CK_UNIT_COST = 18, CK_UNIT_COST_FEW = 6;
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // A weight is carried as 2^CK_LIFT times itself relative to the row's reference, its largest logit in the first tile, or
 // where the reference was last raised.  fp16 ends 13 powers of two above, and a weight 17 below keeps its 11 bits (one
@@ -898,11 +898,17 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             if (FEW && n_share > 1 && !(ok = wait(&sm.q_free, n_share & 1))) break;
             {
                 const uint4* src = reinterpret_cast<const uint4*>(a.rot + (at - (live ? in_block : 0)) * D);  // of the block's first row
+                // two rows at a time; FEW: four, half the channels each.  (All loads before the first store: one after the
+                // other, each with L2's latency, they took 7 us of a block's start.)
+                const int y = FEW ? 8 * t + (lane & 7) : lane & 15, x0 = FEW ? lane >> 3 : lane >> 4, rows = g.rows;
+                uint4 q[FEW ? 8 : 16];
 #pragma unroll
-                for (int i = 0; i < (FEW ? 8 : 16); ++i) {  // two rows at a time; FEW: four, half the channels each
-                    const int y = FEW ? 8 * t + (lane & 7) : lane & 15, x = FEW ? 4 * i + (lane >> 3) : 2 * i + (lane >> 4), from = in_block - lane + x;
-                    *reinterpret_cast<uint4*>(q_slot(x, y)) = __ldcg(src + (size_t)(from < g.rows ? from : 0) * (D / 8) + y);
+                for (int i = 0; i < (FEW ? 8 : 16); ++i) {
+                    const int from = in_block - lane + x0 + (FEW ? 4 : 2) * i;
+                    q[i] = __ldcg(src + (size_t)(from < rows ? from : 0) * (D / 8) + y);
                 }
+#pragma unroll
+                for (int i = 0; i < (FEW ? 8 : 16); ++i) *reinterpret_cast<uint4*>(q_slot(x0 + (FEW ? 4 : 2) * i, y)) = q[i];
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.q_full[(n_share - 1) % CK_SHARES]);
@@ -1026,10 +1032,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     }
                 } else {
                     // through the queries' place, which no product reads any more, so that a store covers two rows' 256 bytes
-                    // (a row a lane touched 32 lines: that and the queries' way in, likewise, made a block's start take 13 us)
+                    // (a row a lane, it touched 32 lines)
+                    const int rows = g.rows - (in_block - lane);
                     out -= (int64_t)lane * PART_STRIDE;  // of the warp's first row
 #pragma unroll 1
-                    for (int c = 0; c < 2 && in_block - lane < g.rows; ++c) {
+                    for (int c = 0; c < 2 && rows > 0; ++c) {
                         uint32_t o[64];
                         ck_tmem_ld32(o, o_at + 64 * c);
                         ck_tmem_ld32(o + 32, o_at + 64 * c + 32);
@@ -1040,9 +1047,15 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
+                            const uint4 v = lds128(q_slot(2 * i + (lane >> 4), lane & 15));
+                            o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
                             const int x = 2 * i + (lane >> 4);
-                            if (in_block - lane + x < g.rows)
-                                *reinterpret_cast<uint4*>(out + (int64_t)x * PART_STRIDE + 4 + 64 * c + 4 * (lane & 15)) = lds128(q_slot(x, lane & 15));
+                            if (x < rows)
+                                *reinterpret_cast<uint4*>(out + (int64_t)x * PART_STRIDE + 4 + 64 * c + 4 * (lane & 15)) =
+                                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
                         __syncwarp();
                     }
