@@ -30,7 +30,7 @@ constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // A weight is carried as 2^CK_LIFT times itself relative to the row's reference, its largest logit in the first tile, or
 // where the reference was last raised.  fp16 ends 13 powers of two above, and a weight 17 below keeps its 11 bits (one
 // further below, 2^-28 of the reference's).  Raising drains the stream's products: with 9 powers above, one tile in fifty
-// raised some row of a warp, and 2K tokens of 32K took 994 us instead of 954.
+// raised some row of a warp, and 2K tokens of 32K took 994 us instead of 952.
 constexpr float CK_LIFT = 3.f;
 constexpr long long CK_SHORT_WAIT_CYCLES = 2000000LL;
 
@@ -229,7 +229,7 @@ __host__ __device__ constexpr int ck_key_at(int ch) { return (ch & ~7) | (ch & 3
 // (A value channel 32 g + 4 r + i stands at 32 g + 8 i + r.)
 
 // CTAs of 256 threads, 128 rows each (a warp 16); the last CTA of a head's row makes the plan.  4096 tokens of 32 heads:
-// 35 us for 67 MB (10 at the copy rate), the matrix's way into the operands' layout and a tile or two behind it.
+// 31 us for 67 MB (10 at the copy rate), the matrix's way into the operands' layout and a tile or two behind it.
 struct __align__(16) CkRotate {
     CkMatrix R;
     __align__(16) __half out[8][16][D / 2 + 8];  // half a row at a time, so that four CTAs share an SM
@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
 // the warpgroups take every other tile of tokens of it (two streams, each with sums of its
 // own).  In either case the products of one stream run while the other one's softmax does.
 //
-// 2048 tokens of 32K, 32 q / 8 KV heads: 0.96 ms, 1.11 PFLOP/s, 0.56 of a library product's rate.  Bound by the roles'
-// instructions and their waits together: tensor pipe 40 %, issue 51 %, FMA 29 %; alone, the products took 783 us, the
+// 2048 tokens of 32K, 32 q / 8 KV heads: 0.90 ms, 1.18 PFLOP/s, 0.59 of a library product's rate.  Bound by the roles'
+// instructions and their waits together: tensor pipe 44 %, issue 57 %; alone, the products took 783 us, the
 // softmax 802 and the unpacking 620.  (With 128 logit columns a product and one buffer a stream, for which tensor memory
 // has room, products alone took 637 us, and all of it 1164.)
 //
