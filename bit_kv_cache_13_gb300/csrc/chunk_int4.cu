@@ -26,6 +26,10 @@ constexpr int CK_PAGES = 4, CK_TILE = CK_PAGES * PAGE;  // pages and cached toke
 // out.  A 4K prompt: 294 us for 8, 267 for 11, 245 for 14, 242 for 18, 249 for 24; 8 x 5 tokens at 32K, in blocks of one row
 // tile: 173 us for 4 and 6, 175 for 9.
 constexpr int CK_UNIT_COST = 18, CK_UNIT_COST_FEW = 6;
+// The least share worth a CTA, in the same units: the finish merges a block's shares one after the other.  32 q / 8 KV heads,
+// 5 tokens of 2000: 56 us for 1, 34 for 6, 32 for 12 and 20, 45 for 45; 5 of 500: 28, 24, 26, 30, 40; 64 of 1000, in blocks
+// of two row tiles: 74 for 1, 43 for 12 and 20, 50 for 45; 64 of 4000: 73 for 12, 62 for 20, 59 for 45.
+constexpr int CK_LEAST_SHARE = 20, CK_LEAST_SHARE_FEW = 12;
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // A weight is carried as 2^CK_LIFT times itself relative to the row's reference, its largest logit in the first tile, or
 // where the reference was last raised.  fp16 ends 13 powers of two above, and a weight 17 below keeps its 11 bits (one
@@ -161,7 +165,8 @@ __device__ void ck_make_plan(const ChunkArgs& a) {
         if (e < n_blocks) a.block[e] = k;
         base += total;
     }
-    const int64_t total = base * a.H_kv, C = min((int64_t)a.ctas, total);
+    const int64_t least = a.block_rows == CK_ROWS ? CK_LEAST_SHARE : CK_LEAST_SHARE_FEW;
+    const int64_t total = base * a.H_kv, C = min((int64_t)a.ctas, (total + least - 1) / least);
     for (int c = tid; c <= C; c += 256) a.cut[c] = C ? c * total / C : 0;
     if (tid == 0) {
         a.plan->blocks = n_blocks;

@@ -171,6 +171,13 @@ def test_bad_row_starts_are_reported():
     assert torch.equal(got[15:], torch.full_like(got[15:], 7.0))
 
 
+@pytest.mark.parametrize("new,ctx,h_q,h_kv", [([5], [2000], 8, 2), ([1], [3000], 4, 1), ([64], [1000], 4, 2), ([70, 1], [1300, 900], 8, 2)])
+def test_small_calls_in_few_and_many_shares(new, ctx, h_q, h_kv):
+    """A unit's tiles over several CTAs, whose sums are merged, from one tile up to dozens a share."""
+    c = Case(30 + sum(new), new, ctx, h_q, h_kv)
+    c.check(c.run())
+
+
 def test_row_starts_up_and_down_of_a_wide_batch():
     """Every other sequence claims all the rows: far more blocks than the workspace has places for, none written behind it."""
     rows, B = 3000, 40001
