@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
     }
     __syncthreads();
     for (; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 128) {
-        // a row's largest value to 2^7..2^8: its rotated ones stay within 2^12 and far from fp16's other end; keys are
-        // carried at 2^-4 (the sign of the logits' scale goes into the queries, so that row_scale is positive)
+        // a row's largest value to 2^7..2^8: its rotated ones stay within 2^12 and far from fp16's other end (the sign of the
+        // logits' scale goes into the queries, so that row_scale is positive)
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
             const float sigma = ck_scale(top);
             f[e] = unit * sigma;
             const int64_t row = r0 + r + 8 * e;
-            if (t == 0 && row < rows) a.row_scale[(int64_t)h * rows + row] = unit == 0.f ? 1.f : fmaxf(16.f * fabsf(a.scale_log2) / sigma, 1e-30f);
+            if (t == 0 && row < rows) a.row_scale[(int64_t)h * rows + row] = unit == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) / sigma, 1e-30f);
         }
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
@@ -368,7 +368,7 @@ constexpr int CK_THREADS = 32 * (CK_SOFTMAX + CK_UNPACK + 4);
 
 struct __align__(16) CkInfo {  // of a tile of tokens, written with its keys
     int base[4];          // first position of each page, -1 without one
-    uint32_t poison[4];   // tokens of each page whose values are not finite
+    uint32_t marks[4];    // tokens of each page: bits 0..15 values that are not finite, bits 16..31 keys carried at 2^-4
     uint32_t special;     // bit t: stream t's rows do not all see all of it
 };
 struct __align__(16) CkShare {  // what the roles need of a share
@@ -770,13 +770,26 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     const uint32_t st = tile % CK_K_STAGES, slot = tile % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
                     if (tile >= CK_K_STAGES && !(ok = wait(&sm.k_free[st], (tile / CK_K_STAGES - 1) & 1))) break;
-                    const __half2 tiny = u32_as_h2(cc.sixteenth);  // with it no key leaves fp16
+                    uint32_t big = 0;  // of this thread's tokens
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e) {  // tokens tok and tok + 8
-                        const uint4 codes = lds128(sm.raw[slot] + from + 512 * e), meta = lds128(sm.raw[slot] + meta_from + 128 * e);
+                        const uint4 codes = lds128(sm.raw[slot] + from + 512 * e);
+                        uint4 meta = lds128(sm.raw[slot] + meta_from + 128 * e);
                         const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
-                        const __half2 s01 = __hmul2(u32_as_h2(meta.x), tiny), s23 = __hmul2(u32_as_h2(meta.y), tiny);
-                        const __half2 m01 = __hmul2(u32_as_h2(meta.z), tiny), m23 = __hmul2(u32_as_h2(meta.w), tiny);
+                        // min + code * scale is exact or has its 11 bits at any size.  A token whose scales reach 2^11 or whose mins
+                        // reach 2^15 might leave fp16: its keys are carried at 2^-4, and its logits times 2^4 in the softmax.
+                        const __half2 top_s = __hmax2_nan(__habs2(u32_as_h2(meta.x)), __habs2(u32_as_h2(meta.y)));
+                        const __half2 top_m = __hmax2_nan(__habs2(u32_as_h2(meta.z)), __habs2(u32_as_h2(meta.w)));
+                        const bool leaves = !(__hblt2(top_s, __float2half2_rn(2048.f)) && __hblt2(top_m, __float2half2_rn(32768.f)));
+                        if (__any_sync(0xffffffffu, leaves)) {
+                            const __half2 f = leaves ? u32_as_h2(cc.sixteenth) : __float2half2_rn(1.f);
+                            meta.x = h2_as_u32(__hmul2(u32_as_h2(meta.x), f));
+                            meta.y = h2_as_u32(__hmul2(u32_as_h2(meta.y), f));
+                            meta.z = h2_as_u32(__hmul2(u32_as_h2(meta.z), f));
+                            meta.w = h2_as_u32(__hmul2(u32_as_h2(meta.w), f));
+                            if (leaves) big |= 0x10000u << ((tok & 15) + 8 * e);
+                        }
+                        const __half2 s01 = u32_as_h2(meta.x), s23 = u32_as_h2(meta.y), m01 = u32_as_h2(meta.z), m23 = u32_as_h2(meta.w);
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             const __half2 s = g & 1 ? __high2half2(g < 2 ? s01 : s23) : __low2half2(g < 2 ? s01 : s23);
@@ -799,7 +812,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
 #pragma unroll
                             for (int o = 8; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
                         }
-                        if (lane == 0) info.poison[part] = sm.raw_base[slot][part] < 0 ? 0u : bad;
+                        if (__any_sync(0xffffffffu, big)) bad |= __reduce_or_sync(0xffffffffu, big);
+                        if (lane == 0) info.marks[part] = sm.raw_base[slot][part] < 0 ? 0u : bad;
                     }
                     if (part == 0) {
                         const int at = sm.raw_base[slot][lane & 3];
@@ -932,9 +946,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 ck_tmem_ld32(s, p_at);
                 ck_tmem_ld32(s + 32, p_at + 32);
                 const CkInfo& info = sm.info[(tile0 + (two ? x : 2 * x + t)) % CK_INFOS];
-                const uint4 bad4 = lds128(info.poison);
+                const uint4 bad4 = lds128(info.marks);
                 const bool special = (info.special >> t & 1) | ((bad4.x | bad4.y | bad4.z | bad4.w) != 0);
-                // 32 tokens, two pages: what the row does not see is -inf, what is not finite NaN
+                // 32 tokens, two pages: what the row does not see is -inf, what is not finite NaN; keys carried at 2^-4
                 auto mask = [&](uint32_t* s, int c) {
 #pragma unroll
                     for (int pg = 0; pg < 2; ++pg) {
@@ -944,10 +958,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             const int low = min(PAGE, max(0, pos - a.window + 1 - base)), sink = min(PAGE, max(0, a.sinks - base));
                             see &= ~((1u << low) - 1u) | ((1u << sink) - 1u);
                         }
-                        const uint32_t bad = info.poison[2 * c + pg];
+                        const uint32_t marks = info.marks[2 * c + pg];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            if (bad >> i & 1) s[16 * pg + i] = 0x7fffffffu;
+                            if (marks >> (16 + i) & 1) s[16 * pg + i] = __float_as_uint(__uint_as_float(s[16 * pg + i]) * 16.f);
+                            if (marks >> i & 1) s[16 * pg + i] = 0x7fffffffu;
                             if (!(see >> i & 1)) s[16 * pg + i] = 0xff800000u;
                         }
                     }

@@ -276,3 +276,49 @@ def chunk(q, q_start, cache, block_table, ctx_lens, rk32, rv32, scale, window: i
                 e = np.where(see, e, 0.0)
                 bound[rows, j] = (w * e) @ size + 2.0 ** -11 * (w @ size) + 2.0 ** -10 * np.linalg.norm(o, axis=1) + (w * e).sum(1) * np.linalg.norm(o, axis=1) + 1e-6 * size.max(initial=0.0)
     return out, bound
+
+
+def chunk_spread(q, q_start, cache, block_table, ctx_lens, rk32, rv32, scale, window: int = 0, sinks: int = 0):
+    """What chunk() returns and, instead of its bound, the variance [n, H_q] of the 2-norm of the error that fp16 operands
+    leave: each is rounded by at most 2^-11 of itself, in standard deviation u = 2^-11 / sqrt(3) at the most, all of them
+    independent.  With weights w_t, logits a_t = sum_j q'_j k_tj scale, q'_j = sum_i q_i R_ij:
+      * q'_j and the R_ij move all tokens' logits together: by g_j k_tj with var g_j = u^2 (q'_j^2 + sum_i q_i^2 R_ij^2), and
+        an error e_t of logit t moves the output by w_t e_t (v_t - o): sum_j var g_j scale^2 |sum_t w_t k_tj (v_t - o)|^2;
+      * a key k_tj by itself: u^2 scale^2 sum_t w_t^2 |v_t - o|^2 sum_j (q'_j k_tj)^2;
+      * weights and values: 2 u^2 sum_t w_t^2 |v_t|^2;  the sums and R_v, which is orthogonal: 2 u^2 |o|^2."""
+    u2 = 2.0 ** -22 / 3
+    out, _ = chunk(q, q_start, cache, block_table, ctx_lens, rk32, rv32, scale, window, sinks)
+    q = np.asarray(q, np.float64)
+    h_q, d = q.shape[1:]
+    h_kv = cache.shape[1]
+    g = h_q // h_kv
+    var = np.zeros(q.shape[:2])
+    sc = float(np.float32(scale))
+    for b, ctx in enumerate(np.clip(np.asarray(ctx_lens, np.int64), 0, PAGE * block_table.shape[1])):
+        n = int(q_start[b + 1] - q_start[b])
+        if n <= 0 or ctx == 0:
+            continue
+        pages = np.asarray(block_table[b][: -(-int(ctx) // PAGE)], np.int64)
+        ok = (pages >= 0) & (pages < cache.shape[0])
+        t, p = np.arange(ctx), ctx - n + np.arange(n)[:, None]
+        see = (t <= p) & np.repeat(ok, PAGE)[:ctx]
+        if window:
+            see &= (t > p - window) | (t < sinks)
+        rows, used = slice(int(q_start[b]), int(q_start[b]) + n), see.any(0)
+        for h in range(h_kv):
+            tiles = cache[np.where(ok, pages, 0), h]
+            k, v = (np.where(used[:, None], values(tiles, side).reshape(-1, d)[:ctx], 0.0) for side in (0, 1))
+            rk = np.asarray(rk32[h], np.float32).astype(np.float64)
+            rv = np.asarray(rv32[h], np.float32).astype(np.float64)
+            for j in range(h * g, (h + 1) * g):
+                qr = q[rows, j] @ rk
+                a = np.where(see, qr @ k.T * sc, -np.inf)
+                w = np.where(see, np.exp(a - np.where(see.any(1), a.max(1, initial=-np.inf), 0.0)[:, None]), 0.0)
+                w /= np.where(see.any(1), w.sum(1), 1.0)[:, None]
+                o = out[rows, j] @ rv
+                away = (v * v).sum(1) - 2 * o @ v.T + (o * o).sum(1)[:, None]      # |v_t - o|^2
+                together = np.einsum("nt,tj,td->njd", w, k, v) - (w @ k)[:, :, None] * o[:, None]
+                var[rows, j] = u2 * (sc * sc * (((qr * qr) + (q[rows, j] ** 2) @ (rk * rk)) * (together ** 2).sum(-1)).sum(1)
+                                     + sc * sc * (w * w * np.maximum(away, 0.0) * ((qr * qr) @ (k * k).T)).sum(1)
+                                     + 2 * (w * w) @ (v * v).sum(1) + 2 * (o * o).sum(1))
+    return out, var
