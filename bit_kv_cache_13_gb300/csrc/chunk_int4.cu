@@ -220,8 +220,8 @@ __device__ __forceinline__ uint32_t ck_pack(float lo, float hi) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&x);
 }
-// Power of two that brings x into [2^7, 2^8) (1 for 0 and what is not finite).
-__device__ __forceinline__ float ck_scale(float x) { return x > 0.f && x < CUDART_INF_F ? ldexpf(1.f, max(-100, min(100, 7 - ilogbf(x)))) : 1.f; }
+// Power of two that brings x into [2^to, 2^(to + 1)) (1 for 0 and what is not finite), of any size: itself at least 2^-127.
+__device__ __forceinline__ float ck_scale(float x, int to) { return x > 0.f && x < CUDART_INF_F ? ldexpf(1.f, min(126, to - ilogbf(x))) : 1.f; }
 
 // A matrix as the B operand of m16n8k16: [K step][8 columns][lane].  What a product sums over may come in any order: that of
 // the K steps is such that lane t of a row's four loads its values of a step (or of two) at once.
@@ -292,8 +292,9 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
     }
     __syncthreads();
     for (; r0 < rows; r0 += (int64_t)(gridDim.x - 1) * 128) {
-        // a row's largest value to 2^7..2^8: its rotated ones stay within 2^12 and far from fp16's other end (the sign of the
-        // logits' scale goes into the queries, so that row_scale is positive)
+        // a row's largest value to 1..2: its rotated ones stay within 2^4.5 times R_k's norm, in fp16 for one of up to 2^11, and
+        // lose nothing that counts at fp16's other end, 2^-25, for one down to 2^-11 (the sign of the logits' scale goes into
+        // the queries, so that row_scale is positive)
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
             float top = fmaxf(__low2float(m), __high2float(m));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float sigma = ck_scale(top);
+            const float sigma = ck_scale(top, 0);
             f[e] = unit * sigma;
             const int64_t row = r0 + r + 8 * e;
             if (t == 0 && row < rows) a.row_scale[(int64_t)h * rows + row] = unit == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) / sigma, 1e-30f);
@@ -1202,7 +1203,7 @@ __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_const
                 top = fmaxf(fmaxf(top, fmaxf(fabsf(o[ks][e].x), fabsf(o[ks][e].y))), fmaxf(fabsf(o[ks][e + 2].x), fabsf(o[ks][e + 2].y)));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float sigma = ck_scale(top);
+            const float sigma = ck_scale(top, 7);
             // (no token: 0; NaN stays NaN)
             back[e] = (L[e] > 0.f ? 1.f / L[e] : L[e] == L[e] ? 0.f : L[e]) / sigma;
 #pragma unroll

@@ -466,7 +466,8 @@ size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
  * outside [0, num_pages) as kvq_decode_attn_int4, where a token that a row sees lies
  * on them.  Products take fp16 operands with 11 bits each (rotations, rotated
  * queries, cached keys of any size and values, weights) and add in fp32; a cached
- * value (not a key) beyond +-65504 counts as that, a rotation's entries may not pass it.  A call repeated
+ * value (not a key) beyond +-65504 counts as that, a rotation's entries may not pass
+ * it, and R_k may lengthen a query up to 2^11-fold.  A call repeated
  * gives the same bits.  q, cache, R_k, R_v, out and
  * workspace need 16-byte alignment.  H_q / H_kv <= 64, B and H_kv <= 65535,
  * n_tok * H_q <= 2^30, max_pages_per_seq < 2^27, num_pages * H_kv <= 2^32. */

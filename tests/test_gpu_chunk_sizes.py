@@ -17,6 +17,14 @@ from test_gpu_chunk import SCALE, Case
 pytestmark = pytest.mark.gpu
 
 
+def run(c, scale):
+    args = list(c.device())
+    args[-1] = scale
+    out, ws = torch.full_like(args[0], 7.0), c.workspace()
+    _lib.kvq_chunk_attn_int4(*args, out, ws, window=c.window, sinks=c.sinks)
+    return out.cpu()
+
+
 def close(c, got, scale=SCALE):
     n = int(c.start[-1])
     want, var = int4.chunk_spread(c.q.double().numpy(), c.start, c.cache, c.bt, c.ctx, c.rk, c.rv, scale, c.window, c.sinks)
@@ -67,4 +75,24 @@ def test_small_keys_beside_huge_ones():
     away = -q @ c.rk[0].astype(np.float64)
     for t in (0, 3, 130, 131, 250):
         int4.write_tokens(c.cache[c.bt[0, t // 16], 0], 0, t % 16, *int4.quantize(away * (5e4 / np.abs(away).max())))
+    close(c, c.run())
+
+
+@pytest.mark.parametrize("power,keys", [(-120, 1.0), (-60, 1.0), (60, 1.0), (108, 1.0), (115, 1.0), (117, 1.0), (121, 1e-2), (125, 1e-3)])
+def test_queries_up_to_the_ends_of_their_type(power, keys):
+    """Queries of 0.5 times 2^power, up to bf16's largest, and a scale that makes their logits ordinary ones."""
+    c = Case(6, [40], [300], 4, 1)
+    set_keys(c, keys)
+    x = np.clip(0.5 * c.rng.standard_normal(c.q.shape), -1.9, 1.9)
+    c.q = (torch.as_tensor(x, dtype=torch.float64) * 2.0 ** power).bfloat16()
+    scale = float(np.float32(5 * SCALE / keys * 2.0 ** -power))
+    close(c, run(c, scale), scale)
+
+
+@pytest.mark.parametrize("length", [2.0 ** -11, 2.0 ** -8, 15.0, 40.0, 300.0, 2000.0])
+def test_rotations_that_shorten_or_lengthen(length):
+    """R_k of any norm that the header allows (a scale of the keys' channels may be folded into it)."""
+    c = Case(7, [40], [300], 4, 1)
+    c.rk = (length * c.rk).astype(np.float32)
+    c.q = (c.q.float() / length).bfloat16()
     close(c, c.run())
