@@ -12,6 +12,7 @@
 //              products on tcgen05, the cache unpacked to fp16 in shared memory on the way
 //   3 finish   merges the shares' partial sums, normalises, rotates by R_v^T
 #include <algorithm>
+#include <climits>
 #include <cstddef>
 #include <mutex>
 
@@ -31,11 +32,25 @@ constexpr int CK_UNIT_COST = 18, CK_UNIT_COST_FEW = 6;
 // of two row tiles: 74 for 1, 43 for 12 and 20, 50 for 45; 64 of 4000: 73 for 12, 62 for 20, 59 for 45.
 constexpr int CK_LEAST_SHARE = 20, CK_LEAST_SHARE_FEW = 12;
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
-// A weight is carried as 2^CK_LIFT times itself relative to the row's reference, its largest logit in the first tile, or
-// where the reference was last raised.  fp16 ends 13 powers of two above, and a weight 17 below keeps its 11 bits (one
-// further below, 2^-28 of the reference's).  Raising drains the stream's products: with 9 powers above, one tile in fifty
-// raised some row of a warp, and 2K tokens of 32K took 994 us instead of 952.
+// A token counts in the output by its weight times the size of its values: the power of two of 8 |scale| + |min| of its
+// largest group, relative to the share's own (2^2 less than the largest of the first tile).  A row's reference is the largest
+// such product (as logit + size) in its first tile, or where it was last raised, and a weight is carried as 2^CK_LIFT times
+// itself relative to it, so that a token with a large logit and small values (a sink) does not push the weights of those that
+// make up the output out of fp16.  Where a size lies outside [CK_SIZE_LEAST, CK_SIZE_MOST] the weight also takes what it lies
+// outside by (its level), and the values leave it.  So the largest product's weight stands at 2^0 to 2^6, 16 to 10 powers of
+// two below fp16's end; bits are lost of products 2^-13 of it and less, and those below 2^-24 are gone.  (Without
+// sizes, a sink of no values 20 nats above the others left the output 20 % off; with them 2K tokens of 32K take 950 us
+// instead of 927, a 4K prompt 250 instead of 240.)  Raising drains the stream's products: for a lift of 6, a 4K prompt
+// takes 3 % longer.
 constexpr float CK_LIFT = 3.f;
+constexpr int CK_SIZE_LEAST = -3, CK_SIZE_MOST = 3, CK_SIZE_NONE = -64;  // (of zeros; what is not finite is marked)
+constexpr int CK_SHARE_LEAST = -6, CK_SHARE_MOST = 11;  // (what values are brought to has its bits in fp16)
+__device__ __forceinline__ int ck_size(float z, int share) { return max(CK_SIZE_NONE, (int)(__float_as_uint(z) >> 23) - 127 - share); }
+__device__ __forceinline__ int ck_level(int size) { return size - max(CK_SIZE_LEAST, min(CK_SIZE_MOST, size)); }
+// The same as fp32 numbers, without a conversion (2^23 + n by its bits).
+__device__ __forceinline__ float ck_size_f(float z, float share_bias) { return fmaxf((float)CK_SIZE_NONE, __uint_as_float(0x4b000000u | __float_as_uint(z) >> 23) - share_bias); }
+__device__ __forceinline__ float ck_level_f(float size) { return size - fmaxf((float)CK_SIZE_LEAST, fminf((float)CK_SIZE_MOST, size)); }
+__device__ __forceinline__ float ck_pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 constexpr long long CK_SHORT_WAIT_CYCLES = 2000000LL;
 
 // Rows [r0, r0 + rows) of sequence b (row = token * G + head of the group), and the pages
@@ -370,7 +385,10 @@ constexpr int CK_THREADS = 32 * (CK_SOFTMAX + CK_UNPACK + 4);
 struct __align__(16) CkInfo {  // of a tile of tokens, written with its keys
     int base[4];          // first position of each page, -1 without one
     uint32_t marks[4];    // tokens of each page: bits 0..15 values that are not finite, bits 16..31 keys carried at 2^-4
+    uint32_t flags[4];    // of each page: 1 there are marks, 2 there are levels
+    float z[CK_TILE];     // 8 |scale| + |min| of each token's values
     uint32_t special;     // bit t: stream t's rows do not all see all of it
+    float share_bias;     // the share's size + 127 + 2^23
 };
 struct __align__(16) CkShare {  // what the roles need of a share
     int n, two, from, rows;     // tiles; two row tiles
@@ -391,6 +409,8 @@ struct __align__(1024) CkSmem {
     uint8_t raw[RAW_STAGES][CK_RAW];
     CkInfo info[CK_INFOS];
     CkShare share[CK_SHARES];
+    int share_size[CK_SHARES];  // (known with the share's first tile)
+    float2 share_band[CK_SHARES];  // the sizes z without a level: from .x on, below .y
     __align__(16) int raw_base[RAW_STAGES][CK_PAGES];
     uint64_t raw_full[RAW_STAGES], raw_free[RAW_STAGES], k_full[K_STAGES], k_free[K_STAGES], v_full[V_STAGES], v_free[V_STAGES];
     uint64_t q_full[CK_SHARES], q_free, s_full[2][2], p_full[2][2], o_done[2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
@@ -513,6 +533,21 @@ struct CkConst {
         c[3] = __hfma2(take(v, high), u32_as_h2(sixteenth), u32_as_h2(back));
     }
 };
+
+// Largest of four groups' scales or mins of a slot pair; NaN where one is.
+__device__ __forceinline__ __half2 ck_most(uint4 y) {
+    return __hmax2_nan(__hmax2_nan(__habs2(u32_as_h2(y.x)), __habs2(u32_as_h2(y.y))), __hmax2_nan(__habs2(u32_as_h2(y.z)), __habs2(u32_as_h2(y.w))));
+}
+__device__ __forceinline__ float2 ck_sizes(__half2 scale, __half2 min) {
+    const float2 s = __half22float2(scale), m = __half22float2(min);
+    return make_float2(fmaf(8.f, s.x, m.x), fmaf(8.f, s.y, m.y));
+}
+// Whether the keys of a token's scales and mins might leave fp16.
+__device__ __forceinline__ bool ck_big_keys(uint4 meta) {
+    const __half2 s = __hmax2_nan(__habs2(u32_as_h2(meta.x)), __habs2(u32_as_h2(meta.y)));
+    const __half2 m = __hmax2_nan(__habs2(u32_as_h2(meta.z)), __habs2(u32_as_h2(meta.w)));
+    return !(__hblt2(s, __float2half2_rn(2048.f)) && __hblt2(m, __float2half2_rn(32768.f)));
+}
 
 template <bool FEW>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __grid_constant__ ChunkArgs a) {
@@ -737,12 +772,31 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     if (stage >= CK_RAW_STAGES && !(ok = wait(&sm.raw_free[slot], (stage / CK_RAW_STAGES - 1) & 1))) break;
                     if (leader) {
                         *reinterpret_cast<int4*>(sm.raw_base[slot]) = make_int4(at[0], at[1], at[2], at[3]);
-                        mbar_arrive_expect_tx(&sm.raw_full[slot], bytes);
 #pragma unroll
                         for (int i = 0; i < CK_PAGES; ++i)
                             if (at[i] >= 0 && !(a.drop && stage == 0 && i == 0 && cta == 0))
                                 bulk_g2s(sm.raw[slot] + i * INT4_TILE, reinterpret_cast<const void*>(src[i]), INT4_TILE, &sm.raw_full[slot]);
                     }
+                    __syncwarp();
+                    if (s == 0) {  // the share's size, while the first tile is on its way: a lane looks at a slot pair of a page
+                        const int first = __shfl_sync(0xffffffffu, base, lane >> 3);
+                        const uint8_t* y = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, from, lane >> 3)) + O4_VS + 16 * (lane & 7);
+                        const int left = first < 0 ? 0 : w.k.ctx - first - 2 * (lane & 7);  // tokens of the pair
+                        int size = INT_MIN;
+                        if (left > 0) {
+                            const float2 z = ck_sizes(ck_most(__ldg(reinterpret_cast<const uint4*>(y))), ck_most(__ldg(reinterpret_cast<const uint4*>(y + O4_VM - O4_VS))));
+                            if (z.x > 0.f && z.x < CUDART_INF_F) size = ck_size(z.x, 0);
+                            if (left > 1 && z.y > 0.f && z.y < CUDART_INF_F) size = max(size, ck_size(z.y, 0));
+                        }
+                        size = __reduce_max_sync(0xffffffffu, size);
+                        size = size == INT_MIN ? 0 : max(CK_SHARE_LEAST, min(CK_SHARE_MOST, size - 2));
+                        if (lane == 0) {
+                            sm.share_size[x % CK_SHARES] = size;
+                            sm.share_band[x % CK_SHARES] = make_float2(ck_pow2(CK_SIZE_LEAST + size), ck_pow2(CK_SIZE_MOST + 1 + size));
+                        }
+                        __syncwarp();
+                    }
+                    if (leader) mbar_arrive_expect_tx(&sm.raw_full[slot], bytes);
                     __syncwarp();
                 }
             }
@@ -771,7 +825,29 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     const uint32_t st = tile % CK_K_STAGES, slot = tile % CK_RAW_STAGES;
                     if (!(ok = wait(&sm.raw_full[slot], tile / CK_RAW_STAGES & 1))) break;
                     if (tile >= CK_K_STAGES && !(ok = wait(&sm.k_free[st], (tile / CK_K_STAGES - 1) & 1))) break;
-                    uint32_t big = 0;  // of this thread's tokens
+                    CkInfo& info = sm.info[tile % CK_INFOS];
+                    bool big = false;  // some keys of the page might leave fp16
+                    {   // a warp looks at a page first: a lane at a token's keys, and at a slot pair's scales or mins of the values
+                        const uint8_t* page = sm.raw[slot] + part * INT4_TILE + 16 * (lane & 15);
+                        const uint4 keys = lds128(page + O4_KM);
+                        const __half2 most = ck_most(lds128(page + O4_VS)), they = u32_as_h2(__shfl_xor_sync(0xffffffffu, h2_as_u32(most), 8));
+                        const float2 z = lane & 8 ? ck_sizes(they, most) : ck_sizes(most, they), band = sm.share_band[(n_share - 1) % CK_SHARES];
+                        const int pair = 2 * (lane & 7);
+                        if (lane < 8) *reinterpret_cast<float2*>(info.z + PAGE * part + pair) = z;
+                        const bool usual = __hblt2(ck_most(keys), __float2half2_rn(2048.f)) && z.x >= band.x && z.x < band.y && z.y >= band.x && z.y < band.y;
+                        uint32_t flags = 0;
+                        if (!__all_sync(0xffffffffu, usual)) {  // huge keys, values that are not finite or of another size than most
+                            const int left = sm.raw_base[slot][part] < 0 ? 0 : share.ctx - sm.raw_base[slot][part];
+                            uint32_t marks = ck_big_keys(keys) ? 0x10000u << (lane & 15) : 0u;
+                            big = __any_sync(0xffffffffu, marks);
+                            marks |= ((z.x < CUDART_INF_F ? 0u : 1u) | (z.y < CUDART_INF_F ? 0u : 2u)) << pair;
+                            marks = __reduce_or_sync(0xffffffffu, marks);
+                            const bool out = (pair < left && !(z.x >= band.x && z.x < band.y)) || (pair + 1 < left && !(z.y >= band.x && z.y < band.y));
+                            flags = (left > 0 && marks ? 1u : 0u) | (__any_sync(0xffffffffu, out) ? 2u : 0u);
+                            if (lane == 0) info.marks[part] = marks;
+                        }
+                        if (lane == 0) info.flags[part] = flags;
+                    }
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e) {  // tokens tok and tok + 8
                         const uint4 codes = lds128(sm.raw[slot] + from + 512 * e);
@@ -779,16 +855,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
                         // min + code * scale is exact or has its 11 bits at any size.  A token whose scales reach 2^11 or whose mins
                         // reach 2^15 might leave fp16: its keys are carried at 2^-4, and its logits times 2^4 in the softmax.
-                        const __half2 top_s = __hmax2_nan(__habs2(u32_as_h2(meta.x)), __habs2(u32_as_h2(meta.y)));
-                        const __half2 top_m = __hmax2_nan(__habs2(u32_as_h2(meta.z)), __habs2(u32_as_h2(meta.w)));
-                        const bool leaves = !(__hblt2(top_s, __float2half2_rn(2048.f)) && __hblt2(top_m, __float2half2_rn(32768.f)));
-                        if (__any_sync(0xffffffffu, leaves)) {
-                            const __half2 f = leaves ? u32_as_h2(cc.sixteenth) : __float2half2_rn(1.f);
+                        if (big) {
+                            const __half2 f = ck_big_keys(meta) ? u32_as_h2(cc.sixteenth) : __float2half2_rn(1.f);
                             meta.x = h2_as_u32(__hmul2(u32_as_h2(meta.x), f));
                             meta.y = h2_as_u32(__hmul2(u32_as_h2(meta.y), f));
                             meta.z = h2_as_u32(__hmul2(u32_as_h2(meta.z), f));
                             meta.w = h2_as_u32(__hmul2(u32_as_h2(meta.w), f));
-                            if (leaves) big |= 0x10000u << ((tok & 15) + 8 * e);
                         }
                         const __half2 s01 = u32_as_h2(meta.x), s23 = u32_as_h2(meta.y), m01 = u32_as_h2(meta.z), m23 = u32_as_h2(meta.w);
 #pragma unroll
@@ -802,20 +874,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                                            h2_as_u32(__hfma2(c[3], s, m)));
                         }
                     }
-                    CkInfo& info = sm.info[tile % CK_INFOS];
-                    {   // values that are not finite: a warp looks at a page's scales and mins, a slot pair of either a lane
-                        const uint4 y = lds128(sm.raw[slot] + part * INT4_TILE + O4_VS + 16 * (lane & 15));
-                        const __half2 top = __hmax2_nan(__hmax2_nan(__habs2(u32_as_h2(y.x)), __habs2(u32_as_h2(y.y))),
-                                                        __hmax2_nan(__habs2(u32_as_h2(y.z)), __habs2(u32_as_h2(y.w))));
-                        uint32_t bad = (__half2float(__low2half(top)) < CUDART_INF_F ? 0u : 1u) | (__half2float(__high2half(top)) < CUDART_INF_F ? 0u : 2u);
-                        if (__any_sync(0xffffffffu, bad)) {
-                            bad <<= 2 * (lane & 7);
-#pragma unroll
-                            for (int o = 8; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-                        }
-                        if (__any_sync(0xffffffffu, big)) bad |= __reduce_or_sync(0xffffffffu, big);
-                        if (lane == 0) info.marks[part] = sm.raw_base[slot][part] < 0 ? 0u : bad;
-                    }
                     if (part == 0) {
                         const int at = sm.raw_base[slot][lane & 3];
                         bool cut[2];
@@ -824,7 +882,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             cut[x] = at < 0 || at + PAGE - 1 > share.first[x] || (a.window && at <= share.last[x] - a.window && at + PAGE > a.sinks);
                         const uint32_t s0 = __any_sync(0xffffffffu, cut[0]), s1 = __any_sync(0xffffffffu, cut[1]);
                         if (lane < 4) info.base[lane] = at;
-                        if (lane == 0) info.special = s0 | s1 << 1;
+                        if (lane == 0) {
+                            info.special = s0 | s1 << 1;
+                            info.share_bias = (float)(sm.share_size[(n_share - 1) % CK_SHARES] + 127 + (1 << 23));
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -850,11 +911,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     const int base = sm.raw_base[slot][oct >> 1];
                     // tokens of the octet within the context, none without a page
                     const int valid = base < 0 ? 0 : min(8, max(0, share.ctx - base - 2 * pair0));
-                    // a lane looks at one pair's scales or mins: those from 2^11 or 2^15 up, and NaN, take the long way
-                    const uint2 look = lds64(mp + 16 * (r & 3) + (r & 4 ? O4_VM - O4_VS : 0));
-                    const __half2 most = __hmax2_nan(__habs2(u32_as_h2(look.x)), __habs2(u32_as_h2(look.y)));
-                    const float edge = r & 4 ? 32768.f : 2048.f;
-                    const bool plain = valid == 8 && __low2float(most) < edge && __high2float(most) < edge, all = __all_sync(0xffffffffu, plain);
+                    // a lane looks at one pair's scales or mins; tokens with a level, and NaN, take the long way
+                    const __half2 most = ck_most(lds128(mp - 4 * g0 + 16 * (r & 3) + (r & 4 ? O4_VM - O4_VS : 0)));
+                    const __half2 they = u32_as_h2(__shfl_xor_sync(0xffffffffu, h2_as_u32(most), 4));
+                    const float2 z = r & 4 ? ck_sizes(they, most) : ck_sizes(most, they);
+                    const float2 band = sm.share_band[(n_share - 1) % CK_SHARES];
+                    const bool all = __all_sync(0xffffffffu, valid == 8 && fminf(z.x, z.y) >= band.x && z.x < band.y && z.y < band.y);
 #pragma unroll 1
                     for (int g = 0; g < 2; ++g, cp += 4, mp += 4) {
                         uint32_t x[4][4];
@@ -868,16 +930,20 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                                 for (int n = 0; n < 4; ++n) x[n][p] = h2_as_u32(__hfma2(c[n], u32_as_h2(s), u32_as_h2(m)));
                             }
                         } else {
-                            // in fp32, cut off at fp16's ends; tokens past the context are 0, and so are those that hold what is not
-                            // finite, whose logits the softmax makes NaN instead (a weight of 0 would not hide it from other rows)
+                            // in fp32; tokens past the context are 0, and so are those that hold what is not finite, whose logits
+                            // the softmax makes NaN instead (a weight of 0 would not hide it from other rows; what else they hold,
+                            // which has no level, is cut off at fp16's ends)
+                            const int size = sm.share_size[(n_share - 1) % CK_SHARES];
+                            const float2 level = make_float2(ck_pow2(-ck_level(ck_size(z.x, size))), ck_pow2(-ck_level(ck_size(z.y, size))));
 #pragma unroll 1
                             for (int p = 0; p < 4; ++p) {
                                 const uint32_t c = lds32(cp + 128 * p);
+                                const float lo_f = __shfl_sync(0xffffffffu, level.x, (lane & 24) | p), hi_f = __shfl_sync(0xffffffffu, level.y, (lane & 24) | p);
                                 const float2 s = __half22float2(u32_as_h2(lds32(mp + 16 * p))), m = __half22float2(u32_as_h2(lds32(mp + 16 * p + (O4_VM - O4_VS))));
                                 const bool lo_ok = 2 * p < valid && isfinite(s.x) && isfinite(m.x), hi_ok = 2 * p + 1 < valid && isfinite(s.y) && isfinite(m.y);
 #pragma unroll
                                 for (int n = 0; n < 4; ++n) {
-                                    const float lo = fmaf((float)(c >> (4 * n) & 15), s.x, m.x), hi = fmaf((float)(c >> (16 + 4 * n) & 15), s.y, m.y);
+                                    const float lo = fmaf((float)(c >> (4 * n) & 15), s.x, m.x) * lo_f, hi = fmaf((float)(c >> (16 + 4 * n) & 15), s.y, m.y) * hi_f;
                                     const uint32_t y = pack_half2(lo_ok ? fminf(fmaxf(lo, -65504.f), 65504.f) : 0.f, hi_ok ? fminf(fmaxf(hi, -65504.f), 65504.f) : 0.f);
 #pragma unroll
                                     for (int pp = 0; pp < 4; ++pp)
@@ -943,12 +1009,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                     continue;
                 }
                 ck_fence_after();
-                uint32_t s[64], p[32];
-                ck_tmem_ld32(s, p_at);
-                ck_tmem_ld32(s + 32, p_at + 32);
+                uint32_t p[32];
                 const CkInfo& info = sm.info[(tile0 + (two ? x : 2 * x + t)) % CK_INFOS];
-                const uint4 bad4 = lds128(info.marks);
-                const bool special = (info.special >> t & 1) | ((bad4.x | bad4.y | bad4.z | bad4.w) != 0);
+                const uint4 flags4 = lds128(info.flags);
+                const uint32_t flags = flags4.x | flags4.y | flags4.z | flags4.w;
+                const bool special = (info.special >> t & 1) | (flags & 1), levels = flags & 2;
                 // 32 tokens, two pages: what the row does not see is -inf, what is not finite NaN; keys carried at 2^-4
                 auto mask = [&](uint32_t* s, int c) {
 #pragma unroll
@@ -959,7 +1024,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             const int low = min(PAGE, max(0, pos - a.window + 1 - base)), sink = min(PAGE, max(0, a.sinks - base));
                             see &= ~((1u << low) - 1u) | ((1u << sink) - 1u);
                         }
-                        const uint32_t marks = info.marks[2 * c + pg];
+                        const uint32_t marks = info.flags[2 * c + pg] & 1 ? info.marks[2 * c + pg] : 0u;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             if (marks >> (16 + i) & 1) s[16 * pg + i] = __float_as_uint(__uint_as_float(s[16 * pg + i]) * 16.f);
@@ -968,27 +1033,22 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         }
                     }
                 };
-                ck_loaded32(s);
-                ck_loaded32(s + 32);
-                if (special) {
-                    mask(s, 0);
-                    mask(s + 32, 1);
-                }
-                float2 sum[2];
+                float weights;
                 bool raise = x == 0;
-                while (true) {
-                    if (raise) {  // the row's reference goes up to its largest logit here, what it has so far down by as much
+                while (true) {  // (again, after the logits are read again, where a weight outgrew fp16)
+                    uint32_t s[64];
+                    ck_tmem_ld32(s, p_at);
+                    ck_tmem_ld32(s + 32, p_at + 32);
+                    ck_loaded32(s);
+                    ck_loaded32(s + 32);
+                    if (special) {
+                        mask(s, 0);
+                        mask(s + 32, 1);
+                    }
+                    if (raise) {  // the row's reference goes up to its largest product here, what it has so far down by as much
                         float top = -CUDART_INF_F;
-#pragma unroll 1
-                        for (int c = 0; c < 2; ++c) {  // (read again: a rare path of its own)
-                            uint32_t z[32];
-                            ck_tmem_ld32(z, p_at + 32 * c);
-                            ck_loaded32(z);
-                            if (special) mask(z, c);
 #pragma unroll
-                            for (int y = 0; y < 32; y += 2) top = fmaxf(fmaxf(top, __uint_as_float(z[y])), __uint_as_float(z[y + 1]));
-                        }
-                        top *= f;
+                        for (int y = 0; y < 64; ++y) top = fmaxf(top, fmaf(__uint_as_float(s[y]), f, ck_size_f(info.z[y], info.share_bias)));
                         const float up = top > ref ? ceilf(top) : ref, c0 = ck_ex2(ref - up);
                         ref = up;
                         l *= c0;
@@ -1007,22 +1067,37 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             }
                         }
                     }
-                    const float2 f2 = make_float2(f, f), off = make_float2(CK_LIFT - ref, CK_LIFT - ref);
+                    const float off = CK_LIFT - ref;
+                    float g = f;
+                    if (levels) {  // the weights themselves; then the logits with levels
+                        weights = 0.f;
+                        g = 1.f;
+#pragma unroll
+                        for (int y = 0; y < 64; ++y) {
+                            const float a = __uint_as_float(s[y]);
+                            weights += ck_ex2(fmaf(a, f, off));
+                            s[y] = __float_as_uint(fmaf(a, f, ck_level_f(ck_size_f(info.z[y], info.share_bias))));
+                        }
+                    }
+                    const float2 g2 = make_float2(g, g), off2 = make_float2(off, off);
+                    float2 sum[2];
                     sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        float2 y = ck_fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f2, off);
+                        float2 y = ck_fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), g2, off2);
                         y = make_float2(ck_ex2(y.x), ck_ex2(y.y));
                         sum[i & 1] = ck_add2(sum[i & 1], y);
                         p[i] = pack_half2(y.x, y.y);
                     }
                     sum[0] = ck_add2(sum[0], sum[1]);
+                    const float carried = sum[0].x + sum[0].y;
+                    if (!levels) weights = carried;
                     // (a sum that fp16 holds is one of weights that it holds)
-                    if (raise || !__any_sync(0xffffffffu, sum[0].x + sum[0].y > 65504.f)) break;
+                    if (raise || !__any_sync(0xffffffffu, carried > 65504.f)) break;
                     raise = true;
                 }
                 if (!ok) break;
-                l += sum[0].x + sum[0].y;
+                l += weights;
                 ck_tmem_st32(p, p_at);  // (over logits that were read)
                 ck_wait_st();
                 ck_fence_before();

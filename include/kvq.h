@@ -465,9 +465,10 @@ size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
  * context_lens is clamped to [0, 16 * max_pages_per_seq]; block-table entries
  * outside [0, num_pages) as kvq_decode_attn_int4, where a token that a row sees lies
  * on them.  Products take fp16 operands with 11 bits each (rotations, rotated
- * queries, cached keys of any size and values, weights) and add in fp32; a cached
- * value (not a key) beyond +-65504 counts as that, a rotation's entries may not pass
- * it, and R_k may lengthen a query up to 2^11-fold.  A call repeated
+ * queries, cached keys and values of any size, weights) and add in fp32.  Of a row,
+ * tokens whose weight times their values' size is below 2^-24 of the largest such
+ * product may be lost.  A rotation's entries may not pass 65504, and R_k may lengthen
+ * a query up to 2^11-fold.  A call repeated
  * gives the same bits.  q, cache, R_k, R_v, out and
  * workspace need 16-byte alignment.  H_q / H_kv <= 64, B and H_kv <= 65535,
  * n_tok * H_q <= 2^30, max_pages_per_seq < 2^27, num_pages * H_kv <= 2^32. */

@@ -317,7 +317,7 @@ def chunk_spread(q, q_start, cache, block_table, ctx_lens, rk32, rv32, scale, wi
                 w /= np.where(see.any(1), w.sum(1), 1.0)[:, None]
                 o = out[rows, j] @ rv
                 away = (v * v).sum(1) - 2 * o @ v.T + (o * o).sum(1)[:, None]      # |v_t - o|^2
-                together = np.einsum("nt,tj,td->njd", w, k, v) - (w @ k)[:, :, None] * o[:, None]
+                together = (w[:, None] * k.T) @ v - (w @ k)[:, :, None] * o[:, None]
                 var[rows, j] = u2 * (sc * sc * (((qr * qr) + (q[rows, j] ** 2) @ (rk * rk)) * (together ** 2).sum(-1)).sum(1)
                                      + sc * sc * (w * w * np.maximum(away, 0.0) * ((qr * qr) @ (k * k).T)).sum(1)
                                      + 2 * (w * w) @ (v * v).sum(1) + 2 * (o * o).sum(1))

@@ -5,7 +5,12 @@ bf16 adds the distance of the exact row from the nearest bf16 one, which is know
 relative to their rows' squared norms may sum to 1.1 times the sum of both: the variance is an upper bound (every rounding
 as at the lower end of its power of two, where it is largest), and the two parts' product, which has no mean, is below
 3 % of it at 4096 outputs or more.  Of a single row the bf16 rounding is at most 2^-8 of each value, and the rest is taken at
-six standard deviations."""
+six standard deviations.
+
+Where all rows' queries lie along one direction and one token's key takes most of their weight, the roundings of both are
+the same for all rows, so that the variances do not average out over a call: the sum of that part is a single draw, and may
+be 25 times its variance (five standard deviations; the same roundings made in numpy give sums of up to 1.4 times).  The
+rounding to bf16 still averages."""
 import numpy as np
 import pytest
 import torch
@@ -25,7 +30,7 @@ def run(c, scale):
     return out.cpu()
 
 
-def close(c, got, scale=SCALE):
+def close(c, got, scale=SCALE, one_draw=False):
     n = int(c.start[-1])
     want, var = int4.chunk_spread(c.q.double().numpy(), c.start, c.cache, c.bt, c.ctx, c.rk, c.rv, scale, c.window, c.sinks)
     want, var, got = want[:n], var[:n], got.double().numpy()[:n]
@@ -36,8 +41,8 @@ def close(c, got, scale=SCALE):
     near2 = ((int4.to_bf16(want) - want) ** 2).sum(-1)
     on = size2 > 0
     assert got[on].size >= 4096
-    ratio = (err2[on] / size2[on]).sum() / ((near2[on] + var[on]) / size2[on]).sum()
-    assert ratio <= 1.1, ratio
+    ratio = (err2[on] / size2[on]).sum() / ((near2[on] * 1.1 + var[on] * (25 if one_draw else 1.1)) / size2[on]).sum()
+    assert ratio <= 1, ratio
 
 
 def set_keys(c, size, spread=0.5):
@@ -95,4 +100,56 @@ def test_rotations_that_shorten_or_lengthen(length):
     c = Case(7, [40], [300], 4, 1)
     c.rk = (length * c.rk).astype(np.float32)
     c.q = (c.q.float() / length).bfloat16()
+    close(c, c.run())
+
+
+def set_values(c, size):
+    """Normal values, size [pages, H_kv, 16] (or a number) times themselves."""
+    x = np.asarray(size)[..., None] * c.rng.standard_normal(c.cache.shape[:2] + (16, 128))
+    for s in range(16):
+        int4.write_tokens(c.cache, 1, s, *int4.quantize(x[:, :, s]))
+
+
+def set_sinks(c, tokens, gap, size):
+    """Queries along one direction, 0.3 to 1 times; tokens whose keys lie `gap` nats along it, with values of that size."""
+    q = c.rng.standard_normal(128)
+    c.q = torch.as_tensor(np.broadcast_to(q, c.q.shape) * c.rng.uniform(0.3, 1.0, c.q.shape[:2] + (1,)), dtype=torch.float32).bfloat16()
+    for h in range(c.h_kv):
+        k = q @ c.rk[h].astype(np.float64)
+        for t in tokens:
+            tile = c.cache[c.bt[0, t // 16], h]
+            int4.write_tokens(tile, 0, t % 16, *int4.quantize(k * (gap / SCALE / (k @ k))))
+            int4.write_tokens(tile, 1, t % 16, *int4.quantize(size * c.rng.standard_normal(128)))
+
+
+@pytest.mark.parametrize("size", [0.0, 1e-6, 1e-3, 0.02, 0.3, 3.0, 100.0])
+@pytest.mark.parametrize("gap", [5.0, 12.0, 17.0, 20.0, 24.0, 40.0])
+def test_sinks(gap, size):
+    """A token that draws all of the weight, with values from none to far larger ones than the others': at the front, later
+    in the context (where the reference is raised), the whole first tile, in a window's sinks; values of other sizes too."""
+    for tokens, new, ctx, window, others in (((0,), [40], 500, 0, 1.0), ((0, 1, 2, 3), [70], 700, 0, 30.0), ((170,), [40], 400, 0, 1.0),
+                                             (range(64), [40], 500, 0, 1.0), ((0, 2), [40], 700, 100, 1e-3)):
+        c = Case(8, new, [ctx], 4, 1, window, 4 if window else 0)
+        set_values(c, others)
+        set_sinks(c, tokens, gap, size * others)
+        close(c, c.run(), one_draw=True)
+
+
+def test_values_of_sizes_that_differ_by_token():
+    """Sizes spread over 35 powers of two from token to token, page to page, and zeros among them."""
+    for seed, new, ctx, h_q in ((1, [60], [500], 4), (2, [300], [900], 2), (3, [20, 20], [300, 64], 4)):
+        c = Case(seed, new, ctx, h_q, 1)
+        shape = c.cache.shape[:2] + (16,)
+        for size in (2.0 ** c.rng.uniform(-20, 15, shape), np.broadcast_to(2.0 ** c.rng.uniform(-20, 15, shape[:2] + (1,)), shape),
+                     np.where(c.rng.random(shape) < 0.5, 0.0, 1.0), np.where(c.rng.random(shape[:2] + (1,)) < 0.5, 0.0, np.ones(shape))):
+            set_values(c, size)
+            close(c, c.run())
+
+
+def test_values_past_the_type_s_largest():
+    """min + 15 scale up to a million, which bf16 holds and fp16 does not."""
+    c = Case(9, [40], [300], 4, 1)
+    set_values(c, 2e5)
+    close(c, c.run())
+    set_values(c, np.where(c.rng.random(c.cache.shape[:2] + (16,)) < 0.1, 2e5, 1e-2))
     close(c, c.run())
