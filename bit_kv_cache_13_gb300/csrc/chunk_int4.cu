@@ -31,6 +31,10 @@ constexpr int CK_UNIT_COST = 18, CK_UNIT_COST_FEW = 6;
 // 5 tokens of 2000: 56 us for 1, 34 for 6, 32 for 12 and 20, 45 for 45; 5 of 500: 28, 24, 26, 30, 40; 64 of 1000, in blocks
 // of two row tiles: 74 for 1, 43 for 12 and 20, 50 for 45; 64 of 4000: 73 for 12, 62 for 20, 59 for 45.
 constexpr int CK_LEAST_SHARE = 20, CK_LEAST_SHARE_FEW = 12;
+// Most tiles of a block that are summed in tensor memory at a time: a product cuts its sum off below fp32, by 2^-23.6 of it on
+// the average, so that the 4 * 16384 of a million tokens of equal weight took 0.3 % off.  What a CTA has of a block beyond
+// that is a run of its own, added in fp32 to the partial before it (1024 tiles, 64K tokens: at most 2^-11).
+constexpr int CK_RUN = 1024;
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // A token counts in the output by its weight times the size of its values: the power of two of 8 |scale| + |min| of its
 // largest group, relative to the share's own (2^2 less than the largest of the first tile).  A row's reference is the largest
@@ -391,7 +395,8 @@ struct __align__(16) CkInfo {  // of a tile of tokens, written with its keys
     float share_bias;     // the share's size + 127 + 2^23
 };
 struct __align__(16) CkShare {  // what the roles need of a share
-    int n, two, from, rows;     // tiles; two row tiles
+    int n, two, from, rows;     // tiles; two row tiles; from > 0: not the block's first share
+    int again;                  // a further run of the same share
     int r0, pos0, ctx, b;       // pos0: position of the sequence's first new token
     int first[2], last[2];      // positions of the streams' first and last rows
     int64_t row0;               // the sequence's first row among all of a head's
@@ -714,14 +719,21 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             uint32_t stage = 0;
             bool ok = true;
             const bool leader = ck_elect();
+            int run = 0, to = 0;  // tiles of the share that are still to come
             for (uint32_t x = 0; ok; ++x) {
-                const bool have = w.next(a);
+                bool have = run < to;
+                if (!have && (have = w.next(a))) {
+                    run = w.from;
+                    to = w.to;
+                }
+                const int n = min(to - run, CK_RUN);
                 if (x >= CK_SHARES && !(ok = wait(&sm.share_free[x % CK_SHARES], (x / CK_SHARES - 1) & 1))) break;
                 if (lane == 0) {
                     CkShare& g = sm.share[x % CK_SHARES];
                     g.end = !have;
                     if (have) {
-                        g.n = w.to - w.from;
+                        g.n = n;
+                        g.again = run > w.from;
                         g.two = w.k.rows > CK_ROW_TILE;
                         g.from = w.from;
                         g.rows = w.k.rows;
@@ -742,7 +754,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                 __syncwarp();
                 if (!have) break;
                 // a lane's page of the next eight tiles' 32: its first position (-1: none, or a bad entry) and where it stands
-                const int p0 = CK_PAGES * w.from, p1 = min(w.k.pages, CK_PAGES * w.to), n = w.to - w.from, sinks = w.k.sinks, skip = w.k.skip;
+                const int p0 = CK_PAGES * run, p1 = min(w.k.pages, CK_PAGES * (run + n)), sinks = w.k.sinks, skip = w.k.skip;
+                run += n;
                 const int32_t* table = a.block_table + (size_t)w.k.b * a.max_pages;
                 auto ids = [&](int first) {
                     const int p = first + lane;
@@ -1113,7 +1126,23 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                              : two || !t     ? a.main + (at + (live ? 0 : in_block)) * PART_STRIDE
                              : a.second_rows ? a.second + (((int64_t)g.b * a.H_kv + g.h) * a.second_rows + row) * PART_STRIDE
                                              : a.second + (at + (live ? 0 : in_block)) * PART_STRIDE;
-                if (live) *reinterpret_cast<float2*>(out) = make_float2(ref - CK_LIFT, l);
+                float m = ref - CK_LIFT, before = 0.f, now = 1.f;  // factors of the partial that stands there and of this run's
+                if (g.again) {
+                    const float2 ml = live ? __ldcg(reinterpret_cast<const float2*>(out)) : make_float2(m, 0.f);
+                    const float top = fmaxf(m, ml.x);
+                    before = ck_ex2(ml.x - top);
+                    now = ck_ex2(m - top);
+                    m = top;
+                    l = fmaf(ml.y, before, l * now);
+                }
+                auto add = [&](uint32_t* o, const float* to, float before, float now) {  // (what this thread left there)
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(to));
+                    o[0] = __float_as_uint(fmaf(y.x, before, __uint_as_float(o[0]) * now));
+                    o[1] = __float_as_uint(fmaf(y.y, before, __uint_as_float(o[1]) * now));
+                    o[2] = __float_as_uint(fmaf(y.z, before, __uint_as_float(o[2]) * now));
+                    o[3] = __float_as_uint(fmaf(y.w, before, __uint_as_float(o[3]) * now));
+                };
+                if (live) *reinterpret_cast<float2*>(out) = make_float2(m, l);
                 if constexpr (FEW) {
 #pragma unroll 1
                     for (int c = 0; c < 4 && !idle; ++c) {
@@ -1122,8 +1151,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         ck_loaded32(o);
                         if (live) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
+                            for (int i = 0; i < 32; i += 4) {
+                                if (g.again) add(o + i, out + 4 + 32 * c + i, before, now);
                                 *reinterpret_cast<uint4*>(out + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            }
                         }
                     }
                 } else {
@@ -1145,6 +1176,14 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         for (int i = 0; i < 16; ++i) {
                             const uint4 v = lds128(q_slot(2 * i + (lane >> 4), lane & 15));
                             o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
+                        }
+                        if (g.again) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int x = 2 * i + (lane >> 4);
+                                const float before_x = __shfl_sync(0xffffffffu, before, x), now_x = __shfl_sync(0xffffffffu, now, x);
+                                if (x < rows) add(o + 4 * i, out + (int64_t)x * PART_STRIDE + 4 + 64 * c + 4 * (lane & 15), before_x, now_x);
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
