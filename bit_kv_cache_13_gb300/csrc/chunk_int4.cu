@@ -418,7 +418,7 @@ struct __align__(1024) CkSmem {
     float2 share_band[CK_SHARES];  // the sizes z without a level: from .x on, below .y
     __align__(16) int raw_base[RAW_STAGES][CK_PAGES];
     uint64_t raw_full[RAW_STAGES], raw_free[RAW_STAGES], k_full[K_STAGES], k_free[K_STAGES], v_full[V_STAGES], v_free[V_STAGES];
-    uint64_t q_full[CK_SHARES], q_free, s_full[2][2], p_full[2][2], o_done[2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
+    uint64_t q_full[CK_SHARES], q_free, s_full[2][2], p_full[2][2], o_done[2][2], o_full[2], drained[2], share_full[CK_SHARES], share_free[CK_SHARES];
     uint32_t tmem;
     int dead;
     uint32_t stages;  // raw stages fetched
@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&sm.s_full[i][h], 1);
                 mbar_init(&sm.p_full[i][h], 4);
+                mbar_init(&sm.o_done[i][h], 1);
             }
-            mbar_init(&sm.o_done[i], 1);
             mbar_init(&sm.o_full[i], 1);
             mbar_init(&sm.drained[i], 1);
         }
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                             ck_mma_ts(o_at, p_at, vd, x > 2, CK_IDESC);
 #pragma unroll
                             for (int i = 1; i < 4; ++i) ck_mma_ts(o_at, p_at + 8 * i, vd + 2 * i, true, CK_IDESC);
-                            ck_commit(&sm.o_done[t]);
+                            ck_commit(&sm.o_done[t][step & 1]);
                             if (x == ns + 1) ck_commit(&sm.o_full[t]);
                             ck_commit(&sm.v_free[st]);
                             if (!two) ck_commit(&sm.v_free[st]);
@@ -1066,8 +1066,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         ref = up;
                         l *= c0;
                         if (x > 0) {
-                            // the tile before is in the sums (the one before that was before these logits, whose product came after it)
-                            if (!(ok = wait(&sm.o_done[t], (done - 1) & 1))) break;
+                            // the tile before is in the sums.  (Tiles take turns on two barriers: the parity then only has to tell it
+                            // from the tile three before these logits, whose sums the logits of the tile before came after.)
+                            if (!(ok = wait(&sm.o_done[t][(done - 1) & 1], (done - 1) >> 1 & 1))) break;
                             ck_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < 8; ++c) {

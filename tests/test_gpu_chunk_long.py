@@ -5,7 +5,7 @@ import torch
 
 from bit_kv_cache_13_gb300 import _lib
 from oracle import int4
-from test_gpu_chunk import SCALE, _cache, _dev, _rot
+from test_gpu_chunk import SCALE, Case, _cache, _dev, _rot
 
 pytestmark = pytest.mark.gpu
 B, H, PAGES = 19, 8, 64      # 152 units: a CTA each, where the sequences are as long as one another
@@ -63,3 +63,22 @@ def test_runs_are_joined(n, ctx):
             err = np.linalg.norm(got[b, :, h] - want[:, 0], axis=-1)
             # (far fewer tokens count than there are: a third of the oracle's bound)
             assert (err <= bound[:, 0] / 3 + 2.0 ** -8 * np.linalg.norm(want[:, 0], axis=-1)).all(), (b, h)
+
+
+@pytest.mark.parametrize("h_q,h_kv,new,ctx", [(2, 1, [256], [4000]), (4, 1, [5], [9000]), (8, 2, [64, 100], [3000, 5000])])
+def test_references_that_rise_in_every_tile(h_q, h_kv, new, ctx):
+    """Logits grow by 40 nats a tile for a while, then every third tile: sums are taken down right after the product that
+    left them, in either stream and in shares that begin anywhere."""
+    c = Case(sum(ctx), new, ctx, h_q, h_kv, peak=1.0)
+    q = c.rng.standard_normal(128)
+    c.q = torch.as_tensor(np.broadcast_to(q, c.q.shape) * c.rng.uniform(0.7, 1.0, c.q.shape[:2] + (1,)), dtype=torch.float32).bfloat16()
+    for h in range(h_kv):
+        k = q @ c.rk[h].astype(np.float64)
+        for b, n in enumerate(ctx):
+            for i, tile in enumerate([*range(1, 30), *range(30, n // 64, 3)]):
+                if 64 * tile < n:
+                    t = 64 * tile + 17 * i % 64
+                    if t < n:
+                        int4.write_tokens(c.cache[c.bt[b, t // 16], h], 0, t % 16, *int4.quantize(k * (40 * (i + 1) / SCALE / (k @ k))))
+    for _ in range(3):
+        c.check(c.run())
