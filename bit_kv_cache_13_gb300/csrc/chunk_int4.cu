@@ -1400,7 +1400,7 @@ static ChunkLayout chunk_layout(int n_tok, int B, int H_q, int H_kv) {
     const bool few = l.block_rows == CK_ROWS && (int64_t)B * H_kv * CK_ROW_TILE < rows;
     l.max_blocks = (int)((int64_t)n_tok * G / l.block_rows + B);
     l.second_rows = few ? CK_ROW_TILE : 0;
-    l.plan = WS_HEADER;
+    l.plan = INT4_WS_BODY;
     l.cut = l.plan + 256;
     l.block = align_up(l.cut + (size_t)(kvq_device_sm_count() + 1) * 8, 256);
     l.scale = align_up(l.block + (size_t)l.max_blocks * sizeof(CkBlock), 256);

@@ -1531,17 +1531,13 @@ static int64_t d4_ctas(int B, int H_kv, int num_splits) {
     return num_splits > 0 ? (int64_t)num_splits * B * H_kv : kvq_device_sm_count();
 }
 
-// (The tickets stand at one place whatever the shape, so that what a call of another
-// shape left in the workspace is never taken for one.)
-constexpr int D4_TICKETS = 1024;
-
 struct D4Layout {
     size_t query, info, partials, logits, total;
 };
 static D4Layout d4_layout(int B, int H_q, int H_kv, int max_pages, int64_t C, bool weights) {
     const size_t units = (size_t)B * H_kv, G = (size_t)(H_q / H_kv);
     D4Layout l;
-    l.query = WS_HEADER + D4_TICKETS * 4;
+    l.query = INT4_WS_BODY;
     l.info = align_up(l.query + units * (G <= 4 ? sizeof(D4Query<1>) : sizeof(D4Query<2>)), 256);
     l.partials = align_up(l.info + units * sizeof(int2), 256);
     l.logits = align_up(l.partials + (units + (size_t)C) * G * PART_STRIDE * 4, 256);  // a slot per (unit + CTA)
@@ -1664,7 +1660,7 @@ static kvq_status decode_int4(const char* fn, const void* q, int B, int H_q, int
     const int64_t most_pages = window ? std::min((int64_t)max_pages, ((int64_t)window + PAGE - 2) / PAGE + 1 + ((int64_t)sinks + PAGE - 1) / PAGE)
                                       : max_pages;
     const bool small = most_pages <= (int64_t)D4_ONE_PAGES * per_unit;
-    const bool one = num_splits == 0 && per_unit >= 1 && units <= D4_TICKETS &&
+    const bool one = num_splits == 0 && per_unit >= 1 && units <= INT4_TICKETS &&
                      ((small && (!with_weights || per_unit <= 2)) || (B == 1 && per_unit >= 4));
     if (!one) {
         // 1: one sequence a CTA, up to eight CTAs per SM

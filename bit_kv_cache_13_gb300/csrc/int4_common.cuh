@@ -10,6 +10,10 @@ namespace kvq {
 
 // INT4 tile of one (page, KV head): see kvq_int4_tile_bytes in kvq.h.
 constexpr int INT4_TILE = 2560;
+// A workspace of the INT4 calls begins with the header and the decode's tickets, at one place whatever the shape and the
+// call, so that what another call left there is never taken for one: tickets are zeros between calls.
+constexpr int INT4_TICKETS = 1024;
+constexpr int INT4_WS_BODY = WS_HEADER + INT4_TICKETS * 4;
 constexpr int O4_KC = 0, O4_KM = 1024, O4_VC = 1280, O4_VS = 2304, O4_VM = 2432;
 constexpr int INT4_LEVELS = 15;  // highest code
 

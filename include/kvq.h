@@ -345,8 +345,8 @@ kvq_status kvq_dequant_int4(const void* cache, int64_t num_pages, int H_kv, int 
  * num_splits as passed to the call (0 = automatic on the current device).  The
  * workspace must be zero-filled once before its first use.  Calls (and captured
  * graphs) that may overlap on the GPU need a workspace each.  Its error word is
- * read by kvq_workspace_status.  A workspace may serve calls of any shape and form
- * that it is large enough for, one after another.  Returns 0 for sizes that the
+ * read by kvq_workspace_status.  A workspace may serve INT4 calls of any shape and form
+ * that it is large enough for, one after another (chunk attention too).  Returns 0 for sizes that the
  * call refuses. */
 size_t kvq_int4_workspace_bytes(int B, int H_q, int H_kv, int max_pages_per_seq, int num_splits,
                                 int weights);
@@ -444,8 +444,8 @@ kvq_status kvq_append_rope_int4(const void* q, int64_t q_stride, const void* k, 
 /* Bytes of workspace for kvq_chunk_attn_int4.  It must be zero-filled once before
  * its first use; calls (and captured graphs) that may overlap on the GPU need one
  * each.  A workspace may serve calls of any shape that it is large enough for, one
- * after another, but no decode call besides: those count on zeros in theirs, where
- * this one leaves sums.  Returns 0 for sizes that the call refuses. */
+ * after another, and the INT4 decode calls between them, but not the decode calls of
+ * the other formats.  Returns 0 for sizes that the call refuses. */
 size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
 
 /* Attention of each sequence's last tokens over the INT4 cache, causal among
