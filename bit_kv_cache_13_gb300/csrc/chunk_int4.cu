@@ -1400,10 +1400,12 @@ static ChunkLayout chunk_layout(int n_tok, int B, int H_q, int H_kv) {
     const bool few = l.block_rows == CK_ROWS && (int64_t)B * H_kv * CK_ROW_TILE < rows;
     l.max_blocks = (int)((int64_t)n_tok * G / l.block_rows + B);
     l.second_rows = few ? CK_ROW_TILE : 0;
+    // (room for blocks of one row tile in either case: a workspace serves any call of fewer tokens or sequences)
+    const size_t room = (size_t)((int64_t)n_tok * G / CK_ROW_TILE + B);
     l.plan = INT4_WS_BODY;
     l.cut = l.plan + 256;
     l.block = align_up(l.cut + (size_t)(kvq_device_sm_count() + 1) * 8, 256);
-    l.scale = align_up(l.block + (size_t)l.max_blocks * sizeof(CkBlock), 256);
+    l.scale = align_up(l.block + room * sizeof(CkBlock), 256);
     l.rot = align_up(l.scale + (size_t)rows * 4, 256);
     l.main = align_up(l.rot + (size_t)rows * D * 2, 256);
     l.second = align_up(l.main + (size_t)(rows * part), 256);

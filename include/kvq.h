@@ -443,9 +443,10 @@ kvq_status kvq_append_rope_int4(const void* q, int64_t q_stride, const void* k, 
 
 /* Bytes of workspace for kvq_chunk_attn_int4.  It must be zero-filled once before
  * its first use; calls (and captured graphs) that may overlap on the GPU need one
- * each.  A workspace may serve calls of any shape that it is large enough for, one
- * after another, and the INT4 decode calls between them, but not the decode calls of
- * the other formats.  Returns 0 for sizes that the call refuses. */
+ * each.  A workspace may serve calls of any shape that it is large enough for (of the
+ * same heads: any with no more tokens and sequences), one after another, and the INT4
+ * decode calls between them, but not the decode calls of the other formats.  Returns 0
+ * for sizes that the call refuses. */
 size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
 
 /* Attention of each sequence's last tokens over the INT4 cache, causal among

@@ -102,3 +102,17 @@ def test_binding_refuses_tensors(lib):
         _lib._heads(torch.zeros(2, 128, 4, dtype=torch.bfloat16).transpose(1, 2), 2, -1, "q")
     with pytest.raises(ValueError, match="shape"):
         _lib._heads(x, 3, -1, "q")
+
+
+def test_chunk_workspace_serves_smaller_calls(lib):
+    """A workspace for the largest call of a shape holds any with fewer tokens or sequences."""
+    sizes = [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1000, 4095, 4096, 30000, 65535]
+    for h_q, h_kv in ((1, 1), (4, 1), (32, 8), (64, 8), (64, 1)):
+        for fixed in sizes:
+            by_tokens = [lib.kvq_chunk_workspace_bytes(n, fixed, h_q, h_kv) for n in sizes]
+            by_batch = [lib.kvq_chunk_workspace_bytes(fixed, b, h_q, h_kv) for b in sizes]
+            assert by_tokens == sorted(by_tokens) and by_batch == sorted(by_batch), (fixed, h_q, h_kv)
+            # where blocks of 256 rows take over from those of 128: 128 rows a sequence
+            edge = 128 * fixed // (h_q // h_kv)
+            around = [lib.kvq_chunk_workspace_bytes(n, fixed, h_q, h_kv) for n in range(max(edge - 2, 1), edge + 3)]
+            assert around == sorted(around), (fixed, h_q, h_kv, around)
