@@ -140,12 +140,13 @@ class Int4Layer(Int2Layer):
         return torch.zeros(n, dtype=torch.uint8, device=self.device)
 
     def append_rope(self, q, k, v, positions, rope, slots, q_weight=None, k_weight=None, interleaved: bool = False,
-                    err_count=None):
-        """Norms and rotates the heads of q [n, H_q, d] and k [n, H_kv, d] and appends the keys and v; returns the
-        rotated queries and keys."""
+                    err_count=None, eps: float = 1e-6, clip: float = 1.0):
+        """Norms (with eps, where there are weights) and rotates the heads of q [n, H_q, d] and k [n, H_kv, d] and appends
+        the keys and v (with a clip ratio); returns the rotated queries and keys."""
         q_out, k_out = (torch.empty(x.shape, dtype=torch.bfloat16, device=self.device) for x in (q, k))
         _lib.kvq_append_rope_int4(q, k, v, positions, rope, slots, self.mu, self.R_k, self.R_v, self.cache, self.num_pages,
-                                  q_out, k_out, q_weight, k_weight, interleaved=interleaved, err_count=err_count)
+                                  q_out, k_out, q_weight, k_weight, eps=eps, interleaved=interleaved, clip=clip,
+                                  err_count=err_count)
         return q_out, k_out
 
     def chunk_workspace(self, n_tok: int) -> torch.Tensor:
@@ -161,7 +162,8 @@ class Int4Layer(Int2Layer):
     def decode(self, q, out, ws, num_splits: int = 0, decay: float | None = None, window: int = 0, sinks: int = 0):
         """Attends over context_lens tokens; with decay given, accumulates
         the tokens' attention weights too; with a window, over the last
-        `window` tokens and the first `sinks`."""
+        `window` tokens and the first `sinks` (without one all tokens are
+        seen, the first ones too)."""
         args = (q, self.cache, self.num_pages, self.block_table, self.context_lens, self.R_k, self.R_v, self.scale)
         if window:
             if decay is not None:

@@ -36,3 +36,16 @@ def test_new_slots_of_an_empty_sequence_and_past_the_table():
     layer.context_lens = torch.tensor([1, 9 * 16 + 1], dtype=I32)
     with pytest.raises(IndexError):
         layer.new_slots()
+
+
+def test_append_rope_takes_the_model_s_eps_and_clip(monkeypatch):
+    from bit_kv_cache_13_gb300 import _lib
+    layer, seen = _layer(), {}
+    layer.mu = torch.zeros(1, 128)
+    monkeypatch.setattr(_lib, "kvq_append_rope_int4", lambda *args, **kw: seen.update(kw))
+    x = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    q, k = layer.append_rope(x, x[:, :1], x[:, :1], None, None, None, eps=1e-5, clip=0.9)
+    assert q.shape == x.shape and k.shape == (3, 1, 128)
+    assert seen["eps"] == 1e-5 and seen["clip"] == 0.9
+    layer.append_rope(x, x[:, :1], x[:, :1], None, None, None)
+    assert seen["eps"] == 1e-6 and seen["clip"] == 1.0
