@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
 //
 //   TMEM     S [stream][2 buffers] (the logits of a tile, and over them its weights P as
 //            fp16), O [stream]
-//   shared   Q [stream], K [2 stages] and V [4] as K-major operands in the 128-byte swizzle
-//            (V transposed: rows are channels), six raw stages
+//   shared   Q [stream], K [4 stages] and V [2] as K-major operands in the 128-byte swizzle
+//            (V transposed: rows are channels), six raw stages; FEW: one Q, four stages of V
 constexpr int CK_QUERIES = CK_ROW_TILE * D * 2, CK_OPERAND = CK_TILE * D * 2;  // bytes
 constexpr int CK_RAW = CK_PAGES * INT4_TILE, CK_INFOS = 8, CK_SHARES = 4;
 constexpr int CK_SOFTMAX = 8, CK_UNPACK = 16;  // warps
@@ -409,6 +409,10 @@ struct __align__(1024) CkSmem {
     static constexpr int K_STAGES = 4, V_STAGES = FEW ? 4 : 2, RAW_STAGES = 6;
     // (A tile's stages are its number modulo their count.  The warps of the even tiles never wait for an odd one's phase:
     // with an odd count they could ask for a stage's next phase while the last one is open, and be let through.)
+    // (A tile's keys come with what the softmax reads of it, in the place of the tile CK_INFOS before.  They wait for the
+    // logits of the tile K_STAGES before, which their stream forms after the softmax of its second tile before that one:
+    // 2 K_STAGES before, where streams take every other tile, K_STAGES + 2 where they take all.)
+    static_assert(CK_INFOS >= 2 * K_STAGES && CK_INFOS >= K_STAGES + 2, "the softmax is done with an info's place");
     static_assert(RAW_STAGES % 2 == 0 && K_STAGES % 2 == 0 && V_STAGES % 2 == 0, "even and odd tiles have stages of their own");
     uint8_t q[FEW ? 1 : 2][CK_QUERIES], k[K_STAGES][CK_OPERAND], v[V_STAGES][CK_OPERAND];
     uint8_t raw[RAW_STAGES][CK_RAW];

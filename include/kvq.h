@@ -461,7 +461,7 @@ size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
  *            nothing (p < 0 among them) gets zeros
  *   q_start  device int32 [B+1], ascending within 0..n_tok; a sequence whose two
  *            entries are not has no rows, and kvq_workspace_status reports
- *            KVQ_ERR_INVALID_ARG (rows that others then share hold either's result)
+ *            KVQ_ERR_INVALID_ARG (what rows hold that others then share is undefined)
  *   window   0: all tokens; sinks >= 0 (without a window it makes no difference)
  * context_lens is clamped to [0, 16 * max_pages_per_seq]; block-table entries
  * outside [0, num_pages) as kvq_decode_attn_int4, where a token that a row sees lies
