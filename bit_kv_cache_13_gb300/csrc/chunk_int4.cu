@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
     const float* Rk = a.Rk + (size_t)h * D * D;
     const int64_t rows = (int64_t)a.n_tok * a.G;
-    const float unit = a.scale_log2 < 0.f ? -1.f : a.scale_log2 > 0.f ? 1.f : 0.f;
+    const float unit = a.scale_log2 < 0.f ? -1.f : a.scale_log2 > 0.f ? 1.f : a.scale_log2;  // (NaN stays NaN)
     auto fetch = [&](int64_t r0, uint32_t (&x)[8][4]) {
         const __nv_bfloat16* q[2];
 #pragma unroll

@@ -153,3 +153,20 @@ def test_values_past_the_type_s_largest():
     close(c, c.run())
     set_values(c, np.where(c.rng.random(c.cache.shape[:2] + (16,)) < 0.1, 2e5, 1e-2))
     close(c, c.run())
+
+
+def test_queries_and_scales_that_are_not_finite():
+    """A query of NaN or infinity makes its own row NaN and no other; a scale of NaN every row that sees a token."""
+    c = Case(10, [40], [30], 4, 2)               # rows before position 0 see nothing
+    clean = c.run()
+    for x in (float("nan"), float("inf"), -float("inf")):
+        q = c.q.clone()
+        q[25, 1, 7] = q[38, 3, 100] = x
+        keep, c.q = c.q, q
+        got = c.run()
+        c.q = keep
+        hit = torch.zeros(got.shape[:2], dtype=torch.bool)
+        hit[25, 1] = hit[38, 3] = True
+        assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
+    got = run(c, float("nan"))
+    assert torch.isnan(got[10:]).all() and not got[:10].any()
