@@ -12,7 +12,6 @@
 //              products on tcgen05, the cache unpacked to fp16 in shared memory on the way
 //   3 finish   merges the shares' partial sums, normalises, rotates by R_v^T
 #include <algorithm>
-#include <climits>
 #include <cstddef>
 #include <mutex>
 
@@ -37,17 +36,17 @@ constexpr int CK_LEAST_SHARE = 20, CK_LEAST_SHARE_FEW = 12;
 constexpr int CK_RUN = 1024;
 constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // A token counts in the output by its weight times the size of its values: the power of two of 8 |scale| + |min| of its
-// largest group, relative to the share's own (2^2 less than the largest of the first tile).  A row's reference is the largest
-// such product (as logit + size) in its first tile, or where it was last raised, and a weight is carried as 2^CK_LIFT times
-// itself relative to it, so that a token with a large logit and small values (a sink) does not push the weights of those that
-// make up the output out of fp16.  Where a size lies outside [CK_SIZE_LEAST, CK_SIZE_MOST] the weight also takes what it lies
-// outside by (its level), and the values leave it.  So the largest product's weight stands at 2^0 to 2^6, 16 to 10 powers of
-// two below fp16's end; bits are lost of products 2^-13 of it and less, and those below 2^-24 are gone.  (Without
-// sizes, a sink of no values 20 nats above the others left the output 20 % off; with them 2K tokens of 32K take 950 us
-// instead of 927, a 4K prompt 250 instead of 240.)  Raising drains the stream's products: for a lift of 6, a 4K prompt
-// takes 3 % longer.
+// largest group, relative to the share's own (half the mean size of the first tile, whatever single tokens hold).  A row's
+// reference is the largest such product (as logit + size) in its first tile, or where it was last raised, and a weight is
+// carried as 2^CK_LIFT times itself relative to it, so that a token with a large logit and small values (a sink) does not
+// push the weights of those that make up the output out of fp16.  Where a size lies outside [CK_SIZE_LEAST, CK_SIZE_MOST]
+// the weight also takes what it lies outside by (its level), and the values leave it.  So the largest product's weight
+// stands at 2^0 to 2^12, 16 to 4 powers of two below fp16's end (at 2^2 for values of the mean size); bits are lost of
+// products 2^-13 of it and less, and those below 2^-24 are gone.  (Without sizes, a sink of no values 20 nats above the
+// others left the output 20 % off; with them 2K tokens of 32K take 950 us instead of 927, a 4K prompt 250 instead of 240.)
+// Raising drains the stream's products: for a lift of 6, a 4K prompt takes 3 % longer.
 constexpr float CK_LIFT = 3.f;
-constexpr int CK_SIZE_LEAST = -3, CK_SIZE_MOST = 3, CK_SIZE_NONE = -64;  // (of zeros; what is not finite is marked)
+constexpr int CK_SIZE_LEAST = -9, CK_SIZE_MOST = 3, CK_SIZE_NONE = -64;  // (of zeros; what is not finite is marked)
 constexpr int CK_SHARE_LEAST = -6, CK_SHARE_MOST = 11;  // (what values are brought to has its bits in fp16)
 __device__ __forceinline__ int ck_size(float z, int share) { return max(CK_SIZE_NONE, (int)(__float_as_uint(z) >> 23) - 127 - share); }
 __device__ __forceinline__ int ck_level(int size) { return size - max(CK_SIZE_LEAST, min(CK_SIZE_MOST, size)); }
@@ -799,14 +798,15 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
                         const int first = __shfl_sync(0xffffffffu, base, lane >> 3);
                         const uint8_t* y = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, from, lane >> 3)) + O4_VS + 16 * (lane & 7);
                         const int left = first < 0 ? 0 : w.k.ctx - first - 2 * (lane & 7);  // tokens of the pair
-                        int size = INT_MIN;
+                        int size = 0, count = 0;
                         if (left > 0) {
                             const float2 z = ck_sizes(ck_most(__ldg(reinterpret_cast<const uint4*>(y))), ck_most(__ldg(reinterpret_cast<const uint4*>(y + O4_VM - O4_VS))));
-                            if (z.x > 0.f && z.x < CUDART_INF_F) size = ck_size(z.x, 0);
-                            if (left > 1 && z.y > 0.f && z.y < CUDART_INF_F) size = max(size, ck_size(z.y, 0));
+                            if (z.x > 0.f && z.x < CUDART_INF_F) size = ck_size(z.x, 0), count = 1;
+                            if (left > 1 && z.y > 0.f && z.y < CUDART_INF_F) size += ck_size(z.y, 0), ++count;
                         }
-                        size = __reduce_max_sync(0xffffffffu, size);
-                        size = size == INT_MIN ? 0 : max(CK_SHARE_LEAST, min(CK_SHARE_MOST, size - 2));
+                        size = __reduce_add_sync(0xffffffffu, size);
+                        count = __reduce_add_sync(0xffffffffu, count);
+                        size = count ? max(CK_SHARE_LEAST, min(CK_SHARE_MOST, __float2int_rn((float)size / (float)count) - 1)) : 0;
                         if (lane == 0) {
                             sm.share_size[x % CK_SHARES] = size;
                             sm.share_band[x % CK_SHARES] = make_float2(ck_pow2(CK_SIZE_LEAST + size), ck_pow2(CK_SIZE_MOST + 1 + size));
