@@ -148,8 +148,9 @@ __device__ __forceinline__ float2 rope_fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
-// A warp takes `per` heads of a token, two at a time (16 lanes a head, 16 bytes each).  Bound by its instructions: 8192 tokens
-// of 32 + 8 heads 77 us, 168 MB (25 us at the copy rate), 358 instructions a head pair.
+// A warp takes `per` heads of a token, two at a time (16 lanes a head, 16 bytes each).  8192 tokens of
+// 32 + 8 heads: 77 us, 168 MB (25 us at the copy rate).  Bound by 358 instructions a head pair, most of them for the bound on
+// the rounding, and by waits for loads between them: 62 % of the issue slots are taken, long scoreboard is the largest stall.
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(128, 6) rope_kernel(const __grid_constant__ RopeArgs a) {
     const int lane = threadIdx.x & 31, l = lane & 15, rows = a.H_q + a.H_kv, groups = (rows + a.per - 1) / a.per;

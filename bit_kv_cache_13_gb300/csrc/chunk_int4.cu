@@ -23,12 +23,12 @@ constexpr int CK_ROWS = 256;       // most rows of a block: two row tiles of 128
 constexpr int CK_ROW_TILE = 128;
 constexpr int CK_PAGES = 4, CK_TILE = CK_PAGES * PAGE;  // pages and cached tokens of a tile
 // What starting a block costs, in tiles of one row tile: its queries' way in, a pipeline filled and drained, its sums' way
-// out.  A 4K prompt: 294 us for 8, 267 for 11, 245 for 14, 242 for 18, 249 for 24; 8 x 5 tokens at 32K, in blocks of one row
-// tile: 173 us for 4 and 6, 175 for 9.
+// out.  A 4K prompt: 312 us for 8, 278 for 11, 256 for 14, 252 for 18, 258 for 24; 8 x 5 tokens at 32K, in blocks of one row
+// tile: 191 us for 4 and 6, 192 for 9.
 constexpr int CK_UNIT_COST = 18, CK_UNIT_COST_FEW = 6;
 // The least share worth a CTA, in the same units: the finish merges a block's shares one after the other.  32 q / 8 KV heads,
-// 5 tokens of 2000: 56 us for 1, 34 for 6, 32 for 12 and 20, 45 for 45; 5 of 500: 28, 24, 26, 30, 40; 64 of 1000, in blocks
-// of two row tiles: 74 for 1, 43 for 12 and 20, 50 for 45; 64 of 4000: 73 for 12, 62 for 20, 59 for 45.
+// 5 tokens of 2000: 58 us for 1, 36 for 6, 34 for 12 and 20, 49 for 45; 5 of 500: 29, 26, 29, 33, 44; 64 of 1000, in blocks
+// of two row tiles: 75 for 1, 45 for 12 and 20, 54 for 45; 64 of 4000: 75 for 12, 63 for 20, 62 for 45.
 constexpr int CK_LEAST_SHARE = 20, CK_LEAST_SHARE_FEW = 12;
 // Most tiles of a block that are summed in tensor memory at a time: a product cuts its sum off below fp32, by 2^-23.6 of it on
 // the average, so that the 4 * 16384 of a million tokens of equal weight took 0.3 % off.  What a CTA has of a block beyond
@@ -43,7 +43,7 @@ constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // the weight also takes what it lies outside by (its level), and the values leave it.  So the largest product's weight
 // stands at 2^0 to 2^12, 16 to 4 powers of two below fp16's end (at 2^2 for values of the mean size); bits are lost of
 // products 2^-13 of it and less, and those below 2^-24 are gone.  (Without sizes, a sink of no values 20 nats above the
-// others left the output 20 % off; with them 2K tokens of 32K take 950 us instead of 927, a 4K prompt 250 instead of 240.)
+// others left the output 20 % off; with them 2K tokens of 32K take 938 us instead of 915, a 4K prompt 252 instead of 241.)
 // Raising drains the stream's products: for a lift of 6, a 4K prompt takes 3 % longer.
 constexpr float CK_LIFT = 3.f;
 constexpr int CK_SIZE_LEAST = -9, CK_SIZE_MOST = 3, CK_SIZE_NONE = -64;  // (of zeros; what is not finite is marked)
@@ -252,7 +252,7 @@ __host__ __device__ constexpr int ck_key_at(int ch) { return (ch & ~7) | (ch & 3
 // (A value channel 32 g + 4 r + i stands at 32 g + 8 i + r.)
 
 // CTAs of 256 threads, 128 rows each (a warp 16); the last CTA of a head's row makes the plan.  4096 tokens of 32 heads:
-// 31 us for 67 MB (10 at the copy rate), the matrix's way into the operands' layout and a tile or two behind it.
+// 33 us for 67 MB (10 at the copy rate), the matrix's way into the operands' layout and a tile or two behind it.
 struct __align__(16) CkRotate {
     CkMatrix R;
     __align__(16) __half out[8][16][D / 2 + 8];  // half a row at a time, so that four CTAs share an SM
@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(256, 4) chunk_rotate_kernel(const __grid_const
 // the warpgroups take every other tile of tokens of it (two streams, each with sums of its
 // own).  In either case the products of one stream run while the other one's softmax does.
 //
-// 2048 tokens of 32K, 32 q / 8 KV heads: 0.90 ms, 1.18 PFLOP/s, 0.59 of a library product's rate.  Bound by the roles'
-// instructions and their waits together: tensor pipe 44 %, issue 57 %; alone, the products took 783 us, the
+// 2048 tokens of 32K, 32 q / 8 KV heads: 0.94 ms, 1.14 PFLOP/s, 0.57 of a library product's rate.  Bound by the roles'
+// instructions and their waits together: tensor pipe 44 %, issue 56 %; alone, of 1010 us, the products took 783, the
 // softmax 802 and the unpacking 620.  (With 128 logit columns a product and one buffer a stream, for which tensor memory
 // has room, products alone took 637 us, and all of it 1164.)
 //
@@ -1220,7 +1220,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_stream_kernel(const __gri
 // ------------------------------------------------------------------ 3: finish
 
 // CTAs of 256 threads take row tiles of a KV head, a warp 16 rows: their partials are merged in the layout of the A
-// operand (a lane has eight times four values of two rows), normalised and rotated by R_v^T.  A 4K prompt of 32 heads: 42 us
+// operand (a lane has eight times four values of two rows), normalised and rotated by R_v^T.  A 4K prompt of 32 heads: 43 us
 // for 69 MB of partials and 34 of output (15 at the copy rate), bound by latency with two CTAs an SM.
 __global__ void __launch_bounds__(256, 2) chunk_finish_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
