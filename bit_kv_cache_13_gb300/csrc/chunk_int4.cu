@@ -46,7 +46,7 @@ constexpr float CK_NEG = -3e38f;   // reference of a row before it sees a token
 // others left the output 20 % off; with them 2K tokens of 32K take 938 us instead of 915, a 4K prompt 252 instead of 241.)
 // Raising drains the stream's products: for a lift of 6, a 4K prompt takes 3 % longer.
 constexpr float CK_LIFT = 3.f;
-constexpr int CK_SIZE_LEAST = -9, CK_SIZE_MOST = 3, CK_SIZE_NONE = -64;  // (of zeros; what is not finite is marked)
+constexpr int CK_SIZE_LEAST = -9, CK_SIZE_MOST = 3, CK_SIZE_NONE = -90;  // (of zeros: sums of their weights stay below 2^93 a token)
 constexpr int CK_SHARE_LEAST = -6, CK_SHARE_MOST = 11;  // (what values are brought to has its bits in fp16)
 __device__ __forceinline__ int ck_size(float z, int share) { return max(CK_SIZE_NONE, (int)(__float_as_uint(z) >> 23) - 127 - share); }
 __device__ __forceinline__ int ck_level(int size) { return size - max(CK_SIZE_LEAST, min(CK_SIZE_MOST, size)); }

@@ -467,8 +467,8 @@ size_t kvq_chunk_workspace_bytes(int n_tok, int B, int H_q, int H_kv);
  * outside [0, num_pages) as kvq_decode_attn_int4, where a token that a row sees lies
  * on them.  Products take fp16 operands with 11 bits each (rotations, rotated
  * queries, cached keys and values of any size, weights) and add in fp32.  Of a row,
- * tokens whose weight times their values' size is below 2^-24 of the largest such
- * product may be lost.  A rotation's entries may not pass 65504, and R_k may lengthen
+ * tokens whose weight times their values' size (for zeros 2^-90 of what is usual) is
+ * below 2^-24 of the largest such product may be lost.  A rotation's entries may not pass 65504, and R_k may lengthen
  * a query up to 2^11-fold.  A call repeated
  * gives the same bits.  q, cache, R_k, R_v, out and
  * workspace need 16-byte alignment.  H_q / H_kv <= 64, B and H_kv <= 65535,

@@ -123,7 +123,7 @@ def set_sinks(c, tokens, gap, size):
 
 
 @pytest.mark.parametrize("size", [0.0, 1e-6, 1e-3, 0.02, 0.3, 3.0, 100.0])
-@pytest.mark.parametrize("gap", [5.0, 12.0, 17.0, 20.0, 24.0, 40.0])
+@pytest.mark.parametrize("gap", [5.0, 12.0, 17.0, 20.0, 24.0, 40.0, 75.0])
 def test_sinks(gap, size):
     """A token that draws all of the weight, with values from none to far larger ones than the others': at the front, later
     in the context (where the reference is raised), the whole first tile, in a window's sinks; values of other sizes too."""
