@@ -6,7 +6,10 @@
 // The rotated values are those of the real numbers, rounded once: a cached code depends
 // on every bit of the key, so the key must not depend on which kernel formed it.  Fp32
 // gives each value to within 2^-20 of its terms; where a rounding to bf16 lies within
-// that (one value in a thousand or two) it is formed again in pairs of fp32 values.
+// that (one value in a thousand or two) it is formed again in pairs of fp32 values, which
+// leave less than 2^-42 of the terms: the mean of squares 2^-43.5 (seven additions of low
+// parts, four across lanes), halved by the root, and 2^-46 each for Newton's step, the
+// root's low part and the product's.
 #include <cstddef>
 
 #include "int4_common.cuh"

@@ -425,8 +425,10 @@ kvq_status kvq_decode_attn_int4_sliding(const void* q, int B, int H_q, int H_kv,
  *               are normed, y = x * weight / sqrt(mean(x^2) + eps); eps >= 0
  *   q_out, k_out  device bf16 [n_tok][H_q][d], [n_tok][H_kv][d], written: with
  *               (a, b) a pair of y, a cos - b sin and b cos + a sin.  The real
- *               numbers, rounded once (they are formed as far as that takes).  Each
- *               may be its input, where that is dense; else no overlap.
+ *               numbers, rounded once; a normed one nearer than 2^-42 of its terms
+ *               to half-way between two bf16 numbers (mean(x^2) far below eps, where
+ *               1/sqrt(eps) is a round number) goes to either.  Each may be its
+ *               input, where that is dense; else no overlap.
  *   other arguments as kvq_append_int4, whose cache bytes for (k_out, v) these are
  * A token whose position lies outside [0, max_pos) gets zeros in q_out and k_out;
  * it is not appended and counts in err_count as one with a bad slot does (once;
